@@ -293,8 +293,9 @@ hf_status hf_sync(hf_handle* h, void* stream);
 
 /* Message for the last non-OK status of this handle ("" if none); the
  * pointer stays valid until the next call on the handle. h may be NULL
- * (then the message of the last failed call without a handle -- hf_create
- * or hf_attention_noalloc -- in this thread). */
+ * (then the message of the last failed call without a handle -- hf_create,
+ * hf_attention_noalloc or a call of the target model's half of a round --
+ * in this thread). */
 const char* hf_last_error(const hf_handle* h);
 
 /* Static name of a status code. */
@@ -468,6 +469,192 @@ hf_status hf_attention_noalloc(int32_t dtype, int32_t batch, int32_t n_q_heads,
                                int32_t block, const float* proj, int32_t proj_ld,
                                const void* ring_k, const void* ring_v, const int64_t* pos,
                                void* out, int32_t out_ld, int32_t* status, void* stream);
+
+/* ---- the target model's half of a round ------------------------------
+ *
+ * The pages describe the drafter and leave the target model to the serving
+ * loop around it. The calls below are what that loop runs between hf_draft
+ * and hf_commit: attention over new prompts, a paged cache of the target's
+ * keys and values, attention of the verified rows over that cache, and the
+ * acceptance of the drafted tokens. They have no handle: every buffer is the
+ * caller's, on the current device; nothing allocates or synchronises, so all
+ * of them may be captured into CUDA graphs. Messages of refused calls:
+ * hf_last_error(NULL). Two calls that can overlap on the GPU must not share
+ * a workspace, and calls on one cache must be ordered by the caller.
+ *
+ * status (optional, NULL: not reported): an int32 device word that device
+ * checks OR these bits into; the caller zeroes it and reads it when it likes. */
+enum {
+  HF_S_BAD = 1,     /* an index, length or value out of its range */
+  HF_S_TIMEOUT = 2, /* a bounded wait gave up: the call's output is not valid */
+  HF_S_FULL = 4     /* hf_pages_extend: too few free pages or table columns */
+};
+
+/* Causal attention over whole prompts, packed one after another: sequence s
+ * holds rows offsets[s] .. offsets[s+1]-1 of q, k, v and out, and
+ *   out[i, h] = sum_{j <= i in the sequence} softmax_j(scale q[i,h].k[j,g]) v[j,g]
+ * with g = h / (n_q_heads / n_kv_heads). Scores, softmax and sums are fp32
+ * (bf16: the probabilities enter the second product rounded to bf16).
+ *   dtype      HF_F32 or HF_BF16, of q, k, v and out.
+ *   n_seq      sequences (>= 0); total: rows of the buffers (>= 0).
+ *   q, k, v    [total, *_ld] DEVICE, 16-byte aligned: head h of a row at
+ *              columns [h*head_dim, (h+1)*head_dim); *_ld in elements, a
+ *              multiple of 16 bytes, at least heads * head_dim. They may be
+ *              parts of one projection's output.
+ *   offsets    DEVICE int32 [n_seq + 1], 0 <= offsets[0], not decreasing,
+ *              offsets[n_seq] <= total; a sequence may be empty. Rows outside
+ *              every sequence are not written. Bounds that break this rule
+ *              set HF_S_BAD, and out is not valid.
+ *   head_dim   a multiple of 8, at most 256. n_q_heads / n_kv_heads <= 64.
+ *   scale      > 0, or 0 for 1/sqrt(head_dim).
+ *   out        as q; may not overlap q, k or v. */
+hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t total, int32_t n_q_heads,
+                              int32_t n_kv_heads, int32_t head_dim, const void* q, int64_t q_ld,
+                              const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                              const int32_t* offsets, float scale, void* out, int64_t out_ld,
+                              int32_t* status, void* stream);
+
+/* A paged cache of the target's keys and values, all buffers DEVICE and the
+ * caller's. Request r holds lens[r] tokens; token t of it lies in row
+ * t % page of page table[r][t / page], the same page in every layer. refs[i]
+ * counts the requests that hold page i; a page with refs[i] = 0 is free. A
+ * new cache has lens and refs all zero (table and pools need no values).
+ * Table entries behind a request's last page are -1 or unused. */
+typedef struct {
+  void* k;          /* dtype [n_layers, n_pages, n_kv_heads, page, head_dim], 16-byte aligned */
+  void* v;          /* the same */
+  int32_t* table;   /* [n_requests, table_ld] page ids */
+  int32_t* lens;    /* [n_requests] */
+  int32_t* refs;    /* [n_pages] */
+  int32_t* work;    /* hf_pages_work_ints() ints of scratch, zeroed once by the caller */
+  int32_t* status;  /* status word, or NULL */
+  int32_t dtype;    /* hf_dtype */
+  int32_t n_layers, n_pages, n_kv_heads;
+  int32_t page;     /* tokens per page: 8, 16, 32, 64 or 128 */
+  int32_t head_dim; /* a multiple of 8, at most 256 */
+  int32_t n_requests; /* at most 4096 */
+  int32_t table_ld;
+} hf_pages;
+
+/* Ints of p->work; 0 for a descriptor that the calls would refuse. */
+size_t hf_pages_work_ints(const hf_pages* p);
+
+/* The calls below name requests by DEVICE int32 lists of n entries (NULL:
+ * requests 0 .. n-1), 0 <= n <= n_requests. They see the cache as it is when
+ * the call starts. Where an entry is out of range or a list that must not
+ * repeat a request does, HF_S_BAD is set and the call changes nothing. Which
+ * page is taken never depends on timing: always the lowest free ones, in
+ * list order. */
+
+/* Make room for counts[i] >= 0 more tokens of request i (DEVICE int32 [n]) and
+ * add them to its length. New pages are taken as needed. If counts[i] > 0 and
+ * the request's last page is partly filled and held by others too, the request
+ * first takes a copy of that page in its place (all layers, the whole page).
+ * Too few free pages, or a table row too short: HF_S_FULL, and the call changes
+ * nothing. No request twice. */
+hf_status hf_pages_extend(const hf_pages* p, const int32_t* requests, const int32_t* counts,
+                          int32_t n, void* stream);
+
+/* Write the newest rows: entry i's rows offsets[i] .. offsets[i+1]-1 (DEVICE
+ * int32 [n + 1]) of k and v become the last tokens of its request, in layers
+ * layer .. layer + layers - 1. k, v: DEVICE [layers, total, heads * head_dim] with row
+ * stride ld and layer stride layer_stride (elements), 16-byte aligned, strides
+ * multiples of 16 bytes. Rows of a bad entry (out of range, a request named
+ * twice, more rows than the request has tokens, a page id out of range) are
+ * skipped (HF_S_BAD). The pages written must be the request's alone, as
+ * hf_pages_extend leaves them. */
+hf_status hf_pages_write(const hf_pages* p, int32_t layer, int32_t layers, const void* k,
+                         const void* v, int64_t ld, int64_t layer_stride,
+                         const int32_t* requests, const int32_t* offsets, int32_t n,
+                         int32_t total, void* stream);
+
+/* Let request into[i], which must hold no tokens, share all tokens of request
+ * from[i] (DEVICE int32 [n] each). No copies: pages are held by one more
+ * request. No request twice in `into`, and none in both; `from` may repeat. */
+hf_status hf_pages_fork(const hf_pages* p, const int32_t* from, const int32_t* into, int32_t n,
+                        void* stream);
+
+/* Cut request i to keep[i] tokens, 0 <= keep[i] <= lens (DEVICE int32 [n]):
+ * pages behind the last kept token lose a holder, and are free when they have
+ * none; their table entries become -1. keep = 0 frees the request. No request
+ * twice. */
+hf_status hf_pages_truncate(const hf_pages* p, const int32_t* requests, const int32_t* keep,
+                            int32_t n, void* stream);
+
+/* Move the pages in use to the front of the pool: with L pages in use, the
+ * j-th used page at or behind L moves to the j-th free one before it; tables
+ * follow. n_used (DEVICE int32, or NULL) receives L. */
+hf_status hf_pages_compact(const hf_pages* p, int32_t* n_used, void* stream);
+
+/* Attention of the newest `rows` tokens of n requests over the cache: row r of
+ * entry i stands at position lens - rows + r of its request and sees the
+ * tokens up to and with that position; a row that sees none (position below 0,
+ * an empty request) is zero. rows = 1: plain decoding.
+ *   q, out     [n * rows, *_ld] DEVICE: row i * rows + r, head h at columns
+ *              [h*head_dim, (h+1)*head_dim); alignment as hf_attention_prompt.
+ *              out may not overlap q.
+ *   rows       1 .. 64; n_q_heads / n_kv_heads <= 64.
+ *   shared     tokens, a multiple of page: the first `shared` tokens of all entries
+ *              lie in the same pages (those of entry 0) and are read once for all
+ *              of them. 0: nothing is shared. Every entry must hold at least
+ *              `shared` tokens or none, and entry 0 must hold some if any does:
+ *              one that breaks this sets HF_S_BAD and its rows are zero. One whose
+ *              pages differ from entry 0's there sets HF_S_BAD and its output is
+ *              not valid.
+ *   requests   DEVICE int32 [n], or NULL for 0 .. n-1; may repeat. An entry out of
+ *              range, or a length below 0 or past the table, sets HF_S_BAD: zeros.
+ *   workspace  DEVICE, 16-byte aligned, hf_attention_pages_workspace() bytes;
+ *              needs no values.
+ * A page id out of range in a request's used part sets HF_S_BAD: that request's
+ * output is not valid (entry 0's shared part: none is). Values behind a request's
+ * last token are never used, whatever they are. */
+hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_t n, int32_t rows,
+                             int32_t n_q_heads, const void* q, int64_t q_ld,
+                             const int32_t* requests, int32_t shared, float scale, void* out,
+                             int64_t out_ld, void* workspace, size_t workspace_bytes,
+                             void* stream);
+/* Bytes of its workspace for these sizes (0: refused sizes). */
+size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows,
+                                    int32_t n_q_heads, int32_t shared);
+
+/* Verification of drafted tokens by speculative sampling. Request b has drafts
+ * d_s = draft_tokens[b, s], s < n_draft[b], the target's logits x_s at s = 0 ..
+ * n_draft[b], and the drafter's y_s. With p_s = softmax(x_s / T), q_s =
+ * softmax(y_s / T), T = temperature[b]:
+ *   draft s is accepted iff u[b, s] q_s(d_s) < p_s(d_s); a is the number of
+ *   drafts before the first that is not;
+ *   the next token is argmax_i w_i / noise[b, i] (the lowest i among equals)
+ *   with w = max(p_a - q_a, 0), or w = p_a if every draft was accepted or
+ *   p_a - q_a is nowhere positive. With noise from the exponential distribution
+ *   of rate 1 it is i with probability w_i / sum(w).
+ * T = 0: draft s is accepted iff it is argmax x_s (the lowest token among
+ * equals), and the next token is argmax x_a.
+ *   target_logits [batch, block + 1, vocab] DEVICE, HF_F32 or HF_BF16, row stride
+ *                target_ld elements (>= vocab); no alignment beyond the type's.
+ *   draft_logits  [batch, block, vocab] DEVICE with row stride draft_ld, or NULL:
+ *                the drafts were chosen greedily (q_s is one at d_s).
+ *   draft_tokens  int32 [batch, block]; n_draft: int32 [batch] in 0..block, or
+ *                NULL for block each. block is 1..16, vocab >= 1.
+ *   u [batch, block] in [0, 1), noise [batch, vocab] (> 0; row stride noise_ld),
+ *                temperature [batch] or NULL for 1: fp32 DEVICE.
+ *   n_accepted    int32 [batch]: a + 1, the rows that hf_commit takes (the last
+ *                committed token's row and the accepted drafts').
+ *   tokens        int32 [batch, block + 1]: the a accepted drafts, the next token,
+ *                then -1.
+ *   workspace     DEVICE, 16-byte aligned, hf_verify_workspace() bytes.
+ * A request with a draft outside 0..vocab-1, n_draft out of range, a T that is
+ * negative or not finite, or logits without a softmax (NaN, +infinity, or nothing above
+ * -infinity) in a row that the rule above reads, sets HF_S_BAD and gets n_accepted = 0
+ * and tokens -1: hf_commit then leaves it as it is. */
+hf_status hf_verify_tokens(int32_t target_dtype, const void* target_logits, int64_t target_ld,
+                           int32_t draft_dtype, const void* draft_logits, int64_t draft_ld,
+                           const int32_t* draft_tokens, const int32_t* n_draft, const float* u,
+                           const float* noise, int64_t noise_ld, const float* temperature,
+                           int32_t batch, int32_t block, int32_t vocab, int32_t* n_accepted,
+                           int32_t* tokens, void* workspace, size_t workspace_bytes,
+                           int32_t* status, void* stream);
+/* Bytes of its workspace (0: refused sizes). */
+size_t hf_verify_workspace(int32_t batch, int32_t block, int32_t vocab);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,8 @@ below load on first use, so the build module stays importable before the
 library exists; using any of them without the library raises ImportError.
 """
 _BINDING_NAMES = ("EXPORTED", "Drafter", "Family", "HfBlockWeights", "HfConfig", "HfLayerWeights", "HyflashError",
-                  "LIB_PATH", "Status", "Tensor", "make_config")
+                  "LIB_PATH", "Status", "Tensor", "make_config", "HfPages", "Pages", "CallStatus", "attention_prompt",
+                  "verify_tokens", "verify_workspace")
 
 __all__ = list(_BINDING_NAMES)
 

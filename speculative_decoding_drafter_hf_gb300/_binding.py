@@ -148,6 +148,30 @@ hf_set_block_weights = _sig("hf_set_block_weights", _st, _h, _i32, ctypes.POINTE
                             ctypes.POINTER(HfBlockWeights))
 hf_set_head_weights = _sig("hf_set_head_weights", _st, _h, _vp, _vp)
 hf_draft_tokens = _sig("hf_draft_tokens", _st, _h, _vp, _vp, _vp, _i32, _vp)
+
+
+class HfPages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "table", "lens", "refs", "work", "status")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "n_layers", "n_pages", "n_kv_heads", "page", "head_dim",
+                                      "n_requests", "table_ld")]
+
+
+_i64, _f32, _sz = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_pp = ctypes.POINTER(HfPages)
+hf_attention_prompt = _sig("hf_attention_prompt", _st, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
+                           _vp, _i64, _vp, _f32, _vp, _i64, _vp, _vp)
+hf_attention_pages = _sig("hf_attention_pages", _st, _pp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i32, _f32,
+                          _vp, _i64, _vp, _sz, _vp)
+hf_attention_pages_workspace = _sig("hf_attention_pages_workspace", _sz, _pp, _i32, _i32, _i32, _i32)
+hf_pages_work_ints = _sig("hf_pages_work_ints", _sz, _pp)
+hf_pages_extend = _sig("hf_pages_extend", _st, _pp, _vp, _vp, _i32, _vp)
+hf_pages_write = _sig("hf_pages_write", _st, _pp, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _vp)
+hf_pages_fork = _sig("hf_pages_fork", _st, _pp, _vp, _vp, _i32, _vp)
+hf_pages_truncate = _sig("hf_pages_truncate", _st, _pp, _vp, _vp, _i32, _vp)
+hf_pages_compact = _sig("hf_pages_compact", _st, _pp, _vp, _vp)
+hf_verify_tokens = _sig("hf_verify_tokens", _st, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
+                        _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp)
+hf_verify_workspace = _sig("hf_verify_workspace", _sz, _i32, _i32, _i32)
 hf_debug_set_wait_limit = _sig("hf_debug_set_wait_limit", _st, _h, ctypes.c_int64)
 hf_debug_fail_alloc = _sig("hf_debug_fail_alloc", _st, ctypes.c_int64)
 hf_debug_check_guards = _sig("hf_debug_check_guards", _st, _h)
@@ -157,7 +181,10 @@ EXPORTED = ("hf_create", "hf_destroy", "hf_set_weights", "hf_set_weights_q4", "h
             "hf_context_bytes", "hf_export_context", "hf_import_context", "hf_profile_enable",
             "hf_profile_collect", "hf_profile_read", "hf_launch_count", "hf_attention_noalloc",
             "hf_debug_set_wait_limit", "hf_debug_fail_alloc", "hf_debug_check_guards",
-            "hf_set_block_weights", "hf_set_head_weights", "hf_draft_tokens")
+            "hf_set_block_weights", "hf_set_head_weights", "hf_draft_tokens",
+            "hf_attention_prompt", "hf_attention_pages", "hf_attention_pages_workspace", "hf_pages_work_ints",
+            "hf_pages_extend", "hf_pages_write", "hf_pages_fork", "hf_pages_truncate", "hf_pages_compact",
+            "hf_verify_tokens", "hf_verify_workspace")
 
 
 class HyflashError(RuntimeError):
@@ -466,3 +493,305 @@ class Drafter:
     def check_guards(self):
         """Raise if a guard region around one of the handle's buffers changed."""
         self._check(hf_debug_check_guards(self._h))
+
+
+# ---------------------------------------------------------------- the target model's half of a round
+class CallStatus(enum.IntFlag):
+    """Bits that device checks set in a call's status word."""
+    BAD = 1
+    TIMEOUT = 2
+    FULL = 4
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return HF_BF16
+    if t.dtype == torch.float32:
+        return HF_F32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+class _On:
+    """The device and stream of one call: every tensor lies on the first one's
+    device; the call is made with that device current, on `stream` or the
+    device's current stream. New outputs belong to the call's stream."""
+
+    def __init__(self, first, stream):
+        import torch
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError("expected CUDA tensors")
+        self.device = first.device
+        self.given = stream
+        if stream is None:
+            self.ptr = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            self.ptr = stream if isinstance(stream, int) else stream.cuda_stream
+
+    def arg(self, t, name, dtype=None, shape=None, contiguous=True):
+        if not t.is_cuda or t.device != self.device:
+            raise TypeError(f"{name} must be a CUDA tensor on {self.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def empty(self, shape, dtype):
+        import torch
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        s = self.given
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, device=self.device)
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def call(self, f, *args):
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            s = f(*args, self.ptr)
+        else:
+            with torch.cuda.device(self.device):
+                s = f(*args, self.ptr)
+        if s != 0:
+            raise HyflashError(s, hf_last_error(None).decode())
+
+
+def _heads_ld(t, name):
+    """Row stride of [..., heads, head_dim] whose heads follow each other."""
+    h, d = t.shape[-2], t.shape[-1]
+    s = t.stride()
+    if (d > 1 and s[-1] != 1) or (h > 1 and s[-2] != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[-3] if t.shape[-3] > 1 else h * d
+
+
+def attention_prompt(q, k, v, offsets, *, scale=0.0, out=None, status=None, stream=None):
+    """hf_attention_prompt: causal attention over packed prompts. q [T, Hq, dh],
+    k and v [T, Hkv, dh] (row strides are free: parts of one projection will do),
+    offsets int32 [n + 1]. Returns out [T, Hq, dh]; rows outside every sequence keep
+    what `out` held."""
+    import torch
+    on = _On(q, stream)
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    T, hq, dh = q.shape
+    hkv = k.shape[1]
+    code = _dtype_code(q, "q")
+    qp = on.arg(q, "q", None, None, False)
+    kp = on.arg(k, "k", q.dtype, (T, hkv, dh), False)
+    vp = on.arg(v, "v", q.dtype, (T, hkv, dh), False)
+    op = on.arg(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be [sequences + 1]")
+    if out is None:
+        out = on.empty((T, hq, dh), q.dtype)
+    rp = on.arg(out, "out", q.dtype, (T, hq, dh), False)
+    sp = None if status is None else on.arg(status, "status", torch.int32)
+    on.call(hf_attention_prompt, code, offsets.shape[0] - 1, T, hq, hkv, dh, qp, _heads_ld(q, "q"), kp,
+            _heads_ld(k, "k"), vp, _heads_ld(v, "v"), op, float(scale or 0.0), rp, _heads_ld(out, "out"), sp)
+    return out
+
+
+def verify_workspace(target_logits, draft_logits=None):
+    """A workspace for verify_tokens with logits of these sizes."""
+    import torch
+    B, S1, V = target_logits.shape
+    n = hf_verify_workspace(B, S1 - 1, V)
+    if n == 0:
+        raise ValueError("verify_workspace: sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device=target_logits.device)
+
+
+def verify_tokens(target_logits, draft_tokens, u, noise, *, draft_logits=None, temperature=None, n_draft=None,
+                  n_accepted=None, tokens=None, workspace=None, status=None, stream=None):
+    """hf_verify_tokens: (n_accepted int32 [B], tokens int32 [B, S + 1]) from the
+    target's logits [B, S + 1, V] and the drafts int32 [B, S]; u [B, S] uniform and
+    noise [B, V] exponential random numbers. n_accepted is what Drafter.commit takes."""
+    import torch
+    on = _On(target_logits, stream)
+    if target_logits.dim() != 3 or target_logits.shape[1] < 2:
+        raise ValueError("target_logits must be [batch, block + 1, vocab]")
+    B, S, V = target_logits.shape[0], target_logits.shape[1] - 1, target_logits.shape[2]
+
+    def rows(t, name, n):
+        if tuple(t.shape) != (B, n, V):
+            raise ValueError(f"{name} must have shape {(B, n, V)}, got {tuple(t.shape)}")
+        s = t.stride()
+        if (V > 1 and s[2] != 1) or (B > 1 and n > 1 and s[0] != n * s[1]):
+            raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+        return max(s[1] if n > 1 else s[0] if B > 1 else V, V) if B else V
+
+    f32, i32 = torch.float32, torch.int32
+    tp = on.arg(target_logits, "target_logits", None, None, False)
+    t_ld = rows(target_logits, "target_logits", S + 1)
+    dp, d_ld, d_code = None, 0, 0
+    if draft_logits is not None:
+        dp = on.arg(draft_logits, "draft_logits", None, None, False)
+        d_ld = rows(draft_logits, "draft_logits", S)
+        d_code = _dtype_code(draft_logits, "draft_logits")
+    kp = on.arg(draft_tokens, "draft_tokens", i32, (B, S))
+    up = on.arg(u, "u", f32, (B, S))
+    ep = on.arg(noise, "noise", f32, (B, V))
+    np_ = None if n_draft is None else on.arg(n_draft, "n_draft", i32, (B,))
+    hp = None if temperature is None else on.arg(temperature, "temperature", f32, (B,))
+    if n_accepted is None:
+        n_accepted = on.empty((B,), i32)
+    if tokens is None:
+        tokens = on.empty((B, S + 1), i32)
+    ap = on.arg(n_accepted, "n_accepted", i32, (B,))
+    op = on.arg(tokens, "tokens", i32, (B, S + 1))
+    if workspace is None:
+        workspace = on.empty((max(hf_verify_workspace(B, S, V), 16),), torch.uint8)
+    wp = on.arg(workspace, "workspace", torch.uint8)
+    sp = None if status is None else on.arg(status, "status", i32)
+    on.call(hf_verify_tokens, _dtype_code(target_logits, "target_logits"), tp, t_ld, d_code, dp, d_ld, kp, np_, up,
+            ep, V, hp, B, S, V, ap, op, wp, workspace.numel(), sp)
+    return n_accepted, tokens
+
+
+class Pages:
+    """A paged key/value cache of the target over the caller's tensors (hf_pages):
+    k and v [layers, pages, kv heads, page, head_dim], table int32 [requests,
+    columns], lens int32 [requests], refs int32 [pages]. Methods map one-to-one
+    onto the C calls; ``status`` is the word their device checks write to."""
+
+    def __init__(self, k, v, table, lens, refs):
+        import torch
+        on = _On(k, None)
+        if k.dim() != 5 or table.dim() != 2:
+            raise ValueError("k must be [layers, pages, kv heads, page, head_dim], table [requests, columns]")
+        L, n, hkv, page, dh = k.shape
+        R, ld = table.shape
+        i32 = torch.int32
+        d = HfPages(dtype=_dtype_code(k, "k"), n_layers=L, n_pages=n, n_kv_heads=hkv, page=page, head_dim=dh,
+                    n_requests=R, table_ld=ld)
+        d.k = on.arg(k, "k")
+        d.v = on.arg(v, "v", k.dtype, tuple(k.shape))
+        d.table = on.arg(table, "table", i32)
+        d.lens = on.arg(lens, "lens", i32, (R,))
+        d.refs = on.arg(refs, "refs", i32, (n,))
+        ints = hf_pages_work_ints(ctypes.byref(d))
+        self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
+        # scratch of the page calls, and the status word
+        self._work = torch.zeros(max(ints, 1), dtype=i32, device=k.device)
+        self.status = torch.zeros(1, dtype=i32, device=k.device)
+        d.work, d.status = self._work.data_ptr(), self.status.data_ptr()
+        self._d, self._ref = d, ctypes.byref(d)
+        if ints == 0:  # let a call say what is wrong with the descriptor
+            on.call(hf_pages_compact, self._ref, None)
+
+    @classmethod
+    def empty(cls, n_layers, n_pages, n_kv_heads, page, head_dim, n_requests, columns, dtype=None, device="cuda"):
+        """A new cache that holds no request."""
+        import torch
+        shape = (n_layers, n_pages, n_kv_heads, page, head_dim)
+        k = torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
+        ints = dict(dtype=torch.int32, device=device)
+        return cls(k, torch.empty_like(k), torch.full((n_requests, columns), -1, **ints),
+                   torch.zeros(n_requests, **ints), torch.zeros(n_pages, **ints))
+
+    def check(self):
+        """Read and clear the status word (synchronises)."""
+        s = CallStatus(int(self.status.item()))
+        self.status.zero_()
+        return s
+
+    def _lists(self, on, requests, n):
+        import torch
+        return None if requests is None else on.arg(requests, "requests", torch.int32, (n,))
+
+    def extend(self, counts, requests=None, stream=None):
+        """Room for counts[i] more tokens of requests[i] (default: request i)."""
+        import torch
+        on = _On(self.k, stream)
+        n = counts.shape[0]
+        cp = on.arg(counts, "counts", torch.int32, (n,))
+        on.call(hf_pages_extend, self._ref, self._lists(on, requests, n), cp, n)
+
+    def truncate(self, keep, requests=None, stream=None):
+        """Cut requests[i] to keep[i] tokens; 0 frees it."""
+        import torch
+        on = _On(self.k, stream)
+        n = keep.shape[0]
+        kp = on.arg(keep, "keep", torch.int32, (n,))
+        on.call(hf_pages_truncate, self._ref, self._lists(on, requests, n), kp, n)
+
+    def fork(self, source, into, stream=None):
+        """Requests into[i] (empty) share all tokens of source[i]."""
+        import torch
+        on = _On(self.k, stream)
+        n = into.shape[0]
+        sp = on.arg(source, "source", torch.int32, (n,))
+        ip = on.arg(into, "into", torch.int32, (n,))
+        on.call(hf_pages_fork, self._ref, sp, ip, n)
+
+    def compact(self, n_used=None, stream=None):
+        """Move the pages in use to the front of the pool; n_used int32 [1] receives
+        their number."""
+        import torch
+        on = _On(self.k, stream)
+        up = None if n_used is None else on.arg(n_used, "n_used", torch.int32, (1,))
+        on.call(hf_pages_compact, self._ref, up)
+
+    def write(self, k, v, offsets, requests=None, layer=None, stream=None):
+        """The newest rows of the requests: k and v [layers, T, kv heads, head_dim]
+        for layers 0 .. layers - 1, or [T, kv heads, head_dim] with `layer`; entry i's
+        rows are offsets[i] .. offsets[i + 1] - 1."""
+        import torch
+        on = _On(self.k, stream)
+        L, _, hkv, _, dh = self.k.shape
+        if k.dim() != (4 if layer is None else 3) or tuple(k.shape[-2:]) != (hkv, dh) or (layer is None and k.shape[0] > L):
+            raise ValueError("k must be [layers, tokens, kv heads, head_dim], or [tokens, kv heads, head_dim] with layer")
+        T = k.shape[-3]
+        kp = on.arg(k, "k", self.k.dtype, None, False)
+        vp = on.arg(v, "v", self.k.dtype, tuple(k.shape), False)
+        ld = _heads_ld(k, "k")
+        step = k.stride(0) if layer is None and k.shape[0] > 1 else 0
+        if T and (_heads_ld(v, "v") != ld or (step and v.stride(0) != step)):
+            raise ValueError("k and v must have the same strides")
+        n = offsets.shape[0] - 1
+        op = on.arg(offsets, "offsets", torch.int32, (n + 1,))
+        on.call(hf_pages_write, self._ref, layer or 0, k.shape[0] if layer is None else 1, kp, vp, ld, step,
+                self._lists(on, requests, n), op, n, T)
+
+    def attend_workspace(self, q, shared=0):
+        """A workspace for attend with queries of this shape."""
+        import torch
+        n, rows, hq, _ = q.shape
+        b = hf_attention_pages_workspace(self._ref, n, rows, hq, shared)
+        if b == 0:
+            raise ValueError("attend_workspace: sizes out of range")
+        return torch.empty(b, dtype=torch.uint8, device=self.k.device)
+
+    def attend(self, q, requests=None, *, layer=0, shared=0, scale=0.0, out=None, workspace=None, stream=None):
+        """hf_attention_pages: q [n, rows, Hq, dh] are the newest `rows` tokens of the
+        requests; returns out of the same shape."""
+        import torch
+        on = _On(self.k, stream)
+        if q.dim() != 4 or q.shape[3] != self._d.head_dim:
+            raise ValueError("q must be [requests, rows, heads, head_dim]")
+        n, rows, hq, dh = q.shape
+
+        def ld(t, name):
+            s = _heads_ld(t, name)
+            if rows == 1 and n > 1:
+                s = t.stride(0)
+            elif n > 1 and t.stride(0) != rows * s:
+                raise ValueError(f"{name}: its rows must be evenly spaced")
+            return s
+
+        qp = on.arg(q, "q", self.k.dtype, None, False)
+        if out is None:
+            out = on.empty(tuple(q.shape), q.dtype)
+        op = on.arg(out, "out", q.dtype, tuple(q.shape), False)
+        if workspace is None:
+            b = hf_attention_pages_workspace(self._ref, n, rows, hq, shared)
+            workspace = on.empty((max(b, 16),), torch.uint8)
+        wp = on.arg(workspace, "workspace", torch.uint8)
+        on.call(hf_attention_pages, self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._lists(on, requests, n),
+                shared, float(scale or 0.0), op, ld(out, "out"), wp, workspace.numel())
+        return out

@@ -1,0 +1,118 @@
+// Attention of query rows over packed prompts or a paged cache: what its variants
+// (attn_rows.cu on CUDA cores, attn_tc.cu and attn_own.cu on tensor cores) share.
+//
+// Rows that use one KV head are numbered token * G + (query head in its group), so
+// that a tile of rows always shares its keys, whatever the group size G is.
+#pragma once
+
+#include "common.cuh"
+
+namespace hf {
+
+struct AttnRows {
+  int Hq, Hkv, G, dh, esize;
+  float qscale;  // scale * log2(e): scores are kept in the base-2 domain
+  const void* q;
+  long long q_ld;  // elements
+  void* out;
+  long long out_ld;
+  int32_t* status;
+  // prompts
+  const void* k;  // packed: [total, k_ld]; paged: the layer's pool
+  const void* v;
+  long long k_ld, v_ld;
+  const int32_t* off;
+  int n_seq, total;
+  // paged cache
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* req;
+  int n, rows, page, n_pages, n_requests, table_ld;
+  int shared;      // tokens of the common prefix
+  // pieces of the key axis: npre of the prefix (pre_keys keys each), then up to
+  // nown of each request's own tokens (own_keys each). One piece in all: rows go
+  // straight to out; else to part_o / part_ml, piece by piece, rows (token, query
+  // head) within, joined by attn_join.
+  int npre, pre_keys, nown, own_keys;
+  float* part_o;   // [npre + nown][n * rows * Hq][dh], not normalised
+  float2* part_ml; // the same rows: maximum (base 2), sum
+};
+
+__host__ __device__ inline bool attn_direct(const AttnRows& a) { return a.npre + a.nown == 1; }
+
+// Length of entry i as the call takes it: 0 for entries that break a rule (bad set).
+__device__ __forceinline__ int attn_raw_len(const AttnRows& a, int i, bool& bad) {
+  const int r = a.req ? __ldg(&a.req[i]) : i;
+  if (r < 0 || r >= a.n_requests) {
+    bad = true;
+    return 0;
+  }
+  const int len = __ldg(&a.lens[r]);
+  if (len < 0 || len > (long long)a.table_ld * a.page || (len > 0 && len < a.shared)) {
+    bad = true;
+    return 0;
+  }
+  return len;
+}
+__device__ __forceinline__ int attn_len(const AttnRows& a, int i, bool& bad) {
+  const int len = attn_raw_len(a, i, bad);
+  if (len > 0 && a.shared > 0 && i > 0 && attn_raw_len(a, 0, bad) == 0) {
+    bad = true;
+    return 0;
+  }
+  return len;
+}
+
+__device__ __forceinline__ const int32_t* attn_table(const AttnRows& a, int i) {
+  const int r = a.req ? __ldg(&a.req[i]) : i;
+  return a.table + (size_t)r * a.table_ld;
+}
+
+// Slot of a prompt tile -> sequence and tile within it: a sequence of rows
+// [off_s, off_e) owns the slots [floor(off_s G / BM) + s, floor(off_e G / BM) + s + 1),
+// at least as many as it has tiles, so no prefix sum over the sequences is needed.
+__host__ __device__ inline long long prompt_slots(long long total, int n_seq, int G, int BM) {
+  return total * G / BM + n_seq;
+}
+struct PromptTile {
+  int start, len, tile;  // first row and length of the sequence, tile in it
+  bool ok;
+};
+__device__ __forceinline__ PromptTile prompt_tile(const AttnRows& a, int slot, int BM) {
+  int lo = 0, hi = a.n_seq;  // the last sequence whose first slot is at or before `slot`
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    const long long first = (long long)max(0, min(__ldg(&a.off[mid]), a.total)) * a.G / BM + mid;
+    if (first <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  PromptTile t{};
+  const int s0 = __ldg(&a.off[lo]), s1 = __ldg(&a.off[lo + 1]);
+  t.ok = s0 >= 0 && s0 <= s1 && s1 <= a.total;
+  if (!t.ok) return t;
+  t.start = s0;
+  t.len = s1 - s0;
+  t.tile = slot - (int)((long long)s0 * a.G / BM + lo);
+  t.ok = t.tile >= 0 && (long long)t.tile * BM < (long long)t.len * a.G;
+  return t;
+}
+
+// One CTA's check of the whole list of sequence bounds.
+__device__ __forceinline__ void check_offsets(const AttnRows& a) {
+  if (!a.status) return;
+  bool bad = false;
+  for (int s = threadIdx.x; s <= a.n_seq; s += blockDim.x) {
+    const int x = __ldg(&a.off[s]);
+    bad = bad || x < 0 || x > a.total || (s > 0 && x < __ldg(&a.off[s - 1]));
+  }
+  if (bad) atomicOr(a.status, HF_S_BAD);
+}
+
+cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
+cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st);
+cudaError_t launch_attn_rows_own(int dtype, const AttnRows& a, cudaStream_t st);
+cudaError_t launch_attn_join(int dtype, const AttnRows& a, cudaStream_t st);
+
+}  // namespace hf

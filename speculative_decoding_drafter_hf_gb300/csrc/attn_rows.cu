@@ -1,0 +1,578 @@
+// Attention of query rows on CUDA cores, and the entry points hf_attention_prompt
+// and hf_attention_pages.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(s_ij - m_i),  s_ij = qscale q_i.k_j
+// over the keys j < limit_i, in one pass over the keys: a tile's scores raise the
+// running maximum m_i, and what was summed so far is scaled by 2^(old m - new m).
+//
+// A CTA takes 64 rows of one KV head and walks its keys in tiles of 64: 16 x 16
+// threads, 4 x 4 scores each, then the same 4 rows times the value columns 4 tx +
+// 64 c. Everything is fp32 in shared memory and registers: this is the variant for
+// fp32 inputs and for head dims that the tensor-core kernels do not take; bound by
+// the fp32 multiply-adds.
+//
+// Masked keys: scores are selected, never added to a mask value, so whatever K
+// holds there cannot matter; V's non-finite values in a tile that any row masks
+// are taken as zero (0 * NaN would reach every row) and added back at the end to
+// the rows that do see them.
+#include <cmath>
+#include <cstdio>
+#include <mutex>
+
+#include "attn.cuh"
+#include "pages.cuh"
+
+namespace hf {
+namespace {
+
+constexpr int BM = 64, BN = 64, RT = 256;
+constexpr int PLD = BN + 4;
+enum { PROMPT = 0, PREFIX = 1, OWN = 2 };
+
+__host__ __device__ inline size_t rows_smem(int dh) {
+  return ((size_t)(BM + 2 * BN) * (dh + 4) + (size_t)BM * PLD) * sizeof(float);
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ bool odd_value(float x) { return !(fabsf(x) < INFINITY); }
+
+// Element offset of key j's row of KV head g in K (kind 0) or V; -1: no such page.
+template <int MODE>
+__device__ __forceinline__ long long key_at(const AttnRows& a, int start, const int32_t* tab, int g, int j, int kv) {
+  if (MODE == PROMPT) return (long long)(start + j) * (kv ? a.v_ld : a.k_ld) + (long long)g * a.dh;
+  const int id = __ldg(&tab[j / a.page]);
+  if (id < 0 || id >= a.n_pages) return -1;
+  return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
+}
+
+template <typename T, int MODE, int MAXC>
+__global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
+  extern __shared__ __align__(16) float smf[];
+  const int dh = a.dh, ldq = dh + 4;
+  float* sq = smf;
+  float* sk = sq + BM * ldq;
+  float* sv = sk + BN * ldq;
+  float* sp = sv + BN * ldq;
+  __shared__ int s_odd;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  pdl_trigger();
+  pdl_wait();
+
+  // the item: rows [row0, row0 + nrows) of KV head g, keys [j0, j1)
+  const int g = blockIdx.y;
+  int row0, nrows, j0 = 0, j1, start = 0, entry = 0, piece = 0, len = 0;
+  const int32_t* tab = nullptr;
+  if (MODE == PROMPT) {
+    if (blockIdx.x == 0 && g == 0) check_offsets(a);
+    const PromptTile t = prompt_tile(a, (int)(gridDim.x - 1 - blockIdx.x), BM);
+    if (!t.ok) return;
+    start = t.start;
+    row0 = t.tile * BM;
+    nrows = (int)min((long long)BM, (long long)t.len * a.G - row0);
+    j1 = (row0 + nrows - 1) / a.G + 1;
+  } else if (MODE == PREFIX) {
+    row0 = blockIdx.x * BM;
+    nrows = min(BM, a.n * a.rows * a.G - row0);
+    piece = blockIdx.z;
+    j0 = piece * a.pre_keys;
+    j1 = min(a.shared, j0 + a.pre_keys);
+    bool bad = false;
+    if (attn_raw_len(a, 0, bad) == 0) {  // nothing is shared then: every row is empty
+      j1 = j0;
+    } else {
+      tab = attn_table(a, 0);
+    }
+  } else {
+    const int blocks = (a.rows * a.G + BM - 1) / BM;
+    entry = blockIdx.x / blocks;
+    row0 = (blockIdx.x % blocks) * BM;
+    nrows = min(BM, a.rows * a.G - row0);
+    piece = a.npre + blockIdx.z;
+    bool bad = false;
+    len = attn_len(a, entry, bad);
+    j0 = a.shared + blockIdx.z * a.own_keys;
+    j1 = min(len, j0 + a.own_keys);
+    if (blockIdx.z > 0 && j0 >= j1) return;  // piece 0 always reports (a direct call has no other)
+    if (len > 0) {
+      tab = attn_table(a, entry);
+      if (blockIdx.z == 0 && g == 0 && row0 == 0 && a.shared > 0) {
+        const int32_t* first = attn_table(a, 0);
+        for (int j = tid; j < a.shared / a.page; j += RT) bad = bad || __ldg(&tab[j]) != __ldg(&first[j]);
+      }
+    }
+    if (bad && a.status && blockIdx.z == 0 && g == 0 && row0 == 0) atomicOr(a.status, HF_S_BAD);
+  }
+
+  // this thread's rows: keys they see, and where they come from and go to
+  int limit[4];
+  size_t orow[4];  // token row of q and out
+  int head[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = row0 + ty * 4 + i;
+    limit[i] = 0;
+    orow[i] = 0;
+    head[i] = 0;
+    if (ty * 4 + i >= nrows) continue;
+    const int t = rr / a.G;
+    head[i] = g * a.G + rr % a.G;
+    if (MODE == PROMPT) {
+      limit[i] = t + 1;
+      orow[i] = (size_t)start + t;
+    } else if (MODE == PREFIX) {
+      bool bad = false;
+      const int l = attn_len(a, t / a.rows, bad);
+      limit[i] = max(0, min(a.shared, l - a.rows + t % a.rows + 1));
+      orow[i] = t;
+    } else {
+      limit[i] = max(0, len - a.rows + t + 1);
+      orow[i] = (size_t)entry * a.rows + t;
+    }
+  }
+  if (tid == 0) s_odd = 0;
+  const int c4 = dh / 4;
+  for (int e = tid; e < BM * c4; e += RT) {
+    const int r = e / c4, c = (e % c4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nrows) {
+      const int rr = row0 + r, t = rr / a.G;
+      const size_t qr = MODE == PROMPT ? (size_t)start + t : MODE == PREFIX ? (size_t)t : (size_t)entry * a.rows + t;
+      x = load4(static_cast<const T*>(a.q) + qr * a.q_ld + (size_t)(g * a.G + rr % a.G) * dh + c);
+    }
+    *reinterpret_cast<float4*>(&sq[r * ldq + c]) =
+        make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
+  }
+
+  float m[4], l[4], o[4][MAXC * 4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < MAXC * 4; ++c) o[i][c] = 0.f;
+  }
+  const int low = min(min(limit[0], limit[1]), min(limit[2], limit[3]));
+  int odd_from = j1;  // first key of a tile whose odd values were taken as zero
+
+  for (int jt = j0; jt < j1; jt += BN) {
+    __syncthreads();
+    for (int e = tid; e < 2 * BN * c4; e += RT) {
+      const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (jt + j < j1) {
+        const long long at = key_at<MODE>(a, start, tab, g, jt + j, kv);
+        if (at >= 0)
+          x = load4(static_cast<const T*>(kv ? a.v : a.k) + at + c);
+        else if (a.status)
+          atomicOr(a.status, HF_S_BAD);
+      }
+      *reinterpret_cast<float4*>(&(kv ? sv : sk)[j * ldq + c]) = x;
+    }
+    // some row masks keys of this tile: its odd values of V are set aside
+    const bool cut = __syncthreads_or(low < jt + BN && low < j1);
+    if (cut) {
+      bool odd = false;
+      for (int e = tid; e < BN * dh; e += RT) {
+        float* x = &sv[(e / dh) * ldq + e % dh];
+        if (odd_value(*x)) {
+          *x = 0.f;
+          odd = true;
+        }
+      }
+      if (__syncthreads_or(odd)) odd_from = min(odd_from, jt);
+    }
+
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int d = 0; d < dh; d += 4) {
+      float4 qv[4], kv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sq[(ty * 4 + i) * ldq + d]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sk[(tx + 16 * j) * ldq + d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, s[i][j]))));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lim = min(limit[i], j1);
+      float t = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (jt + tx + 16 * j >= lim) s[i][j] = -INFINITY;
+        t = fmaxf(t, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
+      const float nm = fmaxf(m[i], t);
+      const float base = nm > -INFINITY ? nm : 0.f;  // a row that has seen nothing: all terms 2^-inf = 0
+      const float f = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[i][j] - base);
+        sum += e;
+        sp[(ty * 4 + i) * PLD + tx + 16 * j] = e;
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[i] = l[i] * f + sum;
+      m[i] = nm;
+#pragma unroll
+      for (int c = 0; c < MAXC * 4; ++c) o[i][c] *= f;
+    }
+    __syncwarp();  // a row's 16 threads are in one warp
+    for (int j = 0; j < BN; j += 4) {
+      float4 p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&sp[(ty * 4 + i) * PLD + j]);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c) {
+          if (tx * 4 + 64 * c >= dh) continue;
+          const float4 x = *reinterpret_cast<const float4*>(&sv[(j + jj) * ldq + tx * 4 + 64 * c]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+            o[i][4 * c + 0] = fmaf(w, x.x, o[i][4 * c + 0]);
+            o[i][4 * c + 1] = fmaf(w, x.y, o[i][4 * c + 1]);
+            o[i][4 * c + 2] = fmaf(w, x.z, o[i][4 * c + 2]);
+            o[i][4 * c + 3] = fmaf(w, x.w, o[i][4 * c + 3]);
+          }
+        }
+    }
+  }
+
+  if (odd_from < j1) {  // rows that see an odd value of V get it after all
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      for (int j = odd_from; j < min(limit[i], j1); ++j) {
+        const long long at = key_at<MODE>(a, start, tab, g, j, 1);
+        if (at < 0) continue;
+#pragma unroll
+        for (int c = 0; c < MAXC * 4; ++c) {
+          const int d = tx * 4 + 64 * (c / 4) + c % 4;
+          if (d >= dh) continue;
+          const float x = to_f(static_cast<const T*>(a.v)[at + d]);
+          if (odd_value(x)) o[i][c] += x;
+        }
+      }
+  }
+  const bool direct = MODE == PROMPT || attn_direct(a);
+  const size_t N = (size_t)a.n * a.rows * a.Hq;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (ty * 4 + i >= nrows) continue;
+    if (direct) {
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+      T* dst = static_cast<T*>(a.out) + orow[i] * a.out_ld + (size_t)head[i] * dh;
+#pragma unroll
+      for (int c = 0; c < MAXC * 4; ++c) {
+        const int d = tx * 4 + 64 * (c / 4) + c % 4;
+        if (d < dh) dst[d] = from_f<T>(o[i][c] * inv);
+      }
+    } else {
+      const size_t r = piece * N + orow[i] * a.Hq + head[i];
+      if (tx == 0) a.part_ml[r] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c)
+        if (tx * 4 + 64 * c < dh)
+          *reinterpret_cast<float4*>(&a.part_o[r * dh + tx * 4 + 64 * c]) =
+              make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
+    }
+  }
+}
+
+// One warp per row: the row's pieces weighted by 2^(m - max m).
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, dh = a.dh;
+  const size_t N = (size_t)a.n * a.rows * a.Hq;
+  const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= N) return;
+  const int token = (int)(row / a.Hq), head = (int)(row % a.Hq);
+  bool bad = false;
+  const int len = attn_len(a, token / a.rows, bad);
+  const int own = (max(0, len - a.shared) + a.own_keys - 1) / a.own_keys;
+  const int pieces = len > 0 ? a.npre + own : 0;  // the prefix's come first
+  float m = -INFINITY;
+  for (int p = lane; p < pieces; p += 32) m = fmaxf(m, __ldcg(&a.part_ml[p * N + row]).x);
+  m = warp_max(m);
+  float acc[8] = {};
+  float l = 0.f;
+  const float base = m > -INFINITY ? m : 0.f;
+  for (int p = 0; p < pieces; ++p) {
+    const float2 ml = __ldcg(&a.part_ml[p * N + row]);
+    if (ml.y == 0.f) continue;  // saw nothing there (its row holds zeros)
+    const float w = exp2f(ml.x - base);
+    l = fmaf(ml.y, w, l);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (lane * 4 + 128 * c < dh) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(&a.part_o[(p * N + row) * dh + lane * 4 + 128 * c]));
+        acc[4 * c + 0] = fmaf(w, x.x, acc[4 * c + 0]);
+        acc[4 * c + 1] = fmaf(w, x.y, acc[4 * c + 1]);
+        acc[4 * c + 2] = fmaf(w, x.z, acc[4 * c + 2]);
+        acc[4 * c + 3] = fmaf(w, x.w, acc[4 * c + 3]);
+      }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(a.out) + (size_t)token * a.out_ld + (size_t)head * dh;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (lane * 4 + 128 * c < dh)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dst[lane * 4 + 128 * c + k] = from_f<T>(acc[4 * c + k] * inv);
+}
+
+constexpr int kMaxDev = 64;
+std::mutex g_mu;
+bool g_set[kMaxDev][2][3][3] = {};
+
+template <typename T, int MODE, int MAXC>
+cudaError_t launch_one(const AttnRows& a, dim3 grid, cudaStream_t st) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][MAXC / 2];
+    if (!set || dev >= kMaxDev) {
+      e = cudaFuncSetAttribute(rows_kernel<T, MODE, MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)rows_smem(64 * MAXC));
+      if (e != cudaSuccess) return e;
+      set = true;
+    }
+  }
+  return launch_pdl(rows_kernel<T, MODE, MAXC>, grid, dim3(RT), rows_smem(a.dh), st, a);
+}
+
+template <int MODE>
+cudaError_t launch_mode(int dtype, const AttnRows& a, dim3 grid, cudaStream_t st) {
+  const int c = a.dh <= 64 ? 1 : a.dh <= 128 ? 2 : 4;
+  using bf = __nv_bfloat16;
+  if (dtype == HF_F32)
+    return c == 1 ? launch_one<float, MODE, 1>(a, grid, st)
+                  : c == 2 ? launch_one<float, MODE, 2>(a, grid, st) : launch_one<float, MODE, 4>(a, grid, st);
+  return c == 1 ? launch_one<bf, MODE, 1>(a, grid, st)
+                : c == 2 ? launch_one<bf, MODE, 2>(a, grid, st) : launch_one<bf, MODE, 4>(a, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st) {
+  return launch_mode<PROMPT>(dtype, a, dim3((unsigned)prompt_slots(a.total, a.n_seq, a.G, BM), a.Hkv), st);
+}
+cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st) {
+  const long long rows = (long long)a.n * a.rows * a.G;
+  return launch_mode<PREFIX>(dtype, a, dim3((unsigned)((rows + BM - 1) / BM), a.Hkv, a.npre), st);
+}
+cudaError_t launch_attn_rows_own(int dtype, const AttnRows& a, cudaStream_t st) {
+  const int blocks = (a.rows * a.G + BM - 1) / BM;
+  return launch_mode<OWN>(dtype, a, dim3((unsigned)(a.n * blocks), a.Hkv, a.nown), st);
+}
+cudaError_t launch_attn_join(int dtype, const AttnRows& a, cudaStream_t st) {
+  const long long N = (long long)a.n * a.rows * a.Hq;
+  const dim3 grid((unsigned)((N + 7) / 8));
+  if (dtype == HF_F32) return launch_pdl(join_kernel<float>, grid, dim3(256), 0, st, a);
+  return launch_pdl(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a);
+}
+
+namespace {
+
+hf_status refuse(const char* m) {
+  set_thread_error(m);
+  return HF_EINVAL;
+}
+hf_status done(cudaError_t e) {
+  if (e == cudaSuccess) return HF_OK;
+  set_thread_error(cudaGetErrorString(e));
+  return HF_ECUDA;
+}
+bool off(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+const char* heads_bad(int hq, int hkv, int dh, float scale) {
+  if (hq < 1 || hkv < 1 || hkv > 1024 || hq % hkv) return "n_kv_heads must be 1..1024 and divide n_q_heads";
+  if (hq / hkv > 64) return "n_q_heads / n_kv_heads must be <= 64";
+  if (dh < 8 || dh % 8 || dh > 256) return "head_dim must be a multiple of 8, <= 256";
+  if (!(scale >= 0.f) || !(scale < INFINITY)) return "scale must be finite and >= 0 (0: 1/sqrt(head_dim))";
+  return nullptr;
+}
+const char* ld_bad(int64_t ld, long long least, int esize, const void* p) {
+  if (ld < least || ld > (1LL << 40)) return "a row stride is smaller than heads * head_dim";
+  if (ld * esize % 16 || off(p, 16)) return "q, k, v and out must be 16-byte aligned, their strides multiples of 16 bytes";
+  return nullptr;
+}
+float base2_scale(float scale, int dh) {
+  return (float)(1.4426950408889634 * (scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)dh)));
+}
+
+// Pieces of the key axis: as many as give every SM two CTAs, of at least 256 keys.
+// A request's own pieces go by its table's reach, not by its length, which only the
+// device knows: at most 16.
+void plan_pieces(AttnRows& a) {
+  const long long pre_tiles = ((long long)a.n * a.rows * a.G + BM - 1) / BM * a.Hkv;
+  auto split = [](long long keys, long long tiles, int most, int& count, int& each) {
+    if (keys <= 0) {
+      count = 0;
+      each = 256;
+      return;
+    }
+    long long c = std::max<long long>(1, std::min<long long>({(304 + tiles - 1) / std::max<long long>(tiles, 1), (keys + 255) / 256, (long long)most}));
+    each = (int)(((keys + c - 1) / c + 127) / 128 * 128);
+    count = (int)((keys + each - 1) / each);
+  };
+  split(a.shared, pre_tiles, 32, a.npre, a.pre_keys);
+  const long long own = (long long)a.table_ld * a.page - a.shared;
+  const long long own_tiles = (long long)a.n * a.Hkv * ((a.rows * a.G + BM - 1) / BM);
+  split(own, own_tiles, 32, a.nown, a.own_keys);
+  a.nown = std::max(a.nown, 1);  // it also reports bad entries, and writes the empty rows of a direct call
+}
+
+const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq, int shared, AttnRows& a) {
+  if (const char* m = pages_bad(p, buffers)) return m;
+  if (const char* m = heads_bad(hq, p->n_kv_heads, p->head_dim, 0.f)) return m;
+  if (n < 0 || n > (1 << 20)) return "n must be 0..1048576";
+  if (rows < 1 || rows > 64) return "rows must be 1..64";
+  if (shared < 0 || shared % p->page || shared > (long long)p->table_ld * p->page)
+    return "shared must be a multiple of page, at most table_ld * page";
+  if ((long long)n * rows * hq > 0x7fffffffLL / 4) return "n * rows * n_q_heads is too large";
+  a.Hq = hq;
+  a.Hkv = p->n_kv_heads;
+  a.G = hq / p->n_kv_heads;
+  a.dh = p->head_dim;
+  a.esize = p->dtype == HF_F32 ? 4 : 2;
+  a.table = p->table;
+  a.lens = p->lens;
+  a.status = p->status;
+  a.n = n;
+  a.rows = rows;
+  a.page = p->page;
+  a.n_pages = p->n_pages;
+  a.n_requests = p->n_requests;
+  a.table_ld = p->table_ld;
+  a.shared = shared;
+  plan_pieces(a);
+  return nullptr;
+}
+size_t part_bytes(const AttnRows& a, size_t& ml) {
+  const size_t rows = (size_t)(a.npre + a.nown) * a.n * a.rows * a.Hq;
+  ml = rows * a.dh * sizeof(float);
+  return attn_direct(a) ? 16 : ml + rows * sizeof(float2);
+}
+
+}  // namespace
+}  // namespace hf
+
+extern "C" hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t total, int32_t n_q_heads,
+                                         int32_t n_kv_heads, int32_t head_dim, const void* q, int64_t q_ld,
+                                         const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                                         const int32_t* offsets, float scale, void* out, int64_t out_ld,
+                                         int32_t* status, void* stream) {
+  using namespace hf;
+  if (dtype != HF_F32 && dtype != HF_BF16) return refuse("dtype must be HF_F32 or HF_BF16");
+  if (n_seq < 0 || n_seq > (1 << 24) || total < 0) return refuse("n_seq must be 0..16777216 and total >= 0");
+  if (const char* m = heads_bad(n_q_heads, n_kv_heads, head_dim, scale)) return refuse(m);
+  if ((long long)total * (n_q_heads / n_kv_heads) > 0x7fffffffLL) return refuse("total * group is too large");
+  if (n_seq == 0 || total == 0) return HF_OK;
+  if (!q || !k || !v || !offsets || !out) return refuse("NULL buffer");
+  const int esize = dtype == HF_F32 ? 4 : 2;
+  const long long qd = (long long)n_q_heads * head_dim, kd = (long long)n_kv_heads * head_dim;
+  for (const char* m : {ld_bad(q_ld, qd, esize, q), ld_bad(k_ld, kd, esize, k), ld_bad(v_ld, kd, esize, v),
+                        ld_bad(out_ld, qd, esize, out)})
+    if (m) return refuse(m);
+  if (off(offsets, 4) || off(status, 4)) return refuse("offsets and status must be 4-byte aligned");
+  AttnRows a{};
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.G = n_q_heads / n_kv_heads;
+  a.dh = head_dim;
+  a.esize = esize;
+  a.qscale = base2_scale(scale, head_dim);
+  a.q = q;
+  a.q_ld = q_ld;
+  a.k = k;
+  a.k_ld = k_ld;
+  a.v = v;
+  a.v_ld = v_ld;
+  a.out = out;
+  a.out_ld = out_ld;
+  a.off = offsets;
+  a.n_seq = n_seq;
+  a.total = total;
+  a.status = status;
+  return done(launch_attn_rows_prompt(dtype, a, (cudaStream_t)stream));
+}
+
+extern "C" size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows, int32_t n_q_heads,
+                                               int32_t shared) {
+  hf::AttnRows a{};
+  if (hf::pages_args(p, false, std::max(n, 1), rows, n_q_heads, shared, a)) return 0;
+  size_t ml;
+  return hf::part_bytes(a, ml);
+}
+
+extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_t n, int32_t rows,
+                                        int32_t n_q_heads, const void* q, int64_t q_ld, const int32_t* requests,
+                                        int32_t shared, float scale, void* out, int64_t out_ld, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  using namespace hf;
+  AttnRows a{};
+  if (const char* m = pages_args(p, true, n, rows, n_q_heads, shared, a)) return refuse(m);
+  if (const char* m = heads_bad(n_q_heads, p->n_kv_heads, p->head_dim, scale)) return refuse(m);
+  if (layer < 0 || layer >= p->n_layers) return refuse("layer must be a layer of the cache");
+  if (!requests && n > p->n_requests) return refuse("n must be <= n_requests without a list of requests");
+  if (n == 0) return HF_OK;
+  if (!q || !out || !workspace) return refuse("NULL buffer");
+  for (const char* m : {ld_bad(q_ld, (long long)n_q_heads * p->head_dim, a.esize, q),
+                        ld_bad(out_ld, (long long)n_q_heads * p->head_dim, a.esize, out)})
+    if (m) return refuse(m);
+  if (off(requests, 4)) return refuse("requests must be 4-byte aligned");
+  size_t ml;
+  const size_t need = part_bytes(a, ml);
+  if (off(workspace, 16) || workspace_bytes < need) {
+    char m[160];
+    snprintf(m, sizeof m, "workspace must be 16-byte aligned and hold %zu bytes (hf_attention_pages_workspace), got %zu",
+             need, workspace_bytes);
+    return refuse(m);
+  }
+  const size_t layer_bytes = (size_t)p->n_pages * pages_block(p) * a.esize;
+  a.qscale = base2_scale(scale, p->head_dim);
+  a.q = q;
+  a.q_ld = q_ld;
+  a.out = out;
+  a.out_ld = out_ld;
+  a.k = static_cast<const uint8_t*>(p->k) + layer * layer_bytes;
+  a.v = static_cast<const uint8_t*>(p->v) + layer * layer_bytes;
+  a.req = requests;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ml);
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
+  if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
+  if (e == cudaSuccess && !attn_direct(a)) e = launch_attn_join(p->dtype, a, st);
+  return done(e);
+}

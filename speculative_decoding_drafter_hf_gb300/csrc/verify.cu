@@ -1,0 +1,467 @@
+// Verification of drafted tokens by speculative sampling (hf_verify_tokens).
+//
+// Per request: p_s = softmax(x_s / T), q_s = softmax(y_s / T); draft s passes
+// iff u_s q_s(d_s) < p_s(d_s); the next token is argmax_i w_i / e_i with
+// w = max(p_a - q_a, 0) at the first slot a that did not pass (w = p_a when all
+// did). The race w_i / e_i draws i with probability w_i / sum(w) and needs no
+// prefix sum over the vocabulary: its result depends on two neighbouring
+// scores only, not on the order in which a sum was formed.
+//
+// Two launches. verify_stats reads every logit once: (row, chunk) CTAs form
+// the chunk's maximum and sum of exponentials (T = 0: maximum and its lowest
+// index, target rows only). verify_race: each (request, chunk) CTA joins its
+// request's chunks, finds the stop slot, and runs the race over its chunk of
+// that slot's rows; the request's last CTA (ticket) joins the chunks. Bound by
+// the reads of the logits.
+#include <cstdio>
+
+#include "common.cuh"
+
+namespace hf {
+namespace {
+
+constexpr int VT = 256;         // threads per CTA
+constexpr int VMAXS = 16;       // drafted tokens per request
+constexpr float kNegInf = -INFINITY;
+
+struct VArgs {
+  const void* x;  // target logits
+  const void* y;  // draft logits (or NULL)
+  long long x_ld, y_ld, e_ld;
+  const int32_t* tok;
+  const int32_t* n_draft;
+  const float* u;
+  const float* e;  // noise
+  const float* temp;
+  int B, S, V;
+  int chunk, nchunk;    // stats: vocabulary entries per CTA
+  int rchunk, nrchunk;  // race
+  float2* stats;        // [B * (2S + 1)][nchunk]: target rows, then draft rows, per request
+  float4* race;         // [B][nrchunk]: best w score, its index, best p score, its index
+  int* tickets;         // [B]
+  int32_t* n_acc;
+  int32_t* out;
+  int32_t* status;
+};
+
+__device__ __forceinline__ bool temp_ok(float t) { return t >= 0.f && t < INFINITY; }
+
+// Calls f(index, value) for the entries [i0, i1) of a row: single loads up to a
+// 16-byte boundary, 16-byte loads (UN of them in flight) from there.
+template <typename T, int UN, typename F>
+__device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& f) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  const int tid = threadIdx.x;
+  const int off = (int)((reinterpret_cast<uintptr_t>(row + i0) & 15) / sizeof(T));
+  const int head = min(i1 - i0, off ? VE - off : 0);
+  if (tid < head) f(i0 + tid, to_f(row[i0 + tid]));
+  const int b0 = i0 + head, nv = (i1 - b0) / VE;
+  const uint4* p = reinterpret_cast<const uint4*>(row + b0);
+  for (int v0 = tid; v0 < nv; v0 += VT * UN) {
+    uint4 r[UN];
+#pragma unroll
+    for (int k = 0; k < UN; ++k)
+      if (v0 + k * VT < nv) r[k] = __ldcs(p + v0 + k * VT);
+#pragma unroll
+    for (int k = 0; k < UN; ++k)
+      if (v0 + k * VT < nv) {
+        const T* t = reinterpret_cast<const T*>(&r[k]);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) f(b0 + (v0 + k * VT) * VE + j, to_f(t[j]));
+      }
+  }
+  const int t0 = b0 + nv * VE;
+  if (t0 + tid < i1) f(t0 + tid, to_f(row[t0 + tid]));
+}
+
+// (m, l) of two parts: maximum and sum of 2^((x - m) c). A part without
+// anything above -infinity has m = -infinity, l = 0.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2, float c) {
+  const float mm = fmaxf(m, m2);
+  if (mm > kNegInf) {
+    l = (m > kNegInf ? l * exp2f((m - mm) * c) : l) + (m2 > kNegInf ? l2 * exp2f((m2 - mm) * c) : l2);
+  } else {
+    l += l2;
+  }
+  m = mm;
+}
+
+// (value, lowest index) of the larger of two.
+__device__ __forceinline__ void best(float& v, int& i, float v2, int i2) {
+  if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
+    v = v2;
+    i = i2;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t, int chunk, float2* out) {
+  __shared__ float sm[VT / 32], sl[VT / 32];
+  __shared__ int si[VT / 32];
+  const int i0 = chunk * a.chunk, i1 = min(a.V, i0 + a.chunk);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (t == 0.f) {
+    float v = kNegInf;
+    int idx = -1;
+    for_row<T, 4>(row, i0, i1, [&](int i, float x) {
+      if (x > v) {  // a thread's entries come in rising order: the first of equals stays
+        v = x;
+        idx = i;
+      }
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      best(v, idx, __shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, idx, o));
+    if (lane == 0) {
+      sm[warp] = v;
+      si[warp] = idx;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < VT / 32; ++w) best(v, idx, sm[w], si[w]);
+      *out = make_float2(v, __int_as_float(idx));
+    }
+    return;
+  }
+  const float c = 1.4426950408889634f / t;
+  float m = kNegInf, l = 0.f;
+  for_row<T, 4>(row, i0, i1, [&](int, float x) {
+    if (x > m) {
+      l = m > kNegInf ? l * exp2f((m - x) * c) : l;
+      m = x;
+    }
+    // x <= m, or NaN (which stays in l); m = x = -infinity adds nothing
+    if (!(x == kNegInf)) l += exp2f((x - m) * c);
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+    join(m, l, m2, l2, c);
+  }
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < VT / 32; ++w) join(m, l, sm[w], sl[w], c);
+    *out = make_float2(m, l);
+  }
+}
+
+// One CTA per (row, chunk): rows b * (2S + 1) + s, s <= S the target's, then the
+// draft's.
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(VT) verify_stats(VArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int chunk = blockIdx.x % a.nchunk, r = blockIdx.x / a.nchunk;
+  const int per = a.y ? 2 * a.S + 1 : a.S + 1;
+  const int b = r / per, s = r % per;
+  if (s == 0 && chunk == 0 && threadIdx.x == 0) a.tickets[b] = 0;
+  const float t = a.temp ? __ldg(&a.temp[b]) : 1.f;
+  const int nd = a.n_draft ? __ldg(&a.n_draft[b]) : a.S;
+  if (!temp_ok(t)) return;
+  float2* out = a.stats + ((size_t)b * (2 * a.S + 1) + s) * a.nchunk + chunk;
+  if (s <= a.S) {
+    if (s > nd) return;
+    stats_cta<TX>(a, static_cast<const TX*>(a.x) + ((size_t)b * (a.S + 1) + s) * a.x_ld, t, chunk, out);
+  } else {
+    if (t == 0.f || s - a.S - 1 >= nd) return;
+    stats_cta<TY>(a, static_cast<const TY*>(a.y) + ((size_t)b * a.S + s - a.S - 1) * a.y_ld, t, chunk, out);
+  }
+}
+
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(VT) verify_race(VArgs a) {
+  __shared__ float sm[2 * VMAXS + 1], sl[2 * VMAXS + 1];
+  __shared__ int s_stop, s_bad, s_last;
+  __shared__ float4 red[VT / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int chunk = blockIdx.x % a.nrchunk, b = blockIdx.x / a.nrchunk;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, S = a.S;
+  const float t = a.temp ? __ldg(&a.temp[b]) : 1.f;
+  const int nd = a.n_draft ? __ldg(&a.n_draft[b]) : S;
+  const bool range_ok = temp_ok(t) && nd >= 0 && nd <= S;
+  const bool cold = t == 0.f;
+  const float c = cold ? 0.f : 1.4426950408889634f / t;
+  if (range_ok) {
+    for (int r = warp; r < 2 * S + 1; r += VT / 32) {
+      if (r <= S ? r > nd : (cold || !a.y || r - S - 1 >= nd)) continue;
+      const float2* st = a.stats + ((size_t)b * (2 * S + 1) + r) * a.nchunk;
+      float m = kNegInf, l = 0.f;
+      int idx = -1;
+      for (int k = lane; k < a.nchunk; k += 32) {
+        const float2 v = __ldcg(&st[k]);
+        if (cold)
+          best(m, idx, v.x, __float_as_int(v.y));
+        else
+          join(m, l, v.x, v.y, c);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
+        if (cold)
+          best(m, idx, m2, __shfl_xor_sync(0xffffffffu, idx, o));
+        else
+          join(m, l, m2, __shfl_xor_sync(0xffffffffu, l, o), c);
+      }
+      if (lane == 0) {
+        sm[r] = m;
+        sl[r] = cold ? __int_as_float(idx) : l;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // lane s tests slot s; the first that fails is the stop slot
+    bool bad = !range_ok, pass = false, row_bad = false;
+    if (!bad && lane <= nd) {
+      const bool has = lane < nd;
+      const int d = has ? __ldg(&a.tok[(size_t)b * S + lane]) : 0;
+      if (d < 0 || d >= a.V) {
+        row_bad = true;
+      } else if (cold) {
+        const int idx = __float_as_int(sl[lane]);
+        row_bad = idx < 0;
+        pass = has && idx == d;
+      } else {
+        row_bad = !(sl[lane] > 0.f && sl[lane] < INFINITY);
+        float q = 1.f;
+        if (has && a.y) {
+          const float lq = sl[S + 1 + lane];
+          row_bad = row_bad || !(lq > 0.f && lq < INFINITY);
+          const float yv = to_f(static_cast<const TY*>(a.y)[((size_t)b * S + lane) * a.y_ld + d]);
+          q = exp2f((yv - sm[S + 1 + lane]) * c) / lq;
+        }
+        const float xv = to_f(static_cast<const TX*>(a.x)[((size_t)b * (S + 1) + lane) * a.x_ld + d]);
+        const float p = exp2f((xv - sm[lane]) * c) / sl[lane];
+        pass = has && !row_bad && __ldg(&a.u[(size_t)b * S + lane]) * q < p;
+      }
+    }
+    const unsigned fails = ~__ballot_sync(0xffffffffu, pass);
+    const unsigned bads = __ballot_sync(0xffffffffu, row_bad);
+    // a draft that names no token is refused wherever it stands
+    const int stop = __ffs(fails) - 1;
+    bool tok_bad = false;
+    if (range_ok && lane < nd) {
+      const int d = __ldg(&a.tok[(size_t)b * S + lane]);
+      tok_bad = d < 0 || d >= a.V;
+    }
+    tok_bad = __any_sync(0xffffffffu, tok_bad);
+    if (lane == 0) {
+      s_stop = stop;
+      s_bad = bad || tok_bad || (stop < 32 && ((bads >> stop) & 1));
+    }
+  }
+  __syncthreads();
+  const int stop = s_stop;
+  int32_t* out = a.out + (size_t)b * (S + 1);
+  if (s_bad || cold) {  // uniform in the request: no race
+    if (chunk == 0 && tid <= S) {
+      int v = -1;
+      if (!s_bad) v = tid < stop ? __ldg(&a.tok[(size_t)b * S + tid]) : tid == stop ? __float_as_int(sl[stop]) : -1;
+      out[tid] = v;
+      if (tid == 0) {
+        a.n_acc[b] = s_bad ? 0 : stop + 1;
+        if (s_bad && a.status) atomicOr(a.status, HF_S_BAD);
+      }
+    }
+    return;
+  }
+
+  // the race over this chunk of the stop slot's rows
+  const TX* x = static_cast<const TX*>(a.x) + ((size_t)b * (S + 1) + stop) * a.x_ld;
+  const bool residual = stop < nd;
+  const TY* y = residual && a.y ? static_cast<const TY*>(a.y) + ((size_t)b * S + stop) * a.y_ld : nullptr;
+  const int dtok = residual && !a.y ? __ldg(&a.tok[(size_t)b * S + stop]) : -1;
+  const float* e = a.e + (size_t)b * a.e_ld;
+  const float mp = sm[stop], ip = 1.f / sl[stop];
+  const float mq = y ? sm[S + 1 + stop] : 0.f, iq = y ? 1.f / sl[S + 1 + stop] : 0.f;
+  const int i0 = chunk * a.rchunk, i1 = min(a.V, i0 + a.rchunk);
+  float vw = 0.f, vp = 0.f;
+  int iw = -1, ipx = -1;
+#pragma unroll 4
+  for (int i = i0 + tid; i < i1; i += VT) {
+    const float p = exp2f((to_f(x[i]) - mp) * c) * ip;
+    float w = y ? p - exp2f((to_f(y[i]) - mq) * c) * iq : p;
+    if (i == dtok) w = 0.f;
+    const float n = __ldg(&e[i]);
+    if (w > 0.f) {
+      const float s = w / n;
+      if (iw < 0 ? s == s : s > vw) {
+        vw = s;
+        iw = i;
+      }
+    }
+    if (residual && p > 0.f) {
+      const float s = p / n;
+      if (ipx < 0 ? s == s : s > vp) {
+        vp = s;
+        ipx = i;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    best(vw, iw, __shfl_xor_sync(0xffffffffu, vw, o), __shfl_xor_sync(0xffffffffu, iw, o));
+    best(vp, ipx, __shfl_xor_sync(0xffffffffu, vp, o), __shfl_xor_sync(0xffffffffu, ipx, o));
+  }
+  if (lane == 0) red[warp] = make_float4(vw, __int_as_float(iw), vp, __int_as_float(ipx));
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < VT / 32; ++w) {
+      best(vw, iw, red[w].x, __float_as_int(red[w].y));
+      best(vp, ipx, red[w].z, __float_as_int(red[w].w));
+    }
+    a.race[(size_t)b * a.nrchunk + chunk] = make_float4(vw, __int_as_float(iw), vp, __int_as_float(ipx));
+    __threadfence();
+    s_last = atomicAdd(&a.tickets[b], 1) == a.nrchunk - 1;
+  }
+  __syncthreads();
+  if (!s_last || warp != 0) return;
+  __threadfence();
+  vw = vp = 0.f;
+  iw = ipx = -1;
+  for (int k = lane; k < a.nrchunk; k += 32) {
+    const float4 v = __ldcg(&a.race[(size_t)b * a.nrchunk + k]);
+    best(vw, iw, v.x, __float_as_int(v.y));
+    best(vp, ipx, v.z, __float_as_int(v.w));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    best(vw, iw, __shfl_xor_sync(0xffffffffu, vw, o), __shfl_xor_sync(0xffffffffu, iw, o));
+    best(vp, ipx, __shfl_xor_sync(0xffffffffu, vp, o), __shfl_xor_sync(0xffffffffu, ipx, o));
+  }
+  const int next = iw >= 0 ? iw : ipx;  // p - q nowhere positive: p itself
+  if (lane <= S) out[lane] = next < 0 ? -1 : lane < stop ? __ldg(&a.tok[(size_t)b * S + lane]) : lane == stop ? next : -1;
+  if (lane == 0) {
+    a.n_acc[b] = next < 0 ? 0 : stop + 1;
+    if (next < 0 && a.status) atomicOr(a.status, HF_S_BAD);
+  }
+}
+
+// Chunk of the vocabulary per CTA: enough CTAs to fill the GPU several times
+// over, at least 2048 entries (8 per thread) each.
+int chunk_for(long long rows, int V, int least) {
+  const long long want = (152 * 16 + rows - 1) / rows;  // CTAs per row
+  const long long c = (V + want - 1) / want;
+  return (int)std::max<long long>(least, std::min<long long>((c + 255) / 256 * 256, 32768));
+}
+
+struct VPlan {
+  int chunk, nchunk, rchunk, nrchunk;
+  size_t stats, race, tickets, total;
+};
+
+VPlan plan_for(int B, int S, int V) {
+  VPlan p{};
+  p.chunk = chunk_for((long long)B * (S + 1), V, 2048);
+  p.nchunk = (V + p.chunk - 1) / p.chunk;
+  p.rchunk = chunk_for(B, V, 1024);
+  p.nrchunk = (V + p.rchunk - 1) / p.rchunk;
+  p.stats = 0;
+  p.race = (p.stats + (size_t)B * (2 * S + 1) * p.nchunk * sizeof(float2) + 15) / 16 * 16;
+  p.tickets = p.race + (size_t)B * p.nrchunk * sizeof(float4);
+  p.total = (p.tickets + (size_t)B * sizeof(int) + 15) / 16 * 16;
+  return p;
+}
+
+const char* sizes_bad(int batch, int block, int vocab) {
+  if (batch < 0 || batch > (1 << 20)) return "batch must be 0..1048576";
+  if (block < 1 || block > VMAXS) return "block must be 1..16";
+  if (vocab < 1 || vocab > (1 << 28)) return "vocab must be 1..268435456";
+  const VPlan p = plan_for(std::max(batch, 1), block, vocab);
+  if ((long long)batch * (2 * block + 1) * p.nchunk > 0x7fffffffLL || (long long)batch * p.nrchunk > 0x7fffffffLL)
+    return "batch * block * vocab is too large for one launch";
+  return nullptr;
+}
+
+template <typename TX, typename TY>
+cudaError_t launch(const VArgs& a, cudaStream_t st) {
+  const int per = a.y ? 2 * a.S + 1 : a.S + 1;
+  cudaError_t e = launch_pdl(verify_stats<TX, TY>, dim3((unsigned)(a.B * per * a.nchunk)), dim3(VT), 0, st, a);
+  if (e == cudaSuccess)
+    e = launch_pdl(verify_race<TX, TY>, dim3((unsigned)(a.B * a.nrchunk)), dim3(VT), 0, st, a);
+  return e;
+}
+
+}  // namespace
+}  // namespace hf
+
+extern "C" size_t hf_verify_workspace(int32_t batch, int32_t block, int32_t vocab) {
+  if (hf::sizes_bad(batch, block, vocab)) return 0;
+  return hf::plan_for(std::max(batch, 1), block, vocab).total;
+}
+
+extern "C" hf_status hf_verify_tokens(int32_t target_dtype, const void* target_logits, int64_t target_ld,
+                                      int32_t draft_dtype, const void* draft_logits, int64_t draft_ld,
+                                      const int32_t* draft_tokens, const int32_t* n_draft, const float* u,
+                                      const float* noise, int64_t noise_ld, const float* temperature,
+                                      int32_t batch, int32_t block, int32_t vocab, int32_t* n_accepted,
+                                      int32_t* tokens, void* workspace, size_t workspace_bytes,
+                                      int32_t* status, void* stream) {
+  using namespace hf;
+  auto bad = [](const char* m) {
+    set_thread_error(m);
+    return HF_EINVAL;
+  };
+  if (target_dtype != HF_F32 && target_dtype != HF_BF16) return bad("target_dtype must be HF_F32 or HF_BF16");
+  if (draft_logits && draft_dtype != HF_F32 && draft_dtype != HF_BF16)
+    return bad("draft_dtype must be HF_F32 or HF_BF16");
+  if (const char* m = sizes_bad(batch, block, vocab)) return bad(m);
+  if (target_ld < vocab || noise_ld < vocab || (draft_logits && draft_ld < vocab))
+    return bad("target_ld, draft_ld and noise_ld must be >= vocab");
+  if (batch == 0) return HF_OK;
+  if (!target_logits || !draft_tokens || !u || !noise || !n_accepted || !tokens || !workspace)
+    return bad("NULL buffer");
+  auto off = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+  if (off(target_logits, target_dtype == HF_F32 ? 4 : 2) ||
+      (draft_logits && off(draft_logits, draft_dtype == HF_F32 ? 4 : 2)) || off(draft_tokens, 4) ||
+      off(n_draft, 4) || off(u, 4) || off(noise, 4) || off(temperature, 4) || off(n_accepted, 4) ||
+      off(tokens, 4) || off(status, 4))
+    return bad("a buffer is not aligned to its element type");
+  if (off(workspace, 16)) return bad("workspace must be 16-byte aligned");
+  const VPlan p = plan_for(batch, block, vocab);
+  if (workspace_bytes < p.total) {
+    char m[120];
+    snprintf(m, sizeof m, "workspace has %zu bytes, hf_verify_workspace asks for %zu", workspace_bytes, p.total);
+    return bad(m);
+  }
+  VArgs a{};
+  a.x = target_logits;
+  a.y = draft_logits;
+  a.x_ld = target_ld;
+  a.y_ld = draft_ld;
+  a.e_ld = noise_ld;
+  a.tok = draft_tokens;
+  a.n_draft = n_draft;
+  a.u = u;
+  a.e = noise;
+  a.temp = temperature;
+  a.B = batch;
+  a.S = block;
+  a.V = vocab;
+  a.chunk = p.chunk;
+  a.nchunk = p.nchunk;
+  a.rchunk = p.rchunk;
+  a.nrchunk = p.nrchunk;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.stats = reinterpret_cast<float2*>(w + p.stats);
+  a.race = reinterpret_cast<float4*>(w + p.race);
+  a.tickets = reinterpret_cast<int*>(w + p.tickets);
+  a.n_acc = n_accepted;
+  a.out = tokens;
+  a.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  using bf = __nv_bfloat16;
+  const bool xf = target_dtype == HF_F32, yf = !draft_logits || draft_dtype == HF_F32;
+  const cudaError_t e = xf ? (yf ? launch<float, float>(a, st) : launch<float, bf>(a, st))
+                           : (yf ? launch<bf, float>(a, st) : launch<bf, bf>(a, st));
+  if (e != cudaSuccess) {
+    set_thread_error(cudaGetErrorString(e));
+    return HF_ECUDA;
+  }
+  return HF_OK;
+}
