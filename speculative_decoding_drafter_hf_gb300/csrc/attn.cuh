@@ -78,11 +78,11 @@ struct PromptTile {
   int start, len, tile;  // first row and length of the sequence, tile in it
   bool ok;
 };
-__device__ __forceinline__ PromptTile prompt_tile(const AttnRows& a, int slot, int BM) {
+__device__ __forceinline__ PromptTile prompt_tile(const AttnRows& a, int slot, int BM, int G) {
   int lo = 0, hi = a.n_seq;  // the last sequence whose first slot is at or before `slot`
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    const long long first = (long long)max(0, min(__ldg(&a.off[mid]), a.total)) * a.G / BM + mid;
+    const long long first = (long long)max(0, min(__ldg(&a.off[mid]), a.total)) * G / BM + mid;
     if (first <= slot)
       lo = mid;
     else
@@ -94,8 +94,8 @@ __device__ __forceinline__ PromptTile prompt_tile(const AttnRows& a, int slot, i
   if (!t.ok) return t;
   t.start = s0;
   t.len = s1 - s0;
-  t.tile = slot - (int)((long long)s0 * a.G / BM + lo);
-  t.ok = t.tile >= 0 && (long long)t.tile * BM < (long long)t.len * a.G;
+  t.tile = slot - (int)((long long)s0 * G / BM + lo);
+  t.ok = t.tile >= 0 && (long long)t.tile * BM < (long long)t.len * G;
   return t;
 }
 
@@ -109,6 +109,11 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a) {
   }
   if (bad) atomicOr(a.status, HF_S_BAD);
 }
+
+// Tensor-core variants (attn_tc.cu), where attn_tc_ok.
+bool attn_tc_ok(int dtype, const AttnRows& a);
+cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
+cudaError_t launch_attn_tc_prefix(const AttnRows& a, cudaStream_t st);
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
 cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st);

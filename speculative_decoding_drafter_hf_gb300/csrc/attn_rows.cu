@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
   const int32_t* tab = nullptr;
   if (MODE == PROMPT) {
     if (blockIdx.x == 0 && g == 0) check_offsets(a);
-    const PromptTile t = prompt_tile(a, (int)(gridDim.x - 1 - blockIdx.x), BM);
+    const PromptTile t = prompt_tile(a, (int)(gridDim.x - 1 - blockIdx.x), BM, a.G);
     if (!t.ok) return;
     start = t.start;
     row0 = t.tile * BM;
@@ -523,7 +523,8 @@ extern "C" hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t t
   a.n_seq = n_seq;
   a.total = total;
   a.status = status;
-  return done(launch_attn_rows_prompt(dtype, a, (cudaStream_t)stream));
+  cudaStream_t st = (cudaStream_t)stream;
+  return done(attn_tc_ok(dtype, a) ? launch_attn_tc_prompt(a, st) : launch_attn_rows_prompt(dtype, a, st));
 }
 
 extern "C" size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows, int32_t n_q_heads,
@@ -571,7 +572,7 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ml);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
+  if (a.npre) e = attn_tc_ok(p->dtype, a) ? launch_attn_tc_prefix(a, st) : launch_attn_rows_prefix(p->dtype, a, st);
   if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
   if (e == cudaSuccess && !attn_direct(a)) e = launch_attn_join(p->dtype, a, st);
   return done(e);

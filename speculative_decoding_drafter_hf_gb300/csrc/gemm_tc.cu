@@ -627,6 +627,21 @@ cudaError_t make_map(CUtensorMap* map, const void* base, long long rows, long lo
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_map_3d(CUtensorMap* map, const void* base, long long n0, long long n1, long long n2,
+                        long long stride1, long long stride2, int b1, int b2) {
+  cudaError_t e = get_encoder();
+  if (e != cudaSuccess) return e;
+  cuuint64_t dims[3] = {(cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+  cuuint64_t strides[2] = {(cuuint64_t)(stride1 * 2), (cuuint64_t)(stride2 * 2)};
+  cuuint32_t box[3] = {64u, (cuuint32_t)b1, (cuuint32_t)b2};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // 2-D fp32 tensor map over rows x cols (row stride cols elements, a multiple
 // of 4), box 32 columns (128 bytes) x box_rows, 128-byte swizzle.
 cudaError_t make_map_f32(CUtensorMap* map, const void* base, long long rows, long long cols,
