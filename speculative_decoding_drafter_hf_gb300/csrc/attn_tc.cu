@@ -53,25 +53,46 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Descriptor of a row-major [keys][64] tile (rows of 128 bytes, 128-byte swizzle)
-// read along its rows: the operand's N runs along a row, its K over the rows. Groups
-// of 8 rows are 1024 bytes apart; the next 64 columns are a tile of BN rows further.
-__device__ __forceinline__ uint64_t sdesc_rows(const void* p) {
-  uint64_t d = (smem_u32(p) >> 4) & 0x3FFFull;
-  d |= (uint64_t)((BN * 128) >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= 1ull << 46;
-  d |= 2ull << 61;
-  return d;
+// Products issued by a whole warp in uniform control flow: every lane computes the
+// same operands (they stay in uniform registers), `lead` is set in one lane.
+// Descriptors come as their low words; the high words are constants.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+// A row-major [keys][64] tile read along its rows (the operand's N runs along a row, its
+// K over the rows): the next 64 columns are a tile of BN rows further.
+__device__ __forceinline__ uint32_t desc_lo_rows(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFFu) | ((uint32_t)(BN * 128) >> 4) << 16;
 }
-
-// D[128 x n] (+)= A B with A in TMEM (bf16 pairs along a lane's columns).
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc, uint32_t acc) {
+// D (+)= A B, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(db), "r"(idesc), "r"(acc));
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%2, %6};\n\tmov.b64 y, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %4, p;\n\t}\n" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi));
+}
+// The same with A in TMEM (bf16 pairs along a lane's columns).
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], y, %4, p;\n\t}\n" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi));
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(lead),
+      "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
@@ -124,6 +145,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ bool odd_half(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+
+// Bounded wait of a whole warp; the answer is the same in every lane.
+__device__ __forceinline__ bool try_wait_addr(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  for (;;) {
+    if (try_wait_addr(bar, parity)) return true;
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity) {
+  return try_wait_addr(bar, parity) || wait_slow(bar, parity);
+}
 
 struct TcArgs {
   AttnRows a;
@@ -279,48 +323,64 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         }
       }
       if (lane == 0) *issued = i;
-    } else if (warp == 1 && lane == 0 && nt > 0) {
+    } else if (warp == 1 && nt > 0) {
       // ---- products: S0(0), S1(0), then PV0(j), S0(j+1), PV1(j), S1(j+1)
       constexpr uint32_t id_s = idesc_bf16(BN);
       constexpr uint32_t id_o = idesc_bf16(DH) | (1u << 16);
+      const uint32_t lead = elect_one();
+      const int un = __shfl_sync(0xffffffffu, nt, 0), un0 = __shfl_sync(0xffffffffu, nt0, 0),
+                un1 = __shfl_sync(0xffffffffu, nt1, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t aq = desc_lo(smem_u32(sQ)), ak = desc_lo(smem_u32(sKV)), av = desc_lo_rows(smem_u32(sKV));
+      const uint32_t b_full = smem_u32(full), b_empty = smem_u32(empty), b_s = smem_u32(s_full), b_p = smem_u32(p_full),
+                     b_o = smem_u32(o_full);
       auto score = [&](int r, int slot) {
-        const uint64_t dq = sdesc_sw128(sQ + r * L::TILE), dk = sdesc_sw128(sKV + (size_t)slot * L::TILE);
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k) {
-          const uint64_t step = (uint64_t)((k / 4) * (HALF >> 4) + (k % 4) * 2);
-          umma_bf16(tmem + r * BN, dq + step, dk + step, id_s, k > 0);
+          const uint32_t step = (uint32_t)((k / 4) * (HALF >> 4) + (k % 4) * 2);
+          mma_ss(lead, tm + r * BN, aq + r * (L::TILE >> 4) + step, ak + slot * (L::TILE >> 4) + step, id_s, k > 0);
         }
-        umma_commit(&s_full[r]);
+        mma_commit(lead, b_s + 8 * r);
       };
-      bool ok = mbar_wait(q_full, 0) && mbar_wait(&full[0], 0);
+      bool ok = wait_uniform(smem_u32(q_full), 0) && wait_uniform(b_full, 0);
       if (ok) {
         tc_fence_after();
         score(0, 0);
-        if (nt1 > 0) score(1, 0);
-        umma_commit(&empty[0]);
+        if (un1 > 0) score(1, 0);
+        mma_commit(lead, b_empty);
       }
-      for (int j = 0; j < nt && ok; ++j) {
-        const int vi = 2 * j + 1, vs = vi % NS, ks = (vi + 1) % NS;
-        const bool more = j + 1 < nt;
-        ok = mbar_wait(&full[vs], (uint32_t)(vi / NS) & 1u) &&
-             (!more || mbar_wait(&full[ks], (uint32_t)((vi + 1) / NS) & 1u));
-        for (int r = 0; r < 2 && ok; ++r) {
-          const int mine = r ? nt1 : nt0;
-          if (j >= mine) continue;
-          ok = mbar_wait(&p_full[r], (uint32_t)j & 1u);
-          if (!ok) break;
+      int vs = 1 % NS, ks = 2 % NS;    // slots of V(j), K(j+1) and the parity of their fill
+      uint32_t vph = 0, kph = 0;
+      for (int j = 0; j < un && ok; ++j) {
+        const bool more = j + 1 < un;
+        ok = wait_uniform(b_full + 8 * vs, vph) && (!more || wait_uniform(b_full + 8 * ks, kph));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int mine = r ? un1 : un0;
+          if (!ok || j >= mine) continue;
+          ok = wait_uniform(b_p + 8 * r, (uint32_t)j & 1u);
+          if (!ok) continue;
           tc_fence_after();
-          const uint64_t dv = sdesc_rows(sKV + (size_t)vs * L::TILE);
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
-            umma_bf16_ta(tmem + L::O_COL + r * DH, tmem + r * BN + k * 8, dv + (uint64_t)(k * (2048 >> 4)), id_o,
-                         j > 0 || k > 0);
-          umma_commit(&o_full[r]);
+            mma_ts(lead, tm + L::O_COL + r * DH, tm + r * BN + k * 8, av + vs * (L::TILE >> 4) + k * (2048 >> 4), id_o,
+                   j > 0 || k > 0);
+          mma_commit(lead, b_o + 8 * r);
           if (j + 1 < mine) score(r, ks);
         }
         if (ok) {
-          umma_commit(&empty[vs]);
-          if (more) umma_commit(&empty[ks]);
+          mma_commit(lead, b_empty + 8 * vs);
+          if (more) mma_commit(lead, b_empty + 8 * ks);
+        }
+        vs += 2;
+        if (vs >= NS) {
+          vs -= NS;
+          vph ^= 1u;
+        }
+        ks += 2;
+        if (ks >= NS) {
+          ks -= NS;
+          kph ^= 1u;
         }
       }
       if (!ok) *abort_flag = 1;
