@@ -1,5 +1,5 @@
 // Attention of query rows over packed prompts or a paged cache: what its variants
-// (attn_rows.cu on CUDA cores, attn_tc.cu and attn_own.cu on tensor cores) share.
+// (attn_rows.cu on CUDA cores, attn_tc.cu on tensor cores) share.
 //
 // Rows that use one KV head are numbered token * G + (query head in its group), so
 // that a tile of rows always shares its keys, whatever the group size G is.
@@ -29,16 +29,34 @@ struct AttnRows {
   const int32_t* req;
   int n, rows, page, n_pages, n_requests, table_ld;
   int shared;      // tokens of the common prefix
-  // pieces of the key axis: npre of the prefix (pre_keys keys each), then up to
-  // nown of each request's own tokens (own_keys each). One piece in all: rows go
-  // straight to out; else to part_o / part_ml, piece by piece, rows (token, query
-  // head) within, joined by attn_join.
+  // pieces of the key axis: npre of the prefix (pre_keys keys each), then each
+  // entry's own tokens: on CUDA cores nown pieces of own_keys each (unused ones
+  // among them), on tensor cores as many as the plan gives it. An entry of one
+  // piece in all has its rows written straight to out; the others' go to part_o /
+  // part_ml, rows (token, query head) within a piece, and attn_join joins them: the
+  // prefix's pieces of n * rows * Hq rows, then the entries' of rows * Hq.
   int npre, pre_keys, nown, own_keys;
-  float* part_o;   // [npre + nown][n * rows * Hq][dh], not normalised
+  float* part_o;   // [...][dh], not normalised
   float2* part_ml; // the same rows: maximum (base 2), sum
+  // written on the device before the pieces are read
+  int* eff;        // [n] tokens of each entry, 0 for those that break a rule
+  int* plan;       // tensor cores: [0] item counter, [1] keys per piece, [2] pieces
+  int* base;       // [n + 1] first piece of each entry
+  int* piece_of;   // entry of each piece
 };
 
 __host__ __device__ inline bool attn_direct(const AttnRows& a) { return a.npre + a.nown == 1; }
+
+// First piece of entry i's own tokens, and how many there are.
+__device__ __forceinline__ int attn_pieces(const AttnRows& a, int i, int& count) {
+  if (a.plan) {
+    const int b = __ldcg(&a.base[i]);
+    count = __ldcg(&a.base[i + 1]) - b;
+    return b;
+  }
+  count = max(1, (max(0, __ldcg(&a.eff[i]) - a.shared) + a.own_keys - 1) / a.own_keys);
+  return i * a.nown;
+}
 
 // Length of entry i as the call takes it: 0 for entries that break a rule (bad set).
 __device__ __forceinline__ int attn_raw_len(const AttnRows& a, int i, bool& bad) {
@@ -111,9 +129,14 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a) {
 }
 
 // Tensor-core variants (attn_tc.cu), where attn_tc_ok.
-bool attn_tc_ok(int dtype, const AttnRows& a);
+bool attn_tc_ok(int dtype, int dh);
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
-cudaError_t launch_attn_tc_prefix(const AttnRows& a, cudaStream_t st);
+// Over a paged cache: items of one piece of the prefix and of one piece of an entry,
+// and how many pieces of the entries there are at most beside n (a.npre, a.pre_keys set).
+void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget);
+cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, int budget, cudaStream_t st);
+// Entries' lengths and status checks; with budget > 0 the pieces of the entries.
+cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, cudaStream_t st);
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
 cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st);

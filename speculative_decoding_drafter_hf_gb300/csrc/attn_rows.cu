@@ -89,31 +89,21 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     piece = blockIdx.z;
     j0 = piece * a.pre_keys;
     j1 = min(a.shared, j0 + a.pre_keys);
-    bool bad = false;
-    if (attn_raw_len(a, 0, bad) == 0) {  // nothing is shared then: every row is empty
+    if (__ldcg(&a.eff[0]) == 0)  // nothing is shared then: every row is empty
       j1 = j0;
-    } else {
+    else
       tab = attn_table(a, 0);
-    }
   } else {
     const int blocks = (a.rows * a.G + BM - 1) / BM;
     entry = blockIdx.x / blocks;
     row0 = (blockIdx.x % blocks) * BM;
     nrows = min(BM, a.rows * a.G - row0);
-    piece = a.npre + blockIdx.z;
-    bool bad = false;
-    len = attn_len(a, entry, bad);
+    piece = blockIdx.z;
+    len = __ldcg(&a.eff[entry]);
     j0 = a.shared + blockIdx.z * a.own_keys;
     j1 = min(len, j0 + a.own_keys);
     if (blockIdx.z > 0 && j0 >= j1) return;  // piece 0 always reports (a direct call has no other)
-    if (len > 0) {
-      tab = attn_table(a, entry);
-      if (blockIdx.z == 0 && g == 0 && row0 == 0 && a.shared > 0) {
-        const int32_t* first = attn_table(a, 0);
-        for (int j = tid; j < a.shared / a.page; j += RT) bad = bad || __ldg(&tab[j]) != __ldg(&first[j]);
-      }
-    }
-    if (bad && a.status && blockIdx.z == 0 && g == 0 && row0 == 0) atomicOr(a.status, HF_S_BAD);
+    if (len > 0) tab = attn_table(a, entry);
   }
 
   // this thread's rows: keys they see, and where they come from and go to
@@ -133,8 +123,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
       limit[i] = t + 1;
       orow[i] = (size_t)start + t;
     } else if (MODE == PREFIX) {
-      bool bad = false;
-      const int l = attn_len(a, t / a.rows, bad);
+      const int l = __ldcg(&a.eff[t / a.rows]);
       limit[i] = max(0, min(a.shared, l - a.rows + t % a.rows + 1));
       orow[i] = t;
     } else {
@@ -292,7 +281,9 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
         if (d < dh) dst[d] = from_f<T>(o[i][c] * inv);
       }
     } else {
-      const size_t r = piece * N + orow[i] * a.Hq + head[i];
+      const size_t r = MODE == PREFIX ? piece * N + orow[i] * a.Hq + head[i]
+                                      : a.npre * N + (((size_t)entry * a.nown + piece) * a.rows +
+                                                      (orow[i] - (size_t)entry * a.rows)) * a.Hq + head[i];
       if (tx == 0) a.part_ml[r] = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < MAXC; ++c)
@@ -312,26 +303,33 @@ __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
   const size_t N = (size_t)a.n * a.rows * a.Hq;
   const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= N) return;
-  const int token = (int)(row / a.Hq), head = (int)(row % a.Hq);
-  bool bad = false;
-  const int len = attn_len(a, token / a.rows, bad);
-  const int own = (max(0, len - a.shared) + a.own_keys - 1) / a.own_keys;
-  const int pieces = len > 0 ? a.npre + own : 0;  // the prefix's come first
+  const int token = (int)(row / a.Hq), head = (int)(row % a.Hq), entry = token / a.rows;
+  int own;
+  const int first = attn_pieces(a, entry, own);
+  if (a.npre == 0 && own == 1 && (a.plan || attn_direct(a))) return;  // written already
+  const int pieces = __ldcg(&a.eff[entry]) > 0 ? a.npre + own : 0;
+  // piece p's row: the prefix's pieces come first
+  auto at = [&](int p) {
+    return p < a.npre ? p * N + row
+                      : a.npre * N + ((size_t)(first + p - a.npre) * a.rows + token % a.rows) * a.Hq + head;
+  };
   float m = -INFINITY;
-  for (int p = lane; p < pieces; p += 32) m = fmaxf(m, __ldcg(&a.part_ml[p * N + row]).x);
+  for (int p = lane; p < pieces; p += 32) m = fmaxf(m, __ldcg(&a.part_ml[at(p)]).x);
   m = warp_max(m);
   float acc[8] = {};
   float l = 0.f;
   const float base = m > -INFINITY ? m : 0.f;
+#pragma unroll 4
   for (int p = 0; p < pieces; ++p) {
-    const float2 ml = __ldcg(&a.part_ml[p * N + row]);
-    if (ml.y == 0.f) continue;  // saw nothing there (its row holds zeros)
+    const size_t r = at(p);
+    const float2 ml = __ldcg(&a.part_ml[r]);
+    if (ml.y == 0.f) continue;  // saw nothing there (its row was not written)
     const float w = exp2f(ml.x - base);
     l = fmaf(ml.y, w, l);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
       if (lane * 4 + 128 * c < dh) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(&a.part_o[(p * N + row) * dh + lane * 4 + 128 * c]));
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(&a.part_o[r * dh + lane * 4 + 128 * c]));
         acc[4 * c + 0] = fmaf(w, x.x, acc[4 * c + 0]);
         acc[4 * c + 1] = fmaf(w, x.y, acc[4 * c + 1]);
         acc[4 * c + 2] = fmaf(w, x.z, acc[4 * c + 2]);
@@ -429,9 +427,9 @@ float base2_scale(float scale, int dh) {
   return (float)(1.4426950408889634 * (scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)dh)));
 }
 
-// Pieces of the key axis: as many as give every SM two CTAs, of at least 256 keys.
-// A request's own pieces go by its table's reach, not by its length, which only the
-// device knows: at most 16.
+// Pieces of the key axis on CUDA cores: as many as give every SM two CTAs, of at
+// least 256 keys. A request's own pieces go by its table's reach, not by its length,
+// which only the device knows.
 void plan_pieces(AttnRows& a) {
   const long long pre_tiles = ((long long)a.n * a.rows * a.G + BM - 1) / BM * a.Hkv;
   auto split = [](long long keys, long long tiles, int most, int& count, int& each) {
@@ -448,7 +446,34 @@ void plan_pieces(AttnRows& a) {
   const long long own = (long long)a.table_ld * a.page - a.shared;
   const long long own_tiles = (long long)a.n * a.Hkv * ((a.rows * a.G + BM - 1) / BM);
   split(own, own_tiles, 32, a.nown, a.own_keys);
-  a.nown = std::max(a.nown, 1);  // it also reports bad entries, and writes the empty rows of a direct call
+  a.nown = std::max(a.nown, 1);  // it also writes the empty rows of a direct call
+}
+
+// Sizes and workspace of a call.
+struct PagesPlan {
+  bool tc;
+  int pre_items, units, budget;         // tensor cores
+  size_t eff, base, piece_of, ml, o, total;  // offsets in the workspace (the plan is at 0)
+};
+PagesPlan plan_call(AttnRows& a, int dtype) {
+  PagesPlan w{};
+  w.tc = attn_tc_ok(dtype, a.dh);
+  size_t pieces;
+  if (w.tc) {
+    attn_tc_sizes(a, w.pre_items, w.units, w.budget);
+    pieces = (size_t)a.n + w.budget;
+  } else {
+    plan_pieces(a);
+    pieces = attn_direct(a) ? 0 : (size_t)a.n * a.nown;
+  }
+  const size_t rows = (attn_direct(a) && !w.tc ? 0 : (size_t)a.npre * a.n * a.rows * a.Hq) + pieces * a.rows * a.Hq;
+  w.eff = 16;
+  w.base = w.eff + (size_t)a.n * sizeof(int);
+  w.piece_of = w.base + (w.tc ? ((size_t)a.n + 1) * sizeof(int) : 0);
+  w.ml = (w.piece_of + (w.tc ? pieces * sizeof(int) : 0) + 15) / 16 * 16;
+  w.o = (w.ml + rows * sizeof(float2) + 15) / 16 * 16;
+  w.total = w.o + rows * a.dh * sizeof(float);
+  return w;
 }
 
 const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq, int shared, AttnRows& a) {
@@ -474,13 +499,7 @@ const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq,
   a.n_requests = p->n_requests;
   a.table_ld = p->table_ld;
   a.shared = shared;
-  plan_pieces(a);
   return nullptr;
-}
-size_t part_bytes(const AttnRows& a, size_t& ml) {
-  const size_t rows = (size_t)(a.npre + a.nown) * a.n * a.rows * a.Hq;
-  ml = rows * a.dh * sizeof(float);
-  return attn_direct(a) ? 16 : ml + rows * sizeof(float2);
 }
 
 }  // namespace
@@ -524,15 +543,14 @@ extern "C" hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t t
   a.total = total;
   a.status = status;
   cudaStream_t st = (cudaStream_t)stream;
-  return done(attn_tc_ok(dtype, a) ? launch_attn_tc_prompt(a, st) : launch_attn_rows_prompt(dtype, a, st));
+  return done(attn_tc_ok(dtype, head_dim) ? launch_attn_tc_prompt(a, st) : launch_attn_rows_prompt(dtype, a, st));
 }
 
 extern "C" size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows, int32_t n_q_heads,
                                                int32_t shared) {
   hf::AttnRows a{};
   if (hf::pages_args(p, false, std::max(n, 1), rows, n_q_heads, shared, a)) return 0;
-  size_t ml;
-  return hf::part_bytes(a, ml);
+  return hf::plan_call(a, p->dtype).total;
 }
 
 extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_t n, int32_t rows,
@@ -551,12 +569,11 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
                         ld_bad(out_ld, (long long)n_q_heads * p->head_dim, a.esize, out)})
     if (m) return refuse(m);
   if (off(requests, 4)) return refuse("requests must be 4-byte aligned");
-  size_t ml;
-  const size_t need = part_bytes(a, ml);
-  if (off(workspace, 16) || workspace_bytes < need) {
+  const PagesPlan w = plan_call(a, p->dtype);
+  if (off(workspace, 16) || workspace_bytes < w.total) {
     char m[160];
     snprintf(m, sizeof m, "workspace must be 16-byte aligned and hold %zu bytes (hf_attention_pages_workspace), got %zu",
-             need, workspace_bytes);
+             w.total, workspace_bytes);
     return refuse(m);
   }
   const size_t layer_bytes = (size_t)p->n_pages * pages_block(p) * a.esize;
@@ -568,12 +585,22 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
   a.k = static_cast<const uint8_t*>(p->k) + layer * layer_bytes;
   a.v = static_cast<const uint8_t*>(p->v) + layer * layer_bytes;
   a.req = requests;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ml);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.eff = reinterpret_cast<int*>(ws + w.eff);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaSuccess;
-  if (a.npre) e = attn_tc_ok(p->dtype, a) ? launch_attn_tc_prefix(a, st) : launch_attn_rows_prefix(p->dtype, a, st);
-  if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
-  if (e == cudaSuccess && !attn_direct(a)) e = launch_attn_join(p->dtype, a, st);
+  cudaError_t e;
+  if (w.tc) {
+    a.plan = reinterpret_cast<int*>(ws);
+    a.base = reinterpret_cast<int*>(ws + w.base);
+    a.piece_of = reinterpret_cast<int*>(ws + w.piece_of);
+    e = launch_attn_tc_pages(a, w.pre_items, w.units, w.budget, st);
+  } else {
+    e = launch_attn_plan(a, 0, 0, 0, st);
+    if (e == cudaSuccess && a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
+    if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
+  }
+  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, st);
   return done(e);
 }

@@ -1,22 +1,23 @@
-// Attention of many query rows on the tensor cores (bf16, head dim 64 or 128):
-// whole prompts, and the common prefix of a paged cache.
+// Attention on the tensor cores (bf16, head dim 64 or 128): whole prompts, and the
+// newest rows of requests over a paged cache, its common prefix read once for all.
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(qscale s_ij - m_i),  s_ij = q_i.k_j
-// in one pass over key tiles of 128 with a running m_i. A CTA has two tiles of 128
-// rows of one KV head (rows are token * G + head in the group, so the group's
-// heads share every key tile). tcgen05 forms S = Q K^T into TMEM; one thread per row
-// reads its 128 scores, writes the weights back over them as bf16, and tcgen05 adds
-// P V to the row's sums in TMEM, with P read from TMEM and V straight from its
-// row-major tile (the transposed operand form). m_i is raised only when a tile's
-// maximum passes it by more than 2^8 (in the exponent): until then weights stay
-// below 2^8 and nothing is rescaled, so the sums in TMEM are touched by the tensor
-// cores alone for most tiles.
+// in one pass over key tiles of 128 with a running m_i. A CTA works on two tiles of 128
+// rows (rows are token * G + head in the group, so the group's heads share every key
+// tile). tcgen05 forms S = Q K^T into TMEM; one thread per row reads its 128 scores and
+// writes the weights back over them as bf16, and tcgen05 adds P V to the row's sums in
+// TMEM, with P read from TMEM and V straight from its row-major tile. m_i is raised only
+// when a tile's maximum passes it by more than 8 (a factor 2^8): until then nothing is
+// rescaled, so for most tiles only the tensor cores touch the sums.
 //
-// While the softmax threads of one row tile work, the tensor cores work for the
-// other: warp 0 loads (TMA), warp 1 issues the products, warps 4-7 and 8-11 are the
-// two softmax groups. Per key tile the two products of both row tiles take 4 x 512
-// tensor cycles, and each group's 128 x 128 exponentials and conversions have to fit
-// beside them.
+// While the softmax threads of one row tile work, the tensor cores work for the other.
+// The two row tiles use the same keys (prompts, a prefix that more rows share than fit
+// one tile), or, where one tile holds all rows, belong to two KV heads and have keys of
+// their own. Warp 0 loads (TMA), warp 1 issues the products, warp 2 hands out items,
+// warps 4-7 and 8-11 are the softmax groups; CTAs stay and take item after item, so that
+// the next item's loads and first product run beside the last one's end. Prompt items are
+// the launch's own CTAs, taken over from the ones not started yet (heaviest first); cache
+// items come from a counter in the workspace.
 //
 // Masked keys: scores are selected by position. V's non-finite values in a tile that
 // some row masks are set to zero in shared memory (0 * NaN would reach every row) and
@@ -31,14 +32,15 @@ namespace {
 
 constexpr int BN = 128;        // keys per tile
 constexpr int TCT = 384;       // threads
-enum { PROMPT = 0, PREFIX = 1 };
+enum { PROMPT = 0, PAGED = 1 };
+constexpr int kNone = 0x7fffffff;
 
 template <int DH>
 struct Tc {
   static constexpr int TILE = BN * DH * 2;            // bytes of a K, V or Q tile
   static constexpr int SLOTS = DH == 128 ? 5 : 10;    // ring of K and V tiles
   static constexpr int O_COL = 256;                   // TMEM: S0 | S1 | O0 | O1
-  static constexpr size_t smem() { return 1024 + (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 8) * 8 + 64; }
+  static constexpr size_t smem() { return 1024 + (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 16) * 8 + 16 + 2 * 80 + 32; }
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -158,7 +160,7 @@ __device__ __forceinline__ bool try_wait_addr(uint32_t bar, uint32_t parity) {
       : "memory");
   return __all_sync(0xffffffffu, ok != 0);
 }
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   for (;;) {
     if (try_wait_addr(bar, parity)) return true;
@@ -172,24 +174,143 @@ __device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity) {
 struct TcArgs {
   AttnRows a;
   int tb;          // tokens per row tile: 128 / G
-  int items;       // row blocks (prompt: slots) of 2 tb tokens
+  int blocks;      // prompt: slots of 2 tb tokens; paged: blocks of the prefix rows
   int box_rows;    // rows of a K / V box (prompt: 128, paged: the page)
+  int pre_items;   // paged: items of the prefix
+  int units;       // paged: items per piece of a request's own keys
 };
 
+// What a CTA works on at a time, written by warp 2. Tile r's rows are tokens
+// tok0 + (split ? 0 : r tb) .. of KV head g + (split ? r : 0).
+struct Item {
+  int kind;        // 0 prompt, 1 prefix, 2 own keys, -1 the end
+  int g, split;    // split: two KV heads with keys of their own; else the same keys
+  int nt[2];       // key tiles of each row tile
+  int j0, j1;      // keys
+  int tok0, ntok;  // first row of q and out, tokens
+  int t0;          // prompt, own: position of tok0 in its sequence or entry
+  int start;       // prompt: row of key 0
+  int entry, len;  // own: the entry and its tokens
+  int direct;      // rows go to out
+  int part;        // else: first row of the partial results / (rows * Hq), own; piece, prefix
+  int low[2];      // least number of keys that a row of the tile sees
+  int odd[2];      // first key of a tile whose odd values of V were taken as zero
+};
+static_assert(sizeof(Item) <= 80, "item slots");
+
+__device__ __forceinline__ void take_next_cta(uint4* answer, uint64_t* bar) {
+  mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The index of the CTA taken over, or -1: all have started.
+__device__ __forceinline__ int taken_cta(const uint4* answer) {
+  int x = -1;
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}\n"
+      : "=&r"(x), "=&r"(got)
+      : "r"(smem_u32(answer))
+      : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return got ? x : -1;
+}
+
 template <int MODE>
-__device__ __forceinline__ long long v_at(const AttnRows& a, int start, const int32_t* tab, int g, int j) {
-  if (MODE == PROMPT) return (long long)(start + j) * a.v_ld + (long long)g * a.dh;
-  const int id = __ldg(&tab[j / a.page]);
+__device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it) {
+  const AttnRows& a = c.a;
+  it.split = 0;
+  it.start = it.entry = it.len = it.part = 0;
+  it.low[0] = it.low[1] = it.odd[0] = it.odd[1] = kNone;
+  int nt;
+  if (MODE == PROMPT) {
+    const PromptTile t = prompt_tile(a, c.blocks - 1 - idx / a.Hkv, 2 * c.tb, 1);
+    if (!t.ok) return false;
+    it.kind = 0;
+    it.g = idx % a.Hkv;
+    it.t0 = t.tile * 2 * c.tb;
+    it.start = t.start;
+    it.tok0 = t.start + it.t0;
+    it.ntok = min(2 * c.tb, t.len - it.t0);
+    it.j0 = 0;
+    it.j1 = it.t0 + it.ntok;
+    it.direct = 1;
+    nt = (it.j1 + BN - 1) / BN;
+    // the first row tile ends earlier
+    it.nt[0] = min(nt, (min(it.j1, it.t0 + c.tb) + BN - 1) / BN);
+    it.nt[1] = it.ntok > c.tb ? nt : 0;
+    return true;
+  }
+  const int heads = (a.Hkv + 1) / 2;  // split: pairs of heads
+  if (idx < c.pre_items) {
+    const int tokens = a.n * a.rows;
+    it.kind = 1;
+    it.split = tokens <= c.tb;
+    if (it.split) {
+      it.g = 2 * (idx % heads);
+      it.part = idx / heads;
+      it.t0 = 0;
+    } else {
+      it.t0 = idx % c.blocks * 2 * c.tb;
+      it.g = idx / c.blocks % a.Hkv;
+      it.part = idx / c.blocks / a.Hkv;
+    }
+    it.tok0 = it.t0;
+    it.ntok = min(it.split ? c.tb : 2 * c.tb, tokens - it.t0);
+    it.j0 = it.part * a.pre_keys;
+    it.j1 = __ldcg(&a.eff[0]) ? min(a.shared, it.j0 + a.pre_keys) : it.j0;  // entry 0 empty: so is every row
+    it.direct = 0;
+  } else {
+    const int k = idx - c.pre_items, i = k / c.units, u = k % c.units;
+    const int chunk = __ldcg(&a.plan[1]);
+    it.kind = 2;
+    it.entry = __ldcg(&a.piece_of[i]);
+    const int base = __ldcg(&a.base[it.entry]);
+    it.len = __ldcg(&a.eff[it.entry]);
+    it.split = a.rows <= c.tb;
+    if (it.split) {
+      it.g = 2 * u;
+      it.t0 = 0;
+    } else {
+      it.g = u % a.Hkv;
+      it.t0 = u / a.Hkv * 2 * c.tb;
+    }
+    it.tok0 = it.entry * a.rows + it.t0;
+    it.ntok = min(it.split ? c.tb : 2 * c.tb, a.rows - it.t0);
+    it.j0 = a.shared + (i - base) * chunk;
+    it.j1 = max(it.j0, min(it.len, it.j0 + chunk));
+    it.direct = a.npre == 0 && __ldcg(&a.base[it.entry + 1]) - base == 1;
+    it.part = i;
+  }
+  nt = (it.j1 - it.j0 + BN - 1) / BN;
+  it.nt[0] = nt;
+  it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? nt : 0;
+  return true;
+}
+
+// Element offset in V of key j's row of KV head g.
+template <int MODE>
+__device__ __forceinline__ long long v_at(const AttnRows& a, const Item& it, int g, int j) {
+  if (MODE == PROMPT) return (long long)(it.start + j) * a.v_ld + (long long)g * a.dh;
+  const int id = __ldg(&attn_table(a, it.entry)[j / a.page]);
   if (id < 0 || id >= a.n_pages) return -1;
   return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
 }
 
-// What row `o[32]` (columns d0 ..) gets from V's non-finite values at keys [j0, j1).
+// What a row's column d gets from V's non-finite values at keys [j0, j1).
 template <int MODE>
-__device__ __noinline__ float odd_sum(const AttnRows& a, int start, const int32_t* tab, int g, int j0, int j1, int d) {
+__device__ __noinline__ float odd_sum(const AttnRows& a, const Item& it, int g, int j0, int j1, int d) {
   float s = 0.f;
   for (int j = j0; j < j1; ++j) {
-    const long long at = v_at<MODE>(a, start, tab, g, j);
+    const long long at = v_at<MODE>(a, it, g, j);
     if (at < 0) continue;
     const float x = to_f(static_cast<const __nv_bfloat16*>(a.v)[at + d]);
     if (!(fabsf(x) < INFINITY)) s += x;
@@ -200,7 +321,7 @@ __device__ __noinline__ float odd_sum(const AttnRows& a, int start, const int32_
 template <int DH, int MODE>
 __global__ void __launch_bounds__(TCT, 1)
 tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-          const __grid_constant__ CUtensorMap mv, const TcArgs c) {
+          const __grid_constant__ CUtensorMap mv, const __grid_constant__ TcArgs c) {
   using L = Tc<DH>;
   constexpr int NS = L::SLOTS, HALVES = DH / 64, HALF = BN * 128;
   const AttnRows& a = c.a;
@@ -211,14 +332,18 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   uint64_t* full = reinterpret_cast<uint64_t*>(sKV + (size_t)NS * L::TILE);
   uint64_t* empty = full + NS;
   uint64_t* q_full = empty + NS;
-  uint64_t* s_full = q_full + 1;  // [2]
-  uint64_t* p_full = s_full + 2;  // [2]
-  uint64_t* o_full = p_full + 2;  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;   // [2]
+  uint64_t* p_full = q_full + 4;   // [2]
+  uint64_t* o_full = q_full + 6;   // [2]
+  uint64_t* i_full = q_full + 8;   // [2] items
+  uint64_t* i_empty = q_full + 10; // [2]
+  uint64_t* n_full = q_full + 12;  // the next CTA's index has come
+  uint4* answer = reinterpret_cast<uint4*>(q_full + 14);
+  Item* items = reinterpret_cast<Item*>(answer + 1);  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* odd_from = reinterpret_cast<int*>(tmem_slot + 2);
-  int* low = odd_from + 1;  // [2] least limit of a group's rows
-  int* issued = low + 2;    // tiles that the loader has asked for
+  volatile int* issued = abort_flag + 1;  // [0] tiles, [1] row-tile loads that the loader has asked for
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -228,15 +353,17 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(n_full, 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
       mbar_init(&o_full[g], 1);
+      mbar_init(&i_full[g], 1);
+      mbar_init(&i_empty[g], 10);  // the loader, the products, eight softmax warps
     }
     *abort_flag = 0;
-    *odd_from = 0x7fffffff;
-    low[0] = low[1] = 0x7fffffff;
-    *issued = 0;
+    issued[0] = issued[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -245,95 +372,100 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-
-  // the item: tokens [t0, t0 + ntok) of KV head g, keys [j0, j1)
-  const int g = blockIdx.x % a.Hkv, block = blockIdx.x / a.Hkv;
-  int start = 0, t0, ntok, j0 = 0, j1, piece = 0;
-  const int32_t* tab = nullptr;
-  bool work = true;
-  if (MODE == PROMPT) {
-    if (blockIdx.x == 0) check_offsets(a);
-    const PromptTile t = prompt_tile(a, c.items - 1 - block, 2 * c.tb, 1);
-    work = t.ok;
-    start = t.start;
-    t0 = t.tile * 2 * c.tb;
-    ntok = min(2 * c.tb, t.len - t0);
-    j1 = t0 + ntok;
-  } else {
-    t0 = block * 2 * c.tb;
-    ntok = min(2 * c.tb, a.n * a.rows - t0);
-    piece = blockIdx.y;
-    j0 = piece * a.pre_keys;
-    j1 = min(a.shared, j0 + a.pre_keys);
-    bool bad = false;
-    if (attn_raw_len(a, 0, bad) == 0)
-      j1 = j0;
-    else
-      tab = attn_table(a, 0);
-  }
-  const int nt = work ? (j1 - j0 + BN - 1) / BN : 0;
-  // prompt: the first row tile ends earlier
-  const int nt0 = MODE == PROMPT ? min(nt, (min(j1, t0 + c.tb) + BN - 1) / BN) : nt;
-  const int nt1 = ntok > c.tb ? nt : 0;  // no second row tile
+  if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a);
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0 && nt > 0) {
-      // ---- loads: Q, then K(0), V(0), K(1), ... through the ring
-      if (lane == 0) {
-        const uint32_t rows = (uint32_t)(c.tb * a.G);
-        mbar_expect_tx(q_full, (nt1 > 0 ? 2u : 1u) * HALVES * rows * 128u);
-        for (int r = 0; r < (nt1 > 0 ? 2 : 1); ++r)
-          for (int h = 0; h < HALVES; ++h)
-            tma_load_3d(sQ + r * L::TILE + h * HALF, &mq, q_full, h * 64, g * a.G, start + t0 + r * c.tb);
-      }
-      const int nbox = HALVES * (BN / c.box_rows);
-      int i = 0;
-      for (; i < 2 * nt; ++i) {
-        const int s = i % NS;
-        bool ok = true;
-        if (lane == 0) {
-          if (i >= NS) ok = mbar_wait(&empty[s], ((uint32_t)(i / NS) & 1u) ^ 1u);
-          if (ok && !*abort_flag)
-            mbar_expect_tx(&full[s], L::TILE);
-          else
+    if (warp == 0) {
+      // ---- loads: a stream's K(0), the rows, then V(j), K(j+1) through the ring
+      int ri = 0, qn = 0;  // tiles, row-tile loads so far
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const Item& it = items[n & 1];
+        ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+        if (!ok || it.kind < 0) break;
+        const int nt0 = it.nt[0], nt1 = it.nt[1], nt = max(nt0, nt1), j1 = it.j1, split = it.split, g = it.g;
+        const int32_t* tab = MODE == PROMPT ? nullptr : attn_table(a, it.entry);
+        const int nbox = HALVES * (BN / c.box_rows);
+        auto tile = [&](int j, int r, bool is_v) {  // tile j of stream r
+          if (!ok) return;
+          const int s = ri % NS;
+          if (ri >= NS) ok = wait_uniform(smem_u32(&empty[s]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
+          if (!ok || *abort_flag) {
             ok = false;
-        }
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
-          *abort_flag = 1;
-          break;
-        }
-        if (lane < nbox) {
-          const int h = lane % HALVES, b = lane / HALVES;
-          const int j = j0 + (i >> 1) * BN + b * c.box_rows;
-          uint8_t* dst = sKV + (size_t)s * L::TILE + h * HALF + b * c.box_rows * 128;
-          if (MODE == PROMPT) {
-            tma_load_3d(dst, (i & 1) ? &mv : &mk, &full[s], h * 64, g, start + j);
-          } else {
-            int z = a.n_pages * a.Hkv;  // behind the pool: reads zeros
-            if (j < j1) {
-              const int id = __ldg(&tab[j / a.page]);
-              if (id >= 0 && id < a.n_pages)
-                z = id * a.Hkv + g;
-              else if (a.status)
-                atomicOr(a.status, HF_S_BAD);
+            return;
+          }
+          if (lane == 0) mbar_expect_tx(&full[s], L::TILE);
+          __syncwarp();
+          if (lane < nbox) {
+            const int h = lane % HALVES, b = lane / HALVES;
+            const int key = it.j0 + j * BN + b * c.box_rows;
+            uint8_t* dst = sKV + (size_t)s * L::TILE + h * HALF + b * c.box_rows * 128;
+            if (MODE == PROMPT) {
+              tma_load_3d(dst, is_v ? &mv : &mk, &full[s], h * 64, g, it.start + key);
+            } else {
+              int z = a.n_pages * a.Hkv;  // behind the pool: reads zeros
+              if (key < j1) {
+                const int id = __ldg(&tab[key / a.page]);
+                if (id >= 0 && id < a.n_pages)
+                  z = id * a.Hkv + g + r;
+                else if (a.status)
+                  atomicOr(a.status, HF_S_BAD);
+              }
+              tma_load_3d(dst, is_v ? &mv : &mk, &full[s], h * 64, 0, z);
             }
-            tma_load_3d(dst, (i & 1) ? &mv : &mk, &full[s], h * 64, 0, z);
+          }
+          ++ri;
+        };
+        if (nt > 0) {
+          tile(0, 0, false);
+          if (split && nt1 > 0) tile(0, 1, false);
+          if (ok && qn > 0) ok = wait_uniform(smem_u32(q_empty), (uint32_t)(qn - 1) & 1u);
+          if (ok && lane == 0) {
+            const int tiles = nt1 > 0 ? 2 : 1;
+            mbar_expect_tx(q_full, (uint32_t)(tiles * HALVES * c.tb * a.G) * 128u);
+            for (int r = 0; r < tiles; ++r)
+              for (int h = 0; h < HALVES; ++h)
+                tma_load_3d(sQ + r * L::TILE + h * HALF, &mq, q_full, h * 64, (g + (split ? r : 0)) * a.G,
+                            it.tok0 + (split ? 0 : r * c.tb));
+          }
+          if (ok) ++qn;
+          for (int j = 0; j < nt && ok; ++j) {
+            const int streams = split && nt1 > 0 ? 2 : 1;
+            for (int r = 0; r < streams; ++r) {
+              tile(j, r, true);
+              if (j + 1 < nt) tile(j + 1, r, false);
+            }
           }
         }
+        if (lane == 0) mbar_arrive(&i_empty[n & 1]);
       }
-      if (lane == 0) *issued = i;
-    } else if (warp == 1 && nt > 0) {
-      // ---- products: S0(0), S1(0), then PV0(j), S0(j+1), PV1(j), S1(j+1)
+      if (lane == 0) {
+        issued[0] = ri;
+        issued[1] = qn;
+        if (!ok) *abort_flag = 1;
+      }
+    } else if (warp == 1) {
+      // ---- products: S_r(0), then P V_r(j), S_r(j+1) for r = 0, 1 in turn
       constexpr uint32_t id_s = idesc_bf16(BN);
       constexpr uint32_t id_o = idesc_bf16(DH) | (1u << 16);
       const uint32_t lead = elect_one();
-      const int un = __shfl_sync(0xffffffffu, nt, 0), un0 = __shfl_sync(0xffffffffu, nt0, 0),
-                un1 = __shfl_sync(0xffffffffu, nt1, 0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t aq = desc_lo(smem_u32(sQ)), ak = desc_lo(smem_u32(sKV)), av = desc_lo_rows(smem_u32(sKV));
       const uint32_t b_full = smem_u32(full), b_empty = smem_u32(empty), b_s = smem_u32(s_full), b_p = smem_u32(p_full),
                      b_o = smem_u32(o_full);
+      int at = 0;           // next slot of the ring, and the parity of its fill
+      uint32_t ph = 0, qph = 0, pph[2] = {0, 0};
+      bool ok = true;
+      auto next = [&]() {  // waits for the next slot of the ring
+        const int s = at;
+        ok = ok && wait_uniform(b_full + 8 * s, ph);
+        if (++at == NS) {
+          at = 0;
+          ph ^= 1u;
+        }
+        return s;
+      };
       auto score = [&](int r, int slot) {
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k) {
@@ -342,45 +474,102 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         }
         mma_commit(lead, b_s + 8 * r);
       };
-      bool ok = wait_uniform(smem_u32(q_full), 0) && wait_uniform(b_full, 0);
-      if (ok) {
-        tc_fence_after();
-        score(0, 0);
-        if (un1 > 0) score(1, 0);
-        mma_commit(lead, b_empty);
+      for (int n = 0; ok; ++n) {
+        const Item& it = items[n & 1];
+        ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+        if (!ok || __shfl_sync(0xffffffffu, it.kind, 0) < 0) break;
+        const int nt0 = __shfl_sync(0xffffffffu, it.nt[0], 0), nt1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
+        const bool two = MODE == PAGED && __shfl_sync(0xffffffffu, it.split, 0) && nt1 > 0;  // two streams of keys
+        const int nt = max(nt0, nt1);
+        if (nt > 0) {
+          int ks = next();
+          int ks1 = two ? next() : ks;
+          ok = ok && wait_uniform(smem_u32(q_full), qph);
+          qph ^= 1u;
+          if (ok) {
+            tc_fence_after();
+            score(0, ks);
+            if (two) mma_commit(lead, b_empty + 8 * ks);
+            if (nt1 > 0) score(1, ks1);
+            mma_commit(lead, b_empty + 8 * ks1);
+            if (nt == 1) mma_commit(lead, smem_u32(q_empty));
+          }
+          int vs = 0;
+          for (int j = 0; j < nt && ok; ++j) {
+            const bool more = j + 1 < nt;
+            if (!two) {
+              vs = next();
+              if (more) ks = next();
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int mine = r ? nt1 : nt0;
+              if (!ok || j >= mine) continue;
+              if (two) vs = next();
+              ok = ok && wait_uniform(b_p + 8 * r, pph[r]);
+              pph[r] ^= 1u;
+              if (!ok) continue;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < BN / 16; ++k)
+                mma_ts(lead, tm + L::O_COL + r * DH, tm + r * BN + k * 8, av + vs * (L::TILE >> 4) + k * (2048 >> 4),
+                       id_o, j > 0 || k > 0);
+              mma_commit(lead, b_o + 8 * r);
+              if (two) mma_commit(lead, b_empty + 8 * vs);
+              if (j + 1 < mine) {
+                if (two) ks = next();
+                if (!ok) continue;
+                tc_fence_after();
+                score(r, ks);
+                if (two) mma_commit(lead, b_empty + 8 * ks);
+              }
+            }
+            if (ok) {
+              if (!two) {
+                mma_commit(lead, b_empty + 8 * vs);
+                if (more) mma_commit(lead, b_empty + 8 * ks);
+              }
+              if (j + 2 == nt) mma_commit(lead, smem_u32(q_empty));  // the last scores are on their way
+            }
+          }
+        }
+        if (lane == 0) mbar_arrive(&i_empty[n & 1]);
       }
-      int vs = 1 % NS, ks = 2 % NS;    // slots of V(j), K(j+1) and the parity of their fill
-      uint32_t vph = 0, kph = 0;
-      for (int j = 0; j < un && ok; ++j) {
-        const bool more = j + 1 < un;
-        ok = wait_uniform(b_full + 8 * vs, vph) && (!more || wait_uniform(b_full + 8 * ks, kph));
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int mine = r ? un1 : un0;
-          if (!ok || j >= mine) continue;
-          ok = wait_uniform(b_p + 8 * r, (uint32_t)j & 1u);
-          if (!ok) continue;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_ts(lead, tm + L::O_COL + r * DH, tm + r * BN + k * 8, av + vs * (L::TILE >> 4) + k * (2048 >> 4), id_o,
-                   j > 0 || k > 0);
-          mma_commit(lead, b_o + 8 * r);
-          if (j + 1 < mine) score(r, ks);
+      if (!ok) *abort_flag = 1;
+    } else if (warp == 2) {
+      // ---- items
+      bool ok = true;
+      int idx = blockIdx.x;
+      const int total = MODE == PROMPT ? 0 : c.pre_items + __ldcg(&a.plan[2]) * c.units;
+      int taken = 0;
+      for (int n = 0; ok;) {
+        if (MODE == PROMPT && lane == 0 && idx >= 0) take_next_cta(answer, n_full);
+        bool put = idx < 0 || (MODE == PAGED && idx >= total);
+        const bool end = put;
+        Item it;
+        it.kind = -1;
+        if (!end) put = make_item<MODE>(c, idx, it);
+        if (put) {
+          if (n >= 2) ok = wait_uniform(smem_u32(&i_empty[n & 1]), ((uint32_t)(n >> 1) & 1u) ^ 1u);
+          if (!ok) {  // the answer asked for above still has to land
+            if (MODE == PROMPT && idx >= 0) wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
+            break;
+          }
+          if (lane == 0) {
+            items[n & 1] = it;
+            mbar_arrive(&i_full[n & 1]);
+          }
+          ++n;
         }
-        if (ok) {
-          mma_commit(lead, b_empty + 8 * vs);
-          if (more) mma_commit(lead, b_empty + 8 * ks);
-        }
-        vs += 2;
-        if (vs >= NS) {
-          vs -= NS;
-          vph ^= 1u;
-        }
-        ks += 2;
-        if (ks >= NS) {
-          ks -= NS;
-          kph ^= 1u;
+        if (end) break;
+        if (MODE == PROMPT) {
+          ok = wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
+          ++taken;
+          idx = ok ? taken_cta(answer) : -1;
+          __syncwarp();
+        } else {
+          if (lane == 0) idx = atomicAdd(&a.plan[0], 1);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
         }
       }
       if (!ok) *abort_flag = 1;
@@ -389,192 +578,287 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---- softmax: one thread per row
     const int r = warp >= 8, quad = warp & 3, row = quad * 32 + lane;
-    const int mine = r ? nt1 : nt0;
-    const int tl = r * c.tb + row / a.G;  // token within the item
-    const bool valid = row < c.tb * a.G && tl < ntok && mine > 0;
-    const int head = g * a.G + row % a.G;
-    int limit = 0x7fffffff;  // keys below it are seen (rows without a token: all, and dropped)
-    bool dead = false;       // an entry without tokens
-    const size_t orow = (size_t)start + t0 + tl;
-    if (valid) {
-      if (MODE == PROMPT) {
-        limit = t0 + tl + 1;
-      } else {
-        bool bad = false;
-        const int t = t0 + tl, len = attn_len(a, t / a.rows, bad);
-        dead = len == 0;
-        if (!dead) limit = max(0, len - a.rows + t % a.rows + 1);
-      }
-    }
-    if (valid && !dead) atomicMin(&low[r], limit);
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
-    const int glow = *(volatile int*)&low[r];
-    const int wlow = __reduce_min_sync(0xffffffffu, min(limit, j1));
-    const int lim = min(limit, j1);
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tmem + lanes + r * BN, to = tmem + lanes + L::O_COL + r * DH;
-    float mb = -INFINITY, l = 0.f;  // maximum in use, times qscale; sum of the weights
+    const uint32_t b_s = smem_u32(&s_full[r]), b_o = smem_u32(&o_full[r]);
+    const int row_tok = row / c.a.G, row_head = row % c.a.G;
+    int tiles = 0;  // key tiles of this row tile so far, and all tiles of the ring
+    int ring = 0;
     bool ok = true;
-    for (int j = 0; j < mine; ++j) {
-      const int jt = j0 + j * BN;
-      ok = mbar_wait(&s_full[r], (uint32_t)j & 1u);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      float s[BN];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s + q * 32);
-      tmem_wait_ld();
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_hold32(s + q * 32);
-      if (jt + BN > wlow) {
-#pragma unroll
-        for (int q = 0; q < BN; ++q)
-          if (jt + q >= lim) s[q] = -INFINITY;
+    for (int n = 0; ok; ++n) {
+      Item& it = items[n & 1];
+      ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+      if (!ok || it.kind < 0) break;
+      const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1;
+      const int g = it.g + (split ? r : 0);
+      const int tl = (split ? 0 : r * c.tb) + row_tok;  // token within the item
+      // a row of its own in out (also where there is no key at all)
+      const bool valid = row < c.tb * a.G && tl < it.ntok && g < a.Hkv;
+      const size_t orow = (size_t)it.tok0 + tl;
+      const int head = g * a.G + row_head;
+      int limit = kNone;   // keys below it are seen (rows without a token: all, and dropped)
+      bool dead = false;   // an entry without tokens
+      if (valid) {
+        if (MODE == PROMPT) {
+          limit = it.t0 + tl + 1;
+        } else {
+          const int t = it.t0 + tl;
+          const int len = it.kind == 1 ? __ldcg(&a.eff[t / a.rows]) : it.len;
+          dead = len == 0;
+          if (!dead) limit = max(0, len - a.rows + (it.kind == 1 ? t % a.rows : t) + 1);
+        }
       }
-      float t4[4] = {s[0], s[1], s[2], s[3]};
+      const int wleast = __reduce_min_sync(0xffffffffu, limit);
+      if (lane == 0) atomicMin(&it.low[r], wleast);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
+      const int glow = *(volatile int*)&it.low[r];
+      const bool any = __any_sync(0xffffffffu, valid);
+      const int wlow = min(wleast, j1), lim = min(limit, j1);
+      const int streams = split && it.nt[1] > 0 ? 2 : 1;
+      float mb = -INFINITY, l = 0.f;  // maximum in use, times qscale; sum of the weights
+      for (int j = 0; j < mine; ++j) {
+        const int jt = j0 + j * BN;
+        ok = wait_uniform(b_s, (uint32_t)(tiles + j) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        if (any) {
+          float s[BN];
 #pragma unroll
-      for (int q = 4; q < BN; ++q) t4[q & 3] = fmaxf(t4[q & 3], s[q]);
-      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.qscale;
-      bool lift = top > mb + 8.f;
-      if (__any_sync(0xffffffffu, lift)) {
-        // (mb = -infinity: the sums are zero, or not written yet)
-        const float nm = lift ? top : mb;
-        const float f = mb > -INFINITY ? ex2(mb - nm) : 1.f;
-        if (j > 0 && __any_sync(0xffffffffu, lift && mb > -INFINITY)) {
-          ok = mbar_wait(&o_full[r], (uint32_t)(j - 1) & 1u);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after();
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s + q * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_hold32(s + q * 32);
+          if (jt + BN > wlow) {
+#pragma unroll
+            for (int q = 0; q < BN; ++q)
+              if (jt + q >= lim) s[q] = -INFINITY;
+          }
+          float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int q = 4; q < BN; ++q) t4[q & 3] = fmaxf(t4[q & 3], s[q]);
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.qscale;
+          const bool lift = top > mb + 8.f;
+          if (__any_sync(0xffffffffu, lift)) {
+            // (mb = -infinity: the sums are zero, or not written yet)
+            const float nm = lift ? top : mb;
+            const float f = mb > -INFINITY ? ex2(mb - nm) : 1.f;
+            if (j > 0 && __any_sync(0xffffffffu, lift && mb > -INFINITY)) {
+              ok = wait_uniform(b_o, (uint32_t)(tiles + j - 1) & 1u);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < DH; q += 32) {
-            float o[32];
+              for (int q = 0; q < DH; q += 32) {
+                float o[32];
+                tmem_ld32(to + q, o);
+                tmem_wait_ld();
+                tmem_hold32(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= f;
+                tmem_st32(to + q, reinterpret_cast<uint32_t*>(o));
+              }
+              tmem_wait_st();
+            }
+            l *= f;
+            mb = nm;
+          }
+          const float base = mb > -INFINITY ? mb : 0.f;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float e0 = ex2(fmaf(s[h * 64 + 2 * q], a.qscale, -base));
+              const float e1 = ex2(fmaf(s[h * 64 + 2 * q + 1], a.qscale, -base));
+              l4[q & 1] += e0;
+              l4[2 + (q & 1)] += e1;
+              p[q] = pack_bf16(e0, e1);
+            }
+            tmem_st32(ts + h * 32, p);
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          tmem_wait_st();
+        }
+        if (min(glow, j1) < (MODE == PROMPT ? jt + BN : min(jt + BN, (j1 + a.page - 1) / a.page * a.page))) {
+          // some row of the group masks keys that the tile holds (behind the last page it holds zeros)
+          const int nt = max(it.nt[0], it.nt[1]);
+          const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j + (j + 1 < nt ? 2 * r : r)), vs = vi % NS;
+          ok = wait_uniform(smem_u32(&full[vs]), (uint32_t)(vi / NS) & 1u);
+          if (!ok) break;
+          uint4* v = reinterpret_cast<uint4*>(sKV + (size_t)vs * L::TILE);
+          for (int q = row; q < L::TILE / 16; q += 128) {
+            uint4 x = v[q];
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (odd_half(w[k])) {
+                w[k] &= 0xffff0000u;
+                odd = true;
+              }
+              if (odd_half(w[k] >> 16)) {
+                w[k] &= 0x0000ffffu;
+                odd = true;
+              }
+            }
+            if (odd) {
+              atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
+              __threadfence_block();
+              v[q] = x;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[r]);
+      }
+      if (!ok) break;
+      // ---- the item's end
+      if (mine > 0) {
+        ok = wait_uniform(b_o, (uint32_t)(tiles + mine - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      tiles += mine;
+      ring += 2 * max(it.nt[0], it.nt[1]) * streams;
+      if (any) {
+        const bool direct = it.direct;
+        const float inv = l == 0.f || dead ? 0.f : 1.f / l;
+        const int from = *(volatile int*)&it.odd[streams == 1 ? 0 : r];
+        const size_t N = (size_t)a.n * a.rows * a.Hq;
+        const size_t pr = it.kind == 1 ? it.part * N + orow * a.Hq + head
+                                       : a.npre * N + ((size_t)it.part * a.rows + it.t0 + tl) * a.Hq + head;
+#pragma unroll 1
+        for (int q = 0; q < DH; q += 32) {
+          float o[32];
+          if (mine > 0) {
             tmem_ld32(to + q, o);
             tmem_wait_ld();
             tmem_hold32(o);
+          } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= f;
-            tmem_st32(to + q, reinterpret_cast<uint32_t*>(o));
+            for (int k = 0; k < 32; ++k) o[k] = 0.f;
           }
-          tmem_wait_st();
-        }
-        l *= f;
-        mb = nm;
-      }
-      const float base = mb > -INFINITY ? mb : 0.f;
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          if (valid && !dead && from < lim)
+            for (int k = 0; k < 32; ++k) o[k] += odd_sum<MODE>(a, it, g, from, lim, q + k);
+          if (!valid) continue;
+          if (direct) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.out_ld +
+                                                  (size_t)head * DH + q);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const float e0 = ex2(fmaf(s[h * 64 + 2 * q], a.qscale, -base));
-          const float e1 = ex2(fmaf(s[h * 64 + 2 * q + 1], a.qscale, -base));
-          l4[q & 1] += e0;
-          l4[2 + (q & 1)] += e1;
-          p[q] = pack_bf16(e0, e1);
-        }
-        tmem_st32(ts + h * 32, p);
-      }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tmem_wait_st();
-      if (glow < (MODE == PROMPT ? jt + BN : min(jt + BN, j1))) {
-        // some row of the group masks keys of this tile
-        const int vi = 2 * j + 1, vs = vi % NS;
-        ok = mbar_wait(&full[vs], (uint32_t)(vi / NS) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        uint4* v = reinterpret_cast<uint4*>(sKV + (size_t)vs * L::TILE);
-        for (int q = row; q < L::TILE / 16; q += 128) {
-          uint4 x = v[q];
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-          bool odd = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (odd_half(w[k])) {
-              w[k] &= 0xffff0000u;
-              odd = true;
+              for (int x = 0; x < 4; ++x)
+                w[x] = dead ? 0u : pack_bf16(o[8 * k + 2 * x] * inv, o[8 * k + 2 * x + 1] * inv);
+              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (odd_half(w[k] >> 16)) {
-              w[k] &= 0x0000ffffu;
-              odd = true;
-            }
-          }
-          if (odd) {
-            atomicMin(odd_from, jt);
-            __threadfence_block();
-            v[q] = x;
+          } else if (mine > 0) {
+            float4* dst = reinterpret_cast<float4*>(&a.part_o[pr * DH + q]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (!direct && valid)
+          a.part_ml[pr] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(mb, l);
+        tc_fence_before();
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[r]);
+      if (lane == 0) mbar_arrive(&i_empty[n & 1]);
     }
-    // ---- epilogue
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && mine > 0) {
-      ok = mbar_wait(&o_full[r], (uint32_t)(mine - 1) & 1u);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (!ok) {
-      *abort_flag = 1;
-    } else if (work) {
-      const bool direct = MODE == PROMPT || attn_direct(a);
-      const float inv = l == 0.f || dead ? 0.f : 1.f / l;
-      const int from = *(volatile int*)odd_from;
-      const size_t N = (size_t)a.n * a.rows * a.Hq;
-      const bool mine_row = row < c.tb * a.G && tl < ntok;  // also where there was no key at all
-      const size_t pr = piece * N + orow * a.Hq + head;
-#pragma unroll 1
-      for (int q = 0; q < DH; q += 32) {
-        float o[32];
-        if (mine > 0) {
-          tmem_ld32(to + q, o);
-          tmem_wait_ld();
-          tmem_hold32(o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        }
-        if (valid && !dead && from < lim)
-          for (int k = 0; k < 32; ++k) o[k] += odd_sum<MODE>(a, start, tab, g, from, lim, q + k);
-        if (!mine_row) continue;
-        if (direct) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.out_ld +
-                                                (size_t)head * DH + q);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = dead ? 0u : pack_bf16(o[8 * k + 2 * x] * inv, o[8 * k + 2 * x + 1] * inv);
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (mine > 0) {
-          float4* dst = reinterpret_cast<float4*>(&a.part_o[pr * DH + q]);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
-      }
-      if (!direct && mine_row) {
-        a.part_ml[pr] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(mb, l);
-      }
-    }
-    tc_fence_before();
+    if (!ok) *abort_flag = 1;
   }
   __syncwarp();
   __syncthreads();
   if (*abort_flag) {
     if (tid == 0) {
       if (a.status) atomicOr(a.status, HF_S_TIMEOUT);
-      if (nt > 0) mbar_wait(q_full, 0);
       // the copies still in flight land before the CTA's shared memory goes
-      for (int i = max(0, *issued - NS); i < *issued; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u);
+      if (issued[1] > 0) mbar_wait(q_full, (uint32_t)(issued[1] - 1) & 1u);
+      for (int i = max(0, issued[0] - NS); i < issued[0]; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u);
     }
     __syncthreads();
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Which entries the call sees, and how the requests' own keys are cut: one CTA for
+// the lengths and the list of pieces, the others compare the entries' prefixes.
+//   plan: [0] counter of items, [1] keys per piece, [2] pieces
+__global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int units, int first) {
+  __shared__ long long s_sum[32];
+  __shared__ int s_scan[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x > 0) {
+    if (a.shared == 0 || !a.status) return;
+    bool bad = false, first_bad = false;
+    if (attn_raw_len(a, 0, first_bad) == 0) return;
+    const int32_t* t0 = attn_table(a, 0);
+    for (int i = blockIdx.x; i < a.n; i += gridDim.x - 1) {
+      bool skip = false;
+      if (attn_raw_len(a, i, skip) == 0) continue;
+      const int32_t* t = attn_table(a, i);
+      for (int j = tid; j < a.shared / a.page; j += 1024) bad = bad || __ldg(&t[j]) != __ldg(&t0[j]);
+    }
+    if (bad) atomicOr(a.status, HF_S_BAD);
+    return;
+  }
+  bool bad = false;
+  long long tiles = 0;
+  for (int i = tid; i < a.n; i += 1024) {
+    const int len = attn_len(a, i, bad);
+    a.eff[i] = len;
+    tiles += (max(0, len - a.shared) + BN - 1) / BN;
+  }
+  if (bad && a.status) atomicOr(a.status, HF_S_BAD);
+  if (budget <= 0) return;  // pieces of a fixed number of keys
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  if (lane == 0) s_sum[warp] = tiles;
+  __syncthreads();
+  long long all = 0;
+  for (int w = 0; w < 32; ++w) all += s_sum[w];
+  // as many pieces as the workspace holds at most; few keys per piece where that keeps
+  // the SMs busy, else at least 4 tiles
+  const int c_room = (int)((all + budget - 1) / budget);
+  const long long busy = (all * units + 303) / 304;
+  const int chunk = max(1, max(c_room, (int)min(busy, 4ll)));
+  int carry = 0;
+  for (int i0 = 0; i0 < a.n; i0 += 1024) {
+    const int i = i0 + tid;
+    int p = 0;
+    if (i < a.n) p = max(1, ((max(0, a.eff[i] - a.shared) + BN - 1) / BN + chunk - 1) / chunk);
+    int x = p;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = carry, sum = carry;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      sum += s_scan[w];
+    }
+    const int b = before + x - p;
+    if (i < a.n) {
+      a.base[i] = b;
+      for (int k = 0; k < p; ++k) a.piece_of[b + k] = i;
+    }
+    carry = sum;
+  }
+  if (tid == 0) {
+    a.base[a.n] = carry;
+    a.plan[0] = first;
+    a.plan[1] = chunk * BN;
+    a.plan[2] = carry;
+  }
 }
 
 constexpr int kMaxDev = 64;
@@ -600,35 +884,80 @@ cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mq, const CUtensorMap
   return launch_pdl(tc_kernel<DH, MODE>, grid, dim3(TCT), Tc<DH>::smem(), st, mq, mk, mv, c);
 }
 
-template <int MODE>
-cudaError_t launch_mode(const AttnRows& a, cudaStream_t st) {
+}  // namespace
+
+bool attn_tc_ok(int dtype, int dh) { return dtype == HF_BF16 && (dh == 64 || dh == 128); }
+
+cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) {
   TcArgs c{};
   c.a = a;
   c.tb = 128 / a.G;
-  const long long tokens = MODE == PROMPT ? a.total : (long long)a.n * a.rows;
-  c.items = (int)(MODE == PROMPT ? prompt_slots(a.total, a.n_seq, 1, 2 * c.tb) : (tokens + 2 * c.tb - 1) / (2 * c.tb));
-  c.box_rows = MODE == PROMPT ? BN : a.page;
+  c.blocks = (int)prompt_slots(a.total, a.n_seq, 1, 2 * c.tb);
+  c.box_rows = BN;
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = make_map_3d(&mq, a.q, a.dh, a.Hq, a.total, a.dh, a.q_ld, a.G, c.tb);
+  if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.Hkv, a.total, a.dh, a.k_ld, 1, BN);
+  if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.Hkv, a.total, a.dh, a.v_ld, 1, BN);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((long long)c.blocks * a.Hkv));
+  return a.dh == 128 ? launch_one<128, PROMPT>(c, mq, mk, mv, grid, st)
+                     : launch_one<64, PROMPT>(c, mq, mk, mv, grid, st);
+}
+
+cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, cudaStream_t st) {
+  const int checks = a.shared > 0 && a.status ? std::min(a.n, 151) : 0;
+  return launch_pdl(plan_kernel, dim3(1 + checks), dim3(1024), 0, st, a, budget, units, first);
+}
+
+// Rows of a tile, blocks and items of a call over a paged cache.
+void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget) {
+  const int tb = 128 / a.G, heads = (a.Hkv + 1) / 2;
+  const long long tokens = (long long)a.n * a.rows;
+  const long long blocks = tokens <= tb ? 1 : (tokens + 2 * tb - 1) / (2 * tb);
+  const long long per = tokens <= tb ? heads : blocks * a.Hkv;  // items of one piece of the prefix
+  units = a.rows <= tb ? heads : (a.rows + 2 * tb - 1) / (2 * tb) * a.Hkv;
+  a.npre = 0;
+  a.pre_keys = BN;
+  if (a.shared > 0) {
+    // pieces of the prefix: the least of (rounds of items over the SMs) * (tiles of a piece,
+    // an item's start and end) plus what a piece costs to write and join
+    const int tiles = (a.shared + BN - 1) / BN;
+    double best = 1e30;
+    for (int p = 1; p <= 64 && p <= tiles; ++p) {
+      const int each = (tiles + p - 1) / p;
+      const double rounds = (double)((per * p + 151) / 152);
+      const double cost = rounds * (each + 2) + 0.02 * (double)p * (double)tokens * a.Hq * a.dh / (152 * 4096.0);
+      if (cost < best) {
+        best = cost;
+        a.npre = (tiles + each - 1) / each;
+        a.pre_keys = each * BN;
+      }
+    }
+  }
+  pre_items = (int)(per * a.npre);
+  budget = std::max(8, (152 * 4 + units - 1) / units);
+}
+
+cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, int budget, cudaStream_t st) {
+  TcArgs c{};
+  c.a = a;
+  c.tb = 128 / a.G;
+  const long long tokens = (long long)a.n * a.rows, block = (long long)a.page * a.dh;
+  c.blocks = (int)((tokens + 2 * c.tb - 1) / (2 * c.tb));
+  c.box_rows = a.page;
+  c.pre_items = pre_items;
+  c.units = units;
   CUtensorMap mq, mk, mv;
   cudaError_t e = make_map_3d(&mq, a.q, a.dh, a.Hq, tokens, a.dh, a.q_ld, a.G, c.tb);
-  if (MODE == PROMPT) {
-    if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.Hkv, a.total, a.dh, a.k_ld, 1, BN);
-    if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.Hkv, a.total, a.dh, a.v_ld, 1, BN);
-  } else {
-    const long long block = (long long)a.page * a.dh;
-    if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
-    if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
-  }
+  if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
+  if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((long long)c.items * a.Hkv), MODE == PROMPT ? 1 : a.npre);
-  return a.dh == 128 ? launch_one<128, MODE>(c, mq, mk, mv, grid, st) : launch_one<64, MODE>(c, mq, mk, mv, grid, st);
+  const long long most = pre_items + ((long long)a.n + budget) * units;
+  const int grid = (int)std::min<long long>(most, 152);
+  e = launch_attn_plan(a, budget, units, grid, st);
+  if (e != cudaSuccess) return e;
+  return a.dh == 128 ? launch_one<128, PAGED>(c, mq, mk, mv, dim3(grid), st)
+                     : launch_one<64, PAGED>(c, mq, mk, mv, dim3(grid), st);
 }
-
-}  // namespace
-
-bool attn_tc_ok(int dtype, const AttnRows& a) {
-  return dtype == HF_BF16 && (a.dh == 64 || a.dh == 128);
-}
-cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) { return launch_mode<PROMPT>(a, st); }
-cudaError_t launch_attn_tc_prefix(const AttnRows& a, cudaStream_t st) { return launch_mode<PREFIX>(a, st); }
 
 }  // namespace hf
