@@ -294,55 +294,125 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
   }
 }
 
-// One warp per row: the row's pieces weighted by 2^(m - max m).
-template <typename T>
+// The row's pieces weighted by 2^(m - max m): WPR warps of a CTA share a row, each
+// joins every WPR-th piece, the CTA's last step joins the warps. Pieces that saw
+// nothing hold no values and are not read.
+template <typename T, int WPR>
 __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
+  constexpr int RPC = 8 / WPR;  // rows per CTA
+  __shared__ float s_acc[WPR > 1 ? 8 : 1][WPR > 1 ? 256 : 1];
+  __shared__ float2 s_ml[8];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, dh = a.dh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR, dh = a.dh;
   const size_t N = (size_t)a.n * a.rows * a.Hq;
-  const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= N) return;
-  const int token = (int)(row / a.Hq), head = (int)(row % a.Hq), entry = token / a.rows;
+  const size_t row = (size_t)blockIdx.x * RPC + warp / WPR;
+  bool on = row < N;
+  const int token = on ? (int)(row / a.Hq) : 0, head = on ? (int)(row % a.Hq) : 0, entry = token / a.rows;
   int own;
   const int first = attn_pieces(a, entry, own);
-  if (a.npre == 0 && own == 1 && (a.plan || attn_direct(a))) return;  // written already
-  const int pieces = __ldcg(&a.eff[entry]) > 0 ? a.npre + own : 0;
+  if (a.npre == 0 && own == 1 && (a.plan || attn_direct(a))) on = false;  // written already
+  const int pieces = on && __ldcg(&a.eff[entry]) > 0 ? a.npre + own : 0;
   // piece p's row: the prefix's pieces come first
   auto at = [&](int p) {
     return p < a.npre ? p * N + row
                       : a.npre * N + ((size_t)(first + p - a.npre) * a.rows + token % a.rows) * a.Hq + head;
   };
-  float m = -INFINITY;
-  for (int p = lane; p < pieces; p += 32) m = fmaxf(m, __ldcg(&a.part_ml[at(p)]).x);
-  m = warp_max(m);
-  float acc[8] = {};
-  float l = 0.f;
-  const float base = m > -INFINITY ? m : 0.f;
-#pragma unroll 4
-  for (int p = 0; p < pieces; ++p) {
-    const size_t r = at(p);
-    const float2 ml = __ldcg(&a.part_ml[r]);
-    if (ml.y == 0.f) continue;  // saw nothing there (its row was not written)
-    const float w = exp2f(ml.x - base);
-    l = fmaf(ml.y, w, l);
+  float m = -INFINITY, l = 0.f, acc[8] = {};
+  for (int p0 = sub; p0 < pieces; p0 += 32 * WPR) {
+    // this lane's piece of the next 32
+    const int p = p0 + lane * WPR;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    size_t r = 0;
+    if (p < pieces) {
+      r = at(p);
+      ml = __ldcg(&a.part_ml[r]);
+    }
+    const float nm = fmaxf(m, warp_max(ml.x));
+    const float base = nm > -INFINITY ? nm : 0.f;
+    const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - base), f = exp2f(m - base);
+    const bool used = !(ml.y == 0.f);
+    l = l * f + warp_sum(used ? ml.y * w : 0.f);
+    m = nm;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= f;
+    const int count = min(32, (pieces - p0 + WPR - 1) / WPR);
+    for (int k0 = 0; k0 < count; k0 += 4) {
+      float4 x[4][2];
+      float wk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const size_t rk = __shfl_sync(0xffffffffu, r, (k0 + k) & 31);
+        wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        const bool read = k0 + k < count && __shfl_sync(0xffffffffu, (int)used, (k0 + k) & 31);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          x[k][c] = read && lane * 4 + 128 * c < dh
+                        ? __ldcg(reinterpret_cast<const float4*>(&a.part_o[rk * dh + lane * 4 + 128 * c]))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!read) wk[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          acc[4 * c + 0] = fmaf(wk[k], x[k][c].x, acc[4 * c + 0]);
+          acc[4 * c + 1] = fmaf(wk[k], x[k][c].y, acc[4 * c + 1]);
+          acc[4 * c + 2] = fmaf(wk[k], x[k][c].z, acc[4 * c + 2]);
+          acc[4 * c + 3] = fmaf(wk[k], x[k][c].w, acc[4 * c + 3]);
+        }
+    }
+  }
+  if (WPR > 1) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      if (lane * 4 + 128 * c < dh) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(&a.part_o[r * dh + lane * 4 + 128 * c]));
-        acc[4 * c + 0] = fmaf(w, x.x, acc[4 * c + 0]);
-        acc[4 * c + 1] = fmaf(w, x.y, acc[4 * c + 1]);
-        acc[4 * c + 2] = fmaf(w, x.z, acc[4 * c + 2]);
-        acc[4 * c + 3] = fmaf(w, x.w, acc[4 * c + 3]);
-      }
+      if (lane * 4 + 128 * c < dh)
+        *reinterpret_cast<float4*>(&s_acc[warp][lane * 4 + 128 * c]) =
+            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (sub) return;
+    float nm = m;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) nm = fmaxf(nm, s_ml[warp + k].x);
+    const float base = nm > -INFINITY ? nm : 0.f;
+    const float f = exp2f(m - base);
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= f;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      const float2 ml = s_ml[warp + k];
+      const float w = exp2f(ml.x - base);
+      l += ml.y == 0.f ? 0.f : ml.y * w;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (lane * 4 + 128 * c < dh) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_acc[warp + k][lane * 4 + 128 * c]);
+          acc[4 * c + 0] = fmaf(w, x.x, acc[4 * c + 0]);
+          acc[4 * c + 1] = fmaf(w, x.y, acc[4 * c + 1]);
+          acc[4 * c + 2] = fmaf(w, x.z, acc[4 * c + 2]);
+          acc[4 * c + 3] = fmaf(w, x.w, acc[4 * c + 3]);
+        }
+    }
   }
+  if (!on) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* dst = static_cast<T*>(a.out) + (size_t)token * a.out_ld + (size_t)head * dh;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    if (lane * 4 + 128 * c < dh)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) dst[lane * 4 + 128 * c + k] = from_f<T>(acc[4 * c + k] * inv);
+    if (lane * 4 + 128 * c < dh) {
+      const int d = lane * 4 + 128 * c;
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(&dst[d]) =
+            make_float4(acc[4 * c] * inv, acc[4 * c + 1] * inv, acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
+      } else {
+        uint2 x;
+        *reinterpret_cast<__nv_bfloat162*>(&x.x) = __floats2bfloat162_rn(acc[4 * c] * inv, acc[4 * c + 1] * inv);
+        *reinterpret_cast<__nv_bfloat162*>(&x.y) = __floats2bfloat162_rn(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
+        *reinterpret_cast<uint2*>(&dst[d]) = x;
+      }
+    }
 }
 
 constexpr int kMaxDev = 64;
@@ -391,11 +461,16 @@ cudaError_t launch_attn_rows_own(int dtype, const AttnRows& a, cudaStream_t st) 
   const int blocks = (a.rows * a.G + BM - 1) / BM;
   return launch_mode<OWN>(dtype, a, dim3((unsigned)(a.n * blocks), a.Hkv, a.nown), st);
 }
-cudaError_t launch_attn_join(int dtype, const AttnRows& a, cudaStream_t st) {
+cudaError_t launch_attn_join(int dtype, const AttnRows& a, int pieces, cudaStream_t st) {
   const long long N = (long long)a.n * a.rows * a.Hq;
-  const dim3 grid((unsigned)((N + 7) / 8));
-  if (dtype == HF_F32) return launch_pdl(join_kernel<float>, grid, dim3(256), 0, st, a);
-  return launch_pdl(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a);
+  const int wpr = pieces > 12 ? 8 : pieces > 6 ? 2 : 1;
+  const dim3 grid((unsigned)((N * wpr + 7) / 8));
+  using bf = __nv_bfloat16;
+  if (dtype == HF_F32)
+    return launch_pdl(wpr == 8 ? join_kernel<float, 8> : wpr == 2 ? join_kernel<float, 2> : join_kernel<float, 1>, grid,
+                      dim3(256), 0, st, a);
+  return launch_pdl(wpr == 8 ? join_kernel<bf, 8> : wpr == 2 ? join_kernel<bf, 2> : join_kernel<bf, 1>, grid, dim3(256),
+                    0, st, a);
 }
 
 namespace {
@@ -601,6 +676,6 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
     if (e == cudaSuccess && a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
     if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
   }
-  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, st);
+  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, a.npre + (w.tc ? 1 + w.budget / n : a.nown), st);
   return done(e);
 }

@@ -40,7 +40,7 @@ struct Tc {
   static constexpr int TILE = BN * DH * 2;            // bytes of a K, V or Q tile
   static constexpr int SLOTS = DH == 128 ? 5 : 10;    // ring of K and V tiles
   static constexpr int O_COL = 256;                   // TMEM: S0 | S1 | O0 | O1
-  static constexpr size_t smem() { return 1024 + (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 16) * 8 + 16 + 2 * 80 + 32; }
+  static constexpr size_t smem() { return (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 14) * 8 + 16 + 2 * 80 + 48; }
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -140,6 +140,32 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two floats a 64-bit register: one instruction for two multiply-adds or sums.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -325,8 +351,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   using L = Tc<DH>;
   constexpr int NS = L::SLOTS, HALVES = DH / 64, HALF = BN * 128;
   const AttnRows& a = c.a;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (no other shared memory in this kernel: the tiles start at the alignment that their swizzle needs)
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * L::TILE;
   uint64_t* full = reinterpret_cast<uint64_t*>(sKV + (size_t)NS * L::TILE);
@@ -588,6 +614,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     for (int n = 0; ok; ++n) {
       Item& it = items[n & 1];
       ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+      // (a warp that gives up still arrives at the barrier that its partners may come to)
+      if (!ok) asm volatile("bar.arrive %0, 128;" ::"r"(1 + r) : "memory");
       if (!ok || it.kind < 0) break;
       const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1;
       const int g = it.g + (split ? r : 0);
@@ -613,6 +641,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
       const int glow = *(volatile int*)&it.low[r];
       const bool any = __any_sync(0xffffffffu, valid);
+      const int hold = MODE == PROMPT ? kNone : (j1 + a.page - 1) / a.page * a.page;
       const int wlow = min(wleast, j1), lim = min(limit, j1);
       const int streams = split && it.nt[1] > 0 ? 2 : 1;
       float mb = -INFINITY, l = 0.f;  // maximum in use, times qscale; sum of the weights
@@ -633,10 +662,14 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             for (int q = 0; q < BN; ++q)
               if (jt + q >= lim) s[q] = -INFINITY;
           }
-          float t4[4] = {s[0], s[1], s[2], s[3]};
+          float t8[8];
 #pragma unroll
-          for (int q = 4; q < BN; ++q) t4[q & 3] = fmaxf(t4[q & 3], s[q]);
-          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.qscale;
+          for (int q = 0; q < 8; ++q) t8[q] = fmaxf(s[q], s[q + 8]);
+#pragma unroll
+          for (int q = 16; q < BN; q += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t8[k] = max3(t8[k], s[q + k], s[q + k + 8]);
+          const float top = max3(max3(t8[0], t8[1], t8[2]), max3(t8[3], t8[4], t8[5]), fmaxf(t8[6], t8[7])) * a.qscale;
           const bool lift = top > mb + 8.f;
           if (__any_sync(0xffffffffu, lift)) {
             // (mb = -infinity: the sums are zero, or not written yet)
@@ -662,25 +695,27 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             mb = nm;
           }
           const float base = mb > -INFINITY ? mb : 0.f;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t qs2 = pair(a.qscale, a.qscale), base2 = pair(-base, -base);
+          uint64_t l2[2] = {0, 0};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t p[32];
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float e0 = ex2(fmaf(s[h * 64 + 2 * q], a.qscale, -base));
-              const float e1 = ex2(fmaf(s[h * 64 + 2 * q + 1], a.qscale, -base));
-              l4[q & 1] += e0;
-              l4[2 + (q & 1)] += e1;
-              p[q] = pack_bf16(e0, e1);
+              float2 e = unpair(fma2(pair(s[h * 64 + 2 * q], s[h * 64 + 2 * q + 1]), qs2, base2));
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              l2[q & 1] = add2(l2[q & 1], pair(e.x, e.y));
+              p[q] = pack_bf16(e.x, e.y);
             }
             tmem_st32(ts + h * 32, p);
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          const float2 la = unpair(l2[0]), lb = unpair(l2[1]);
+          l += (la.x + la.y) + (lb.x + lb.y);
           tmem_wait_st();
         }
-        if (min(glow, j1) < (MODE == PROMPT ? jt + BN : min(jt + BN, (j1 + a.page - 1) / a.page * a.page))) {
-          // some row of the group masks keys that the tile holds (behind the last page it holds zeros)
+        // some row of the group masks keys that the tile holds (behind the last page it holds zeros)
+        if (min(glow, j1) < min(jt + BN, hold)) {
           const int nt = max(it.nt[0], it.nt[1]);
           const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j + (j + 1 < nt ? 2 * r : r)), vs = vi % NS;
           ok = wait_uniform(smem_u32(&full[vs]), (uint32_t)(vi / NS) & 1u);
@@ -741,7 +776,12 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
           }
           if (valid && !dead && from < lim)
-            for (int k = 0; k < 32; ++k) o[k] += odd_sum<MODE>(a, it, g, from, lim, q + k);
+#pragma unroll 1
+            for (int k = 0; k < 32; ++k) {
+              const float x = odd_sum<MODE>(a, it, g, from, lim, q + k);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = i == k ? o[i] + x : o[i];
+            }
           if (!valid) continue;
           if (direct) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.out_ld +
@@ -788,7 +828,6 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 // the lengths and the list of pieces, the others compare the entries' prefixes.
 //   plan: [0] counter of items, [1] keys per piece, [2] pieces
 __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int units, int first) {
-  __shared__ long long s_sum[32];
   __shared__ int s_scan[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -808,25 +847,43 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
     return;
   }
   bool bad = false;
-  long long tiles = 0;
-  for (int i = tid; i < a.n; i += 1024) {
-    const int len = attn_len(a, i, bad);
-    a.eff[i] = len;
-    tiles += (max(0, len - a.shared) + BN - 1) / BN;
-  }
+  for (int i = tid; i < a.n; i += 1024) a.eff[i] = attn_len(a, i, bad);
   if (bad && a.status) atomicOr(a.status, HF_S_BAD);
   if (budget <= 0) return;  // pieces of a fixed number of keys
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-  if (lane == 0) s_sum[warp] = tiles;
+  // Keys per piece: of some sizes the one with the least (rounds of items over the SMs) *
+  // (tiles of an item + about one for its start and end), the pieces fitting the workspace
+  constexpr int NC = 8;
+  __shared__ int s_count[NC + 1];
+  auto size_of = [](int k) { return 1 << k; };
+  if (tid <= NC) s_count[tid] = 0;
   __syncthreads();
-  long long all = 0;
-  for (int w = 0; w < 32; ++w) all += s_sum[w];
-  // as many pieces as the workspace holds at most; few keys per piece where that keeps
-  // the SMs busy, else at least 4 tiles
-  const int c_room = (int)((all + budget - 1) / budget);
-  const long long busy = (all * units + 303) / 304;
-  const int chunk = max(1, max(c_room, (int)min(busy, 4ll)));
+  int mine[NC + 1] = {};
+  for (int i = tid; i < a.n; i += 1024) {
+    const int t = (max(0, a.eff[i] - a.shared) + BN - 1) / BN;
+    mine[NC] += t;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) mine[k] += max(1, (t + size_of(k) - 1) / size_of(k));
+  }
+#pragma unroll
+  for (int k = 0; k <= NC; ++k) {
+    const int s = __reduce_add_sync(0xffffffffu, mine[k]);
+    if (lane == 0 && s) atomicAdd(&s_count[k], s);
+  }
+  __syncthreads();
+  const int all = s_count[NC];
+  int chunk = max(1, all / budget + 1);  // always fits
+  {
+    float best = 3e38f;
+    for (int k = 0; k < NC; ++k) {
+      if (s_count[k] > a.n + budget) continue;
+      const float rounds = (float)s_count[k] * units * (1.f / 152.f);
+      const float cost = (rounds < 6.f ? ceilf(rounds) : rounds + 0.5f) * ((float)min(size_of(k), all) + 1.5f);
+      if (cost < best) {
+        best = cost;
+        chunk = size_of(k);
+      }
+    }
+  }
   int carry = 0;
   for (int i0 = 0; i0 < a.n; i0 += 1024) {
     const int i = i0 + tid;
@@ -935,7 +992,7 @@ void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget) {
     }
   }
   pre_items = (int)(per * a.npre);
-  budget = std::max(8, (152 * 4 + units - 1) / units);
+  budget = std::max(8, (152 * 8 + units - 1) / units);
 }
 
 cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, int budget, cudaStream_t st) {
