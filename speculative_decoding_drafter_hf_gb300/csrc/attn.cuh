@@ -33,10 +33,12 @@ struct AttnRows {
   // entry's own tokens: on CUDA cores nown pieces of own_keys each (unused ones
   // among them), on tensor cores as many as the plan gives it. An entry of one
   // piece in all has its rows written straight to out; the others' go to part_o /
-  // part_ml, rows (token, query head) within a piece, and attn_join joins them: the
-  // prefix's pieces of n * rows * Hq rows, then the entries' of rows * Hq.
+  // part_ml and attn_join joins them: the prefix's pieces of n * rows * Hq rows each,
+  // then the entries' of rows * Hq. Within a piece rows are ordered (KV head, token,
+  // head in its group), and part_o holds 8 columns of all rows, then the next 8: a
+  // warp with a row per lane writes whole lines.
   int npre, pre_keys, nown, own_keys;
-  float* part_o;   // [...][dh], not normalised
+  float* part_o;   // [...][dh / 8][rows of the piece][8], not normalised
   float2* part_ml; // the same rows: maximum (base 2), sum
   // written on the device before the pieces are read
   int* eff;        // [n] tokens of each entry, 0 for those that break a rule
@@ -46,6 +48,16 @@ struct AttnRows {
 };
 
 __host__ __device__ inline bool attn_direct(const AttnRows& a) { return a.npre + a.nown == 1; }
+
+// Rows before piece p of the prefix or, own, before a piece of an entry, and the row
+// of (KV head g, token t of `tokens`, head i in the group) within it.
+__device__ __forceinline__ size_t part_first(const AttnRows& a, bool own, int p) {
+  const size_t N = (size_t)a.n * a.rows * a.Hq;
+  return own ? a.npre * N + (size_t)p * a.rows * a.Hq : p * N;
+}
+__device__ __forceinline__ int part_row(const AttnRows& a, bool own, int g, int t, int i) {
+  return (g * (own ? a.rows : a.n * a.rows) + t) * a.G + i;
+}
 
 // First piece of entry i's own tokens, and how many there are.
 __device__ __forceinline__ int attn_pieces(const AttnRows& a, int i, int& count) {
@@ -136,7 +148,7 @@ cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
 void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget);
 cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, int budget, cudaStream_t st);
 // Entries' lengths and status checks; with budget > 0 the pieces of the entries.
-cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, cudaStream_t st);
+cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, int pre_items, cudaStream_t st);
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
 cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st);

@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
       }
   }
   const bool direct = MODE == PROMPT || attn_direct(a);
-  const size_t N = (size_t)a.n * a.rows * a.Hq;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (ty * 4 + i >= nrows) continue;
@@ -281,138 +280,126 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
         if (d < dh) dst[d] = from_f<T>(o[i][c] * inv);
       }
     } else {
-      const size_t r = MODE == PREFIX ? piece * N + orow[i] * a.Hq + head[i]
-                                      : a.npre * N + (((size_t)entry * a.nown + piece) * a.rows +
-                                                      (orow[i] - (size_t)entry * a.rows)) * a.Hq + head[i];
-      if (tx == 0) a.part_ml[r] = make_float2(m[i], l[i]);
+      const bool own = MODE == OWN;
+      const size_t first = part_first(a, own, own ? entry * a.nown + piece : piece);
+      const size_t region = (size_t)(own ? a.rows : a.n * a.rows) * a.Hq;
+      const int rr = row0 + ty * 4 + i;
+      const size_t r = part_row(a, own, g, rr / a.G, rr % a.G);
+      if (tx == 0) a.part_ml[first + r] = make_float2(m[i], l[i]);
 #pragma unroll
-      for (int c = 0; c < MAXC; ++c)
-        if (tx * 4 + 64 * c < dh)
-          *reinterpret_cast<float4*>(&a.part_o[r * dh + tx * 4 + 64 * c]) =
+      for (int c = 0; c < MAXC; ++c) {
+        const int d = tx * 4 + 64 * c;
+        if (d < dh)
+          *reinterpret_cast<float4*>(&a.part_o[first * dh + ((d / 8) * region + r) * 8 + d % 8]) =
               make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
+      }
     }
   }
 }
 
-// The row's pieces weighted by 2^(m - max m): WPR warps of a CTA share a row, each
-// joins every WPR-th piece, the CTA's last step joins the warps. Pieces that saw
-// nothing hold no values and are not read.
-template <typename T, int WPR>
+// A row's pieces weighted by 2^(m - max m). A warp takes four neighbouring rows of an
+// entry, lane = (8 columns, row): its loads are whole lines. WPR warps of a CTA share
+// the rows, each joining every WPR-th piece; the CTA's last step joins the warps. SEGS:
+// groups of 64 columns. Pieces that saw nothing hold no values: what lies there is
+// read, and left out. Bound by the reads of the pieces.
+template <typename T, int WPR, int SEGS>
 __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
-  constexpr int RPC = 8 / WPR;  // rows per CTA
-  __shared__ float s_acc[WPR > 1 ? 8 : 1][WPR > 1 ? 256 : 1];
-  __shared__ float2 s_ml[8];
+  constexpr int BATCH = SEGS == 1 ? 4 : SEGS == 2 ? 2 : 1;  // pieces in flight per warp
+  __shared__ float s_acc[WPR > 1 ? 8 : 1][WPR > 1 ? SEGS * 8 : 1][WPR > 1 ? 33 : 1];
+  __shared__ float2 s_ml[8][4];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR, dh = a.dh;
-  const size_t N = (size_t)a.n * a.rows * a.Hq;
-  const size_t row = (size_t)blockIdx.x * RPC + warp / WPR;
-  bool on = row < N;
-  const int token = on ? (int)(row / a.Hq) : 0, head = on ? (int)(row % a.Hq) : 0, entry = token / a.rows;
-  int own;
-  const int first = attn_pieces(a, entry, own);
+  const int per = a.rows * a.Hq, fours = (per + 3) / 4;
+  const long long unit = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const int entry = (int)(unit / fours), lr = (int)(unit % fours) * 4 + (lane & 3), col = (lane >> 2) * 8;
+  bool on = entry < a.n && lr < per;
+  int own = 1, first = 0;
+  if (on) first = attn_pieces(a, entry, own);
   if (a.npre == 0 && own == 1 && (a.plan || attn_direct(a))) on = false;  // written already
   const int pieces = on && __ldcg(&a.eff[entry]) > 0 ? a.npre + own : 0;
-  // piece p's row: the prefix's pieces come first
-  auto at = [&](int p) {
-    return p < a.npre ? p * N + row
-                      : a.npre * N + ((size_t)(first + p - a.npre) * a.rows + token % a.rows) * a.Hq + head;
-  };
-  float m = -INFINITY, l = 0.f, acc[8] = {};
-  for (int p0 = sub; p0 < pieces; p0 += 32 * WPR) {
-    // this lane's piece of the next 32
-    const int p = p0 + lane * WPR;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    size_t r = 0;
-    if (p < pieces) {
-      r = at(p);
-      ml = __ldcg(&a.part_ml[r]);
+  const int g = on ? lr / (a.rows * a.G) : 0, t = on ? lr / a.G % a.rows : 0, i = on ? lr % a.G : 0;
+  const size_t all = (size_t)a.n * per;
+  const int prow = part_row(a, false, g, entry * a.rows + t, i);
+  float m = -INFINITY, l = 0.f, acc[SEGS][8] = {};
+  for (int p0 = sub; p0 < pieces; p0 += BATCH * WPR) {
+    float2 ml[BATCH];
+    float4 x[BATCH][SEGS][2];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int p = p0 + k * WPR;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (p >= pieces) continue;
+      const bool mine = p >= a.npre;
+      const size_t f = part_first(a, mine, mine ? first + p - a.npre : p), region = mine ? (size_t)per : all;
+      const size_t r = mine ? lr : prow;
+      ml[k] = __ldcg(&a.part_ml[f + r]);
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s)
+        if (col + 64 * s < dh) {
+          const float4* src =
+              reinterpret_cast<const float4*>(&a.part_o[f * dh + ((size_t)(col / 8 + 8 * s) * region + r) * 8]);
+          x[k][s][0] = __ldcg(src);
+          x[k][s][1] = __ldcg(src + 1);
+        }
     }
-    const float nm = fmaxf(m, warp_max(ml.x));
-    const float base = nm > -INFINITY ? nm : 0.f;
-    const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - base), f = exp2f(m - base);
-    const bool used = !(ml.y == 0.f);
-    l = l * f + warp_sum(used ? ml.y * w : 0.f);
-    m = nm;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= f;
-    const int count = min(32, (pieces - p0 + WPR - 1) / WPR);
-    for (int k0 = 0; k0 < count; k0 += 4) {
-      float4 x[4][2];
-      float wk[4];
+    for (int k = 0; k < BATCH; ++k) {
+      if (ml[k].y == 0.f) continue;
+      const float nm = fmaxf(m, ml[k].x), base = nm > -INFINITY ? nm : 0.f;
+      const float f = exp2f(m - base), w = exp2f(ml[k].x - base);
+      m = nm;
+      l = l * f + ml[k].y * w;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const size_t rk = __shfl_sync(0xffffffffu, r, (k0 + k) & 31);
-        wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-        const bool read = k0 + k < count && __shfl_sync(0xffffffffu, (int)used, (k0 + k) & 31);
+      for (int s = 0; s < SEGS; ++s)
+        if (col + 64 * s < dh) {
+          const float* v = reinterpret_cast<const float*>(x[k][s]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          x[k][c] = read && lane * 4 + 128 * c < dh
-                        ? __ldcg(reinterpret_cast<const float4*>(&a.part_o[rk * dh + lane * 4 + 128 * c]))
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!read) wk[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          acc[4 * c + 0] = fmaf(wk[k], x[k][c].x, acc[4 * c + 0]);
-          acc[4 * c + 1] = fmaf(wk[k], x[k][c].y, acc[4 * c + 1]);
-          acc[4 * c + 2] = fmaf(wk[k], x[k][c].z, acc[4 * c + 2]);
-          acc[4 * c + 3] = fmaf(wk[k], x[k][c].w, acc[4 * c + 3]);
+          for (int c = 0; c < 8; ++c) acc[s][c] = acc[s][c] * f + w * v[c];
         }
     }
   }
   if (WPR > 1) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (lane * 4 + 128 * c < dh)
-        *reinterpret_cast<float4*>(&s_acc[warp][lane * 4 + 128 * c]) =
-            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    for (int s = 0; s < SEGS; ++s)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s_acc[warp][s * 8 + c][lane] = acc[s][c];
+    if (col == 0) s_ml[warp][lane & 3] = make_float2(m, l);
     __syncthreads();
     if (sub) return;
-    float nm = m;
-#pragma unroll
-    for (int k = 1; k < WPR; ++k) nm = fmaxf(nm, s_ml[warp + k].x);
-    const float base = nm > -INFINITY ? nm : 0.f;
-    const float f = exp2f(m - base);
-    l *= f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= f;
 #pragma unroll
     for (int k = 1; k < WPR; ++k) {
-      const float2 ml = s_ml[warp + k];
-      const float w = exp2f(ml.x - base);
-      l += ml.y == 0.f ? 0.f : ml.y * w;
+      const float2 ml = s_ml[warp + k][lane & 3];
+      if (ml.y == 0.f) continue;
+      const float nm = fmaxf(m, ml.x), base = nm > -INFINITY ? nm : 0.f;
+      const float f = exp2f(m - base), w = exp2f(ml.x - base);
+      m = nm;
+      l = l * f + ml.y * w;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (lane * 4 + 128 * c < dh) {
-          const float4 x = *reinterpret_cast<const float4*>(&s_acc[warp + k][lane * 4 + 128 * c]);
-          acc[4 * c + 0] = fmaf(w, x.x, acc[4 * c + 0]);
-          acc[4 * c + 1] = fmaf(w, x.y, acc[4 * c + 1]);
-          acc[4 * c + 2] = fmaf(w, x.z, acc[4 * c + 2]);
-          acc[4 * c + 3] = fmaf(w, x.w, acc[4 * c + 3]);
-        }
+      for (int s = 0; s < SEGS; ++s)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[s][c] = acc[s][c] * f + w * s_acc[warp + k][s * 8 + c][lane];
     }
   }
   if (!on) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* dst = static_cast<T*>(a.out) + (size_t)token * a.out_ld + (size_t)head * dh;
+  T* dst = static_cast<T*>(a.out) + ((size_t)entry * a.rows + t) * a.out_ld + (size_t)(g * a.G + i) * dh + col;
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (lane * 4 + 128 * c < dh) {
-      const int d = lane * 4 + 128 * c;
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(&dst[d]) =
-            make_float4(acc[4 * c] * inv, acc[4 * c + 1] * inv, acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
-      } else {
-        uint2 x;
-        *reinterpret_cast<__nv_bfloat162*>(&x.x) = __floats2bfloat162_rn(acc[4 * c] * inv, acc[4 * c + 1] * inv);
-        *reinterpret_cast<__nv_bfloat162*>(&x.y) = __floats2bfloat162_rn(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
-        *reinterpret_cast<uint2*>(&dst[d]) = x;
-      }
+  for (int s = 0; s < SEGS; ++s) {
+    if (col + 64 * s >= dh) continue;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        reinterpret_cast<float4*>(dst + 64 * s)[h] = make_float4(acc[s][4 * h] * inv, acc[s][4 * h + 1] * inv,
+                                                                 acc[s][4 * h + 2] * inv, acc[s][4 * h + 3] * inv);
+    } else {
+      uint4 y;
+      __nv_bfloat162* y2 = reinterpret_cast<__nv_bfloat162*>(&y);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) y2[h] = __floats2bfloat162_rn(acc[s][2 * h] * inv, acc[s][2 * h + 1] * inv);
+      *reinterpret_cast<uint4*>(dst + 64 * s) = y;
     }
+  }
 }
 
 constexpr int kMaxDev = 64;
@@ -461,16 +448,24 @@ cudaError_t launch_attn_rows_own(int dtype, const AttnRows& a, cudaStream_t st) 
   const int blocks = (a.rows * a.G + BM - 1) / BM;
   return launch_mode<OWN>(dtype, a, dim3((unsigned)(a.n * blocks), a.Hkv, a.nown), st);
 }
+namespace {
+template <typename T, int SEGS>
+cudaError_t join(const AttnRows& a, int pieces, cudaStream_t st) {
+  const long long units = (long long)a.n * ((a.rows * a.Hq + 3) / 4);
+  // few rows: several warps per row, so that its pieces are read side by side
+  const int wpr = units * 2 >= 152 * 32 || pieces <= 2 ? 1 : units * 8 >= 152 * 32 || pieces <= 8 ? 2 : 8;
+  const dim3 grid((unsigned)((units * wpr + 7) / 8));
+  return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : wpr == 2 ? join_kernel<T, 2, SEGS> : join_kernel<T, 1, SEGS>,
+                    grid, dim3(256), 0, st, a);
+}
+}  // namespace
+
 cudaError_t launch_attn_join(int dtype, const AttnRows& a, int pieces, cudaStream_t st) {
-  const long long N = (long long)a.n * a.rows * a.Hq;
-  const int wpr = pieces > 12 ? 8 : pieces > 6 ? 2 : 1;
-  const dim3 grid((unsigned)((N * wpr + 7) / 8));
   using bf = __nv_bfloat16;
   if (dtype == HF_F32)
-    return launch_pdl(wpr == 8 ? join_kernel<float, 8> : wpr == 2 ? join_kernel<float, 2> : join_kernel<float, 1>, grid,
-                      dim3(256), 0, st, a);
-  return launch_pdl(wpr == 8 ? join_kernel<bf, 8> : wpr == 2 ? join_kernel<bf, 2> : join_kernel<bf, 1>, grid, dim3(256),
-                    0, st, a);
+    return a.dh <= 64 ? join<float, 1>(a, pieces, st) : a.dh <= 128 ? join<float, 2>(a, pieces, st)
+                                                                    : join<float, 4>(a, pieces, st);
+  return a.dh <= 64 ? join<bf, 1>(a, pieces, st) : a.dh <= 128 ? join<bf, 2>(a, pieces, st) : join<bf, 4>(a, pieces, st);
 }
 
 namespace {
@@ -546,8 +541,8 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   w.base = w.eff + (size_t)a.n * sizeof(int);
   w.piece_of = w.base + (w.tc ? ((size_t)a.n + 1) * sizeof(int) : 0);
   w.ml = (w.piece_of + (w.tc ? pieces * sizeof(int) : 0) + 15) / 16 * 16;
-  w.o = (w.ml + rows * sizeof(float2) + 15) / 16 * 16;
-  w.total = w.o + rows * a.dh * sizeof(float);
+  w.o = (w.ml + rows * sizeof(float2) + 31) / 32 * 32;
+  w.total = w.o + rows * a.dh * sizeof(float) + 16;  // (the rows start on 32 bytes)
   return w;
 }
 
@@ -663,7 +658,7 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.eff = reinterpret_cast<int*>(ws + w.eff);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws + w.o) + 31) / 32 * 32);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
   if (w.tc) {
@@ -672,7 +667,7 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
     a.piece_of = reinterpret_cast<int*>(ws + w.piece_of);
     e = launch_attn_tc_pages(a, w.pre_items, w.units, w.budget, st);
   } else {
-    e = launch_attn_plan(a, 0, 0, 0, st);
+    e = launch_attn_plan(a, 0, 0, 0, 0, st);
     if (e == cudaSuccess && a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
     if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
   }

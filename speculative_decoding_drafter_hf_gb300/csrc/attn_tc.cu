@@ -136,6 +136,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
       : "memory");
 }
 
+// 32 bytes at once: whole sectors of the L2.
+__device__ __forceinline__ void store8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -172,7 +179,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ bool odd_half(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
 
 // Bounded wait of a whole warp; the answer is the same in every lane.
 __device__ __forceinline__ bool try_wait_addr(uint32_t bar, uint32_t parity) {
@@ -204,6 +210,7 @@ struct TcArgs {
   int box_rows;    // rows of a K / V box (prompt: 128, paged: the page)
   int pre_items;   // paged: items of the prefix
   int units;       // paged: items per piece of a request's own keys
+  int wide;        // rows of out start on 32 bytes
 };
 
 // What a CTA works on at a time, written by warp 2. Tile r's rows are tokens
@@ -721,25 +728,23 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           ok = wait_uniform(smem_u32(&full[vs]), (uint32_t)(vi / NS) & 1u);
           if (!ok) break;
           uint4* v = reinterpret_cast<uint4*>(sKV + (size_t)vs * L::TILE);
-          for (int q = row; q < L::TILE / 16; q += 128) {
-            uint4 x = v[q];
+          // rows (keys) k0 .. k1 - 1 of the tile, a half of 64 columns after the other
+          const int k0 = max(0, min(glow, j1) - jt), k1 = min(BN, hold - jt), per = (k1 - k0) * 8;
+          for (int q = row; q < per * HALVES; q += 128) {
+            const int h = q >= per;
+            uint4* at = v + h * (HALF / 16) + k0 * 8 + (q - h * per);
+            uint4 x = *at;
             uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            bool odd = false;
+            // an exponent of all ones carries into its half's top bit
+            uint32_t hit[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (odd_half(w[k])) {
-                w[k] &= 0xffff0000u;
-                odd = true;
-              }
-              if (odd_half(w[k] >> 16)) {
-                w[k] &= 0x0000ffffu;
-                odd = true;
-              }
-            }
-            if (odd) {
+            for (int k = 0; k < 4; ++k) hit[k] = ((w[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+            if (hit[0] | hit[1] | hit[2] | hit[3]) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] &= ~((hit[k] >> 15) * 0xffffu);
               atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
               __threadfence_block();
-              v[q] = x;
+              *at = x;
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -761,9 +766,9 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         const bool direct = it.direct;
         const float inv = l == 0.f || dead ? 0.f : 1.f / l;
         const int from = *(volatile int*)&it.odd[streams == 1 ? 0 : r];
-        const size_t N = (size_t)a.n * a.rows * a.Hq;
-        const size_t pr = it.kind == 1 ? it.part * N + orow * a.Hq + head
-                                       : a.npre * N + ((size_t)it.part * a.rows + it.t0 + tl) * a.Hq + head;
+        const bool own = it.kind == 2;
+        const size_t first = part_first(a, own, it.part), region = (size_t)(own ? a.rows : a.n * a.rows) * a.Hq;
+        const size_t pr = part_row(a, own, g, it.t0 + tl, row_head);
 #pragma unroll 1
         for (int q = 0; q < DH; q += 32) {
           float o[32];
@@ -784,24 +789,26 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             }
           if (!valid) continue;
           if (direct) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.out_ld +
-                                                  (size_t)head * DH + q);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + orow * a.out_ld + (size_t)head * DH + q;
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+            for (int x = 0; x < 16; ++x) w[x] = dead ? 0u : pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+            if (c.wide) {
+              store8(dst, w);
+              store8(dst + 16, w + 8);
+            } else {
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = dead ? 0u : pack_bf16(o[8 * k + 2 * x] * inv, o[8 * k + 2 * x + 1] * inv);
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k)
+                reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
           } else if (mine > 0) {
-            float4* dst = reinterpret_cast<float4*>(&a.part_o[pr * DH + q]);
+            float* dst = a.part_o + first * DH + ((q / 8) * region + pr) * 8;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) store8(dst + k * region * 8, reinterpret_cast<uint32_t*>(o) + 8 * k);
           }
         }
         if (!direct && valid)
-          a.part_ml[pr] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(mb, l);
+          a.part_ml[first + pr] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(mb, l);
         tc_fence_before();
       }
       __syncwarp();
@@ -827,7 +834,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 // Which entries the call sees, and how the requests' own keys are cut: one CTA for
 // the lengths and the list of pieces, the others compare the entries' prefixes.
 //   plan: [0] counter of items, [1] keys per piece, [2] pieces
-__global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int units, int first) {
+__global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int units, int first, int pre_items) {
   __shared__ int s_scan[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -850,39 +857,52 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
   for (int i = tid; i < a.n; i += 1024) a.eff[i] = attn_len(a, i, bad);
   if (bad && a.status) atomicOr(a.status, HF_S_BAD);
   if (budget <= 0) return;  // pieces of a fixed number of keys
-  // Keys per piece: of some sizes the one with the least (rounds of items over the SMs) *
-  // (tiles of an item + about one for its start and end), the pieces fitting the workspace
-  constexpr int NC = 8;
+  // Keys per piece: of some sizes the one whose items take the SMs the least time (a few
+  // rounds: whole ones; more, or beside the prefix's items: their sum and half a last
+  // one), the pieces fitting the workspace
+  constexpr int NC = 16;
   __shared__ int s_count[NC + 1];
-  auto size_of = [](int k) { return 1 << k; };
   if (tid <= NC) s_count[tid] = 0;
   __syncthreads();
-  int mine[NC + 1] = {};
-  for (int i = tid; i < a.n; i += 1024) {
-    const int t = (max(0, a.eff[i] - a.shared) + BN - 1) / BN;
-    mine[NC] += t;
+  int tiles = 0;
+  for (int i = tid; i < a.n; i += 1024) tiles += (max(0, a.eff[i] - a.shared) + BN - 1) / BN;
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  if (lane == 0 && tiles) atomicAdd(&s_count[NC], tiles);
+  __syncthreads();
+  // candidates: what k + 1 rounds over 152 SMs would take, and a quarter more
+  const int all = s_count[NC];
+  const int cand = max(1, (int)(((float)all * units / (152.f * (lane / 2 + 1))) * (lane & 1 ? 1.25f : 1.f) + 0.999f));
+  int mine[NC] = {};
+  for (int i = tid; i < (a.n + 31) / 32 * 32; i += 1024) {
+    const int t = i < a.n ? (max(0, a.eff[i] - a.shared) + BN - 1) / BN : -1;
 #pragma unroll
-    for (int k = 0; k < NC; ++k) mine[k] += max(1, (t + size_of(k) - 1) / size_of(k));
+    for (int k = 0; k < NC; ++k) {
+      const int c = __shfl_sync(0xffffffffu, cand, k);
+      if (t >= 0) mine[k] += max(1, (int)((unsigned)(t + c - 1) / (unsigned)c));
+    }
   }
 #pragma unroll
-  for (int k = 0; k <= NC; ++k) {
+  for (int k = 0; k < NC; ++k) {
     const int s = __reduce_add_sync(0xffffffffu, mine[k]);
     if (lane == 0 && s) atomicAdd(&s_count[k], s);
   }
   __syncthreads();
-  const int all = s_count[NC];
-  int chunk = max(1, all / budget + 1);  // always fits
+  int chunk;
   {
-    float best = 3e38f;
-    for (int k = 0; k < NC; ++k) {
-      if (s_count[k] > a.n + budget) continue;
-      const float rounds = (float)s_count[k] * units * (1.f / 152.f);
-      const float cost = (rounds < 6.f ? ceilf(rounds) : rounds + 0.5f) * ((float)min(size_of(k), all) + 1.5f);
-      if (cost < best) {
-        best = cost;
-        chunk = size_of(k);
-      }
-    }
+    // one lane per candidate; the last one always fits the workspace
+    const int c = lane < NC ? cand : all / budget + 1;
+    const int pieces = lane < NC ? s_count[lane] : a.n + budget;
+    const float rounds = (float)pieces * units * (1.f / 152.f);
+    // an item's start and end, and its rows' way to the join and back, in tiles
+    const float extra = 1.5f + 0.5f * (float)(a.rows * a.G) * (1.f / 32.f);
+    float cost = rounds < 6.f && pre_items == 0 ? ceilf(rounds) * ((float)min(c, all) + extra)
+                                                : (float)all * units * (1.f / 152.f) + rounds * extra + 0.5f * c;
+    if (pieces > a.n + budget || lane > NC) cost = 3e38f;
+    float least = cost;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    const uint32_t who = __ballot_sync(0xffffffffu, cost == least && lane <= NC);
+    chunk = __shfl_sync(0xffffffffu, c, __ffs(who) - 1);
   }
   int carry = 0;
   for (int i0 = 0; i0 < a.n; i0 += 1024) {
@@ -945,9 +965,14 @@ cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mq, const CUtensorMap
 
 bool attn_tc_ok(int dtype, int dh) { return dtype == HF_BF16 && (dh == 64 || dh == 128); }
 
+namespace {
+int wide_rows(const AttnRows& a) { return reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_ld % 16 == 0; }
+}  // namespace
+
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) {
   TcArgs c{};
   c.a = a;
+  c.wide = wide_rows(a);
   c.tb = 128 / a.G;
   c.blocks = (int)prompt_slots(a.total, a.n_seq, 1, 2 * c.tb);
   c.box_rows = BN;
@@ -961,9 +986,9 @@ cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) {
                      : launch_one<64, PROMPT>(c, mq, mk, mv, grid, st);
 }
 
-cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, cudaStream_t st) {
+cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, int pre_items, cudaStream_t st) {
   const int checks = a.shared > 0 && a.status ? std::min(a.n, 151) : 0;
-  return launch_pdl(plan_kernel, dim3(1 + checks), dim3(1024), 0, st, a, budget, units, first);
+  return launch_pdl(plan_kernel, dim3(1 + checks), dim3(1024), 0, st, a, budget, units, first, pre_items);
 }
 
 // Rows of a tile, blocks and items of a call over a paged cache.
@@ -1002,6 +1027,7 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, in
   const long long tokens = (long long)a.n * a.rows, block = (long long)a.page * a.dh;
   c.blocks = (int)((tokens + 2 * c.tb - 1) / (2 * c.tb));
   c.box_rows = a.page;
+  c.wide = wide_rows(a);
   c.pre_items = pre_items;
   c.units = units;
   CUtensorMap mq, mk, mv;
@@ -1011,7 +1037,7 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, in
   if (e != cudaSuccess) return e;
   const long long most = pre_items + ((long long)a.n + budget) * units;
   const int grid = (int)std::min<long long>(most, 152);
-  e = launch_attn_plan(a, budget, units, grid, st);
+  e = launch_attn_plan(a, budget, units, grid, pre_items, st);
   if (e != cudaSuccess) return e;
   return a.dh == 128 ? launch_one<128, PAGED>(c, mq, mk, mv, dim3(grid), st)
                      : launch_one<64, PAGED>(c, mq, mk, mv, dim3(grid), st);
