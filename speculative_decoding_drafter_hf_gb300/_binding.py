@@ -516,6 +516,7 @@ class _On:
     """The device and stream of one call: every tensor lies on the first one's
     device; the call is made with that device current, on `stream` or the
     device's current stream. New outputs belong to the call's stream."""
+    __slots__ = ("device", "given", "ptr")
 
     def __init__(self, first, stream):
         import torch
@@ -524,17 +525,17 @@ class _On:
         self.device = first.device
         self.given = stream
         if stream is None:
-            self.ptr = torch.cuda.current_stream(self.device).cuda_stream
+            self.ptr = torch._C._cuda_getCurrentRawStream(self.device.index)
         else:
             self.ptr = stream if isinstance(stream, int) else stream.cuda_stream
 
     def arg(self, t, name, dtype=None, shape=None, contiguous=True):
-        if not t.is_cuda or t.device != self.device:
+        if t.device != self.device:
             raise TypeError(f"{name} must be a CUDA tensor on {self.device}")
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-        if shape is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if contiguous and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
@@ -551,7 +552,7 @@ class _On:
 
     def call(self, f, *args):
         import torch
-        if torch.cuda.current_device() == self.device.index:
+        if torch._C._cuda_getDevice() == self.device.index:
             s = f(*args, self.ptr)
         else:
             with torch.cuda.device(self.device):
@@ -748,7 +749,7 @@ class Pages:
             raise ValueError("k must be [layers, tokens, kv heads, head_dim], or [tokens, kv heads, head_dim] with layer")
         T = k.shape[-3]
         kp = on.arg(k, "k", self.k.dtype, None, False)
-        vp = on.arg(v, "v", self.k.dtype, tuple(k.shape), False)
+        vp = on.arg(v, "v", self.k.dtype, k.shape, False)
         ld = _heads_ld(k, "k")
         step = k.stride(0) if layer is None and k.shape[0] > 1 else 0
         if T and (_heads_ld(v, "v") != ld or (step and v.stride(0) != step)):
@@ -787,7 +788,7 @@ class Pages:
         qp = on.arg(q, "q", self.k.dtype, None, False)
         if out is None:
             out = on.empty(tuple(q.shape), q.dtype)
-        op = on.arg(out, "out", q.dtype, tuple(q.shape), False)
+        op = on.arg(out, "out", q.dtype, q.shape, False)
         if workspace is None:
             b = hf_attention_pages_workspace(self._ref, n, rows, hq, shared)
             workspace = on.empty((max(b, 16),), torch.uint8)

@@ -5,16 +5,21 @@
 // over the keys j < limit_i, in one pass over the keys: a tile's scores raise the
 // running maximum m_i, and what was summed so far is scaled by 2^(old m - new m).
 //
-// A CTA takes 64 rows of one KV head and walks its keys in tiles of 64: 16 x 16
+// A CTA takes 32 rows of one KV head and walks its keys in tiles of 64: 8 x 16
 // threads, 4 x 4 scores each, then the same 4 rows times the value columns 4 tx +
-// 64 c. Everything is fp32 in shared memory and registers: this is the variant for
-// fp32 inputs and for head dims that the tensor-core kernels do not take; bound by
-// the fp32 multiply-adds.
+// 64 c. Everything is fp32 in shared memory and registers (fp32 inputs: the next tile
+// comes in by asynchronous copies meanwhile): this is the variant for fp32 inputs and
+// for head dims that the tensor-core kernels do not take; bound by the fp32
+// multiply-adds. A prompt's rows are few for the GPU and their keys many: a cluster of
+// four CTAs shares a tile of rows, each walking every fourth tile of keys, and joins
+// the parts through distributed shared memory.
 //
 // Masked keys: scores are selected, never added to a mask value, so whatever K
 // holds there cannot matter; V's non-finite values in a tile that any row masks
 // are taken as zero (0 * NaN would reach every row) and added back at the end to
 // the rows that do see them.
+#include <cooperative_groups.h>
+
 #include <cmath>
 #include <cstdio>
 #include <mutex>
@@ -25,12 +30,23 @@
 namespace hf {
 namespace {
 
-constexpr int BM = 64, BN = 64, RT = 256;
+namespace cg = cooperative_groups;
+
+constexpr int BM = 32, BN = 64, RT = 128;
 constexpr int PLD = BN + 4;
+constexpr int CLUSTER = 4;  // CTAs that share a prompt's tile of rows
 enum { PROMPT = 0, PREFIX = 1, OWN = 2 };
 
-__host__ __device__ inline size_t rows_smem(int dh) {
-  return ((size_t)(BM + 2 * BN) * (dh + 4) + (size_t)BM * PLD) * sizeof(float);
+// K and V tiles in flight: two where they fit
+__host__ __device__ inline int rows_stages(int dh, int esize) { return esize == 4 && dh <= 128 ? 2 : 1; }
+__host__ __device__ inline size_t rows_smem(int dh, int esize) {
+  return ((size_t)(BM + 2 * BN * rows_stages(dh, esize)) * (dh + 4) + (size_t)BM * PLD) * sizeof(float);
+}
+
+// 16 bytes to shared memory, zeros where there is nothing to read.
+__device__ __forceinline__ void copy16(float* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
 }
 
 template <typename T>
@@ -58,16 +74,21 @@ __device__ __forceinline__ long long key_at(const AttnRows& a, int start, const 
   return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
 }
 
-template <typename T, int MODE, int MAXC>
+// DHT: the head dim, or 0 for any up to 64 * MAXC.
+template <typename T, int MODE, int MAXC, int DHT>
 __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
   extern __shared__ __align__(16) float smf[];
-  const int dh = a.dh, ldq = dh + 4;
+  constexpr bool F32 = sizeof(T) == 4;
+  const int dh = DHT ? DHT : a.dh, ldq = dh + 4, c4 = dh / 4;
+  const int stages = rows_stages(dh, (int)sizeof(T));
   float* sq = smf;
-  float* sk = sq + BM * ldq;
-  float* sv = sk + BN * ldq;
-  float* sp = sv + BN * ldq;
-  __shared__ int s_odd;
+  float* skv = sq + BM * ldq;  // K, V of one stage, then of the next
+  float* sp = skv + 2 * BN * ldq * stages;
+  __shared__ int s_odd, s_low;
+  __shared__ float2 s_ml[BM];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  constexpr int CL = MODE == PROMPT ? CLUSTER : 1;
+  const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
   pdl_trigger();
   pdl_wait();
 
@@ -77,8 +98,8 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
   const int32_t* tab = nullptr;
   if (MODE == PROMPT) {
     if (blockIdx.x == 0 && g == 0) check_offsets(a);
-    const PromptTile t = prompt_tile(a, (int)(gridDim.x - 1 - blockIdx.x), BM, a.G);
-    if (!t.ok) return;
+    const PromptTile t = prompt_tile(a, (int)((gridDim.x - 1 - blockIdx.x) / CL), BM, a.G);
+    if (!t.ok) return;  // (all CTAs of the cluster)
     start = t.start;
     row0 = t.tile * BM;
     nrows = (int)min((long long)BM, (long long)t.len * a.G - row0);
@@ -106,10 +127,48 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     if (len > 0) tab = attn_table(a, entry);
   }
 
+  // K and V of the keys from jt on into a stage
+  auto load = [&](int stage, int jt) {
+    float* dst = skv + stage * 2 * BN * ldq;
+    constexpr int U = 8;
+    for (int e0 = tid; e0 < 2 * BN * c4; e0 += RT * U) {
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * RT;
+        if (e >= 2 * BN * c4) continue;
+        const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
+        const long long at = jt + j < j1 ? key_at<MODE>(a, start, tab, g, jt + j, kv) : -2;
+        if (at == -1 && a.status) atomicOr(a.status, HF_S_BAD);
+        const T* src = static_cast<const T*>(kv ? a.v : a.k) + (at < 0 ? 0 : at + c);
+        if constexpr (F32)
+          copy16(&dst[(kv * BN + j) * ldq + c], src, at >= 0);
+        else
+          x[u] = at >= 0 ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if constexpr (!F32) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int e = e0 + u * RT;
+          if (e >= 2 * BN * c4) continue;
+          const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
+          *reinterpret_cast<float4*>(&dst[(kv * BN + j) * ldq + c]) = x[u];
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int first = j0 + rank * BN;
+  if (stages == 2 && first < j1) load(0, first);
+
   // this thread's rows: keys they see, and where they come from and go to
-  int limit[4];
+  int limit[4], head[4];
   size_t orow[4];  // token row of q and out
-  int head[4];
+  if (tid == 0) {
+    s_odd = j1;
+    s_low = 0x7fffffff;
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int rr = row0 + ty * 4 + i;
@@ -119,20 +178,21 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     if (ty * 4 + i >= nrows) continue;
     const int t = rr / a.G;
     head[i] = g * a.G + rr % a.G;
+    bool dead = false;
     if (MODE == PROMPT) {
       limit[i] = t + 1;
       orow[i] = (size_t)start + t;
     } else if (MODE == PREFIX) {
       const int l = __ldcg(&a.eff[t / a.rows]);
+      dead = l == 0;
       limit[i] = max(0, min(a.shared, l - a.rows + t % a.rows + 1));
       orow[i] = t;
     } else {
       limit[i] = max(0, len - a.rows + t + 1);
       orow[i] = (size_t)entry * a.rows + t;
     }
+    if (tx == 0 && !dead) atomicMin(&s_low, limit[i]);
   }
-  if (tid == 0) s_odd = 0;
-  const int c4 = dh / 4;
   for (int e = tid; e < BM * c4; e += RT) {
     const int r = e / c4, c = (e % c4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -144,6 +204,8 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     *reinterpret_cast<float4*>(&sq[r * ldq + c]) =
         make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
   }
+  __syncthreads();
+  const int low = s_low;
 
   float m[4], l[4], o[4][MAXC * 4];
 #pragma unroll
@@ -153,35 +215,35 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
 #pragma unroll
     for (int c = 0; c < MAXC * 4; ++c) o[i][c] = 0.f;
   }
-  const int low = min(min(limit[0], limit[1]), min(limit[2], limit[3]));
-  int odd_from = j1;  // first key of a tile whose odd values were taken as zero
 
-  for (int jt = j0; jt < j1; jt += BN) {
-    __syncthreads();
-    for (int e = tid; e < 2 * BN * c4; e += RT) {
-      const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (jt + j < j1) {
-        const long long at = key_at<MODE>(a, start, tab, g, jt + j, kv);
-        if (at >= 0)
-          x = load4(static_cast<const T*>(kv ? a.v : a.k) + at + c);
-        else if (a.status)
-          atomicOr(a.status, HF_S_BAD);
+  int stage = 0;
+  for (int jt = first; jt < j1; jt += CL * BN) {
+    const int next = jt + CL * BN;
+    if (stages == 2) {
+      if (next < j1) {
+        load(stage ^ 1, next);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      *reinterpret_cast<float4*>(&(kv ? sv : sk)[j * ldq + c]) = x;
+    } else {
+      load(0, jt);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
+    __syncthreads();
+    float* sk = skv + stage * 2 * BN * ldq;
+    float* sv = sk + BN * ldq;
+    if (stages == 2) stage ^= 1;
     // some row masks keys of this tile: its odd values of V are set aside
-    const bool cut = __syncthreads_or(low < jt + BN && low < j1);
-    if (cut) {
-      bool odd = false;
+    if (low < min(jt + BN, j1)) {
       for (int e = tid; e < BN * dh; e += RT) {
         float* x = &sv[(e / dh) * ldq + e % dh];
         if (odd_value(*x)) {
           *x = 0.f;
-          odd = true;
+          atomicMin(&s_odd, jt);
         }
       }
-      if (__syncthreads_or(odd)) odd_from = min(odd_from, jt);
+      __syncthreads();
     }
 
     float s[4][4];
@@ -189,6 +251,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
     for (int d = 0; d < dh; d += 4) {
       float4 qv[4], kv[4];
 #pragma unroll
@@ -222,14 +285,13 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
         sum += e;
         sp[(ty * 4 + i) * PLD + tx + 16 * j] = e;
       }
-#pragma unroll
-      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      l[i] = l[i] * f + sum;
+      l[i] = l[i] * f + sum;  // this thread's columns; joined at the end
       m[i] = nm;
 #pragma unroll
       for (int c = 0; c < MAXC * 4; ++c) o[i][c] *= f;
     }
     __syncwarp();  // a row's 16 threads are in one warp
+#pragma unroll 4
     for (int j = 0; j < BN; j += 4) {
       float4 p[4];
 #pragma unroll
@@ -250,11 +312,74 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
           }
         }
     }
+    __syncthreads();  // the tile has been read
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
 
-  if (odd_from < j1) {  // rows that see an odd value of V get it after all
+  int odd_from = s_odd;
+  if constexpr (CL > 1) {
+    // the cluster's parts meet in the first CTA's place: each CTA shows its sums where its
+    // tiles were, and joins a quarter of the rows (thread rows i = rank)
+    cg::cluster_group cluster = cg::this_cluster();
+    float* so = skv;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (tx == 0) s_ml[ty * 4 + i] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c)
+        if (tx * 4 + 64 * c < dh)
+          *reinterpret_cast<float4*>(&so[(ty * 4 + i) * ldq + tx * 4 + 64 * c]) =
+              make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
+    }
+    cluster.sync();
+    const int r = ty * 4 + rank;
+    float2 ml[CL];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < CL; ++k) {
+      ml[k] = *cluster.map_shared_rank(&s_ml[r], k);
+      odd_from = min(odd_from, *cluster.map_shared_rank(&s_odd, k));
+      top = fmaxf(top, ml[k].x);
+    }
+    const float base = top > -INFINITY ? top : 0.f;
+    float sum = 0.f, v[MAXC * 4];
+#pragma unroll
+    for (int c = 0; c < MAXC * 4; ++c) v[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < CL; ++k) {
+      if (ml[k].y == 0.f) continue;
+      const float w = exp2f(ml[k].x - base);
+      sum += ml[k].y * w;
+      const float* src = cluster.map_shared_rank(so, k);
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c)
+        if (tx * 4 + 64 * c < dh) {
+          const float4 x = *reinterpret_cast<const float4*>(&src[r * ldq + tx * 4 + 64 * c]);
+          v[4 * c] += w * x.x;
+          v[4 * c + 1] += w * x.y;
+          v[4 * c + 2] += w * x.z;
+          v[4 * c + 3] += w * x.w;
+        }
+    }
+    cluster.sync();  // read by all before a CTA of the cluster ends
+    // only thread row `rank` goes on
 #pragma unroll
     for (int i = 0; i < 4; ++i)
+      if (i == rank) {
+        m[i] = top;
+        l[i] = sum;
+#pragma unroll
+        for (int c = 0; c < MAXC * 4; ++c) o[i][c] = v[c];
+      }
+  }
+  const bool direct = MODE == PROMPT || attn_direct(a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (ty * 4 + i >= nrows || (CL > 1 && i != rank)) continue;
+    if (odd_from < j1)  // rows that see an odd value of V get it after all
       for (int j = odd_from; j < min(limit[i], j1); ++j) {
         const long long at = key_at<MODE>(a, start, tab, g, j, 1);
         if (at < 0) continue;
@@ -266,31 +391,32 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
           if (odd_value(x)) o[i][c] += x;
         }
       }
-  }
-  const bool direct = MODE == PROMPT || attn_direct(a);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (ty * 4 + i >= nrows) continue;
     if (direct) {
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
       T* dst = static_cast<T*>(a.out) + orow[i] * a.out_ld + (size_t)head[i] * dh;
 #pragma unroll
-      for (int c = 0; c < MAXC * 4; ++c) {
-        const int d = tx * 4 + 64 * (c / 4) + c % 4;
-        if (d < dh) dst[d] = from_f<T>(o[i][c] * inv);
+      for (int c = 0; c < MAXC; ++c) {
+        const int d = tx * 4 + 64 * c;
+        if (d >= dh) continue;
+        if constexpr (F32)
+          *reinterpret_cast<float4*>(dst + d) =
+              make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
+        else
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[d + k] = from_f<T>(o[i][4 * c + k] * inv);
       }
     } else {
       const bool own = MODE == OWN;
-      const size_t first = part_first(a, own, own ? entry * a.nown + piece : piece);
+      const size_t first_row = part_first(a, own, own ? entry * a.nown + piece : piece);
       const size_t region = (size_t)(own ? a.rows : a.n * a.rows) * a.Hq;
       const int rr = row0 + ty * 4 + i;
       const size_t r = part_row(a, own, g, rr / a.G, rr % a.G);
-      if (tx == 0) a.part_ml[first + r] = make_float2(m[i], l[i]);
+      if (tx == 0) a.part_ml[first_row + r] = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < MAXC; ++c) {
         const int d = tx * 4 + 64 * c;
         if (d < dh)
-          *reinterpret_cast<float4*>(&a.part_o[first * dh + ((d / 8) * region + r) * 8 + d % 8]) =
+          *reinterpret_cast<float4*>(&a.part_o[first_row * dh + ((d / 8) * region + r) * 8 + d % 8]) =
               make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
       }
     }
@@ -404,41 +530,61 @@ __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-bool g_set[kMaxDev][2][3][3] = {};
+bool g_set[kMaxDev][2][3][5] = {};
 
-template <typename T, int MODE, int MAXC>
+template <typename T, int MODE, int MAXC, int DHT>
 cudaError_t launch_one(const AttnRows& a, dim3 grid, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  auto* kern = rows_kernel<T, MODE, MAXC, DHT>;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][MAXC / 2];
+    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][DHT ? 3 + (DHT == 128) : MAXC / 2];
     if (!set || dev >= kMaxDev) {
-      e = cudaFuncSetAttribute(rows_kernel<T, MODE, MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)rows_smem(64 * MAXC));
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)rows_smem(DHT ? DHT : 64 * MAXC, (int)sizeof(T)));
       if (e != cudaSuccess) return e;
       set = true;
     }
   }
-  return launch_pdl(rows_kernel<T, MODE, MAXC>, grid, dim3(RT), rows_smem(a.dh), st, a);
+  if (MODE != PROMPT) return launch_pdl(kern, grid, dim3(RT), rows_smem(a.dh, (int)sizeof(T)), st, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(RT);
+  cfg.dynamicSmemBytes = rows_smem(a.dh, (int)sizeof(T));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CLUSTER;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <typename T, int MODE>
+cudaError_t launch_dh(const AttnRows& a, dim3 grid, cudaStream_t st) {
+  if (sizeof(T) == 4 && a.dh == 64) return launch_one<T, MODE, 1, sizeof(T) == 4 ? 64 : 0>(a, grid, st);
+  if (sizeof(T) == 4 && a.dh == 128) return launch_one<T, MODE, 2, sizeof(T) == 4 ? 128 : 0>(a, grid, st);
+  if (a.dh <= 64) return launch_one<T, MODE, 1, 0>(a, grid, st);
+  if (a.dh <= 128) return launch_one<T, MODE, 2, 0>(a, grid, st);
+  return launch_one<T, MODE, 4, 0>(a, grid, st);
 }
 
 template <int MODE>
 cudaError_t launch_mode(int dtype, const AttnRows& a, dim3 grid, cudaStream_t st) {
-  const int c = a.dh <= 64 ? 1 : a.dh <= 128 ? 2 : 4;
-  using bf = __nv_bfloat16;
-  if (dtype == HF_F32)
-    return c == 1 ? launch_one<float, MODE, 1>(a, grid, st)
-                  : c == 2 ? launch_one<float, MODE, 2>(a, grid, st) : launch_one<float, MODE, 4>(a, grid, st);
-  return c == 1 ? launch_one<bf, MODE, 1>(a, grid, st)
-                : c == 2 ? launch_one<bf, MODE, 2>(a, grid, st) : launch_one<bf, MODE, 4>(a, grid, st);
+  return dtype == HF_F32 ? launch_dh<float, MODE>(a, grid, st) : launch_dh<__nv_bfloat16, MODE>(a, grid, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st) {
-  return launch_mode<PROMPT>(dtype, a, dim3((unsigned)prompt_slots(a.total, a.n_seq, a.G, BM), a.Hkv), st);
+  const long long slots = prompt_slots(a.total, a.n_seq, a.G, BM) * CLUSTER;
+  if (slots > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_mode<PROMPT>(dtype, a, dim3((unsigned)slots, a.Hkv), st);
 }
 cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st) {
   const long long rows = (long long)a.n * a.rows * a.G;
@@ -497,25 +643,19 @@ float base2_scale(float scale, int dh) {
   return (float)(1.4426950408889634 * (scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)dh)));
 }
 
-// Pieces of the key axis on CUDA cores: as many as give every SM two CTAs, of at
-// least 256 keys. A request's own pieces go by its table's reach, not by its length,
-// which only the device knows.
+// Pieces of the key axis on CUDA cores: as many as give every SM eight CTAs of four warps,
+// of at least two tiles of keys. A request's own pieces go by its table's reach, not by
+// its length, which only the device knows.
 void plan_pieces(AttnRows& a) {
-  const long long pre_tiles = ((long long)a.n * a.rows * a.G + BM - 1) / BM * a.Hkv;
-  auto split = [](long long keys, long long tiles, int most, int& count, int& each) {
-    if (keys <= 0) {
-      count = 0;
-      each = 256;
-      return;
-    }
-    long long c = std::max<long long>(1, std::min<long long>({(304 + tiles - 1) / std::max<long long>(tiles, 1), (keys + 255) / 256, (long long)most}));
-    each = (int)(((keys + c - 1) / c + 127) / 128 * 128);
+  auto split = [](long long keys, long long tiles, int& count, int& each) {
+    const long long want = (152 * 8 + tiles - 1) / std::max<long long>(tiles, 1);
+    const long long c = std::max<long long>(1, std::min<long long>({want, (keys + 2 * BN - 1) / (2 * BN), 64}));
+    each = (int)std::max<long long>(2 * BN, ((keys + c - 1) / c + BN - 1) / BN * BN);
     count = (int)((keys + each - 1) / each);
   };
-  split(a.shared, pre_tiles, 32, a.npre, a.pre_keys);
-  const long long own = (long long)a.table_ld * a.page - a.shared;
-  const long long own_tiles = (long long)a.n * a.Hkv * ((a.rows * a.G + BM - 1) / BM);
-  split(own, own_tiles, 32, a.nown, a.own_keys);
+  split(a.shared, ((long long)a.n * a.rows * a.G + BM - 1) / BM * a.Hkv, a.npre, a.pre_keys);
+  split((long long)a.table_ld * a.page - a.shared, (long long)a.n * a.Hkv * ((a.rows * a.G + BM - 1) / BM), a.nown,
+        a.own_keys);
   a.nown = std::max(a.nown, 1);  // it also writes the empty rows of a direct call
 }
 

@@ -44,34 +44,43 @@ struct VArgs {
   int32_t* status;
 };
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ bool temp_ok(float t) { return t >= 0.f && t < INFINITY; }
 
-// Calls f(index, value) for the entries [i0, i1) of a row: single loads up to a
-// 16-byte boundary, 16-byte loads (UN of them in flight) from there.
-template <typename T, int UN, typename F>
-__device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& f) {
+// The entries [i0, i1) of a row: single ones up to a 16-byte boundary and behind the
+// last whole 16 bytes go to one(index, value); of the rest, each thread gets UN 16-byte
+// loads at a time, as some(index, values, how many): load k's values are at index +
+// k * VT * VE.
+template <typename T, int UN, typename F, typename G>
+__device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& one, G&& some) {
   constexpr int VE = 16 / (int)sizeof(T);
   const int tid = threadIdx.x;
   const int off = (int)((reinterpret_cast<uintptr_t>(row + i0) & 15) / sizeof(T));
   const int head = min(i1 - i0, off ? VE - off : 0);
-  if (tid < head) f(i0 + tid, to_f(row[i0 + tid]));
+  if (tid < head) one(i0 + tid, to_f(row[i0 + tid]));
   const int b0 = i0 + head, nv = (i1 - b0) / VE;
   const uint4* p = reinterpret_cast<const uint4*>(row + b0);
   for (int v0 = tid; v0 < nv; v0 += VT * UN) {
     uint4 r[UN];
+    float x[UN * VE];
 #pragma unroll
     for (int k = 0; k < UN; ++k)
       if (v0 + k * VT < nv) r[k] = __ldcs(p + v0 + k * VT);
+    const int n = min(UN, (nv - v0 + VT - 1) / VT);
 #pragma unroll
     for (int k = 0; k < UN; ++k)
-      if (v0 + k * VT < nv) {
-        const T* t = reinterpret_cast<const T*>(&r[k]);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) f(b0 + (v0 + k * VT) * VE + j, to_f(t[j]));
-      }
+      for (int j = 0; j < VE; ++j)
+        x[k * VE + j] = k < n ? to_f(reinterpret_cast<const T*>(&r[k])[j]) : kNegInf;
+    some(b0 + v0 * VE, x, n);
   }
   const int t0 = b0 + nv * VE;
-  if (t0 + tid < i1) f(t0 + tid, to_f(row[t0 + tid]));
+  if (t0 + tid < i1) one(t0 + tid, to_f(row[t0 + tid]));
 }
 
 // (m, l) of two parts: maximum and sum of 2^((x - m) c). A part without
@@ -79,7 +88,7 @@ __device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& f) {
 __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, float c) {
   const float mm = fmaxf(m, m2);
   if (mm > kNegInf) {
-    l = (m > kNegInf ? l * exp2f((m - mm) * c) : l) + (m2 > kNegInf ? l2 * exp2f((m2 - mm) * c) : l2);
+    l = (m > kNegInf ? l * ex2((m - mm) * c) : l) + (m2 > kNegInf ? l2 * ex2((m2 - mm) * c) : l2);
   } else {
     l += l2;
   }
@@ -100,14 +109,23 @@ __device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t,
   __shared__ int si[VT / 32];
   const int i0 = chunk * a.chunk, i1 = min(a.V, i0 + a.chunk);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int VE = 16 / (int)sizeof(T), UN = 4;
   if (t == 0.f) {
     float v = kNegInf;
     int idx = -1;
-    for_row<T, 4>(row, i0, i1, [&](int i, float x) {
-      if (x > v) {  // a thread's entries come in rising order: the first of equals stays
+    auto one = [&](int i, float x) {
+      if (x > v || (x == v && i < idx)) {
         v = x;
         idx = i;
       }
+    };
+    for_row<T, UN>(row, i0, i1, one, [&](int i, const float* x, int n) {
+#pragma unroll
+      for (int k = 0; k < UN * VE; ++k)  // rising indices: the first of equals stays
+        if (x[k] > v) {
+          v = x[k];
+          idx = i + k / VE * (VT * VE) + k % VE;
+        }
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -124,14 +142,26 @@ __device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t,
     return;
   }
   const float c = 1.4426950408889634f / t;
+  // one maximum and one rescaling for all values of a step; a NaN stays in l, and so does
+  // +infinity (as infinity - infinity); without anything above -infinity nothing is added
   float m = kNegInf, l = 0.f;
-  for_row<T, 4>(row, i0, i1, [&](int, float x) {
-    if (x > m) {
-      l = m > kNegInf ? l * exp2f((m - x) * c) : l;
-      m = x;
-    }
-    // x <= m, or NaN (which stays in l); m = x = -infinity adds nothing
-    if (!(x == kNegInf)) l += exp2f((x - m) * c);
+  auto one = [&](int, float x) {
+    const float nm = fmaxf(m, x), base = nm > kNegInf ? nm : 0.f;
+    l = l * ex2((m - base) * c) + ex2((x - base) * c);
+    m = nm;
+  };
+  for_row<T, UN>(row, i0, i1, one, [&](int, const float* x, int) {
+    float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int k = 4; k < UN * VE; ++k) t4[k & 3] = fmaxf(t4[k & 3], x[k]);
+    const float nm = fmaxf(m, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+    const float base = nm > kNegInf ? nm : 0.f;
+    if (nm > m) l *= ex2((m - base) * c);
+    m = nm;
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < UN * VE; ++k) s4[k & 3] += ex2((x[k] - base) * c);
+    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -170,6 +200,16 @@ __global__ void __launch_bounds__(VT) verify_stats(VArgs a) {
     if (t == 0.f || s - a.S - 1 >= nd) return;
     stats_cta<TY>(a, static_cast<const TY*>(a.y) + ((size_t)b * a.S + s - a.S - 1) * a.y_ld, t, chunk, out);
   }
+}
+
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 x = __ldcs(reinterpret_cast<const uint2*>(p));
+  const __nv_bfloat16* t = reinterpret_cast<const __nv_bfloat16*>(&x);
+  v[0] = to_f(t[0]), v[1] = to_f(t[1]), v[2] = to_f(t[2]), v[3] = to_f(t[3]);
 }
 
 template <typename TX, typename TY>
@@ -233,10 +273,10 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
           const float lq = sl[S + 1 + lane];
           row_bad = row_bad || !(lq > 0.f && lq < INFINITY);
           const float yv = to_f(static_cast<const TY*>(a.y)[((size_t)b * S + lane) * a.y_ld + d]);
-          q = exp2f((yv - sm[S + 1 + lane]) * c) / lq;
+          q = ex2((yv - sm[S + 1 + lane]) * c) / lq;
         }
         const float xv = to_f(static_cast<const TX*>(a.x)[((size_t)b * (S + 1) + lane) * a.x_ld + d]);
-        const float p = exp2f((xv - sm[lane]) * c) / sl[lane];
+        const float p = ex2((xv - sm[lane]) * c) / sl[lane];
         pass = has && !row_bad && __ldg(&a.u[(size_t)b * S + lane]) * q < p;
       }
     }
@@ -282,12 +322,11 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   const int i0 = chunk * a.rchunk, i1 = min(a.V, i0 + a.rchunk);
   float vw = 0.f, vp = 0.f;
   int iw = -1, ipx = -1;
-#pragma unroll 4
-  for (int i = i0 + tid; i < i1; i += VT) {
-    const float p = exp2f((to_f(x[i]) - mp) * c) * ip;
-    float w = y ? p - exp2f((to_f(y[i]) - mq) * c) * iq : p;
+  // an entry's scores (indices rise: the first of equals stays)
+  auto run = [&](int i, float xv, float yv, float n) {
+    const float p = ex2((xv - mp) * c) * ip;
+    float w = y ? p - ex2((yv - mq) * c) * iq : p;
     if (i == dtok) w = 0.f;
-    const float n = __ldg(&e[i]);
     if (w > 0.f) {
       const float s = w / n;
       if (iw < 0 ? s == s : s > vw) {
@@ -302,7 +341,23 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
         ipx = i;
       }
     }
+  };
+  // four neighbouring entries at a time where the three rows allow it
+  auto off = [](const void* q, int n) { return reinterpret_cast<uintptr_t>(q) % n != 0; };
+  const bool fours = !off(x + i0, 4 * sizeof(TX)) && !(y && off(y + i0, 4 * sizeof(TY))) && !off(e + i0, 16);
+  const int i4 = fours ? i0 + (i1 - i0) / 4 * 4 : i0;
+#pragma unroll 2
+  for (int i = i0 + 4 * tid; i < i4; i += 4 * VT) {
+    float xv[4], yv[4] = {};
+    load4(x + i, xv);
+    if (y) load4(y + i, yv);
+    const float4 n = __ldcs(reinterpret_cast<const float4*>(e + i));
+    run(i, xv[0], yv[0], n.x);
+    run(i + 1, xv[1], yv[1], n.y);
+    run(i + 2, xv[2], yv[2], n.z);
+    run(i + 3, xv[3], yv[3], n.w);
   }
+  for (int i = i4 + tid; i < i1; i += VT) run(i, to_f(x[i]), y ? to_f(y[i]) : 0.f, __ldg(&e[i]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     best(vw, iw, __shfl_xor_sync(0xffffffffu, vw, o), __shfl_xor_sync(0xffffffffu, iw, o));
@@ -347,7 +402,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
 int chunk_for(long long rows, int V, int least) {
   const long long want = (152 * 16 + rows - 1) / rows;  // CTAs per row
   const long long c = (V + want - 1) / want;
-  return (int)std::max<long long>(least, std::min<long long>((c + 255) / 256 * 256, 32768));
+  return (int)std::max<long long>(least, std::min<long long>((c + 1023) / 1024 * 1024, 32768));
 }
 
 struct VPlan {
