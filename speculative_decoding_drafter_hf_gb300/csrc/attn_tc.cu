@@ -34,13 +34,14 @@ constexpr int BN = 128;        // keys per tile
 constexpr int TCT = 384;       // threads
 enum { PROMPT = 0, PAGED = 1 };
 constexpr int kNone = 0x7fffffff;
+constexpr int kSmall = 256;    // entries of a call that every CTA plans for itself
 
 template <int DH>
 struct Tc {
   static constexpr int TILE = BN * DH * 2;            // bytes of a K, V or Q tile
   static constexpr int SLOTS = DH == 128 ? 5 : 10;    // ring of K and V tiles
   static constexpr int O_COL = 256;                   // TMEM: S0 | S1 | O0 | O1
-  static constexpr size_t smem() { return (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 14) * 8 + 16 + 2 * 80 + 48; }
+  static constexpr size_t smem() { return (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 14) * 8 + 16 + 2 * 80 + 48 + (2 * kSmall + 2) * 4; }
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -211,6 +212,8 @@ struct TcArgs {
   int pre_items;   // paged: items of the prefix
   int units;       // paged: items per piece of a request's own keys
   int wide;        // rows of out start on 32 bytes
+  int small;       // paged: every CTA plans for itself, items are dealt out by index
+  int budget;      // pieces of the entries' own keys that there is room for, beside n
 };
 
 // What a CTA works on at a time, written by warp 2. Tile r's rows are tokens
@@ -257,8 +260,10 @@ __device__ __forceinline__ int taken_cta(const uint4* answer) {
   return got ? x : -1;
 }
 
+// eff, base: the entries' lengths and first pieces (in shared memory, or the workspace).
 template <int MODE>
-__device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it) {
+__device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, const int* eff, const int* base,
+                                          int chunk) {
   const AttnRows& a = c.a;
   it.split = 0;
   it.start = it.entry = it.len = it.part = 0;
@@ -299,15 +304,26 @@ __device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it) {
     it.tok0 = it.t0;
     it.ntok = min(it.split ? c.tb : 2 * c.tb, tokens - it.t0);
     it.j0 = it.part * a.pre_keys;
-    it.j1 = __ldcg(&a.eff[0]) ? min(a.shared, it.j0 + a.pre_keys) : it.j0;  // entry 0 empty: so is every row
+    it.j1 = eff[0] ? min(a.shared, it.j0 + a.pre_keys) : it.j0;  // entry 0 empty: so is every row
     it.direct = 0;
   } else {
     const int k = idx - c.pre_items, i = k / c.units, u = k % c.units;
-    const int chunk = __ldcg(&a.plan[1]);
+    if (c.small) {  // the last entry whose first piece is at or before i
+      int lo = 0, hi = a.n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid] <= i)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      it.entry = lo;
+    } else {
+      it.entry = __ldcg(&a.piece_of[i]);
+    }
     it.kind = 2;
-    it.entry = __ldcg(&a.piece_of[i]);
-    const int base = __ldcg(&a.base[it.entry]);
-    it.len = __ldcg(&a.eff[it.entry]);
+    const int first = base[it.entry];
+    it.len = eff[it.entry];
     it.split = a.rows <= c.tb;
     if (it.split) {
       it.g = 2 * u;
@@ -318,15 +334,92 @@ __device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it) {
     }
     it.tok0 = it.entry * a.rows + it.t0;
     it.ntok = min(it.split ? c.tb : 2 * c.tb, a.rows - it.t0);
-    it.j0 = a.shared + (i - base) * chunk;
+    it.j0 = a.shared + (i - first) * chunk;
     it.j1 = max(it.j0, min(it.len, it.j0 + chunk));
-    it.direct = a.npre == 0 && __ldcg(&a.base[it.entry + 1]) - base == 1;
+    it.direct = a.npre == 0 && base[it.entry + 1] - first == 1;
     it.part = i;
   }
   nt = (it.j1 - it.j0 + BN - 1) / BN;
   it.nt[0] = nt;
   it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? nt : 0;
   return true;
+}
+
+// Time of a call's own pieces, in key tiles per SM: `pieces` items * units of at most c
+// tiles, `all` tiles in total. A few rounds: whole ones; more, or beside the prefix's
+// items: their sum and half a last one.
+__device__ __forceinline__ float pieces_cost(const AttnRows& a, float pieces, int units, int c, int all, bool pre) {
+  const float rounds = pieces * units * (1.f / 152.f);
+  // an item's start and end, and its rows' way to the join and back, in tiles
+  const float extra = 1.5f + 0.5f * (float)(a.rows * a.G) * (1.f / 32.f);
+  return rounds < 6.f && !pre ? ceilf(rounds) * ((float)min(c, all) + extra)
+                              : (float)all * units * (1.f / 152.f) + rounds * extra + 0.5f * c;
+}
+// Candidates of keys per piece, in tiles: what k + 1 rounds over 152 SMs would take, and a
+// quarter more.
+constexpr int NC = 16;
+__device__ __forceinline__ int piece_candidate(int all, int units, int k) {
+  return max(1, (int)(((float)all * units / (152.f * (k / 2 + 1))) * (k & 1 ? 1.25f : 1.f) + 0.999f));
+}
+
+// A small call's plan, by one warp: eff[n], base[n + 1] in shared memory, the keys per
+// piece returned; eff is there already.
+__device__ __forceinline__ int plan_small(const TcArgs& c, const int* eff, int* base) {
+  const AttnRows& a = c.a;
+  const int lane = threadIdx.x & 31;
+  int all = 0;
+  for (int i = lane; i < a.n; i += 32) all += (max(0, eff[i] - a.shared) + BN - 1) / BN;
+  all = __reduce_add_sync(0xffffffffu, all);
+  // a candidate per lane (counted in floats: only the choice depends on it)
+  const int cand = piece_candidate(all, c.units, min(lane, NC - 1));
+  const float inv = 1.f / (float)cand;
+  float pieces = 0.f;
+  for (int i = 0; i < a.n; ++i) {
+    const float t = (float)((max(0, eff[i] - a.shared) + BN - 1) / BN);
+    pieces += fmaxf(1.f, ceilf(t * inv - 1e-4f));
+  }
+  float cost = lane < NC && pieces <= (float)(a.n + c.budget) ? pieces_cost(a, pieces, c.units, cand, all, c.pre_items > 0)
+                                                              : 3e38f;
+  float least = cost;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+  const int who = __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1;
+  int chunk = least < 3e38f ? __shfl_sync(0xffffffffu, cand, who) : all / c.budget + 1;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    int carry = 0;
+    for (int i0 = 0; i0 < a.n; i0 += 32) {
+      const int i = i0 + lane;
+      const int p = i < a.n ? max(1, ((max(0, eff[i] - a.shared) + BN - 1) / BN + chunk - 1) / chunk) : 0;
+      int x = p;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i < a.n) base[i] = carry + x - p;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) base[a.n] = carry;
+    __syncwarp();
+    if (carry <= a.n + c.budget) break;
+    chunk = all / c.budget + 1;  // always fits
+  }
+  return chunk * BN;
+}
+
+// Whether the entries from first on, every step-th, have entry 0's pages before `shared`;
+// by one CTA or warp (tid of threads).
+__device__ __forceinline__ void check_prefixes(const AttnRows& a, int first, int step, int tid, int threads) {
+  if (a.shared == 0 || !a.status) return;
+  bool bad = false, skip = false;
+  if (attn_raw_len(a, 0, skip) == 0) return;
+  const int32_t* t0 = attn_table(a, 0);
+  for (int i = first; i < a.n; i += step) {
+    if (attn_raw_len(a, i, skip) == 0) continue;
+    const int32_t* t = attn_table(a, i);
+    for (int j = tid; j < a.shared / a.page; j += threads) bad = bad || __ldg(&t[j]) != __ldg(&t0[j]);
+  }
+  if (bad) atomicOr(a.status, HF_S_BAD);
 }
 
 // Element offset in V of key j's row of KV head g.
@@ -377,6 +470,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;  // [0] tiles, [1] row-tile loads that the loader has asked for
+  int* s_eff = const_cast<int*>(issued) + 2;  // small calls: [kSmall] lengths, [kSmall + 1] first pieces
+  int* s_base = s_eff + kSmall;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -572,40 +667,73 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     } else if (warp == 2) {
       // ---- items
       bool ok = true;
-      int idx = blockIdx.x;
-      const int total = MODE == PROMPT ? 0 : c.pre_items + __ldcg(&a.plan[2]) * c.units;
-      int taken = 0;
-      for (int n = 0; ok;) {
-        if (MODE == PROMPT && lane == 0 && idx >= 0) take_next_cta(answer, n_full);
-        bool put = idx < 0 || (MODE == PAGED && idx >= total);
-        const bool end = put;
-        Item it;
-        it.kind = -1;
-        if (!end) put = make_item<MODE>(c, idx, it);
-        if (put) {
-          if (n >= 2) ok = wait_uniform(smem_u32(&i_empty[n & 1]), ((uint32_t)(n >> 1) & 1u) ^ 1u);
-          if (!ok) {  // the answer asked for above still has to land
-            if (MODE == PROMPT && idx >= 0) wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
-            break;
-          }
-          if (lane == 0) {
-            items[n & 1] = it;
-            mbar_arrive(&i_full[n & 1]);
-          }
-          ++n;
+      int n = 0;
+      auto put = [&](const Item& it) {
+        if (n >= 2) ok = wait_uniform(smem_u32(&i_empty[n & 1]), ((uint32_t)(n >> 1) & 1u) ^ 1u);
+        if (!ok) return;
+        if (lane == 0) {
+          items[n & 1] = it;
+          mbar_arrive(&i_full[n & 1]);
         }
-        if (end) break;
-        if (MODE == PROMPT) {
-          ok = wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
+        ++n;
+      };
+      Item it;
+      if (MODE == PROMPT) {
+        int idx = blockIdx.x, taken = 0;
+        while (ok && idx >= 0) {
+          if (lane == 0) take_next_cta(answer, n_full);
+          if (make_item<MODE>(c, idx, it, nullptr, nullptr, 0)) put(it);
+          // (also after a failure: the answer asked for has to land)
+          const bool came = wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
           ++taken;
-          idx = ok ? taken_cta(answer) : -1;
+          idx = came ? taken_cta(answer) : -1;
+          ok = ok && came;
           __syncwarp();
-        } else {
+        }
+      } else if (c.small) {
+        bool bad = false;
+        for (int i = lane; i < a.n; i += 32) {
+          s_eff[i] = attn_len(a, i, bad);
+          if (blockIdx.x == 0) a.eff[i] = s_eff[i];
+        }
+        if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, HF_S_BAD);
+        __syncwarp();
+        const int me = blockIdx.x, all = gridDim.x;
+        for (int idx = me; ok && idx < c.pre_items; idx += all) {
+          make_item<MODE>(c, idx, it, s_eff, s_base, 0);
+          put(it);
+        }
+        const int chunk = plan_small(c, s_eff, s_base);
+        const int pieces = s_base[a.n];
+        if (blockIdx.x == 0)
+          for (int i = lane; i <= a.n; i += 32) a.base[i] = s_base[i];
+        // CTAs with one item of the prefix less than the others first take what fills that time
+        const int own = pieces * c.units, heavy = c.pre_items % all, light = all - heavy;
+        const int fill = heavy ? (int)((a.pre_keys + BN) / (float)(min(chunk, a.table_ld * a.page) + 2 * BN)) : 0;
+        const int dealt = min(own, light * fill);
+        if (me >= heavy)
+          for (int q = me - heavy; ok && q < dealt; q += light) {
+            make_item<MODE>(c, c.pre_items + q, it, s_eff, s_base, chunk);
+            put(it);
+          }
+        for (int q = dealt + (me - heavy + all) % all; ok && q < own; q += all) {
+          make_item<MODE>(c, c.pre_items + q, it, s_eff, s_base, chunk);
+          put(it);
+        }
+      } else {
+        const int total = c.pre_items + __ldcg(&a.plan[2]) * c.units, chunk = __ldcg(&a.plan[1]);
+        for (int idx = blockIdx.x; ok && idx < total;) {
+          make_item<MODE>(c, idx, it, a.eff, a.base, chunk);
+          put(it);
           if (lane == 0) idx = atomicAdd(&a.plan[0], 1);
           idx = __shfl_sync(0xffffffffu, idx, 0);
         }
       }
+      it.kind = -1;
+      if (ok) put(it);
       if (!ok) *abort_flag = 1;
+    } else if (MODE == PAGED && c.small) {
+      check_prefixes(a, 1 + blockIdx.x, gridDim.x, lane, 32);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -638,7 +766,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           limit = it.t0 + tl + 1;
         } else {
           const int t = it.t0 + tl;
-          const int len = it.kind == 1 ? __ldcg(&a.eff[t / a.rows]) : it.len;
+          const int len = it.kind == 1 ? (c.small ? s_eff[t / a.rows] : __ldcg(&a.eff[t / a.rows])) : it.len;
           dead = len == 0;
           if (!dead) limit = max(0, len - a.rows + (it.kind == 1 ? t % a.rows : t) + 1);
         }
@@ -840,27 +968,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x > 0) {
-    if (a.shared == 0 || !a.status) return;
-    bool bad = false, first_bad = false;
-    if (attn_raw_len(a, 0, first_bad) == 0) return;
-    const int32_t* t0 = attn_table(a, 0);
-    for (int i = blockIdx.x; i < a.n; i += gridDim.x - 1) {
-      bool skip = false;
-      if (attn_raw_len(a, i, skip) == 0) continue;
-      const int32_t* t = attn_table(a, i);
-      for (int j = tid; j < a.shared / a.page; j += 1024) bad = bad || __ldg(&t[j]) != __ldg(&t0[j]);
-    }
-    if (bad) atomicOr(a.status, HF_S_BAD);
+    check_prefixes(a, blockIdx.x, gridDim.x - 1, tid, 1024);
     return;
   }
   bool bad = false;
   for (int i = tid; i < a.n; i += 1024) a.eff[i] = attn_len(a, i, bad);
   if (bad && a.status) atomicOr(a.status, HF_S_BAD);
   if (budget <= 0) return;  // pieces of a fixed number of keys
-  // Keys per piece: of some sizes the one whose items take the SMs the least time (a few
-  // rounds: whole ones; more, or beside the prefix's items: their sum and half a last
-  // one), the pieces fitting the workspace
-  constexpr int NC = 16;
+  // keys per piece: of some sizes the one that takes the least time, the pieces fitting
+  // the workspace
   __shared__ int s_count[NC + 1];
   if (tid <= NC) s_count[tid] = 0;
   __syncthreads();
@@ -869,9 +985,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   if (lane == 0 && tiles) atomicAdd(&s_count[NC], tiles);
   __syncthreads();
-  // candidates: what k + 1 rounds over 152 SMs would take, and a quarter more
   const int all = s_count[NC];
-  const int cand = max(1, (int)(((float)all * units / (152.f * (lane / 2 + 1))) * (lane & 1 ? 1.25f : 1.f) + 0.999f));
+  const int cand = piece_candidate(all, units, min(lane, NC - 1));
   int mine[NC] = {};
   for (int i = tid; i < (a.n + 31) / 32 * 32; i += 1024) {
     const int t = i < a.n ? (max(0, a.eff[i] - a.shared) + BN - 1) / BN : -1;
@@ -892,11 +1007,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
     // one lane per candidate; the last one always fits the workspace
     const int c = lane < NC ? cand : all / budget + 1;
     const int pieces = lane < NC ? s_count[lane] : a.n + budget;
-    const float rounds = (float)pieces * units * (1.f / 152.f);
-    // an item's start and end, and its rows' way to the join and back, in tiles
-    const float extra = 1.5f + 0.5f * (float)(a.rows * a.G) * (1.f / 32.f);
-    float cost = rounds < 6.f && pre_items == 0 ? ceilf(rounds) * ((float)min(c, all) + extra)
-                                                : (float)all * units * (1.f / 152.f) + rounds * extra + 0.5f * c;
+    float cost = pieces_cost(a, (float)pieces, units, c, all, pre_items > 0);
     if (pieces > a.n + budget || lane > NC) cost = 3e38f;
     float least = cost;
 #pragma unroll
@@ -1037,7 +1148,9 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, in
   if (e != cudaSuccess) return e;
   const long long most = pre_items + ((long long)a.n + budget) * units;
   const int grid = (int)std::min<long long>(most, 152);
-  e = launch_attn_plan(a, budget, units, grid, pre_items, st);
+  c.budget = budget;
+  c.small = a.n <= kSmall;
+  if (!c.small) e = launch_attn_plan(a, budget, units, grid, pre_items, st);
   if (e != cudaSuccess) return e;
   return a.dh == 128 ? launch_one<128, PAGED>(c, mq, mk, mv, dim3(grid), st)
                      : launch_one<64, PAGED>(c, mq, mk, mv, dim3(grid), st);

@@ -209,6 +209,21 @@ def test_attend(hf, dtype, hq, hkv, dh, page, rows, shared, own):
     assert not c.check()
 
 
+@pytest.mark.parametrize("shared", [0, 32])
+def test_attend_many_entries(hf, shared):
+    """More entries than requests: a list that repeats them, some of them empty, some long."""
+    own = [3, 17, 200, None, 64, 1, 33, 700, 16]
+    k, v, table, lens, refs = _shared_cache("bf16", 2, 64, 16, shared, own, 8)
+    c = _on_gpu(hf, k, v, table, lens, refs)
+    rng = random.Random(5)
+    req = [0] + [rng.randrange(len(own)) for _ in range(339)]
+    q = _randn((340, 2, 4, 64), "bf16", 5)
+    o = R.to64(c.attend(q.cuda(), _i32(req), shared=shared))
+    want, tol = R.pages(q, k[0], v[0], table, lens, 64 ** -0.5, True, req)
+    R.check_attention(o, want, tol)
+    assert not c.check()
+
+
 def test_attend_lists_repeats_and_strange_entries(hf):
     k, v, table, lens, refs = _shared_cache("bf16", 2, 128, 16, 32, [5, 60, 33, 9], 3)
     c = _on_gpu(hf, k, v, table, lens, refs)
