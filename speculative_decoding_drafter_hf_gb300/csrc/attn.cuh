@@ -31,43 +31,80 @@ struct AttnRows {
   int shared;      // tokens of the common prefix
   // pieces of the key axis: npre of the prefix (pre_keys keys each), then each
   // entry's own tokens: on CUDA cores nown pieces of own_keys each (unused ones
-  // among them), on tensor cores as many as the plan gives it. An entry of one
-  // piece in all has its rows written straight to out; the others' go to part_o /
-  // part_ml and attn_join joins them: the prefix's pieces of n * rows * Hq rows each,
-  // then the entries' of rows * Hq. Within a piece rows are ordered (KV head, token,
-  // head in its group), and part_o holds 8 columns of all rows, then the next 8: a
-  // warp with a row per lane writes whole lines.
+  // among them), on tensor cores wherever the line of all tiles is cut (AttnLine). Rows
+  // of one piece in all are written straight to out; the others' parts go to part_o /
+  // part_ml and attn_join joins them. part_o holds 8 columns of all rows of a piece,
+  // then the next 8: a warp with a row per lane writes whole lines. PartAt says where.
   int npre, pre_keys, nown, own_keys;
   float* part_o;   // [...][dh / 8][rows of the piece][8], not normalised
   float2* part_ml; // the same rows: maximum (base 2), sum
   // written on the device before the pieces are read
   int* eff;        // [n] tokens of each entry, 0 for those that break a rule
-  int* plan;       // tensor cores: [0] item counter, [1] keys per piece, [2] pieces
-  int* base;       // [n + 1] first piece of each entry
-  int* piece_of;   // entry of each piece
+  int* line;       // tensor cores: an AttnLine
+  int* tile0;      // [n + 1] where each entry starts on the line
+  int tb, units, unit_rows;  // tensor cores: tokens of a row tile; units of an entry's rows
 };
 
 __host__ __device__ inline bool attn_direct(const AttnRows& a) { return a.npre + a.nown == 1; }
 
-// Rows before piece p of the prefix or, own, before a piece of an entry, and the row
-// of (KV head g, token t of `tokens`, head i in the group) within it.
-__device__ __forceinline__ size_t part_first(const AttnRows& a, bool own, int p) {
-  const size_t N = (size_t)a.n * a.rows * a.Hq;
-  return own ? a.npre * N + (size_t)p * a.rows * a.Hq : p * N;
+constexpr int kKeyTile = 128;  // keys of a tile (tensor cores)
+
+// Where the part of one row of one piece lies.
+struct PartAt {
+  size_t first;  // rows before the piece
+  int region;    // rows of the piece
+  int row;       // in the piece
+};
+__device__ __forceinline__ PartAt part_prefix(const AttnRows& a, int piece, int g, int t, int i) {
+  const int N = a.n * a.rows * a.Hq;
+  return {(size_t)piece * N, N, (g * a.n * a.rows + t) * a.G + i};
 }
-__device__ __forceinline__ int part_row(const AttnRows& a, bool own, int g, int t, int i) {
-  return (g * (own ? a.rows : a.n * a.rows) + t) * a.G + i;
+__device__ __forceinline__ PartAt part_own_rows(const AttnRows& a, int entry, int piece, int g, int t, int i) {
+  const int N = a.rows * a.Hq;
+  return {(size_t)a.npre * a.n * N + ((size_t)entry * a.nown + piece) * N, N, (g * a.rows + t) * a.G + i};
+}
+// unit: a pair of KV heads with all rows, or 2 tb tokens of one head (where all rows
+// are more than a tile); slots are numbered along the line.
+__device__ __forceinline__ PartAt part_own_unit(const AttnRows& a, int slot, int g, int t, int i) {
+  const int row = a.rows <= a.tb ? ((g & 1) * a.rows + t) * a.G + i : t % (2 * a.tb) * a.G + i;
+  return {(size_t)a.npre * a.n * a.rows * a.Hq + (size_t)slot * a.unit_rows, a.unit_rows, row};
+}
+__device__ __forceinline__ int unit_of(const AttnRows& a, int g, int t) {
+  return a.rows <= a.tb ? g / 2 : t / (2 * a.tb) * a.Hkv + g;
 }
 
-// First piece of entry i's own tokens, and how many there are.
-__device__ __forceinline__ int attn_pieces(const AttnRows& a, int i, int& count) {
-  if (a.plan) {
-    const int b = __ldcg(&a.base[i]);
-    count = __ldcg(&a.base[i + 1]) - b;
-    return b;
+// The entries' own key tiles, entry after entry, once per unit, laid out on one line
+// that is cut into a stretch per CTA: the first `light` CTAs get `more` places each, the
+// others `less`. A piece is what a CTA has of one entry and unit. An entry with tiles
+// first has kItemStart empty places: what an item costs beside its tiles (measured, 64 x 8
+// rows: about 2.2 us a tile, 1.7 us an item).
+constexpr int kItemStart = 1;
+__device__ __forceinline__ int entry_places(int keys) {
+  return keys > 0 ? (keys + kKeyTile - 1) / kKeyTile + kItemStart : 0;
+}
+struct AttnLine {
+  int tiles;  // places of all entries (times units: the line's length)
+  int light, more, less;
+  __device__ __forceinline__ int cta(int pos) const {  // whose stretch pos lies in
+    const int head = light * more;
+    return pos < head ? pos / more : light + (pos - head) / max(less, 1);
   }
-  count = max(1, (max(0, __ldcg(&a.eff[i]) - a.shared) + a.own_keys - 1) / a.own_keys);
-  return i * a.nown;
+  __device__ __forceinline__ int start(int c) const { return c <= light ? c * more : light * more + (c - light) * less; }
+};
+// heavy: CTAs that have an item of the prefix more, as long as `pre` tiles, than the others.
+__device__ __forceinline__ AttnLine make_line(int tiles, int units, int ctas, int heavy, int pre) {
+  AttnLine l{tiles, ctas, 0, 0};
+  const int all = tiles * units;
+  if (heavy > 0) {
+    l.light = ctas - heavy;
+    const int rest = all - l.light * pre;  // what is left once all have as much to do
+    l.less = rest > 0 ? (rest + ctas - 1) / ctas : 0;
+    l.more = rest > 0 ? l.less + pre : (all + l.light - 1) / l.light;
+  } else {
+    l.more = (all + ctas - 1) / ctas;
+  }
+  l.more = max(l.more, 1);
+  return l;
 }
 
 // Length of entry i as the call takes it: 0 for entries that break a rule (bad set).
@@ -143,12 +180,12 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a) {
 // Tensor-core variants (attn_tc.cu), where attn_tc_ok.
 bool attn_tc_ok(int dtype, int dh);
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
-// Over a paged cache: items of one piece of the prefix and of one piece of an entry,
-// and how many pieces of the entries there are at most beside n (a.npre, a.pre_keys set).
-void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget);
-cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, int budget, cudaStream_t st);
-// Entries' lengths and status checks; with budget > 0 the pieces of the entries.
-cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, int pre_items, cudaStream_t st);
+// Over a paged cache: the prefix's pieces and the rows' units (fields of a), items of the
+// prefix and slots of own pieces.
+void attn_tc_sizes(AttnRows& a, int& pre_items, long long& slots);
+cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t st);
+// Entries' lengths and status checks; tensor cores (ctas > 0): the line too.
+cudaError_t launch_attn_plan(const AttnRows& a, int ctas, int heavy, cudaStream_t st);
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
 cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st);

@@ -406,17 +406,15 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
           for (int k = 0; k < 4; ++k) dst[d + k] = from_f<T>(o[i][4 * c + k] * inv);
       }
     } else {
-      const bool own = MODE == OWN;
-      const size_t first_row = part_first(a, own, own ? entry * a.nown + piece : piece);
-      const size_t region = (size_t)(own ? a.rows : a.n * a.rows) * a.Hq;
       const int rr = row0 + ty * 4 + i;
-      const size_t r = part_row(a, own, g, rr / a.G, rr % a.G);
-      if (tx == 0) a.part_ml[first_row + r] = make_float2(m[i], l[i]);
+      const PartAt at = MODE == OWN ? part_own_rows(a, entry, piece, g, rr / a.G, rr % a.G)
+                                    : part_prefix(a, piece, g, rr / a.G, rr % a.G);
+      if (tx == 0) a.part_ml[at.first + at.row] = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < MAXC; ++c) {
         const int d = tx * 4 + 64 * c;
         if (d < dh)
-          *reinterpret_cast<float4*>(&a.part_o[first_row * dh + ((d / 8) * region + r) * 8 + d % 8]) =
+          *reinterpret_cast<float4*>(&a.part_o[at.first * dh + ((size_t)(d / 8) * at.region + at.row) * 8 + d % 8]) =
               make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
       }
     }
@@ -440,13 +438,23 @@ __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
   const long long unit = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
   const int entry = (int)(unit / fours), lr = (int)(unit % fours) * 4 + (lane & 3), col = (lane >> 2) * 8;
   bool on = entry < a.n && lr < per;
-  int own = 1, first = 0;
-  if (on) first = attn_pieces(a, entry, own);
-  if (a.npre == 0 && own == 1 && (a.plan || attn_direct(a))) on = false;  // written already
-  const int pieces = on && __ldcg(&a.eff[entry]) > 0 ? a.npre + own : 0;
   const int g = on ? lr / (a.rows * a.G) : 0, t = on ? lr / a.G % a.rows : 0, i = on ? lr % a.G : 0;
-  const size_t all = (size_t)a.n * per;
-  const int prow = part_row(a, false, g, entry * a.rows + t, i);
+  const int len = on ? __ldcg(&a.eff[entry]) : 0;
+  // the entry's own pieces: `own` of them from number `first` on
+  int own = 0, first = 0, slot = 0;
+  if (len > 0 && a.line) {
+    const AttnLine line = {__ldcg(&a.line[0]), __ldcg(&a.line[1]), __ldcg(&a.line[2]), __ldcg(&a.line[3])};
+    const int u = unit_of(a, g, t), t0 = __ldcg(&a.tile0[entry]), t1 = __ldcg(&a.tile0[entry + 1]);
+    if (t1 > t0) {
+      first = line.cta(u * line.tiles + t0 + kItemStart);
+      own = line.cta(u * line.tiles + t1 - 1) - first + 1;
+    }
+    slot = u * a.n + entry;
+    if (a.npre == 0 && own == 1) on = false;  // written already
+  } else if (len > 0) {
+    own = max(1, (max(0, len - a.shared) + a.own_keys - 1) / a.own_keys);
+  }
+  const int pieces = on && len > 0 ? a.npre + own : 0;
   float m = -INFINITY, l = 0.f, acc[SEGS][8] = {};
   for (int p0 = sub; p0 < pieces; p0 += BATCH * WPR) {
     float2 ml[BATCH];
@@ -456,15 +464,16 @@ __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
       const int p = p0 + k * WPR;
       ml[k] = make_float2(-INFINITY, 0.f);
       if (p >= pieces) continue;
-      const bool mine = p >= a.npre;
-      const size_t f = part_first(a, mine, mine ? first + p - a.npre : p), region = mine ? (size_t)per : all;
-      const size_t r = mine ? lr : prow;
-      ml[k] = __ldcg(&a.part_ml[f + r]);
+      const int k_own = first + p - a.npre;
+      const PartAt at = p < a.npre ? part_prefix(a, p, g, entry * a.rows + t, i)
+                        : a.line   ? part_own_unit(a, slot + k_own, g, t, i)
+                                   : part_own_rows(a, entry, k_own, g, t, i);
+      ml[k] = __ldcg(&a.part_ml[at.first + at.row]);
 #pragma unroll
       for (int s = 0; s < SEGS; ++s)
         if (col + 64 * s < dh) {
           const float4* src =
-              reinterpret_cast<const float4*>(&a.part_o[f * dh + ((size_t)(col / 8 + 8 * s) * region + r) * 8]);
+              reinterpret_cast<const float4*>(&a.part_o[at.first * dh + ((size_t)(col / 8 + 8 * s) * at.region + at.row) * 8]);
           x[k][s][0] = __ldcg(src);
           x[k][s][1] = __ldcg(src + 1);
         }
@@ -662,25 +671,27 @@ void plan_pieces(AttnRows& a) {
 // Sizes and workspace of a call.
 struct PagesPlan {
   bool tc;
-  int pre_items, units, budget;         // tensor cores
-  size_t eff, base, piece_of, ml, o, total;  // offsets in the workspace (the plan is at 0)
+  int pre_items, pieces;                // tensor cores: items of the prefix; about how many pieces a row has
+  size_t eff, tile0, ml, o, total;      // offsets in the workspace (the line is at 0)
 };
 PagesPlan plan_call(AttnRows& a, int dtype) {
   PagesPlan w{};
   w.tc = attn_tc_ok(dtype, a.dh);
-  size_t pieces;
+  const size_t N = (size_t)a.n * a.rows * a.Hq;
+  size_t rows;
   if (w.tc) {
-    attn_tc_sizes(a, w.pre_items, w.units, w.budget);
-    pieces = (size_t)a.n + w.budget;
+    long long slots;
+    attn_tc_sizes(a, w.pre_items, slots);
+    rows = a.npre * N + (size_t)slots * a.unit_rows;
+    w.pieces = a.npre + 1 + 152 / (a.units * a.n);
   } else {
     plan_pieces(a);
-    pieces = attn_direct(a) ? 0 : (size_t)a.n * a.nown;
+    rows = attn_direct(a) ? 0 : (a.npre + a.nown) * N;
+    w.pieces = a.npre + a.nown;
   }
-  const size_t rows = (attn_direct(a) && !w.tc ? 0 : (size_t)a.npre * a.n * a.rows * a.Hq) + pieces * a.rows * a.Hq;
   w.eff = 16;
-  w.base = w.eff + (size_t)a.n * sizeof(int);
-  w.piece_of = w.base + (w.tc ? ((size_t)a.n + 1) * sizeof(int) : 0);
-  w.ml = (w.piece_of + (w.tc ? pieces * sizeof(int) : 0) + 15) / 16 * 16;
+  w.tile0 = w.eff + (size_t)a.n * sizeof(int);
+  w.ml = (w.tile0 + ((size_t)a.n + 1) * sizeof(int) + 15) / 16 * 16;
   w.o = (w.ml + rows * sizeof(float2) + 31) / 32 * 32;
   w.total = w.o + rows * a.dh * sizeof(float) + 16;  // (the rows start on 32 bytes)
   return w;
@@ -693,7 +704,9 @@ const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq,
   if (rows < 1 || rows > 64) return "rows must be 1..64";
   if (shared < 0 || shared % p->page || shared > (long long)p->table_ld * p->page)
     return "shared must be a multiple of page, at most table_ld * page";
-  if ((long long)n * rows * hq > 0x7fffffffLL / 4) return "n * rows * n_q_heads is too large";
+  if ((long long)n * rows * hq > 0x7fffffffLL / 4 ||
+      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart) * n * ((long long)rows * hq / 128 + p->n_kv_heads) > 0x7fffffffLL)
+    return "n * rows * n_q_heads, or that times the table's reach, is too large";
   a.Hq = hq;
   a.Hkv = p->n_kv_heads;
   a.G = hq / p->n_kv_heads;
@@ -802,15 +815,14 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
   if (w.tc) {
-    a.plan = reinterpret_cast<int*>(ws);
-    a.base = reinterpret_cast<int*>(ws + w.base);
-    a.piece_of = reinterpret_cast<int*>(ws + w.piece_of);
-    e = launch_attn_tc_pages(a, w.pre_items, w.units, w.budget, st);
+    a.line = reinterpret_cast<int*>(ws);
+    a.tile0 = reinterpret_cast<int*>(ws + w.tile0);
+    e = launch_attn_tc_pages(a, w.pre_items, st);
   } else {
-    e = launch_attn_plan(a, 0, 0, 0, 0, st);
+    e = launch_attn_plan(a, 0, 0, st);
     if (e == cudaSuccess && a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
     if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
   }
-  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, a.npre + (w.tc ? 1 + w.budget / n : a.nown), st);
+  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, w.pieces, st);
   return done(e);
 }

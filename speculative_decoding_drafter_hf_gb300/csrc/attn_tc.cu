@@ -30,7 +30,7 @@
 namespace hf {
 namespace {
 
-constexpr int BN = 128;        // keys per tile
+constexpr int BN = kKeyTile;   // keys per tile
 constexpr int TCT = 384;       // threads
 enum { PROMPT = 0, PAGED = 1 };
 constexpr int kNone = 0x7fffffff;
@@ -210,10 +210,8 @@ struct TcArgs {
   int blocks;      // prompt: slots of 2 tb tokens; paged: blocks of the prefix rows
   int box_rows;    // rows of a K / V box (prompt: 128, paged: the page)
   int pre_items;   // paged: items of the prefix
-  int units;       // paged: items per piece of a request's own keys
   int wide;        // rows of out start on 32 bytes
-  int small;       // paged: every CTA plans for itself, items are dealt out by index
-  int budget;      // pieces of the entries' own keys that there is room for, beside n
+  int small;       // paged: every CTA plans for itself
 };
 
 // What a CTA works on at a time, written by warp 2. Tile r's rows are tokens
@@ -228,7 +226,7 @@ struct Item {
   int start;       // prompt: row of key 0
   int entry, len;  // own: the entry and its tokens
   int direct;      // rows go to out
-  int part;        // else: first row of the partial results / (rows * Hq), own; piece, prefix
+  int part;        // else: the prefix's piece, the own pieces' slot
   int low[2];      // least number of keys that a row of the tile sees
   int odd[2];      // first key of a tile whose odd values of V were taken as zero
 };
@@ -260,10 +258,9 @@ __device__ __forceinline__ int taken_cta(const uint4* answer) {
   return got ? x : -1;
 }
 
-// eff, base: the entries' lengths and first pieces (in shared memory, or the workspace).
+// Prompt: the tile of CTA idx's slot, if it has one. Paged: item idx of the prefix.
 template <int MODE>
-__device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, const int* eff, const int* base,
-                                          int chunk) {
+__device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, const int* eff) {
   const AttnRows& a = c.a;
   it.split = 0;
   it.start = it.entry = it.len = it.part = 0;
@@ -288,123 +285,97 @@ __device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, co
     return true;
   }
   const int heads = (a.Hkv + 1) / 2;  // split: pairs of heads
-  if (idx < c.pre_items) {
-    const int tokens = a.n * a.rows;
-    it.kind = 1;
-    it.split = tokens <= c.tb;
-    if (it.split) {
-      it.g = 2 * (idx % heads);
-      it.part = idx / heads;
-      it.t0 = 0;
-    } else {
-      it.t0 = idx % c.blocks * 2 * c.tb;
-      it.g = idx / c.blocks % a.Hkv;
-      it.part = idx / c.blocks / a.Hkv;
-    }
-    it.tok0 = it.t0;
-    it.ntok = min(it.split ? c.tb : 2 * c.tb, tokens - it.t0);
-    it.j0 = it.part * a.pre_keys;
-    it.j1 = eff[0] ? min(a.shared, it.j0 + a.pre_keys) : it.j0;  // entry 0 empty: so is every row
-    it.direct = 0;
+  const int tokens = a.n * a.rows;
+  it.kind = 1;
+  it.split = tokens <= c.tb;
+  if (it.split) {
+    it.g = 2 * (idx % heads);
+    it.part = idx / heads;
+    it.t0 = 0;
   } else {
-    const int k = idx - c.pre_items, i = k / c.units, u = k % c.units;
-    if (c.small) {  // the last entry whose first piece is at or before i
-      int lo = 0, hi = a.n;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (base[mid] <= i)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      it.entry = lo;
-    } else {
-      it.entry = __ldcg(&a.piece_of[i]);
-    }
-    it.kind = 2;
-    const int first = base[it.entry];
-    it.len = eff[it.entry];
-    it.split = a.rows <= c.tb;
-    if (it.split) {
-      it.g = 2 * u;
-      it.t0 = 0;
-    } else {
-      it.g = u % a.Hkv;
-      it.t0 = u / a.Hkv * 2 * c.tb;
-    }
-    it.tok0 = it.entry * a.rows + it.t0;
-    it.ntok = min(it.split ? c.tb : 2 * c.tb, a.rows - it.t0);
-    it.j0 = a.shared + (i - first) * chunk;
-    it.j1 = max(it.j0, min(it.len, it.j0 + chunk));
-    it.direct = a.npre == 0 && base[it.entry + 1] - first == 1;
-    it.part = i;
+    it.t0 = idx % c.blocks * 2 * c.tb;
+    it.g = idx / c.blocks % a.Hkv;
+    it.part = idx / c.blocks / a.Hkv;
   }
-  nt = (it.j1 - it.j0 + BN - 1) / BN;
-  it.nt[0] = nt;
+  it.tok0 = it.t0;
+  it.ntok = min(it.split ? c.tb : 2 * c.tb, tokens - it.t0);
+  it.j0 = it.part * a.pre_keys;
+  it.j1 = eff[0] ? min(a.shared, it.j0 + a.pre_keys) : it.j0;  // entry 0 empty: so is every row
+  it.direct = 0;
+  it.nt[0] = nt = (it.j1 - it.j0 + BN - 1) / BN;
   it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? nt : 0;
   return true;
 }
 
-// Time of a call's own pieces, in key tiles per SM: `pieces` items * units of at most c
-// tiles, `all` tiles in total. A few rounds: whole ones; more, or beside the prefix's
-// items: their sum and half a last one.
-__device__ __forceinline__ float pieces_cost(const AttnRows& a, float pieces, int units, int c, int all, bool pre) {
-  const float rounds = pieces * units * (1.f / 152.f);
-  // an item's start and end, and its rows' way to the join and back, in tiles
-  const float extra = 1.5f + 0.5f * (float)(a.rows * a.G) * (1.f / 32.f);
-  return rounds < 6.f && !pre ? ceilf(rounds) * ((float)min(c, all) + extra)
-                              : (float)all * units * (1.f / 152.f) + rounds * extra + 0.5f * c;
-}
-// Candidates of keys per piece, in tiles: what k + 1 rounds over 152 SMs would take, and a
-// quarter more.
-constexpr int NC = 16;
-__device__ __forceinline__ int piece_candidate(int all, int units, int k) {
-  return max(1, (int)(((float)all * units / (152.f * (k / 2 + 1))) * (k & 1 ? 1.25f : 1.f) + 0.999f));
+// The item at pos of the line, in the stretch [pos, end) of its CTA `cta`, if a tile lies
+// there; the places that it takes are returned. eff, tile0: in shared memory or the
+// workspace.
+__device__ __forceinline__ int make_own(const TcArgs& c, const AttnLine& line, int cta, int pos, int end, Item& it,
+                                        bool& some, const int* eff, const int* tile0) {
+  const AttnRows& a = c.a;
+  const int u = pos / line.tiles, at = pos - u * line.tiles;
+  int lo = 0, hi = a.n;  // the last entry that starts at or before `at`
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile0[mid] <= at)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int first = tile0[lo] + kItemStart, last = tile0[lo + 1], skip = max(0, first - at);
+  const int take = min(end - pos, last - at) - skip, from = at + skip;
+  some = take > 0;
+  if (!some) return min(end - pos, skip);
+  it.kind = 2;
+  it.entry = lo;
+  it.len = eff[lo];
+  it.start = 0;
+  it.low[0] = it.low[1] = it.odd[0] = it.odd[1] = kNone;
+  it.split = a.rows <= c.tb;
+  if (it.split) {
+    it.g = 2 * u;
+    it.t0 = 0;
+  } else {
+    it.g = u % a.Hkv;
+    it.t0 = u / a.Hkv * 2 * c.tb;
+  }
+  it.tok0 = lo * a.rows + it.t0;
+  it.ntok = min(it.split ? c.tb : 2 * c.tb, a.rows - it.t0);
+  it.j0 = a.shared + (from - first) * BN;
+  it.j1 = min(it.len, it.j0 + take * BN);
+  it.direct = a.npre == 0 && line.cta(u * line.tiles + first) == line.cta(u * line.tiles + last - 1);
+  it.part = u * a.n + lo + cta;
+  it.nt[0] = take;
+  it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? take : 0;
+  return skip + take;
 }
 
-// A small call's plan, by one warp: eff[n], base[n + 1] in shared memory, the keys per
-// piece returned; eff is there already.
-__device__ __forceinline__ int plan_small(const TcArgs& c, const int* eff, int* base) {
-  const AttnRows& a = c.a;
+// An item of the prefix, in tiles of own keys: its two row tiles share their keys (measured
+// 1.56 us a tile), or are two heads with keys of their own (2.9 us), and end with more rows.
+__device__ __forceinline__ int prefix_places(const AttnRows& a) {
+  const int tiles = a.pre_keys / BN;
+  return (a.n * a.rows <= a.tb ? tiles * 5 / 4 : tiles * 9 / 16) + 2;
+}
+
+// One warp: where the entries start on the line, from their lengths; all places returned.
+__device__ __forceinline__ int scan_tiles(const AttnRows& a, const int* eff, int* tile0) {
   const int lane = threadIdx.x & 31;
-  int all = 0;
-  for (int i = lane; i < a.n; i += 32) all += (max(0, eff[i] - a.shared) + BN - 1) / BN;
-  all = __reduce_add_sync(0xffffffffu, all);
-  // a candidate per lane (counted in floats: only the choice depends on it)
-  const int cand = piece_candidate(all, c.units, min(lane, NC - 1));
-  const float inv = 1.f / (float)cand;
-  float pieces = 0.f;
-  for (int i = 0; i < a.n; ++i) {
-    const float t = (float)((max(0, eff[i] - a.shared) + BN - 1) / BN);
-    pieces += fmaxf(1.f, ceilf(t * inv - 1e-4f));
-  }
-  float cost = lane < NC && pieces <= (float)(a.n + c.budget) ? pieces_cost(a, pieces, c.units, cand, all, c.pre_items > 0)
-                                                              : 3e38f;
-  float least = cost;
+  int carry = 0;
+  for (int i0 = 0; i0 < a.n; i0 += 32) {
+    const int i = i0 + lane;
+    const int t = i < a.n ? entry_places(eff[i] - a.shared) : 0;
+    int x = t;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-  const int who = __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1;
-  int chunk = least < 3e38f ? __shfl_sync(0xffffffffu, cand, who) : all / c.budget + 1;
-  for (int attempt = 0; attempt < 2; ++attempt) {
-    int carry = 0;
-    for (int i0 = 0; i0 < a.n; i0 += 32) {
-      const int i = i0 + lane;
-      const int p = i < a.n ? max(1, ((max(0, eff[i] - a.shared) + BN - 1) / BN + chunk - 1) / chunk) : 0;
-      int x = p;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (i < a.n) base[i] = carry + x - p;
-      carry += __shfl_sync(0xffffffffu, x, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    if (lane == 0) base[a.n] = carry;
-    __syncwarp();
-    if (carry <= a.n + c.budget) break;
-    chunk = all / c.budget + 1;  // always fits
+    if (i < a.n) tile0[i] = carry + x - t;
+    carry += __shfl_sync(0xffffffffu, x, 31);
   }
-  return chunk * BN;
+  if (lane == 0) tile0[a.n] = carry;
+  __syncwarp();
+  return carry;
 }
 
 // Whether the entries from first on, every step-th, have entry 0's pages before `shared`;
@@ -470,8 +441,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;  // [0] tiles, [1] row-tile loads that the loader has asked for
-  int* s_eff = const_cast<int*>(issued) + 2;  // small calls: [kSmall] lengths, [kSmall + 1] first pieces
-  int* s_base = s_eff + kSmall;
+  int* s_eff = const_cast<int*>(issued) + 2;  // small calls: [kSmall] lengths, [kSmall + 1] places on the line
+  int* s_tile0 = s_eff + kSmall;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -682,7 +653,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         int idx = blockIdx.x, taken = 0;
         while (ok && idx >= 0) {
           if (lane == 0) take_next_cta(answer, n_full);
-          if (make_item<MODE>(c, idx, it, nullptr, nullptr, 0)) put(it);
+          if (make_item<MODE>(c, idx, it, nullptr)) put(it);
           // (also after a failure: the answer asked for has to land)
           const bool came = wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
           ++taken;
@@ -690,43 +661,40 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           ok = ok && came;
           __syncwarp();
         }
-      } else if (c.small) {
-        bool bad = false;
-        for (int i = lane; i < a.n; i += 32) {
-          s_eff[i] = attn_len(a, i, bad);
-          if (blockIdx.x == 0) a.eff[i] = s_eff[i];
-        }
-        if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, HF_S_BAD);
-        __syncwarp();
-        const int me = blockIdx.x, all = gridDim.x;
-        for (int idx = me; ok && idx < c.pre_items; idx += all) {
-          make_item<MODE>(c, idx, it, s_eff, s_base, 0);
-          put(it);
-        }
-        const int chunk = plan_small(c, s_eff, s_base);
-        const int pieces = s_base[a.n];
-        if (blockIdx.x == 0)
-          for (int i = lane; i <= a.n; i += 32) a.base[i] = s_base[i];
-        // CTAs with one item of the prefix less than the others first take what fills that time
-        const int own = pieces * c.units, heavy = c.pre_items % all, light = all - heavy;
-        const int fill = heavy ? (int)((a.pre_keys + BN) / (float)(min(chunk, a.table_ld * a.page) + 2 * BN)) : 0;
-        const int dealt = min(own, light * fill);
-        if (me >= heavy)
-          for (int q = me - heavy; ok && q < dealt; q += light) {
-            make_item<MODE>(c, c.pre_items + q, it, s_eff, s_base, chunk);
-            put(it);
-          }
-        for (int q = dealt + (me - heavy + all) % all; ok && q < own; q += all) {
-          make_item<MODE>(c, c.pre_items + q, it, s_eff, s_base, chunk);
-          put(it);
-        }
       } else {
-        const int total = c.pre_items + __ldcg(&a.plan[2]) * c.units, chunk = __ldcg(&a.plan[1]);
-        for (int idx = blockIdx.x; ok && idx < total;) {
-          make_item<MODE>(c, idx, it, a.eff, a.base, chunk);
+        const int me = blockIdx.x, all = gridDim.x;
+        const int *eff = a.eff, *tile0 = a.tile0;
+        if (c.small) {
+          bool bad = false;
+          for (int i = lane; i < a.n; i += 32) {
+            s_eff[i] = attn_len(a, i, bad);
+            if (me == 0) a.eff[i] = s_eff[i];
+          }
+          if (bad && a.status && me == 0) atomicOr(a.status, HF_S_BAD);
+          eff = s_eff;
+          tile0 = s_tile0;
+          __syncwarp();
+        }
+        for (int idx = me; ok && idx < c.pre_items; idx += all) {
+          make_item<MODE>(c, idx, it, eff);
           put(it);
-          if (lane == 0) idx = atomicAdd(&a.plan[0], 1);
-          idx = __shfl_sync(0xffffffffu, idx, 0);
+        }
+        const int heavy = c.pre_items % all;
+        AttnLine line;
+        if (c.small) {
+          line = make_line(scan_tiles(a, s_eff, s_tile0), a.units, all, heavy, prefix_places(a));
+          if (me == 0) {
+            for (int i = lane; i <= a.n; i += 32) a.tile0[i] = s_tile0[i];
+            if (lane == 0) *reinterpret_cast<AttnLine*>(a.line) = line;
+          }
+        } else {
+          line = *reinterpret_cast<const AttnLine*>(a.line);
+        }
+        const int cta = (me - heavy + all) % all, end = min(line.start(cta + 1), line.tiles * a.units);
+        for (int pos = line.start(cta); ok && pos < end;) {
+          bool some;
+          pos += make_own(c, line, cta, pos, end, it, some, eff, tile0);
+          if (some) put(it);
         }
       }
       it.kind = -1;
@@ -894,9 +862,10 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         const bool direct = it.direct;
         const float inv = l == 0.f || dead ? 0.f : 1.f / l;
         const int from = *(volatile int*)&it.odd[streams == 1 ? 0 : r];
-        const bool own = it.kind == 2;
-        const size_t first = part_first(a, own, it.part), region = (size_t)(own ? a.rows : a.n * a.rows) * a.Hq;
-        const size_t pr = part_row(a, own, g, it.t0 + tl, row_head);
+        PartAt at{};
+        if (MODE == PAGED)
+          at = it.kind == 1 ? part_prefix(a, it.part, g, it.t0 + tl, row_head)
+                            : part_own_unit(a, it.part, g, it.t0 + tl, row_head);
 #pragma unroll 1
         for (int q = 0; q < DH; q += 32) {
           float o[32];
@@ -930,13 +899,13 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
                 reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
           } else if (mine > 0) {
-            float* dst = a.part_o + first * DH + ((q / 8) * region + pr) * 8;
+            float* dst = a.part_o + at.first * DH + ((size_t)(q / 8) * at.region + at.row) * 8;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) store8(dst + k * region * 8, reinterpret_cast<uint32_t*>(o) + 8 * k);
+            for (int k = 0; k < 4; ++k) store8(dst + (size_t)k * at.region * 8, reinterpret_cast<uint32_t*>(o) + 8 * k);
           }
         }
         if (!direct && valid)
-          a.part_ml[first + pr] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(mb, l);
+          a.part_ml[at.first + at.row] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(mb, l);
         tc_fence_before();
       }
       __syncwarp();
@@ -959,10 +928,9 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Which entries the call sees, and how the requests' own keys are cut: one CTA for
-// the lengths and the list of pieces, the others compare the entries' prefixes.
-//   plan: [0] counter of items, [1] keys per piece, [2] pieces
-__global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int units, int first, int pre_items) {
+// Which entries the call sees, and the line of their tiles: one CTA for the lengths and
+// the places on the line, the others compare the entries' prefixes.
+__global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int ctas, int heavy) {
   __shared__ int s_scan[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -972,55 +940,17 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
     return;
   }
   bool bad = false;
-  for (int i = tid; i < a.n; i += 1024) a.eff[i] = attn_len(a, i, bad);
-  if (bad && a.status) atomicOr(a.status, HF_S_BAD);
-  if (budget <= 0) return;  // pieces of a fixed number of keys
-  // keys per piece: of some sizes the one that takes the least time, the pieces fitting
-  // the workspace
-  __shared__ int s_count[NC + 1];
-  if (tid <= NC) s_count[tid] = 0;
-  __syncthreads();
-  int tiles = 0;
-  for (int i = tid; i < a.n; i += 1024) tiles += (max(0, a.eff[i] - a.shared) + BN - 1) / BN;
-  tiles = __reduce_add_sync(0xffffffffu, tiles);
-  if (lane == 0 && tiles) atomicAdd(&s_count[NC], tiles);
-  __syncthreads();
-  const int all = s_count[NC];
-  const int cand = piece_candidate(all, units, min(lane, NC - 1));
-  int mine[NC] = {};
-  for (int i = tid; i < (a.n + 31) / 32 * 32; i += 1024) {
-    const int t = i < a.n ? (max(0, a.eff[i] - a.shared) + BN - 1) / BN : -1;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int c = __shfl_sync(0xffffffffu, cand, k);
-      if (t >= 0) mine[k] += max(1, (int)((unsigned)(t + c - 1) / (unsigned)c));
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int s = __reduce_add_sync(0xffffffffu, mine[k]);
-    if (lane == 0 && s) atomicAdd(&s_count[k], s);
-  }
-  __syncthreads();
-  int chunk;
-  {
-    // one lane per candidate; the last one always fits the workspace
-    const int c = lane < NC ? cand : all / budget + 1;
-    const int pieces = lane < NC ? s_count[lane] : a.n + budget;
-    float cost = pieces_cost(a, (float)pieces, units, c, all, pre_items > 0);
-    if (pieces > a.n + budget || lane > NC) cost = 3e38f;
-    float least = cost;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-    const uint32_t who = __ballot_sync(0xffffffffu, cost == least && lane <= NC);
-    chunk = __shfl_sync(0xffffffffu, c, __ffs(who) - 1);
-  }
   int carry = 0;
   for (int i0 = 0; i0 < a.n; i0 += 1024) {
     const int i = i0 + tid;
-    int p = 0;
-    if (i < a.n) p = max(1, ((max(0, a.eff[i] - a.shared) + BN - 1) / BN + chunk - 1) / chunk);
-    int x = p;
+    int t = 0;
+    if (i < a.n) {
+      const int len = attn_len(a, i, bad);
+      a.eff[i] = len;
+      t = entry_places(len - a.shared);
+    }
+    if (ctas == 0) continue;  // CUDA cores: pieces of a fixed number of keys
+    int x = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -1034,18 +964,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int budget, int 
       if (w < warp) before += s_scan[w];
       sum += s_scan[w];
     }
-    const int b = before + x - p;
-    if (i < a.n) {
-      a.base[i] = b;
-      for (int k = 0; k < p; ++k) a.piece_of[b + k] = i;
-    }
+    if (i < a.n) a.tile0[i] = before + x - t;
     carry = sum;
   }
-  if (tid == 0) {
-    a.base[a.n] = carry;
-    a.plan[0] = first;
-    a.plan[1] = chunk * BN;
-    a.plan[2] = carry;
+  if (bad && a.status) atomicOr(a.status, HF_S_BAD);
+  if (ctas > 0 && tid == 0) {
+    a.tile0[a.n] = carry;
+    *reinterpret_cast<AttnLine*>(a.line) = make_line(carry, a.units, ctas, heavy, prefix_places(a));
   }
 }
 
@@ -1097,18 +1022,19 @@ cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) {
                      : launch_one<64, PROMPT>(c, mq, mk, mv, grid, st);
 }
 
-cudaError_t launch_attn_plan(const AttnRows& a, int budget, int units, int first, int pre_items, cudaStream_t st) {
+cudaError_t launch_attn_plan(const AttnRows& a, int ctas, int heavy, cudaStream_t st) {
   const int checks = a.shared > 0 && a.status ? std::min(a.n, 151) : 0;
-  return launch_pdl(plan_kernel, dim3(1 + checks), dim3(1024), 0, st, a, budget, units, first, pre_items);
+  return launch_pdl(plan_kernel, dim3(1 + checks), dim3(1024), 0, st, a, ctas, heavy);
 }
 
-// Rows of a tile, blocks and items of a call over a paged cache.
-void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget) {
+void attn_tc_sizes(AttnRows& a, int& pre_items, long long& slots) {
   const int tb = 128 / a.G, heads = (a.Hkv + 1) / 2;
   const long long tokens = (long long)a.n * a.rows;
-  const long long blocks = tokens <= tb ? 1 : (tokens + 2 * tb - 1) / (2 * tb);
+  const long long blocks = (tokens + 2 * tb - 1) / (2 * tb);
   const long long per = tokens <= tb ? heads : blocks * a.Hkv;  // items of one piece of the prefix
-  units = a.rows <= tb ? heads : (a.rows + 2 * tb - 1) / (2 * tb) * a.Hkv;
+  a.tb = tb;
+  a.units = a.rows <= tb ? heads : (a.rows + 2 * tb - 1) / (2 * tb) * a.Hkv;
+  a.unit_rows = (a.rows <= tb ? 2 * a.rows : 2 * tb) * a.G;
   a.npre = 0;
   a.pre_keys = BN;
   if (a.shared > 0) {
@@ -1128,29 +1054,28 @@ void attn_tc_sizes(AttnRows& a, int& pre_items, int& units, int& budget) {
     }
   }
   pre_items = (int)(per * a.npre);
-  budget = std::max(8, (152 * 8 + units - 1) / units);
+  slots = (long long)a.units * a.n + 152;
 }
 
-cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, int units, int budget, cudaStream_t st) {
+cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t st) {
   TcArgs c{};
   c.a = a;
-  c.tb = 128 / a.G;
+  c.tb = a.tb;
   const long long tokens = (long long)a.n * a.rows, block = (long long)a.page * a.dh;
   c.blocks = (int)((tokens + 2 * c.tb - 1) / (2 * c.tb));
   c.box_rows = a.page;
   c.wide = wide_rows(a);
   c.pre_items = pre_items;
-  c.units = units;
   CUtensorMap mq, mk, mv;
   cudaError_t e = make_map_3d(&mq, a.q, a.dh, a.Hq, tokens, a.dh, a.q_ld, a.G, c.tb);
   if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
   if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
   if (e != cudaSuccess) return e;
-  const long long most = pre_items + ((long long)a.n + budget) * units;
-  const int grid = (int)std::min<long long>(most, 152);
-  c.budget = budget;
+  // (the line is at most as long as all tables reach)
+  const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;
+  const int grid = (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
   c.small = a.n <= kSmall;
-  if (!c.small) e = launch_attn_plan(a, budget, units, grid, pre_items, st);
+  if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
   if (e != cudaSuccess) return e;
   return a.dh == 128 ? launch_one<128, PAGED>(c, mq, mk, mv, dim3(grid), st)
                      : launch_one<64, PAGED>(c, mq, mk, mv, dim3(grid), st);
