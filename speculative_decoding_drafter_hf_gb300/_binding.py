@@ -682,6 +682,7 @@ class Pages:
         self.status = torch.zeros(1, dtype=i32, device=k.device)
         d.work, d.status = self._work.data_ptr(), self.status.data_ptr()
         self._d, self._ref = d, ctypes.byref(d)
+        self._i32, self._device = i32, k.device
         if ints == 0:  # let a call say what is wrong with the descriptor
             on.call(hf_pages_compact, self._ref, None)
 
@@ -701,48 +702,42 @@ class Pages:
         self.status.zero_()
         return s
 
-    def _lists(self, on, requests, n):
-        import torch
-        return None if requests is None else on.arg(requests, "requests", torch.int32, (n,))
+    def _ints(self, t, n, name):
+        """Pointer of an int32 list of n entries on the cache's device."""
+        if t is None:
+            return None
+        if t.dtype is not self._i32 or t.device != self._device or t.dim() != 1 or t.shape[0] != n or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on {self._device}")
+        return t.data_ptr()
 
     def extend(self, counts, requests=None, stream=None):
         """Room for counts[i] more tokens of requests[i] (default: request i)."""
-        import torch
-        on = _On(self.k, stream)
         n = counts.shape[0]
-        cp = on.arg(counts, "counts", torch.int32, (n,))
-        on.call(hf_pages_extend, self._ref, self._lists(on, requests, n), cp, n)
+        _On(self.k, stream).call(hf_pages_extend, self._ref, self._ints(requests, n, "requests"),
+                                 self._ints(counts, n, "counts"), n)
 
     def truncate(self, keep, requests=None, stream=None):
         """Cut requests[i] to keep[i] tokens; 0 frees it."""
-        import torch
-        on = _On(self.k, stream)
         n = keep.shape[0]
-        kp = on.arg(keep, "keep", torch.int32, (n,))
-        on.call(hf_pages_truncate, self._ref, self._lists(on, requests, n), kp, n)
+        _On(self.k, stream).call(hf_pages_truncate, self._ref, self._ints(requests, n, "requests"),
+                                 self._ints(keep, n, "keep"), n)
 
     def fork(self, source, into, stream=None):
         """Requests into[i] (empty) share all tokens of source[i]."""
-        import torch
-        on = _On(self.k, stream)
         n = into.shape[0]
-        sp = on.arg(source, "source", torch.int32, (n,))
-        ip = on.arg(into, "into", torch.int32, (n,))
-        on.call(hf_pages_fork, self._ref, sp, ip, n)
+        _On(self.k, stream).call(hf_pages_fork, self._ref, self._ints(source, n, "source"),
+                                 self._ints(into, n, "into"), n)
 
     def compact(self, n_used=None, stream=None):
         """Move the pages in use to the front of the pool; n_used int32 [1] receives
         their number."""
-        import torch
-        on = _On(self.k, stream)
-        up = None if n_used is None else on.arg(n_used, "n_used", torch.int32, (1,))
-        on.call(hf_pages_compact, self._ref, up)
+        _On(self.k, stream).call(hf_pages_compact, self._ref, self._ints(n_used, 1, "n_used"))
 
     def write(self, k, v, offsets, requests=None, layer=None, stream=None):
         """The newest rows of the requests: k and v [layers, T, kv heads, head_dim]
         for layers 0 .. layers - 1, or [T, kv heads, head_dim] with `layer`; entry i's
         rows are offsets[i] .. offsets[i + 1] - 1."""
-        import torch
         on = _On(self.k, stream)
         L, _, hkv, _, dh = self.k.shape
         if k.dim() != (4 if layer is None else 3) or tuple(k.shape[-2:]) != (hkv, dh) or (layer is None and k.shape[0] > L):
@@ -755,9 +750,9 @@ class Pages:
         if T and (_heads_ld(v, "v") != ld or (step and v.stride(0) != step)):
             raise ValueError("k and v must have the same strides")
         n = offsets.shape[0] - 1
-        op = on.arg(offsets, "offsets", torch.int32, (n + 1,))
+        op = self._ints(offsets, n + 1, "offsets")
         on.call(hf_pages_write, self._ref, layer or 0, k.shape[0] if layer is None else 1, kp, vp, ld, step,
-                self._lists(on, requests, n), op, n, T)
+                self._ints(requests, n, "requests"), op, n, T)
 
     def attend_workspace(self, q, shared=0):
         """A workspace for attend with queries of this shape."""
@@ -793,6 +788,6 @@ class Pages:
             b = hf_attention_pages_workspace(self._ref, n, rows, hq, shared)
             workspace = on.empty((max(b, 16),), torch.uint8)
         wp = on.arg(workspace, "workspace", torch.uint8)
-        on.call(hf_attention_pages, self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._lists(on, requests, n),
+        on.call(hf_attention_pages, self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._ints(requests, n, "requests"),
                 shared, float(scale or 0.0), op, ld(out, "out"), wp, workspace.numel())
         return out

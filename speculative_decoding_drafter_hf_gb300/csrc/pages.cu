@@ -10,7 +10,7 @@
 // works on its share of the table entries; the last CTA (ticket in work[0], left
 // at zero) writes the lengths that the others still read. extend and compact:
 // one CTA plans (prefix sums over the lists and over refs), then a wide launch
-// moves the pages. write: one warp per (row, layer, K or V).
+// moves the pages. write: one warp per row and a few layers of it.
 #include <cstdio>
 
 #include "pages.cuh"
@@ -189,79 +189,96 @@ __global__ void __launch_bounds__(CT) fork_kernel(hf_pages p, const int32_t* fro
 }
 
 // -------------------------------------------------------------------- extend
-// One CTA. Request i needs `copy` (0 or 1: its partly filled last page is held
-// by others) + new pages; ranks over the list give each its place in the order of
-// the free pages. The free pages themselves are ranked by scanning refs.
+// One CTA. Entry i needs `copy` (0 or 1: its partly filled last page is held by
+// others) + new pages; ranks over the list give each its place in the order of the free
+// pages, which come from scanning refs. Bound by the latency of its dependent loads: the
+// list's are made once and kept, the first 8192 counts are on their way meanwhile, and the
+// order of the free pages stays in shared memory as far as it fits.
 __global__ void __launch_bounds__(PT) extend_plan(hf_pages p, const int32_t* req, const int32_t* counts, int n) {
-  constexpr int PER = kMaxRequests / PT;
+  constexpr int PER = kMaxRequests / PT, NEAR = 4096;
+  __shared__ int32_t s_free[NEAR];
   const int tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
   int32_t* src = p.work + kMoves;
   int32_t* dst = src + move_room(p);
-  bool full = false;
-  bool ok = list_ok(p, req, nullptr, n, [&](int i, int r) {
-    const int c = __ldcg(&counts[i]), len = __ldcg(&p.lens[r]);
-    if (c < 0 || len < 0) return false;
-    if ((long long)len + c > (long long)p.table_ld * p.page) full = true;
-    return true;
-  });
-  // entries i = tid * PER + k, in list order
-  int need[PER], copy[PER], mine = 0, copies = 0;
-  if (ok) {
+  auto free_bits = [&](int b0) {
+    uint32_t bits = 0;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int i = tid * PER + k;
-      need[k] = copy[k] = 0;
-      if (i >= n) continue;
-      const int r = req ? __ldcg(&req[i]) : i, c = __ldcg(&counts[i]), len = __ldcg(&p.lens[r]);
-      if (c == 0 || (long long)len + c > (long long)p.table_ld * p.page) continue;
-      const int have = pages_of(len, p.page);
-      need[k] = pages_of(len + c, p.page) - have;
-      if (len % p.page) {
-        const int id = __ldcg(&p.table[(size_t)r * p.table_ld + have - 1]);
-        if (id < 0 || id >= p.n_pages)
-          ok = false;
-        else
-          copy[k] = __ldcg(&p.refs[id]) > 1;
-      }
-      need[k] += copy[k];
-      mine += need[k];
-      copies += copy[k];
+    for (int k = 0; k < 8; ++k)
+      if (b0 + k < p.n_pages && __ldcg(&p.refs[b0 + k]) == 0) bits |= 1u << k;
+    return bits;
+  };
+  uint32_t is_free = free_bits(tid * 8);
+  bool full = false, ok = true;
+  // entries i = tid * per + k, in list order
+  const int per = (n + PT - 1) / PT;
+  int req_[PER], len_[PER], cnt_[PER], last_[PER], need[PER], copy[PER], mine = 0, copies = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = tid * per + k;
+    req_[k] = -1;
+    need[k] = copy[k] = len_[k] = cnt_[k] = 0;
+    last_[k] = -1;
+    if (k >= per || i >= n) continue;
+    const int r = req ? __ldcg(&req[i]) : i, c = __ldcg(&counts[i]);
+    if (r < 0 || r >= p.n_requests || c < 0) {
+      ok = false;
+      continue;
     }
+    const int len = __ldcg(&p.lens[r]);
+    if (len < 0) {
+      ok = false;
+      continue;
+    }
+    req_[k] = r;
+    len_[k] = len;
+    cnt_[k] = c;
+    if ((long long)len + c > (long long)p.table_ld * p.page) {
+      full = true;
+      continue;
+    }
+    if (c == 0) continue;
+    const int have = pages_of(len, p.page);
+    need[k] = pages_of(len + c, p.page) - have;
+    if (len % p.page) {
+      const int id = __ldcg(&p.table[(size_t)r * p.table_ld + have - 1]);
+      if (id < 0 || id >= p.n_pages)
+        ok = false;
+      else
+        copy[k] = __ldcg(&p.refs[id]) > 1;
+      last_[k] = id;
+    }
+    need[k] += copy[k];
+    mine += need[k];
+    copies += copy[k];
   }
-  ok = __syncthreads_and(ok);
+  // (checks the list for repeats)
+  ok = list_ok(p, req, nullptr, n, [&](int, int) { return true; }) && __syncthreads_and(ok);
   full = __syncthreads_or(full);
   int total = 0, ncopy = 0, at = 0, cat = 0;
   if (ok && !full) {
     at = cta_scan(mine, total);
     cat = cta_scan(copies, ncopy);
-    // the free pages among the first ones, until enough are found; each thread
-    // looks at 8 neighbouring pages a step
+    // the free pages among the first ones, until enough are found; each thread looks at 8
+    // neighbouring pages a step
     int found = 0;
     for (int base = 0; base < p.n_pages && found < total; base += PT * 8) {
       const int b0 = base + tid * 8;
-      int c = 0;
-      uint32_t is_free = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (b0 + k < p.n_pages && __ldcg(&p.refs[b0 + k]) == 0) {
-          is_free |= 1u << k;
-          ++c;
-        }
+      if (base) is_free = free_bits(b0);
       int sum;
-      int rank = found + cta_scan(c, sum);
+      int rank = found + cta_scan(__popc(is_free), sum);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (is_free >> k & 1) {
-          if (rank < total) dst[rank] = b0 + k;  // the order of free pages
+          if (rank < total) (rank < NEAR ? s_free : dst)[rank] = b0 + k;  // the order of free pages
           ++rank;
         }
       found += sum;
     }
     full = found < total;
   }
-  __syncthreads();  // dst written by all threads of this CTA
+  __syncthreads();  // the order has been written by all threads of this CTA
   if (!ok || full) {
     if (tid == 0) {
       p.work[1] = 0;
@@ -269,37 +286,34 @@ __global__ void __launch_bounds__(PT) extend_plan(hf_pages p, const int32_t* req
     }
     return;
   }
-  // a request's copy comes first, then its new pages
-  int cdst[PER], csrc[PER];
+  auto page_at = [&](int rank) { return rank < NEAR ? s_free[rank] : dst[rank]; };
+  // an entry's copy comes first, then its new pages
+  int cdst[PER];
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    const int i = tid * PER + k;
     cdst[k] = -1;
-    csrc[k] = -1;
-    if (i >= n) continue;
-    const int r = req ? __ldcg(&req[i]) : i, c = __ldcg(&counts[i]), len = __ldcg(&p.lens[r]);
-    const int have = pages_of(len, p.page);
-    int32_t* row = p.table + (size_t)r * p.table_ld;
+    if (req_[k] < 0 || cnt_[k] == 0) continue;
+    const int have = pages_of(len_[k], p.page);
+    int32_t* row = p.table + (size_t)req_[k] * p.table_ld;
     if (copy[k]) {
-      csrc[k] = row[have - 1];
-      cdst[k] = dst[at];
+      cdst[k] = page_at(at);
       row[have - 1] = cdst[k];
       p.refs[cdst[k]] = 1;
-      atomicSub(&p.refs[csrc[k]], 1);
+      atomicSub(&p.refs[last_[k]], 1);
     }
     for (int j = copy[k]; j < need[k]; ++j) {
-      const int id = dst[at + j];
+      const int id = page_at(at + j);
       row[have + j - copy[k]] = id;
       p.refs[id] = 1;
     }
     at += need[k];
-    p.lens[r] = len + c;
+    p.lens[req_[k]] = len_[k] + cnt_[k];
   }
   __syncthreads();  // the order of free pages has been read: the moves take its place
 #pragma unroll
   for (int k = 0; k < PER; ++k)
     if (cdst[k] >= 0) {
-      src[cat] = csrc[k];
+      src[cat] = last_[k];
       dst[cat] = cdst[k];
       ++cat;
     }
@@ -432,40 +446,50 @@ struct WriteArgs {
   int n, total, layer, layers;
 };
 
-// One warp per (row, layer, K or V): heads * head_dim elements go to as many
-// places of head_dim elements as there are heads.
+// The last index in [0, n) whose offset is at or before t (offsets rise), by one warp: 32
+// of them are looked at side by side, so that three dependent loads do for 4096.
+__device__ __forceinline__ int find_entry(const int32_t* off, int n, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, count = n;
+  while (count > 1) {
+    const int step = (count + 31) / 32, i = lane * step;
+    const bool before = i < count && __ldcg(&off[lo + i]) <= t;
+    const int k = max(0, 31 - __clz(__ballot_sync(0xffffffffu, before)));
+    lo += k * step;
+    count = min(step, count - k * step);
+  }
+  return lo;
+}
+
+// One warp per row and up to kCopies of its (layer, K or V): heads * head_dim elements go
+// to as many places of head_dim elements as there are heads. Small calls are bound by the
+// dependent look-ups, so they are made once for several copies; large ones by the copies.
+constexpr int kCopies = 8;
 __global__ void __launch_bounds__(CT) write_kernel(hf_pages p, WriteArgs a) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long units = (long long)a.total * a.layers * 2;
+  const int groups = (2 * a.layers + kCopies - 1) / kCopies;
+  const long long units = (long long)a.total * groups;
   const int esize = p.dtype == HF_F32 ? 4 : 2;
   const int hv = p.head_dim * esize / 16, vecs = p.n_kv_heads * hv;  // 16-byte pieces of a head, of a row
   const long long block = (long long)p.n_kv_heads * p.page * hv;
+  const int first = __ldcg(&a.off[0]), end = __ldcg(&a.off[a.n]);
   for (long long u = (long long)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < units;
        u += (long long)gridDim.x * (CT / 32)) {
-    const int kv = (int)(u & 1);
-    const int layer = (int)((u >> 1) % a.layers), t = (int)((u >> 1) / a.layers);
-    const int end = __ldcg(&a.off[a.n]);
-    if (t < __ldcg(&a.off[0]) || t >= end) continue;
-    int lo = 0, hi = a.n;  // the last entry that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldcg(&a.off[mid]) <= t)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int o1 = __ldcg(&a.off[lo + 1]), r = a.req ? __ldcg(&a.req[lo]) : lo;
-    bool ok = t < o1 && end <= a.total && r >= 0 && r < p.n_requests;
+    const int t = (int)(u / groups), c0 = (int)(u % groups) * kCopies;
+    if (t < first || t >= end) continue;
+    const int e = find_entry(a.off, a.n, t);
+    const int o0 = __ldcg(&a.off[e]), o1 = __ldcg(&a.off[e + 1]), r = a.req ? __ldcg(&a.req[e]) : e;
+    bool ok = t >= o0 && t < o1 && end <= a.total && r >= 0 && r < p.n_requests;
     if (a.req)  // named twice: its rows would have two sources
-      for (int i = lane; i < a.n; i += 32) ok = ok && (i == lo || __ldcg(&a.req[i]) != r);
+      for (int i = lane; i < a.n; i += 32) ok = ok && (i == e || __ldcg(&a.req[i]) != r);
     ok = __all_sync(0xffffffffu, ok);
     int id = -1, at = -1;
     if (ok) {
       const int len = __ldcg(&p.lens[r]);
       at = len - o1 + t;
-      ok = at >= 0 && len - o1 + __ldcg(&a.off[lo]) >= 0 && at / p.page < p.table_ld;
+      ok = at >= 0 && len - o1 + o0 >= 0 && at / p.page < p.table_ld;
       if (ok) id = __ldcg(&p.table[(size_t)r * p.table_ld + at / p.page]);
       ok = ok && id >= 0 && id < p.n_pages;
     }
@@ -473,10 +497,25 @@ __global__ void __launch_bounds__(CT) write_kernel(hf_pages p, WriteArgs a) {
       if (lane == 0) flag(p, HF_S_BAD);
       continue;
     }
-    const uint4* s = reinterpret_cast<const uint4*>((kv ? a.v : a.k) + (long long)layer * a.layer_stride + t * a.ld);
-    uint4* d = reinterpret_cast<uint4*>(kv ? p.v : p.k) +
-               ((long long)(a.layer + layer) * p.n_pages + id) * block + (long long)(at % p.page) * hv;
-    for (int i = lane; i < vecs; i += 32) d[(long long)(i / hv) * p.page * hv + i % hv] = __ldcs(s + i);
+    const long long row = (long long)t * a.ld;
+    const long long to = (long long)id * block + (long long)(at % p.page) * hv;
+    const int c1 = min(c0 + kCopies, 2 * a.layers);
+    for (int i = lane; i < vecs; i += 32) {
+      const long long d = to + (long long)(i / hv) * p.page * hv + i % hv;
+      uint4 x[kCopies];
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k)
+        if (c0 + k < c1) {
+          const int c = c0 + k;
+          x[k] = __ldcs(reinterpret_cast<const uint4*>((c & 1 ? a.v : a.k) + (long long)(c >> 1) * a.layer_stride + row) + i);
+        }
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k)
+        if (c0 + k < c1) {
+          const int c = c0 + k;
+          (reinterpret_cast<uint4*>(c & 1 ? p.v : p.k) + (long long)(a.layer + (c >> 1)) * p.n_pages * block)[d] = x[k];
+        }
+    }
   }
 }
 
@@ -583,7 +622,7 @@ extern "C" hf_status hf_pages_write(const hf_pages* p, int32_t layer, int32_t la
   a.total = total;
   a.layer = layer;
   a.layers = layers;
-  const long long warps = (long long)total * layers * 2;
+  const long long warps = (long long)total * ((2 * layers + kCopies - 1) / kCopies);
   const long long grid = std::min<long long>((warps + CT / 32 - 1) / (CT / 32), 152 * 8);
   return done(launch_pdl(write_kernel, dim3((unsigned)grid), dim3(CT), 0, (cudaStream_t)stream, *p, a));
 }

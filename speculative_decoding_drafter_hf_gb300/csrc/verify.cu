@@ -226,6 +226,18 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   const bool range_ok = temp_ok(t) && nd >= 0 && nd <= S;
   const bool cold = t == 0.f;
   const float c = cold ? 0.f : 1.4426950408889634f / t;
+  // the drafts, their logits and the slots' random numbers: on their way while the
+  // statistics are joined (warp 0, lane = slot)
+  const bool has = warp == 0 && range_ok && lane < nd;
+  int d = 0;
+  float xv = 0.f, yv = 0.f, uv = 0.f;
+  if (has) d = __ldg(&a.tok[(size_t)b * S + lane]);
+  const bool names = d >= 0 && d < a.V;
+  if (has && names && !cold) {
+    uv = __ldg(&a.u[(size_t)b * S + lane]);
+    xv = to_f(static_cast<const TX*>(a.x)[((size_t)b * (S + 1) + lane) * a.x_ld + d]);
+    if (a.y) yv = to_f(static_cast<const TY*>(a.y)[((size_t)b * S + lane) * a.y_ld + d]);
+  }
   if (range_ok) {
     for (int r = warp; r < 2 * S + 1; r += VT / 32) {
       if (r <= S ? r > nd : (cold || !a.y || r - S - 1 >= nd)) continue;
@@ -258,9 +270,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
     // lane s tests slot s; the first that fails is the stop slot
     bool bad = !range_ok, pass = false, row_bad = false;
     if (!bad && lane <= nd) {
-      const bool has = lane < nd;
-      const int d = has ? __ldg(&a.tok[(size_t)b * S + lane]) : 0;
-      if (d < 0 || d >= a.V) {
+      if (!names) {
         row_bad = true;
       } else if (cold) {
         const int idx = __float_as_int(sl[lane]);
@@ -272,23 +282,16 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
         if (has && a.y) {
           const float lq = sl[S + 1 + lane];
           row_bad = row_bad || !(lq > 0.f && lq < INFINITY);
-          const float yv = to_f(static_cast<const TY*>(a.y)[((size_t)b * S + lane) * a.y_ld + d]);
           q = ex2((yv - sm[S + 1 + lane]) * c) / lq;
         }
-        const float xv = to_f(static_cast<const TX*>(a.x)[((size_t)b * (S + 1) + lane) * a.x_ld + d]);
-        const float p = ex2((xv - sm[lane]) * c) / sl[lane];
-        pass = has && !row_bad && __ldg(&a.u[(size_t)b * S + lane]) * q < p;
+        pass = has && !row_bad && uv * q < ex2((xv - sm[lane]) * c) / sl[lane];
       }
     }
     const unsigned fails = ~__ballot_sync(0xffffffffu, pass);
     const unsigned bads = __ballot_sync(0xffffffffu, row_bad);
     // a draft that names no token is refused wherever it stands
     const int stop = __ffs(fails) - 1;
-    bool tok_bad = false;
-    if (range_ok && lane < nd) {
-      const int d = __ldg(&a.tok[(size_t)b * S + lane]);
-      tok_bad = d < 0 || d >= a.V;
-    }
+    bool tok_bad = has && !names;
     tok_bad = __any_sync(0xffffffffu, tok_bad);
     if (lane == 0) {
       s_stop = stop;
@@ -397,10 +400,11 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   }
 }
 
-// Chunk of the vocabulary per CTA: enough CTAs to fill the GPU several times
-// over, at least 2048 entries (8 per thread) each.
-int chunk_for(long long rows, int V, int least) {
-  const long long want = (152 * 16 + rows - 1) / rows;  // CTAs per row
+// Chunk of the vocabulary per CTA: about `per_sm` CTAs per SM in all (statistics: several
+// rounds of small CTAs; race: one round, since every CTA first joins its request's
+// statistics, which measured 4 us), at least `least` entries each.
+int chunk_for(long long rows, int V, int least, int per_sm) {
+  const long long want = (152 * per_sm + rows - 1) / rows;  // CTAs per row
   const long long c = (V + want - 1) / want;
   return (int)std::max<long long>(least, std::min<long long>((c + 1023) / 1024 * 1024, 32768));
 }
@@ -412,9 +416,9 @@ struct VPlan {
 
 VPlan plan_for(int B, int S, int V) {
   VPlan p{};
-  p.chunk = chunk_for((long long)B * (S + 1), V, 2048);
+  p.chunk = chunk_for((long long)B * (S + 1), V, 2048, 16);
   p.nchunk = (V + p.chunk - 1) / p.chunk;
-  p.rchunk = chunk_for(B, V, 1024);
+  p.rchunk = chunk_for(B, V, 1024, 6);
   p.nrchunk = (V + p.rchunk - 1) / p.rchunk;
   p.stats = 0;
   p.race = (p.stats + (size_t)B * (2 * S + 1) * p.nchunk * sizeof(float2) + 15) / 16 * 16;
