@@ -188,8 +188,7 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t 
 cudaError_t launch_attn_plan(const AttnRows& a, int ctas, int heavy, cudaStream_t st);
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
-cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st);
-cudaError_t launch_attn_rows_own(int dtype, const AttnRows& a, cudaStream_t st);
+cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st);
 // `pieces`: about how many a row has (how many warps share a row).
 cudaError_t launch_attn_join(int dtype, const AttnRows& a, int pieces, cudaStream_t st);
 

@@ -5,14 +5,17 @@
 // over the keys j < limit_i, in one pass over the keys: a tile's scores raise the
 // running maximum m_i, and what was summed so far is scaled by 2^(old m - new m).
 //
-// A CTA takes 32 rows of one KV head and walks its keys in tiles of 64: 8 x 16
-// threads, 4 x 4 scores each, then the same 4 rows times the value columns 4 tx +
-// 64 c. Everything is fp32 in shared memory and registers (fp32 inputs: the next tile
-// comes in by asynchronous copies meanwhile): this is the variant for fp32 inputs and
-// for head dims that the tensor-core kernels do not take; bound by the fp32
-// multiply-adds. A prompt's rows are few for the GPU and their keys many: a cluster of
-// four CTAs shares a tile of rows, each walking every fourth tile of keys, and joins
-// the parts through distributed shared memory.
+// A CTA takes 8 RPT rows of one KV head and walks its keys in tiles of 64: 8 x 16
+// threads, RPT x 4 scores each, then the same rows times the value columns 4 tx + 64 c.
+// Everything is fp32 in shared memory and registers: this is the variant for fp32 inputs
+// and for head dims that the tensor-core kernels do not take; bound by the fp32
+// multiply-adds and the shared-memory reads that feed them (RPT = 8: 128 multiply-adds
+// for 12 reads), which is why several CTAs per SM rather than two tiles in flight hide
+// the loads (8 prompts of 100 to 1201 tokens, heads of 64: two tiles in flight, two CTAs
+// per SM, RPT = 4 measured 103 us, one tile and four CTAs 75 us). A prompt's rows are
+// few for the GPU and their keys many: a cluster of four CTAs shares a tile of rows, each
+// walking every fourth tile of keys, and joins the parts through distributed shared
+// memory. Over a paged cache, RPT goes by the rows of a request.
 //
 // Masked keys: scores are selected, never added to a mask value, so whatever K
 // holds there cannot matter; V's non-finite values in a tile that any row masks
@@ -32,15 +35,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int BM = 32, BN = 64, RT = 128;
+constexpr int BN = 64, RT = 128;
 constexpr int PLD = BN + 4;
 constexpr int CLUSTER = 4;  // CTAs that share a prompt's tile of rows
-enum { PROMPT = 0, PREFIX = 1, OWN = 2 };
+enum { PROMPT = 0, PAGED = 1 };
 
-// K and V tiles in flight: two where they fit
-__host__ __device__ inline int rows_stages(int dh, int esize) { return esize == 4 && dh <= 128 ? 2 : 1; }
-__host__ __device__ inline size_t rows_smem(int dh, int esize) {
-  return ((size_t)(BM + 2 * BN * rows_stages(dh, esize)) * (dh + 4) + (size_t)BM * PLD) * sizeof(float);
+__host__ __device__ inline size_t rows_smem(int dh, int bm) {
+  return ((size_t)(bm + 2 * BN) * (dh + 4) + (size_t)bm * PLD) * sizeof(float);
 }
 
 // 16 bytes to shared memory, zeros where there is nothing to read.
@@ -74,16 +75,17 @@ __device__ __forceinline__ long long key_at(const AttnRows& a, int start, const 
   return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
 }
 
-// DHT: the head dim, or 0 for any up to 64 * MAXC.
-template <typename T, int MODE, int MAXC, int DHT>
-__global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
+// DHT: the head dim, or 0 for any up to 64 * MAXC. pre_x: CTAs (paged) of the prefix.
+template <typename T, int MODE, int MAXC, int DHT, int RPT>
+__global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
   extern __shared__ __align__(16) float smf[];
   constexpr bool F32 = sizeof(T) == 4;
+  constexpr int BM = 8 * RPT;
   const int dh = DHT ? DHT : a.dh, ldq = dh + 4, c4 = dh / 4;
-  const int stages = rows_stages(dh, (int)sizeof(T));
   float* sq = smf;
-  float* skv = sq + BM * ldq;  // K, V of one stage, then of the next
-  float* sp = skv + 2 * BN * ldq * stages;
+  float* sk = sq + BM * ldq;
+  float* sv = sk + BN * ldq;
+  float* sp = sv + BN * ldq;
   __shared__ int s_odd, s_low;
   __shared__ float2 s_ml[BM];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
   const int g = blockIdx.y;
   int row0, nrows, j0 = 0, j1, start = 0, entry = 0, piece = 0, len = 0;
   const int32_t* tab = nullptr;
+  const bool pre = MODE == PAGED && (int)blockIdx.x < pre_x;
   if (MODE == PROMPT) {
     if (blockIdx.x == 0 && g == 0) check_offsets(a);
     const PromptTile t = prompt_tile(a, (int)((gridDim.x - 1 - blockIdx.x) / CL), BM, a.G);
@@ -104,10 +107,10 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     row0 = t.tile * BM;
     nrows = (int)min((long long)BM, (long long)t.len * a.G - row0);
     j1 = (row0 + nrows - 1) / a.G + 1;
-  } else if (MODE == PREFIX) {
-    row0 = blockIdx.x * BM;
+  } else if (pre) {
+    piece = blockIdx.x % a.npre;
+    row0 = blockIdx.x / a.npre * BM;
     nrows = min(BM, a.n * a.rows * a.G - row0);
-    piece = blockIdx.z;
     j0 = piece * a.pre_keys;
     j1 = min(a.shared, j0 + a.pre_keys);
     if (__ldcg(&a.eff[0]) == 0)  // nothing is shared then: every row is empty
@@ -115,21 +118,23 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     else
       tab = attn_table(a, 0);
   } else {
-    const int blocks = (a.rows * a.G + BM - 1) / BM;
-    entry = blockIdx.x / blocks;
-    row0 = (blockIdx.x % blocks) * BM;
+    const int x = blockIdx.x - pre_x, blocks = (a.rows * a.G + BM - 1) / BM;
+    piece = x % a.nown;
+    entry = x / a.nown / blocks;
+    row0 = x / a.nown % blocks * BM;
     nrows = min(BM, a.rows * a.G - row0);
-    piece = blockIdx.z;
     len = __ldcg(&a.eff[entry]);
-    j0 = a.shared + blockIdx.z * a.own_keys;
+    j0 = a.shared + piece * a.own_keys;
     j1 = min(len, j0 + a.own_keys);
-    if (blockIdx.z > 0 && j0 >= j1) return;  // piece 0 always reports (a direct call has no other)
+    if (piece > 0 && j0 >= j1) return;  // piece 0 always reports (a direct call has no other)
     if (len > 0) tab = attn_table(a, entry);
   }
+  // token row of q and out of the item's row rr, and its query head
+  auto token = [&](int rr) { return (size_t)(MODE == PROMPT ? start : pre ? 0 : entry * a.rows) + rr / a.G; };
+  auto head = [&](int rr) { return g * a.G + rr % a.G; };
 
-  // K and V of the keys from jt on into a stage
-  auto load = [&](int stage, int jt) {
-    float* dst = skv + stage * 2 * BN * ldq;
+  // K and V of the keys from jt on
+  auto load = [&](int jt) {
     constexpr int U = 8;
     for (int e0 = tid; e0 < 2 * BN * c4; e0 += RT * U) {
       float4 x[U];
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
         if (at == -1 && a.status) atomicOr(a.status, HF_S_BAD);
         const T* src = static_cast<const T*>(kv ? a.v : a.k) + (at < 0 ? 0 : at + c);
         if constexpr (F32)
-          copy16(&dst[(kv * BN + j) * ldq + c], src, at >= 0);
+          copy16(&sk[(kv * BN + j) * ldq + c], src, at >= 0);
         else
           x[u] = at >= 0 ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -152,92 +157,68 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
           const int e = e0 + u * RT;
           if (e >= 2 * BN * c4) continue;
           const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
-          *reinterpret_cast<float4*>(&dst[(kv * BN + j) * ldq + c]) = x[u];
+          *reinterpret_cast<float4*>(&sk[(kv * BN + j) * ldq + c]) = x[u];
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int first = j0 + rank * BN;
-  if (stages == 2 && first < j1) load(0, first);
+  if (first < j1) load(first);
 
-  // this thread's rows: keys they see, and where they come from and go to
-  int limit[4], head[4];
-  size_t orow[4];  // token row of q and out
+  // this thread's rows: the keys they see
+  int limit[RPT];
   if (tid == 0) {
     s_odd = j1;
     s_low = 0x7fffffff;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rr = row0 + ty * 4 + i;
+  for (int i = 0; i < RPT; ++i) {
     limit[i] = 0;
-    orow[i] = 0;
-    head[i] = 0;
-    if (ty * 4 + i >= nrows) continue;
-    const int t = rr / a.G;
-    head[i] = g * a.G + rr % a.G;
+    if (ty * RPT + i >= nrows) continue;
+    const int t = (row0 + ty * RPT + i) / a.G;
     bool dead = false;
     if (MODE == PROMPT) {
       limit[i] = t + 1;
-      orow[i] = (size_t)start + t;
-    } else if (MODE == PREFIX) {
+    } else if (pre) {
       const int l = __ldcg(&a.eff[t / a.rows]);
       dead = l == 0;
       limit[i] = max(0, min(a.shared, l - a.rows + t % a.rows + 1));
-      orow[i] = t;
     } else {
       limit[i] = max(0, len - a.rows + t + 1);
-      orow[i] = (size_t)entry * a.rows + t;
     }
     if (tx == 0 && !dead) atomicMin(&s_low, limit[i]);
   }
   for (int e = tid; e < BM * c4; e += RT) {
     const int r = e / c4, c = (e % c4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < nrows) {
-      const int rr = row0 + r, t = rr / a.G;
-      const size_t qr = MODE == PROMPT ? (size_t)start + t : MODE == PREFIX ? (size_t)t : (size_t)entry * a.rows + t;
-      x = load4(static_cast<const T*>(a.q) + qr * a.q_ld + (size_t)(g * a.G + rr % a.G) * dh + c);
-    }
+    if (r < nrows)
+      x = load4(static_cast<const T*>(a.q) + token(row0 + r) * a.q_ld + (size_t)head(row0 + r) * dh + c);
     *reinterpret_cast<float4*>(&sq[r * ldq + c]) =
         make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
   }
   __syncthreads();
   const int low = s_low;
 
-  float m[4], l[4], o[4][MAXC * 4];
+  float m[RPT], l[RPT], o[RPT][MAXC * 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RPT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
     for (int c = 0; c < MAXC * 4; ++c) o[i][c] = 0.f;
   }
 
-  int stage = 0;
   for (int jt = first; jt < j1; jt += CL * BN) {
-    const int next = jt + CL * BN;
-    if (stages == 2) {
-      if (next < j1) {
-        load(stage ^ 1, next);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
-    } else {
-      load(0, jt);
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
+    if (jt != first) load(jt);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    float* sk = skv + stage * 2 * BN * ldq;
-    float* sv = sk + BN * ldq;
-    if (stages == 2) stage ^= 1;
-    // some row masks keys of this tile: its odd values of V are set aside
+    // some row masks keys of this tile: the odd values of V there are set aside
     if (low < min(jt + BN, j1)) {
-      for (int e = tid; e < BN * dh; e += RT) {
-        float* x = &sv[(e / dh) * ldq + e % dh];
+      const int k0 = max(0, low - jt);
+      for (int e = tid; e < (BN - k0) * dh; e += RT) {
+        float* x = &sv[(k0 + e / dh) * ldq + e % dh];
         if (odd_value(*x)) {
           *x = 0.f;
           atomicMin(&s_odd, jt);
@@ -246,26 +227,26 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
       __syncthreads();
     }
 
-    float s[4][4];
+    float s[RPT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
     for (int d = 0; d < dh; d += 4) {
-      float4 qv[4], kv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sq[(ty * 4 + i) * ldq + d]);
+      float4 kv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sk[(tx + 16 * j) * ldq + d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RPT; ++i) {
+        const float4 qv = *reinterpret_cast<const float4*>(&sq[(ty * RPT + i) * ldq + d]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, s[i][j]))));
+          s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       const int lim = min(limit[i], j1);
       float t = -INFINITY;
 #pragma unroll
@@ -283,7 +264,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
       for (int j = 0; j < 4; ++j) {
         const float e = exp2f(s[i][j] - base);
         sum += e;
-        sp[(ty * 4 + i) * PLD + tx + 16 * j] = e;
+        sp[(ty * RPT + i) * PLD + tx + 16 * j] = e;
       }
       l[i] = l[i] * f + sum;  // this thread's columns; joined at the end
       m[i] = nm;
@@ -291,11 +272,11 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
       for (int c = 0; c < MAXC * 4; ++c) o[i][c] *= f;
     }
     __syncwarp();  // a row's 16 threads are in one warp
-#pragma unroll 4
+#pragma unroll 2
     for (int j = 0; j < BN; j += 4) {
-      float4 p[4];
+      float4 p[RPT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&sp[(ty * 4 + i) * PLD + j]);
+      for (int i = 0; i < RPT; ++i) p[i] = *reinterpret_cast<const float4*>(&sp[(ty * RPT + i) * PLD + j]);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
@@ -303,7 +284,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
           if (tx * 4 + 64 * c >= dh) continue;
           const float4 x = *reinterpret_cast<const float4*>(&sv[(j + jj) * ldq + tx * 4 + 64 * c]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < RPT; ++i) {
             const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
             o[i][4 * c + 0] = fmaf(w, x.x, o[i][4 * c + 0]);
             o[i][4 * c + 1] = fmaf(w, x.y, o[i][4 * c + 1]);
@@ -315,70 +296,74 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
     __syncthreads();  // the tile has been read
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RPT; ++i)
 #pragma unroll
     for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
 
   int odd_from = s_odd;
   if constexpr (CL > 1) {
-    // the cluster's parts meet in the first CTA's place: each CTA shows its sums where its
-    // tiles were, and joins a quarter of the rows (thread rows i = rank)
+    // each CTA shows its sums where its tiles were, and joins a quarter of the rows: those
+    // with i % 4 = its rank
     cg::cluster_group cluster = cg::this_cluster();
-    float* so = skv;
+    float* so = sk;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (tx == 0) s_ml[ty * 4 + i] = make_float2(m[i], l[i]);
+    for (int i = 0; i < RPT; ++i) {
+      if (tx == 0) s_ml[ty * RPT + i] = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < MAXC; ++c)
         if (tx * 4 + 64 * c < dh)
-          *reinterpret_cast<float4*>(&so[(ty * 4 + i) * ldq + tx * 4 + 64 * c]) =
+          *reinterpret_cast<float4*>(&so[(ty * RPT + i) * ldq + tx * 4 + 64 * c]) =
               make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
     }
     cluster.sync();
-    const int r = ty * 4 + rank;
-    float2 ml[CL];
-    float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < CL; ++k) {
-      ml[k] = *cluster.map_shared_rank(&s_ml[r], k);
-      odd_from = min(odd_from, *cluster.map_shared_rank(&s_odd, k));
-      top = fmaxf(top, ml[k].x);
-    }
-    const float base = top > -INFINITY ? top : 0.f;
-    float sum = 0.f, v[MAXC * 4];
+    for (int k = 0; k < CL; ++k) odd_from = min(odd_from, *cluster.map_shared_rank(&s_odd, k));
 #pragma unroll
-    for (int c = 0; c < MAXC * 4; ++c) v[c] = 0.f;
+    for (int i0 = 0; i0 < RPT; i0 += CL) {
+      const int r = ty * RPT + i0 + rank;
+      float2 ml[CL];
+      float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < CL; ++k) {
-      if (ml[k].y == 0.f) continue;
-      const float w = exp2f(ml[k].x - base);
-      sum += ml[k].y * w;
-      const float* src = cluster.map_shared_rank(so, k);
+      for (int k = 0; k < CL; ++k) {
+        ml[k] = *cluster.map_shared_rank(&s_ml[r], k);
+        top = fmaxf(top, ml[k].x);
+      }
+      const float base = top > -INFINITY ? top : 0.f;
+      float sum = 0.f, v[MAXC * 4];
 #pragma unroll
-      for (int c = 0; c < MAXC; ++c)
-        if (tx * 4 + 64 * c < dh) {
-          const float4 x = *reinterpret_cast<const float4*>(&src[r * ldq + tx * 4 + 64 * c]);
-          v[4 * c] += w * x.x;
-          v[4 * c + 1] += w * x.y;
-          v[4 * c + 2] += w * x.z;
-          v[4 * c + 3] += w * x.w;
+      for (int c = 0; c < MAXC * 4; ++c) v[c] = 0.f;
+#pragma unroll
+      for (int k = 0; k < CL; ++k) {
+        if (ml[k].y == 0.f) continue;
+        const float w = exp2f(ml[k].x - base);
+        sum += ml[k].y * w;
+        const float* src = cluster.map_shared_rank(so, k);
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c)
+          if (tx * 4 + 64 * c < dh) {
+            const float4 x = *reinterpret_cast<const float4*>(&src[r * ldq + tx * 4 + 64 * c]);
+            v[4 * c] += w * x.x;
+            v[4 * c + 1] += w * x.y;
+            v[4 * c + 2] += w * x.z;
+            v[4 * c + 3] += w * x.w;
+          }
+      }
+#pragma unroll
+      for (int i = i0; i < i0 + CL; ++i)
+        if (i - i0 == rank) {
+          m[i] = top;
+          l[i] = sum;
+#pragma unroll
+          for (int c = 0; c < MAXC * 4; ++c) o[i][c] = v[c];
         }
     }
     cluster.sync();  // read by all before a CTA of the cluster ends
-    // only thread row `rank` goes on
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i == rank) {
-        m[i] = top;
-        l[i] = sum;
-#pragma unroll
-        for (int c = 0; c < MAXC * 4; ++c) o[i][c] = v[c];
-      }
   }
   const bool direct = MODE == PROMPT || attn_direct(a);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (ty * 4 + i >= nrows || (CL > 1 && i != rank)) continue;
+  for (int i = 0; i < RPT; ++i) {
+    const int rr = row0 + ty * RPT + i;
+    if (ty * RPT + i >= nrows || (CL > 1 && i % CL != rank)) continue;
     if (odd_from < j1)  // rows that see an odd value of V get it after all
       for (int j = odd_from; j < min(limit[i], j1); ++j) {
         const long long at = key_at<MODE>(a, start, tab, g, j, 1);
@@ -393,7 +378,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
       }
     if (direct) {
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-      T* dst = static_cast<T*>(a.out) + orow[i] * a.out_ld + (size_t)head[i] * dh;
+      T* dst = static_cast<T*>(a.out) + token(rr) * a.out_ld + (size_t)head(rr) * dh;
 #pragma unroll
       for (int c = 0; c < MAXC; ++c) {
         const int d = tx * 4 + 64 * c;
@@ -406,9 +391,8 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a) {
           for (int k = 0; k < 4; ++k) dst[d + k] = from_f<T>(o[i][4 * c + k] * inv);
       }
     } else {
-      const int rr = row0 + ty * 4 + i;
-      const PartAt at = MODE == OWN ? part_own_rows(a, entry, piece, g, rr / a.G, rr % a.G)
-                                    : part_prefix(a, piece, g, rr / a.G, rr % a.G);
+      const PartAt at = pre ? part_prefix(a, piece, g, rr / a.G, rr % a.G)
+                            : part_own_rows(a, entry, piece, g, rr / a.G, rr % a.G);
       if (tx == 0) a.part_ml[at.first + at.row] = make_float2(m[i], l[i]);
 #pragma unroll
       for (int c = 0; c < MAXC; ++c) {
@@ -539,29 +523,30 @@ __global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-bool g_set[kMaxDev][2][3][5] = {};
+bool g_set[kMaxDev][2][2][5][4] = {};
 
-template <typename T, int MODE, int MAXC, int DHT>
-cudaError_t launch_one(const AttnRows& a, dim3 grid, cudaStream_t st) {
+template <typename T, int MODE, int MAXC, int DHT, int RPT>
+cudaError_t launch_one(const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto* kern = rows_kernel<T, MODE, MAXC, DHT>;
+  auto* kern = rows_kernel<T, MODE, MAXC, DHT, RPT>;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][DHT ? 3 + (DHT == 128) : MAXC / 2];
+    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][DHT ? 3 + (DHT == 128) : MAXC / 2][RPT / 4 + (RPT == 8)];
     if (!set || dev >= kMaxDev) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)rows_smem(DHT ? DHT : 64 * MAXC, (int)sizeof(T)));
+                               (int)rows_smem(DHT ? DHT : 64 * MAXC, 8 * RPT));
       if (e != cudaSuccess) return e;
       set = true;
     }
   }
-  if (MODE != PROMPT) return launch_pdl(kern, grid, dim3(RT), rows_smem(a.dh, (int)sizeof(T)), st, a);
+  const size_t smem = rows_smem(a.dh, 8 * RPT);
+  if (MODE != PROMPT) return launch_pdl(kern, grid, dim3(RT), smem, st, a, pre_x);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(RT);
-  cfg.dynamicSmemBytes = rows_smem(a.dh, (int)sizeof(T));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -571,38 +556,51 @@ cudaError_t launch_one(const AttnRows& a, dim3 grid, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, a, pre_x);
 }
 
-template <typename T, int MODE>
-cudaError_t launch_dh(const AttnRows& a, dim3 grid, cudaStream_t st) {
-  if (sizeof(T) == 4 && a.dh == 64) return launch_one<T, MODE, 1, sizeof(T) == 4 ? 64 : 0>(a, grid, st);
-  if (sizeof(T) == 4 && a.dh == 128) return launch_one<T, MODE, 2, sizeof(T) == 4 ? 128 : 0>(a, grid, st);
-  if (a.dh <= 64) return launch_one<T, MODE, 1, 0>(a, grid, st);
-  if (a.dh <= 128) return launch_one<T, MODE, 2, 0>(a, grid, st);
-  return launch_one<T, MODE, 4, 0>(a, grid, st);
+template <typename T, int MODE, int RPT>
+cudaError_t launch_dh(const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st) {
+  constexpr bool F32 = sizeof(T) == 4;
+  if (F32 && a.dh == 64) return launch_one<T, MODE, 1, F32 ? 64 : 0, RPT>(a, pre_x, grid, st);
+  if (F32 && a.dh == 128) return launch_one<T, MODE, 2, F32 ? 128 : 0, RPT>(a, pre_x, grid, st);
+  if (a.dh <= 64) return launch_one<T, MODE, 1, 0, RPT>(a, pre_x, grid, st);
+  if (a.dh <= 128) return launch_one<T, MODE, 2, 0, RPT>(a, pre_x, grid, st);
+  return launch_one<T, MODE, 4, 0, RPT>(a, pre_x, grid, st);
 }
 
-template <int MODE>
-cudaError_t launch_mode(int dtype, const AttnRows& a, dim3 grid, cudaStream_t st) {
-  return dtype == HF_F32 ? launch_dh<float, MODE>(a, grid, st) : launch_dh<__nv_bfloat16, MODE>(a, grid, st);
+template <int MODE, int RPT>
+cudaError_t launch_mode(int dtype, const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st) {
+  return dtype == HF_F32 ? launch_dh<float, MODE, RPT>(a, pre_x, grid, st)
+                         : launch_dh<__nv_bfloat16, MODE, RPT>(a, pre_x, grid, st);
 }
+
+// Rows of a thread: as many as an item has rows for, and as leave room for two CTAs per SM
+// (8 rows and a head dim of 128: 118 KB).
+int prompt_rpt(const AttnRows& a) { return a.dh <= 64 ? 8 : 4; }
+int paged_rpt(const AttnRows& a) { return a.rows * a.G <= 16 ? 2 : a.rows * a.G <= 32 || a.dh > 64 ? 4 : 8; }
 
 }  // namespace
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st) {
-  const long long slots = prompt_slots(a.total, a.n_seq, a.G, BM) * CLUSTER;
+  const int rpt = prompt_rpt(a);
+  const long long slots = prompt_slots(a.total, a.n_seq, a.G, 8 * rpt) * CLUSTER;
   if (slots > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_mode<PROMPT>(dtype, a, dim3((unsigned)slots, a.Hkv), st);
+  const dim3 grid((unsigned)slots, a.Hkv);
+  return rpt == 8 ? launch_mode<PROMPT, 8>(dtype, a, 0, grid, st) : launch_mode<PROMPT, 4>(dtype, a, 0, grid, st);
 }
-cudaError_t launch_attn_rows_prefix(int dtype, const AttnRows& a, cudaStream_t st) {
+cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st) {
+  const int rpt = paged_rpt(a), bm = 8 * rpt;
   const long long rows = (long long)a.n * a.rows * a.G;
-  return launch_mode<PREFIX>(dtype, a, dim3((unsigned)((rows + BM - 1) / BM), a.Hkv, a.npre), st);
+  const long long pre_x = (rows + bm - 1) / bm * a.npre;
+  const long long own_x = (long long)a.n * ((a.rows * a.G + bm - 1) / bm) * a.nown;
+  if (pre_x + own_x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(pre_x + own_x), a.Hkv);
+  return rpt == 8   ? launch_mode<PAGED, 8>(dtype, a, (int)pre_x, grid, st)
+         : rpt == 4 ? launch_mode<PAGED, 4>(dtype, a, (int)pre_x, grid, st)
+                    : launch_mode<PAGED, 2>(dtype, a, (int)pre_x, grid, st);
 }
-cudaError_t launch_attn_rows_own(int dtype, const AttnRows& a, cudaStream_t st) {
-  const int blocks = (a.rows * a.G + BM - 1) / BM;
-  return launch_mode<OWN>(dtype, a, dim3((unsigned)(a.n * blocks), a.Hkv, a.nown), st);
-}
+
 namespace {
 template <typename T, int SEGS>
 cudaError_t join(const AttnRows& a, int pieces, cudaStream_t st) {
@@ -653,17 +651,18 @@ float base2_scale(float scale, int dh) {
 }
 
 // Pieces of the key axis on CUDA cores: as many as give every SM eight CTAs of four warps,
-// of at least two tiles of keys. A request's own pieces go by its table's reach, not by
+// of a tile of keys at least. A request's own pieces go by its table's reach, not by
 // its length, which only the device knows.
 void plan_pieces(AttnRows& a) {
   auto split = [](long long keys, long long tiles, int& count, int& each) {
     const long long want = (152 * 8 + tiles - 1) / std::max<long long>(tiles, 1);
-    const long long c = std::max<long long>(1, std::min<long long>({want, (keys + 2 * BN - 1) / (2 * BN), 64}));
-    each = (int)std::max<long long>(2 * BN, ((keys + c - 1) / c + BN - 1) / BN * BN);
+    const long long c = std::max<long long>(1, std::min<long long>({want, (keys + BN - 1) / BN, 64}));
+    each = (int)(((keys + c - 1) / c + BN - 1) / BN * BN);
     count = (int)((keys + each - 1) / each);
   };
-  split(a.shared, ((long long)a.n * a.rows * a.G + BM - 1) / BM * a.Hkv, a.npre, a.pre_keys);
-  split((long long)a.table_ld * a.page - a.shared, (long long)a.n * a.Hkv * ((a.rows * a.G + BM - 1) / BM), a.nown,
+  const int bm = 8 * paged_rpt(a);
+  split(a.shared, ((long long)a.n * a.rows * a.G + bm - 1) / bm * a.Hkv, a.npre, a.pre_keys);
+  split((long long)a.table_ld * a.page - a.shared, (long long)a.n * a.Hkv * ((a.rows * a.G + bm - 1) / bm), a.nown,
         a.own_keys);
   a.nown = std::max(a.nown, 1);  // it also writes the empty rows of a direct call
 }
@@ -820,8 +819,7 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
     e = launch_attn_tc_pages(a, w.pre_items, st);
   } else {
     e = launch_attn_plan(a, 0, 0, st);
-    if (e == cudaSuccess && a.npre) e = launch_attn_rows_prefix(p->dtype, a, st);
-    if (e == cudaSuccess) e = launch_attn_rows_own(p->dtype, a, st);
+    if (e == cudaSuccess) e = launch_attn_rows_pages(p->dtype, a, st);
   }
   if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, w.pieces, st);
   return done(e);
