@@ -516,22 +516,22 @@ class _On:
     """The device and stream of one call: every tensor lies on the first one's
     device; the call is made with that device current, on `stream` or the
     device's current stream. New outputs belong to the call's stream."""
-    __slots__ = ("device", "given", "ptr")
+    __slots__ = ("index", "given", "ptr")
 
     def __init__(self, first, stream):
         import torch
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("expected CUDA tensors")
-        self.device = first.device
+        self.index = first.get_device()
         self.given = stream
         if stream is None:
-            self.ptr = torch._C._cuda_getCurrentRawStream(self.device.index)
+            self.ptr = torch._C._cuda_getCurrentRawStream(self.index)
         else:
             self.ptr = stream if isinstance(stream, int) else stream.cuda_stream
 
     def arg(self, t, name, dtype=None, shape=None, contiguous=True):
-        if t.device != self.device:
-            raise TypeError(f"{name} must be a CUDA tensor on {self.device}")
+        if t.get_device() != self.index:
+            raise TypeError(f"{name} must be a CUDA tensor on cuda:{self.index}")
         if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
         if shape is not None and t.shape != shape:
@@ -543,19 +543,19 @@ class _On:
     def empty(self, shape, dtype):
         import torch
         if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=self.index)
         s = self.given
         if isinstance(s, int):
-            s = torch.cuda.ExternalStream(s, device=self.device)
+            s = torch.cuda.ExternalStream(s, device=self.index)
         with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=self.index)
 
     def call(self, f, *args):
         import torch
-        if torch._C._cuda_getDevice() == self.device.index:
+        if torch._C._cuda_getDevice() == self.index:
             s = f(*args, self.ptr)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self.index):
                 s = f(*args, self.ptr)
         if s != 0:
             raise HyflashError(s, hf_last_error(None).decode())
@@ -682,7 +682,8 @@ class Pages:
         self.status = torch.zeros(1, dtype=i32, device=k.device)
         d.work, d.status = self._work.data_ptr(), self.status.data_ptr()
         self._d, self._ref = d, ctypes.byref(d)
-        self._i32, self._device = i32, k.device
+        self._i32, self._index = i32, k.get_device()
+        self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         if ints == 0:  # let a call say what is wrong with the descriptor
             on.call(hf_pages_compact, self._ref, None)
 
@@ -706,53 +707,62 @@ class Pages:
         """Pointer of an int32 list of n entries on the cache's device."""
         if t is None:
             return None
-        if t.dtype is not self._i32 or t.device != self._device or t.dim() != 1 or t.shape[0] != n or \
-                not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on {self._device}")
+        if t.dtype is not self._i32 or t.get_device() != self._index or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{self._index}")
         return t.data_ptr()
+
+    def _call(self, f, stream, *args):
+        if stream is None:
+            stream = self._raw_stream(self._index)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if self._current() == self._index:
+            s = f(self._ref, *args, stream)
+        else:
+            import torch
+            with torch.cuda.device(self._index):
+                s = f(self._ref, *args, stream)
+        if s != 0:
+            raise HyflashError(s, hf_last_error(None).decode())
 
     def extend(self, counts, requests=None, stream=None):
         """Room for counts[i] more tokens of requests[i] (default: request i)."""
         n = counts.shape[0]
-        _On(self.k, stream).call(hf_pages_extend, self._ref, self._ints(requests, n, "requests"),
-                                 self._ints(counts, n, "counts"), n)
+        self._call(hf_pages_extend, stream, self._ints(requests, n, "requests"), self._ints(counts, n, "counts"), n)
 
     def truncate(self, keep, requests=None, stream=None):
         """Cut requests[i] to keep[i] tokens; 0 frees it."""
         n = keep.shape[0]
-        _On(self.k, stream).call(hf_pages_truncate, self._ref, self._ints(requests, n, "requests"),
-                                 self._ints(keep, n, "keep"), n)
+        self._call(hf_pages_truncate, stream, self._ints(requests, n, "requests"), self._ints(keep, n, "keep"), n)
 
     def fork(self, source, into, stream=None):
         """Requests into[i] (empty) share all tokens of source[i]."""
         n = into.shape[0]
-        _On(self.k, stream).call(hf_pages_fork, self._ref, self._ints(source, n, "source"),
-                                 self._ints(into, n, "into"), n)
+        self._call(hf_pages_fork, stream, self._ints(source, n, "source"), self._ints(into, n, "into"), n)
 
     def compact(self, n_used=None, stream=None):
         """Move the pages in use to the front of the pool; n_used int32 [1] receives
         their number."""
-        _On(self.k, stream).call(hf_pages_compact, self._ref, self._ints(n_used, 1, "n_used"))
+        self._call(hf_pages_compact, stream, self._ints(n_used, 1, "n_used"))
 
     def write(self, k, v, offsets, requests=None, layer=None, stream=None):
         """The newest rows of the requests: k and v [layers, T, kv heads, head_dim]
         for layers 0 .. layers - 1, or [T, kv heads, head_dim] with `layer`; entry i's
         rows are offsets[i] .. offsets[i + 1] - 1."""
-        on = _On(self.k, stream)
         L, _, hkv, _, dh = self.k.shape
-        if k.dim() != (4 if layer is None else 3) or tuple(k.shape[-2:]) != (hkv, dh) or (layer is None and k.shape[0] > L):
+        if k.dim() != (4 if layer is None else 3) or k.shape[-2:] != (hkv, dh) or (layer is None and k.shape[0] > L):
             raise ValueError("k must be [layers, tokens, kv heads, head_dim], or [tokens, kv heads, head_dim] with layer")
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype is not self.k.dtype or t.get_device() != self._index:
+                raise TypeError(f"{name} must be {self.k.dtype} on cuda:{self._index}")
         T = k.shape[-3]
-        kp = on.arg(k, "k", self.k.dtype, None, False)
-        vp = on.arg(v, "v", self.k.dtype, k.shape, False)
         ld = _heads_ld(k, "k")
         step = k.stride(0) if layer is None and k.shape[0] > 1 else 0
-        if T and (_heads_ld(v, "v") != ld or (step and v.stride(0) != step)):
-            raise ValueError("k and v must have the same strides")
+        if v.shape != k.shape or (T and (_heads_ld(v, "v") != ld or (step and v.stride(0) != step))):
+            raise ValueError("k and v must have the same shape and strides")
         n = offsets.shape[0] - 1
-        op = self._ints(offsets, n + 1, "offsets")
-        on.call(hf_pages_write, self._ref, layer or 0, k.shape[0] if layer is None else 1, kp, vp, ld, step,
-                self._ints(requests, n, "requests"), op, n, T)
+        self._call(hf_pages_write, stream, layer or 0, k.shape[0] if layer is None else 1, k.data_ptr(), v.data_ptr(),
+                   ld, step, self._ints(requests, n, "requests"), self._ints(offsets, n + 1, "offsets"), n, T)
 
     def attend_workspace(self, q, shared=0):
         """A workspace for attend with queries of this shape."""

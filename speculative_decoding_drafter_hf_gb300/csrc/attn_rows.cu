@@ -10,9 +10,9 @@
 // Everything is fp32 in shared memory and registers: this is the variant for fp32 inputs
 // and for head dims that the tensor-core kernels do not take; bound by the fp32
 // multiply-adds and the shared-memory reads that feed them (RPT = 8: 128 multiply-adds
-// for 12 reads), which is why several CTAs per SM rather than two tiles in flight hide
-// the loads (8 prompts of 100 to 1201 tokens, heads of 64: two tiles in flight, two CTAs
-// per SM, RPT = 4 measured 103 us, one tile and four CTAs 75 us). A prompt's rows are
+// for 12 reads). K and V have one place each, refilled in turn while the other is used:
+// that leaves room for three or four CTAs per SM (8 prompts of 100 to 1201 tokens, heads
+// of 64: 71 us with RPT = 4, 76 us with 8; two places each and two CTAs per SM 103 us). A prompt's rows are
 // few for the GPU and their keys many: a cluster of four CTAs shares a tile of rows, each
 // walking every fourth tile of keys, and joins the parts through distributed shared
 // memory. Over a paged cache, RPT goes by the rows of a request.
@@ -133,21 +133,23 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
   auto token = [&](int rr) { return (size_t)(MODE == PROMPT ? start : pre ? 0 : entry * a.rows) + rr / a.G; };
   auto head = [&](int rr) { return g * a.G + rr % a.G; };
 
-  // K and V of the keys from jt on
-  auto load = [&](int jt) {
+  // K (kv = 0) or V of the keys from jt on. K of the next tile comes in while this one's
+  // values are summed, V while the next one's scores are formed.
+  auto load = [&](int kv, int jt) {
     constexpr int U = 8;
-    for (int e0 = tid; e0 < 2 * BN * c4; e0 += RT * U) {
+    float* to = kv ? sv : sk;
+    const T* from = static_cast<const T*>(kv ? a.v : a.k);
+    for (int e0 = tid; jt < j1 && e0 < BN * c4; e0 += RT * U) {
       float4 x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int e = e0 + u * RT;
-        if (e >= 2 * BN * c4) continue;
-        const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
+        const int e = e0 + u * RT, j = e / c4, c = (e % c4) * 4;
+        if (e >= BN * c4) continue;
         const long long at = jt + j < j1 ? key_at<MODE>(a, start, tab, g, jt + j, kv) : -2;
         if (at == -1 && a.status) atomicOr(a.status, HF_S_BAD);
-        const T* src = static_cast<const T*>(kv ? a.v : a.k) + (at < 0 ? 0 : at + c);
+        const T* src = from + (at < 0 ? 0 : at + c);
         if constexpr (F32)
-          copy16(&sk[(kv * BN + j) * ldq + c], src, at >= 0);
+          copy16(&to[j * ldq + c], src, at >= 0);
         else
           x[u] = at >= 0 ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -155,16 +157,15 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int e = e0 + u * RT;
-          if (e >= 2 * BN * c4) continue;
-          const int kv = e / (BN * c4), j = (e / c4) % BN, c = (e % c4) * 4;
-          *reinterpret_cast<float4*>(&sk[(kv * BN + j) * ldq + c]) = x[u];
+          if (e < BN * c4) *reinterpret_cast<float4*>(&to[e / c4 * ldq + (e % c4) * 4]) = x[u];
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int first = j0 + rank * BN;
-  if (first < j1) load(first);
+  load(0, first);
+  load(1, first);
 
   // this thread's rows: the keys they see
   int limit[RPT];
@@ -211,22 +212,8 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
   }
 
   for (int jt = first; jt < j1; jt += CL * BN) {
-    if (jt != first) load(jt);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // K; V may still be on its way
     __syncthreads();
-    // some row masks keys of this tile: the odd values of V there are set aside
-    if (low < min(jt + BN, j1)) {
-      const int k0 = max(0, low - jt);
-      for (int e = tid; e < (BN - k0) * dh; e += RT) {
-        float* x = &sv[(k0 + e / dh) * ldq + e % dh];
-        if (odd_value(*x)) {
-          *x = 0.f;
-          atomicMin(&s_odd, jt);
-        }
-      }
-      __syncthreads();
-    }
-
     float s[RPT][4];
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
@@ -245,6 +232,8 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
           s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
       }
     }
+    __syncthreads();  // K has been read
+    load(0, jt + CL * BN);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int lim = min(limit[i], j1);
@@ -271,7 +260,20 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
 #pragma unroll
       for (int c = 0; c < MAXC * 4; ++c) o[i][c] *= f;
     }
-    __syncwarp();  // a row's 16 threads are in one warp
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
+    __syncthreads();
+    // some row masks keys of this tile: the odd values of V there are set aside
+    if (low < min(jt + BN, j1)) {
+      const int k0 = max(0, low - jt);
+      for (int e = tid; e < (BN - k0) * dh; e += RT) {
+        float* x = &sv[(k0 + e / dh) * ldq + e % dh];
+        if (odd_value(*x)) {
+          *x = 0.f;
+          atomicMin(&s_odd, jt);
+        }
+      }
+      __syncthreads();
+    }
 #pragma unroll 2
     for (int j = 0; j < BN; j += 4) {
       float4 p[RPT];
@@ -293,8 +295,10 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
           }
         }
     }
-    __syncthreads();  // the tile has been read
+    __syncthreads();  // V has been read
+    load(1, jt + CL * BN);
   }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
 #pragma unroll
@@ -575,19 +579,17 @@ cudaError_t launch_mode(int dtype, const AttnRows& a, int pre_x, dim3 grid, cuda
                          : launch_dh<__nv_bfloat16, MODE, RPT>(a, pre_x, grid, st);
 }
 
-// Rows of a thread: as many as an item has rows for, and as leave room for two CTAs per SM
-// (8 rows and a head dim of 128: 118 KB).
-int prompt_rpt(const AttnRows& a) { return a.dh <= 64 ? 8 : 4; }
+// Rows of a thread, over a paged cache: as many as a request has rows for, and as leave
+// room for two CTAs per SM (8 rows and a head dim of 128: 118 KB).
+constexpr int kPromptRpt = 4;
 int paged_rpt(const AttnRows& a) { return a.rows * a.G <= 16 ? 2 : a.rows * a.G <= 32 || a.dh > 64 ? 4 : 8; }
 
 }  // namespace
 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st) {
-  const int rpt = prompt_rpt(a);
-  const long long slots = prompt_slots(a.total, a.n_seq, a.G, 8 * rpt) * CLUSTER;
+  const long long slots = prompt_slots(a.total, a.n_seq, a.G, 8 * kPromptRpt) * CLUSTER;
   if (slots > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)slots, a.Hkv);
-  return rpt == 8 ? launch_mode<PROMPT, 8>(dtype, a, 0, grid, st) : launch_mode<PROMPT, 4>(dtype, a, 0, grid, st);
+  return launch_mode<PROMPT, kPromptRpt>(dtype, a, 0, dim3((unsigned)slots, a.Hkv), st);
 }
 cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st) {
   const int rpt = paged_rpt(a), bm = 8 * rpt;
