@@ -826,21 +826,28 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           uint4* v = reinterpret_cast<uint4*>(sKV + (size_t)vs * L::TILE);
           // rows (keys) k0 .. k1 - 1 of the tile, a half of 64 columns after the other
           const int k0 = max(0, min(glow, j1) - jt), k1 = min(BN, hold - jt), per = (k1 - k0) * 8;
-          for (int q = row; q < per * HALVES; q += 128) {
-            const int h = q >= per;
-            uint4* at = v + h * (HALF / 16) + k0 * 8 + (q - h * per);
-            uint4 x = *at;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            // an exponent of all ones carries into its half's top bit
-            uint32_t hit[4];
+          for (int q0 = row; q0 < per * HALVES; q0 += 4 * 128) {
+            uint4 x[4];
+            auto at = [&](int u) {
+              const int q = q0 + u * 128, h = q >= per;
+              return v + h * (HALF / 16) + k0 * 8 + (q - h * per);
+            };
 #pragma unroll
-            for (int k = 0; k < 4; ++k) hit[k] = ((w[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-            if (hit[0] | hit[1] | hit[2] | hit[3]) {
+            for (int u = 0; u < 4; ++u) x[u] = q0 + u * 128 < per * HALVES ? *at(u) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) w[k] &= ~((hit[k] >> 15) * 0xffffu);
-              atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
-              __threadfence_block();
-              *at = x;
+            for (int u = 0; u < 4; ++u) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x[u]);
+              // an exponent of all ones carries into its half's top bit
+              uint32_t hit[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) hit[k] = ((w[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+              if (hit[0] | hit[1] | hit[2] | hit[3]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] &= ~((hit[k] >> 15) * 0xffffu);
+                atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
+                __threadfence_block();
+                *at(u) = x[u];
+              }
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
