@@ -50,6 +50,8 @@ PROMPTS = [  # dtype, Hq, Hkv, dh, lengths
     ("bf16", 2, 1, 256, [70, 5]),
     ("bf16", 64, 1, 128, [9, 3]),
     ("bf16", 1, 1, 128, [0, 0, 300, 0]),
+    ("bf16", 2, 1, 64, [(7 * i) % 23 for i in range(60)] + [300]),   # more sequences than a warp has lanes
+    ("bf16", 2, 1, 64, [(5 * i) % 13 for i in range(200)] + [150]),  # more than are sorted by their work
 ]
 
 
