@@ -506,7 +506,7 @@ enum {
  *              every sequence are not written. Bounds that break this rule
  *              set HF_S_BAD, and out is not valid.
  *   head_dim   a multiple of 8, at most 256. n_q_heads / n_kv_heads <= 64.
- *   scale      > 0, or 0 for 1/sqrt(head_dim).
+ *   scale      > 0, at most 1e38, or 0 for 1/sqrt(head_dim).
  *   out        as q; may not overlap q, k or v. */
 hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t total, int32_t n_q_heads,
                               int32_t n_kv_heads, int32_t head_dim, const void* q, int64_t q_ld,
@@ -643,7 +643,7 @@ size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows,
  *                then -1.
  *   workspace     DEVICE, 16-byte aligned, hf_verify_workspace() bytes.
  * A request with a draft outside 0..vocab-1, n_draft out of range, a T that is
- * negative or not finite, or logits without a softmax (NaN, +infinity, or nothing above
+ * negative, not finite or above 0 but below 2^-126, or logits without a softmax (NaN, +infinity, or nothing above
  * -infinity) in a row that the rule above reads, sets HF_S_BAD and gets n_accepted = 0
  * and tokens -1: hf_commit then leaves it as it is. */
 hf_status hf_verify_tokens(int32_t target_dtype, const void* target_logits, int64_t target_ld,

@@ -624,7 +624,10 @@ def verify_tokens(target_logits, draft_tokens, u, noise, *, draft_logits=None, t
         s = t.stride()
         if (V > 1 and s[2] != 1) or (B > 1 and n > 1 and s[0] != n * s[1]):
             raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
-        return max(s[1] if n > 1 else s[0] if B > 1 else V, V) if B else V
+        ld = s[1] if n > 1 else s[0] if B > 1 else V
+        if B and ld < V:
+            raise ValueError(f"{name}: rows must not overlap")
+        return max(ld, V)
 
     f32, i32 = torch.float32, torch.int32
     tp = on.arg(target_logits, "target_logits", None, None, False)

@@ -640,11 +640,11 @@ const char* heads_bad(int hq, int hkv, int dh, float scale) {
   if (hq < 1 || hkv < 1 || hkv > 1024 || hq % hkv) return "n_kv_heads must be 1..1024 and divide n_q_heads";
   if (hq / hkv > 64) return "n_q_heads / n_kv_heads must be <= 64";
   if (dh < 8 || dh % 8 || dh > 256) return "head_dim must be a multiple of 8, <= 256";
-  if (!(scale >= 0.f) || !(scale < INFINITY)) return "scale must be finite and >= 0 (0: 1/sqrt(head_dim))";
+  if (!(scale >= 0.f) || !(scale <= 1e38f)) return "scale must be in 0..1e38 (0: 1/sqrt(head_dim))";
   return nullptr;
 }
 const char* ld_bad(int64_t ld, long long least, int esize, const void* p) {
-  if (ld < least || ld > (1LL << 40)) return "a row stride is smaller than heads * head_dim";
+  if (ld < least || ld > (1LL << 36)) return "a row stride is smaller than heads * head_dim, or above 2^36";
   if (ld * esize % 16 || off(p, 16)) return "q, k, v and out must be 16-byte aligned, their strides multiples of 16 bytes";
   return nullptr;
 }
@@ -706,7 +706,7 @@ const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq,
   if (shared < 0 || shared % p->page || shared > (long long)p->table_ld * p->page)
     return "shared must be a multiple of page, at most table_ld * page";
   if ((long long)n * rows * hq > 0x7fffffffLL / 4 ||
-      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart) * n * ((long long)rows * hq / 128 + p->n_kv_heads) > 0x7fffffffLL)
+      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart) * n * ((long long)rows * hq / 128 + p->n_kv_heads) > 0x3fffffffLL)
     return "n * rows * n_q_heads, or that times the table's reach, is too large";
   a.Hq = hq;
   a.Hkv = p->n_kv_heads;
@@ -738,7 +738,9 @@ extern "C" hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t t
   if (dtype != HF_F32 && dtype != HF_BF16) return refuse("dtype must be HF_F32 or HF_BF16");
   if (n_seq < 0 || n_seq > (1 << 24) || total < 0) return refuse("n_seq must be 0..16777216 and total >= 0");
   if (const char* m = heads_bad(n_q_heads, n_kv_heads, head_dim, scale)) return refuse(m);
-  if ((long long)total * (n_q_heads / n_kv_heads) > 0x7fffffffLL) return refuse("total * group is too large");
+  // (CTAs: at most a slot per 2 tokens and one per sequence, for each KV head, times four)
+  if (((long long)total * (n_q_heads / n_kv_heads) / 32 + total / 4 + n_seq) * n_kv_heads > 0x7fffffffLL / 4)
+    return refuse("total * n_q_heads, or n_seq * n_kv_heads, is too large");
   if (n_seq == 0 || total == 0) return HF_OK;
   if (!q || !k || !v || !offsets || !out) return refuse("NULL buffer");
   const int esize = dtype == HF_F32 ? 4 : 2;

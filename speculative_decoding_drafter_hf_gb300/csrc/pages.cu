@@ -48,7 +48,8 @@ constexpr int CT = 256;   // threads of the copying CTAs
 constexpr int kMoves = 16;
 
 __device__ __forceinline__ int move_room(const hf_pages& p) { return max(p.n_pages, p.n_requests); }
-__device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
+// (lengths near 2^31 too)
+__device__ __forceinline__ int pages_of(int len, int page) { return len / page + (len % page > 0); }
 __device__ __forceinline__ void flag(const hf_pages& p, int bit) {
   if (p.status) atomicOr(p.status, bit);
 }
@@ -162,8 +163,9 @@ __global__ void __launch_bounds__(CT) fork_kernel(hf_pages p, const int32_t* fro
   pdl_wait();
   const bool ok = list_ok(p, into, from, n, [&](int i, int r) {
     const int s = __ldcg(&from[i]);
-    return s >= 0 && s < p.n_requests && __ldcg(&p.lens[r]) == 0 &&
-           pages_of(__ldcg(&p.lens[s]), p.page) <= p.table_ld;
+    if (s < 0 || s >= p.n_requests) return false;
+    const int len = __ldcg(&p.lens[s]);
+    return __ldcg(&p.lens[r]) == 0 && len >= 0 && pages_of(len, p.page) <= p.table_ld;
   });
   if (ok) {
     for (int i = blockIdx.x; i < n; i += gridDim.x) {

@@ -50,7 +50,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ bool temp_ok(float t) { return t >= 0.f && t < INFINITY; }
+// (a T below the normal numbers would make 1 / T infinite)
+__device__ __forceinline__ bool temp_ok(float t) { return t == 0.f || (t >= 1.17549435e-38f && t < INFINITY); }
 
 // The entries [i0, i1) of a row: single ones up to a 16-byte boundary and behind the
 // last whole 16 bytes go to one(index, value); of the rest, each thread gets UN 16-byte

@@ -304,6 +304,44 @@ def test_attend_odd_values_stay_with_the_rows_that_see_them(hf, dtype):
         assert np.isnan(o[0, 6:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_pool_past_32_bits(hf, dtype):
+    """Pages whose elements lie behind the first 2^32: extended, written, copied, attended, compacted."""
+    hkv, page, dh = (16, 64, 128) if dtype == "bf16" else (16, 64, 64)
+    n_pages = (1 << 32) // (hkv * page * dh) + 70
+    c = hf.Pages.empty(1, n_pages, hkv, page, dh, 3, 6, dtype=DT[dtype])
+    c.refs.fill_(1)
+    c.refs[-40:] = 0  # only the last ones are free
+    c.extend(_i32([100]), _i32([1]))
+    k, v = (_randn((1, 100, hkv, dh), dtype, s) for s in (1, 2))
+    c.write(k.cuda(), v.cuda(), _i32([0, 100]), _i32([1]))
+    c.fork(_i32([1]), _i32([2]))
+    c.extend(_i32([4, 4]), _i32([1, 2]))  # both take a copy of the half-filled page
+    more = [_randn((1, 8, hkv, dh), dtype, s) for s in (3, 4)]
+    c.write(more[0].cuda(), more[1].cuda(), _i32([0, 4, 8]), _i32([1, 2]))
+    assert not c.check() and c.lens.tolist() == [0, 104, 104]
+    q = _randn((2, 4, 2 * hkv, dh), dtype, 5)
+
+    def expect(o):
+        for i in range(2):
+            kk = torch.cat([k[0], more[0][0, 4 * i:4 * i + 4]])
+            vv = torch.cat([v[0], more[1][0, 4 * i:4 * i + 4]])
+            for r in range(4):
+                for h in range(0, 2 * hkv, 5):
+                    want, tol = R.attention(R.to64(q[i, r, h]), R.to64(kk[:101 + r, h // 2]), R.to64(vv[:101 + r, h // 2]),
+                                            dh ** -0.5, dtype == "bf16")
+                    R.check_attention(o[i, r, h], want, tol, f"request {i} row {r} head {h}")
+
+    for shared in (0, 64):
+        expect(R.to64(c.attend(q.cuda(), _i32([1, 2]), shared=shared)))
+    assert int(c.table[1, 0]) >= n_pages - 40 and not c.check()
+    c.refs[5:20] = 0  # holes far before them
+    c.compact()
+    assert not c.check() and int(c.table[:, :2].max()) < n_pages - 40
+    expect(R.to64(c.attend(q.cuda(), _i32([1, 2]))))
+    assert not c.check()
+
+
 # ----------------------------------------------------------------- page tables
 def _same(c, ref, what):
     assert c.lens.tolist() == ref.lens, what
@@ -488,6 +526,32 @@ def test_verify_masked_logits_and_bad_requests(hf):
     nd = torch.tensor([0, 0, 0, 4, -1, 0, 0, 0, 0], dtype=torch.int32)
     n, t = hf.verify_tokens(x.cuda(), tok.cuda(), u.cuda(), noise.cuda(), n_draft=nd.cuda())
     assert [v > 0 for v in n.tolist()] == [True, True, True, False, False, True, True, True, True]
+
+
+def test_verify_refuses_rows_that_overlap(hf):
+    x = torch.zeros(1, 1, 50, device="cuda")
+    tok, u, noise = torch.zeros(3, 1, dtype=torch.int32, device="cuda"), torch.zeros(3, 1, device="cuda"), torch.ones(3, 50, device="cuda")
+    with pytest.raises(ValueError):
+        hf.verify_tokens(x.expand(3, 2, 50), tok, u, noise)
+    with pytest.raises(ValueError):
+        hf.verify_tokens(torch.zeros(3, 2, 50, device="cuda"), tok, u, noise, draft_logits=x.expand(3, 1, 50))
+    with pytest.raises(hf.HyflashError):
+        q = torch.zeros(1, 2, 64, device="cuda").expand(5, 2, 64)
+        hf.attention_prompt(q, q, q, _i32([0, 5]))
+
+
+def test_verify_temperatures_at_the_edges(hf):
+    """The smallest T picks the largest logit, the largest one is nearly uniform; a T that is no number is refused."""
+    V = 40
+    x = torch.randn((5, 2, V), generator=_gen(1))
+    tok = x[:, :1].argmax(-1).int()
+    temp = torch.tensor([1.2e-38, 3e38, float("inf"), float("nan"), 1e-39])
+    noise = torch.ones(5, V)
+    noise[1, 7] = 0.5
+    n, t = hf.verify_tokens(x.cuda(), tok.cuda(), torch.full((5, 1), 0.5).cuda(), noise.cuda(), temperature=temp.cuda())
+    assert n.tolist() == [2, 1, 0, 0, 0]
+    assert t[0].tolist() == [int(tok[0]), int(x[0, 1].argmax())]
+    assert t[1].tolist() == [7, -1] and (t[2:] == -1).all()
 
 
 def test_verify_draws_from_the_residual(hf):

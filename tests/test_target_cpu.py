@@ -30,7 +30,9 @@ PROMPT = dict(dtype=1, n_seq=2, total=10, hq=4, hkv=2, dh=64, q=16, q_ld=256, k=
     (dict(off=None), "NULL"), (dict(out=None), "NULL"), (dict(q=8), "16-byte"), (dict(out=24), "16-byte"),
     (dict(q_ld=252), "stride"), (dict(k_ld=120), "stride"), (dict(v_ld=132), "16-byte"), (dict(out_ld=260), "16-byte"),
     (dict(off=18), "4-byte"), (dict(status=2), "4-byte"),
-    (dict(total=1 << 30), "too large"),
+    (dict(total=1 << 30), "too large"), (dict(n_seq=1 << 24, hq=256, hkv=256, q_ld=1 << 14, k_ld=1 << 14, v_ld=1 << 14,
+                                              out_ld=1 << 14), "too large"),
+    (dict(scale=2e38), "scale"), (dict(q_ld=1 << 37), "stride"),
 ])
 def test_prompt_refusals(B, change, msg):
     _refused(B, B.hf_attention_prompt(*{**PROMPT, **change}.values()), msg)
@@ -115,7 +117,7 @@ ATTEND = dict(layer=0, n=2, rows=8, hq=4, q=16, q_ld=256, req=16, shared=32, sca
     (dict(shared=-16), "multiple of page"), (dict(shared=96), "table_ld"), (dict(scale=-2.0), "scale"),
     (dict(req=None, n=5), "without a list"), (dict(q=None), "NULL"), (dict(out=None), "NULL"), (dict(ws=None), "NULL"),
     (dict(q_ld=248), "stride"), (dict(q=8), "16-byte"), (dict(out_ld=260), "16-byte"), (dict(req=18), "4-byte"),
-    (dict(ws=24), "workspace"), (dict(bytes=0), "workspace"),
+    (dict(ws=24), "workspace"), (dict(bytes=0), "workspace"), (dict(n=1 << 20, rows=64, hq=128), "too large"),
 ])
 def test_attend_refusals(B, change, msg):
     p = ctypes.byref(_cache(B))
