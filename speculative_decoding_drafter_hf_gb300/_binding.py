@@ -503,13 +503,18 @@ class CallStatus(enum.IntFlag):
     FULL = 4
 
 
+_CODES = {}  # torch dtypes -> hf_dtype, filled at the first call
+
+
 def _dtype_code(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return HF_BF16
-    if t.dtype == torch.float32:
-        return HF_F32
-    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    c = _CODES.get(t.dtype)
+    if c is None:
+        import torch
+        _CODES.update({torch.float32: HF_F32, torch.bfloat16: HF_BF16})
+        c = _CODES.get(t.dtype)
+        if c is None:
+            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return c
 
 
 class _On:
@@ -561,13 +566,12 @@ class _On:
             raise HyflashError(s, hf_last_error(None).decode())
 
 
-def _heads_ld(t, name):
-    """Row stride of [..., heads, head_dim] whose heads follow each other."""
-    h, d = t.shape[-2], t.shape[-1]
+def _heads_ld(t, n, h, d, name):
+    """Row stride of [..., n, h heads, d] whose heads follow each other."""
     s = t.stride()
-    if (d > 1 and s[-1] != 1) or (h > 1 and s[-2] != d):
+    if (s[-1] != 1 and d > 1) or (s[-2] != d and h > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return s[-3] if t.shape[-3] > 1 else h * d
+    return s[-3] if n > 1 else h * d
 
 
 def attention_prompt(q, k, v, offsets, *, scale=0.0, out=None, status=None, stream=None):
@@ -577,23 +581,22 @@ def attention_prompt(q, k, v, offsets, *, scale=0.0, out=None, status=None, stre
     what `out` held."""
     import torch
     on = _On(q, stream)
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    if q.dim() != 3 or k.dim() != 3 or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim], offsets [sequences + 1]")
     T, hq, dh = q.shape
     hkv = k.shape[1]
+    dt, kv = q.dtype, (T, hkv, dh)
     code = _dtype_code(q, "q")
-    qp = on.arg(q, "q", None, None, False)
-    kp = on.arg(k, "k", q.dtype, (T, hkv, dh), False)
-    vp = on.arg(v, "v", q.dtype, (T, hkv, dh), False)
+    kp = on.arg(k, "k", dt, kv, False)
+    vp = on.arg(v, "v", dt, kv, False)
     op = on.arg(offsets, "offsets", torch.int32)
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must be [sequences + 1]")
     if out is None:
-        out = on.empty((T, hq, dh), q.dtype)
-    rp = on.arg(out, "out", q.dtype, (T, hq, dh), False)
+        out = on.empty((T, hq, dh), dt)
+    rp = on.arg(out, "out", dt, q.shape, False)
     sp = None if status is None else on.arg(status, "status", torch.int32)
-    on.call(hf_attention_prompt, code, offsets.shape[0] - 1, T, hq, hkv, dh, qp, _heads_ld(q, "q"), kp,
-            _heads_ld(k, "k"), vp, _heads_ld(v, "v"), op, float(scale or 0.0), rp, _heads_ld(out, "out"), sp)
+    on.call(hf_attention_prompt, code, offsets.shape[0] - 1, T, hq, hkv, dh, q.data_ptr(), _heads_ld(q, T, hq, dh, "q"),
+            kp, _heads_ld(k, T, hkv, dh, "k"), vp, _heads_ld(v, T, hkv, dh, "v"), op, scale or 0.0, rp,
+            _heads_ld(out, T, hq, dh, "out"), sp)
     return out
 
 
@@ -616,13 +619,12 @@ def verify_tokens(target_logits, draft_tokens, u, noise, *, draft_logits=None, t
     on = _On(target_logits, stream)
     if target_logits.dim() != 3 or target_logits.shape[1] < 2:
         raise ValueError("target_logits must be [batch, block + 1, vocab]")
-    B, S, V = target_logits.shape[0], target_logits.shape[1] - 1, target_logits.shape[2]
+    B, S, V = target_logits.shape
+    S -= 1
 
     def rows(t, name, n):
-        if tuple(t.shape) != (B, n, V):
-            raise ValueError(f"{name} must have shape {(B, n, V)}, got {tuple(t.shape)}")
         s = t.stride()
-        if (V > 1 and s[2] != 1) or (B > 1 and n > 1 and s[0] != n * s[1]):
+        if (s[2] != 1 and V > 1) or (B > 1 and n > 1 and s[0] != n * s[1]):
             raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
         ld = s[1] if n > 1 else s[0] if B > 1 else V
         if B and ld < V:
@@ -630,30 +632,28 @@ def verify_tokens(target_logits, draft_tokens, u, noise, *, draft_logits=None, t
         return max(ld, V)
 
     f32, i32 = torch.float32, torch.int32
-    tp = on.arg(target_logits, "target_logits", None, None, False)
+    batch, slots, drafts = (B,), (B, S + 1), (B, S)
     t_ld = rows(target_logits, "target_logits", S + 1)
     dp, d_ld, d_code = None, 0, 0
     if draft_logits is not None:
-        dp = on.arg(draft_logits, "draft_logits", None, None, False)
+        dp = on.arg(draft_logits, "draft_logits", None, (B, S, V), False)
         d_ld = rows(draft_logits, "draft_logits", S)
         d_code = _dtype_code(draft_logits, "draft_logits")
-    kp = on.arg(draft_tokens, "draft_tokens", i32, (B, S))
-    up = on.arg(u, "u", f32, (B, S))
+    kp = on.arg(draft_tokens, "draft_tokens", i32, drafts)
+    up = on.arg(u, "u", f32, drafts)
     ep = on.arg(noise, "noise", f32, (B, V))
-    np_ = None if n_draft is None else on.arg(n_draft, "n_draft", i32, (B,))
-    hp = None if temperature is None else on.arg(temperature, "temperature", f32, (B,))
+    np_ = None if n_draft is None else on.arg(n_draft, "n_draft", i32, batch)
+    hp = None if temperature is None else on.arg(temperature, "temperature", f32, batch)
     if n_accepted is None:
-        n_accepted = on.empty((B,), i32)
+        n_accepted = on.empty(batch, i32)
     if tokens is None:
-        tokens = on.empty((B, S + 1), i32)
-    ap = on.arg(n_accepted, "n_accepted", i32, (B,))
-    op = on.arg(tokens, "tokens", i32, (B, S + 1))
+        tokens = on.empty(slots, i32)
     if workspace is None:
         workspace = on.empty((max(hf_verify_workspace(B, S, V), 16),), torch.uint8)
-    wp = on.arg(workspace, "workspace", torch.uint8)
-    sp = None if status is None else on.arg(status, "status", i32)
-    on.call(hf_verify_tokens, _dtype_code(target_logits, "target_logits"), tp, t_ld, d_code, dp, d_ld, kp, np_, up,
-            ep, V, hp, B, S, V, ap, op, wp, workspace.numel(), sp)
+    on.call(hf_verify_tokens, _dtype_code(target_logits, "target_logits"), target_logits.data_ptr(), t_ld, d_code, dp,
+            d_ld, kp, np_, up, ep, V, hp, B, S, V, on.arg(n_accepted, "n_accepted", i32, batch),
+            on.arg(tokens, "tokens", i32, slots), on.arg(workspace, "workspace", torch.uint8), workspace.shape[0],
+            None if status is None else on.arg(status, "status", i32))
     return n_accepted, tokens
 
 
@@ -759,9 +759,9 @@ class Pages:
             if t.dtype is not self.k.dtype or t.get_device() != self._index:
                 raise TypeError(f"{name} must be {self.k.dtype} on cuda:{self._index}")
         T = k.shape[-3]
-        ld = _heads_ld(k, "k")
+        ld = _heads_ld(k, T, hkv, dh, "k")
         step = k.stride(0) if layer is None and k.shape[0] > 1 else 0
-        if v.shape != k.shape or (T and (_heads_ld(v, "v") != ld or (step and v.stride(0) != step))):
+        if v.shape != k.shape or (T and (_heads_ld(v, T, hkv, dh, "v") != ld or (step and v.stride(0) != step))):
             raise ValueError("k and v must have the same shape and strides")
         n = offsets.shape[0] - 1
         self._call(hf_pages_write, stream, layer or 0, k.shape[0] if layer is None else 1, k.data_ptr(), v.data_ptr(),
@@ -786,7 +786,7 @@ class Pages:
         n, rows, hq, dh = q.shape
 
         def ld(t, name):
-            s = _heads_ld(t, name)
+            s = _heads_ld(t, rows, hq, dh, name)
             if rows == 1 and n > 1:
                 s = t.stride(0)
             elif n > 1 and t.stride(0) != rows * s:
@@ -802,5 +802,5 @@ class Pages:
             workspace = on.empty((max(b, 16),), torch.uint8)
         wp = on.arg(workspace, "workspace", torch.uint8)
         on.call(hf_attention_pages, self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._ints(requests, n, "requests"),
-                shared, float(scale or 0.0), op, ld(out, "out"), wp, workspace.numel())
+                shared, scale or 0.0, op, ld(out, "out"), wp, workspace.shape[0])
         return out
