@@ -67,12 +67,17 @@ __device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& one, G
   if (tid < head) one(i0 + tid, to_f(row[i0 + tid]));
   const int b0 = i0 + head, nv = (i1 - b0) / VE;
   const uint4* p = reinterpret_cast<const uint4*>(row + b0);
+  uint4 r[UN];
+#pragma unroll
+  for (int k = 0; k < UN; ++k)
+    if (tid + k * VT < nv) r[k] = __ldg(p + tid + k * VT);
   for (int v0 = tid; v0 < nv; v0 += VT * UN) {
-    uint4 r[UN];
-    float x[UN * VE];
+    const int v1 = v0 + VT * UN;  // the next loads are on their way meanwhile
+    uint4 next[UN];
 #pragma unroll
     for (int k = 0; k < UN; ++k)
-      if (v0 + k * VT < nv) r[k] = __ldg(p + v0 + k * VT);
+      if (v1 + k * VT < nv) next[k] = __ldg(p + v1 + k * VT);
+    float x[UN * VE];
     const int n = min(UN, (nv - v0 + VT - 1) / VT);
 #pragma unroll
     for (int k = 0; k < UN; ++k)
@@ -80,6 +85,8 @@ __device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& one, G
       for (int j = 0; j < VE; ++j)
         x[k * VE + j] = k < n ? to_f(reinterpret_cast<const T*>(&r[k])[j]) : kNegInf;
     some(b0 + v0 * VE, x, n);
+#pragma unroll
+    for (int k = 0; k < UN; ++k) r[k] = next[k];
   }
   const int t0 = b0 + nv * VE;
   if (t0 + tid < i1) one(t0 + tid, to_f(row[t0 + tid]));
@@ -111,7 +118,7 @@ __device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t,
   __shared__ int si[VT / 32];
   const int i0 = chunk * a.chunk, i1 = min(a.V, i0 + a.chunk);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr int VE = 16 / (int)sizeof(T), UN = 4;
+  constexpr int VE = 16 / (int)sizeof(T), UN = 16 / VE;
   if (t == 0.f) {
     float v = kNegInf;
     int idx = -1;
