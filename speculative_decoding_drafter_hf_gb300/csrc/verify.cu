@@ -407,13 +407,15 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   }
 }
 
-// Chunk of the vocabulary per CTA: about `per_sm` CTAs per SM in all (statistics: several
-// rounds of small CTAs; race: one round, since every CTA first joins its request's
-// statistics, which measured 4 us), at least `least` entries each.
+// Chunk of the vocabulary per CTA: about `per_sm` CTAs per SM in all, at least `least`
+// entries each. Both kernels' CTAs begin with a chain of dependent loads (in the race 4 us:
+// the request's statistics are joined), so few long ones are faster: 64 x 7 drafts of 100352
+// tokens took 82, 69 and 65 us with 32, 16 and 6 for the statistics, 73, 69 and 72 us with 12,
+// 4 and 3 for the race.
 int chunk_for(long long rows, int V, int least, int per_sm) {
   const long long want = (152 * per_sm + rows - 1) / rows;  // CTAs per row
   const long long c = (V + want - 1) / want;
-  return (int)std::max<long long>(least, std::min<long long>((c + 1023) / 1024 * 1024, 32768));
+  return (int)std::max<long long>(least, std::min<long long>((c + 1023) / 1024 * 1024, 65536));
 }
 
 struct VPlan {
@@ -423,7 +425,7 @@ struct VPlan {
 
 VPlan plan_for(int B, int S, int V) {
   VPlan p{};
-  p.chunk = chunk_for((long long)B * (S + 1), V, 2048, 16);
+  p.chunk = chunk_for((long long)B * (S + 1), V, 2048, 6);
   p.nchunk = (V + p.chunk - 1) / p.chunk;
   p.rchunk = chunk_for(B, V, 1024, 4);
   p.nrchunk = (V + p.rchunk - 1) / p.rchunk;
