@@ -835,9 +835,15 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_hold32(s + q * 32);
           if (jt + BN > wlow) {
+            const int seen = lim - jt;  // keys of this tile
 #pragma unroll
-            for (int q = 0; q < BN; ++q)
-              if (jt + q >= lim) s[q] = -INFINITY;
+            for (int h = 0; h < BN; h += 32) {
+              // bits rather than comparisons: a register of them becomes predicates at once
+              const uint32_t bits = seen >= h + 32 ? 0xffffffffu : seen <= h ? 0u : (1u << (seen - h)) - 1u;
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (!(bits >> q & 1)) s[h + q] = -INFINITY;
+            }
           }
           float t8[8];
 #pragma unroll
