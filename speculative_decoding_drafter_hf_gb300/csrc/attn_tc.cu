@@ -17,7 +17,7 @@
 // warps 4-7 and 8-11 are the softmax groups; CTAs stay and take item after item, so that
 // the next item's loads and first product run beside the last one's end. Prompt items are
 // the launch's own CTAs, taken over from the ones not started yet, heaviest first (16
-// prompts of 1 to 1969 tokens: 93 us, in the order of the pack 107). Over a cache the
+// prompts of 1 to 1969 tokens: in the order of the pack 15% more). Over a cache the
 // prefix's items go round the CTAs, and what each has of the requests' own tiles is a
 // stretch of one line (AttnLine).
 //
@@ -49,7 +49,8 @@ struct Tc {
   static constexpr int TILE = BN * DH * 2;            // bytes of a K, V or Q tile
   static constexpr int SLOTS = DH == 128 ? 5 : 10;    // ring of K and V tiles
   static constexpr int O_COL = 256;                   // TMEM: S0 | S1 | O0 | O1
-  static constexpr size_t smem() { return (size_t)(2 + SLOTS) * TILE + (2 * SLOTS + 14) * 8 + 16 + 2 * 80 + 48 + (2 * kSmall + 2) * 4; }
+  static constexpr int BARS = 2 * SLOTS + 14;
+  static constexpr size_t smem() { return (size_t)(2 + SLOTS) * TILE + BARS * 8 + 16 + 2 * 80 + 48 + (2 * kSmall + 2) * 4; }
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -235,8 +236,13 @@ struct Item {
   int entry, len;  // own: the entry and its tokens
   int direct;      // rows go to out
   int part;        // else: the prefix's piece, the own pieces' slot
-  int low[2];      // least number of keys that a row of the tile sees
+  int low, hold;   // least number of keys that a row sees; keys behind `hold` read as zeros
   int odd[2];      // first key of a tile whose odd values of V were taken as zero
+  // first key tile that holds keys which some row masks (so does every later one)
+  __device__ __forceinline__ int first_cut() const {
+    const int m = min(low, j1);
+    return m < hold ? max(0, m - j0) / BN : kNone;
+  }
 };
 static_assert(sizeof(Item) <= 80, "item slots");
 
@@ -335,7 +341,7 @@ __device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, co
   const AttnRows& a = c.a;
   it.split = 0;
   it.start = it.entry = it.len = it.part = 0;
-  it.low[0] = it.low[1] = it.odd[0] = it.odd[1] = kNone;
+  it.odd[0] = it.odd[1] = kNone;
   int nt;
   if (MODE == PROMPT) {
     if (!t.ok) return false;
@@ -348,6 +354,8 @@ __device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, co
     it.j0 = 0;
     it.j1 = it.t0 + it.ntok;
     it.direct = 1;
+    it.low = it.t0 + 1;
+    it.hold = kNone;
     nt = (it.j1 + BN - 1) / BN;
     // the first row tile ends earlier
     it.nt[0] = min(nt, (min(it.j1, it.t0 + c.tb) + BN - 1) / BN);
@@ -372,6 +380,13 @@ __device__ __forceinline__ bool make_item(const TcArgs& c, int idx, Item& it, co
   it.j0 = it.part * a.pre_keys;
   it.j1 = eff[0] ? min(a.shared, it.j0 + a.pre_keys) : it.j0;  // entry 0 empty: so is every row
   it.direct = 0;
+  it.hold = it.j1;  // (whole pages)
+  int low = kNone;  // an entry's first row sees least
+  for (int e = it.t0 / a.rows + (threadIdx.x & 31); e * a.rows < it.t0 + it.ntok; e += 32) {
+    const int row = max(e * a.rows, it.t0) - e * a.rows;
+    if (eff[e] > 0) low = min(low, max(0, eff[e] - a.rows + row + 1));
+  }
+  it.low = __reduce_min_sync(0xffffffffu, low);
   it.nt[0] = nt = (it.j1 - it.j0 + BN - 1) / BN;
   it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? nt : 0;
   return true;
@@ -400,7 +415,7 @@ __device__ __forceinline__ int make_own(const TcArgs& c, const AttnLine& line, i
   it.entry = lo;
   it.len = eff[lo];
   it.start = 0;
-  it.low[0] = it.low[1] = it.odd[0] = it.odd[1] = kNone;
+  it.odd[0] = it.odd[1] = kNone;
   it.split = a.rows <= c.tb;
   if (it.split) {
     it.g = 2 * u;
@@ -413,6 +428,8 @@ __device__ __forceinline__ int make_own(const TcArgs& c, const AttnLine& line, i
   it.ntok = min(it.split ? c.tb : 2 * c.tb, a.rows - it.t0);
   it.j0 = a.shared + (from - first) * BN;
   it.j1 = min(it.len, it.j0 + take * BN);
+  it.low = max(0, it.len - a.rows + it.t0 + 1);
+  it.hold = (it.j1 + a.page - 1) / a.page * a.page;
   it.direct = a.npre == 0 && line.cta(u * line.tiles + first) == line.cta(u * line.tiles + last - 1);
   it.part = u * a.n + lo + cta;
   it.nt[0] = take;
@@ -506,7 +523,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   uint64_t* i_full = q_full + 8;   // [2] items
   uint64_t* i_empty = q_full + 10; // [2]
   uint64_t* n_full = q_full + 12;  // the next CTA's index has come
-  uint4* answer = reinterpret_cast<uint4*>(q_full + 14);
+  uint4* answer = reinterpret_cast<uint4*>(full + L::BARS);
   Item* items = reinterpret_cast<Item*>(answer + 1);  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -664,18 +681,23 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             if (nt == 1) mma_commit(lead, smem_u32(q_empty));
           }
           int vs = 0;
+          // from tile `look` on the softmax groups look V over before they hand their weights
+          // on; where both have the tile, each looks at half of it
+          const int look = __shfl_sync(0xffffffffu, it.first_cut(), 0);
           for (int j = 0; j < nt && ok; ++j) {
             const bool more = j + 1 < nt;
             if (!two) {
               vs = next();
               if (more) ks = next();
             }
+            const bool both = !two && j >= look && j < nt0 && j < nt1;
+            if (both) ok = ok && wait_uniform(b_p, pph[0]) && wait_uniform(b_p + 8, pph[1]);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const int mine = r ? nt1 : nt0;
               if (!ok || j >= mine) continue;
               if (two) vs = next();
-              ok = ok && wait_uniform(b_p + 8 * r, pph[r]);
+              if (!both) ok = ok && wait_uniform(b_p + 8 * r, pph[r]);
               pph[r] ^= 1u;
               if (!ok) continue;
               tc_fence_after();
@@ -791,8 +813,6 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     for (int n = 0; ok; ++n) {
       Item& it = items[n & 1];
       ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
-      // (a warp that gives up still arrives at the barrier that its partners may come to)
-      if (!ok) asm volatile("bar.arrive %0, 128;" ::"r"(1 + r) : "memory");
       if (!ok || it.kind < 0) break;
       const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1;
       const int g = it.g + (split ? r : 0);
@@ -813,14 +833,9 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           if (!dead) limit = max(0, len - a.rows + (it.kind == 1 ? t % a.rows : t) + 1);
         }
       }
-      const int wleast = __reduce_min_sync(0xffffffffu, limit);
-      if (lane == 0) atomicMin(&it.low[r], wleast);
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + r) : "memory");
-      const int glow = *(volatile int*)&it.low[r];
       const bool any = __any_sync(0xffffffffu, valid);
-      const int hold = MODE == PROMPT ? kNone : (j1 + a.page - 1) / a.page * a.page;
-      const int wlow = min(wleast, j1), lim = min(limit, j1);
-      const int streams = split && it.nt[1] > 0 ? 2 : 1;
+      const int lim = min(limit, j1), wlow = __reduce_min_sync(0xffffffffu, lim);
+      const int streams = split && it.nt[1] > 0 ? 2 : 1, look = it.first_cut();
       float mb = -INFINITY, l = 0.f;  // maximum in use, times qscale; sum of the weights
       for (int j = 0; j < mine; ++j) {
         const int jt = j0 + j * BN;
@@ -897,23 +912,25 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           l += (la.x + la.y) + (lb.x + lb.y);
           tmem_wait_st();
         }
-        // some row of the group masks keys that the tile holds (behind the last page it holds zeros)
-        if (min(glow, j1) < min(jt + BN, hold)) {
+        if (j >= look) {
+          // some row masks keys that the tile holds
           const int nt = max(it.nt[0], it.nt[1]);
           const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j + (j + 1 < nt ? 2 * r : r)), vs = vi % NS;
           ok = wait_uniform(smem_u32(&full[vs]), (uint32_t)(vi / NS) & 1u);
           if (!ok) break;
           uint4* v = reinterpret_cast<uint4*>(sKV + (size_t)vs * L::TILE);
           // rows (keys) k0 .. k1 - 1 of the tile, a half of 64 columns after the other
-          const int k0 = max(0, min(glow, j1) - jt), k1 = min(BN, hold - jt), per = (k1 - k0) * 8;
-          for (int q0 = row; q0 < per * HALVES; q0 += 4 * 128) {
+          const int k0 = max(0, min(it.low, j1) - jt), k1 = min(BN, it.hold - jt), per = (k1 - k0) * 8;
+          const bool both = streams == 1 && j < it.nt[0] && j < it.nt[1];
+          const int step = both ? 256 : 128;
+          for (int q0 = both ? r * 128 + row : row; q0 < per * HALVES; q0 += 4 * step) {
             uint4 x[4];
             auto at = [&](int u) {
-              const int q = q0 + u * 128, h = q >= per;
+              const int q = q0 + u * step, h = q >= per;
               return v + h * (HALF / 16) + k0 * 8 + (q - h * per);
             };
 #pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = q0 + u * 128 < per * HALVES ? *at(u) : make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < 4; ++u) x[u] = q0 + u * step < per * HALVES ? *at(u) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t* w = reinterpret_cast<uint32_t*>(&x[u]);
@@ -925,7 +942,6 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[k] &= ~((hit[k] >> 15) * 0xffffu);
                 atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
-                __threadfence_block();
                 *at(u) = x[u];
               }
             }
