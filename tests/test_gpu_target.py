@@ -40,6 +40,7 @@ PROMPTS = [  # dtype, Hq, Hkv, dh, lengths
     ("f32", 3, 1, 40, [33, 100]),
     ("f32", 2, 2, 256, [70]),
     ("f32", 5, 1, 8, [1]),
+    ("f32", 2, 1, 64, [(7 * i) % 19 for i in range(40)]),            # more sequences than a warp has lanes
     ("bf16", 8, 2, 128, [1, 0, 17, 64, 65, 130]),
     ("bf16", 4, 2, 64, [200, 3, 1, 129]),
     ("bf16", 2, 2, 128, [257]),
