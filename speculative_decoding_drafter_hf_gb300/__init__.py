@@ -16,5 +16,6 @@ __all__ = list(_BINDING_NAMES)
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
-        return getattr(_binding, name)
+        globals()[name] = value = getattr(_binding, name)  # (later uses do not come here)
+        return value
     raise AttributeError(name)

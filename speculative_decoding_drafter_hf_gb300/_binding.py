@@ -521,13 +521,14 @@ class _On:
     """The device and stream of one call: every tensor lies on the first one's
     device; the call is made with that device current, on `stream` or the
     device's current stream. New outputs belong to the call's stream."""
-    __slots__ = ("index", "given", "ptr")
+    __slots__ = ("index", "first", "given", "ptr")
 
     def __init__(self, first, stream):
         import torch
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("expected CUDA tensors")
         self.index = first.get_device()
+        self.first = first
         self.given = stream
         if stream is None:
             self.ptr = torch._C._cuda_getCurrentRawStream(self.index)
@@ -535,20 +536,22 @@ class _On:
             self.ptr = stream if isinstance(stream, int) else stream.cuda_stream
 
     def arg(self, t, name, dtype=None, shape=None, contiguous=True):
+        # (one test for the tensors that are right: a small call is bound by these checks)
+        if (t.get_device() == self.index and (dtype is None or t.dtype is dtype)
+                and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+            return t.data_ptr()
         if t.get_device() != self.index:
             raise TypeError(f"{name} must be a CUDA tensor on cuda:{self.index}")
         if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous")
 
     def empty(self, shape, dtype):
-        import torch
         if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.index)
+            return self.first.new_empty(shape, dtype=dtype)
+        import torch
         s = self.given
         if isinstance(s, int):
             s = torch.cuda.ExternalStream(s, device=self.index)
@@ -623,6 +626,8 @@ def verify_tokens(target_logits, draft_tokens, u, noise, *, draft_logits=None, t
     S -= 1
 
     def rows(t, name, n):
+        if t.is_contiguous():
+            return V
         s = t.stride()
         if (s[2] != 1 and V > 1) or (B > 1 and n > 1 and s[0] != n * s[1]):
             raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
@@ -685,7 +690,7 @@ class Pages:
         self.status = torch.zeros(1, dtype=i32, device=k.device)
         d.work, d.status = self._work.data_ptr(), self.status.data_ptr()
         self._d, self._ref = d, ctypes.byref(d)
-        self._i32, self._index = i32, k.get_device()
+        self._i32, self._index, self._dtype, self._layers, self._row = i32, k.get_device(), k.dtype, L, (hkv, dh)
         self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         if ints == 0:  # let a call say what is wrong with the descriptor
             on.call(hf_pages_compact, self._ref, None)
@@ -752,19 +757,21 @@ class Pages:
         """The newest rows of the requests: k and v [layers, T, kv heads, head_dim]
         for layers 0 .. layers - 1, or [T, kv heads, head_dim] with `layer`; entry i's
         rows are offsets[i] .. offsets[i + 1] - 1."""
-        L, _, hkv, _, dh = self.k.shape
-        if k.dim() != (4 if layer is None else 3) or k.shape[-2:] != (hkv, dh) or (layer is None and k.shape[0] > L):
+        shape, ks, vs = k.shape, k.stride(), v.stride()
+        if (len(shape) != (4 if layer is None else 3) or shape[-2:] != self._row
+                or (layer is None and shape[0] > self._layers)):
             raise ValueError("k must be [layers, tokens, kv heads, head_dim], or [tokens, kv heads, head_dim] with layer")
         for t, name in ((k, "k"), (v, "v")):
-            if t.dtype is not self.k.dtype or t.get_device() != self._index:
-                raise TypeError(f"{name} must be {self.k.dtype} on cuda:{self._index}")
-        T = k.shape[-3]
+            if t.dtype is not self._dtype or t.get_device() != self._index:
+                raise TypeError(f"{name} must be {self._dtype} on cuda:{self._index}")
+        T, (hkv, dh) = shape[-3], self._row
         ld = _heads_ld(k, T, hkv, dh, "k")
-        step = k.stride(0) if layer is None and k.shape[0] > 1 else 0
-        if v.shape != k.shape or (T and (_heads_ld(v, T, hkv, dh, "v") != ld or (step and v.stride(0) != step))):
+        layers = shape[0] if layer is None else 1
+        step = ks[0] if layers > 1 else 0
+        if v.shape != shape or (T and vs != ks and (_heads_ld(v, T, hkv, dh, "v") != ld or (step and vs[0] != step))):
             raise ValueError("k and v must have the same shape and strides")
         n = offsets.shape[0] - 1
-        self._call(hf_pages_write, stream, layer or 0, k.shape[0] if layer is None else 1, k.data_ptr(), v.data_ptr(),
+        self._call(hf_pages_write, stream, layer or 0, layers, k.data_ptr(), v.data_ptr(),
                    ld, step, self._ints(requests, n, "requests"), self._ints(offsets, n + 1, "offsets"), n, T)
 
     def attend_workspace(self, q, shared=0):
