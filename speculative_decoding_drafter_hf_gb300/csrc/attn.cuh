@@ -9,6 +9,33 @@
 
 namespace hf {
 
+// Two floats a 64-bit register: one instruction for two multiply-adds, sums or products.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 struct AttnRows {
   int Hq, Hkv, G, dh, esize;
   float qscale;  // scale * log2(e): scores are kept in the base-2 domain
@@ -135,6 +162,21 @@ __device__ __forceinline__ const int32_t* attn_table(const AttnRows& a, int i) {
   return a.table + (size_t)r * a.table_ld;
 }
 
+// Whether the entries from first on, every step-th, have entry 0's pages before `shared`;
+// by one CTA or warp (tid of threads).
+__device__ __forceinline__ void check_prefixes(const AttnRows& a, int first, int step, int tid, int threads) {
+  if (a.shared == 0 || !a.status) return;
+  bool bad = false, skip = false;
+  if (attn_raw_len(a, 0, skip) == 0) return;
+  const int32_t* t0 = attn_table(a, 0);
+  for (int i = first; i < a.n; i += step) {
+    if (attn_raw_len(a, i, skip) == 0) continue;
+    const int32_t* t = attn_table(a, i);
+    for (int j = tid; j < a.shared / a.page; j += threads) bad = bad || __ldg(&t[j]) != __ldg(&t0[j]);
+  }
+  if (bad) atomicOr(a.status, HF_S_BAD);
+}
+
 // Slot of a prompt tile -> sequence and tile within it: a sequence of rows
 // [off_s, off_e) owns the slots [floor(off_s G / BM) + s, floor(off_e G / BM) + s + 1),
 // at least as many as it has tiles, so no prefix sum over the sequences is needed.
@@ -184,9 +226,6 @@ cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
 // prefix and slots of own pieces.
 void attn_tc_sizes(AttnRows& a, int& pre_items, long long& slots);
 cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t st);
-// Entries' lengths and status checks; tensor cores (ctas > 0): the line too.
-cudaError_t launch_attn_plan(const AttnRows& a, int ctas, int heavy, cudaStream_t st);
-
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
 cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st);
 // `pieces`: about how many a row has (how many warps share a row).

@@ -70,14 +70,16 @@ __device__ __forceinline__ bool odd_value(float x) { return !(fabsf(x) < INFINIT
 template <int MODE>
 __device__ __forceinline__ long long key_at(const AttnRows& a, int start, const int32_t* tab, int g, int j, int kv) {
   if (MODE == PROMPT) return (long long)(start + j) * (kv ? a.v_ld : a.k_ld) + (long long)g * a.dh;
-  const int id = __ldg(&tab[j / a.page]);
+  const int shift = 31 - __clz(a.page);  // (a power of two)
+  const int id = __ldg(&tab[j >> shift]);
   if (id < 0 || id >= a.n_pages) return -1;
-  return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
+  return (((((long long)id * a.Hkv + g) << shift) + (j & (a.page - 1))) * a.dh);
 }
 
-// DHT: the head dim, or 0 for any up to 64 * MAXC. pre_x: CTAs (paged) of the prefix.
+// DHT: the head dim, or 0 for any up to 64 * MAXC. Paged: the first pre_x CTAs work on the
+// prefix, those up to all_x on the entries' own keys, the others compare the entries' prefixes.
 template <typename T, int MODE, int MAXC, int DHT, int RPT>
-__global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
+__global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all_x) {
   extern __shared__ __align__(16) float smf[];
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int BM = 8 * RPT;
@@ -91,9 +93,14 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   constexpr int CL = MODE == PROMPT ? CLUSTER : 1;
   const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
+  if (tid == 0) s_low = 0x7fffffff;
   pdl_trigger();
   pdl_wait();
-
+  if (MODE == PAGED && (int)blockIdx.x >= all_x) {
+    if (blockIdx.y == 0) check_prefixes(a, 1 + (int)blockIdx.x - all_x, (int)gridDim.x - all_x, tid, RT);
+    return;
+  }
+  bool bad = false;  // (reported by an entry's first CTA)
   // the item: rows [row0, row0 + nrows) of KV head g, keys [j0, j1)
   const int g = blockIdx.y;
   int row0, nrows, j0 = 0, j1, start = 0, entry = 0, piece = 0, len = 0;
@@ -113,7 +120,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
     nrows = min(BM, a.n * a.rows * a.G - row0);
     j0 = piece * a.pre_keys;
     j1 = min(a.shared, j0 + a.pre_keys);
-    if (__ldcg(&a.eff[0]) == 0)  // nothing is shared then: every row is empty
+    if (attn_len(a, 0, bad) == 0)  // nothing is shared then: every row is empty
       j1 = j0;
     else
       tab = attn_table(a, 0);
@@ -123,7 +130,11 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
     entry = x / a.nown / blocks;
     row0 = x / a.nown % blocks * BM;
     nrows = min(BM, a.rows * a.G - row0);
-    len = __ldcg(&a.eff[entry]);
+    len = attn_len(a, entry, bad);
+    if (piece == 0 && row0 == 0 && g == 0 && tid == 0) {
+      a.eff[entry] = len;  // for the join
+      if (bad && a.status) atomicOr(a.status, HF_S_BAD);
+    }
     j0 = a.shared + piece * a.own_keys;
     j1 = min(len, j0 + a.own_keys);
     if (piece > 0 && j0 >= j1) return;  // piece 0 always reports (a direct call has no other)
@@ -164,15 +175,21 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int first = j0 + rank * BN;
+  for (int e = tid; e < BM * c4; e += RT) {  // q comes with the first K
+    const int r = e / c4, c = (e % c4) * 4;
+    const T* src = static_cast<const T*>(a.q) + c;
+    if (r < nrows) src += token(row0 + r) * a.q_ld + (size_t)head(row0 + r) * dh;
+    if constexpr (F32)
+      copy16(&sq[r * ldq + c], src, r < nrows);
+    else
+      *reinterpret_cast<float4*>(&sq[r * ldq + c]) = r < nrows ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   load(0, first);
   load(1, first);
 
   // this thread's rows: the keys they see
   int limit[RPT];
-  if (tid == 0) {
-    s_odd = j1;
-    s_low = 0x7fffffff;
-  }
+  if (tid == 0) s_odd = j1;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -183,7 +200,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
     if (MODE == PROMPT) {
       limit[i] = t + 1;
     } else if (pre) {
-      const int l = __ldcg(&a.eff[t / a.rows]);
+      const int l = attn_len(a, t / a.rows, bad);
       dead = l == 0;
       limit[i] = max(0, min(a.shared, l - a.rows + t % a.rows + 1));
     } else {
@@ -191,46 +208,45 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
     }
     if (tx == 0 && !dead) atomicMin(&s_low, limit[i]);
   }
-  for (int e = tid; e < BM * c4; e += RT) {
-    const int r = e / c4, c = (e % c4) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < nrows)
-      x = load4(static_cast<const T*>(a.q) + token(row0 + r) * a.q_ld + (size_t)head(row0 + r) * dh + c);
-    *reinterpret_cast<float4*>(&sq[r * ldq + c]) =
-        make_float4(x.x * a.qscale, x.y * a.qscale, x.z * a.qscale, x.w * a.qscale);
-  }
-  __syncthreads();
-  const int low = s_low;
-
-  float m[RPT], l[RPT], o[RPT][MAXC * 4];
+  float m[RPT], l[RPT];
+  uint64_t o2[RPT][MAXC * 2];  // pairs of neighbouring columns
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < MAXC * 4; ++c) o[i][c] = 0.f;
+    for (int c = 0; c < MAXC * 2; ++c) o2[i][c] = 0;
   }
 
   for (int jt = first; jt < j1; jt += CL * BN) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // K; V may still be on its way
     __syncthreads();
     float s[RPT][4];
+    {
+      uint64_t s2[RPT][4];  // sums over the even and the odd dimensions
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+      for (int i = 0; i < RPT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 2
-    for (int d = 0; d < dh; d += 4) {
-      float4 kv[4];
+        for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+#pragma unroll 8
+      for (int d = 0; d < dh; d += 4) {
+        ulonglong2 kv[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sk[(tx + 16 * j) * ldq + d]);
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(&sk[(tx + 16 * j) * ldq + d]);
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) {
-        const float4 qv = *reinterpret_cast<const float4*>(&sq[(ty * RPT + i) * ldq + d]);
+        for (int i = 0; i < RPT; ++i) {
+          const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(&sq[(ty * RPT + i) * ldq + d]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+          for (int j = 0; j < 4; ++j) s2[i][j] = fma2(qv.y, kv[j].y, fma2(qv.x, kv[j].x, s2[i][j]));
+        }
       }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = unpair(s2[i][j]);
+          s[i][j] = (x.x + x.y) * a.qscale;
+        }
     }
     __syncthreads();  // K has been read
     load(0, jt + CL * BN);
@@ -258,11 +274,12 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
       l[i] = l[i] * f + sum;  // this thread's columns; joined at the end
       m[i] = nm;
 #pragma unroll
-      for (int c = 0; c < MAXC * 4; ++c) o[i][c] *= f;
+      for (int c = 0; c < MAXC * 2; ++c) o2[i][c] = mul2(o2[i][c], pair(f, f));
     }
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
     __syncthreads();
     // some row masks keys of this tile: the odd values of V there are set aside
+    const int low = s_low;
     if (low < min(jt + BN, j1)) {
       const int k0 = max(0, low - jt);
       for (int e = tid; e < (BN - k0) * dh; e += RT) {
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
       }
       __syncthreads();
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < BN; j += 4) {
       float4 p[RPT];
 #pragma unroll
@@ -284,21 +301,29 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x) {
 #pragma unroll
         for (int c = 0; c < MAXC; ++c) {
           if (tx * 4 + 64 * c >= dh) continue;
-          const float4 x = *reinterpret_cast<const float4*>(&sv[(j + jj) * ldq + tx * 4 + 64 * c]);
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sv[(j + jj) * ldq + tx * 4 + 64 * c]);
 #pragma unroll
           for (int i = 0; i < RPT; ++i) {
             const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
-            o[i][4 * c + 0] = fmaf(w, x.x, o[i][4 * c + 0]);
-            o[i][4 * c + 1] = fmaf(w, x.y, o[i][4 * c + 1]);
-            o[i][4 * c + 2] = fmaf(w, x.z, o[i][4 * c + 2]);
-            o[i][4 * c + 3] = fmaf(w, x.w, o[i][4 * c + 3]);
+            o2[i][2 * c] = fma2(pair(w, w), x.x, o2[i][2 * c]);
+            o2[i][2 * c + 1] = fma2(pair(w, w), x.y, o2[i][2 * c + 1]);
           }
         }
     }
     __syncthreads();  // V has been read
     load(1, jt + CL * BN);
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // (q, where there was no tile)
   __syncthreads();
+  float o[RPT][MAXC * 4];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+#pragma unroll
+    for (int c = 0; c < MAXC * 2; ++c) {
+      const float2 x = unpair(o2[i][c]);
+      o[i][2 * c] = x.x;
+      o[i][2 * c + 1] = x.y;
+    }
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
 #pragma unroll
@@ -530,7 +555,7 @@ std::mutex g_mu;
 bool g_set[kMaxDev][2][2][5][4] = {};
 
 template <typename T, int MODE, int MAXC, int DHT, int RPT>
-cudaError_t launch_one(const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st) {
+cudaError_t launch_one(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -546,7 +571,7 @@ cudaError_t launch_one(const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st)
     }
   }
   const size_t smem = rows_smem(a.dh, 8 * RPT);
-  if (MODE != PROMPT) return launch_pdl(kern, grid, dim3(RT), smem, st, a, pre_x);
+  if (MODE != PROMPT) return launch_pdl(kern, grid, dim3(RT), smem, st, a, pre_x, all_x);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(RT);
@@ -560,23 +585,23 @@ cudaError_t launch_one(const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st)
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, pre_x);
+  return cudaLaunchKernelEx(&cfg, kern, a, pre_x, all_x);
 }
 
 template <typename T, int MODE, int RPT>
-cudaError_t launch_dh(const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st) {
+cudaError_t launch_dh(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
   constexpr bool F32 = sizeof(T) == 4;
-  if (F32 && a.dh == 64) return launch_one<T, MODE, 1, F32 ? 64 : 0, RPT>(a, pre_x, grid, st);
-  if (F32 && a.dh == 128) return launch_one<T, MODE, 2, F32 ? 128 : 0, RPT>(a, pre_x, grid, st);
-  if (a.dh <= 64) return launch_one<T, MODE, 1, 0, RPT>(a, pre_x, grid, st);
-  if (a.dh <= 128) return launch_one<T, MODE, 2, 0, RPT>(a, pre_x, grid, st);
-  return launch_one<T, MODE, 4, 0, RPT>(a, pre_x, grid, st);
+  if (F32 && a.dh == 64) return launch_one<T, MODE, 1, F32 ? 64 : 0, RPT>(a, pre_x, all_x, grid, st);
+  if (F32 && a.dh == 128) return launch_one<T, MODE, 2, F32 ? 128 : 0, RPT>(a, pre_x, all_x, grid, st);
+  if (a.dh <= 64) return launch_one<T, MODE, 1, 0, RPT>(a, pre_x, all_x, grid, st);
+  if (a.dh <= 128) return launch_one<T, MODE, 2, 0, RPT>(a, pre_x, all_x, grid, st);
+  return launch_one<T, MODE, 4, 0, RPT>(a, pre_x, all_x, grid, st);
 }
 
 template <int MODE, int RPT>
-cudaError_t launch_mode(int dtype, const AttnRows& a, int pre_x, dim3 grid, cudaStream_t st) {
-  return dtype == HF_F32 ? launch_dh<float, MODE, RPT>(a, pre_x, grid, st)
-                         : launch_dh<__nv_bfloat16, MODE, RPT>(a, pre_x, grid, st);
+cudaError_t launch_mode(int dtype, const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
+  return dtype == HF_F32 ? launch_dh<float, MODE, RPT>(a, pre_x, all_x, grid, st)
+                         : launch_dh<__nv_bfloat16, MODE, RPT>(a, pre_x, all_x, grid, st);
 }
 
 // Rows of a thread, over a paged cache: as many as a request has rows for, and as leave
@@ -589,18 +614,19 @@ int paged_rpt(const AttnRows& a) { return a.rows * a.G <= 16 ? 2 : a.rows * a.G 
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st) {
   const long long slots = prompt_slots(a.total, a.n_seq, a.G, 8 * kPromptRpt) * CLUSTER;
   if (slots > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_mode<PROMPT, kPromptRpt>(dtype, a, 0, dim3((unsigned)slots, a.Hkv), st);
+  return launch_mode<PROMPT, kPromptRpt>(dtype, a, 0, 0, dim3((unsigned)slots, a.Hkv), st);
 }
 cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st) {
   const int rpt = paged_rpt(a), bm = 8 * rpt;
   const long long rows = (long long)a.n * a.rows * a.G;
   const long long pre_x = (rows + bm - 1) / bm * a.npre;
   const long long own_x = (long long)a.n * ((a.rows * a.G + bm - 1) / bm) * a.nown;
-  if (pre_x + own_x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(pre_x + own_x), a.Hkv);
-  return rpt == 8   ? launch_mode<PAGED, 8>(dtype, a, (int)pre_x, grid, st)
-         : rpt == 4 ? launch_mode<PAGED, 4>(dtype, a, (int)pre_x, grid, st)
-                    : launch_mode<PAGED, 2>(dtype, a, (int)pre_x, grid, st);
+  const long long all_x = pre_x + own_x, checks = a.shared > 0 && a.status ? std::min(a.n, 152) : 0;
+  if (all_x + checks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(all_x + checks), a.Hkv);
+  return rpt == 8   ? launch_mode<PAGED, 8>(dtype, a, (int)pre_x, (int)all_x, grid, st)
+         : rpt == 4 ? launch_mode<PAGED, 4>(dtype, a, (int)pre_x, (int)all_x, grid, st)
+                    : launch_mode<PAGED, 2>(dtype, a, (int)pre_x, (int)all_x, grid, st);
 }
 
 namespace {
@@ -822,8 +848,7 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
     a.tile0 = reinterpret_cast<int*>(ws + w.tile0);
     e = launch_attn_tc_pages(a, w.pre_items, st);
   } else {
-    e = launch_attn_plan(a, 0, 0, st);
-    if (e == cudaSuccess) e = launch_attn_rows_pages(p->dtype, a, st);
+    e = launch_attn_rows_pages(p->dtype, a, st);
   }
   if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, w.pieces, st);
   return done(e);

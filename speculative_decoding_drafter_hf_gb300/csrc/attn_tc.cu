@@ -158,27 +158,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two floats a 64-bit register: one instruction for two multiply-adds or sums.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t r) {
-  float2 v;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
-  return v;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -463,21 +442,6 @@ __device__ __forceinline__ int scan_tiles(const AttnRows& a, const int* eff, int
   if (lane == 0) tile0[a.n] = carry;
   __syncwarp();
   return carry;
-}
-
-// Whether the entries from first on, every step-th, have entry 0's pages before `shared`;
-// by one CTA or warp (tid of threads).
-__device__ __forceinline__ void check_prefixes(const AttnRows& a, int first, int step, int tid, int threads) {
-  if (a.shared == 0 || !a.status) return;
-  bool bad = false, skip = false;
-  if (attn_raw_len(a, 0, skip) == 0) return;
-  const int32_t* t0 = attn_table(a, 0);
-  for (int i = first; i < a.n; i += step) {
-    if (attn_raw_len(a, i, skip) == 0) continue;
-    const int32_t* t = attn_table(a, i);
-    for (int j = tid; j < a.shared / a.page; j += threads) bad = bad || __ldg(&t[j]) != __ldg(&t0[j]);
-  }
-  if (bad) atomicOr(a.status, HF_S_BAD);
 }
 
 // Element offset in V of key j's row of KV head g.
@@ -1052,7 +1016,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int ctas, int he
       a.eff[i] = len;
       t = entry_places(len - a.shared);
     }
-    if (ctas == 0) continue;  // CUDA cores: pieces of a fixed number of keys
     int x = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1071,7 +1034,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int ctas, int he
     carry = sum;
   }
   if (bad && a.status) atomicOr(a.status, HF_S_BAD);
-  if (ctas > 0 && tid == 0) {
+  if (tid == 0) {
     a.tile0[a.n] = carry;
     *reinterpret_cast<AttnLine*>(a.line) = make_line(carry, a.units, ctas, heavy, prefix_places(a));
   }
@@ -1125,7 +1088,7 @@ cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) {
                      : launch_one<64, PROMPT>(c, mq, mk, mv, grid, st);
 }
 
-cudaError_t launch_attn_plan(const AttnRows& a, int ctas, int heavy, cudaStream_t st) {
+static cudaError_t launch_plan(const AttnRows& a, int ctas, int heavy, cudaStream_t st) {
   const int checks = a.shared > 0 && a.status ? std::min(a.n, 151) : 0;
   return launch_pdl(plan_kernel, dim3(1 + checks), dim3(1024), 0, st, a, ctas, heavy);
 }
@@ -1178,7 +1141,7 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t 
   const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;
   const int grid = (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
   c.small = a.n <= kSmall;
-  if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
+  if (!c.small) e = launch_plan(a, grid, pre_items % grid, st);
   if (e != cudaSuccess) return e;
   return a.dh == 128 ? launch_one<128, PAGED>(c, mq, mk, mv, dim3(grid), st)
                      : launch_one<64, PAGED>(c, mq, mk, mv, dim3(grid), st);
