@@ -10,12 +10,15 @@
 // Everything is fp32 in shared memory and registers: this is the variant for fp32 inputs
 // and for head dims that the tensor-core kernels do not take; bound by the fp32
 // multiply-adds and the shared-memory reads that feed them (RPT = 8: 128 multiply-adds
-// for 12 reads). K and V have one place each, refilled in turn while the other is used:
-// that leaves room for three or four CTAs per SM (8 prompts of 100 to 1201 tokens, heads
-// of 64: 71 us with RPT = 4, 76 us with 8; two places each and two CTAs per SM 103 us). A prompt's rows are
-// few for the GPU and their keys many: a cluster of four CTAs shares a tile of rows, each
-// walking every fourth tile of keys, and joins the parts through distributed shared
-// memory. Over a paged cache, RPT goes by the rows of a request.
+// for 12 reads), which go in pairs, two to an instruction. K and V have one place each,
+// refilled in turn while the other is used: that leaves room for three or four CTAs per SM
+// (8 prompts of 100 to 1201 tokens, heads of 64: 67 us with RPT = 4, 73 us with 8; before
+// the pairs two places each and two CTAs per SM took 103 us, one place each 75). A prompt's
+// rows are few for the GPU and their keys many: a cluster of four CTAs shares a tile of rows,
+// each walking every fourth tile of keys, and joins the parts through distributed shared
+// memory (clusters of two: 71 us). What bounds that call is latency: a scheduler has four
+// warps and issues in 42% of the cycles. Over a paged cache, RPT goes by the rows of a
+// request (8 requests of 8 rows x 2 heads: 17.9 us with 2, 20.8 us with 4).
 //
 // Masked keys: scores are selected, never added to a mask value, so whatever K
 // holds there cannot matter; V's non-finite values in a tile that any row masks
@@ -434,30 +437,43 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all
   }
 }
 
+// Warps of a CTA: four leave few idle ones in the last round (64 x 8 rows over a prefix of
+// 8192, all: 103.7 us, with eight 104.2).
+constexpr int join_warps(int wpr) { return wpr > 4 ? wpr : 4; }
+
 // A row's pieces weighted by 2^(m - max m). A warp takes four neighbouring rows of an
 // entry, lane = (8 columns, row): its loads are whole lines. WPR warps of a CTA share
 // the rows, each joining every WPR-th piece; the CTA's last step joins the warps. SEGS:
 // groups of 64 columns. Pieces that saw nothing hold no values: what lies there is
 // read, and left out. Bound by the reads of the pieces.
 template <typename T, int WPR, int SEGS>
-__global__ void __launch_bounds__(256) join_kernel(AttnRows a) {
+__global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) {
+  constexpr int WARPS = join_warps(WPR);
   constexpr int BATCH = SEGS == 1 ? 4 : SEGS == 2 ? 2 : 1;  // pieces in flight per warp
-  __shared__ float s_acc[WPR > 1 ? 8 : 1][WPR > 1 ? SEGS * 8 : 1][WPR > 1 ? 33 : 1];
-  __shared__ float2 s_ml[8][4];
+  __shared__ float s_acc[WPR > 1 ? WARPS : 1][WPR > 1 ? SEGS * 8 : 1][WPR > 1 ? 33 : 1];
+  __shared__ float2 s_ml[WARPS][4];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR, dh = a.dh;
   const int per = a.rows * a.Hq, fours = (per + 3) / 4;
-  const long long unit = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const long long unit = (long long)blockIdx.x * (WARPS / WPR) + warp / WPR;
   const int entry = (int)(unit / fours), lr = (int)(unit % fours) * 4 + (lane & 3), col = (lane >> 2) * 8;
   bool on = entry < a.n && lr < per;
   const int g = on ? lr / (a.rows * a.G) : 0, t = on ? lr / a.G % a.rows : 0, i = on ? lr % a.G : 0;
+  // (all of them at once: small calls are bound by the chain of dependent loads)
   const int len = on ? __ldcg(&a.eff[entry]) : 0;
+  int t0 = 0, t1 = 0;
+  int4 ln = {};
+  if (a.line && on) {
+    ln = __ldcg(reinterpret_cast<const int4*>(a.line));
+    t0 = __ldcg(&a.tile0[entry]);
+    t1 = __ldcg(&a.tile0[entry + 1]);
+  }
   // the entry's own pieces: `own` of them from number `first` on
   int own = 0, first = 0, slot = 0;
   if (len > 0 && a.line) {
-    const AttnLine line = {__ldcg(&a.line[0]), __ldcg(&a.line[1]), __ldcg(&a.line[2]), __ldcg(&a.line[3])};
-    const int u = unit_of(a, g, t), t0 = __ldcg(&a.tile0[entry]), t1 = __ldcg(&a.tile0[entry + 1]);
+    const AttnLine line = {ln.x, ln.y, ln.z, ln.w};
+    const int u = unit_of(a, g, t);
     if (t1 > t0) {
       first = line.cta(u * line.tiles + t0 + kItemStart);
       own = line.cta(u * line.tiles + t1 - 1) - first + 1;
@@ -635,9 +651,10 @@ cudaError_t join(const AttnRows& a, int pieces, cudaStream_t st) {
   const long long units = (long long)a.n * ((a.rows * a.Hq + 3) / 4);
   // few rows: several warps per row, so that its pieces are read side by side
   const int wpr = units * 2 >= 152 * 32 || pieces <= 2 ? 1 : units * 8 >= 152 * 32 || pieces <= 8 ? 2 : 8;
-  const dim3 grid((unsigned)((units * wpr + 7) / 8));
+  const int warps = join_warps(wpr);
+  const dim3 grid((unsigned)((units * wpr + warps - 1) / warps));
   return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : wpr == 2 ? join_kernel<T, 2, SEGS> : join_kernel<T, 1, SEGS>,
-                    grid, dim3(256), 0, st, a);
+                    grid, dim3(32 * warps), 0, st, a);
 }
 }  // namespace
 
