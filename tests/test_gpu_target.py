@@ -250,6 +250,44 @@ def test_attend_lists_repeats_and_strange_entries(hf):
     assert c.check() == hf.CallStatus.BAD
 
 
+@pytest.mark.parametrize("dtype,dh", [("f32", 64), ("bf16", 32)])
+def test_attend_on_cuda_cores_strange_entries_and_prefixes(hf, dtype, dh):
+    """The same rules where the CTAs look the lengths up for themselves."""
+    k, v, table, lens, refs = _shared_cache(dtype, 2, dh, 16, 64, [5, 60, 33, 9], 6)
+    c = _on_gpu(hf, k, v, table, lens, refs)
+    req = [2, -1, 0, 4, 2] + [3, 1] * 200  # (more entries than CTAs that compare prefixes)
+    n = len(req)
+    q = _randn((n, 3, 4, dh), dtype, 5)
+    good = [i for i in range(n) if 0 <= req[i] < 4]
+    want, tol = R.pages(q[good], k[0], v[0], table, lens, dh ** -0.5, dtype == "bf16", [req[i] for i in good])
+    for shared in (0, 64):
+        o = R.to64(c.attend(q.cuda(), _i32(req), shared=shared))
+        R.check_attention(o[good], want, tol)
+        assert (o[[1, 3]] == 0).all() and c.check() == hf.CallStatus.BAD
+        o = R.to64(c.attend(q[good].cuda(), _i32([req[i] for i in good]), shared=shared))
+        R.check_attention(o, want, tol)
+        assert not c.check()
+    # one entry whose prefix is another (the last of 203): reported, the others as before
+    t = [list(r) for r in table]
+    t[0][2], t[0][4] = t[0][4], t[0][2]
+    c = _on_gpu(hf, k, v, t, lens, refs)
+    o = R.to64(c.attend(q[:203].cuda(), _i32([2, 2] + [1] * 200 + [0]), shared=64))
+    want, tol = R.pages(q[:202], k[0], v[0], table, lens, dh ** -0.5, dtype == "bf16", [2, 2] + [1] * 200)
+    R.check_attention(o[:202], want, tol)
+    assert c.check() == hf.CallStatus.BAD
+    # an empty first entry: nothing is shared, so the others' lengths break the rule
+    c = _on_gpu(hf, k, v, table, [0] + lens[1:], refs)
+    assert (c.attend(q[:4].cuda(), shared=64) == 0).all()
+    assert c.check() == hf.CallStatus.BAD
+    # lengths of an entry that fit neither the table nor the prefix
+    for bad in (10 ** 6, -5, 40):
+        c = _on_gpu(hf, k, v, table, [lens[0], bad, lens[2], lens[3]], refs)
+        o = R.to64(c.attend(q[:4].cuda(), shared=64))
+        want, tol = R.pages(q[:4], k[0], v[0], table, [lens[0], 0, lens[2], lens[3]], dh ** -0.5, dtype == "bf16")
+        R.check_attention(o, want, tol)
+        assert c.check() == hf.CallStatus.BAD
+
+
 def test_attend_bad_pages_and_unequal_prefixes_are_reported(hf):
     k, v, table, lens, refs = _shared_cache("bf16", 2, 128, 16, 64, [5, 60, 33], 4)
     q = _randn((3, 2, 8, 128), "bf16", 5)
