@@ -53,14 +53,7 @@ __device__ __forceinline__ void copy16(float* dst, const void* src, bool on) {
                : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
   const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
   const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
@@ -444,8 +437,11 @@ constexpr int join_warps(int wpr) { return wpr > 4 ? wpr : 4; }
 // A row's pieces weighted by 2^(m - max m). A warp takes four neighbouring rows of an
 // entry, lane = (8 columns, row): its loads are whole lines. WPR warps of a CTA share
 // the rows, each joining every WPR-th piece; the CTA's last step joins the warps. SEGS:
-// groups of 64 columns. Pieces that saw nothing hold no values: what lies there is
-// read, and left out. Bound by the reads of the pieces.
+// groups of 64 columns of a warp, all of them where warps share rows (24 x 40 rows over a
+// prefix of 32768, all: 50.6 us, by 64 columns 52.1), else one, with four pieces in flight
+// (64 x 8 rows over 8192, all: 101.4 us, all columns 102.9). Pieces that saw nothing
+// hold no values: what lies there is read, and left out. Bound by the latency of the look-ups
+// and the reads of the pieces.
 template <typename T, int WPR, int SEGS>
 __global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) {
   constexpr int WARPS = join_warps(WPR);
@@ -457,8 +453,9 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR, dh = a.dh;
   const int per = a.rows * a.Hq, fours = (per + 3) / 4;
   const long long unit = (long long)blockIdx.x * (WARPS / WPR) + warp / WPR;
-  const int entry = (int)(unit / fours), lr = (int)(unit % fours) * 4 + (lane & 3), col = (lane >> 2) * 8;
-  bool on = entry < a.n && lr < per;
+  const int entry = (int)(unit / fours), lr = (int)(unit % fours) * 4 + (lane & 3);
+  const int col = blockIdx.y * 64 * SEGS + (lane >> 2) * 8;
+  bool on = entry < a.n && lr < per && col < dh;
   const int g = on ? lr / (a.rows * a.G) : 0, t = on ? lr / a.G % a.rows : 0, i = on ? lr % a.G : 0;
   // (all of them at once: small calls are bound by the chain of dependent loads)
   const int len = on ? __ldcg(&a.eff[entry]) : 0;
@@ -528,7 +525,7 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) 
     for (int s = 0; s < SEGS; ++s)
 #pragma unroll
       for (int c = 0; c < 8; ++c) s_acc[warp][s * 8 + c][lane] = acc[s][c];
-    if (col == 0) s_ml[warp][lane & 3] = make_float2(m, l);
+    if (lane < 4) s_ml[warp][lane & 3] = make_float2(m, l);
     __syncthreads();
     if (sub) return;
 #pragma unroll
@@ -652,8 +649,8 @@ cudaError_t join(const AttnRows& a, int pieces, cudaStream_t st) {
   // few rows: several warps per row, so that its pieces are read side by side
   const int wpr = units * 2 >= 152 * 32 || pieces <= 2 ? 1 : units * 8 >= 152 * 32 || pieces <= 8 ? 2 : 8;
   const int warps = join_warps(wpr);
-  const dim3 grid((unsigned)((units * wpr + warps - 1) / warps));
-  return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : wpr == 2 ? join_kernel<T, 2, SEGS> : join_kernel<T, 1, SEGS>,
+  const dim3 grid((unsigned)((units * wpr + warps - 1) / warps), wpr == 1 ? (a.dh + 63) / 64 : 1);
+  return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : wpr == 2 ? join_kernel<T, 2, SEGS> : join_kernel<T, 1, 1>,
                     grid, dim3(32 * warps), 0, st, a);
 }
 }  // namespace
