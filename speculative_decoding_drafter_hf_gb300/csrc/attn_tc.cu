@@ -517,6 +517,10 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (tid >= 64 && tid < 67) {  // (the first copies would wait for them)
+    const CUtensorMap* map = tid == 64 ? &mq : tid == 65 ? &mk : &mv;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+  }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   __syncthreads();
   tc_fence_after();
