@@ -9,7 +9,7 @@
 //
 // Two launches. verify_stats reads every logit once: (row, chunk) CTAs form
 // the chunk's maximum and sum of exponentials (T = 0: maximum and its lowest
-// index, target rows only). verify_race: each (request, chunk) CTA joins its
+// index, or that the chunk holds a NaN or +infinity; target rows only). verify_race: each (request, chunk) CTA joins its
 // request's chunks, finds the stop slot, and runs the race over its chunk of
 // that slot's rows; the request's last CTA (ticket) joins the chunks. Bound by the
 // reads of the logits: 64 requests x 7 drafts, 100352 tokens, bf16 and fp32 logits, 282 MB
@@ -104,9 +104,11 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, flo
   m = mm;
 }
 
-// (value, lowest index) of the larger of two.
+// (value, lowest index) of the larger of two. kOdd: a part with a NaN or +infinity in it,
+// and so is what it is joined with.
+constexpr int kOdd = -2;
 __device__ __forceinline__ void best(float& v, int& i, float v2, int i2) {
-  if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
+  if (i2 == kOdd || (i2 >= 0 && i != kOdd && (i < 0 || v2 > v || (v2 == v && i2 < i)))) {
     v = v2;
     i = i2;
   }
@@ -122,7 +124,9 @@ __device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t,
   if (t == 0.f) {
     float v = kNegInf;
     int idx = -1;
+    bool odd = false;  // (a comparison with NaN is false)
     auto one = [&](int i, float x) {
+      odd = odd || !(x < INFINITY);
       if (x > v || (x == v && i < idx)) {
         v = x;
         idx = i;
@@ -130,12 +134,15 @@ __device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t,
     };
     for_row<T, UN>(row, i0, i1, one, [&](int i, const float* x, int n) {
 #pragma unroll
-      for (int k = 0; k < UN * VE; ++k)  // rising indices: the first of equals stays
+      for (int k = 0; k < UN * VE; ++k) {  // rising indices: the first of equals stays
+        odd = odd || !(x[k] < INFINITY);
         if (x[k] > v) {
           v = x[k];
           idx = i + k / VE * (VT * VE) + k % VE;
         }
+      }
     });
+    if (odd) idx = kOdd;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       best(v, idx, __shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, idx, o));

@@ -1,0 +1,45 @@
+"""Rules of the target-side calls at their edges, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import _target_ref as R
+from test_gpu_target import DT, _gen, hf  # noqa: F401 (hf is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- verification
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("V,pad", [(9, 0), (3001, 0), (70001, 5)])
+def test_greedy_rows_without_a_largest_logit_are_refused(hf, xt, V, pad):
+    """T = 0: NaN, +infinity or nothing above -infinity in a row that is read refuses the request, wherever
+    in the row it stands; in a row that is not read it does not matter."""
+    B, S, nan, inf = 11, 3, float("nan"), float("inf")
+    x = (torch.randn((B, S + 1, V + pad), generator=_gen(V)) * 2.5).to(DT[xt])
+    x[9, :, ::2] = -inf  # masked tokens are no fault
+    tok = x[:, :S, :V].float().argmax(-1).int()
+    x[1, 0, 0] = nan
+    x[2, 1, V - 1] = nan
+    x[3, 3, V // 2] = nan  # the row of the next token
+    x[4, 0, V // 3] = inf
+    x[5, 2, V - 2] = inf
+    x[6, 1] = -inf
+    tok[7, 0] = (tok[7, 0] + 1) % V  # not the largest: the rows behind are not read
+    x[7, 1, 0], x[7, 2], x[7, 3, 1] = nan, -inf, inf
+    tok[8, 1] = (tok[8, 1] + 1) % V
+    x[8, 1, 5] = nan
+    x[10, 3, 0] = nan  # behind the drafts: n_draft is 2
+    nd = torch.full((B,), S, dtype=torch.int32)
+    nd[10] = 2
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    n, t = hf.verify_tokens(x.cuda()[..., :V], tok.cuda(), torch.zeros(B, S).cuda(), torch.ones(B, V).cuda(),
+                            temperature=torch.zeros(B).cuda(), n_draft=nd.cuda(), status=status)
+    n, t = n.tolist(), t.tolist()
+    assert hf.CallStatus(int(status)) == hf.CallStatus.BAD
+    for b in range(B):
+        if b in (0, 7, 9, 10):
+            a, want, _ = R.verify(R.to64(x[b, :, :V]), None, tok[b].tolist(), int(nd[b]), [0.0] * S, np.ones(V), 0.0)
+            assert (n[b], t[b]) == (a, want), b
+        else:
+            assert (n[b], t[b]) == (0, [-1] * (S + 1)), b
