@@ -559,9 +559,10 @@ hf_status hf_pages_extend(const hf_pages* p, const int32_t* requests, const int3
  * int32 [n + 1]) of k and v become the last tokens of its request, in layers
  * layer .. layer + layers - 1. k, v: DEVICE [layers, total, heads * head_dim] with row
  * stride ld and layer stride layer_stride (elements), 16-byte aligned, strides
- * multiples of 16 bytes. Rows of a bad entry (out of range, a request named
- * twice, more rows than the request has tokens, a page id out of range) are
- * skipped (HF_S_BAD). The pages written must be the request's alone, as
+ * multiples of 16 bytes. Rows of a bad entry (bounds or request out of range, a
+ * request named twice, more rows than the request has tokens, a page id out of
+ * range) are skipped (HF_S_BAD); offsets that decrease set HF_S_BAD and nothing is
+ * written. Rows of no entry are not read. The pages written must be the request's alone, as
  * hf_pages_extend leaves them. */
 hf_status hf_pages_write(const hf_pages* p, int32_t layer, int32_t layers, const void* k,
                          const void* v, int64_t ld, int64_t layer_stride,

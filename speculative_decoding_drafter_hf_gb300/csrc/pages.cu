@@ -476,14 +476,22 @@ __global__ void __launch_bounds__(CT) write_kernel(hf_pages p, WriteArgs a) {
   const int esize = p.dtype == HF_F32 ? 4 : 2;
   const int hv = p.head_dim * esize / 16, vecs = p.n_kv_heads * hv;  // 16-byte pieces of a head, of a row
   const long long block = (long long)p.n_kv_heads * p.page * hv;
-  const int first = __ldcg(&a.off[0]), end = __ldcg(&a.off[a.n]);
+  // bounds that decrease name rows twice, or name entries that the search does not find
+  bool falls = false, range = true;
+  for (int i = threadIdx.x; i <= a.n; i += CT) {
+    const int x = __ldcg(&a.off[i]);
+    falls = falls || (i > 0 && x < __ldcg(&a.off[i - 1]));
+    range = range && x >= 0 && x <= a.total;
+  }
+  if (blockIdx.x == 0 && (falls || !range)) flag(p, HF_S_BAD);
+  if (__syncthreads_or(falls)) return;
   for (long long u = (long long)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < units;
        u += (long long)gridDim.x * (CT / 32)) {
     const int t = (int)(u / groups), c0 = (int)(u % groups) * kCopies;
-    if (t < first || t >= end) continue;
     const int e = find_entry(a.off, a.n, t);
     const int o0 = __ldcg(&a.off[e]), o1 = __ldcg(&a.off[e + 1]), r = a.req ? __ldcg(&a.req[e]) : e;
-    bool ok = t >= o0 && t < o1 && end <= a.total && r >= 0 && r < p.n_requests;
+    if (t < o0 || t >= o1) continue;  // nobody's row
+    bool ok = o0 >= 0 && o1 <= a.total && r >= 0 && r < p.n_requests;
     if (a.req)  // named twice: its rows would have two sources
       for (int i = lane; i < a.n; i += 32) ok = ok && (i == e || __ldcg(&a.req[i]) != r);
     ok = __all_sync(0xffffffffu, ok);

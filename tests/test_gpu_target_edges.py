@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import _target_ref as R
-from test_gpu_target import DT, _gen, hf  # noqa: F401 (hf is a fixture)
+from test_gpu_target import DT, _gen, _i32, _randn, _same, _small, hf  # noqa: F401 (hf is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,25 @@ def test_greedy_rows_without_a_largest_logit_are_refused(hf, xt, V, pad):
             assert (n[b], t[b]) == (a, want), b
         else:
             assert (n[b], t[b]) == (0, [-1] * (S + 1)), b
+
+
+# ----------------------------------------------------------------- page tables
+def test_write_bounds(hf):
+    """Bounds that decrease: nothing is written. Bounds out of range: the rows of their entries are skipped."""
+    c, ref = _small(hf)
+    bad = hf.CallStatus.BAD
+    k, v = (_randn((2, 8, 2, 16), "bf16", s) for s in (1, 2))
+    for ends, rs in [([0, 8, 4], [2, 0]), ([0, 4, 2, 5], [2, 0, 1]), ([3, 0], [2]), ([5, 3, 4], [2, 0]), ([-2, 3], [2]),
+                     ([0, 9], [2])]:
+        c.write(k.cuda(), v.cuda(), _i32(ends), _i32(rs))
+        assert c.check() == bad, ends
+        _same(c, ref, f"write {ends}")
+    for ends, rs, first in [([0, 4, 9], [2, 0], 4), ([2, 8, 9], [2, 0], 8)]:
+        c.write(k.cuda(), v.cuda(), _i32(ends), _i32(rs))
+        assert c.check() == bad, ends
+        ref.write([2], [ends[0], first], R.to64(k), R.to64(v))
+        _same(c, ref, f"write {ends}")
+    c.write(k.cuda(), v.cuda(), _i32([1, 3]), _i32([0]))  # rows before and behind the entries are nobody's
+    assert not c.check()
+    ref.write([0], [1, 3], R.to64(k), R.to64(v))
+    _same(c, ref, "write some rows")
