@@ -104,14 +104,20 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, flo
   m = mm;
 }
 
-// (value, lowest index) of the larger of two. kOdd: a part with a NaN or +infinity in it,
-// and so is what it is joined with.
-constexpr int kOdd = -2;
+// (value, lowest index) of the larger of two.
 __device__ __forceinline__ void best(float& v, int& i, float v2, int i2) {
-  if (i2 == kOdd || (i2 >= 0 && i != kOdd && (i < 0 || v2 > v || (v2 == v && i2 < i)))) {
+  if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
     v = v2;
     i = i2;
   }
+}
+// The same for parts of a row (T = 0): kOdd, a NaN or +infinity in it, stays.
+constexpr int kOdd = -2;
+__device__ __forceinline__ void best_logit(float& v, int& i, float v2, int i2) {
+  if (i2 == kOdd)
+    i = kOdd;
+  else if (i != kOdd)
+    best(v, i, v2, i2);
 }
 
 template <typename T>
@@ -126,33 +132,38 @@ __device__ __forceinline__ void stats_cta(const VArgs& a, const T* row, float t,
     int idx = -1;
     bool odd = false;  // (a comparison with NaN is false)
     auto one = [&](int i, float x) {
-      odd = odd || !(x < INFINITY);
+      odd |= !(x < INFINITY);
       if (x > v || (x == v && i < idx)) {
         v = x;
         idx = i;
       }
     };
     for_row<T, UN>(row, i0, i1, one, [&](int i, const float* x, int n) {
+      float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int k = 0; k < UN * VE; ++k) {  // rising indices: the first of equals stays
-        odd = odd || !(x[k] < INFINITY);
-        if (x[k] > v) {
-          v = x[k];
-          idx = i + k / VE * (VT * VE) + k % VE;
-        }
+      for (int k = 0; k < UN * VE; ++k) {
+        odd |= !(x[k] < INFINITY);
+        if (k >= 4) t4[k & 3] = fmaxf(t4[k & 3], x[k]);
+      }
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      if (top > v) {  // (seldom, after the first steps) rising indices: the first of equals
+        v = top;
+#pragma unroll
+        for (int k = UN * VE - 1; k >= 0; --k)
+          if (x[k] == top) idx = i + k / VE * (VT * VE) + k % VE;
       }
     });
     if (odd) idx = kOdd;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      best(v, idx, __shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, idx, o));
+      best_logit(v, idx, __shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, idx, o));
     if (lane == 0) {
       sm[warp] = v;
       si[warp] = idx;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int w = 1; w < VT / 32; ++w) best(v, idx, sm[w], si[w]);
+      for (int w = 1; w < VT / 32; ++w) best_logit(v, idx, sm[w], si[w]);
       *out = make_float2(v, __int_as_float(idx));
     }
     return;
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
       for (int k = lane; k < a.nchunk; k += 32) {
         const float2 v = __ldcg(&st[k]);
         if (cold)
-          best(m, idx, v.x, __float_as_int(v.y));
+          best_logit(m, idx, v.x, __float_as_int(v.y));
         else
           join(m, l, v.x, v.y, c);
       }
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
       for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
         if (cold)
-          best(m, idx, m2, __shfl_xor_sync(0xffffffffu, idx, o));
+          best_logit(m, idx, m2, __shfl_xor_sync(0xffffffffu, idx, o));
         else
           join(m, l, m2, __shfl_xor_sync(0xffffffffu, l, o), c);
       }
