@@ -134,14 +134,20 @@ __device__ __forceinline__ AttnLine make_line(int tiles, int units, int ctas, in
   return l;
 }
 
+// Lengths, tables, lists, offsets and, on CUDA cores, the rows themselves come from
+// calls that may still be running when a CTA starts (programmatic launches): they are read
+// after pdl_wait and never through the non-coherent path, which is for data that nobody
+// writes while the kernel lives. Many CTAs look the same lengths, bounds and ids up: they
+// go through the L1 (8 fp32 prompts 66.8 us, past it 68.7).
+
 // Length of entry i as the call takes it: 0 for entries that break a rule (bad set).
 __device__ __forceinline__ int attn_raw_len(const AttnRows& a, int i, bool& bad) {
-  const int r = a.req ? __ldg(&a.req[i]) : i;
+  const int r = a.req ? a.req[i] : i;
   if (r < 0 || r >= a.n_requests) {
     bad = true;
     return 0;
   }
-  const int len = __ldg(&a.lens[r]);
+  const int len = a.lens[r];
   if (len < 0 || len > (long long)a.table_ld * a.page || (len > 0 && len < a.shared)) {
     bad = true;
     return 0;
@@ -158,7 +164,7 @@ __device__ __forceinline__ int attn_len(const AttnRows& a, int i, bool& bad) {
 }
 
 __device__ __forceinline__ const int32_t* attn_table(const AttnRows& a, int i) {
-  const int r = a.req ? __ldg(&a.req[i]) : i;
+  const int r = a.req ? a.req[i] : i;
   return a.table + (size_t)r * a.table_ld;
 }
 
@@ -172,7 +178,7 @@ __device__ __forceinline__ void check_prefixes(const AttnRows& a, int first, int
   for (int i = first; i < a.n; i += step) {
     if (attn_raw_len(a, i, skip) == 0) continue;
     const int32_t* t = attn_table(a, i);
-    for (int j = tid; j < a.shared / a.page; j += threads) bad = bad || __ldg(&t[j]) != __ldg(&t0[j]);
+    for (int j = tid; j < a.shared / a.page; j += threads) bad = bad || t[j] != t0[j];
   }
   if (bad) atomicOr(a.status, HF_S_BAD);
 }
@@ -191,14 +197,14 @@ __device__ __forceinline__ PromptTile prompt_tile(const AttnRows& a, int slot, i
   int lo = 0, hi = a.n_seq;  // the last sequence whose first slot is at or before `slot`
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    const long long first = (long long)max(0, min(__ldg(&a.off[mid]), a.total)) * G / BM + mid;
+    const long long first = (long long)max(0, min(a.off[mid], a.total)) * G / BM + mid;
     if (first <= slot)
       lo = mid;
     else
       hi = mid;
   }
   PromptTile t{};
-  const int s0 = __ldg(&a.off[lo]), s1 = __ldg(&a.off[lo + 1]);
+  const int s0 = a.off[lo], s1 = a.off[lo + 1];
   t.ok = s0 >= 0 && s0 <= s1 && s1 <= a.total;
   if (!t.ok) return t;
   t.start = s0;
@@ -213,8 +219,8 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a) {
   if (!a.status) return;
   bool bad = false;
   for (int s = threadIdx.x; s <= a.n_seq; s += blockDim.x) {
-    const int x = __ldg(&a.off[s]);
-    bad = bad || x < 0 || x > a.total || (s > 0 && x < __ldg(&a.off[s - 1]));
+    const int x = a.off[s];
+    bad = bad || x < 0 || x > a.total || (s > 0 && x < a.off[s - 1]);
   }
   if (bad) atomicOr(a.status, HF_S_BAD);
 }

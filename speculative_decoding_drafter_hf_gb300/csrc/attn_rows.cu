@@ -54,7 +54,7 @@ __device__ __forceinline__ void copy16(float* dst, const void* src, bool on) {
 }
 
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 r = __ldcg(reinterpret_cast<const uint2*>(p));
   const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
   const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
   return make_float4(a.x, a.y, b.x, b.y);
@@ -67,7 +67,7 @@ template <int MODE>
 __device__ __forceinline__ long long key_at(const AttnRows& a, int start, const int32_t* tab, int g, int j, int kv) {
   if (MODE == PROMPT) return (long long)(start + j) * (kv ? a.v_ld : a.k_ld) + (long long)g * a.dh;
   const int shift = 31 - __clz(a.page);  // (a power of two)
-  const int id = __ldg(&tab[j >> shift]);
+  const int id = tab[j >> shift];
   if (id < 0 || id >= a.n_pages) return -1;
   return (((((long long)id * a.Hkv + g) << shift) + (j & (a.page - 1))) * a.dh);
 }

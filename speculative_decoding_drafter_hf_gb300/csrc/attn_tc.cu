@@ -265,7 +265,7 @@ struct TileOrder {
 #pragma unroll
     for (int k = 0; k < kSorted / 32; ++k) {
       const int s = (threadIdx.x & 31) + 32 * k;
-      const int s0 = s < a.n_seq ? __ldg(&a.off[s]) : 0, s1 = s < a.n_seq ? __ldg(&a.off[s + 1]) : 0;
+      const int s0 = s < a.n_seq ? a.off[s] : 0, s1 = s < a.n_seq ? a.off[s + 1] : 0;
       const bool ok = s0 >= 0 && s0 <= s1 && s1 <= a.total;
       start[k] = s0;
       len[k] = ok ? s1 - s0 : 0;
@@ -448,7 +448,7 @@ __device__ __forceinline__ int scan_tiles(const AttnRows& a, const int* eff, int
 template <int MODE>
 __device__ __forceinline__ long long v_at(const AttnRows& a, const Item& it, int g, int j) {
   if (MODE == PROMPT) return (long long)(it.start + j) * a.v_ld + (long long)g * a.dh;
-  const int id = __ldg(&attn_table(a, it.entry)[j / a.page]);
+  const int id = attn_table(a, it.entry)[j / a.page];
   if (id < 0 || id >= a.n_pages) return -1;
   return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
 }
@@ -560,7 +560,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             } else {
               int z = a.n_pages * a.Hkv;  // behind the pool: reads zeros
               if (key < j1) {
-                const int id = __ldg(&tab[key / a.page]);
+                const int id = tab[key / a.page];
                 if (id >= 0 && id < a.n_pages)
                   z = id * a.Hkv + g + r;
                 else if (a.status)

@@ -51,6 +51,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Inputs may be outputs of the launch before (drafts and logits of hf_draft_tokens among
+// them): they are read after pdl_wait and never through the non-coherent path. A request's few
+// numbers, which many CTAs read, go through the L1, logits and noise past it.
+
 // (a T below the normal numbers would make 1 / T infinite)
 __device__ __forceinline__ bool temp_ok(float t) { return t == 0.f || (t >= 1.17549435e-38f && t < INFINITY); }
 
@@ -70,13 +74,13 @@ __device__ __forceinline__ void for_row(const T* row, int i0, int i1, F&& one, G
   uint4 r[UN];
 #pragma unroll
   for (int k = 0; k < UN; ++k)
-    if (tid + k * VT < nv) r[k] = __ldg(p + tid + k * VT);
+    if (tid + k * VT < nv) r[k] = __ldcg(p + tid + k * VT);
   for (int v0 = tid; v0 < nv; v0 += VT * UN) {
     const int v1 = v0 + VT * UN;  // the next loads are on their way meanwhile
     uint4 next[UN];
 #pragma unroll
     for (int k = 0; k < UN; ++k)
-      if (v1 + k * VT < nv) next[k] = __ldg(p + v1 + k * VT);
+      if (v1 + k * VT < nv) next[k] = __ldcg(p + v1 + k * VT);
     float x[UN * VE];
     const int n = min(UN, (nv - v0 + VT - 1) / VT);
 #pragma unroll
@@ -216,8 +220,8 @@ __global__ void __launch_bounds__(VT) verify_stats(VArgs a) {
   const int per = a.y ? 2 * a.S + 1 : a.S + 1;
   const int b = r / per, s = r % per;
   if (s == 0 && chunk == 0 && threadIdx.x == 0) a.tickets[b] = 0;
-  const float t = a.temp ? __ldg(&a.temp[b]) : 1.f;
-  const int nd = a.n_draft ? __ldg(&a.n_draft[b]) : a.S;
+  const float t = a.temp ? a.temp[b] : 1.f;
+  const int nd = a.n_draft ? a.n_draft[b] : a.S;
   if (!temp_ok(t)) return;
   float2* out = a.stats + ((size_t)b * (2 * a.S + 1) + s) * a.nchunk + chunk;
   if (s <= a.S) {
@@ -230,11 +234,11 @@ __global__ void __launch_bounds__(VT) verify_stats(VArgs a) {
 }
 
 __device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
   v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
 }
 __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
-  const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
   const __nv_bfloat16* t = reinterpret_cast<const __nv_bfloat16*>(&x);
   v[0] = to_f(t[0]), v[1] = to_f(t[1]), v[2] = to_f(t[2]), v[3] = to_f(t[3]);
 }
@@ -249,8 +253,8 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   // the last requests first: their logits may still be in the L2
   const int chunk = blockIdx.x % a.nrchunk, b = a.B - 1 - blockIdx.x / a.nrchunk;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, S = a.S;
-  const float t = a.temp ? __ldg(&a.temp[b]) : 1.f;
-  const int nd = a.n_draft ? __ldg(&a.n_draft[b]) : S;
+  const float t = a.temp ? a.temp[b] : 1.f;
+  const int nd = a.n_draft ? a.n_draft[b] : S;
   const bool range_ok = temp_ok(t) && nd >= 0 && nd <= S;
   const bool cold = t == 0.f;
   const float c = cold ? 0.f : 1.4426950408889634f / t;
@@ -259,10 +263,10 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   const bool has = warp == 0 && range_ok && lane < nd;
   int d = 0;
   float xv = 0.f, yv = 0.f, uv = 0.f;
-  if (has) d = __ldg(&a.tok[(size_t)b * S + lane]);
+  if (has) d = a.tok[(size_t)b * S + lane];
   const bool names = d >= 0 && d < a.V;
   if (has && names && !cold) {
-    uv = __ldg(&a.u[(size_t)b * S + lane]);
+    uv = a.u[(size_t)b * S + lane];
     xv = to_f(static_cast<const TX*>(a.x)[((size_t)b * (S + 1) + lane) * a.x_ld + d]);
     if (a.y) yv = to_f(static_cast<const TY*>(a.y)[((size_t)b * S + lane) * a.y_ld + d]);
   }
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   if (s_bad || cold) {  // uniform in the request: no race
     if (chunk == 0 && tid <= S) {
       int v = -1;
-      if (!s_bad) v = tid < stop ? __ldg(&a.tok[(size_t)b * S + tid]) : tid == stop ? __float_as_int(sl[stop]) : -1;
+      if (!s_bad) v = tid < stop ? a.tok[(size_t)b * S + tid] : tid == stop ? __float_as_int(sl[stop]) : -1;
       out[tid] = v;
       if (tid == 0) {
         a.n_acc[b] = s_bad ? 0 : stop + 1;
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   const TX* x = static_cast<const TX*>(a.x) + ((size_t)b * (S + 1) + stop) * a.x_ld;
   const bool residual = stop < nd;
   const TY* y = residual && a.y ? static_cast<const TY*>(a.y) + ((size_t)b * S + stop) * a.y_ld : nullptr;
-  const int dtok = residual && !a.y ? __ldg(&a.tok[(size_t)b * S + stop]) : -1;
+  const int dtok = residual && !a.y ? a.tok[(size_t)b * S + stop] : -1;
   const float* e = a.e + (size_t)b * a.e_ld;
   const float mp = sm[stop], ip = 1.f / sl[stop];
   const float mq = y ? sm[S + 1 + stop] : 0.f, iq = y ? 1.f / sl[S + 1 + stop] : 0.f;
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
     run(i + 2, xv[2], yv[2], n.z);
     run(i + 3, xv[3], yv[3], n.w);
   }
-  for (int i = i4 + tid; i < i1; i += VT) run(i, to_f(x[i]), y ? to_f(y[i]) : 0.f, __ldg(&e[i]));
+  for (int i = i4 + tid; i < i1; i += VT) run(i, to_f(x[i]), y ? to_f(y[i]) : 0.f, __ldcg(&e[i]));
   auto cta_best = [&]() {  // of the CTA's threads, in warp 0
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   cta_best();
   if (iw < 0 && residual) {  // p - q nowhere positive (rare): p itself, by this CTA alone
     for (int i = tid; i < a.V; i += VT) {
-      const float p = ex2((to_f(x[i]) - mp) * c) * ip, s = __fdividef(p, __ldg(&e[i]));
+      const float p = ex2((to_f(x[i]) - mp) * c) * ip, s = __fdividef(p, __ldcg(&e[i]));
       if (p > 0.f && (iw < 0 ? s == s : s > vw)) {
         vw = s;
         iw = i;
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   }
   if (warp != 0) return;
   const int next = iw;
-  if (lane <= S) out[lane] = next < 0 ? -1 : lane < stop ? __ldg(&a.tok[(size_t)b * S + lane]) : lane == stop ? next : -1;
+  if (lane <= S) out[lane] = next < 0 ? -1 : lane < stop ? a.tok[(size_t)b * S + lane] : lane == stop ? next : -1;
   if (lane == 0) {
     a.n_acc[b] = next < 0 ? 0 : stop + 1;
     if (next < 0 && a.status) atomicOr(a.status, HF_S_BAD);

@@ -1,0 +1,23 @@
+"""Rules of the target-side calls that show without a GPU."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "speculative_decoding_drafter_hf_gb300", "csrc")
+TARGET = ["attn.cuh", "attn_rows.cu", "attn_tc.cu", "pages.cu", "pages.cuh", "verify.cu"]
+
+
+def _code(name):
+    with open(os.path.join(CSRC, name)) as f:
+        s = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    return re.sub(r"//[^\n]*", "", s)
+
+
+@pytest.mark.parametrize("name", TARGET)
+def test_what_an_earlier_call_may_still_write_is_read_coherently(name):
+    """The kernels start while the launch before them runs, which may write any of their inputs: lengths, tables,
+    drafts, logits, rows. The non-coherent path is for data that nobody writes while the kernel lives."""
+    code = _code(name)
+    assert "__ldg(" not in code and "ld.global.nc" not in code and "__restrict__" not in code
