@@ -527,6 +527,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a);
+  __syncwarp();  // (its lanes' loops end apart, and the next instruction wants the warp together)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -939,6 +940,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
                             : part_own_unit(a, it.part, g, it.t0 + tl, row_head);
 #pragma unroll 1
         for (int q = 0; q < DH; q += 32) {
+          __syncwarp();  // (lanes without a row come back early: the load wants the warp together)
           float o[32];
           if (mine > 0) {
             tmem_ld32(to + q, o);

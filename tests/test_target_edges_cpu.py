@@ -21,3 +21,16 @@ def test_what_an_earlier_call_may_still_write_is_read_coherently(name):
     drafts, logits, rows. The non-coherent path is for data that nobody writes while the kernel lives."""
     code = _code(name)
     assert "__ldg(" not in code and "ld.global.nc" not in code and "__restrict__" not in code
+
+
+def test_warps_are_together_where_an_instruction_wants_them():
+    """tcgen05.ld and setmaxnreg are executed by a whole warp: behind code that lanes leave apart (a loop whose
+    length goes by the lane, a `continue` of some) a __syncwarp() comes first."""
+    code = _code("attn_tc.cu")
+    kernel = code[code.index("tc_kernel("):]
+    before = kernel[:kernel.index('"setmaxnreg')]
+    assert re.search(r"check_offsets\(a\);\s*__syncwarp\(\);", before)
+    loops = re.split(r"for \(int q = 0; q < DH; q \+= 32\) \{", kernel)[1:]
+    assert len(loops) == 2
+    assert "continue" not in loops[0][:loops[0].index("tmem_st32")]  # the rescaling: no lane leaves it
+    assert "if (!valid) continue;" in loops[1] and re.match(r"\s*__syncwarp\(\);", loops[1])
