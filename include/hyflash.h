@@ -394,7 +394,10 @@ int64_t hf_launch_count(const hf_handle* h);
 
 /* Limit, in clock cycles, of the ring-tile wait of the CUDA-core attention
  * kernel (the fp32 path of hf_draft / hf_round) of handle h; with h NULL,
- * of hf_attention_noalloc's ring-tile wait. cycles < 0 restores the default
+ * of hf_attention_noalloc's ring-tile wait; 0 also goes for every wait of the
+ * tensor-core kernels of hf_attention_prompt and hf_attention_pages (they load
+ * nothing, set HF_S_TIMEOUT, and their output is not valid), which otherwise keep
+ * the default. cycles < 0 restores the default
  * (about 2 s); 0 makes that wait give up at once, so the kernel takes its
  * expiry path: it raises the timeout bit, lets its copies land (default
  * limit), drops its ring tile (the window is left out of that draft) and

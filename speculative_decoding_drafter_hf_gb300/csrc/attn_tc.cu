@@ -30,6 +30,7 @@
 // Masked keys: scores are selected by position. V's non-finite values in a tile that
 // some row masks are set to zero in shared memory (0 * NaN would reach every row) and
 // added back at the end to the rows that see them.
+#include <atomic>
 #include <mutex>
 
 #include "attn.cuh"
@@ -200,6 +201,7 @@ struct TcArgs {
   int pre_items;   // paged: items of the prefix
   int wide;        // rows of out start on 32 bytes
   int small;       // paged: every CTA plans for itself
+  int wait;        // 0: every wait gives up before it begins (set by a test)
 };
 
 // What a CTA works on at a time, written by warp 2. Tile r's rows are tokens
@@ -529,7 +531,9 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a);
   __syncwarp();  // (its lanes' loops end apart, and the next instruction wants the warp together)
 
-  if (warp < 4) {
+  if (c.wait == 0) {
+    *abort_flag = 1;
+  } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---- loads: a stream's K(0), the rows, then V(j), K(j+1) through the ring
@@ -989,6 +993,10 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   __syncwarp();
   __syncthreads();
   if (*abort_flag) {
+    // the lengths and the line that the join reads may be missing: it takes entries without
+    // tokens for empty, and looks at nothing else of them
+    if (MODE == PAGED && c.small && blockIdx.x == 0)
+      for (int i = tid; i < a.n; i += TCT) a.eff[i] = 0;
     if (tid == 0) {
       if (a.status) atomicOr(a.status, HF_S_TIMEOUT);
       // the copies still in flight land before the CTA's shared memory goes
@@ -1049,6 +1057,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int ctas, int he
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
 bool g_set[kMaxDev][2][2] = {};
+std::atomic<long long> g_wait{kWaitCycles};
 
 template <int DH, int MODE>
 cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
@@ -1071,6 +1080,8 @@ cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mq, const CUtensorMap
 
 }  // namespace
 
+void set_target_wait_limit(long long cycles) { g_wait.store(cycles); }
+
 bool attn_tc_ok(int dtype, int dh) { return dtype == HF_BF16 && (dh == 64 || dh == 128); }
 
 namespace {
@@ -1081,6 +1092,7 @@ cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st) {
   TcArgs c{};
   c.a = a;
   c.wide = wide_rows(a);
+  c.wait = g_wait.load() > 0;
   c.tb = 128 / a.G;
   c.blocks = (int)prompt_slots(a.total, a.n_seq, 1, 2 * c.tb);
   c.box_rows = BN;
@@ -1137,6 +1149,7 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t 
   c.blocks = (int)((tokens + 2 * c.tb - 1) / (2 * c.tb));
   c.box_rows = a.page;
   c.wide = wide_rows(a);
+  c.wait = g_wait.load() > 0;
   c.pre_items = pre_items;
   CUtensorMap mq, mk, mv;
   cudaError_t e = make_map_3d(&mq, a.q, a.dh, a.Hq, tokens, a.dh, a.q_ld, a.G, c.tb);

@@ -647,6 +647,8 @@ cudaError_t launch_conv_reset(const Dims& d, int n_req, const int32_t* reqs, flo
 // limit of hf_attention_noalloc's ring-tile waits (clock cycles; 0 = give up
 // at once, the failure-detection tests' hook)
 void set_noalloc_wait_limit(long long cycles);
+// the same for the waits of hf_attention_prompt and hf_attention_pages (attn_tc.cu)
+void set_target_wait_limit(long long cycles);
 
 cudaError_t launch_prefill_finish(int n_req, const int32_t* lens, const int32_t* reqs,
                                   int64_t* pos, cudaStream_t st);

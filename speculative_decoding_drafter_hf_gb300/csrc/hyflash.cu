@@ -1635,6 +1635,7 @@ hf_status hf_debug_set_wait_limit(hf_handle* h, int64_t cycles) {
   const long long lim = cycles < 0 ? hf::kWaitCycles : (long long)cycles;
   if (!h) {
     hf::set_noalloc_wait_limit(lim);
+    hf::set_target_wait_limit(lim);
     return HF_OK;
   }
   h->d.wait = lim;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import _target_ref as R
-from test_gpu_target import DT, _gen, _i32, _randn, _same, _small, hf  # noqa: F401 (hf is a fixture)
+from test_gpu_target import DT, _gen, _i32, _on_gpu, _randn, _same, _shared_cache, _small, hf  # noqa: F401 (hf is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,37 @@ def test_write_bounds(hf):
     assert not c.check()
     ref.write([0], [1, 3], R.to64(k), R.to64(v))
     _same(c, ref, "write some rows")
+
+
+# ------------------------------------------------------------------- attention
+@pytest.mark.parametrize("n,shared", [(3, 64), (3, 0), (300, 64)])
+def test_waits_that_run_out_are_reported(hf, n, shared):
+    """With a limit of 0 every wait gives up: the status says so, nothing is read outside the buffers whatever the
+    workspace held, and the next call is right."""
+    from speculative_decoding_drafter_hf_gb300 import _binding as B
+    k, v, table, lens, refs = _shared_cache("bf16", 2, 128, 16, 64, [5, 60, 33], 4)
+    c = _on_gpu(hf, k, v, table, lens, refs)
+    req = [i % 3 for i in range(n)]
+    q = _randn((n, 2, 8, 128), "bf16", 5)
+    d, list_ = q.cuda(), _i32(req)
+    ws = c.attend_workspace(d, shared)
+    p = [_randn((90, h, 128), "bf16", h) for h in (8, 2, 2)]
+    dp, off = [t.cuda() for t in p], _i32([0, 40, 90])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for fill in (0, 0x7f, 0xff):
+        ws.fill_(fill)
+        try:
+            assert B.hf_debug_set_wait_limit(None, 0) == 0
+            o = c.attend(d, list_, shared=shared, workspace=ws)
+            hf.attention_prompt(*dp, off, status=status)
+            torch.cuda.synchronize()
+        finally:
+            B.hf_debug_set_wait_limit(None, -1)
+        assert c.check() == hf.CallStatus.TIMEOUT and int(status) == hf.CallStatus.TIMEOUT
+        assert n > 256 or (o == 0).all()
+        status.zero_()
+    want, tol = R.pages(q, k[0], v[0], table, lens, 128 ** -0.5, True, req)
+    R.check_attention(R.to64(c.attend(d, list_, shared=shared, workspace=ws)), want, tol)
+    want, tol = R.prompt(*p, [0, 40, 90], 128 ** -0.5, True)
+    R.check_attention(R.to64(hf.attention_prompt(*dp, off, status=status)), want, tol)
+    assert not c.check() and int(status) == 0
