@@ -50,7 +50,7 @@ struct Tc {
   static constexpr int TILE = BN * DH * 2;            // bytes of a K, V or Q tile
   static constexpr int SLOTS = DH == 128 ? 5 : 10;    // ring of K and V tiles
   static constexpr int O_COL = 256;                   // TMEM: S0 | S1 | O0 | O1
-  static constexpr int BARS = 2 * SLOTS + 14;
+  static constexpr int BARS = 2 * SLOTS + 16;  // (an even number: 16 bytes for what comes behind)
   static constexpr size_t smem() { return (size_t)(2 + SLOTS) * TILE + BARS * 8 + 16 + 2 * 80 + 48 + (2 * kSmall + 2) * 4; }
 };
 
@@ -489,6 +489,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   uint64_t* i_full = q_full + 8;   // [2] items
   uint64_t* i_empty = q_full + 10; // [2]
   uint64_t* n_full = q_full + 12;  // the next CTA's index has come
+  uint64_t* drained = q_full + 13; // after a wait that ran out: the products have ended
   uint4* answer = reinterpret_cast<uint4*>(full + L::BARS);
   Item* items = reinterpret_cast<Item*>(answer + 1);  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
@@ -507,6 +508,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(n_full, 1);
+    mbar_init(drained, 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
@@ -723,7 +725,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           const PromptTile t = a.n_seq <= kSorted ? order.at(idx / a.Hkv)
                                                   : prompt_tile(a, c.blocks - 1 - idx / a.Hkv, 2 * c.tb, 1);
           if (make_item<MODE>(c, idx, it, nullptr, t)) put(it);
-          // (also after a failure: the answer asked for has to land)
+          // (also after a failure: the answer asked for lands before the CTA goes)
           const bool came = wait_uniform(smem_u32(n_full), (uint32_t)taken & 1u);
           ++taken;
           idx = came ? taken_cta(answer) : -1;
@@ -997,6 +999,10 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     // tokens for empty, and looks at nothing else of them
     if (MODE == PAGED && c.small && blockIdx.x == 0)
       for (int i = tid; i < a.n; i += TCT) a.eff[i] = 0;
+    if (warp == 1) {  // the products still in flight end before their operands and TMEM go
+      mma_commit(elect_one(), smem_u32(drained));  // (the lane that issued them)
+      wait_uniform(smem_u32(drained), 0);
+    }
     if (tid == 0) {
       if (a.status) atomicOr(a.status, HF_S_TIMEOUT);
       // the copies still in flight land before the CTA's shared memory goes

@@ -34,3 +34,13 @@ def test_warps_are_together_where_an_instruction_wants_them():
     assert len(loops) == 2
     assert "continue" not in loops[0][:loops[0].index("tmem_st32")]  # the rescaling: no lane leaves it
     assert "if (!valid) continue;" in loops[1] and re.match(r"\s*__syncwarp\(\);", loops[1])
+
+
+def test_nothing_is_in_flight_when_a_cta_gives_up():
+    """Behind a wait that ran out: the products issued are waited for (one commit behind them all) before TMEM is
+    given back and the CTA ends, as the copies are."""
+    code = _code("attn_tc.cu")
+    tail = code[code.rindex("if (*abort_flag) {"):code.index("if (warp == 1) tmem_dealloc")]
+    assert re.search(r"mma_commit\(elect_one\(\), smem_u32\(drained\)\);\s*wait_uniform\(smem_u32\(drained\), 0\);", tail)
+    assert tail.count("mbar_wait(") == 2 and tail.rstrip().endswith("tc_fence_after();")
+    assert "mbar_init(drained, 1)" in code
