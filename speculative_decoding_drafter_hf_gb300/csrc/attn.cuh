@@ -214,11 +214,11 @@ __device__ __forceinline__ PromptTile prompt_tile(const AttnRows& a, int slot, i
   return t;
 }
 
-// One CTA's check of the whole list of sequence bounds.
-__device__ __forceinline__ void check_offsets(const AttnRows& a) {
+// Check of the whole list of sequence bounds, by one CTA or warp (tid of threads).
+__device__ __forceinline__ void check_offsets(const AttnRows& a, int tid, int threads) {
   if (!a.status) return;
   bool bad = false;
-  for (int s = threadIdx.x; s <= a.n_seq; s += blockDim.x) {
+  for (int s = tid; s <= a.n_seq; s += threads) {
     const int x = a.off[s];
     bad = bad || x < 0 || x > a.total || (s > 0 && x < a.off[s - 1]);
   }

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all
   const int32_t* tab = nullptr;
   const bool pre = MODE == PAGED && (int)blockIdx.x < pre_x;
   if (MODE == PROMPT) {
-    if (blockIdx.x == 0 && g == 0) check_offsets(a);
+    if (blockIdx.x == 0 && g == 0) check_offsets(a, tid, RT);
     const PromptTile t = prompt_tile(a, (int)((gridDim.x - 1 - blockIdx.x) / CL), BM, a.G);
     if (!t.ok) return;  // (all CTAs of the cluster)
     start = t.start;

@@ -530,7 +530,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a);
+  if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a, tid, TCT);
   __syncwarp();  // (its lanes' loops end apart, and the next instruction wants the warp together)
 
   if (c.wait == 0) {
@@ -730,6 +730,7 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           ++taken;
           idx = came ? taken_cta(answer) : -1;
           ok = ok && came;
+          if (idx == 0) check_offsets(a, lane, 32);  // (CTA 0 never starts then)
           __syncwarp();
         }
       } else {

@@ -29,7 +29,7 @@ def test_warps_are_together_where_an_instruction_wants_them():
     code = _code("attn_tc.cu")
     kernel = code[code.index("tc_kernel("):]
     before = kernel[:kernel.index('"setmaxnreg')]
-    assert re.search(r"check_offsets\(a\);\s*__syncwarp\(\);", before)
+    assert re.search(r"check_offsets\(a, tid, TCT\);\s*__syncwarp\(\);", before)
     loops = re.split(r"for \(int q = 0; q < DH; q \+= 32\) \{", kernel)[1:]
     assert len(loops) == 2
     assert "continue" not in loops[0][:loops[0].index("tmem_st32")]  # the rescaling: no lane leaves it
@@ -44,3 +44,11 @@ def test_nothing_is_in_flight_when_a_cta_gives_up():
     assert re.search(r"mma_commit\(elect_one\(\), smem_u32\(drained\)\);\s*wait_uniform\(smem_u32\(drained\), 0\);", tail)
     assert tail.count("mbar_wait(") == 2 and tail.rstrip().endswith("tc_fence_after();")
     assert "mbar_init(drained, 1)" in code
+
+
+def test_the_bounds_of_prompts_are_checked_whoever_takes_the_first_item():
+    """Items are the launch's CTAs, and one that has not started can be taken over by another: also the first, whose
+    work includes the look at the bounds."""
+    code = _code("attn_tc.cu")
+    loop = code[code.index("take_next_cta(answer, n_full);"):]
+    assert re.search(r"idx = came \? taken_cta\(answer\) : -1;.*?if \(idx == 0\) check_offsets\(a, lane, 32\);", loop, re.S)
