@@ -692,6 +692,9 @@ class Pages:
         self._d, self._ref = d, ctypes.byref(d)
         self._i32, self._index, self._dtype, self._layers, self._row = i32, k.get_device(), k.dtype, L, (hkv, dh)
         self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        with torch.cuda.device(self._index):
+            if not torch.cuda.is_current_stream_capturing():  # calls may come on any stream: both are zero by now
+                torch.cuda.current_stream().synchronize()
         if ints == 0:  # let a call say what is wrong with the descriptor
             on.call(hf_pages_compact, self._ref, None)
 

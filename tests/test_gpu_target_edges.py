@@ -67,6 +67,27 @@ def test_write_bounds(hf):
     _same(c, ref, "write some rows")
 
 
+def test_a_new_cache_is_ready_on_every_stream(hf):
+    """The cache's own buffers are set up when the constructor returns, whatever the current stream still has to do."""
+    _small(hf)[0].truncate(_i32([3]))  # (a kernel's first launch may wait for the whole device)
+    parts = [torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((1, 6, 1, 8, 8),) * 2]
+    table, lens, refs = _i32([[0, 1], [2, -1]]), _i32([9, 3]), _i32([1, 1, 1, 0, 0, 0])
+    keep = _i32([2, 3])
+    used = [torch.full((64,), 77, dtype=torch.int32, device="cuda") for _ in range(20000)]
+    torch.cuda.synchronize()
+    del used  # (what the cache's scratch finds in its memory)
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)
+    c = hf.Pages(*parts, table, lens, refs)
+    c.truncate(keep, stream=s)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        got = lens.tolist(), table.tolist(), refs.tolist()
+    torch.cuda.synchronize()
+    assert got == ([2, 3], [[0, -1], [2, -1]], [1, 0, 1, 0, 0, 0])
+    assert not c.check()
+
+
 # ------------------------------------------------------------------- attention
 @pytest.mark.parametrize("n,shared", [(3, 64), (3, 0), (300, 64)])
 def test_waits_that_run_out_are_reported(hf, n, shared):
