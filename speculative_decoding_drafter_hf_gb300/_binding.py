@@ -709,9 +709,13 @@ class Pages:
                    torch.zeros(n_requests, **ints), torch.zeros(n_pages, **ints))
 
     def check(self):
-        """Read and clear the status word (synchronises)."""
+        """Read and clear the status word. Waits for the device: for calls on every stream."""
+        import torch
+        torch.cuda.synchronize(self._index)
         s = CallStatus(int(self.status.item()))
-        self.status.zero_()
+        if s:
+            self.status.zero_()
+            torch.cuda.synchronize(self._index)  # before a call on another stream writes to it
         return s
 
     def _ints(self, t, n, name):

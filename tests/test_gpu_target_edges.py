@@ -88,6 +88,21 @@ def test_a_new_cache_is_ready_on_every_stream(hf):
     assert not c.check()
 
 
+def test_check_waits_for_every_stream(hf):
+    c, _ = _small(hf)
+    c.truncate(_i32([3]))  # (its first launch may wait for the whole device)
+    s = torch.cuda.Stream()
+    keep = _i32([11])
+    req = _i32([2])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    c.truncate(keep, req, stream=s)
+    assert c.check() == hf.CallStatus.BAD
+    torch.cuda.synchronize()
+    assert not c.check()
+
+
 # ------------------------------------------------------------------- attention
 @pytest.mark.parametrize("n,shared", [(3, 64), (3, 0), (300, 64)])
 def test_waits_that_run_out_are_reported(hf, n, shared):
