@@ -775,7 +775,7 @@ class Pages:
         ld = _heads_ld(k, T, hkv, dh, "k")
         layers = shape[0] if layer is None else 1
         step = ks[0] if layers > 1 else 0
-        if v.shape != shape or (T and vs != ks and (_heads_ld(v, T, hkv, dh, "v") != ld or (step and vs[0] != step))):
+        if v.shape != shape or (T and vs != ks and (_heads_ld(v, T, hkv, dh, "v") != ld or (layers > 1 and vs[0] != step))):
             raise ValueError("k and v must have the same shape and strides")
         n = offsets.shape[0] - 1
         self._call(hf_pages_write, stream, layer or 0, layers, k.data_ptr(), v.data_ptr(),

@@ -67,6 +67,24 @@ def test_write_bounds(hf):
     _same(c, ref, "write some rows")
 
 
+def test_write_takes_the_strides_that_it_says(hf):
+    """Rows and layers with strides of their own; K that is the same in every layer, beside V that is not."""
+    c, ref = _small(hf)
+    x = _randn((2, 8, 7, 16), "bf16", 3)  # one projection's output: K and V are heads of its rows
+    d = x.cuda()
+    c.write(d[:, 1:5, 3:5], d[:, 1:5, 5:7], _i32([0, 4]), _i32([2]))
+    ref.write([2], [0, 4], R.to64(x[:, 1:5, 3:5]), R.to64(x[:, 1:5, 5:7]))
+    _same(c, ref, "parts of a projection")
+    both = d[:1, :6, :2].expand(2, 6, 2, 16)
+    c.write(both, both, _i32([0, 6]), _i32([2]))
+    ref.write([2], [0, 6], R.to64(both), R.to64(both))
+    _same(c, ref, "the same rows in every layer")
+    with pytest.raises(ValueError):
+        c.write(both, d[:, :6, :2], _i32([0, 6]), _i32([2]))
+    _same(c, ref, "refused")
+    assert not c.check()
+
+
 def test_a_new_cache_is_ready_on_every_stream(hf):
     """The cache's own buffers are set up when the constructor returns, whatever the current stream still has to do."""
     _small(hf)[0].truncate(_i32([3]))  # (a kernel's first launch may wait for the whole device)
