@@ -243,6 +243,18 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
   v[0] = to_f(t[0]), v[1] = to_f(t[1]), v[2] = to_f(t[2]), v[3] = to_f(t[3]);
 }
 
+// u q < p by logarithms, for a p that 32 bits hold badly or not at all (a draft far below the
+// largest logit, a small T): x, y the draft's logits, mp, lp and mq, lq the rows' statistics. A
+// logit of -infinity has the probability 0, every other one more.
+__device__ __noinline__ bool accepts_small(float u, float x, float mp, float lp, bool sampled, float y, float mq, float lq,
+                                           float t) {
+  if (!(x > kNegInf)) return false;
+  if (u == 0.f || (sampled && y == kNegInf)) return true;
+  const double c = 1.4426950408889634 / t;
+  const double q = sampled ? ((double)y - mq) * c - log2((double)lq) : 0.0;
+  return log2((double)u) + q < ((double)x - mp) * c - log2((double)lp);
+}
+
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
   __shared__ float sm[2 * VMAXS + 1], sl[2 * VMAXS + 1];
@@ -310,13 +322,17 @@ __global__ void __launch_bounds__(VT) verify_race(VArgs a) {
         pass = has && idx == d;
       } else {
         row_bad = !(sl[lane] > 0.f && sl[lane] < INFINITY);
-        float q = 1.f;
+        float q = 1.f, mq = 0.f, lq = 1.f;
         if (has && a.y) {
-          const float lq = sl[S + 1 + lane];
+          mq = sm[S + 1 + lane];
+          lq = sl[S + 1 + lane];
           row_bad = row_bad || !(lq > 0.f && lq < INFINITY);
-          q = ex2((yv - sm[S + 1 + lane]) * c) / lq;
+          q = ex2((yv - mq) * c) / lq;
         }
-        pass = has && !row_bad && uv * q < ex2((xv - sm[lane]) * c) / sl[lane];
+        if (has && !row_bad) {
+          const float p = ex2((xv - sm[lane]) * c) / sl[lane];
+          pass = p > 1e-30f ? uv * q < p : accepts_small(uv, xv, sm[lane], sl[lane], a.y != nullptr, yv, mq, lq, t);
+        }
       }
     }
     const unsigned fails = ~__ballot_sync(0xffffffffu, pass);

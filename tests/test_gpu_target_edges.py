@@ -45,6 +45,29 @@ def test_greedy_rows_without_a_largest_logit_are_refused(hf, xt, V, pad):
             assert (n[b], t[b]) == (0, [-1] * (S + 1)), b
 
 
+def test_drafts_whose_probabilities_are_below_the_smallest_float(hf):
+    """u q < p by the formula, not by numbers that have become zero."""
+    V, inf = 50, float("inf")
+    rows = [  # x(d), y(d), T, u, accepted
+        (-300.0, -300.0, 1.0, 0.0, True), (-300.0, -310.0, 1.0, 0.5, True), (-300.0, -290.0, 1.0, 0.5, False),
+        (-300.0, -inf, 1.0, 0.5, True), (-inf, -300.0, 1.0, 0.0, False), (-1.0, -1.0, 0.002, 0.0, True),
+        (-1.0, -1.1, 0.002, 0.99, True), (-1.0, -0.9, 0.002, 0.01, False), (-300.0, -300.5, 1.0, 0.999, True),
+        (-300.0, -299.5, 1.0, 0.7, False), (-300.0, -299.5, 1.0, 0.5, True), (-90.0, -inf, 1.0, 0.0, True),
+        (-inf, -inf, 1.0, 0.0, False), (-1.0, -2.0, 1.0, 0.9, True), (-3.0, -1.0, 1.0, 0.9, False)]
+    B = len(rows)
+    x, y = torch.full((B, 2, V), -1000.0), torch.full((B, 1, V), -1000.0)
+    x[:, :, 0] = y[:, :, 0] = 0.0
+    for b, (xd, yd, *_) in enumerate(rows):
+        x[b, 0, 1], y[b, 0, 1] = xd, yd
+    tok = torch.ones((B, 1), dtype=torch.int32)
+    u, temp = torch.tensor([[r[3]] for r in rows]), torch.tensor([r[2] for r in rows])
+    n, _ = hf.verify_tokens(x.cuda(), tok.cuda(), u.cuda(), torch.ones(B, V).cuda(), draft_logits=y.cuda(), temperature=temp.cuda())
+    assert [v == 2 for v in n.tolist()] == [r[4] for r in rows]
+    # drafts chosen greedily: q = 1
+    n, _ = hf.verify_tokens(x.cuda(), tok.cuda(), torch.zeros(B, 1).cuda(), torch.ones(B, V).cuda(), temperature=temp.cuda())
+    assert [v == 2 for v in n.tolist()] == [r[0] > -inf for r in rows]
+
+
 # ----------------------------------------------------------------- page tables
 def test_write_bounds(hf):
     """Bounds that decrease: nothing is written. Bounds out of range: the rows of their entries are skipped."""
