@@ -9,8 +9,8 @@
 // threads, RPT x 4 scores each, then the same rows times the value columns 4 tx + 64 c.
 // Everything is fp32 in shared memory and registers: this is the variant for fp32 inputs
 // and for head dims that the tensor-core kernels do not take; bound by the fp32
-// multiply-adds and the shared-memory reads that feed them (RPT = 8: 128 multiply-adds
-// for 12 reads), which go in pairs, two to an instruction. K and V have one place each,
+// multiply-adds and the shared-memory reads that feed them (RPT = 4: 64 multiply-adds
+// for 8 reads), which go in pairs, two to an instruction. K and V have one place each,
 // refilled in turn while the other is used: that leaves room for three or four CTAs per SM
 // (8 prompts of 100 to 1201 tokens, heads of 64: 67 us with RPT = 4, 73 us with 8; before
 // the pairs two places each and two CTAs per SM took 103 us, one place each 75). A prompt's
@@ -18,7 +18,9 @@
 // each walking every fourth tile of keys, and joins the parts through distributed shared
 // memory (clusters of two: 71 us). What bounds that call is latency: a scheduler has four
 // warps and issues in 42% of the cycles. Over a paged cache, RPT goes by the rows of a
-// request (8 requests of 8 rows x 2 heads: 17.9 us with 2, 20.8 us with 4).
+// request (8 requests of 8 rows x 2 heads: 17.9 us with 2, 20.8 us with 4; of 8 rows x 8
+// heads over 1424 tokens each, the first 1024 in common: 28.9 us with 4, 26.8 us with 8, but 64
+// such requests 121 and 133 us, and 8 of one KV head of 32 17.5 and 23.4 us: no 8).
 //
 // Masked keys: scores are selected, never added to a mask value, so whatever K
 // holds there cannot matter; V's non-finite values in a tile that any row masks
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) 
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-bool g_set[kMaxDev][2][2][5][4] = {};
+bool g_set[kMaxDev][2][2][5][2] = {};
 
 template <typename T, int MODE, int MAXC, int DHT, int RPT>
 cudaError_t launch_one(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
@@ -575,7 +577,7 @@ cudaError_t launch_one(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaS
   auto* kern = rows_kernel<T, MODE, MAXC, DHT, RPT>;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][DHT ? 3 + (DHT == 128) : MAXC / 2][RPT / 4 + (RPT == 8)];
+    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][DHT ? 3 + (DHT == 128) : MAXC / 2][RPT / 4];
     if (!set || dev >= kMaxDev) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)rows_smem(DHT ? DHT : 64 * MAXC, 8 * RPT));
@@ -617,10 +619,9 @@ cudaError_t launch_mode(int dtype, const AttnRows& a, int pre_x, int all_x, dim3
                          : launch_dh<__nv_bfloat16, MODE, RPT>(a, pre_x, all_x, grid, st);
 }
 
-// Rows of a thread, over a paged cache: as many as a request has rows for, and as leave
-// room for two CTAs per SM (8 rows and a head dim of 128: 118 KB).
+// Rows of a thread, over a paged cache: by the rows of a request.
 constexpr int kPromptRpt = 4;
-int paged_rpt(const AttnRows& a) { return a.rows * a.G <= 16 ? 2 : a.rows * a.G <= 32 || a.dh > 64 ? 4 : 8; }
+int paged_rpt(const AttnRows& a) { return a.rows * a.G <= 16 ? 2 : 4; }
 
 }  // namespace
 
@@ -637,9 +638,8 @@ cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st
   const long long all_x = pre_x + own_x, checks = a.shared > 0 && a.status ? std::min(a.n, 152) : 0;
   if (all_x + checks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(all_x + checks), a.Hkv);
-  return rpt == 8   ? launch_mode<PAGED, 8>(dtype, a, (int)pre_x, (int)all_x, grid, st)
-         : rpt == 4 ? launch_mode<PAGED, 4>(dtype, a, (int)pre_x, (int)all_x, grid, st)
-                    : launch_mode<PAGED, 2>(dtype, a, (int)pre_x, (int)all_x, grid, st);
+  return rpt == 4 ? launch_mode<PAGED, 4>(dtype, a, (int)pre_x, (int)all_x, grid, st)
+                  : launch_mode<PAGED, 2>(dtype, a, (int)pre_x, (int)all_x, grid, st);
 }
 
 namespace {

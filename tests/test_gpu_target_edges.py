@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import _target_ref as R
+import test_gpu_target as T
 from test_gpu_target import DT, _gen, _i32, _on_gpu, _randn, _same, _shared_cache, _small, hf  # noqa: F401 (hf is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -176,3 +177,10 @@ def test_waits_that_run_out_are_reported(hf, n, shared):
     want, tol = R.prompt(*p, [0, 40, 90], 128 ** -0.5, True)
     R.check_attention(R.to64(hf.attention_prompt(*dp, off, status=status)), want, tol)
     assert not c.check() and int(status) == 0
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,dh,page,rows,shared,own", [
+    ("f32", 16, 2, 64, 16, 8, 64, [0, 1, 8, 30, 300, None]), ("f32", 8, 1, 64, 16, 5, 0, [3, 200]),
+    ("bf16", 8, 1, 32, 32, 8, 32, [40, 7])])
+def test_attend_more_than_32_rows_of_a_kv_head_on_cuda_cores(hf, dtype, hq, hkv, dh, page, rows, shared, own):
+    T.test_attend(hf, dtype, hq, hkv, dh, page, rows, shared, own)
