@@ -184,3 +184,54 @@ def test_waits_that_run_out_are_reported(hf, n, shared):
     ("bf16", 8, 1, 32, 32, 8, 32, [40, 7])])
 def test_attend_more_than_32_rows_of_a_kv_head_on_cuda_cores(hf, dtype, hq, hkv, dh, page, rows, shared, own):
     T.test_attend(hf, dtype, hq, hkv, dh, page, rows, shared, own)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,dh,lens", [
+    ("f32", 4, 2, 80, [1, 70, 33]), ("f32", 3, 1, 120, [65, 2]), ("f32", 4, 1, 128, [130, 1]), ("f32", 2, 2, 200, [40]),
+    ("bf16", 4, 2, 96, [90, 3]), ("bf16", 5, 1, 112, [33, 70]), ("bf16", 2, 1, 72, [0, 129]), ("bf16", 2, 2, 136, [66])])
+def test_prompt_head_dims_between(hf, dtype, hq, hkv, dh, lens):
+    T.test_prompt(hf, dtype, hq, hkv, dh, lens)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,dh,page,rows,shared,own", [
+    ("f32", 4, 2, 80, 16, 8, 64, [0, 30, 300, None]), ("f32", 3, 1, 120, 8, 1, 0, [1, 77]),
+    ("f32", 4, 2, 128, 32, 16, 32, [20, 100]), ("bf16", 4, 2, 96, 16, 8, 64, [5, 200, None]),
+    ("bf16", 6, 2, 112, 64, 3, 0, [64, 130]), ("bf16", 2, 1, 72, 16, 1, 32, [1, 90])])
+def test_attend_head_dims_between(hf, dtype, hq, hkv, dh, page, rows, shared, own):
+    T.test_attend(hf, dtype, hq, hkv, dh, page, rows, shared, own)
+
+
+def _in_rows(x, pad, fill=0.0):
+    """x [rows, heads, dh] on the GPU as part of rows that are `pad` elements longer, 16 bytes into them."""
+    rows, heads, dh = x.shape
+    first = 16 // x.element_size()
+    buf = torch.full((rows, heads * dh + pad), fill, dtype=x.dtype, device="cuda")
+    part = buf[:, first:first + heads * dh].unflatten(1, (heads, dh))
+    part.copy_(x)
+    return buf, part
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 128), ("bf16", 64), ("bf16", 96), ("f32", 64)])
+def test_rows_that_start_on_16_bytes_only(hf, dtype, dh):
+    """Row strides that are a multiple of 16 bytes and of nothing more, out's too; what lies beside stays."""
+    pad = 24 if dtype == "bf16" else 12
+    x = [_randn((150, h, dh), dtype, h) for h in (8, 2, 2)]
+    q, k, v = (_in_rows(t, pad)[1] for t in x)
+    buf, out = _in_rows(torch.zeros(150, 8, dh, dtype=DT[dtype]), pad, 7.0)
+    assert out.data_ptr() % 32 == 16 and out.stride(0) * out.element_size() % 32 == 16
+    hf.attention_prompt(q, k, v, _i32([0, 20, 150]), out=out)
+    want, tol = R.prompt(*x, [0, 20, 150], dh ** -0.5, dtype == "bf16")
+    R.check_attention(R.to64(out), want, tol)
+    out.fill_(7.0)
+    assert (buf == 7.0).all()
+    pk, pv, table, lens, refs = _shared_cache(dtype, 2, dh, 16, 32, [5, 60, 33], 4)
+    c = _on_gpu(hf, pk, pv, table, lens, refs)
+    y = _randn((3, 4, 8, dh), dtype, 9)
+    q = _in_rows(y.flatten(0, 1), pad)[1].unflatten(0, (3, 4))
+    want, tol = R.pages(y, pk[0], pv[0], table, lens, dh ** -0.5, dtype == "bf16")
+    for shared in (0, 32):
+        c.attend(q, shared=shared, out=out[:12].unflatten(0, (3, 4)))
+        R.check_attention(R.to64(out[:12].unflatten(0, (3, 4))), want, tol)
+        out.fill_(7.0)
+        assert (buf == 7.0).all()
+    assert not c.check()
