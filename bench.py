@@ -213,13 +213,19 @@ def ablation_config(cfg) -> dict:
     return res
 
 
+# sources of the target model's half of a round: no kernel of the workloads here is built from them
+TARGET_SIDE = ("attn.cuh", "attn_rows.cu", "attn_tc.cu", "pages.cu", "pages.cuh", "verify.cu")
+
+
 def kernel_sources_digest() -> str:
-    """sha256 over the CUDA sources (names and bytes, sorted by name)."""
+    """sha256 over the drafter's CUDA sources (names and bytes, sorted by name)."""
     import glob
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_decoding_drafter_hf_gb300", "csrc")
     for f in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
+        if os.path.basename(f) in TARGET_SIDE:
+            continue
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
