@@ -1,4 +1,6 @@
 """Rules of the target-side calls at their edges, on the GPU."""
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -145,6 +147,48 @@ def test_check_waits_for_every_stream(hf):
     assert not c.check()
 
 
+def test_a_cache_of_4096_requests(hf):
+    """Lists at their longest: more free pages taken at once than a CTA holds near, copies for all, every request cut."""
+    n, n_pages, page = 4096, 21000, 8
+    rng = random.Random(1)
+    c = hf.Pages.empty(1, n_pages, 1, page, 8, n, 4)
+    c.k.zero_()
+    c.v.zero_()
+    ref = R.Cache(1, n_pages, 1, page, 8, n, 4)
+
+    def extend_and_write(rs, counts, seed):
+        c.extend(_i32(counts), _i32(rs))
+        assert ref.extend(rs, counts) == "" and not c.check()
+        ends = np.concatenate([[0], np.cumsum(counts)]).tolist()
+        k, v = (_randn((1, ends[-1], 1, 8), "bf16", seed + s) for s in (0, 1))
+        c.write(k.cuda(), v.cuda(), _i32(ends), _i32(rs))
+        assert not c.check()
+        ref.write(rs, ends, R.to64(k), R.to64(v))
+
+    rs = rng.sample(range(n), 3000)
+    extend_and_write(rs, [rng.randint(0, 17) for _ in rs], 1)
+    _same(c, ref, "extended")
+    into = [r for r in range(n) if ref.lens[r] == 0]
+    source = [rng.choice(sorted(set(range(n)) - set(into))) for _ in into]
+    c.fork(_i32(source), _i32(into))
+    assert ref.fork(source, into) == "" and not c.check()
+    _same(c, ref, "forked")
+    rs = rng.sample(range(n), n)
+    extend_and_write(rs, [rng.randint(0, 9) for _ in rs], 3)
+    _same(c, ref, "all extended")
+    keep = [rng.randint(0, x) for x in ref.lens]
+    c.truncate(_i32(keep))
+    assert ref.truncate(list(range(n)), keep) == "" and not c.check()
+    _same(c, ref, "all cut")
+    used = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.compact(used)
+    assert int(used) == ref.compact() and not c.check()
+    _same(c, ref, "compacted")
+    c.truncate(_i32([0] * n))
+    ref.truncate(list(range(n)), [0] * n)
+    _same(c, ref, "empty")
+
+
 # ------------------------------------------------------------------- attention
 @pytest.mark.parametrize("n,shared", [(3, 64), (3, 0), (300, 64)])
 def test_waits_that_run_out_are_reported(hf, n, shared):
@@ -234,4 +278,26 @@ def test_rows_that_start_on_16_bytes_only(hf, dtype, dh):
         R.check_attention(R.to64(out[:12].unflatten(0, (3, 4))), want, tol)
         out.fill_(7.0)
         assert (buf == 7.0).all()
+    assert not c.check()
+
+
+@pytest.mark.parametrize("hq,hkv,dh", [(33, 1, 64), (86, 2, 128), (63, 3, 64)])
+def test_groups_that_do_not_divide_a_tile(hf, hq, hkv, dh):
+    T.test_prompt(hf, "bf16", hq, hkv, dh, [1, 9, 20])
+    T.test_attend(hf, "bf16", hq, hkv, dh, 16, 5, 32, [0, 3, 140, None])
+
+
+def test_calls_without_anything_to_do(hf):
+    c = hf.Pages.empty(1, 4, 2, 16, 64, 2, 2)
+    q = torch.zeros(0, 3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert c.attend(q, _i32([])).shape == q.shape
+    c.extend(_i32([]), _i32([]))
+    c.write(torch.zeros(1, 0, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 0, 2, 64, dtype=torch.bfloat16, device="cuda"),
+            _i32([0, 0]), _i32([1]))
+    p = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert hf.attention_prompt(p, p, p, _i32([0])).shape == p.shape
+    assert hf.attention_prompt(p, p, p, _i32([0, 0])).shape == p.shape
+    n, t = hf.verify_tokens(torch.zeros(0, 4, 9, device="cuda"), torch.zeros(0, 3, dtype=torch.int32, device="cuda"),
+                            torch.zeros(0, 3, device="cuda"), torch.zeros(0, 9, device="cuda"))
+    assert n.shape == (0,) and t.shape == (0, 4)
     assert not c.check()
