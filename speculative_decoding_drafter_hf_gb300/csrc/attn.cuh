@@ -234,7 +234,6 @@ void attn_tc_sizes(AttnRows& a, int& pre_items, long long& slots);
 cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t st);
 cudaError_t launch_attn_rows_prompt(int dtype, const AttnRows& a, cudaStream_t st);
 cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st);
-// `pieces`: about how many a row has (how many warps share a row).
-cudaError_t launch_attn_join(int dtype, const AttnRows& a, int pieces, cudaStream_t st);
+cudaError_t launch_attn_join(int dtype, const AttnRows& a, cudaStream_t st);
 
 }  // namespace hf

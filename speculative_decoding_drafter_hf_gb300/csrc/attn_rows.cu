@@ -643,24 +643,27 @@ cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st
 }
 
 namespace {
+// Warps that share a row's pieces: eight, which read them side by side, where there are few
+// rows, else one. Whole calls in a graph, us with eight / one, by the fours of rows: bf16 8
+// (one request, 32768 tokens) 40.5 / 54.5, 64 (8 of 4096) 36.4 / 39.3, 240 (24 over a prefix
+// of 32768) 64.8 / 87.1, 512 46.9 / 55.7, 768 80.7 / 78.5, 1024 50.2 / 46.2, 1536 67.3 / 59.3,
+// 4096 135 / 115; fp32, whose pieces are shorter and more, 512 46.7 / 49.4, 1024 105.5 / 108.9.
+// (Two were best nowhere by more than 1%.)
 template <typename T, int SEGS>
-cudaError_t join(const AttnRows& a, int pieces, cudaStream_t st) {
+cudaError_t join(const AttnRows& a, cudaStream_t st) {
   const long long units = (long long)a.n * ((a.rows * a.Hq + 3) / 4);
-  // few rows: several warps per row, so that its pieces are read side by side
-  const int wpr = units * 2 >= 152 * 32 || pieces <= 2 ? 1 : units * 8 >= 152 * 32 || pieces <= 8 ? 2 : 8;
+  const int wpr = units >= (sizeof(T) == 4 ? 1216 : 608) ? 1 : 8;
   const int warps = join_warps(wpr);
   const dim3 grid((unsigned)((units * wpr + warps - 1) / warps), wpr == 1 ? (a.dh + 63) / 64 : 1);
-  return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : wpr == 2 ? join_kernel<T, 2, SEGS> : join_kernel<T, 1, 1>,
-                    grid, dim3(32 * warps), 0, st, a);
+  return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : join_kernel<T, 1, 1>, grid, dim3(32 * warps), 0, st, a);
 }
 }  // namespace
 
-cudaError_t launch_attn_join(int dtype, const AttnRows& a, int pieces, cudaStream_t st) {
+cudaError_t launch_attn_join(int dtype, const AttnRows& a, cudaStream_t st) {
   using bf = __nv_bfloat16;
   if (dtype == HF_F32)
-    return a.dh <= 64 ? join<float, 1>(a, pieces, st) : a.dh <= 128 ? join<float, 2>(a, pieces, st)
-                                                                    : join<float, 4>(a, pieces, st);
-  return a.dh <= 64 ? join<bf, 1>(a, pieces, st) : a.dh <= 128 ? join<bf, 2>(a, pieces, st) : join<bf, 4>(a, pieces, st);
+    return a.dh <= 64 ? join<float, 1>(a, st) : a.dh <= 128 ? join<float, 2>(a, st) : join<float, 4>(a, st);
+  return a.dh <= 64 ? join<bf, 1>(a, st) : a.dh <= 128 ? join<bf, 2>(a, st) : join<bf, 4>(a, st);
 }
 
 namespace {
@@ -712,7 +715,7 @@ void plan_pieces(AttnRows& a) {
 // Sizes and workspace of a call.
 struct PagesPlan {
   bool tc;
-  int pre_items, pieces;                // tensor cores: items of the prefix; about how many pieces a row has
+  int pre_items;                        // tensor cores: items of the prefix
   size_t eff, tile0, ml, o, total;      // offsets in the workspace (the line is at 0)
 };
 PagesPlan plan_call(AttnRows& a, int dtype) {
@@ -724,11 +727,9 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
     long long slots;
     attn_tc_sizes(a, w.pre_items, slots);
     rows = a.npre * N + (size_t)slots * a.unit_rows;
-    w.pieces = a.npre + 1 + 152 / (a.units * a.n);
   } else {
     plan_pieces(a);
     rows = attn_direct(a) ? 0 : (a.npre + a.nown) * N;
-    w.pieces = a.npre + a.nown;
   }
   w.eff = 16;
   w.tile0 = w.eff + (size_t)a.n * sizeof(int);
@@ -864,6 +865,6 @@ extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_
   } else {
     e = launch_attn_rows_pages(p->dtype, a, st);
   }
-  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, w.pieces, st);
+  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, st);
   return done(e);
 }
