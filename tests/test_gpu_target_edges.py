@@ -301,3 +301,83 @@ def test_calls_without_anything_to_do(hf):
                             torch.zeros(0, 3, device="cuda"), torch.zeros(0, 9, device="cuda"))
     assert n.shape == (0,) and t.shape == (0, 4)
     assert not c.check()
+
+
+def test_two_streams_at_once_and_graphs_that_share_a_workspace(hf):
+    """Calls on two streams, each with its own workspace, and two graphs replayed one after the other with one."""
+    k, v, table, lens, refs = _shared_cache("bf16", 4, 128, 16, 512, [500, 60, 33, 1000], 4)
+    c = _on_gpu(hf, k, v, table, lens, refs)
+    qs = [_randn((4, r, 16, 128), "bf16", r).cuda() for r in (8, 3)]
+    p = [_randn((900, h, 128), "bf16", h).cuda() for h in (8, 2, 2)]
+    off = _i32([0, 333, 900])
+    x = (torch.randn((3, 8, 9000), generator=_gen(1)) * 2.5).cuda()
+    tok, u, noise = x[:, :7].argmax(-1).int(), torch.full((3, 7), 0.5, device="cuda"), torch.ones(3, 9000, device="cuda")
+
+    def calls(i, stream=None):
+        return (c.attend(qs[i], shared=512 * i, stream=stream), hf.attention_prompt(*p, off, stream=stream),
+                *hf.verify_tokens(x, tok, u, noise, stream=stream))
+
+    want = [calls(0), calls(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        got = [calls(i, s) for i, s in enumerate(streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    ws = torch.empty(max(c.attend_workspace(q, 0).numel() + c.attend_workspace(q, 512).numel() for q in qs),
+                     dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.attend(qs[i], shared=512 * i, workspace=ws))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        graphs[1 - i].replay()
+        assert torch.equal(outs[i], want[i][0]) and torch.equal(outs[1 - i], want[1 - i][0])
+    assert not c.check()
+
+
+def test_calls_one_behind_the_other_without_a_wait(hf):
+    """Every call of a round in one stream, many rounds, no synchronisation between: each sees what the one before
+    left (lengths, tables, rows, drafts), as its copy made between synchronised calls does."""
+    rng = random.Random(3)
+    n, rows, page = 6, 4, 16
+
+    def rounds(wait):
+        c = hf.Pages.empty(1, 120, 2, page, 128, n, 20)
+        c.k.zero_()
+        c.v.zero_()
+        got = []
+        for r in range(12):
+            c.extend(counts[r])
+            wait()
+            c.write(*new[r], ends)
+            wait()
+            got.append(c.attend(q[r]))
+            wait()
+            got += hf.verify_tokens(x[r], tok[r], u, noise)
+            wait()
+            c.truncate((c.lens - rows + got[-2]).to(torch.int32))
+            wait()
+            if r % 4 == 3:
+                c.compact()
+                wait()
+        assert not c.check()
+        return got + [c.lens, c.table, c.refs]
+
+    counts = [_i32([rows] * n) for _ in range(12)]
+    ends = _i32([rows * i for i in range(n + 1)])
+    new = [[_randn((1, n * rows, 2, 128), "bf16", 10 * r + s).cuda() for s in (1, 2)] for r in range(12)]
+    q = [_randn((n, rows, 8, 128), "bf16", 50 + r).cuda() for r in range(12)]
+    x = [(torch.randn((n, rows, 500), generator=_gen(r)) * 2).cuda() for r in range(12)]
+    tok = [t[:, :rows - 1].argmax(-1).int() for t in x]
+    u = torch.tensor([[rng.random() for _ in range(rows - 1)] for _ in range(n)]).cuda()
+    noise = torch.empty((n, 500)).exponential_(generator=_gen(9)).cuda()
+    want = rounds(torch.cuda.synchronize)
+    for _ in range(5):
+        got = rounds(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
