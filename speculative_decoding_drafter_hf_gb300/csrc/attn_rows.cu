@@ -644,15 +644,16 @@ cudaError_t launch_attn_rows_pages(int dtype, const AttnRows& a, cudaStream_t st
 
 namespace {
 // Warps that share a row's pieces: eight, which read them side by side, where there are few
-// rows, else one. Whole calls in a graph, us with eight / one, by the fours of rows: bf16 8
-// (one request, 32768 tokens) 40.5 / 54.5, 64 (8 of 4096) 36.4 / 39.3, 240 (24 over a prefix
-// of 32768) 64.8 / 87.1, 512 46.9 / 55.7, 768 80.7 / 78.5, 1024 50.2 / 46.2, 1536 67.3 / 59.3,
-// 4096 135 / 115; fp32, whose pieces are shorter and more, 512 46.7 / 49.4, 1024 105.5 / 108.9.
-// (Two were best nowhere by more than 1%.)
+// rows, else one; more rows the more pieces they have. Whole calls in a graph, us with eight /
+// one, by the fours of rows. Tensor cores, a prefix: 240 (24 rows over 32768 tokens) 64.8 / 87.1,
+// 512 46.9 / 55.7, 768 80.7 / 78.5, 1024 50.2 / 46.2, 1536 67.3 / 59.3, 4096 135 / 115; no prefix:
+// 8 (one request, 32768 tokens) 40.5 / 54.5, 64 36.4 / 39.3, 240 50.5 / 51.1, 320 110.4 / 110.1,
+// 512 (64 requests of 1000) 56.4 / 54.4, 640 44.1 / 41.2. CUDA cores, whose pieces are shorter:
+// 128 15.2 / 16.3, 512 46.7 / 49.4, 1024 105.5 / 108.9. (Two were best nowhere by more than 1%.)
 template <typename T, int SEGS>
 cudaError_t join(const AttnRows& a, cudaStream_t st) {
   const long long units = (long long)a.n * ((a.rows * a.Hq + 3) / 4);
-  const int wpr = units >= (sizeof(T) == 4 ? 1216 : 608) ? 1 : 8;
+  const int wpr = units >= (!a.line ? 1216 : a.npre > 0 ? 608 : 304) ? 1 : 8;
   const int warps = join_warps(wpr);
   const dim3 grid((unsigned)((units * wpr + warps - 1) / warps), wpr == 1 ? (a.dh + 63) / 64 : 1);
   return launch_pdl(wpr == 8 ? join_kernel<T, 8, SEGS> : join_kernel<T, 1, 1>, grid, dim3(32 * warps), 0, st, a);
