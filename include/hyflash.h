@@ -633,6 +633,8 @@ size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows,
  *   of rate 1 it is i with probability w_i / sum(w).
  * T = 0: draft s is accepted iff it is argmax x_s (the lowest token among
  * equals), and the next token is argmax x_a.
+ * Exponentials and the race's quotients are the fast ones of 32 bits (2 units in the
+ * last place each): scores that near each other may change places.
  *   target_logits [batch, block + 1, vocab] DEVICE, HF_F32 or HF_BF16, row stride
  *                target_ld elements (>= vocab); no alignment beyond the type's.
  *   draft_logits  [batch, block, vocab] DEVICE with row stride draft_ld, or NULL:

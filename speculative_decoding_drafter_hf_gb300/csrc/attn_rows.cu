@@ -12,7 +12,7 @@
 // multiply-adds and the shared-memory reads that feed them (RPT = 4: 64 multiply-adds
 // for 8 reads), which go in pairs, two to an instruction. K and V have one place each,
 // refilled in turn while the other is used: that leaves room for three or four CTAs per SM
-// (8 prompts of 100 to 1201 tokens, heads of 64: 67 us with RPT = 4, 73 us with 8; before
+// (8 prompts of 100 to 1201 tokens, heads of 64: 65 us with RPT = 4, 73 us with 8; before
 // the pairs two places each and two CTAs per SM took 103 us, one place each 75). A prompt's
 // rows are few for the GPU and their keys many: a cluster of four CTAs shares a tile of rows,
 // each walking every fourth tile of keys, and joins the parts through distributed shared

@@ -24,8 +24,10 @@
 // Bound by the chain scores - softmax - values of a row tile, of which two take turns on
 // the tensor cores: about 2700 cycles for two row tiles and 128 keys, where the products
 // alone take 2048 and the exponentials 1024. A prompt of 8192 tokens, 32 heads of 128 over
-// 8: 337 us, 1.63 PFLOP/s. Over a cache, by the reads: 64 requests of 4096 tokens 169 to
-// 182 us, 5.9 to 6.3 TB/s.
+// 8: 367 us in a stream of calls on new inputs (1.50 PFLOP/s), 340 replayed on the same; heads
+// of 64: 286, the softmax threads alone. Over a cache, by the reads: 64 requests of 4096
+// tokens 165 to 172 us (6.2 to 6.5 TB/s), with pages of 16 tokens 215 us (5.0: a copy brings
+// 4 KB).
 //
 // Masked keys: scores are selected by position. V's non-finite values in a tile that
 // some row masks are set to zero in shared memory (0 * NaN would reach every row) and
