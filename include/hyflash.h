@@ -73,7 +73,11 @@ typedef enum {
   HF_EDEVICE = 5   /* a device-side argument check failed (see hf_last_error) */
 } hf_status;
 
-typedef enum { HF_F32 = 0, HF_BF16 = 1 } hf_dtype;
+typedef enum {
+  HF_F32 = 0,
+  HF_BF16 = 1,
+  HF_E4M3 = 2 /* 8 bits (4 of exponent, 3 of mantissa, no infinities): the cache of hf_pages8 only */
+} hf_dtype;
 
 /* Shape of the drafter. Block is the number of draft slots (7 on the pages:
  * "In the paper the block is 7 positions"); commits take up to block+1 rows
@@ -620,6 +624,112 @@ hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_t n, int32_
 /* Bytes of its workspace for these sizes (0: refused sizes). */
 size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows,
                                     int32_t n_q_heads, int32_t shared);
+
+/* ---- the cache in 8 bits ---------------------------------------------
+ *
+ * The same cache with K and V held as e4m3 values and a scale for each layer,
+ * page and KV head: a value is its code times the scale. The scales are powers of
+ * two, 2^-64 .. 2^63, so that a code of a larger scale holds what a smaller
+ * one's held, down to the smallest codes. hf_pages8_write alone sets them:
+ *   - the scale of a page is the least that brings the largest magnitude of
+ *     the written rows to 448 at most, and not below the page's present scale if
+ *     rows before the first written one stay in the page (those are rounded
+ *     again where it grew); a page written from its first row starts anew.
+ *   - codes are the nearest ones, ties to even; magnitudes above 448 2^63 become that.
+ *   - infinities and NaN are held as NaN, and do not count for the scale.
+ * Extending copies and compacting moves a page's scales with it. */
+typedef struct {
+  hf_pages pages;  /* dtype HF_E4M3; k and v hold one byte an element; head_dim a multiple of 16 */
+  float* k_scale;  /* [n_layers, n_pages, n_kv_heads] */
+  float* v_scale;  /* the same */
+  int32_t rows;    /* hf_dtype of the rows that are written and read, of q and out: HF_F32 or HF_BF16 */
+  int32_t reserved; /* 0 */
+} hf_pages8;
+
+/* As the calls on hf_pages. */
+size_t hf_pages8_work_ints(const hf_pages8* p);
+hf_status hf_pages8_extend(const hf_pages8* p, const int32_t* requests, const int32_t* counts,
+                           int32_t n, void* stream);
+hf_status hf_pages8_fork(const hf_pages8* p, const int32_t* from, const int32_t* into, int32_t n,
+                         void* stream);
+hf_status hf_pages8_truncate(const hf_pages8* p, const int32_t* requests, const int32_t* keep,
+                             int32_t n, void* stream);
+hf_status hf_pages8_compact(const hf_pages8* p, int32_t* n_used, void* stream);
+
+/* hf_pages_write, quantising: k and v are rows of type p->rows. Rows behind the
+ * last written one keep their codes. */
+hf_status hf_pages8_write(const hf_pages8* p, int32_t layer, int32_t layers, const void* k,
+                          const void* v, int64_t ld, int64_t layer_stride,
+                          const int32_t* requests, const int32_t* offsets, int32_t n,
+                          int32_t total, void* stream);
+
+/* Read tokens back: rows offsets[i] .. offsets[i+1]-1 (DEVICE int32 [n + 1]) of k and v
+ * become tokens first[i] (DEVICE int32 [n]), first[i] + 1, .. of entry i's request, in layers
+ * layer .. layer + layers - 1, as values of type p->rows (codes times scale, rounded once). k, v:
+ * as hf_pages8_write, written. Entries may repeat a request. Rows of a bad
+ * entry (bounds, request or tokens out of range, a page id out of range) are left
+ * as they are (HF_S_BAD); so are rows of no entry, and all rows if offsets decrease. */
+hf_status hf_pages8_read(const hf_pages8* p, int32_t layer, int32_t layers, void* k, void* v,
+                         int64_t ld, int64_t layer_stride, const int32_t* requests,
+                         const int32_t* first, const int32_t* offsets, int32_t n, int32_t total,
+                         void* stream);
+
+/* hf_attention_pages over it: q and out are of type p->rows. */
+hf_status hf_attention_pages8(const hf_pages8* p, int32_t layer, int32_t n, int32_t rows,
+                              int32_t n_q_heads, const void* q, int64_t q_ld,
+                              const int32_t* requests, int32_t shared, float scale, void* out,
+                              int64_t out_ld, void* workspace, size_t workspace_bytes,
+                              void* stream);
+size_t hf_attention_pages8_workspace(const hf_pages8* p, int32_t n, int32_t rows,
+                                     int32_t n_q_heads, int32_t shared);
+
+/* ---- rotary positions ------------------------------------------------
+ *
+ * Pair i of a head, i < dim / 2, is turned by the angle position * w_i:
+ *   (a, b) -> f (a cos - b sin, b cos + a sin)
+ * with (a, b) the columns (i, i + dim/2) or, interleaved, (2i, 2i + 1); columns from
+ * dim on stay. w_i = base^(-2i/dim), changed for long contexts by `kind`:
+ *   LINEAR  w_i / factor.
+ *   NTK     base * factor^(dim/(dim-2)) for base (dim > 2).
+ *   YARN    w_i (1 - r) + w_i / factor * r, r = (i - lo) / (hi - lo) held to 0..1, with
+ *           lo = floor(c(fast)) >= 0, hi = ceil(c(slow)) <= dim - 1 and c(t) the pair that turns
+ *           t times over `original` positions: dim ln(original / (2 pi t)) / (2 ln base). Its f
+ *           is 0.1 ln(factor) + 1 unless attention > 0 gives it.
+ *   BANDS   w_i t + w_i / factor (1 - t), t = (original w_i / (2 pi) - slow) / (fast - slow)
+ *           held to 0..1.
+ * f = attention, or 1 where that is 0 (but for YARN). Zeros for fast and slow stand for
+ * 32 and 1 (YARN), 4 and 1 (BANDS). */
+enum { HF_ROTARY_NONE = 0, HF_ROTARY_LINEAR = 1, HF_ROTARY_NTK = 2, HF_ROTARY_YARN = 3, HF_ROTARY_BANDS = 4 };
+typedef struct {
+  int32_t kind;      /* HF_ROTARY_* */
+  int32_t original;  /* positions that the target was trained on (YARN, BANDS): >= 1 */
+  double factor;     /* >= 1, finite (all but NONE) */
+  double fast, slow; /* fast > slow > 0, or 0 */
+  double attention;  /* f: >= 0, finite; 0: the kind's own */
+} hf_rotary_scaling;
+
+/* w_i / (2 pi) in units of 2^-64 turns, i < dim/2, into HOST memory, and f: what hf_rotary
+ * takes. dim even, 2..256; base > 1, finite; scaling NULL: NONE. Host only. */
+hf_status hf_rotary_table(int32_t dim, double base, const hf_rotary_scaling* scaling,
+                          uint64_t* turns, float* attention);
+
+/* Turn the queries and keys of `rows` tokens. The angle is position * turns in 64-bit
+ * integers, whole turns dropped: exact for every int32 position.
+ *   dtype       HF_F32 or HF_BF16, of all four buffers.
+ *   interleaved 0: pairs (i, i + dim/2); 1: (2i, 2i + 1).
+ *   dim         even, 2 .. head_dim; head_dim <= 256.
+ *   turns       DEVICE uint64 [dim/2], 8-byte aligned; attention: f.
+ *   positions   DEVICE int32 [rows]; negative ones turn backwards.
+ *   q, q_out    [rows, *_ld] DEVICE: head h at columns [h*head_dim, (h+1)*head_dim);
+ *               aligned to the type. n_q_heads = 0: NULL.
+ *   k, k_out    the same of n_kv_heads; n_kv_heads = 0: NULL.
+ * q_out may be q and k_out k (with the same stride); they may not overlap otherwise. Heads
+ * start on 16 bytes in the fast form; others are turned value by value. */
+hf_status hf_rotary(int32_t dtype, int32_t interleaved, int32_t rows, int32_t n_q_heads,
+                    int32_t n_kv_heads, int32_t head_dim, int32_t dim, const uint64_t* turns,
+                    float attention, const int32_t* positions, const void* q, int64_t q_ld,
+                    const void* k, int64_t k_ld, void* q_out, int64_t q_out_ld, void* k_out,
+                    int64_t k_out_ld, void* stream);
 
 /* Verification of drafted tokens by speculative sampling. Request b has drafts
  * d_s = draft_tokens[b, s], s < n_draft[b], the target's logits x_s at s = 0 ..

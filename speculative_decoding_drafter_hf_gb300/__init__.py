@@ -8,7 +8,7 @@ library exists; using any of them without the library raises ImportError.
 """
 _BINDING_NAMES = ("EXPORTED", "Drafter", "Family", "HfBlockWeights", "HfConfig", "HfLayerWeights", "HyflashError",
                   "LIB_PATH", "Status", "Tensor", "make_config", "HfPages", "Pages", "CallStatus", "attention_prompt",
-                  "verify_tokens", "verify_workspace")
+                  "verify_tokens", "verify_workspace", "HfPages8", "Pages8", "Rotary")
 
 __all__ = list(_BINDING_NAMES)
 

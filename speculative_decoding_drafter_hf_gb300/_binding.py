@@ -62,7 +62,7 @@ class Family(enum.IntEnum):
     HEAD = 9
 
 
-HF_F32, HF_BF16 = 0, 1
+HF_F32, HF_BF16, HF_E4M3 = 0, 1, 2
 
 
 class HfConfig(ctypes.Structure):
@@ -156,8 +156,21 @@ class HfPages(ctypes.Structure):
                                       "n_requests", "table_ld")]
 
 
+class HfPages8(ctypes.Structure):
+    _fields_ = [("pages", HfPages), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class HfRotaryScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("factor", "fast", "slow", "attention")]
+
+
+ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
 _i64, _f32, _sz = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _pp = ctypes.POINTER(HfPages)
+_p8 = ctypes.POINTER(HfPages8)
 hf_attention_prompt = _sig("hf_attention_prompt", _st, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
                            _vp, _i64, _vp, _f32, _vp, _i64, _vp, _vp)
 hf_attention_pages = _sig("hf_attention_pages", _st, _pp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i32, _f32,
@@ -169,6 +182,20 @@ hf_pages_write = _sig("hf_pages_write", _st, _pp, _i32, _i32, _vp, _vp, _i64, _i
 hf_pages_fork = _sig("hf_pages_fork", _st, _pp, _vp, _vp, _i32, _vp)
 hf_pages_truncate = _sig("hf_pages_truncate", _st, _pp, _vp, _vp, _i32, _vp)
 hf_pages_compact = _sig("hf_pages_compact", _st, _pp, _vp, _vp)
+hf_attention_pages8 = _sig("hf_attention_pages8", _st, _p8, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i32, _f32,
+                           _vp, _i64, _vp, _sz, _vp)
+hf_attention_pages8_workspace = _sig("hf_attention_pages8_workspace", _sz, _p8, _i32, _i32, _i32, _i32)
+hf_pages8_work_ints = _sig("hf_pages8_work_ints", _sz, _p8)
+hf_pages8_extend = _sig("hf_pages8_extend", _st, _p8, _vp, _vp, _i32, _vp)
+hf_pages8_fork = _sig("hf_pages8_fork", _st, _p8, _vp, _vp, _i32, _vp)
+hf_pages8_truncate = _sig("hf_pages8_truncate", _st, _p8, _vp, _vp, _i32, _vp)
+hf_pages8_compact = _sig("hf_pages8_compact", _st, _p8, _vp, _vp)
+hf_pages8_write = _sig("hf_pages8_write", _st, _p8, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _vp)
+hf_pages8_read = _sig("hf_pages8_read", _st, _p8, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp)
+hf_rotary_table = _sig("hf_rotary_table", _st, _i32, ctypes.c_double, ctypes.POINTER(HfRotaryScaling), _vp,
+                       ctypes.POINTER(_f32))
+hf_rotary = _sig("hf_rotary", _st, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _f32, _vp, _vp, _i64, _vp, _i64,
+                 _vp, _i64, _vp, _i64, _vp)
 hf_verify_tokens = _sig("hf_verify_tokens", _st, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp,
                         _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp)
 hf_verify_workspace = _sig("hf_verify_workspace", _sz, _i32, _i32, _i32)
@@ -184,7 +211,10 @@ EXPORTED = ("hf_create", "hf_destroy", "hf_set_weights", "hf_set_weights_q4", "h
             "hf_set_block_weights", "hf_set_head_weights", "hf_draft_tokens",
             "hf_attention_prompt", "hf_attention_pages", "hf_attention_pages_workspace", "hf_pages_work_ints",
             "hf_pages_extend", "hf_pages_write", "hf_pages_fork", "hf_pages_truncate", "hf_pages_compact",
-            "hf_verify_tokens", "hf_verify_workspace")
+            "hf_verify_tokens", "hf_verify_workspace",
+            "hf_attention_pages8", "hf_attention_pages8_workspace", "hf_pages8_work_ints", "hf_pages8_extend",
+            "hf_pages8_fork", "hf_pages8_truncate", "hf_pages8_compact", "hf_pages8_write", "hf_pages8_read",
+            "hf_rotary_table", "hf_rotary")
 
 
 class HyflashError(RuntimeError):
@@ -548,15 +578,18 @@ class _On:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} must be contiguous")
 
-    def empty(self, shape, dtype):
+    def zeros(self, shape, dtype):
+        return self.empty(shape, dtype, "zeros")
+
+    def empty(self, shape, dtype, kind="empty"):
         if self.given is None:
-            return self.first.new_empty(shape, dtype=dtype)
+            return getattr(self.first, "new_" + kind)(shape, dtype=dtype)
         import torch
         s = self.given
         if isinstance(s, int):
             s = torch.cuda.ExternalStream(s, device=self.index)
         with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=self.index)
+            return getattr(torch, kind)(shape, dtype=dtype, device=self.index)
 
     def call(self, f, *args):
         import torch
@@ -668,7 +701,15 @@ class Pages:
     columns], lens int32 [requests], refs int32 [pages]. Methods map one-to-one
     onto the C calls; ``status`` is the word their device checks write to."""
 
+    _C = dict(work=hf_pages_work_ints, extend=hf_pages_extend, truncate=hf_pages_truncate, fork=hf_pages_fork,
+              compact=hf_pages_compact, write=hf_pages_write, attend=hf_attention_pages,
+              attend_workspace=hf_attention_pages_workspace)
+
     def __init__(self, k, v, table, lens, refs):
+        self._setup(k, v, table, lens, refs, HfPages(dtype=_dtype_code(k, "k")), k.dtype)
+
+    def _setup(self, k, v, table, lens, refs, d, rows, wrap=lambda on, d: d):
+        """Fill the descriptor d in; rows: the type of rows, q and out; wrap(on, d): what the calls take."""
         import torch
         on = _On(k, None)
         if k.dim() != 5 or table.dim() != 2:
@@ -676,27 +717,28 @@ class Pages:
         L, n, hkv, page, dh = k.shape
         R, ld = table.shape
         i32 = torch.int32
-        d = HfPages(dtype=_dtype_code(k, "k"), n_layers=L, n_pages=n, n_kv_heads=hkv, page=page, head_dim=dh,
-                    n_requests=R, table_ld=ld)
+        d.n_layers, d.n_pages, d.n_kv_heads, d.page, d.head_dim, d.n_requests, d.table_ld = L, n, hkv, page, dh, R, ld
         d.k = on.arg(k, "k")
         d.v = on.arg(v, "v", k.dtype, tuple(k.shape))
         d.table = on.arg(table, "table", i32)
         d.lens = on.arg(lens, "lens", i32, (R,))
         d.refs = on.arg(refs, "refs", i32, (n,))
-        ints = hf_pages_work_ints(ctypes.byref(d))
+        call = wrap(on, d)
+        ints = self._C["work"](ctypes.byref(call))
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
         # scratch of the page calls, and the status word
         self._work = torch.zeros(max(ints, 1), dtype=i32, device=k.device)
         self.status = torch.zeros(1, dtype=i32, device=k.device)
-        d.work, d.status = self._work.data_ptr(), self.status.data_ptr()
-        self._d, self._ref = d, ctypes.byref(d)
-        self._i32, self._index, self._dtype, self._layers, self._row = i32, k.get_device(), k.dtype, L, (hkv, dh)
+        base = call if call is d else call.pages
+        base.work, base.status = self._work.data_ptr(), self.status.data_ptr()
+        self._d, self._keep, self._ref = base, call, ctypes.byref(call)
+        self._i32, self._index, self._dtype, self._layers, self._row = i32, k.get_device(), rows, L, (hkv, dh)
         self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         with torch.cuda.device(self._index):
             if not torch.cuda.is_current_stream_capturing():  # calls may come on any stream: both are zero by now
                 torch.cuda.current_stream().synchronize()
         if ints == 0:  # let a call say what is wrong with the descriptor
-            on.call(hf_pages_compact, self._ref, None)
+            on.call(self._C["compact"], self._ref, None)
 
     @classmethod
     def empty(cls, n_layers, n_pages, n_kv_heads, page, head_dim, n_requests, columns, dtype=None, device="cuda"):
@@ -743,27 +785,25 @@ class Pages:
     def extend(self, counts, requests=None, stream=None):
         """Room for counts[i] more tokens of requests[i] (default: request i)."""
         n = counts.shape[0]
-        self._call(hf_pages_extend, stream, self._ints(requests, n, "requests"), self._ints(counts, n, "counts"), n)
+        self._call(self._C["extend"], stream, self._ints(requests, n, "requests"), self._ints(counts, n, "counts"), n)
 
     def truncate(self, keep, requests=None, stream=None):
         """Cut requests[i] to keep[i] tokens; 0 frees it."""
         n = keep.shape[0]
-        self._call(hf_pages_truncate, stream, self._ints(requests, n, "requests"), self._ints(keep, n, "keep"), n)
+        self._call(self._C["truncate"], stream, self._ints(requests, n, "requests"), self._ints(keep, n, "keep"), n)
 
     def fork(self, source, into, stream=None):
         """Requests into[i] (empty) share all tokens of source[i]."""
         n = into.shape[0]
-        self._call(hf_pages_fork, stream, self._ints(source, n, "source"), self._ints(into, n, "into"), n)
+        self._call(self._C["fork"], stream, self._ints(source, n, "source"), self._ints(into, n, "into"), n)
 
     def compact(self, n_used=None, stream=None):
         """Move the pages in use to the front of the pool; n_used int32 [1] receives
         their number."""
-        self._call(hf_pages_compact, stream, self._ints(n_used, 1, "n_used"))
+        self._call(self._C["compact"], stream, self._ints(n_used, 1, "n_used"))
 
-    def write(self, k, v, offsets, requests=None, layer=None, stream=None):
-        """The newest rows of the requests: k and v [layers, T, kv heads, head_dim]
-        for layers 0 .. layers - 1, or [T, kv heads, head_dim] with `layer`; entry i's
-        rows are offsets[i] .. offsets[i + 1] - 1."""
+    def _rows(self, k, v, layer):
+        """Layers, tokens, row and layer stride of rows k and v."""
         shape, ks, vs = k.shape, k.stride(), v.stride()
         if (len(shape) != (4 if layer is None else 3) or shape[-2:] != self._row
                 or (layer is None and shape[0] > self._layers)):
@@ -777,15 +817,22 @@ class Pages:
         step = ks[0] if layers > 1 else 0
         if v.shape != shape or (T and vs != ks and (_heads_ld(v, T, hkv, dh, "v") != ld or (layers > 1 and vs[0] != step))):
             raise ValueError("k and v must have the same shape and strides")
+        return layers, T, ld, step
+
+    def write(self, k, v, offsets, requests=None, layer=None, stream=None):
+        """The newest rows of the requests: k and v [layers, T, kv heads, head_dim]
+        for layers 0 .. layers - 1, or [T, kv heads, head_dim] with `layer`; entry i's
+        rows are offsets[i] .. offsets[i + 1] - 1."""
+        layers, T, ld, step = self._rows(k, v, layer)
         n = offsets.shape[0] - 1
-        self._call(hf_pages_write, stream, layer or 0, layers, k.data_ptr(), v.data_ptr(),
+        self._call(self._C["write"], stream, layer or 0, layers, k.data_ptr(), v.data_ptr(),
                    ld, step, self._ints(requests, n, "requests"), self._ints(offsets, n + 1, "offsets"), n, T)
 
     def attend_workspace(self, q, shared=0):
         """A workspace for attend with queries of this shape."""
         import torch
         n, rows, hq, _ = q.shape
-        b = hf_attention_pages_workspace(self._ref, n, rows, hq, shared)
+        b = self._C["attend_workspace"](self._ref, n, rows, hq, shared)
         if b == 0:
             raise ValueError("attend_workspace: sizes out of range")
         return torch.empty(b, dtype=torch.uint8, device=self.k.device)
@@ -807,14 +854,126 @@ class Pages:
                 raise ValueError(f"{name}: its rows must be evenly spaced")
             return s
 
-        qp = on.arg(q, "q", self.k.dtype, None, False)
+        qp = on.arg(q, "q", self._dtype, None, False)
         if out is None:
             out = on.empty(tuple(q.shape), q.dtype)
         op = on.arg(out, "out", q.dtype, q.shape, False)
         if workspace is None:
-            b = hf_attention_pages_workspace(self._ref, n, rows, hq, shared)
+            b = self._C["attend_workspace"](self._ref, n, rows, hq, shared)
             workspace = on.empty((max(b, 16),), torch.uint8)
         wp = on.arg(workspace, "workspace", torch.uint8)
-        on.call(hf_attention_pages, self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._ints(requests, n, "requests"),
+        on.call(self._C["attend"], self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._ints(requests, n, "requests"),
                 shared, scale or 0.0, op, ld(out, "out"), wp, workspace.shape[0])
         return out
+
+
+class Pages8(Pages):
+    """The cache in 8 bits (hf_pages8): k and v float8_e4m3fn [layers, pages, kv heads,
+    page, head_dim], k_scale and v_scale float32 [layers, pages, kv heads], rows, queries
+    and outputs of `dtype`. The methods of Pages; `write` quantises."""
+
+    _C = dict(work=hf_pages8_work_ints, extend=hf_pages8_extend, truncate=hf_pages8_truncate, fork=hf_pages8_fork,
+              compact=hf_pages8_compact, write=hf_pages8_write, attend=hf_attention_pages8,
+              attend_workspace=hf_attention_pages8_workspace)
+
+    def __init__(self, k, v, k_scale, v_scale, table, lens, refs, dtype=None):
+        import torch
+        dtype = dtype or torch.bfloat16
+        if k.dtype is not torch.float8_e4m3fn:
+            raise TypeError(f"k must be float8_e4m3fn, got {k.dtype}")
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+
+        def wrap(on, d):
+            f32, shape = torch.float32, tuple(k.shape[:3])
+            return HfPages8(pages=d, k_scale=on.arg(k_scale, "k_scale", f32, shape),
+                            v_scale=on.arg(v_scale, "v_scale", f32, shape),
+                            rows=HF_F32 if dtype is f32 else HF_BF16)
+
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self._setup(k, v, table, lens, refs, HfPages(dtype=HF_E4M3), dtype, wrap)
+
+    @classmethod
+    def empty(cls, n_layers, n_pages, n_kv_heads, page, head_dim, n_requests, columns, dtype=None, device="cuda"):
+        """A new cache that holds no request; dtype: of the rows."""
+        import torch
+        shape = (n_layers, n_pages, n_kv_heads, page, head_dim)
+        k = torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
+        scale = torch.ones(shape[:3], dtype=torch.float32, device=device)
+        ints = dict(dtype=torch.int32, device=device)
+        return cls(k, torch.empty_like(k), scale, torch.ones_like(scale),
+                   torch.full((n_requests, columns), -1, **ints), torch.zeros(n_requests, **ints),
+                   torch.zeros(n_pages, **ints), dtype)
+
+    def read(self, first, offsets, requests=None, layer=None, *, total=None, k=None, v=None, stream=None):
+        """Tokens as rows: entry i's rows offsets[i] .. offsets[i + 1] - 1 of k and v become the
+        tokens of requests[i] from first[i] on, in all layers, or in `layer`. k and v (or
+        `total`, the rows of new ones, zeros where no entry writes) [layers, T, kv heads, head_dim],
+        without the first dim if `layer` is given. Returns them."""
+        if (k is None) != (v is None) or (k is None) == (total is None):
+            raise ValueError("give k and v, or total")
+        if k is None:
+            shape = (total, *self._row) if layer is not None else (self._layers, total, *self._row)
+            on = _On(self.k, stream)
+            k, v = on.zeros(shape, self._dtype), on.zeros(shape, self._dtype)
+        layers, T, ld, step = self._rows(k, v, layer)
+        n = offsets.shape[0] - 1
+        self._call(hf_pages8_read, stream, layer or 0, layers, k.data_ptr(), v.data_ptr(), ld, step,
+                   self._ints(requests, n, "requests"), self._ints(first, n, "first"),
+                   self._ints(offsets, n + 1, "offsets"), n, T)
+        return k, v
+
+
+class Rotary:
+    """Rotary positions of queries and keys (hf_rotary): the table of a head of `head_dim`
+    columns, the first `dim` of them turned (default: all), pairs (i, i + dim/2) or, interleaved,
+    (2i, 2i + 1). scaling: "none", "linear", "ntk", "yarn" or "bands" with their factor, original,
+    fast, slow and attention (hf_rotary_table)."""
+
+    def __init__(self, head_dim, base=1e6, dim=None, interleaved=False, scaling="none", factor=1.0, original=0, fast=0.0,
+                 slow=0.0, attention=0.0, device="cuda"):
+        import torch
+        if scaling not in ROTARY_SCALING:
+            raise ValueError(f"scaling must be one of {', '.join(ROTARY_SCALING)}")
+        self.head_dim, self.dim, self.interleaved = head_dim, dim if dim is not None else head_dim, bool(interleaved)
+        if self.dim > head_dim:
+            raise ValueError("dim must be at most head_dim")
+        host = np.zeros(max(self.dim // 2, 1), dtype=np.uint64)
+        s = HfRotaryScaling(kind=ROTARY_SCALING[scaling], original=original, factor=factor, fast=fast, slow=slow,
+                            attention=attention)
+        f = ctypes.c_float()
+        e = hf_rotary_table(self.dim, base, ctypes.byref(s), host.ctypes.data, ctypes.byref(f))
+        if e != 0:
+            raise HyflashError(e, hf_last_error(None).decode())
+        self.attention = f.value
+        self.turns = torch.from_numpy(host.view(np.int64)).to(device)  # w_i / (2 pi) in 2^-64 turns, unsigned
+        if self.turns.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.turns.device).synchronize()  # calls may come on any stream
+
+    def __call__(self, q, k, positions, *, q_out=None, k_out=None, stream=None):
+        """q [T, Hq, dh] and k [T, Hkv, dh] (or None) turned by positions int32 [T]: into q_out and
+        k_out, which may be q and k, or new tensors. Row strides are free. Returns (q_out, k_out)."""
+        import torch
+        on = _On(q, stream)
+        if q.dim() != 3 or q.shape[2] != self.head_dim or (k is not None and k.dim() != 3):
+            raise ValueError("q and k must be [tokens, heads, head_dim]")
+        T, hq, dh = q.shape
+        dt = q.dtype
+        code = _dtype_code(q, "q")
+        tp = on.arg(self.turns, "the table")
+        pp = on.arg(positions, "positions", torch.int32, (T,))
+        if q_out is None:
+            q_out = on.empty((T, hq, dh), dt)
+        qo = on.arg(q_out, "q_out", dt, q.shape, False)
+        hkv, kp, k_ld, ko, ko_ld = 0, None, 0, None, 0
+        if k is not None:
+            hkv = k.shape[1]
+            kp = on.arg(k, "k", dt, (T, hkv, dh), False)
+            k_ld = _heads_ld(k, T, hkv, dh, "k")
+            if k_out is None:
+                k_out = on.empty((T, hkv, dh), dt)
+            ko = on.arg(k_out, "k_out", dt, k.shape, False)
+            ko_ld = _heads_ld(k_out, T, hkv, dh, "k_out")
+        on.call(hf_rotary, code, int(self.interleaved), T, hq, hkv, dh, self.dim, tp, self.attention, pp, q.data_ptr(),
+                _heads_ld(q, T, hq, dh, "q"), kp, k_ld, qo, _heads_ld(q_out, T, hq, dh, "q_out"), ko, ko_ld)
+        return q_out, k_out

@@ -56,6 +56,9 @@ struct AttnRows {
   const int32_t* req;
   int n, rows, page, n_pages, n_requests, table_ld;
   int shared;      // tokens of the common prefix
+  // 8-bit cache: the layer's scales [n_pages, Hkv]; NULL of any other
+  const float* k_scale;
+  const float* v_scale;
   // pieces of the key axis: npre of the prefix (pre_keys keys each), then each
   // entry's own tokens: on CUDA cores nown pieces of own_keys each (unused ones
   // among them), on tensor cores wherever the line of all tiles is cut (AttnLine). Rows

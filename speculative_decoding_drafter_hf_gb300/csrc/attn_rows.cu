@@ -33,6 +33,7 @@
 #include <mutex>
 
 #include "attn.cuh"
+#include "e4m3.cuh"
 #include "pages.cuh"
 
 namespace hf {
@@ -62,24 +63,36 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+__device__ __forceinline__ float4 load4(const uint8_t* p, float scale) {
+  const uint32_t c = __ldcg(reinterpret_cast<const uint32_t*>(p));
+  const float2 a = from_e4m3x2(c & 0xffff), b = from_e4m3x2(c >> 16);
+  return make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale);
+}
+
 __device__ __forceinline__ bool odd_value(float x) { return !(fabsf(x) < INFINITY); }
 
-// Element offset of key j's row of KV head g in K (kind 0) or V; -1: no such page.
+// Element offset of key j's row of KV head g in K (kind 0) or V; -1: no such page. block: its page
+// and head, where the scales of an 8-bit cache lie.
 template <int MODE>
-__device__ __forceinline__ long long key_at(const AttnRows& a, int start, const int32_t* tab, int g, int j, int kv) {
+__device__ __forceinline__ long long key_at(const AttnRows& a, int start, const int32_t* tab, int g, int j, int kv,
+                                            long long* block = nullptr) {
   if (MODE == PROMPT) return (long long)(start + j) * (kv ? a.v_ld : a.k_ld) + (long long)g * a.dh;
   const int shift = 31 - __clz(a.page);  // (a power of two)
   const int id = tab[j >> shift];
   if (id < 0 || id >= a.n_pages) return -1;
-  return (((((long long)id * a.Hkv + g) << shift) + (j & (a.page - 1))) * a.dh);
+  const long long b = (long long)id * a.Hkv + g;
+  if (block) *block = b;
+  return ((b << shift) + (j & (a.page - 1))) * a.dh;
 }
 
 // DHT: the head dim, or 0 for any up to 64 * MAXC. Paged: the first pre_x CTAs work on the
 // prefix, those up to all_x on the entries' own keys, the others compare the entries' prefixes.
-template <typename T, int MODE, int MAXC, int DHT, int RPT>
+// KV: the type of the keys and values, T or an 8-bit cache's codes (paged), which become
+// values as they come in.
+template <typename T, typename KV, int MODE, int MAXC, int DHT, int RPT>
 __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all_x) {
   extern __shared__ __align__(16) float smf[];
-  constexpr bool F32 = sizeof(T) == 4;
+  constexpr bool F32 = sizeof(T) == 4, KV32 = sizeof(KV) == 4;
   constexpr int BM = 8 * RPT;
   const int dh = DHT ? DHT : a.dh, ldq = dh + 4, c4 = dh / 4;
   float* sq = smf;
@@ -147,22 +160,25 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all
   auto load = [&](int kv, int jt) {
     constexpr int U = 8;
     float* to = kv ? sv : sk;
-    const T* from = static_cast<const T*>(kv ? a.v : a.k);
+    const KV* from = static_cast<const KV*>(kv ? a.v : a.k);
     for (int e0 = tid; jt < j1 && e0 < BN * c4; e0 += RT * U) {
       float4 x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int e = e0 + u * RT, j = e / c4, c = (e % c4) * 4;
         if (e >= BN * c4) continue;
-        const long long at = jt + j < j1 ? key_at<MODE>(a, start, tab, g, jt + j, kv) : -2;
+        long long block = 0;
+        const long long at = jt + j < j1 ? key_at<MODE>(a, start, tab, g, jt + j, kv, &block) : -2;
         if (at == -1 && a.status) atomicOr(a.status, HF_S_BAD);
-        const T* src = from + (at < 0 ? 0 : at + c);
-        if constexpr (F32)
+        const KV* src = from + (at < 0 ? 0 : at + c);
+        if constexpr (KV32)
           copy16(&to[j * ldq + c], src, at >= 0);
+        else if constexpr (sizeof(KV) == 1)
+          x[u] = at >= 0 ? load4(src, __ldcg(&(kv ? a.v_scale : a.k_scale)[block])) : make_float4(0.f, 0.f, 0.f, 0.f);
         else
           x[u] = at >= 0 ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      if constexpr (!F32) {
+      if constexpr (!KV32) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int e = e0 + u * RT;
@@ -399,7 +415,11 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all
         for (int c = 0; c < MAXC * 4; ++c) {
           const int d = tx * 4 + 64 * (c / 4) + c % 4;
           if (d >= dh) continue;
-          const float x = to_f(static_cast<const T*>(a.v)[at + d]);
+          float x;
+          if constexpr (sizeof(KV) == 1)
+            x = from_e4m3(static_cast<const KV*>(a.v)[at + d]);  // (NaN is NaN at any scale)
+          else
+            x = to_f(static_cast<const KV*>(a.v)[at + d]);
           if (odd_value(x)) o[i][c] += x;
         }
       }
@@ -567,17 +587,17 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) 
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-bool g_set[kMaxDev][2][2][5][2] = {};
+bool g_set[kMaxDev][2][3][5][2] = {};
 
-template <typename T, int MODE, int MAXC, int DHT, int RPT>
+template <typename T, typename KV, int MODE, int MAXC, int DHT, int RPT>
 cudaError_t launch_one(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto* kern = rows_kernel<T, MODE, MAXC, DHT, RPT>;
+  auto* kern = rows_kernel<T, KV, MODE, MAXC, DHT, RPT>;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][MODE][DHT ? 3 + (DHT == 128) : MAXC / 2][RPT / 4];
+    bool& set = g_set[dev & (kMaxDev - 1)][sizeof(T) == 4][sizeof(KV) == 1 ? 2 : MODE][DHT ? 3 + (DHT == 128) : MAXC / 2][RPT / 4];
     if (!set || dev >= kMaxDev) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)rows_smem(DHT ? DHT : 64 * MAXC, 8 * RPT));
@@ -603,20 +623,25 @@ cudaError_t launch_one(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaS
   return cudaLaunchKernelEx(&cfg, kern, a, pre_x, all_x);
 }
 
-template <typename T, int MODE, int RPT>
+template <typename T, typename KV, int MODE, int RPT>
 cudaError_t launch_dh(const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
   constexpr bool F32 = sizeof(T) == 4;
-  if (F32 && a.dh == 64) return launch_one<T, MODE, 1, F32 ? 64 : 0, RPT>(a, pre_x, all_x, grid, st);
-  if (F32 && a.dh == 128) return launch_one<T, MODE, 2, F32 ? 128 : 0, RPT>(a, pre_x, all_x, grid, st);
-  if (a.dh <= 64) return launch_one<T, MODE, 1, 0, RPT>(a, pre_x, all_x, grid, st);
-  if (a.dh <= 128) return launch_one<T, MODE, 2, 0, RPT>(a, pre_x, all_x, grid, st);
-  return launch_one<T, MODE, 4, 0, RPT>(a, pre_x, all_x, grid, st);
+  if (F32 && a.dh == 64) return launch_one<T, KV, MODE, 1, F32 ? 64 : 0, RPT>(a, pre_x, all_x, grid, st);
+  if (F32 && a.dh == 128) return launch_one<T, KV, MODE, 2, F32 ? 128 : 0, RPT>(a, pre_x, all_x, grid, st);
+  if (a.dh <= 64) return launch_one<T, KV, MODE, 1, 0, RPT>(a, pre_x, all_x, grid, st);
+  if (a.dh <= 128) return launch_one<T, KV, MODE, 2, 0, RPT>(a, pre_x, all_x, grid, st);
+  return launch_one<T, KV, MODE, 4, 0, RPT>(a, pre_x, all_x, grid, st);
 }
 
 template <int MODE, int RPT>
 cudaError_t launch_mode(int dtype, const AttnRows& a, int pre_x, int all_x, dim3 grid, cudaStream_t st) {
-  return dtype == HF_F32 ? launch_dh<float, MODE, RPT>(a, pre_x, all_x, grid, st)
-                         : launch_dh<__nv_bfloat16, MODE, RPT>(a, pre_x, all_x, grid, st);
+  using bf = __nv_bfloat16;
+  if constexpr (MODE == PAGED)
+    if (a.k_scale)
+      return dtype == HF_F32 ? launch_dh<float, uint8_t, MODE, RPT>(a, pre_x, all_x, grid, st)
+                             : launch_dh<bf, uint8_t, MODE, RPT>(a, pre_x, all_x, grid, st);
+  return dtype == HF_F32 ? launch_dh<float, float, MODE, RPT>(a, pre_x, all_x, grid, st)
+                         : launch_dh<bf, bf, MODE, RPT>(a, pre_x, all_x, grid, st);
 }
 
 // Rows of a thread, over a paged cache: by the rows of a request.
@@ -719,9 +744,9 @@ struct PagesPlan {
   int pre_items;                        // tensor cores: items of the prefix
   size_t eff, tile0, ml, o, total;      // offsets in the workspace (the line is at 0)
 };
-PagesPlan plan_call(AttnRows& a, int dtype) {
+PagesPlan plan_call(AttnRows& a, int dtype, bool e4m3) {
   PagesPlan w{};
-  w.tc = attn_tc_ok(dtype, a.dh);
+  w.tc = !e4m3 && attn_tc_ok(dtype, a.dh);
   const size_t N = (size_t)a.n * a.rows * a.Hq;
   size_t rows;
   if (w.tc) {
@@ -740,8 +765,21 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   return w;
 }
 
-const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq, int shared, AttnRows& a) {
-  if (const char* m = pages_bad(p, buffers)) return m;
+// A cache of either kind: its descriptor, the scales of an 8-bit one and the type of q and out.
+struct AnyPages {
+  const hf_pages* p;
+  bool e4m3;
+  PageScales s;
+  int dtype;
+};
+AnyPages any_pages(const hf_pages* p) { return {p, false, {}, p ? p->dtype : 0}; }
+AnyPages any_pages(const hf_pages8* p) {
+  return p ? AnyPages{&p->pages, true, {p->k_scale, p->v_scale}, p->rows} : AnyPages{nullptr, true, {}, 0};
+}
+
+const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq, int shared, AttnRows& a) {
+  const hf_pages* p = c.p;
+  if (const char* m = pages_bad(p, buffers, c.e4m3)) return m;
   if (const char* m = heads_bad(hq, p->n_kv_heads, p->head_dim, 0.f)) return m;
   if (n < 0 || n > (1 << 20)) return "n must be 0..1048576";
   if (rows < 1 || rows > 64) return "rows must be 1..64";
@@ -754,7 +792,7 @@ const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq,
   a.Hkv = p->n_kv_heads;
   a.G = hq / p->n_kv_heads;
   a.dh = p->head_dim;
-  a.esize = p->dtype == HF_F32 ? 4 : 2;
+  a.esize = pages_esize(c.dtype);
   a.table = p->table;
   a.lens = p->lens;
   a.status = p->status;
@@ -766,6 +804,64 @@ const char* pages_args(const hf_pages* p, bool buffers, int n, int rows, int hq,
   a.table_ld = p->table_ld;
   a.shared = shared;
   return nullptr;
+}
+
+
+size_t attend_workspace(const AnyPages& c, int n, int rows, int hq, int shared) {
+  AttnRows a{};
+  if (pages_args(c, false, std::max(n, 1), rows, hq, shared, a)) return 0;
+  return plan_call(a, c.dtype, c.e4m3).total;
+}
+
+hf_status attend(const AnyPages& c, int32_t layer, int32_t n, int32_t rows, int32_t n_q_heads, const void* q,
+                 int64_t q_ld, const int32_t* requests, int32_t shared, float scale, void* out, int64_t out_ld,
+                 void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  const hf_pages* p = c.p;
+  AttnRows a{};
+  if (const char* m = pages_args(c, true, n, rows, n_q_heads, shared, a)) return refuse(m);
+  if (const char* m = heads_bad(n_q_heads, p->n_kv_heads, p->head_dim, scale)) return refuse(m);
+  if (layer < 0 || layer >= p->n_layers) return refuse("layer must be a layer of the cache");
+  if (!requests && n > p->n_requests) return refuse("n must be <= n_requests without a list of requests");
+  if (n == 0) return HF_OK;
+  if (!q || !out || !workspace) return refuse("NULL buffer");
+  for (const char* m : {ld_bad(q_ld, (long long)n_q_heads * p->head_dim, a.esize, q),
+                        ld_bad(out_ld, (long long)n_q_heads * p->head_dim, a.esize, out)})
+    if (m) return refuse(m);
+  if (off(requests, 4)) return refuse("requests must be 4-byte aligned");
+  const PagesPlan w = plan_call(a, c.dtype, c.e4m3);
+  if (off(workspace, 16) || workspace_bytes < w.total) {
+    char m[160];
+    snprintf(m, sizeof m, "workspace must be 16-byte aligned and hold %zu bytes (hf_attention_pages%s_workspace), got %zu",
+             w.total, c.e4m3 ? "8" : "", workspace_bytes);
+    return refuse(m);
+  }
+  const size_t layer_bytes = (size_t)p->n_pages * pages_block(p) * pages_esize(p->dtype);
+  a.qscale = base2_scale(scale, p->head_dim);
+  a.q = q;
+  a.q_ld = q_ld;
+  a.out = out;
+  a.out_ld = out_ld;
+  a.k = static_cast<const uint8_t*>(p->k) + layer * layer_bytes;
+  a.v = static_cast<const uint8_t*>(p->v) + layer * layer_bytes;
+  if (c.e4m3) {
+    a.k_scale = c.s.k + (size_t)layer * p->n_pages * p->n_kv_heads;
+    a.v_scale = c.s.v + (size_t)layer * p->n_pages * p->n_kv_heads;
+  }
+  a.req = requests;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.eff = reinterpret_cast<int*>(ws + w.eff);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws + w.o) + 31) / 32 * 32);
+  cudaError_t e;
+  if (w.tc) {
+    a.line = reinterpret_cast<int*>(ws);
+    a.tile0 = reinterpret_cast<int*>(ws + w.tile0);
+    e = launch_attn_tc_pages(a, w.pre_items, st);
+  } else {
+    e = launch_attn_rows_pages(c.dtype, a, st);
+  }
+  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(c.dtype, a, st);
+  return done(e);
 }
 
 }  // namespace
@@ -816,56 +912,28 @@ extern "C" hf_status hf_attention_prompt(int32_t dtype, int32_t n_seq, int32_t t
 
 extern "C" size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows, int32_t n_q_heads,
                                                int32_t shared) {
-  hf::AttnRows a{};
-  if (hf::pages_args(p, false, std::max(n, 1), rows, n_q_heads, shared, a)) return 0;
-  return hf::plan_call(a, p->dtype).total;
+  return hf::attend_workspace(hf::any_pages(p), n, rows, n_q_heads, shared);
 }
 
 extern "C" hf_status hf_attention_pages(const hf_pages* p, int32_t layer, int32_t n, int32_t rows,
                                         int32_t n_q_heads, const void* q, int64_t q_ld, const int32_t* requests,
                                         int32_t shared, float scale, void* out, int64_t out_ld, void* workspace,
                                         size_t workspace_bytes, void* stream) {
-  using namespace hf;
-  AttnRows a{};
-  if (const char* m = pages_args(p, true, n, rows, n_q_heads, shared, a)) return refuse(m);
-  if (const char* m = heads_bad(n_q_heads, p->n_kv_heads, p->head_dim, scale)) return refuse(m);
-  if (layer < 0 || layer >= p->n_layers) return refuse("layer must be a layer of the cache");
-  if (!requests && n > p->n_requests) return refuse("n must be <= n_requests without a list of requests");
-  if (n == 0) return HF_OK;
-  if (!q || !out || !workspace) return refuse("NULL buffer");
-  for (const char* m : {ld_bad(q_ld, (long long)n_q_heads * p->head_dim, a.esize, q),
-                        ld_bad(out_ld, (long long)n_q_heads * p->head_dim, a.esize, out)})
-    if (m) return refuse(m);
-  if (off(requests, 4)) return refuse("requests must be 4-byte aligned");
-  const PagesPlan w = plan_call(a, p->dtype);
-  if (off(workspace, 16) || workspace_bytes < w.total) {
-    char m[160];
-    snprintf(m, sizeof m, "workspace must be 16-byte aligned and hold %zu bytes (hf_attention_pages_workspace), got %zu",
-             w.total, workspace_bytes);
-    return refuse(m);
-  }
-  const size_t layer_bytes = (size_t)p->n_pages * pages_block(p) * a.esize;
-  a.qscale = base2_scale(scale, p->head_dim);
-  a.q = q;
-  a.q_ld = q_ld;
-  a.out = out;
-  a.out_ld = out_ld;
-  a.k = static_cast<const uint8_t*>(p->k) + layer * layer_bytes;
-  a.v = static_cast<const uint8_t*>(p->v) + layer * layer_bytes;
-  a.req = requests;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.eff = reinterpret_cast<int*>(ws + w.eff);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws + w.o) + 31) / 32 * 32);
-  cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e;
-  if (w.tc) {
-    a.line = reinterpret_cast<int*>(ws);
-    a.tile0 = reinterpret_cast<int*>(ws + w.tile0);
-    e = launch_attn_tc_pages(a, w.pre_items, st);
-  } else {
-    e = launch_attn_rows_pages(p->dtype, a, st);
-  }
-  if (e == cudaSuccess && (w.tc || !attn_direct(a))) e = launch_attn_join(p->dtype, a, st);
-  return done(e);
+  return hf::attend(hf::any_pages(p), layer, n, rows, n_q_heads, q, q_ld, requests, shared, scale, out, out_ld,
+                    workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" size_t hf_attention_pages8_workspace(const hf_pages8* p, int32_t n, int32_t rows, int32_t n_q_heads,
+                                                int32_t shared) {
+  if (hf::pages8_bad(p, false)) return 0;
+  return hf::attend_workspace(hf::any_pages(p), n, rows, n_q_heads, shared);
+}
+
+extern "C" hf_status hf_attention_pages8(const hf_pages8* p, int32_t layer, int32_t n, int32_t rows,
+                                         int32_t n_q_heads, const void* q, int64_t q_ld, const int32_t* requests,
+                                         int32_t shared, float scale, void* out, int64_t out_ld, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  if (const char* m = hf::pages8_bad(p, true)) return hf::refuse(m);
+  return hf::attend(hf::any_pages(p), layer, n, rows, n_q_heads, q, q_ld, requests, shared, scale, out, out_ld,
+                    workspace, workspace_bytes, (cudaStream_t)stream);
 }

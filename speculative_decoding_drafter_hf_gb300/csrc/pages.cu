@@ -17,9 +17,10 @@
 
 namespace hf {
 
-const char* pages_bad(const hf_pages* p, bool buffers) {
+const char* pages_bad(const hf_pages* p, bool buffers, bool e4m3) {
   if (!p) return "NULL cache";
-  if (p->dtype != HF_F32 && p->dtype != HF_BF16) return "cache dtype must be HF_F32 or HF_BF16";
+  if (e4m3 && p->dtype != HF_E4M3) return "cache dtype must be HF_E4M3";
+  if (!e4m3 && p->dtype != HF_F32 && p->dtype != HF_BF16) return "cache dtype must be HF_F32 or HF_BF16";
   if (p->n_layers < 1 || p->n_pages < 1 || p->n_kv_heads < 1 || p->table_ld < 1)
     return "cache: n_layers, n_pages, n_kv_heads and table_ld must be positive";
   if (p->page != 8 && p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128)
@@ -48,11 +49,7 @@ constexpr int CT = 256;   // threads of the copying CTAs
 constexpr int kMoves = 16;
 
 __device__ __forceinline__ int move_room(const hf_pages& p) { return max(p.n_pages, p.n_requests); }
-// (lengths near 2^31 too)
-__device__ __forceinline__ int pages_of(int len, int page) { return len / page + (len % page > 0); }
-__device__ __forceinline__ void flag(const hf_pages& p, int bit) {
-  if (p.status) atomicOr(p.status, bit);
-}
+__device__ __forceinline__ void flag(const hf_pages& p, int bit) { pages_flag(p, bit); }
 
 // Whether the list names requests in range, none twice and none of `others` (NULL:
 // no such list); each entry also has to pass ok(i, request). Same answer in every
@@ -324,11 +321,12 @@ __global__ void __launch_bounds__(PT) extend_plan(hf_pages p, const int32_t* req
 
 // Planned moves src[m] -> dst[m] of whole pages, in every layer, K and V; the
 // tables follow when `remap` is set (compact: entries at or behind `used` move).
-__device__ __forceinline__ void move_pages(const hf_pages& p, int moves) {
+// An 8-bit cache's scales go along.
+__device__ __forceinline__ void move_pages(const hf_pages& p, PageScales sc, int moves) {
   const int32_t* src = p.work + kMoves;
   const int32_t* dst = src + move_room(p);
-  const long long bytes = (long long)p.n_kv_heads * p.page * p.head_dim * (p.dtype == HF_F32 ? 4 : 2);
-  const int vecs = (int)(bytes / 16);  // a page of 8 rows of 8 elements is already 128 bytes
+  const long long bytes = (long long)p.n_kv_heads * p.page * p.head_dim * pages_esize(p.dtype);
+  const int vecs = (int)(bytes / 16);  // a page of 8 rows of 8 elements is already 128 bytes, of 16 bytes too
   const int per = (vecs + CT * 4 - 1) / (CT * 4);  // pieces of 16 KB
   const long long units = (long long)moves * p.n_layers * 2 * per;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -340,6 +338,11 @@ __device__ __forceinline__ void move_pages(const hf_pages& p, int moves) {
     uint8_t* base = static_cast<uint8_t*>(kv ? p.v : p.k) + (long long)layer * p.n_pages * bytes;
     const uint4* s = reinterpret_cast<const uint4*>(base + (long long)__ldcg(&src[m]) * bytes);
     uint4* d = reinterpret_cast<uint4*>(base + (long long)__ldcg(&dst[m]) * bytes);
+    if (sc.k && piece == 0) {
+      float* f = (kv ? sc.v : sc.k) + (size_t)layer * p.n_pages * p.n_kv_heads;
+      for (int h = threadIdx.x; h < p.n_kv_heads; h += CT)
+        f[(size_t)__ldcg(&dst[m]) * p.n_kv_heads + h] = __ldcg(&f[(size_t)__ldcg(&src[m]) * p.n_kv_heads + h]);
+    }
     const int i0 = piece * CT * 4 + threadIdx.x;
     uint4 r[4];
 #pragma unroll
@@ -351,10 +354,10 @@ __device__ __forceinline__ void move_pages(const hf_pages& p, int moves) {
   }
 }
 
-__global__ void __launch_bounds__(CT) extend_copy(hf_pages p) {
+__global__ void __launch_bounds__(CT) extend_copy(hf_pages p, PageScales sc) {
   pdl_trigger();
   pdl_wait();
-  move_pages(p, __ldcg(&p.work[1]));
+  move_pages(p, sc, __ldcg(&p.work[1]));
 }
 
 // ------------------------------------------------------------------- compact
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(PT) compact_plan(hf_pages p, int32_t* n_used) 
   }
 }
 
-__global__ void __launch_bounds__(CT) compact_move(hf_pages p) {
+__global__ void __launch_bounds__(CT) compact_move(hf_pages p, PageScales sc) {
   pdl_trigger();
   pdl_wait();
   const int moves = __ldcg(&p.work[1]), used = __ldcg(&p.work[2]);
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(CT) compact_move(hf_pages p) {
         flag(p, HF_S_BAD);  // a page in a table that nobody counts
     }
   }
-  move_pages(p, moves);
+  move_pages(p, sc, moves);
 }
 
 // --------------------------------------------------------------------- write
@@ -447,21 +450,6 @@ struct WriteArgs {
   const int32_t* off;
   int n, total, layer, layers;
 };
-
-// The last index in [0, n) whose offset is at or before t (offsets rise), by one warp: 32
-// of them are looked at side by side, so that three dependent loads do for 4096.
-__device__ __forceinline__ int find_entry(const int32_t* off, int n, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, count = n;
-  while (count > 1) {
-    const int step = (count + 31) / 32, i = lane * step;
-    const bool before = i < count && __ldcg(&off[lo + i]) <= t;
-    const int k = max(0, 31 - __clz(__ballot_sync(0xffffffffu, before)));
-    lo += k * step;
-    count = min(step, count - k * step);
-  }
-  return lo;
-}
 
 // One warp per row and up to kCopies of its (layer, K or V): heads * head_dim elements go
 // to as many places of head_dim elements as there are heads. Small calls are bound by the
@@ -488,7 +476,7 @@ __global__ void __launch_bounds__(CT) write_kernel(hf_pages p, WriteArgs a) {
   for (long long u = (long long)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < units;
        u += (long long)gridDim.x * (CT / 32)) {
     const int t = (int)(u / groups), c0 = (int)(u % groups) * kCopies;
-    const int e = find_entry(a.off, a.n, t);
+    const int e = pages_find(a.n, t, [&](int i) { return __ldcg(&a.off[i]); });
     const int o0 = __ldcg(&a.off[e]), o1 = __ldcg(&a.off[e + 1]), r = a.req ? __ldcg(&a.req[e]) : e;
     if (t < o0 || t >= o1) continue;  // nobody's row
     bool ok = o0 >= 0 && o1 <= a.total && r >= 0 && r < p.n_requests;
@@ -540,24 +528,22 @@ hf_status done(cudaError_t e) {
 }
 bool off4(const void* q) { return reinterpret_cast<uintptr_t>(q) % 4 != 0; }
 
-const char* list_bad(const hf_pages* p, int32_t n) {
-  if (const char* m = pages_bad(p, true)) return m;
+const char* list_bad(const hf_pages* p, int32_t n, bool e4m3 = false) {
+  if (const char* m = pages_bad(p, true, e4m3)) return m;
   if (n < 0 || n > p->n_requests) return "n must be 0..n_requests";
   return nullptr;
 }
 
 }  // namespace
-}  // namespace hf
 
-extern "C" size_t hf_pages_work_ints(const hf_pages* p) {
-  if (hf::pages_bad(p, false)) return 0;
-  return hf::kMoves + 2 * (size_t)std::max(p->n_pages, p->n_requests);
+size_t pages_work_ints(const hf_pages* p, bool e4m3) {
+  if (pages_bad(p, false, e4m3)) return 0;
+  return kMoves + 2 * (size_t)std::max(p->n_pages, p->n_requests);
 }
 
-extern "C" hf_status hf_pages_truncate(const hf_pages* p, const int32_t* requests, const int32_t* keep,
-                                       int32_t n, void* stream) {
-  using namespace hf;
-  if (const char* m = list_bad(p, n)) return refuse(m);
+hf_status pages_truncate(const hf_pages* p, bool e4m3, const int32_t* requests, const int32_t* keep, int32_t n,
+                         void* stream) {
+  if (const char* m = list_bad(p, n, e4m3)) return refuse(m);
   if (n == 0) return HF_OK;
   if (!keep) return refuse("NULL buffer");
   if (off4(requests) || off4(keep)) return refuse("lists must be 4-byte aligned");
@@ -565,10 +551,8 @@ extern "C" hf_status hf_pages_truncate(const hf_pages* p, const int32_t* request
                          keep, (int)n));
 }
 
-extern "C" hf_status hf_pages_fork(const hf_pages* p, const int32_t* from, const int32_t* into, int32_t n,
-                                   void* stream) {
-  using namespace hf;
-  if (const char* m = list_bad(p, n)) return refuse(m);
+hf_status pages_fork(const hf_pages* p, bool e4m3, const int32_t* from, const int32_t* into, int32_t n, void* stream) {
+  if (const char* m = list_bad(p, n, e4m3)) return refuse(m);
   if (n == 0) return HF_OK;
   if (!from || !into) return refuse("NULL buffer");
   if (off4(from) || off4(into)) return refuse("lists must be 4-byte aligned");
@@ -576,31 +560,52 @@ extern "C" hf_status hf_pages_fork(const hf_pages* p, const int32_t* from, const
                          (int)n));
 }
 
-extern "C" hf_status hf_pages_extend(const hf_pages* p, const int32_t* requests, const int32_t* counts,
-                                     int32_t n, void* stream) {
-  using namespace hf;
-  if (const char* m = list_bad(p, n)) return refuse(m);
+hf_status pages_extend(const hf_pages* p, bool e4m3, PageScales s, const int32_t* requests, const int32_t* counts,
+                       int32_t n, void* stream) {
+  if (const char* m = list_bad(p, n, e4m3)) return refuse(m);
   if (n == 0) return HF_OK;
   if (!counts) return refuse("NULL buffer");
   if (off4(requests) || off4(counts)) return refuse("lists must be 4-byte aligned");
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = launch_pdl(extend_plan, dim3(1), dim3(PT), 0, st, *p, requests, counts, (int)n);
   // at most one copied page per request, in pieces of 16 KB
-  const long long pieces = (pages_block(p) * (p->dtype == HF_F32 ? 4 : 2) / 16 + CT * 4 - 1) / (CT * 4);
+  const long long pieces = (pages_block(p) * pages_esize(p->dtype) / 16 + CT * 4 - 1) / (CT * 4);
   const long long units = (long long)n * p->n_layers * 2 * pieces;
   if (e == cudaSuccess)
-    e = launch_pdl(extend_copy, dim3((unsigned)std::min<long long>(units, 152 * 8)), dim3(CT), 0, st, *p);
+    e = launch_pdl(extend_copy, dim3((unsigned)std::min<long long>(units, 152 * 8)), dim3(CT), 0, st, *p, s);
   return done(e);
 }
 
-extern "C" hf_status hf_pages_compact(const hf_pages* p, int32_t* n_used, void* stream) {
-  using namespace hf;
-  if (const char* m = pages_bad(p, true)) return refuse(m);
+hf_status pages_compact(const hf_pages* p, bool e4m3, PageScales s, int32_t* n_used, void* stream) {
+  if (const char* m = pages_bad(p, true, e4m3)) return refuse(m);
   if (off4(n_used)) return refuse("n_used must be 4-byte aligned");
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = launch_pdl(compact_plan, dim3(1), dim3(PT), 0, st, *p, n_used);
-  if (e == cudaSuccess) e = launch_pdl(compact_move, dim3(152 * 8), dim3(CT), 0, st, *p);
+  if (e == cudaSuccess) e = launch_pdl(compact_move, dim3(152 * 8), dim3(CT), 0, st, *p, s);
   return done(e);
+}
+
+}  // namespace hf
+
+extern "C" size_t hf_pages_work_ints(const hf_pages* p) { return hf::pages_work_ints(p, false); }
+
+extern "C" hf_status hf_pages_truncate(const hf_pages* p, const int32_t* requests, const int32_t* keep,
+                                       int32_t n, void* stream) {
+  return hf::pages_truncate(p, false, requests, keep, n, stream);
+}
+
+extern "C" hf_status hf_pages_fork(const hf_pages* p, const int32_t* from, const int32_t* into, int32_t n,
+                                   void* stream) {
+  return hf::pages_fork(p, false, from, into, n, stream);
+}
+
+extern "C" hf_status hf_pages_extend(const hf_pages* p, const int32_t* requests, const int32_t* counts,
+                                     int32_t n, void* stream) {
+  return hf::pages_extend(p, false, {}, requests, counts, n, stream);
+}
+
+extern "C" hf_status hf_pages_compact(const hf_pages* p, int32_t* n_used, void* stream) {
+  return hf::pages_compact(p, false, {}, n_used, stream);
 }
 
 extern "C" hf_status hf_pages_write(const hf_pages* p, int32_t layer, int32_t layers, const void* k,
