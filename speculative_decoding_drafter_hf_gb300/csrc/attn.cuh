@@ -72,7 +72,8 @@ struct AttnRows {
   int* eff;        // [n] tokens of each entry, 0 for those that break a rule
   int* line;       // tensor cores: an AttnLine
   int* tile0;      // [n + 1] where each entry starts on the line
-  int tb, units, unit_rows;  // tensor cores: tokens of a row tile; units of an entry's rows
+  int tile;        // tensor cores: rows of a row tile
+  int tb, units, unit_rows;  // tokens of a row tile; units of an entry's rows
 };
 
 __host__ __device__ inline bool attn_direct(const AttnRows& a) { return a.npre + a.nown == 1; }
@@ -228,8 +229,11 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a, int tid, int th
   if (bad) atomicOr(a.status, HF_S_BAD);
 }
 
-// Tensor-core variants (attn_tc.cu), where attn_tc_ok.
+// Tensor-core variants (attn_tc.cu; an 8-bit cache: attn_tc8.cu), where attn_tc_ok.
 bool attn_tc_ok(int dtype, int dh);
+constexpr int kTileRows = 128, kTileRows8 = 64;
+cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t st);
+bool attn_gives_up();  // a test made every wait give up before it begins
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
 // Over a paged cache: the prefix's pieces and the rows' units (fields of a), items of the
 // prefix and slots of own pieces.

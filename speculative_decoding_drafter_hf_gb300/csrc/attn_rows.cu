@@ -744,9 +744,9 @@ struct PagesPlan {
   int pre_items;                        // tensor cores: items of the prefix
   size_t eff, tile0, ml, o, total;      // offsets in the workspace (the line is at 0)
 };
-PagesPlan plan_call(AttnRows& a, int dtype, bool e4m3) {
+PagesPlan plan_call(AttnRows& a, int dtype) {
   PagesPlan w{};
-  w.tc = !e4m3 && attn_tc_ok(dtype, a.dh);
+  w.tc = attn_tc_ok(dtype, a.dh);
   const size_t N = (size_t)a.n * a.rows * a.Hq;
   size_t rows;
   if (w.tc) {
@@ -786,13 +786,14 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
   if (shared < 0 || shared % p->page || shared > (long long)p->table_ld * p->page)
     return "shared must be a multiple of page, at most table_ld * page";
   if ((long long)n * rows * hq > 0x7fffffffLL / 4 ||
-      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart) * n * ((long long)rows * hq / 128 + p->n_kv_heads) > 0x3fffffffLL)
+      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart) * n * ((long long)rows * hq / (c.e4m3 ? kTileRows8 : kTileRows) + p->n_kv_heads) > 0x3fffffffLL)
     return "n * rows * n_q_heads, or that times the table's reach, is too large";
   a.Hq = hq;
   a.Hkv = p->n_kv_heads;
   a.G = hq / p->n_kv_heads;
   a.dh = p->head_dim;
   a.esize = pages_esize(c.dtype);
+  a.tile = c.e4m3 ? kTileRows8 : kTileRows;
   a.table = p->table;
   a.lens = p->lens;
   a.status = p->status;
@@ -810,7 +811,7 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
 size_t attend_workspace(const AnyPages& c, int n, int rows, int hq, int shared) {
   AttnRows a{};
   if (pages_args(c, false, std::max(n, 1), rows, hq, shared, a)) return 0;
-  return plan_call(a, c.dtype, c.e4m3).total;
+  return plan_call(a, c.dtype).total;
 }
 
 hf_status attend(const AnyPages& c, int32_t layer, int32_t n, int32_t rows, int32_t n_q_heads, const void* q,
@@ -828,7 +829,7 @@ hf_status attend(const AnyPages& c, int32_t layer, int32_t n, int32_t rows, int3
                         ld_bad(out_ld, (long long)n_q_heads * p->head_dim, a.esize, out)})
     if (m) return refuse(m);
   if (off(requests, 4)) return refuse("requests must be 4-byte aligned");
-  const PagesPlan w = plan_call(a, c.dtype, c.e4m3);
+  const PagesPlan w = plan_call(a, c.dtype);
   if (off(workspace, 16) || workspace_bytes < w.total) {
     char m[160];
     snprintf(m, sizeof m, "workspace must be 16-byte aligned and hold %zu bytes (hf_attention_pages%s_workspace), got %zu",
@@ -856,7 +857,7 @@ hf_status attend(const AnyPages& c, int32_t layer, int32_t n, int32_t rows, int3
   if (w.tc) {
     a.line = reinterpret_cast<int*>(ws);
     a.tile0 = reinterpret_cast<int*>(ws + w.tile0);
-    e = launch_attn_tc_pages(a, w.pre_items, st);
+    e = c.e4m3 ? launch_attn_tc8_pages(a, w.pre_items, st) : launch_attn_tc_pages(a, w.pre_items, st);
   } else {
     e = launch_attn_rows_pages(c.dtype, a, st);
   }

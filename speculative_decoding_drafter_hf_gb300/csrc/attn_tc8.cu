@@ -1,0 +1,821 @@
+// Attention of the newest rows over the 8-bit cache on the tensor cores (bf16 rows, head dim 64 or
+// 128), its common prefix read once for all.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  s_ij = c_i ks_j (q_i . k_j),  p_ij = 2^s_ij
+// with k_j, v_j codes, ks_j, vs_j the scales of their pages, q_i a row in units of its own scale. The
+// codes are operands of the tensor cores as they come from memory (kind::f8f6f4): nothing turns them into a
+// wider type. The products are formed the other way round, keys along the 128 lanes of TMEM:
+//   S' = K Q'  (128 keys x rows),   O' += V' W  (head dim x rows),   w_ij = p_ij vs_j 2^-M_i
+// so that a tile's work goes by its rows (4 of a decoded token, 32 of 8 verified ones) and not by 128, and
+// a softmax thread has a key: one scale of K, one of V, one position to compare, for all rows.
+//
+// Rows and weights have more bits than a code: each goes in as two codes, hi = its nearest, lo = the
+// nearest of the rest, side by side as columns of one product; the two columns of the result are added. That
+// is 8 bits and more: a bf16 row exactly, down to 2^-18 of its largest value; a weight
+// to 2^-8, or 2^-14 of the largest one. Sums, maxima and TMEM are fp32.
+//
+// M_i is raised only when a weight passes 2^8, to where the largest is 2^5: a raise needs
+// the maximum over the 128 threads, so most tiles only vote on one. The sum of p_ij is kept per thread,
+// as w_ij / vs_j, and joined at an item's end.
+//
+// The CTA's warps, items, the line of own tiles and the parts are those of attn_tc.cu: warp 0 loads
+// (TMA; the scales by 4-byte copies beside V's pages), warp 1 issues the products, warp 2 hands out
+// items, warps 4-7 and 8-11 are the softmax groups of two row tiles of up to 64 rows.
+#include <mutex>
+
+#include "attn_tc.cuh"
+#include "e4m3.cuh"
+
+namespace hf {
+namespace {
+
+constexpr int NR = kTileRows8;  // rows of a row tile
+constexpr float kLift = 8.f, kLifted = 5.f;
+constexpr float kNoMax = -1e30f;
+
+template <int DH>
+struct Tc8 {
+  static constexpr int TILE = BN * DH;                // bytes of a K or V tile, and of a row tile's codes
+  static constexpr int SLOTS = DH == 128 ? 9 : 16;    // ring of K and V tiles
+  static constexpr int W = BN * 2 * NR;               // bytes of a tile's weights
+  static constexpr int BARS = 2 * SLOTS + 14;         // (an even number: 16 bytes for what comes behind)
+  static constexpr size_t smem() {
+    return (size_t)(2 + SLOTS) * TILE + 2 * W + BARS * 8 + 2 * 80 + 16 + SLOTS * 32 * 4 + 2 * NR * 4 * 8 + (2 * kSmall + 2) * 4;
+  }
+};
+static_assert(Tc8<128>::smem() <= 232448 && Tc8<64>::smem() <= 232448, "shared memory of a CTA");
+
+// High words of the operands' descriptors. K and the rows along their bytes, V across its keys: rows of DH
+// bytes, swizzled by 128 or 64 bytes, groups of 8 rows one after the other.
+template <int DH>
+constexpr uint32_t kHi = ((uint32_t)(8 * DH) >> 4) | (1u << 14) | ((DH == 128 ? 2u : 4u) << 29);
+// Weights, across their keys, not swizzled: pieces of 16 rows x 8 keys (128 bytes), the next 8 keys
+// 128 bytes further (low word), the next 16 rows 2048.
+constexpr uint32_t kHiW = (2048u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_keys(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+// V as an operand of 128 rows: for heads of 64 the other 64 are whatever lies 512 bytes on (inside the CTA's shared
+// memory), lanes 64 .. 127 of the sums are not read.
+__device__ __forceinline__ uint32_t desc_values(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((512u >> 4) << 16); }
+__device__ __forceinline__ uint32_t desc_weights(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((128u >> 4) << 16); }
+
+// e4m3 x e4m3 -> fp32, 128 x n; bits 15, 16: A, B across their rows.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n, uint32_t across) {
+  return (1u << 4) | across | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma8(uint32_t lead, uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                     uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%2, %6};\n\tmov.b64 y, {%3, %7};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%1], x, y, %4, p;\n\t}\n" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(a_hi), "r"(b_hi));
+}
+
+__device__ __forceinline__ void tmem_ld16_async(uint32_t t, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_hold16(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+      : "memory");
+}
+
+// Barrier of a softmax group; true if some thread says so.
+__device__ __forceinline__ bool group_any(int r, bool x) {
+  uint32_t y;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(y)
+      : "r"((uint32_t)x), "r"(1 + r)
+      : "memory");
+  return y != 0;
+}
+
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0)
+               : "memory");
+}
+// The barrier counts this thread once its copies have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Two weights (0 .. 2^8, or NaN) as two codes each.
+__device__ __forceinline__ void split_codes(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = to_e4m3x2(x, y);
+  const float2 h = from_e4m3x2(hi);
+  lo = to_e4m3x2(x - h.x, y - h.y);
+}
+
+// What a softmax group has in shared memory for its row tile's rows.
+struct GroupRows {
+  float2 cm[NR];   // factor of the scores (base 2) and M
+  int lim[NR];     // keys below it are seen
+  float red[NR];   // maxima, sums or factors being joined
+};
+static_assert(sizeof(GroupRows) == NR * 16, "size in Tc8::smem");
+
+template <int DH>
+struct Group {
+  const TcArgs& c;
+  Item& it;
+  uint8_t* sQ;      // this group's rows
+  uint8_t* sKV;
+  uint8_t* sW;
+  uint64_t* full;
+  const float* sc;  // [slot][K, V][page of the tile]
+  GroupRows* rows;
+  float* red;       // [4][NR]
+  uint32_t b_s, b_o;
+  uint64_t *q_full, *p_full;
+  uint32_t ts, to;
+  int r, quad, lane;
+  const int* s_eff;
+};
+
+// Maxima or sums of 16 columns over a warp's lanes: the one of column (lane >> 1 & 15) in every lane.
+template <bool SUM>
+__device__ __forceinline__ float warp_columns(float* v, int lane) {
+  auto join = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+#pragma unroll
+  for (int o = 16, n = 8; n >= 1; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], o);
+      v[i] = join(up ? v[i + n] : v[i], other);
+    }
+  }
+  return join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+template <int DH>
+__device__ __noinline__ float odd_sum8(const AttnRows& a, const Item& it, int g, int j0, int j1, int d) {
+  for (int j = j0; j < j1; ++j) {
+    const int id = attn_table(a, it.entry)[j / a.page];
+    if (id < 0 || id >= a.n_pages) continue;
+    const size_t at = (((size_t)id * a.Hkv + g) * a.page + j % a.page) * DH + d;
+    if ((static_cast<const uint8_t*>(a.v)[at] & 0x7f) == 0x7f) return NAN;
+  }
+  return 0.f;
+}
+
+// An item's softmax by one group, its rows in NC sixteens. tiles: key tiles of this group so far;
+// ring: tiles of the ring so far. False: a wait ran out (the same answer in all of the group's threads).
+template <int DH, int NC>
+__device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int ring) {
+  using L = Tc8<DH>;
+  constexpr int NS = L::SLOTS, N = NC * 16;
+  const AttnRows& a = G.c.a;
+  Item& it = G.it;
+  const int r = G.r, lane = G.lane, row = G.quad * 32 + lane;
+  const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1, g = it.g + (split ? r : 0);
+  const int tl0 = split ? 0 : r * G.c.tb;  // first token within the item
+  GroupRows& R = *G.rows;
+  bool fail = false;
+
+  // ---- the rows as codes, their factors and limits
+  constexpr int PER = DH / 8;  // threads of a row, 8 values each
+  {
+    uint4 x[N * PER / 128];
+#pragma unroll
+    for (int i = 0; i < N * PER / 128; ++i) {
+      const int n = (i * 128 + row) / PER, part = row % PER, tl = tl0 + n / a.G;
+      const bool on = n < G.c.tb * a.G && tl < it.ntok && g < a.Hkv;
+      x[i] = on ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl) * a.q_ld +
+                                                  (size_t)(g * a.G + n % a.G) * DH + part * 8)
+                : make_uint4(0, 0, 0, 0);
+    }
+    if (row < N) {
+      const int tl = tl0 + row / a.G;
+      int limit = kNone;  // (rows without a token, entries without tokens: all, and dropped)
+      if (row < G.c.tb * a.G && tl < it.ntok) {
+        const int t = it.t0 + tl;
+        const int len = it.kind == 1 ? (G.c.small ? G.s_eff[t / a.rows] : __ldcg(&a.eff[t / a.rows])) : it.len;
+        if (len > 0) limit = max(0, len - a.rows + (it.kind == 1 ? t % a.rows : t) + 1);
+      }
+      R.lim[row] = limit;
+    }
+#pragma unroll
+    for (int i = 0; i < N * PER / 128; ++i) {
+      const int n = (i * 128 + row) / PER, part = row % PER;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float v[8], top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+#pragma unroll
+      for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // as scale_for, for every bf16 value
+      const int bits = __float_as_int(top);
+      const int e = min(max((bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000), -110), 119);
+      const float inv = pow2f(-e);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split_codes(no_inf(v[2 * k]) * inv, no_inf(v[2 * k + 1]) * inv, hi[k], lo[k]);
+      // 16-byte pieces of a row change places by the row's number, as the copies of K do it
+      auto at = [&](int q) {
+        const int piece = (part >> 1) ^ (DH == 128 ? q & 7 : (q >> 1) & 3);
+        return reinterpret_cast<uint2*>(G.sQ + q * DH + piece * 16 + (part & 1) * 8);
+      };
+      *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      if (part == 0) R.cm[n] = make_float2(a.qscale * pow2f(e), kNoMax);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (group_any(r, false)) return false;
+    if (mine > 0 && lane == 0) mbar_arrive(G.q_full);
+  }
+
+  const int streams = split && it.nt[1] > 0 ? 2 : 1, look = it.first_cut(), most = max(it.nt[0], it.nt[1]);
+  const int shift = 31 - __clz(a.page);
+  float l[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) l[n] = 0.f;
+  for (int j = 0; j < mine; ++j) {
+    const int jt = j0 + j * BN, key = jt + row;
+    const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j + (j + 1 < most ? 2 * r : r)), vs = vi % NS;
+    fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)(vi / NS) & 1u);
+    const float ks = held_scale(G.sc[vs * 32 + (row >> shift)]), vscale = held_scale(G.sc[vs * 32 + 16 + (row >> shift)]);
+    const float lv = (float)((__float_as_int(vscale) >> 23) - 127), rv = 1.f / vscale;
+    fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
+    tc_fence_after();
+    float s[N];
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      float t[16];
+      tmem_ld16_async(G.ts + h * 16, s + h * 16);
+      tmem_ld16_async(G.ts + N + h * 16, t);
+      tmem_wait_ld();
+      tmem_hold16(s + h * 16);
+      tmem_hold16(t);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) s[h * 16 + n] = (s[h * 16 + n] + t[n]) * ks;
+    }
+    if (jt + BN > min(it.low, j1)) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (key >= min(R.lim[n], j1)) s[n] = -INFINITY;
+    }
+    // exponents above M; a vote on a raise
+    float top = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < N; ++n) top = fmaxf(top, fmaf(s[n], R.cm[n].x, lv - R.cm[n].y));
+    if (group_any(r, fail || top > kLift)) {
+      // the maximum of every row over the 128 keys
+      if (group_any(r, fail)) return false;
+#pragma unroll
+      for (int h = 0; h < NC; ++h) {
+        float t[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) t[n] = fmaf(s[h * 16 + n], R.cm[h * 16 + n].x, lv);
+        const float m = warp_columns<false>(t, lane);
+        if (!(lane & 1)) G.red[G.quad * NR + h * 16 + (lane >> 1)] = m;
+      }
+      group_any(r, false);
+      if (row < N) {
+        const float m = fmaxf(fmaxf(G.red[row], G.red[NR + row]), fmaxf(G.red[2 * NR + row], G.red[3 * NR + row]));
+        const float old = R.cm[row].y, now = m - old > kLift ? m - kLifted : old;
+        R.red[row] = ex2(old - now);
+        R.cm[row].y = now;
+      }
+      if (j > 0) fail = !wait_uniform(G.b_o, (uint32_t)(tiles + j - 1) & 1u);
+      if (group_any(r, fail)) return false;
+      tc_fence_after();
+      if (j > 0) {
+#pragma unroll
+        for (int h = 0; h < 2 * NC; ++h) {
+          float o[16];
+          tmem_ld16_async(G.to + h * 16, o);
+          tmem_wait_ld();
+          tmem_hold16(o);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) o[n] *= R.red[h % NC * 16 + n];
+          tmem_st16(G.to + h * 16, o);
+        }
+        tmem_wait_st();
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) l[n] *= R.red[n];
+    }
+    uint8_t* w = G.sW + row * 16;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int n = h * 16 + q * 4 + k;
+          p[k] = ex2(fmaf(s[n], R.cm[n].x, lv - R.cm[n].y));
+          l[n] = fmaf(p[k], rv, l[n]);
+        }
+        uint32_t h0, h1, l0, l1;
+        split_codes(p[0], p[1], h0, l0);
+        split_codes(p[2], p[3], h1, l1);
+        hi[q] = h0 | h1 << 16;
+        lo[q] = l0 | l1 << 16;
+      }
+      *reinterpret_cast<uint4*>(w + h * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(w + (NC + h) * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    if (j >= look) {
+      // some row masks keys that the tile holds: NaN codes of V there are set aside
+      uint4* v = reinterpret_cast<uint4*>(G.sKV + (size_t)vs * L::TILE);
+      const int k0 = max(0, min(it.low, j1) - jt), k1 = min(BN, it.hold - jt);
+      const bool both = streams == 1 && j < it.nt[0] && j < it.nt[1];
+      const int step = both ? 256 : 128;
+      for (int q = k0 * (DH / 16) + (both ? r * 128 + row : row); q < k1 * (DH / 16); q += step) {
+        uint4 x = v[q];
+        uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+        uint32_t hit[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) hit[k] = ((xw[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        if (hit[0] | hit[1] | hit[2] | hit[3]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) xw[k] &= ~((hit[k] >> 7) * 0xffu);
+          atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
+          v[q] = x;
+        }
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(G.p_full);
+  }
+
+  // ---- the item's end: the sums over the threads, then the rows
+  if (mine > 0) fail = fail || !wait_uniform(G.b_o, (uint32_t)(tiles + mine - 1) & 1u);
+  tc_fence_after();
+#pragma unroll
+  for (int h = 0; h < NC; ++h) {
+    const float x = warp_columns<true>(l + h * 16, lane);
+    if (!(lane & 1)) G.red[G.quad * NR + h * 16 + (lane >> 1)] = x;
+  }
+  if (group_any(r, fail)) return false;
+  const bool direct = it.direct;
+  const int heads = g < a.Hkv ? min(G.c.tb, it.ntok - tl0) * a.G : 0;  // rows with a token
+  PartAt at{};
+  if (heads > 0) at = it.kind == 1 ? part_prefix(a, it.part, g, it.t0 + tl0, 0) : part_own_unit(a, it.part, g, it.t0 + tl0, 0);
+  if (row < N) {
+    const float sum = G.red[row] + G.red[NR + row] + (G.red[2 * NR + row] + G.red[3 * NR + row]);
+    bool dead = false;
+    if (row < heads && it.kind == 1) {
+      const int e = (it.t0 + tl0 + row / a.G) / a.rows;
+      dead = (G.c.small ? G.s_eff[e] : __ldcg(&a.eff[e])) == 0;
+    }
+    R.red[row] = sum == 0.f || dead ? 0.f : 1.f / sum;
+    if (!direct && row < heads)
+      a.part_ml[at.first + at.row + row] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(R.cm[row].y, sum);
+  }
+  group_any(r, false);
+  const int from = *(volatile int*)&it.odd[streams == 1 ? 0 : r];
+#pragma unroll 1
+  for (int h = 0; h < NC; ++h) {
+    if (h * 16 >= heads) break;
+    __syncwarp();
+    float o[16], t[16];
+    if (mine > 0) {
+      tmem_ld16_async(G.to + h * 16, o);
+      tmem_ld16_async(G.to + N + h * 16, t);
+      tmem_wait_ld();
+      tmem_hold16(o);
+      tmem_hold16(t);
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n) o[n] = mine > 0 ? o[n] + t[n] : 0.f;
+    if (row >= DH) continue;
+    if (from < j1) {
+#pragma unroll 1
+      for (int n = 0; n < 16; ++n) {
+        if (h * 16 + n >= heads) break;
+        const int lim = R.lim[h * 16 + n];
+        if (lim == kNone || from >= min(lim, j1)) continue;
+        const float x = odd_sum8<DH>(a, it, g, from, min(lim, j1), row);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = i == n ? o[i] + x : o[i];
+      }
+    }
+    if (direct) {
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int m = h * 16 + n;
+        if (m >= heads) break;
+        const float inv = R.red[m];
+        static_cast<__nv_bfloat16*>(a.out)[((size_t)it.tok0 + tl0 + m / a.G) * a.out_ld + (size_t)(g * a.G + m % a.G) * DH + row] =
+            __float2bfloat16_rn(inv == 0.f ? 0.f : o[n] * inv);
+      }
+    } else if (mine > 0) {
+      float* dst = a.part_o + at.first * DH + ((size_t)(row / 8) * at.region + at.row + h * 16) * 8 + row % 8;
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+        if (h * 16 + n < heads) dst[n * 8] = o[n];
+    }
+  }
+  tc_fence_before();
+  return true;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(TCT, 1)
+tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ TcArgs c) {
+  using L = Tc8<DH>;
+  constexpr int NS = L::SLOTS;
+  const AttnRows& a = c.a;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * L::TILE;
+  uint8_t* sW = sKV + (size_t)NS * L::TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sW + 2 * L::W);
+  uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;   // [2] rows as codes
+  uint64_t* s_full = q_full + 2;   // [2]
+  uint64_t* p_full = q_full + 4;   // [2]
+  uint64_t* o_full = q_full + 6;   // [2]
+  uint64_t* i_full = q_full + 8;   // [2] items
+  uint64_t* i_empty = q_full + 10; // [2]
+  uint64_t* drained = q_full + 12; // after a wait that ran out: the products have ended
+  Item* items = reinterpret_cast<Item*>(full + L::BARS);  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued = abort_flag + 1;  // tiles that the loader has asked for
+  float* s_sc = reinterpret_cast<float*>(tmem_slot + 4);       // [NS][2][16]
+  GroupRows* s_rows = reinterpret_cast<GroupRows*>(s_sc + NS * 32);  // [2]
+  float* s_red = reinterpret_cast<float*>(s_rows + 2);         // [2][4][NR]
+  int* s_eff = reinterpret_cast<int*>(s_red + 2 * 4 * NR);     // small calls: [kSmall] lengths, [kSmall + 1] places
+  int* s_tile0 = s_eff + kSmall;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 33);  // the tile's bytes, and the scales of 32 lanes
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(drained, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&q_full[g], 4);
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&o_full[g], 1);
+      mbar_init(&i_full[g], 1);
+      mbar_init(&i_empty[g], 10);  // the loader, the products, eight softmax warps
+    }
+    *abort_flag = 0;
+    *issued = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (tid >= 64 && tid < 66) {  // (the first copies would wait for them)
+    const CUtensorMap* map = tid == 64 ? &mk : &mv;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  __syncwarp();
+
+  if (c.wait == 0) {
+    *abort_flag = 1;
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ---- loads: a stream's K(0), then V(j), K(j+1) through the ring
+      int ri = 0;  // tiles so far
+      bool ok = true;
+      const int nbox = BN / a.page, shift = 31 - __clz(a.page);
+      for (int n = 0; ok; ++n) {
+        const Item& it = items[n & 1];
+        ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+        if (!ok || it.kind < 0) break;
+        const int nt0 = it.nt[0], nt1 = it.nt[1], nt = max(nt0, nt1), j1 = it.j1, split = it.split, g = it.g;
+        const int32_t* tab = attn_table(a, it.entry);
+        auto tile = [&](int j, int r, bool is_v) {  // tile j of stream r
+          if (!ok) return;
+          const int s = ri % NS;
+          if (ri >= NS) ok = wait_uniform(smem_u32(&empty[s]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
+          if (!ok || *abort_flag) {
+            ok = false;
+            return;
+          }
+          if (lane == 0) mbar_expect_tx(&full[s], L::TILE);
+          __syncwarp();
+          if (lane < nbox) {
+            const int key = it.j0 + j * BN + lane * a.page;
+            int z = a.n_pages * a.Hkv;  // behind the pool: reads zeros
+            bool on = false;
+            if (key < j1) {
+              const int id = tab[key >> shift];
+              on = id >= 0 && id < a.n_pages;
+              if (on)
+                z = id * a.Hkv + g + r;
+              else if (a.status)
+                atomicOr(a.status, HF_S_BAD);
+            }
+            tma_load_3d(sKV + (size_t)s * L::TILE + lane * a.page * DH, is_v ? &mv : &mk, &full[s], 0, 0, z);
+            if (is_v) {  // both scales: V's slot stays until the weights are there
+              copy4(s_sc + s * 32 + lane, a.k_scale + (on ? z : 0), on);
+              copy4(s_sc + s * 32 + 16 + lane, a.v_scale + (on ? z : 0), on);
+            }
+          }
+          copies_arrive(&full[s]);
+          ++ri;
+        };
+        if (nt > 0) {
+          const int streams = split && nt1 > 0 ? 2 : 1;
+          for (int r = 0; r < streams; ++r) tile(0, r, false);
+          for (int j = 0; j < nt && ok; ++j)
+            for (int r = 0; r < streams; ++r) {
+              tile(j, r, true);
+              if (j + 1 < nt) tile(j + 1, r, false);
+            }
+        }
+        if (lane == 0) mbar_arrive(&i_empty[n & 1]);
+      }
+      if (lane == 0) {
+        *issued = ri;
+        if (!ok) *abort_flag = 1;
+      }
+    } else if (warp == 1) {
+      // ---- products: S_r(0), then V_r(j) W, S_r(j+1) for r = 0, 1 in turn
+      const uint32_t lead = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t dq = desc_keys(smem_u32(sQ)), dk = desc_keys(smem_u32(sKV)), dv = desc_values(smem_u32(sKV)),
+                     dw = desc_weights(smem_u32(sW));
+      const uint32_t b_full = smem_u32(full), b_empty = smem_u32(empty), b_s = smem_u32(s_full), b_p = smem_u32(p_full),
+                     b_o = smem_u32(o_full), b_q = smem_u32(q_full);
+      int at = 0;           // next slot of the ring, and the parity of its fill
+      uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+      bool ok = true;
+      uint32_t id_s = 0, id_o = 0;
+      auto next = [&]() {  // waits for the next slot of the ring
+        const int s = at;
+        ok = ok && wait_uniform(b_full + 8 * s, ph);
+        if (++at == NS) {
+          at = 0;
+          ph ^= 1u;
+        }
+        return s;
+      };
+      auto score = [&](int r, int slot) {
+#pragma unroll
+        for (int k = 0; k < DH / 32; ++k)
+          mma8(lead, tm + r * 128, dk + slot * (L::TILE >> 4) + 2 * k, kHi<DH>, dq + r * (L::TILE >> 4) + 2 * k, kHi<DH>,
+               id_s, k > 0);
+        mma_commit(lead, b_s + 8 * r);
+      };
+      for (int n = 0; ok; ++n) {
+        const Item& it = items[n & 1];
+        ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+        if (!ok || __shfl_sync(0xffffffffu, it.kind, 0) < 0) break;
+        const int nt0 = __shfl_sync(0xffffffffu, it.nt[0], 0), nt1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
+        const bool two = __shfl_sync(0xffffffffu, it.split, 0) && nt1 > 0;  // two streams of keys
+        const int nt = max(nt0, nt1), cols = 32 * __shfl_sync(0xffffffffu, it.cols, 0);
+        id_s = idesc_e4m3(cols, 0);
+        id_o = idesc_e4m3(cols, 3u << 15);
+        if (nt > 0) {
+          int ks = next();
+          int ks1 = two ? next() : ks;
+          if (nt0 > 0) {
+            ok = ok && wait_uniform(b_q, qph[0]);
+            qph[0] ^= 1u;
+          }
+          if (ok) {
+            tc_fence_after();
+            score(0, ks);
+            if (two) mma_commit(lead, b_empty + 8 * ks);
+          }
+          if (nt1 > 0) {
+            ok = ok && wait_uniform(b_q + 8, qph[1]);
+            qph[1] ^= 1u;
+            if (ok) {
+              tc_fence_after();
+              score(1, ks1);
+            }
+          }
+          if (ok) mma_commit(lead, b_empty + 8 * ks1);
+          int vs = 0;
+          // from tile `look` on the softmax groups look V over before they hand their weights
+          // on; where both have the tile, each looks at half of it
+          const int look = __shfl_sync(0xffffffffu, it.first_cut(), 0);
+          for (int j = 0; j < nt && ok; ++j) {
+            const bool more = j + 1 < nt;
+            if (!two) {
+              vs = next();
+              if (more) ks = next();
+            }
+            const bool both = !two && j >= look && j < nt0 && j < nt1;
+            if (both) ok = ok && wait_uniform(b_p, pph[0]) && wait_uniform(b_p + 8, pph[1]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int mine = r ? nt1 : nt0;
+              if (!ok || j >= mine) continue;
+              if (two) vs = next();
+              if (!both) ok = ok && wait_uniform(b_p + 8 * r, pph[r]);
+              pph[r] ^= 1u;
+              if (!ok) continue;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < BN / 32; ++k)
+                mma8(lead, tm + 256 + r * 128, dv + vs * (L::TILE >> 4) + k * (32 * DH >> 4), kHi<DH>,
+                     dw + r * (L::W >> 4) + k * (512 >> 4), kHiW, id_o, j > 0 || k > 0);
+              mma_commit(lead, b_o + 8 * r);
+              if (two) mma_commit(lead, b_empty + 8 * vs);
+              if (j + 1 < mine) {
+                if (two) ks = next();
+                if (!ok) continue;
+                tc_fence_after();
+                score(r, ks);
+                if (two) mma_commit(lead, b_empty + 8 * ks);
+              }
+            }
+            if (ok && !two) {
+              mma_commit(lead, b_empty + 8 * vs);
+              if (more) mma_commit(lead, b_empty + 8 * ks);
+            }
+          }
+        }
+        if (lane == 0) mbar_arrive(&i_empty[n & 1]);
+      }
+      if (!ok) *abort_flag = 1;
+    } else if (warp == 2) {
+      // ---- items
+      bool ok = true;
+      int n = 0;
+      auto put = [&](const Item& it) {
+        if (n >= 2) ok = wait_uniform(smem_u32(&i_empty[n & 1]), ((uint32_t)(n >> 1) & 1u) ^ 1u);
+        if (!ok) return;
+        if (lane == 0) {
+          items[n & 1] = it;
+          mbar_arrive(&i_full[n & 1]);
+        }
+        ++n;
+      };
+      Item it;
+      const int me = blockIdx.x, all = gridDim.x;
+      const int *eff = a.eff, *tile0 = a.tile0;
+      if (c.small) {
+        bool bad = false;
+        for (int i = lane; i < a.n; i += 32) {
+          s_eff[i] = attn_len(a, i, bad);
+          if (me == 0) a.eff[i] = s_eff[i];
+        }
+        if (bad && a.status && me == 0) atomicOr(a.status, HF_S_BAD);
+        eff = s_eff;
+        tile0 = s_tile0;
+        __syncwarp();
+      }
+      for (int idx = me; ok && idx < c.pre_items; idx += all) {
+        make_prefix(c, idx, it, eff);
+        put(it);
+      }
+      const int heavy = c.pre_items % all;
+      AttnLine line;
+      if (c.small) {
+        line = make_line(scan_tiles(a, s_eff, s_tile0), a.units, all, heavy, prefix_places(a));
+        if (me == 0) {
+          for (int i = lane; i <= a.n; i += 32) a.tile0[i] = s_tile0[i];
+          if (lane == 0) *reinterpret_cast<AttnLine*>(a.line) = line;
+        }
+      } else {
+        line = *reinterpret_cast<const AttnLine*>(a.line);
+      }
+      const int cta = (me - heavy + all) % all, end = min(line.start(cta + 1), line.tiles * a.units);
+      for (int pos = line.start(cta); ok && pos < end;) {
+        bool some;
+        pos += make_own(c, line, cta, pos, end, it, some, eff, tile0);
+        if (some) put(it);
+      }
+      it.kind = -1;
+      if (ok) put(it);
+      if (!ok) *abort_flag = 1;
+    } else if (c.small) {
+      check_prefixes(a, 1 + blockIdx.x, gridDim.x, lane, 32);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int r = warp >= 8, quad = warp & 3;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    int tiles = 0, ring = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      Item& it = items[n & 1];
+      // (the group's warps go on together: a wait that ran out in one ends it in all)
+      ok = !group_any(r, !wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u));
+      if (!ok || it.kind < 0) break;
+      const Group<DH> G{c,    it,           sQ + r * L::TILE, sKV,
+                        sW + r * L::W,      full,             s_sc, s_rows + r, s_red + r * 4 * NR,
+                        smem_u32(&s_full[r]), smem_u32(&o_full[r]), &q_full[r], &p_full[r],
+                        tmem + lanes + r * 128, tmem + lanes + 256 + r * 128, r, quad, lane, s_eff};
+      const int cols = it.cols;
+      const int streams = it.split && it.nt[1] > 0 ? 2 : 1;
+      ok = cols == 1   ? soft_item<DH, 1>(G, tiles, ring)
+           : cols == 2 ? soft_item<DH, 2>(G, tiles, ring)
+           : cols == 3 ? soft_item<DH, 3>(G, tiles, ring)
+                       : soft_item<DH, 4>(G, tiles, ring);
+      if (!ok) break;
+      tiles += it.nt[r];
+      ring += 2 * max(it.nt[0], it.nt[1]) * streams;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[n & 1]);
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  __syncwarp();
+  __syncthreads();
+  if (*abort_flag) {
+    // the lengths and the line that the join reads may be missing: it takes entries without
+    // tokens for empty, and looks at nothing else of them
+    if (c.small && blockIdx.x == 0)
+      for (int i = tid; i < a.n; i += TCT) a.eff[i] = 0;
+    if (warp == 1) {  // the products still in flight end before their operands and TMEM go
+      mma_commit(elect_one(), smem_u32(drained));  // (the lane that issued them)
+      wait_uniform(smem_u32(drained), 0);
+    }
+    if (tid == 0) {
+      if (a.status) atomicOr(a.status, HF_S_TIMEOUT);
+      // the copies still in flight land before the CTA's shared memory goes
+      for (int i = max(0, *issued - NS); i < *issued; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u);
+    }
+    __syncthreads();
+  }
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+constexpr int kMaxDev = 64;
+std::mutex g_mu;
+bool g_set[kMaxDev][2] = {};
+
+template <int DH>
+cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mk, const CUtensorMap& mv, dim3 grid, cudaStream_t st) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    bool& set = g_set[dev & (kMaxDev - 1)][DH == 128];
+    if (!set || dev >= kMaxDev) {
+      e = cudaFuncSetAttribute(tc8_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc8<DH>::smem());
+      if (e != cudaSuccess) return e;
+      set = true;
+    }
+  }
+  return launch_pdl(tc8_kernel<DH>, grid, dim3(TCT), Tc8<DH>::smem(), st, mk, mv, c);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t st) {
+  TcArgs c{};
+  c.a = a;
+  c.tb = a.tb;
+  c.blocks = (int)(((long long)a.n * a.rows + 2 * c.tb - 1) / (2 * c.tb));
+  c.box_rows = a.page;
+  c.wait = !attn_gives_up();
+  c.pre_items = pre_items;
+  CUtensorMap mk, mv;
+  cudaError_t e = make_map_pages8(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv);
+  if (e == cudaSuccess) e = make_map_pages8(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv);
+  if (e != cudaSuccess) return e;
+  // (the line is at most as long as all tables reach)
+  const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;
+  const int grid = (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
+  c.small = a.n <= kSmall;
+  if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
+  if (e != cudaSuccess) return e;
+  return a.dh == 128 ? launch_one<128>(c, mk, mv, dim3(grid), st) : launch_one<64>(c, mk, mv, dim3(grid), st);
+}
+
+}  // namespace hf

@@ -642,6 +642,21 @@ cudaError_t make_map_3d(CUtensorMap* map, const void* base, long long n0, long l
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Pages of an 8-bit cache: bytes [blocks][page][dh], dh 64 or 128, one block's rows a box, swizzled by
+// its row.
+cudaError_t make_map_pages8(CUtensorMap* map, const void* base, int dh, int page, long long blocks) {
+  cudaError_t e = get_encoder();
+  if (e != cudaSuccess) return e;
+  cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)page, (cuuint64_t)blocks};
+  cuuint64_t strides[2] = {(cuuint64_t)dh, (cuuint64_t)dh * page};
+  cuuint32_t box[3] = {(cuuint32_t)dh, (cuuint32_t)page, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, dh == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // 2-D fp32 tensor map over rows x cols (row stride cols elements, a multiple
 // of 4), box 32 columns (128 bytes) x box_rows, 128-byte swizzle.
 cudaError_t make_map_f32(CUtensorMap* map, const void* base, long long rows, long long cols,
