@@ -148,7 +148,6 @@ struct Item {
   int direct;      // rows go to out
   int part;        // else: the prefix's piece, the own pieces' slot
   int low, hold;   // least number of keys that a row sees; keys behind `hold` read as zeros
-  int cols;        // 8-bit cache: rows of a row tile in use, in sixteens
   int odd[2];      // first key of a tile whose odd values of V were taken as zero
   // first key tile that holds keys which some row masks (so does every later one)
   __device__ __forceinline__ int first_cut() const {
@@ -191,7 +190,6 @@ __device__ __forceinline__ void make_prefix(const TcArgs& c, int idx, Item& it, 
   it.low = __reduce_min_sync(0xffffffffu, low);
   const int nt = it.nt[0] = (it.j1 - it.j0 + BN - 1) / BN;
   it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? nt : 0;
-  it.cols = (min(it.ntok, c.tb) * a.G + 15) / 16;
 }
 
 // The item at pos of the line, in the stretch [pos, end) of its CTA `cta`, if a tile lies
@@ -236,7 +234,6 @@ __device__ __forceinline__ int make_own(const TcArgs& c, const AttnLine& line, i
   it.part = u * a.n + lo + cta;
   it.nt[0] = take;
   it.nt[1] = (it.split ? it.g + 1 < a.Hkv : it.ntok > c.tb) ? take : 0;
-  it.cols = (min(it.ntok, c.tb) * a.G + 15) / 16;
   return skip + take;
 }
 

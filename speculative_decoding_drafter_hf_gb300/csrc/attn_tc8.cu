@@ -10,13 +10,13 @@
 // a softmax thread has a key: one scale of K, one of V, one position to compare, for all rows.
 //
 // Rows and weights have more bits than a code: each goes in as two codes, hi = its nearest, lo = the
-// nearest of the rest, side by side as columns of one product; the two columns of the result are added. That
-// is 8 bits and more: a bf16 row exactly, down to 2^-18 of its largest value; a weight
-// to 2^-8, or 2^-14 of the largest one. Sums, maxima and TMEM are fp32.
+// nearest of 16 times the rest, side by side as columns of one product; of the two columns of the result the
+// second counts a sixteenth. That is 8 bits and more: a bf16 row exactly, down to 2^-22 of its
+// largest value; a weight to 2^-8, or 2^-15 of the largest one. Sums, maxima and TMEM are fp32.
 //
-// M_i is raised only when a weight passes 2^8, to where the largest is 2^5: a raise needs
-// the maximum over the 128 threads, so most tiles only vote on one. The sum of p_ij is kept per thread,
-// as w_ij / vs_j, and joined at an item's end.
+// M_i is set by an item's first tile, to where the largest weight is 2^1, and raised to there when one
+// passes 2^8: that needs the maximum over the 128 threads, so most tiles only vote on it. The sum of p_ij
+// is kept per thread, as w_ij / vs_j, and joined at an item's end.
 //
 // The CTA's warps, items, the line of own tiles and the parts are those of attn_tc.cu: warp 0 loads
 // (TMA; the scales by 4-byte copies beside V's pages), warp 1 issues the products, warp 2 hands out
@@ -30,8 +30,11 @@ namespace hf {
 namespace {
 
 constexpr int NR = kTileRows8;  // rows of a row tile
-constexpr float kLift = 8.f, kLifted = 5.f;
-constexpr float kNoMax = -1e30f;
+constexpr float kLift = 8.f, kLifted = 1.f;
+constexpr float kFine = 16.f;  // lo is held times this
+
+constexpr int kItems = 160;  // bytes of two items: what comes behind them starts on 16 bytes
+static_assert(2 * sizeof(Item) <= kItems, "item slots");
 
 template <int DH>
 struct Tc8 {
@@ -40,9 +43,10 @@ struct Tc8 {
   static constexpr int W = BN * 2 * NR;               // bytes of a tile's weights
   static constexpr int BARS = 2 * SLOTS + 14;         // (an even number: 16 bytes for what comes behind)
   static constexpr size_t smem() {
-    return (size_t)(2 + SLOTS) * TILE + 2 * W + BARS * 8 + 2 * 80 + 16 + SLOTS * 32 * 4 + 2 * NR * 4 * 8 + (2 * kSmall + 2) * 4;
+    return (size_t)(2 + SLOTS) * TILE + 2 * W + BARS * 8 + kItems + 16 + SLOTS * 32 * 4 + 2 * NR * 4 * 8 + (2 * kSmall + 2) * 4;
   }
 };
+static_assert(Tc8<128>::BARS % 2 == 0 && Tc8<64>::BARS % 2 == 0 && kItems % 16 == 0, "16-byte reads behind the barriers");
 static_assert(Tc8<128>::smem() <= 232448 && Tc8<64>::smem() <= 232448, "shared memory of a CTA");
 
 // High words of the operands' descriptors. K and the rows along their bytes, V across its keys: rows of DH
@@ -123,19 +127,32 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Two weights (0 .. 2^8, or NaN) as two codes each.
+// Two values (magnitude up to 448, or NaN) as two codes each. In 16 bits: a code is exact there, and so is
+// the rest of a value of 11 bits, 2^-12 of it being nothing beside lo's own rounding.
 __device__ __forceinline__ void split_codes(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = to_e4m3x2(x, y);
-  const float2 h = from_e4m3x2(hi);
-  lo = to_e4m3x2(x - h.x, y - h.y);
+  uint32_t r;
+  asm("{\n\t.reg .b32 a, b, c;\n\t.reg .b16 l;\n\t"
+      "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, %1;\n\t"
+      "mov.b32 c, 0x4c004c00;\n\t"        // 16
+      "sub.rn.f16x2 a, a, b;\n\t"
+      "mul.rn.f16x2 a, a, c;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, a;\n\t"
+      "cvt.u32.u16 %0, l;\n\t}\n"
+      : "=r"(r)
+      : "h"((uint16_t)hi), "f"(x), "f"(y));
+  lo = r;
 }
 
 // What a softmax group has in shared memory for its row tile's rows.
 struct GroupRows {
-  float2 cm[NR];   // factor of the scores (base 2) and M
-  int lim[NR];     // keys below it are seen
-  float red[NR];   // maxima, sums or factors being joined
+  float4 cm[NR / 2];  // two rows' factors of the scores (base 2), and their -M
+  int lim[NR];        // keys below it are seen
+  float red[NR];      // maxima, sums or factors being joined
 };
+__device__ __forceinline__ float& row_factor(GroupRows& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + (n & 1)]; }
+__device__ __forceinline__ float& row_minus_m(GroupRows& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + 2 + (n & 1)]; }
 static_assert(sizeof(GroupRows) == NR * 16, "size in Tc8::smem");
 
 template <int DH>
@@ -196,6 +213,9 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
   const int tl0 = split ? 0 : r * G.c.tb;  // first token within the item
   GroupRows& R = *G.rows;
   bool fail = false;
+  // n / G of n < 64, G <= 64
+  const uint32_t by_g = (65535u + a.G) / a.G;
+  auto token_of = [&](int n) { return (int)(n * by_g >> 16); };
 
   // ---- the rows as codes, their factors and limits
   constexpr int PER = DH / 8;  // threads of a row, 8 values each
@@ -203,14 +223,14 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
     uint4 x[N * PER / 128];
 #pragma unroll
     for (int i = 0; i < N * PER / 128; ++i) {
-      const int n = (i * 128 + row) / PER, part = row % PER, tl = tl0 + n / a.G;
+      const int n = (i * 128 + row) / PER, part = row % PER, t = token_of(n), tl = tl0 + t;
       const bool on = n < G.c.tb * a.G && tl < it.ntok && g < a.Hkv;
       x[i] = on ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl) * a.q_ld +
-                                                  (size_t)(g * a.G + n % a.G) * DH + part * 8)
+                                                  (size_t)(g * a.G + n - t * a.G) * DH + part * 8)
                 : make_uint4(0, 0, 0, 0);
     }
     if (row < N) {
-      const int tl = tl0 + row / a.G;
+      const int tl = tl0 + token_of(row);
       int limit = kNone;  // (rows without a token, entries without tokens: all, and dropped)
       if (row < G.c.tb * a.G && tl < it.ntok) {
         const int t = it.t0 + tl;
@@ -247,7 +267,10 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
       };
       *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      if (part == 0) R.cm[n] = make_float2(a.qscale * pow2f(e), kNoMax);
+      if (part == 0) {
+        row_factor(R, n) = a.qscale * pow2f(e);
+        row_minus_m(R, n) = 0.f;
+      }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (group_any(r, false)) return false;
@@ -256,96 +279,122 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
 
   const int streams = split && it.nt[1] > 0 ? 2 : 1, look = it.first_cut(), most = max(it.nt[0], it.nt[1]);
   const int shift = 31 - __clz(a.page);
-  float l[N];
+  uint64_t l2[N / 2];  // sums of two rows each
 #pragma unroll
-  for (int n = 0; n < N; ++n) l[n] = 0.f;
+  for (int n = 0; n < N / 2; ++n) l2[n] = 0;
   for (int j = 0; j < mine; ++j) {
     const int jt = j0 + j * BN, key = jt + row;
     const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j + (j + 1 < most ? 2 * r : r)), vs = vi % NS;
     fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)(vi / NS) & 1u);
     const float ks = held_scale(G.sc[vs * 32 + (row >> shift)]), vscale = held_scale(G.sc[vs * 32 + 16 + (row >> shift)]);
     const float lv = (float)((__float_as_int(vscale) >> 23) - 127), rv = 1.f / vscale;
+    const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), rv2 = pair(rv, rv), fine2 = pair(1.f / kFine, 1.f / kFine);
     fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
     tc_fence_after();
-    float s[N];
-#pragma unroll
-    for (int h = 0; h < NC; ++h) {
-      float t[16];
-      tmem_ld16_async(G.ts + h * 16, s + h * 16);
-      tmem_ld16_async(G.ts + N + h * 16, t);
-      tmem_wait_ld();
-      tmem_hold16(s + h * 16);
-      tmem_hold16(t);
-#pragma unroll
-      for (int n = 0; n < 16; ++n) s[h * 16 + n] = (s[h * 16 + n] + t[n]) * ks;
-    }
-    if (jt + BN > min(it.low, j1)) {
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (key >= min(R.lim[n], j1)) s[n] = -INFINITY;
-    }
-    // exponents above M; a vote on a raise
-    float top = -INFINITY;
-#pragma unroll
-    for (int n = 0; n < N; ++n) top = fmaxf(top, fmaf(s[n], R.cm[n].x, lv - R.cm[n].y));
-    if (group_any(r, fail || top > kLift)) {
-      // the maximum of every row over the 128 keys
-      if (group_any(r, fail)) return false;
-#pragma unroll
-      for (int h = 0; h < NC; ++h) {
-        float t[16];
-#pragma unroll
-        for (int n = 0; n < 16; ++n) t[n] = fmaf(s[h * 16 + n], R.cm[h * 16 + n].x, lv);
-        const float m = warp_columns<false>(t, lane);
-        if (!(lane & 1)) G.red[G.quad * NR + h * 16 + (lane >> 1)] = m;
-      }
-      group_any(r, false);
-      if (row < N) {
-        const float m = fmaxf(fmaxf(G.red[row], G.red[NR + row]), fmaxf(G.red[2 * NR + row], G.red[3 * NR + row]));
-        const float old = R.cm[row].y, now = m - old > kLift ? m - kLifted : old;
-        R.red[row] = ex2(old - now);
-        R.cm[row].y = now;
-      }
-      if (j > 0) fail = !wait_uniform(G.b_o, (uint32_t)(tiles + j - 1) & 1u);
-      if (group_any(r, fail)) return false;
-      tc_fence_after();
-      if (j > 0) {
-#pragma unroll
-        for (int h = 0; h < 2 * NC; ++h) {
-          float o[16];
-          tmem_ld16_async(G.to + h * 16, o);
-          tmem_wait_ld();
-          tmem_hold16(o);
-#pragma unroll
-          for (int n = 0; n < 16; ++n) o[n] *= R.red[h % NC * 16 + n];
-          tmem_st16(G.to + h * 16, o);
-        }
-        tmem_wait_st();
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n) l[n] *= R.red[n];
-    }
+    const bool cut = jt + BN > min(it.low, j1);
     uint8_t* w = G.sW + row * 16;
+    // 32 rows at a time: the exponents of more do not fit the registers beside the sums
 #pragma unroll
-    for (int h = 0; h < NC; ++h) {
-      uint32_t hi[4], lo[4];
+    for (int h0 = 0; h0 < NC; h0 += 2) {
+      constexpr int HB = NC < 2 ? NC : 2;
+      const int hb = NC - h0 < HB ? NC - h0 : HB;
+      float z[HB * 16];  // exponents of the weights
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float p[4];
+      for (int i = 0; i < HB; ++i) {
+        if (i >= hb) continue;
+        const int h = h0 + i;
+        float t[16];
+        tmem_ld16_async(G.ts + h * 16, z + i * 16);
+        tmem_ld16_async(G.ts + N + h * 16, t);
+        tmem_wait_ld();
+        tmem_hold16(z + i * 16);
+        tmem_hold16(t);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int n = h * 16 + q * 4 + k;
-          p[k] = ex2(fmaf(s[n], R.cm[n].x, lv - R.cm[n].y));
-          l[n] = fmaf(p[k], rv, l[n]);
+        for (int n = 0; n < 16; n += 2) {
+          const int m = i * 16 + n;
+          const float4 cm = R.cm[h * 8 + n / 2];
+          const uint64_t s2 = fma2(pair(t[n], t[n + 1]), fine2, pair(z[m], z[m + 1]));
+          const float2 e = unpair(fma2(s2, mul2(pair(cm.x, cm.y), ks2), add2(pair(cm.z, cm.w), lv2)));
+          z[m] = e.x;
+          z[m + 1] = e.y;
         }
-        uint32_t h0, h1, l0, l1;
-        split_codes(p[0], p[1], h0, l0);
-        split_codes(p[2], p[3], h1, l1);
-        hi[q] = h0 | h1 << 16;
-        lo[q] = l0 | l1 << 16;
+        if (cut) {
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (key >= min(R.lim[h * 16 + n], j1)) z[i * 16 + n] = -INFINITY;
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) top[n & 3] = max3(top[n & 3], z[i * 16 + n], z[i * 16 + 8 + n]);
       }
-      *reinterpret_cast<uint4*>(w + h * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(w + (NC + h) * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      // a vote on a raise
+      if (group_any(r, fail || fmaxf(max3(top[0], top[1], top[2]), top[3]) > kLift) || j == 0) {
+        // the maximum of every row over the 128 keys
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+        if (i >= hb) continue;
+        const int h = h0 + i;
+          float t[16];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) t[n] = z[i * 16 + n];
+          const float m = warp_columns<false>(t, lane);
+          if (!(lane & 1)) G.red[G.quad * NR + h * 16 + (lane >> 1)] = m;
+        }
+        if (j > 0) fail = fail || !wait_uniform(G.b_o, (uint32_t)(tiles + j - 1) & 1u);
+        if (group_any(r, fail)) return false;
+        tc_fence_after();
+        if (row >= h0 * 16 && row < (h0 + hb) * 16) {
+          const float m = fmaxf(fmaxf(G.red[row], G.red[NR + row]), fmaxf(G.red[2 * NR + row], G.red[3 * NR + row]));
+          // (a row that sees nothing of the first tile sees nothing of the item)
+          const float down = (j == 0 ? m > -INFINITY : m > kLift) ? kLifted - m : 0.f;
+          R.red[row] = down;
+          row_minus_m(R, row) += down;
+        }
+        group_any(r, false);
+        if (j > 0) {
+#pragma unroll 1
+          for (int i = 0; i < 2 * hb; ++i) {
+            const int c = (h0 + (i >> 1)) * 16, h = h0 + (i >> 1) + (i & 1) * NC;
+            float o[16];
+            tmem_ld16_async(G.to + h * 16, o);
+            tmem_wait_ld();
+            tmem_hold16(o);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n] *= ex2(R.red[c + n]);
+            tmem_st16(G.to + h * 16, o);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int n = 0; n < HB * 16; n += 2) {
+          if (n >= hb * 16) continue;
+          const float2 down = *reinterpret_cast<const float2*>(&R.red[h0 * 16 + n]);
+          l2[h0 * 8 + n / 2] = mul2(l2[h0 * 8 + n / 2], pair(j > 0 ? ex2(down.x) : 1.f, j > 0 ? ex2(down.y) : 1.f));
+          z[n] += down.x;
+          z[n + 1] += down.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < HB; ++i) {
+        if (i >= hb) continue;
+        const int h = h0 + i;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t hh[2], ll[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int n = q * 4 + k * 2;
+            const float x = ex2(z[i * 16 + n]), y = ex2(z[i * 16 + n + 1]);
+            l2[h * 8 + n / 2] = fma2(pair(x, y), rv2, l2[h * 8 + n / 2]);
+            split_codes(x, y, hh[k], ll[k]);
+          }
+          hi[q] = hh[0] | hh[1] << 16;
+          lo[q] = ll[0] | ll[1] << 16;
+        }
+        *reinterpret_cast<uint4*>(w + h * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(w + (NC + h) * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
     if (j >= look) {
       // some row masks keys that the tile holds: NaN codes of V there are set aside
@@ -378,7 +427,14 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
   tc_fence_after();
 #pragma unroll
   for (int h = 0; h < NC; ++h) {
-    const float x = warp_columns<true>(l + h * 16, lane);
+    float t[16];
+#pragma unroll
+    for (int n = 0; n < 16; n += 2) {
+      const float2 x = unpair(l2[h * 8 + n / 2]);
+      t[n] = x.x;
+      t[n + 1] = x.y;
+    }
+    const float x = warp_columns<true>(t, lane);
     if (!(lane & 1)) G.red[G.quad * NR + h * 16 + (lane >> 1)] = x;
   }
   if (group_any(r, fail)) return false;
@@ -390,12 +446,12 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
     const float sum = G.red[row] + G.red[NR + row] + (G.red[2 * NR + row] + G.red[3 * NR + row]);
     bool dead = false;
     if (row < heads && it.kind == 1) {
-      const int e = (it.t0 + tl0 + row / a.G) / a.rows;
+      const int e = (it.t0 + tl0 + token_of(row)) / a.rows;
       dead = (G.c.small ? G.s_eff[e] : __ldcg(&a.eff[e])) == 0;
     }
     R.red[row] = sum == 0.f || dead ? 0.f : 1.f / sum;
     if (!direct && row < heads)
-      a.part_ml[at.first + at.row + row] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(R.cm[row].y, sum);
+      a.part_ml[at.first + at.row + row] = dead || mine == 0 ? make_float2(-INFINITY, 0.f) : make_float2(-row_minus_m(R, row), sum);
   }
   group_any(r, false);
   const int from = *(volatile int*)&it.odd[streams == 1 ? 0 : r];
@@ -412,7 +468,7 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
       tmem_hold16(t);
     }
 #pragma unroll
-    for (int n = 0; n < 16; ++n) o[n] = mine > 0 ? o[n] + t[n] : 0.f;
+    for (int n = 0; n < 16; ++n) o[n] = mine > 0 ? fmaf(t[n], 1.f / kFine, o[n]) : 0.f;
     if (row >= DH) continue;
     if (from < j1) {
 #pragma unroll 1
@@ -428,10 +484,10 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
     if (direct) {
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
-        const int m = h * 16 + n;
+        const int m = h * 16 + n, t = token_of(m);
         if (m >= heads) break;
         const float inv = R.red[m];
-        static_cast<__nv_bfloat16*>(a.out)[((size_t)it.tok0 + tl0 + m / a.G) * a.out_ld + (size_t)(g * a.G + m % a.G) * DH + row] =
+        static_cast<__nv_bfloat16*>(a.out)[((size_t)it.tok0 + tl0 + t) * a.out_ld + (size_t)(g * a.G + m - t * a.G) * DH + row] =
             __float2bfloat16_rn(inv == 0.f ? 0.f : o[n] * inv);
       }
     } else if (mine > 0) {
@@ -445,7 +501,9 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
   return true;
 }
 
-template <int DH>
+// NO, NP: sixteens of rows of a row tile, of an entry's own keys and of the prefix (0: none). One pair a
+// kernel: a softmax loop for every number of rows in one kernel spills its registers.
+template <int DH, int NO, int NP>
 __global__ void __launch_bounds__(TCT, 1)
 tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ TcArgs c) {
   using L = Tc8<DH>;
@@ -465,7 +523,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   uint64_t* i_empty = q_full + 10; // [2]
   uint64_t* drained = q_full + 12; // after a wait that ran out: the products have ended
   Item* items = reinterpret_cast<Item*>(full + L::BARS);  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(items) + kItems);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;  // tiles that the loader has asked for
   float* s_sc = reinterpret_cast<float*>(tmem_slot + 4);       // [NS][2][16]
@@ -521,7 +579,13 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (!ok || it.kind < 0) break;
         const int nt0 = it.nt[0], nt1 = it.nt[1], nt = max(nt0, nt1), j1 = it.j1, split = it.split, g = it.g;
         const int32_t* tab = attn_table(a, it.entry);
-        auto tile = [&](int j, int r, bool is_v) {  // tile j of stream r
+        // this lane's page of tile j, looked up a tile ahead: once for K and V of both streams
+        auto page_at = [&](int j) {
+          const int key = it.j0 + j * BN + lane * a.page;
+          return j < nt && lane < nbox && key < j1 ? tab[key >> shift] : -2;
+        };
+        int now = page_at(0), then = page_at(1);
+        auto tile = [&](int id, int r, bool is_v) {  // of stream r
           if (!ok) return;
           const int s = ri % NS;
           if (ri >= NS) ok = wait_uniform(smem_u32(&empty[s]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
@@ -532,17 +596,9 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           if (lane == 0) mbar_expect_tx(&full[s], L::TILE);
           __syncwarp();
           if (lane < nbox) {
-            const int key = it.j0 + j * BN + lane * a.page;
-            int z = a.n_pages * a.Hkv;  // behind the pool: reads zeros
-            bool on = false;
-            if (key < j1) {
-              const int id = tab[key >> shift];
-              on = id >= 0 && id < a.n_pages;
-              if (on)
-                z = id * a.Hkv + g + r;
-              else if (a.status)
-                atomicOr(a.status, HF_S_BAD);
-            }
+            const bool on = id >= 0 && id < a.n_pages;
+            const int z = on ? id * a.Hkv + g + r : a.n_pages * a.Hkv;  // behind the pool: reads zeros
+            if (!on && id != -2 && a.status) atomicOr(a.status, HF_S_BAD);
             tma_load_3d(sKV + (size_t)s * L::TILE + lane * a.page * DH, is_v ? &mv : &mk, &full[s], 0, 0, z);
             if (is_v) {  // both scales: V's slot stays until the weights are there
               copy4(s_sc + s * 32 + lane, a.k_scale + (on ? z : 0), on);
@@ -554,12 +610,16 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         };
         if (nt > 0) {
           const int streams = split && nt1 > 0 ? 2 : 1;
-          for (int r = 0; r < streams; ++r) tile(0, r, false);
-          for (int j = 0; j < nt && ok; ++j)
+          for (int r = 0; r < streams; ++r) tile(now, r, false);
+          for (int j = 0; j < nt && ok; ++j) {
+            const int next = page_at(j + 2);
             for (int r = 0; r < streams; ++r) {
-              tile(j, r, true);
-              if (j + 1 < nt) tile(j + 1, r, false);
+              tile(now, r, true);
+              if (j + 1 < nt) tile(then, r, false);
             }
+            now = then;
+            then = next;
+          }
         }
         if (lane == 0) mbar_arrive(&i_empty[n & 1]);
       }
@@ -601,7 +661,8 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (!ok || __shfl_sync(0xffffffffu, it.kind, 0) < 0) break;
         const int nt0 = __shfl_sync(0xffffffffu, it.nt[0], 0), nt1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
         const bool two = __shfl_sync(0xffffffffu, it.split, 0) && nt1 > 0;  // two streams of keys
-        const int nt = max(nt0, nt1), cols = 32 * __shfl_sync(0xffffffffu, it.cols, 0);
+        const int nt = max(nt0, nt1);
+        const int cols = 32 * (NP > 0 && __shfl_sync(0xffffffffu, it.kind, 0) == 1 ? NP : NO);
         id_s = idesc_e4m3(cols, 0);
         id_o = idesc_e4m3(cols, 3u << 15);
         if (nt > 0) {
@@ -738,12 +799,11 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                         sW + r * L::W,      full,             s_sc, s_rows + r, s_red + r * 4 * NR,
                         smem_u32(&s_full[r]), smem_u32(&o_full[r]), &q_full[r], &p_full[r],
                         tmem + lanes + r * 128, tmem + lanes + 256 + r * 128, r, quad, lane, s_eff};
-      const int cols = it.cols;
       const int streams = it.split && it.nt[1] > 0 ? 2 : 1;
-      ok = cols == 1   ? soft_item<DH, 1>(G, tiles, ring)
-           : cols == 2 ? soft_item<DH, 2>(G, tiles, ring)
-           : cols == 3 ? soft_item<DH, 3>(G, tiles, ring)
-                       : soft_item<DH, 4>(G, tiles, ring);
+      if (NP > 0 && it.kind == 1)
+        ok = soft_item<DH, NP == 0 ? 1 : NP>(G, tiles, ring);
+      else
+        ok = soft_item<DH, NO>(G, tiles, ring);
       if (!ok) break;
       tiles += it.nt[r];
       ring += 2 * max(it.nt[0], it.nt[1]) * streams;
@@ -776,23 +836,33 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-bool g_set[kMaxDev][2] = {};
+bool g_set[kMaxDev][2][4][2] = {};
 
-template <int DH>
+template <int DH, int NO, int NP>
 cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mk, const CUtensorMap& mv, dim3 grid, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    bool& set = g_set[dev & (kMaxDev - 1)][DH == 128];
+    bool& set = g_set[dev & (kMaxDev - 1)][DH == 128][NO - 1][NP > 0];
     if (!set || dev >= kMaxDev) {
-      e = cudaFuncSetAttribute(tc8_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc8<DH>::smem());
+      e = cudaFuncSetAttribute(tc8_kernel<DH, NO, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc8<DH>::smem());
       if (e != cudaSuccess) return e;
       set = true;
     }
   }
-  return launch_pdl(tc8_kernel<DH>, grid, dim3(TCT), Tc8<DH>::smem(), st, mk, mv, c);
+  return launch_pdl(tc8_kernel<DH, NO, NP>, grid, dim3(TCT), Tc8<DH>::smem(), st, mk, mv, c);
+}
+
+template <int DH, int NP>
+cudaError_t launch_rows(const TcArgs& c, const CUtensorMap& mk, const CUtensorMap& mv, dim3 grid, cudaStream_t st) {
+  switch ((std::min(c.a.rows, c.tb) * c.a.G + 15) / 16) {
+    case 1: return launch_one<DH, 1, NP>(c, mk, mv, grid, st);
+    case 2: return launch_one<DH, 2, NP>(c, mk, mv, grid, st);
+    case 3: return launch_one<DH, 3, NP>(c, mk, mv, grid, st);
+    default: return launch_one<DH, 4, NP>(c, mk, mv, grid, st);
+  }
 }
 
 }  // namespace
@@ -815,7 +885,9 @@ cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t
   c.small = a.n <= kSmall;
   if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
   if (e != cudaSuccess) return e;
-  return a.dh == 128 ? launch_one<128>(c, mk, mv, dim3(grid), st) : launch_one<64>(c, mk, mv, dim3(grid), st);
+  if (pre_items > 0)
+    return a.dh == 128 ? launch_rows<128, 4>(c, mk, mv, dim3(grid), st) : launch_rows<64, 4>(c, mk, mv, dim3(grid), st);
+  return a.dh == 128 ? launch_rows<128, 0>(c, mk, mv, dim3(grid), st) : launch_rows<64, 0>(c, mk, mv, dim3(grid), st);
 }
 
 }  // namespace hf
