@@ -59,6 +59,7 @@ struct AttnRows {
   // 8-bit cache: the layer's scales [n_pages, Hkv]; NULL of any other
   const float* k_scale;
   const float* v_scale;
+  int dense;       // tensor cores: the prefix lies in rows k, v (k_ld, v_ld), only its pieces are computed
   // pieces of the key axis: npre of the prefix (pre_keys keys each), then each
   // entry's own tokens: on CUDA cores nown pieces of own_keys each (unused ones
   // among them), on tensor cores wherever the line of all tiles is cut (AttnLine). Rows

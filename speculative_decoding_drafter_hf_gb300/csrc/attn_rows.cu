@@ -740,18 +740,32 @@ void plan_pieces(AttnRows& a) {
 
 // Sizes and workspace of a call.
 struct PagesPlan {
-  bool tc;
+  bool tc, dense;                       // dense: an 8-bit cache's prefix as bf16 rows
   int pre_items;                        // tensor cores: items of the prefix
-  size_t eff, tile0, ml, o, total;      // offsets in the workspace (the line is at 0)
+  size_t eff, tile0, ml, o, k, v, total; // offsets in the workspace (the line is at 0)
 };
+// More rows of a KV head than two row tiles of codes share the prefix's keys: it is turned into bf16 rows once (a
+// power of two as the scale: exactly) and taken by the kernel for those, 256 rows at a time. MEASURED
+constexpr int kDenseRows = 2 * kTileRows8;
 PagesPlan plan_call(AttnRows& a, int dtype) {
   PagesPlan w{};
   w.tc = attn_tc_ok(dtype, a.dh);
   const size_t N = (size_t)a.n * a.rows * a.Hq;
   size_t rows;
+  w.dense = w.tc && a.tile == kTileRows8 && a.shared > 0 && (long long)a.n * a.rows * a.G > kDenseRows;
   if (w.tc) {
     long long slots;
-    attn_tc_sizes(a, w.pre_items, slots);
+    int pre = 0;
+    if (w.dense) {
+      AttnRows b = a;
+      b.tile = kTileRows;
+      attn_tc_sizes(b, w.pre_items, slots);
+      attn_tc_sizes(a, pre, slots);
+      a.npre = b.npre;
+      a.pre_keys = b.pre_keys;
+    } else {
+      attn_tc_sizes(a, w.pre_items, slots);
+    }
     rows = a.npre * N + (size_t)slots * a.unit_rows;
   } else {
     plan_pieces(a);
@@ -762,6 +776,12 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   w.ml = (w.tile0 + ((size_t)a.n + 1) * sizeof(int) + 15) / 16 * 16;
   w.o = (w.ml + rows * sizeof(float2) + 31) / 32 * 32;
   w.total = w.o + rows * a.dh * sizeof(float) + 16;  // (the rows start on 32 bytes)
+  if (w.dense) {
+    const size_t values = (size_t)a.shared * a.Hkv * a.dh * 2;
+    w.k = (w.total + 15) / 16 * 16;
+    w.v = w.k + values;
+    w.total = w.v + values;
+  }
   return w;
 }
 
@@ -857,7 +877,21 @@ hf_status attend(const AnyPages& c, int32_t layer, int32_t n, int32_t rows, int3
   if (w.tc) {
     a.line = reinterpret_cast<int*>(ws);
     a.tile0 = reinterpret_cast<int*>(ws + w.tile0);
-    e = c.e4m3 ? launch_attn_tc8_pages(a, w.pre_items, st) : launch_attn_tc_pages(a, w.pre_items, st);
+    if (w.dense) {
+      AttnRows b = a;
+      b.dense = 1;
+      b.tile = kTileRows;
+      b.tb = kTileRows / a.G;
+      b.units = 0;  // no keys of the entries' own
+      b.k = ws + w.k;
+      b.v = ws + w.v;
+      b.k_ld = b.v_ld = (long long)a.Hkv * a.dh;
+      e = launch_prefix_values(*p, c.s, layer, requests, a.shared, ws + w.k, ws + w.v, st);
+      if (e == cudaSuccess) e = launch_attn_tc_pages(b, w.pre_items, st);
+      if (e == cudaSuccess) e = launch_attn_tc8_pages(a, 0, st);
+    } else {
+      e = c.e4m3 ? launch_attn_tc8_pages(a, w.pre_items, st) : launch_attn_tc_pages(a, w.pre_items, st);
+    }
   } else {
     e = launch_attn_rows_pages(c.dtype, a, st);
   }

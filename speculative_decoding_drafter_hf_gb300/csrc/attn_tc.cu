@@ -196,7 +196,7 @@ __device__ __forceinline__ bool make_prompt(const TcArgs& c, int idx, Item& it, 
 // Element offset in V of key j's row of KV head g.
 template <int MODE>
 __device__ __forceinline__ long long v_at(const AttnRows& a, const Item& it, int g, int j) {
-  if (MODE == PROMPT) return (long long)(it.start + j) * a.v_ld + (long long)g * a.dh;
+  if (MODE == PROMPT || a.dense) return (long long)(it.start + j) * a.v_ld + (long long)g * a.dh;
   const int id = attn_table(a, it.entry)[j / a.page];
   if (id < 0 || id >= a.n_pages) return -1;
   return (((long long)id * a.Hkv + g) * a.page + j % a.page) * a.dh;
@@ -309,8 +309,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
             const int h = lane % HALVES, b = lane / HALVES;
             const int key = it.j0 + j * BN + b * c.box_rows;
             uint8_t* dst = sKV + (size_t)s * L::TILE + h * HALF + b * c.box_rows * 128;
-            if (MODE == PROMPT) {
-              tma_load_3d(dst, is_v ? &mv : &mk, &full[s], h * 64, g, it.start + key);
+            if (MODE == PROMPT || a.dense) {
+              tma_load_3d(dst, is_v ? &mv : &mk, &full[s], h * 64, g + r, it.start + key);
             } else {
               int z = a.n_pages * a.Hkv;  // behind the pool: reads zeros
               if (key < j1) {
@@ -902,14 +902,19 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t 
   c.tb = a.tb;
   const long long tokens = (long long)a.n * a.rows, block = (long long)a.page * a.dh;
   c.blocks = (int)((tokens + 2 * c.tb - 1) / (2 * c.tb));
-  c.box_rows = a.page;
+  c.box_rows = a.dense ? BN : a.page;
   c.wide = wide_rows(a);
   c.wait = !attn_gives_up();
   c.pre_items = pre_items;
   CUtensorMap mq, mk, mv;
   cudaError_t e = make_map_3d(&mq, a.q, a.dh, a.Hq, tokens, a.dh, a.q_ld, a.G, c.tb);
-  if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
-  if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
+  if (a.dense) {
+    if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.Hkv, a.shared, a.dh, a.k_ld, 1, BN);
+    if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.Hkv, a.shared, a.dh, a.v_ld, 1, BN);
+  } else {
+    if (e == cudaSuccess) e = make_map_3d(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
+    if (e == cudaSuccess) e = make_map_3d(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv, a.dh, block, a.page, 1);
+  }
   if (e != cudaSuccess) return e;
   // (the line is at most as long as all tables reach)
   const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;

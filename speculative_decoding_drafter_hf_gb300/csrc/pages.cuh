@@ -26,6 +26,9 @@ hf_status pages_truncate(const hf_pages* p, bool e4m3, const int32_t* requests, 
                          void* stream);
 hf_status pages_compact(const hf_pages* p, bool e4m3, PageScales s, int32_t* n_used, void* stream);
 size_t pages_work_ints(const hf_pages* p, bool e4m3);
+// The first `shared` tokens of request req[0] (NULL: 0) of an 8-bit cache as bf16 rows [shared, n_kv_heads * head_dim].
+cudaError_t launch_prefix_values(const hf_pages& p, PageScales sc, int layer, const int32_t* req, int shared, void* k,
+                                 void* v, cudaStream_t st);
 
 // Pages that a length fills (lengths near 2^31 too).
 __host__ __device__ __forceinline__ int pages_of(int len, int page) { return len / page + (len % page > 0); }

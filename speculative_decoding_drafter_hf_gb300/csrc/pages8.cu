@@ -59,11 +59,27 @@ __device__ __forceinline__ void unpack16(const uint4& w, float* x) {
   }
 }
 
-// Bounds that decrease; by one CTA. Bounds out of range are reported by CTA 0.
-__device__ __forceinline__ bool offsets_fall(const RowsArgs& a) {
+// Values of a lane that stay in registers between the two looks at them: 4 KB a warp.
+constexpr int KEEP = 8;
+constexpr int kListed = kMaxRequests;  // entries whose bounds a CTA keeps in shared memory
+
+// The list of a call as a CTA has it: bounds in shared memory (few entries) or where they lie.
+struct Entries {
+  const RowsArgs& a;
+  int* s_off;
+  __device__ __forceinline__ int off(int i) const { return a.n <= kListed ? s_off[i] : __ldcg(&a.off[i]); }
+  // An entry of c rows reaches at most c / page + 2 pages: it owns the slots [off / page + 2 e, ..) of all, so
+  // that no prefix sum is needed.
+  __device__ __forceinline__ int first_slot(int e) const { return min(max(off(e), 0), a.total) / a.p.page + 2 * e; }
+};
+
+// Loads the bounds; true where they decrease (names rows twice, or entries that no search finds). Bounds out of
+// range are reported by CTA 0. By one CTA.
+__device__ __forceinline__ bool load_entries(const RowsArgs& a, int* s_off) {
   bool falls = false, range = true;
   for (int i = threadIdx.x; i <= a.n; i += CT) {
     const int x = __ldcg(&a.off[i]);
+    if (a.n <= kListed) s_off[i] = x;
     falls = falls || (i > 0 && x < __ldcg(&a.off[i - 1]));
     range = range && x >= 0 && x <= a.total;
   }
@@ -71,162 +87,257 @@ __device__ __forceinline__ bool offsets_fall(const RowsArgs& a) {
   return __syncthreads_or(falls);
 }
 
-// One warp per page that an entry's rows go to, layer, K or V, and KV head. An entry of c rows reaches
-// at most c / page + 2 pages: it owns the slots [off / page + 2 e, ..) of all, no prefix sum needed.
-template <typename T>
+// Which requests the list names twice, one bit each. By one CTA.
+__device__ __forceinline__ void load_twice(const RowsArgs& a, uint32_t* seen, uint32_t* twice) {
+  for (int i = threadIdx.x; i < kMaxRequests / 32; i += CT) seen[i] = twice[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += CT) {
+    const int r = __ldcg(&a.req[i]);
+    if (r < 0 || r >= a.p.n_requests) continue;
+    const uint32_t bit = 1u << (r & 31);
+    if (atomicOr(&seen[r >> 5], bit) & bit) atomicOr(&twice[r >> 5], bit);
+  }
+  __syncthreads();
+}
+
+// One page of an entry, as the call sees it: rows r0 .. r1 - 1 of page `id` and rows src .. of the caller. False:
+// nothing there; an entry that breaks a rule is reported.
+struct PageOf {
+  int id, r0, r1, src;
+};
+template <bool WRITE>
+__device__ __forceinline__ bool page_of(const Entries& E, int slot, const uint32_t* twice, bool report, PageOf& g) {
+  const RowsArgs& a = E.a;
+  const hf_pages& p = a.p;
+  const int e = pages_find(a.n, slot, [&](int i) { return E.first_slot(i); });
+  const int o0 = E.off(e), o1 = E.off(e + 1), r = a.req ? __ldcg(&a.req[e]) : e;
+  const int c = o1 - o0;
+  if (c == 0) return false;
+  bool ok = o0 >= 0 && o1 <= a.total && r >= 0 && r < p.n_requests;
+  if (WRITE && a.req) ok = ok && !(twice[r >> 5] >> (r & 31) & 1);  // (its rows would have two sources)
+  int first = 0;
+  if (ok) {
+    const int len = __ldcg(&p.lens[r]);
+    first = WRITE ? len - c : __ldcg(&a.first[e]);
+    ok = first >= 0 && first <= len && c <= len - first && pages_of(len, p.page) <= p.table_ld;
+  }
+  if (ok) {
+    const int page = first / p.page + slot - E.first_slot(e);
+    const long long base = (long long)page * p.page, end = (long long)first + c;
+    if (base >= end) return false;
+    g.r0 = (int)max(0LL, first - base);
+    g.r1 = (int)min((long long)p.page, end - base);
+    g.src = o0 + (int)(base + g.r0 - first);
+    g.id = __ldcg(&p.table[(size_t)r * p.table_ld + page]);
+    ok = g.id >= 0 && g.id < p.n_pages;
+  }
+  if (!ok && report) pages_flag(p, HF_S_BAD);
+  return ok;
+}
+
+// WPU warps per page that an entry's rows go to, layer, K or V, and KV head: as many as hold its rows in
+// registers between the maximum and the codes (page of 64 x 128 bf16: four; what is more, 128 rows of
+// 256 fp32 values, is read twice).
+template <typename T, int WPU>
 __global__ void __launch_bounds__(CT) write8_kernel(RowsArgs a) {
-  constexpr int VE = 16 / sizeof(T);
+  constexpr int VE = 16 / sizeof(T), UNITS = CT / 32 / WPU;
+  extern __shared__ int s_off[];
+  __shared__ uint32_t s_seen[kMaxRequests / 32], s_twice[kMaxRequests / 32];
+  __shared__ float s_top[CT / 32];
   pdl_trigger();
   pdl_wait();
   const hf_pages& p = a.p;
-  const int lane = threadIdx.x & 31, H = p.n_kv_heads, dh = p.head_dim, hv = dh / VE;
-  if (offsets_fall(a)) return;
-  auto first_slot = [&](int e) { return min(max(__ldcg(&a.off[e]), 0), a.total) / p.page + 2 * e; };
-  const long long per = (long long)a.layers * 2 * H;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPU, H = p.n_kv_heads, dh = p.head_dim, hv = dh / VE;
+  if (load_entries(a, s_off)) return;
+  if (a.req) load_twice(a, s_seen, s_twice);
+  const Entries E{a, s_off};
+  const int per = a.layers * 2 * H;
   const long long units = ((long long)a.total / p.page + 2 * a.n) * per;
-  for (long long u = (long long)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * (CT / 32)) {
+  for (long long u0 = (long long)blockIdx.x * UNITS; u0 < units; u0 += (long long)gridDim.x * UNITS) {
+    const long long u = u0 + warp / WPU;
     const int slot = (int)(u / per);
     int w = (int)(u % per);
     const int h = w % H;
     w /= H;
     const int kv = w & 1, l = w >> 1;
-    const int e = pages_find(a.n, slot, first_slot);
-    const int o0 = __ldcg(&a.off[e]), o1 = __ldcg(&a.off[e + 1]), r = a.req ? __ldcg(&a.req[e]) : e;
-    if (o1 == o0) continue;
-    bool ok = o0 >= 0 && o1 <= a.total && r >= 0 && r < p.n_requests;
-    if (a.req)  // named twice: its rows would have two sources
-      for (int i = lane; i < a.n; i += 32) ok = ok && (i == e || __ldcg(&a.req[i]) != r);
-    ok = __all_sync(0xffffffffu, ok);
-    int id = -1, r0 = 0, r1 = 0, src = 0;
-    if (ok) {
-      const int len = __ldcg(&p.lens[r]), c = o1 - o0, j = slot - first_slot(e);
-      ok = len >= c && pages_of(len, p.page) <= p.table_ld;
-      if (ok) {
-        const int page = (len - c) / p.page + j;
-        const long long base = (long long)page * p.page;
-        if (base >= len) continue;
-        r0 = (int)max(0LL, len - c - base);
-        r1 = (int)min((long long)p.page, len - base);
-        src = o0 + (int)(base + r0 - (len - c));
-        id = __ldcg(&p.table[(size_t)r * p.table_ld + page]);
-        ok = id >= 0 && id < p.n_pages;
-      }
-    }
-    if (!ok) {
-      if (lane == 0) pages_flag(p, HF_S_BAD);
-      continue;
-    }
-    const uint8_t* rows = (kv ? a.v : a.k) + (long long)l * a.layer_stride + (long long)src * a.ld + (long long)h * dh * sizeof(T);
-    const size_t block = ((size_t)(a.layer + l) * p.n_pages + id) * H + h;
-    uint8_t* codes = static_cast<uint8_t*>(kv ? p.v : p.k) + block * p.page * dh;
-    float* scale = (kv ? a.sc.v : a.sc.k) + block;
-    const int vecs = (r1 - r0) * hv;
-    float top = 0.f;
-    for (int i = lane; i < vecs; i += 32) {
-      float x[VE];
-      unpack16<T>(__ldcg(reinterpret_cast<const uint4*>(rows + (long long)(i / hv) * a.ld) + i % hv), x);
+    PageOf g{};
+    const bool on = u < units && page_of<true>(E, slot, s_twice, lane == 0, g);
+    const uint8_t* rows = nullptr;
+    uint8_t* codes = nullptr;
+    float* scale = nullptr;
+    uint4 x[KEEP];
+    float top = 0.f, old = 0.f;
+    auto look = [&](const uint4& y) {
+      float v[VE];
+      unpack16<T>(y, v);
 #pragma unroll
-      for (int k = 0; k < VE; ++k) top = fmaxf(top, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
+      for (int k = 0; k < VE; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+    };
+    const int vecs = on ? (g.r1 - g.r0) * hv : 0, i0 = sub * 32 + lane;
+    auto vec = [&](int i) { return __ldcg(reinterpret_cast<const uint4*>(rows + (long long)(i / hv) * a.ld) + i % hv); };
+    if (on) {
+      rows = (kv ? a.v : a.k) + (long long)l * a.layer_stride + (long long)g.src * a.ld + (long long)h * dh * sizeof(T);
+      const size_t block = ((size_t)(a.layer + l) * p.n_pages + g.id) * H + h;
+      codes = static_cast<uint8_t*>(kv ? p.v : p.k) + block * p.page * dh;
+      scale = (kv ? a.sc.v : a.sc.k) + block;
+      if (g.r0 > 0) old = held_scale(__ldcg(scale));
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k) {
+        const int i = i0 + k * WPU * 32;
+        if (i < vecs) x[k] = vec(i);
+      }
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k)
+        if (i0 + k * WPU * 32 < vecs) look(x[k]);
+      for (int i = i0 + KEEP * WPU * 32; i < vecs; i += WPU * 32) look(vec(i));
     }
+    __syncwarp();
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    float s = scale_for(top);
-    if (r0 > 0) {
-      const float old = held_scale(__ldcg(scale));
-      if (s > old) {  // the rows that stay, again
-        const float f = old / s;
-        for (int i = lane; i < r0 * dh / 16; i += 32) {
-          uint4 c = reinterpret_cast<uint4*>(codes)[i];
-          uint32_t* cw = reinterpret_cast<uint32_t*>(&c);
+    if constexpr (WPU > 1) {
+      if (lane == 0) s_top[warp] = top;
+      __syncthreads();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 lo = from_e4m3x2(cw[k] & 0xffff), hi = from_e4m3x2(cw[k] >> 16);
-            cw[k] = to_e4m3x2(lo.x * f, lo.y * f) | to_e4m3x2(hi.x * f, hi.y * f) << 16;
-          }
-          reinterpret_cast<uint4*>(codes)[i] = c;
+      for (int k = 0; k < WPU; ++k) top = fmaxf(top, s_top[warp - sub + k]);
+      __syncthreads();  // (read before the next unit's)
+    }
+    if (!on) continue;
+    const float s = fmaxf(scale_for(top), old);
+    if (s > old && old > 0.f) {  // the rows that stay, again
+      const float f = old / s;
+      for (int i = i0; i < g.r0 * dh / 16; i += WPU * 32) {
+        uint4 c = reinterpret_cast<uint4*>(codes)[i];
+        uint32_t* cw = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 lo = from_e4m3x2(cw[k] & 0xffff), hi = from_e4m3x2(cw[k] >> 16);
+          cw[k] = to_e4m3x2(lo.x * f, lo.y * f) | to_e4m3x2(hi.x * f, hi.y * f) << 16;
         }
+        reinterpret_cast<uint4*>(codes)[i] = c;
       }
-      s = fmaxf(s, old);
     }
     const float inv = 1.f / s;  // (a power of two)
-    for (int i = lane; i < vecs; i += 32) {
-      float x[VE];
-      unpack16<T>(__ldcg(reinterpret_cast<const uint4*>(rows + (long long)(i / hv) * a.ld) + i % hv), x);
+    auto put = [&](int i, const uint4& y) {
+      float v[VE];
+      unpack16<T>(y, v);
       uint32_t c[VE / 4];
 #pragma unroll
-      for (int k = 0; k < VE; ++k) x[k] = no_inf(x[k]) * inv;
+      for (int k = 0; k < VE; ++k) v[k] = no_inf(v[k]) * inv;
 #pragma unroll
       for (int k = 0; k < VE / 4; ++k)
-        c[k] = to_e4m3x2(x[4 * k], x[4 * k + 1]) | to_e4m3x2(x[4 * k + 2], x[4 * k + 3]) << 16;
-      uint8_t* to = codes + (size_t)r0 * dh + (size_t)i * VE;
+        c[k] = to_e4m3x2(v[4 * k], v[4 * k + 1]) | to_e4m3x2(v[4 * k + 2], v[4 * k + 3]) << 16;
+      uint8_t* to = codes + (size_t)g.r0 * dh + (size_t)i * VE;
       if constexpr (VE == 8)
         *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
       else
         *reinterpret_cast<uint32_t*>(to) = c[0];
-    }
-    if (lane == 0) *scale = s;
+    };
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+      if (i0 + k * WPU * 32 < vecs) put(i0 + k * WPU * 32, x[k]);
+    for (int i = i0 + KEEP * WPU * 32; i < vecs; i += WPU * 32) put(i, vec(i));
+    if (lane == 0 && sub == 0) *scale = s;
   }
 }
 
-// One warp per row and (layer, K or V): 16 codes a lane and step.
+// 4 KB of a page's codes (rows r0 .. r1 - 1 of them) to rows of values, by one warp.
+template <typename T>
+__device__ __forceinline__ void read_piece(const uint4* codes, const float* scale, uint8_t* rows, long long ld, int piece,
+                                           int r0, int r1, int hv, int shift, int vecs) {
+  const int lane = threadIdx.x & 31;
+  uint4 c[KEEP];
+  float s[KEEP];
+  int row[KEEP], col[KEEP];  // of the caller's rows, in 16 values
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = piece * KEEP * 32 + k * 32 + lane, hr = i / hv, r = hr & ((1 << shift) - 1), h = hr >> shift;
+    row[k] = i < vecs && r >= r0 && r < r1 ? r - r0 : -1;
+    col[k] = h * hv + i - hr * hv;
+    if (row[k] >= 0) {
+      c[k] = __ldcg(codes + i);
+      s[k] = __ldcg(&scale[h]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    if (row[k] < 0) continue;
+    const uint32_t cw[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+    uint8_t* to = rows + (long long)row[k] * ld + (size_t)col[k] * 16 * sizeof(T);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 lo = from_e4m3x2(cw[q] & 0xffff), hi = from_e4m3x2(cw[q] >> 16);
+        reinterpret_cast<float4*>(to)[q] = make_float4(lo.x * s[k], lo.y * s[k], hi.x * s[k], hi.y * s[k]);
+      }
+    } else {
+      uint4 y[2];
+      __nv_bfloat162* y2 = reinterpret_cast<__nv_bfloat162*>(y);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 lo = from_e4m3x2(cw[q] & 0xffff), hi = from_e4m3x2(cw[q] >> 16);
+        y2[2 * q] = __floats2bfloat162_rn(lo.x * s[k], lo.y * s[k]);
+        y2[2 * q + 1] = __floats2bfloat162_rn(hi.x * s[k], hi.y * s[k]);
+      }
+      reinterpret_cast<uint4*>(to)[0] = y[0];
+      reinterpret_cast<uint4*>(to)[1] = y[1];
+    }
+  }
+}
+
+// One warp per 4 KB of codes of a page (all heads), layer, K or V.
 template <typename T>
 __global__ void __launch_bounds__(CT) read8_kernel(RowsArgs a) {
+  extern __shared__ int s_off[];
   pdl_trigger();
   pdl_wait();
   const hf_pages& p = a.p;
-  const int lane = threadIdx.x & 31, H = p.n_kv_heads, dh = p.head_dim, hv = dh / 16;
-  if (offsets_fall(a)) return;
-  const long long units = (long long)a.total * a.layers * 2;
-  for (long long u = (long long)blockIdx.x * (CT / 32) + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * (CT / 32)) {
-    const int t = (int)(u / (2 * a.layers)), w = (int)(u % (2 * a.layers)), kv = w & 1, l = w >> 1;
-    const int e = pages_find(a.n, t, [&](int i) { return __ldcg(&a.off[i]); });
-    const int o0 = __ldcg(&a.off[e]), o1 = __ldcg(&a.off[e + 1]), r = a.req ? __ldcg(&a.req[e]) : e;
-    if (t < o0 || t >= o1) continue;  // nobody's row
-    bool ok = o0 >= 0 && o1 <= a.total && r >= 0 && r < p.n_requests;
-    int id = -1, at = 0;
-    if (ok) {
-      const int len = __ldcg(&p.lens[r]), f = __ldcg(&a.first[e]);
-      ok = f >= 0 && len >= 0 && f <= len && o1 - o0 <= len - f && pages_of(len, p.page) <= p.table_ld;
-      if (ok) {
-        at = f + t - o0;
-        id = __ldcg(&p.table[(size_t)r * p.table_ld + at / p.page]);
-        ok = id >= 0 && id < p.n_pages;
-      }
-    }
-    if (!ok) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = p.n_kv_heads, dh = p.head_dim, hv = dh / 16;
+  if (load_entries(a, s_off)) return;
+  const Entries E{a, s_off};
+  const int shift = 31 - __clz(p.page), vecs = (H * hv) << shift, pieces = (vecs + KEEP * 32 - 1) / (KEEP * 32);
+  const int per = a.layers * 2 * pieces;
+  const long long units = ((long long)a.total / p.page + 2 * a.n) * per;
+  for (long long u = (long long)blockIdx.x * (CT / 32) + warp; u < units; u += (long long)gridDim.x * (CT / 32)) {
+    const int slot = (int)(u / per);
+    int w = (int)(u % per);
+    const int piece = w % pieces;
+    w /= pieces;
+    const int kv = w & 1, l = w >> 1;
+    PageOf g{};
+    const bool on = page_of<false>(E, slot, nullptr, lane == 0, g);
+    __syncwarp();
+    if (!on) continue;
+    const size_t block = ((size_t)(a.layer + l) * p.n_pages + g.id) * H;
+    const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v : p.k) + (block * dh << shift));
+    const float* scale = (kv ? a.sc.v : a.sc.k) + block;
+    uint8_t* rows = (kv ? a.v : a.k) + (long long)l * a.layer_stride + (long long)g.src * a.ld;
+    read_piece<T>(codes, scale, rows, a.ld, piece, g.r0, g.r1, hv, shift, vecs);
+  }
+}
+
+// The first tokens of entry 0 as rows of values, for products that many rows share (its pages that are out of
+// range are reported, their rows left as they are).
+__global__ void __launch_bounds__(CT) prefix8_kernel(RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const hf_pages& p = a.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = p.n_kv_heads, dh = p.head_dim, hv = dh / 16;
+  const int shift = 31 - __clz(p.page), vecs = (H * hv) << shift, pieces = (vecs + KEEP * 32 - 1) / (KEEP * 32);
+  const int r = a.req ? __ldcg(a.req) : 0;
+  if (r < 0 || r >= p.n_requests) return;  // (an entry that breaks a rule is reported by the attention)
+  const int len = __ldcg(&p.lens[r]);
+  if (len < a.total || pages_of(len, p.page) > p.table_ld) return;
+  const int units = a.total / p.page * 2 * pieces;
+  for (int u = blockIdx.x * (CT / 32) + warp; u < units; u += gridDim.x * (CT / 32)) {
+    const int piece = u % pieces, kv = u / pieces & 1, j = u / pieces / 2;
+    const int id = __ldcg(&p.table[(size_t)r * p.table_ld + j]);
+    if (id < 0 || id >= p.n_pages) {
       if (lane == 0) pages_flag(p, HF_S_BAD);
       continue;
     }
-    const size_t block = ((size_t)(a.layer + l) * p.n_pages + id) * H;
-    const uint8_t* codes = static_cast<const uint8_t*>(kv ? p.v : p.k) + (block * p.page + at % p.page) * dh;
-    const float* scale = (kv ? a.sc.v : a.sc.k) + block;
-    uint8_t* row = (kv ? a.v : a.k) + (long long)l * a.layer_stride + (long long)t * a.ld;
-    for (int i = lane; i < H * hv; i += 32) {
-      const int h = i / hv;
-      const uint4 c = __ldcg(reinterpret_cast<const uint4*>(codes + (size_t)h * p.page * dh) + i % hv);
-      const float s = __ldcg(&scale[h]);
-      const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-      uint4* to = reinterpret_cast<uint4*>(row + (size_t)i * 16 * sizeof(T));
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = from_e4m3x2(cw[k] & 0xffff), hi = from_e4m3x2(cw[k] >> 16);
-          reinterpret_cast<float4*>(to)[k] = make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
-        }
-      } else {
-        uint4 y[2];
-        __nv_bfloat162* y2 = reinterpret_cast<__nv_bfloat162*>(y);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = from_e4m3x2(cw[k] & 0xffff), hi = from_e4m3x2(cw[k] >> 16);
-          y2[2 * k] = __floats2bfloat162_rn(lo.x * s, lo.y * s);
-          y2[2 * k + 1] = __floats2bfloat162_rn(hi.x * s, hi.y * s);
-        }
-        to[0] = y[0];
-        to[1] = y[1];
-      }
-    }
+    const size_t block = ((size_t)a.layer * p.n_pages + id) * H;
+    const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v : p.k) + (block * dh << shift));
+    read_piece<__nv_bfloat16>(codes, (kv ? a.sc.v : a.sc.k) + block, (kv ? a.v : a.k) + (long long)j * p.page * a.ld, a.ld, piece, 0,
+                              p.page, hv, shift, vecs);
   }
 }
 
@@ -280,9 +391,41 @@ const char* rows_args(const hf_pages8* p, int32_t layer, int32_t layers, const v
   return nullptr;
 }
 
-dim3 grid_of(long long warps) { return dim3((unsigned)std::min<long long>((warps + CT / 32 - 1) / (CT / 32), 152 * 8)); }
+cudaError_t launch_rows(void (*kern)(RowsArgs), const RowsArgs& a, long long warps, cudaStream_t st) {
+  const long long grid = std::min<long long>((warps + CT / 32 - 1) / (CT / 32), 152 * 8);
+  const size_t smem = a.n <= kListed ? ((size_t)a.n + 1) * sizeof(int) : 0;
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(CT), smem, st, a);
+}
+long long slots_of(const RowsArgs& a) { return ((long long)a.total / a.p.page + 2LL * a.n) * a.layers * 2; }
+
+template <typename T>
+cudaError_t launch_write(const RowsArgs& a, cudaStream_t st) {
+  const long long units = slots_of(a) * a.p.n_kv_heads;
+  const int kb = a.p.page * a.p.head_dim * (int)sizeof(T) / 1024;
+  if (kb <= 4) return launch_rows(write8_kernel<T, 1>, a, units, st);
+  if (kb <= 8) return launch_rows(write8_kernel<T, 2>, a, units * 2, st);
+  if (kb <= 16) return launch_rows(write8_kernel<T, 4>, a, units * 4, st);
+  return launch_rows(write8_kernel<T, 8>, a, units * 8, st);
+}
 
 }  // namespace
+
+cudaError_t launch_prefix_values(const hf_pages& p, PageScales sc, int layer, const int32_t* req, int shared, void* k,
+                                 void* v, cudaStream_t st) {
+  RowsArgs a{};
+  a.p = p;
+  a.sc = sc;
+  a.k = static_cast<uint8_t*>(k);
+  a.v = static_cast<uint8_t*>(v);
+  a.ld = 2LL * p.n_kv_heads * p.head_dim;
+  a.req = req;
+  a.total = shared;
+  a.layer = layer;
+  const long long warps = (long long)shared / p.page * 2 * ((p.n_kv_heads * p.page * p.head_dim / 16 + KEEP * 32 - 1) / (KEEP * 32));
+  return launch_pdl(prefix8_kernel, dim3((unsigned)std::min<long long>((warps + CT / 32 - 1) / (CT / 32), 152 * 8)), dim3(CT),
+                    0, st, a);
+}
+
 }  // namespace hf
 
 extern "C" size_t hf_pages8_work_ints(const hf_pages8* p) {
@@ -321,9 +464,8 @@ extern "C" hf_status hf_pages8_write(const hf_pages8* p, int32_t layer, int32_t 
   if (const char* m = rows_args(p, layer, layers, k, v, ld, layer_stride, requests, nullptr, false, offsets, n, total, a, &run))
     return refuse(m);
   if (!run) return HF_OK;
-  const dim3 grid = grid_of((total / a.p.page + 2LL * n) * layers * 2 * a.p.n_kv_heads);
-  auto* kern = p->rows == HF_F32 ? write8_kernel<float> : write8_kernel<__nv_bfloat16>;
-  return done(launch_pdl(kern, grid, dim3(CT), 0, (cudaStream_t)stream, a));
+  return done(p->rows == HF_F32 ? launch_write<float>(a, (cudaStream_t)stream)
+                               : launch_write<__nv_bfloat16>(a, (cudaStream_t)stream));
 }
 
 extern "C" hf_status hf_pages8_read(const hf_pages8* p, int32_t layer, int32_t layers, void* k, void* v, int64_t ld,
@@ -335,6 +477,7 @@ extern "C" hf_status hf_pages8_read(const hf_pages8* p, int32_t layer, int32_t l
   if (const char* m = rows_args(p, layer, layers, k, v, ld, layer_stride, requests, first, true, offsets, n, total, a, &run))
     return refuse(m);
   if (!run) return HF_OK;
-  auto* kern = p->rows == HF_F32 ? read8_kernel<float> : read8_kernel<__nv_bfloat16>;
-  return done(launch_pdl(kern, grid_of((long long)total * layers * 2), dim3(CT), 0, (cudaStream_t)stream, a));
+  const int pieces = (a.p.n_kv_heads * a.p.page * a.p.head_dim / 16 + KEEP * 32 - 1) / (KEEP * 32);
+  return done(launch_rows(p->rows == HF_F32 ? read8_kernel<float> : read8_kernel<__nv_bfloat16>, a, slots_of(a) * pieces,
+                          (cudaStream_t)stream));
 }
