@@ -20,7 +20,11 @@
 //
 // The CTA's warps, items, the line of own tiles and the parts are those of attn_tc.cu: warp 0 loads
 // (TMA; the scales by 4-byte copies beside V's pages), warp 1 issues the products, warp 2 hands out
-// items, warps 4-7 and 8-11 are the softmax groups of two row tiles of up to 64 rows.
+// items, warps 4-7 and 8-11 are the softmax groups of two row tiles of up to 64 rows. While an item is worked
+// on, warp 3 turns the next one's rows into codes, if a row tile has 16 at most (one warp took longer than
+// an item for more: 64 x 8 rows over 4096 tokens 136 us), or fetches them, if 32; else the groups do it when they
+// come to it. Row tiles of two KV heads read pages that lie side by
+// side: one copy brings both, eight rows of one, eight of the other (4 KB for a page of 16 tokens).
 #include <mutex>
 
 #include "attn_tc.cuh"
@@ -36,23 +40,36 @@ constexpr float kFine = 16.f;  // lo is held times this
 constexpr int kItems = 160;  // bytes of two items: what comes behind them starts on 16 bytes
 static_assert(2 * sizeof(Item) <= kItems, "item slots");
 
-template <int DH>
+// NM: sixteens of rows of the largest row tile.
+template <int DH, int NM>
 struct Tc8 {
-  static constexpr int TILE = BN * DH;                // bytes of a K or V tile, and of a row tile's codes
-  static constexpr int SLOTS = DH == 128 ? 9 : 16;    // ring of K and V tiles
-  static constexpr int W = BN * 2 * NR;               // bytes of a tile's weights
-  static constexpr int BARS = 2 * SLOTS + 14;         // (an even number: 16 bytes for what comes behind)
-  static constexpr size_t smem() {
-    return (size_t)(2 + SLOTS) * TILE + 2 * W + BARS * 8 + kItems + 16 + SLOTS * 32 * 4 + 2 * NR * 4 * 8 + (2 * kSmall + 2) * 4;
+  static constexpr int TILE = BN * DH;                // bytes of a K or V tile
+  static constexpr int Q = 2 * NM * 16 * DH;          // bytes of a row tile's codes
+  static constexpr bool AHEAD = NM == 1;              // warp 3 makes the codes, of two items at a time
+  static constexpr int QN = AHEAD ? 2 : 1;
+  static constexpr int RAW = NM == 2 ? 2 * 32 * DH * 2 : 0;  // rows as warp 3 fetches them
+  static constexpr int W = BN * 2 * NM * 16;          // bytes of a tile's weights
+  static constexpr size_t small(int slots) {          // what comes behind the tiles
+    return (size_t)(2 * slots + 16) * 8 + kItems + 16 + slots * 32 * 4 + 4 * NR * 16 + 2 * NR * 16 + (2 * kSmall + 2) * 4;
   }
+  static constexpr size_t with(int slots) { return (size_t)slots * TILE + 2 * QN * Q + RAW + 2 * W + small(slots); }
+  // ring of K and V tiles; an even number: the two tiles of a copy lie side by side
+  static constexpr int most() {
+    int n = 16;
+    while (with(n) > 232448) n -= 2;
+    return n;
+  }
+  static constexpr int SLOTS = most();
+  static constexpr size_t smem() { return with(SLOTS); }
 };
-static_assert(Tc8<128>::BARS % 2 == 0 && Tc8<64>::BARS % 2 == 0 && kItems % 16 == 0, "16-byte reads behind the barriers");
-static_assert(Tc8<128>::smem() <= 232448 && Tc8<64>::smem() <= 232448, "shared memory of a CTA");
 
 // High words of the operands' descriptors. K and the rows along their bytes, V across its keys: rows of DH
 // bytes, swizzled by 128 or 64 bytes, groups of 8 rows one after the other.
 template <int DH>
 constexpr uint32_t kHi = ((uint32_t)(8 * DH) >> 4) | (1u << 14) | ((DH == 128 ? 2u : 4u) << 29);
+// The same with the groups of two heads in turn.
+template <int DH>
+constexpr uint32_t kHiPair = ((uint32_t)(16 * DH) >> 4) | (1u << 14) | ((DH == 128 ? 2u : 4u) << 29);
 // Weights, across their keys, not swizzled: pieces of 16 rows x 8 keys (128 bytes), the next 8 keys
 // 128 bytes further (low word), the next 16 rows 2048.
 constexpr uint32_t kHiW = (2048u >> 4) | (1u << 14);
@@ -145,6 +162,14 @@ __device__ __forceinline__ void split_codes(float x, float y, uint32_t& hi, uint
   lo = r;
 }
 
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %3, %2, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // What a softmax group has in shared memory for its row tile's rows.
 struct GroupRows {
   float4 cm[NR / 2];  // two rows' factors of the scores (base 2), and their -M
@@ -155,11 +180,9 @@ __device__ __forceinline__ float& row_factor(GroupRows& R, int n) { return reint
 __device__ __forceinline__ float& row_minus_m(GroupRows& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + 2 + (n & 1)]; }
 static_assert(sizeof(GroupRows) == NR * 16, "size in Tc8::smem");
 
-template <int DH>
 struct Group {
   const TcArgs& c;
   Item& it;
-  uint8_t* sQ;      // this group's rows
   uint8_t* sKV;
   uint8_t* sW;
   uint64_t* full;
@@ -167,7 +190,7 @@ struct Group {
   GroupRows* rows;
   float* red;       // [4][NR]
   uint32_t b_s, b_o;
-  uint64_t *q_full, *p_full;
+  uint64_t* p_full;
   uint32_t ts, to;
   int r, quad, lane;
   const int* s_eff;
@@ -200,48 +223,56 @@ __device__ __noinline__ float odd_sum8(const AttnRows& a, const Item& it, int g,
   return 0.f;
 }
 
-// An item's softmax by one group, its rows in NC sixteens. tiles: key tiles of this group so far;
-// ring: tiles of the ring so far. False: a wait ran out (the same answer in all of the group's threads).
-template <int DH, int NC>
-__device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int ring) {
-  using L = Tc8<DH>;
-  constexpr int NS = L::SLOTS, N = NC * 16;
-  const AttnRows& a = G.c.a;
-  Item& it = G.it;
-  const int r = G.r, lane = G.lane, row = G.quad * 32 + lane;
-  const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1, g = it.g + (split ? r : 0);
-  const int tl0 = split ? 0 : r * G.c.tb;  // first token within the item
-  GroupRows& R = *G.rows;
-  bool fail = false;
-  // n / G of n < 64, G <= 64
-  const uint32_t by_g = (65535u + a.G) / a.G;
-  auto token_of = [&](int n) { return (int)(n * by_g >> 16); };
+// n / G of n < 64, G <= 64
+struct ByGroup {
+  uint32_t by;
+  __device__ __forceinline__ explicit ByGroup(int G) : by((65535u + G) / G) {}
+  __device__ __forceinline__ int operator()(int n) const { return (int)(n * by >> 16); }
+};
 
-  // ---- the rows as codes, their factors and limits
-  constexpr int PER = DH / 8;  // threads of a row, 8 values each
-  {
-    uint4 x[N * PER / 128];
-#pragma unroll
-    for (int i = 0; i < N * PER / 128; ++i) {
-      const int n = (i * 128 + row) / PER, part = row % PER, t = token_of(n), tl = tl0 + t;
-      const bool on = n < G.c.tb * a.G && tl < it.ntok && g < a.Hkv;
-      x[i] = on ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl) * a.q_ld +
-                                                  (size_t)(g * a.G + n - t * a.G) * DH + part * 8)
-                : make_uint4(0, 0, 0, 0);
+// Tokens of row tile r of an item, from its first one on.
+__device__ __forceinline__ int tile_tokens(const TcArgs& c, const Item& it, int r) {
+  if (it.split) return it.g + r < c.a.Hkv ? it.ntok : 0;
+  return max(0, min(c.tb, it.ntok - r * c.tb));
+}
+
+// The rows of row tile r of an item as codes, their factors and limits, by T threads. N: rows of a row tile; rows
+// without a token have no codes, and a factor of zero. raw: the rows in shared memory, or NULL: where they lie.
+template <int DH, int N, int T>
+__device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r, uint8_t* to, const uint8_t* raw,
+                                          GroupRows& R, const int* s_eff, int tid) {
+  const AttnRows& a = c.a;
+  const ByGroup token_of(a.G);
+  constexpr int PER = DH / 8, WIDE = T / PER, BATCH = N / WIDE < 4 ? N / WIDE : 4;  // threads of a row, 8 values each; rows at a time
+  const int part = tid % PER;
+  const int heads = tile_tokens(c, it, r) * a.G, tl0 = it.split ? 0 : r * c.tb, g = it.g + (it.split ? r : 0);
+  for (int n = tid; n < N; n += T) {
+    int limit = kNone;  // (rows without a token, entries without tokens: all, and dropped)
+    if (n < heads) {
+      const int t = it.t0 + tl0 + token_of(n);
+      const int len = it.kind == 1 ? (c.small ? s_eff[t / a.rows] : __ldcg(&a.eff[t / a.rows])) : it.len;
+      if (len > 0) limit = max(0, len - a.rows + (it.kind == 1 ? t % a.rows : t) + 1);
     }
-    if (row < N) {
-      const int tl = tl0 + token_of(row);
-      int limit = kNone;  // (rows without a token, entries without tokens: all, and dropped)
-      if (row < G.c.tb * a.G && tl < it.ntok) {
-        const int t = it.t0 + tl;
-        const int len = it.kind == 1 ? (G.c.small ? G.s_eff[t / a.rows] : __ldcg(&a.eff[t / a.rows])) : it.len;
-        if (len > 0) limit = max(0, len - a.rows + (it.kind == 1 ? t % a.rows : t) + 1);
-      }
-      R.lim[row] = limit;
+    R.lim[n] = limit;
+    row_minus_m(R, n) = 0.f;
+    if (n >= heads) row_factor(R, n) = 0.f;
+  }
+#pragma unroll 1
+  for (int first = 0; first < heads; first += WIDE * BATCH) {
+    const int n0 = first + tid / PER;
+    uint4 x[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int n = n0 + i * WIDE, t = token_of(n);
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (n < heads)
+        x[i] = raw ? *reinterpret_cast<const uint4*>(raw + (n * PER + part) * 16)
+                   : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl0 + t) * a.q_ld +
+                                                     (size_t)(g * a.G + n - t * a.G) * DH + part * 8);
     }
 #pragma unroll
-    for (int i = 0; i < N * PER / 128; ++i) {
-      const int n = (i * 128 + row) / PER, part = row % PER;
+    for (int i = 0; i < BATCH; ++i) {
+      const int n = n0 + i * WIDE;
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       float v[8], top = 0.f;
 #pragma unroll
@@ -253,6 +284,7 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
       for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
 #pragma unroll
       for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (n >= heads) continue;
       // as scale_for, for every bf16 value
       const int bits = __float_as_int(top);
       const int e = min(max((bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000), -110), 119);
@@ -263,30 +295,58 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
       // 16-byte pieces of a row change places by the row's number, as the copies of K do it
       auto at = [&](int q) {
         const int piece = (part >> 1) ^ (DH == 128 ? q & 7 : (q >> 1) & 3);
-        return reinterpret_cast<uint2*>(G.sQ + q * DH + piece * 16 + (part & 1) * 8);
+        return reinterpret_cast<uint2*>(to + q * DH + piece * 16 + (part & 1) * 8);
       };
       *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      if (part == 0) {
-        row_factor(R, n) = a.qscale * pow2f(e);
-        row_minus_m(R, n) = 0.f;
-      }
+      if (part == 0) row_factor(R, n) = a.qscale * pow2f(e);
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (group_any(r, false)) return false;
-    if (mine > 0 && lane == 0) mbar_arrive(G.q_full);
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
 
-  const int streams = split && it.nt[1] > 0 ? 2 : 1, look = it.first_cut(), most = max(it.nt[0], it.nt[1]);
+// The rows of an item to shared memory, by one warp.
+template <int DH>
+__device__ __forceinline__ void fetch_rows(const TcArgs& c, const Item& it, uint8_t* raw) {
+  const AttnRows& a = c.a;
+  const ByGroup token_of(a.G);
+  constexpr int PER = DH / 8;
+  for (int r = 0; r < 2; ++r) {
+    const int heads = tile_tokens(c, it, r) * a.G, tl0 = it.split ? 0 : r * c.tb, g = it.g + (it.split ? r : 0);
+    for (int i = threadIdx.x & 31; i < heads * PER; i += 32) {
+      const int n = i / PER, t = token_of(n);
+      const void* src = static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl0 + t) * a.q_ld +
+                        (size_t)(g * a.G + n - t * a.G) * DH + i % PER * 8;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + (r * 32 * PER + i) * 16)), "l"(src) : "memory");
+    }
+  }
+}
+
+// An item's softmax by one group, its rows in NC sixteens. tiles: key tiles of this group so far;
+// ring: tiles of the ring so far; fail: a wait has run out in this warp. False: a wait ran out (the same answer in all of the group's threads).
+template <int DH, int NC, int NS>
+__device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, bool fail) {
+  constexpr int N = NC * 16, TILE = BN * DH;
+  const AttnRows& a = G.c.a;
+  Item& it = G.it;
+  const int r = G.r, lane = G.lane, row = G.quad * 32 + lane;
+  const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1, g = it.g + (split ? r : 0);
+  const int tl0 = split ? 0 : r * G.c.tb;  // first token within the item
+  GroupRows& R = *G.rows;
+  const ByGroup token_of(a.G);
+
+  const int streams = split && it.nt[1] > 0 ? 2 : 1, look = it.first_cut();
   const int shift = 31 - __clz(a.page);
   uint64_t l2[N / 2];  // sums of two rows each
 #pragma unroll
   for (int n = 0; n < N / 2; ++n) l2[n] = 0;
   for (int j = 0; j < mine; ++j) {
     const int jt = j0 + j * BN, key = jt + row;
-    const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j + (j + 1 < most ? 2 * r : r)), vs = vi % NS;
-    fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)(vi / NS) & 1u);
-    const float ks = held_scale(G.sc[vs * 32 + (row >> shift)]), vscale = held_scale(G.sc[vs * 32 + 16 + (row >> shift)]);
+    const int vs = (ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j)) % NS, turn = (ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j)) / NS;
+    fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)turn & 1u);
+    const float* sc = G.sc + (vs + (streams == 1 ? 0 : r)) * 32 + (row >> shift);
+    const float ks = held_scale(sc[0]), vscale = held_scale(sc[16]);
     const float lv = (float)((__float_as_int(vscale) >> 23) - 127), rv = 1.f / vscale;
     const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), rv2 = pair(rv, rv), fine2 = pair(1.f / kFine, 1.f / kFine);
     fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
@@ -398,12 +458,14 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
     }
     if (j >= look) {
       // some row masks keys that the tile holds: NaN codes of V there are set aside
-      uint4* v = reinterpret_cast<uint4*>(G.sKV + (size_t)vs * L::TILE);
+      uint8_t* v = G.sKV + (size_t)vs * TILE;
       const int k0 = max(0, min(it.low, j1) - jt), k1 = min(BN, it.hold - jt);
       const bool both = streams == 1 && j < it.nt[0] && j < it.nt[1];
       const int step = both ? 256 : 128;
       for (int q = k0 * (DH / 16) + (both ? r * 128 + row : row); q < k1 * (DH / 16); q += step) {
-        uint4 x = v[q];
+        // (groups of eight rows; of two heads in turn)
+        uint4* at = reinterpret_cast<uint4*>(v) + (streams == 1 ? q : q + (q / (DH / 2) + r) * (DH / 2));
+        uint4 x = *at;
         uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
         uint32_t hit[4];
 #pragma unroll
@@ -412,7 +474,7 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
 #pragma unroll
           for (int k = 0; k < 4; ++k) xw[k] &= ~((hit[k] >> 7) * 0xffu);
           atomicMin(&it.odd[streams == 1 ? 0 : r], jt);
-          v[q] = x;
+          *at = x;
         }
       }
     }
@@ -439,7 +501,7 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
   }
   if (group_any(r, fail)) return false;
   const bool direct = it.direct;
-  const int heads = g < a.Hkv ? min(G.c.tb, it.ntok - tl0) * a.G : 0;  // rows with a token
+  const int heads = tile_tokens(G.c, it, r) * a.G;  // rows with a token
   PartAt at{};
   if (heads > 0) at = it.kind == 1 ? part_prefix(a, it.part, g, it.t0 + tl0, 0) : part_own_unit(a, it.part, g, it.t0 + tl0, 0);
   if (row < N) {
@@ -505,31 +567,36 @@ __device__ __forceinline__ bool soft_item(const Group<DH>& G, int tiles, int rin
 // kernel: a softmax loop for every number of rows in one kernel spills its registers.
 template <int DH, int NO, int NP>
 __global__ void __launch_bounds__(TCT, 1)
-tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ TcArgs c) {
-  using L = Tc8<DH>;
+tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+           const __grid_constant__ CUtensorMap mk2, const __grid_constant__ CUtensorMap mv2, const __grid_constant__ TcArgs c) {
+  constexpr int NM = NO > NP ? NO : NP;
+  using L = Tc8<DH, NM>;
   constexpr int NS = L::SLOTS;
   const AttnRows& a = c.a;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * L::TILE;
-  uint8_t* sW = sKV + (size_t)NS * L::TILE;
+  uint8_t* sQ = smem;                                        // [QN][2]
+  uint8_t* sRaw = smem + 2 * L::QN * L::Q;                   // [2]
+  uint8_t* sKV = sRaw + L::RAW;
+  uint8_t* sW = sKV + (size_t)NS * L::TILE;                  // [2]
   uint64_t* full = reinterpret_cast<uint64_t*>(sW + 2 * L::W);
   uint64_t* empty = full + NS;
-  uint64_t* q_full = empty + NS;   // [2] rows as codes
-  uint64_t* s_full = q_full + 2;   // [2]
-  uint64_t* p_full = q_full + 4;   // [2]
-  uint64_t* o_full = q_full + 6;   // [2]
-  uint64_t* i_full = q_full + 8;   // [2] items
-  uint64_t* i_empty = q_full + 10; // [2]
-  uint64_t* drained = q_full + 12; // after a wait that ran out: the products have ended
-  Item* items = reinterpret_cast<Item*>(full + L::BARS);  // [2]
+  uint64_t* r_full = empty + NS;   // [2] an item's rows as codes
+  uint64_t* s_full = r_full + 2;   // [2]
+  uint64_t* p_full = r_full + 4;   // [2]
+  uint64_t* o_full = r_full + 6;   // [2]
+  uint64_t* i_full = r_full + 8;   // [2] items
+  uint64_t* i_empty = r_full + 10; // [2]
+  uint64_t* drained = r_full + 12; // after a wait that ran out: the products have ended
+  uint64_t* f_full = r_full + 13;  // rows fetched
+  uint64_t* f_empty = r_full + 14;
+  Item* items = reinterpret_cast<Item*>(r_full + 16);        // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(items) + kItems);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;  // tiles that the loader has asked for
-  float* s_sc = reinterpret_cast<float*>(tmem_slot + 4);       // [NS][2][16]
-  GroupRows* s_rows = reinterpret_cast<GroupRows*>(s_sc + NS * 32);  // [2]
-  float* s_red = reinterpret_cast<float*>(s_rows + 2);         // [2][4][NR]
-  int* s_eff = reinterpret_cast<int*>(s_red + 2 * 4 * NR);     // small calls: [kSmall] lengths, [kSmall + 1] places
+  float* s_sc = reinterpret_cast<float*>(tmem_slot + 4);     // [NS][2][16]
+  GroupRows* s_rows = reinterpret_cast<GroupRows*>(s_sc + NS * 32);  // [2 items][2]
+  float* s_red = reinterpret_cast<float*>(s_rows + 4);       // [2][4][NR]
+  int* s_eff = reinterpret_cast<int*>(s_red + 2 * 4 * NR);   // small calls: [kSmall] lengths, [kSmall + 1] places
   int* s_tile0 = s_eff + kSmall;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -540,21 +607,23 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       mbar_init(&empty[s], 1);
     }
     mbar_init(drained, 1);
+    mbar_init(f_full, 32);
+    mbar_init(f_empty, 8);
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&q_full[g], 4);
+      mbar_init(&r_full[g], L::AHEAD ? 1 : 8);  // warp 3, or eight softmax warps
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
       mbar_init(&o_full[g], 1);
       mbar_init(&i_full[g], 1);
-      mbar_init(&i_empty[g], 10);  // the loader, the products, eight softmax warps
+      mbar_init(&i_empty[g], 11);  // the loader, the products, the rows, eight softmax warps
     }
     *abort_flag = 0;
     *issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (tid >= 64 && tid < 66) {  // (the first copies would wait for them)
-    const CUtensorMap* map = tid == 64 ? &mk : &mv;
+  if (tid >= 64 && tid < 68) {  // (the first copies would wait for them)
+    const CUtensorMap* map = tid == 64 ? &mk : tid == 65 ? &mv : tid == 66 ? &mk2 : &mv2;
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
@@ -569,54 +638,77 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
-      // ---- loads: a stream's K(0), then V(j), K(j+1) through the ring
-      int ri = 0;  // tiles so far
+      // ---- loads: K(0), then V(j), K(j+1) through the ring; of two heads a place and the next one at a time
+      int ri = 0;  // places so far
       bool ok = true;
       const int nbox = BN / a.page, shift = 31 - __clz(a.page);
       for (int n = 0; ok; ++n) {
         const Item& it = items[n & 1];
         ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
         if (!ok || it.kind < 0) break;
-        const int nt0 = it.nt[0], nt1 = it.nt[1], nt = max(nt0, nt1), j1 = it.j1, split = it.split, g = it.g;
+        const int nt = max(it.nt[0], it.nt[1]), j1 = it.j1, g = it.g;
+        const bool two = it.split && it.nt[1] > 0;
         const int32_t* tab = attn_table(a, it.entry);
-        // this lane's page of tile j, looked up a tile ahead: once for K and V of both streams
+        // this lane's page of tile j, looked up a tile ahead, once for K and V
         auto page_at = [&](int j) {
           const int key = it.j0 + j * BN + lane * a.page;
           return j < nt && lane < nbox && key < j1 ? tab[key >> shift] : -2;
         };
         int now = page_at(0), then = page_at(1);
-        auto tile = [&](int id, int r, bool is_v) {  // of stream r
-          if (!ok) return;
+        auto place = [&]() {  // the next place of the ring, free
           const int s = ri % NS;
-          if (ri >= NS) ok = wait_uniform(smem_u32(&empty[s]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
-          if (!ok || *abort_flag) {
-            ok = false;
-            return;
+          if (ri >= NS) ok = ok && wait_uniform(smem_u32(&empty[s]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
+          ok = ok && !*abort_flag;
+          return s;
+        };
+        auto tile = [&](int id, bool is_v) {
+          const int s = place();
+          if (!ok) return;
+          if (two) {
+            ++ri;
+            place();
+            --ri;
+            if (!ok) return;
           }
-          if (lane == 0) mbar_expect_tx(&full[s], L::TILE);
+          if (lane == 0) {
+            mbar_expect_tx(&full[s], two ? 2 * L::TILE : L::TILE);
+            if (two) mbar_arrive(&full[s + 1]);
+          }
           __syncwarp();
           if (lane < nbox) {
             const bool on = id >= 0 && id < a.n_pages;
-            const int z = on ? id * a.Hkv + g + r : a.n_pages * a.Hkv;  // behind the pool: reads zeros
+            const int z = on ? id : a.n_pages;  // behind the pool: reads zeros
             if (!on && id != -2 && a.status) atomicOr(a.status, HF_S_BAD);
-            tma_load_3d(sKV + (size_t)s * L::TILE + lane * a.page * DH, is_v ? &mv : &mk, &full[s], 0, 0, z);
-            if (is_v) {  // both scales: V's slot stays until the weights are there
-              copy4(s_sc + s * 32 + lane, a.k_scale + (on ? z : 0), on);
-              copy4(s_sc + s * 32 + 16 + lane, a.v_scale + (on ? z : 0), on);
+            uint8_t* dst = sKV + (size_t)s * L::TILE + lane * a.page * (two ? 2 * DH : DH);
+            tma_load_page(dst, two ? (is_v ? &mv2 : &mk2) : is_v ? &mv : &mk, &full[s], g, z);
+            if (is_v) {  // all scales: V's places stay until the weights are there
+              const size_t at = on ? (size_t)id * a.Hkv + g : 0;
+              copy4(s_sc + s * 32 + lane, a.k_scale + at, on);
+              copy4(s_sc + s * 32 + 16 + lane, a.v_scale + at, on);
+              if (two) {
+                copy4(s_sc + (s + 1) * 32 + lane, a.k_scale + at + on, on);
+                copy4(s_sc + (s + 1) * 32 + 16 + lane, a.v_scale + at + on, on);
+              }
             }
           }
           copies_arrive(&full[s]);
-          ++ri;
+          if (two) copies_arrive(&full[s + 1]);
+          ri += two ? 2 : 1;
         };
         if (nt > 0) {
-          const int streams = split && nt1 > 0 ? 2 : 1;
-          for (int r = 0; r < streams; ++r) tile(now, r, false);
+          if (two && (ri & 1)) {  // two places lie side by side from an even one on: this one stays empty
+            const int s = place();
+            if (ok) {
+              if (lane == 0) mbar_arrive(&full[s]);
+              copies_arrive(&full[s]);
+              ++ri;
+            }
+          }
+          tile(now, false);
           for (int j = 0; j < nt && ok; ++j) {
             const int next = page_at(j + 2);
-            for (int r = 0; r < streams; ++r) {
-              tile(now, r, true);
-              if (j + 1 < nt) tile(then, r, false);
-            }
+            tile(now, true);
+            if (ok && j + 1 < nt) tile(then, false);
             now = then;
             then = next;
           }
@@ -634,96 +726,81 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       const uint32_t dq = desc_keys(smem_u32(sQ)), dk = desc_keys(smem_u32(sKV)), dv = desc_values(smem_u32(sKV)),
                      dw = desc_weights(smem_u32(sW));
       const uint32_t b_full = smem_u32(full), b_empty = smem_u32(empty), b_s = smem_u32(s_full), b_p = smem_u32(p_full),
-                     b_o = smem_u32(o_full), b_q = smem_u32(q_full);
-      int at = 0;           // next slot of the ring, and the parity of its fill
-      uint32_t ph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+                     b_o = smem_u32(o_full);
+      int ri = 0;  // places so far
+      uint32_t pph[2] = {0, 0};
       bool ok = true;
-      uint32_t id_s = 0, id_o = 0;
-      auto next = [&]() {  // waits for the next slot of the ring
-        const int s = at;
-        ok = ok && wait_uniform(b_full + 8 * s, ph);
-        if (++at == NS) {
-          at = 0;
-          ph ^= 1u;
-        }
-        return s;
-      };
-      auto score = [&](int r, int slot) {
-#pragma unroll
-        for (int k = 0; k < DH / 32; ++k)
-          mma8(lead, tm + r * 128, dk + slot * (L::TILE >> 4) + 2 * k, kHi<DH>, dq + r * (L::TILE >> 4) + 2 * k, kHi<DH>,
-               id_s, k > 0);
-        mma_commit(lead, b_s + 8 * r);
-      };
       for (int n = 0; ok; ++n) {
         const Item& it = items[n & 1];
         ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
         if (!ok || __shfl_sync(0xffffffffu, it.kind, 0) < 0) break;
         const int nt0 = __shfl_sync(0xffffffffu, it.nt[0], 0), nt1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
-        const bool two = __shfl_sync(0xffffffffu, it.split, 0) && nt1 > 0;  // two streams of keys
+        const bool two = __shfl_sync(0xffffffffu, it.split, 0) && nt1 > 0;  // keys of two heads
         const int nt = max(nt0, nt1);
         const int cols = 32 * (NP > 0 && __shfl_sync(0xffffffffu, it.kind, 0) == 1 ? NP : NO);
-        id_s = idesc_e4m3(cols, 0);
-        id_o = idesc_e4m3(cols, 3u << 15);
+        const uint32_t id_s = idesc_e4m3(cols, 0), id_o = idesc_e4m3(cols, 3u << 15);
+        const uint32_t hi = two ? kHiPair<DH> : kHi<DH>, pair_r = two ? 8 * DH >> 4 : 0, groups = two ? 2 : 1;
+        const uint32_t q = dq + (n % L::QN) * (2 * L::Q >> 4);
+        auto next = [&]() {  // waits for the next tile
+          const int s = ri % NS;
+          ok = ok && wait_uniform(b_full + 8 * s, (uint32_t)(ri / NS) & 1u);
+          if (two) ok = ok && wait_uniform(b_full + 8 * (s + 1), (uint32_t)(ri / NS) & 1u);
+          ri += two ? 2 : 1;
+          return s;
+        };
+        auto done = [&](int s) {  // its places are free once the products so far have ended
+          mma_commit(lead, b_empty + 8 * s);
+          if (two) mma_commit(lead, b_empty + 8 * (s + 1));
+        };
+        auto score = [&](int r, int slot) {
+#pragma unroll
+          for (int k = 0; k < DH / 32; ++k)
+            mma8(lead, tm + r * 128, dk + slot * (L::TILE >> 4) + r * pair_r + 2 * k, hi, q + r * (L::Q >> 4) + 2 * k, kHi<DH>,
+                 id_s, k > 0);
+          mma_commit(lead, b_s + 8 * r);
+        };
         if (nt > 0) {
-          int ks = next();
-          int ks1 = two ? next() : ks;
-          if (nt0 > 0) {
-            ok = ok && wait_uniform(b_q, qph[0]);
-            qph[0] ^= 1u;
+          if (two && (ri & 1)) {
+            const int s = ri % NS;
+            ok = ok && wait_uniform(b_full + 8 * s, (uint32_t)(ri / NS) & 1u);
+            if (ok) mma_commit(lead, b_empty + 8 * s);
+            ++ri;
           }
+          int ks = next(), vs = 0;
+          ok = ok && wait_uniform(smem_u32(&r_full[n & 1]), (uint32_t)(n >> 1) & 1u);
           if (ok) {
             tc_fence_after();
             score(0, ks);
-            if (two) mma_commit(lead, b_empty + 8 * ks);
+            if (nt1 > 0) score(1, ks);
+            done(ks);
           }
-          if (nt1 > 0) {
-            ok = ok && wait_uniform(b_q + 8, qph[1]);
-            qph[1] ^= 1u;
-            if (ok) {
-              tc_fence_after();
-              score(1, ks1);
-            }
-          }
-          if (ok) mma_commit(lead, b_empty + 8 * ks1);
-          int vs = 0;
           // from tile `look` on the softmax groups look V over before they hand their weights
           // on; where both have the tile, each looks at half of it
           const int look = __shfl_sync(0xffffffffu, it.first_cut(), 0);
           for (int j = 0; j < nt && ok; ++j) {
             const bool more = j + 1 < nt;
-            if (!two) {
-              vs = next();
-              if (more) ks = next();
-            }
+            vs = next();
+            if (more) ks = next();
             const bool both = !two && j >= look && j < nt0 && j < nt1;
             if (both) ok = ok && wait_uniform(b_p, pph[0]) && wait_uniform(b_p + 8, pph[1]);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const int mine = r ? nt1 : nt0;
               if (!ok || j >= mine) continue;
-              if (two) vs = next();
-              if (!both) ok = ok && wait_uniform(b_p + 8 * r, pph[r]);
+              if (!both) ok = wait_uniform(b_p + 8 * r, pph[r]);
               pph[r] ^= 1u;
               if (!ok) continue;
               tc_fence_after();
 #pragma unroll
               for (int k = 0; k < BN / 32; ++k)
-                mma8(lead, tm + 256 + r * 128, dv + vs * (L::TILE >> 4) + k * (32 * DH >> 4), kHi<DH>,
+                mma8(lead, tm + 256 + r * 128, dv + vs * (L::TILE >> 4) + r * pair_r + k * groups * (32 * DH >> 4), hi,
                      dw + r * (L::W >> 4) + k * (512 >> 4), kHiW, id_o, j > 0 || k > 0);
               mma_commit(lead, b_o + 8 * r);
-              if (two) mma_commit(lead, b_empty + 8 * vs);
-              if (j + 1 < mine) {
-                if (two) ks = next();
-                if (!ok) continue;
-                tc_fence_after();
-                score(r, ks);
-                if (two) mma_commit(lead, b_empty + 8 * ks);
-              }
+              if (j + 1 < mine) score(r, ks);
             }
-            if (ok && !two) {
-              mma_commit(lead, b_empty + 8 * vs);
-              if (more) mma_commit(lead, b_empty + 8 * ks);
+            if (ok) {
+              done(vs);
+              if (more) done(ks);
             }
           }
         }
@@ -757,7 +834,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         tile0 = s_tile0;
         __syncwarp();
       }
-      for (int idx = me; ok && idx < c.pre_items; idx += all) {
+      for (int idx = me; NP > 0 && ok && idx < c.pre_items; idx += all) {
         make_prefix(c, idx, it, eff);
         put(it);
       }
@@ -781,8 +858,30 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       it.kind = -1;
       if (ok) put(it);
       if (!ok) *abort_flag = 1;
-    } else if (c.small) {
-      check_prefixes(a, 1 + blockIdx.x, gridDim.x, lane, 32);
+    } else {
+      // ---- rows
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const Item& it = items[n & 1];
+        // (a place of items is free once all have done with what it held, and so are its codes)
+        ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+        if (!ok || it.kind < 0) break;
+        if constexpr (L::AHEAD) {
+          for (int r = 0; r < 2; ++r)
+            make_rows<DH, 16, 32>(c, it, r, sQ + ((n & 1) * 2 + r) * L::Q, nullptr, s_rows[2 * (n & 1) + r], s_eff, lane);
+          if (lane == 0) mbar_arrive(&r_full[n & 1]);
+        } else if constexpr (L::RAW > 0) {
+          if (n > 0) ok = wait_uniform(smem_u32(f_empty), (uint32_t)(n - 1) & 1u);
+          if (!ok) break;
+          fetch_rows<DH>(c, it, sRaw);
+          copies_arrive(f_full);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[n & 1]);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok) *abort_flag = 1;
+      if (c.small) check_prefixes(a, 1 + blockIdx.x, gridDim.x, lane, 32);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -795,18 +894,36 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       // (the group's warps go on together: a wait that ran out in one ends it in all)
       ok = !group_any(r, !wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u));
       if (!ok || it.kind < 0) break;
-      const Group<DH> G{c,    it,           sQ + r * L::TILE, sKV,
-                        sW + r * L::W,      full,             s_sc, s_rows + r, s_red + r * 4 * NR,
-                        smem_u32(&s_full[r]), smem_u32(&o_full[r]), &q_full[r], &p_full[r],
-                        tmem + lanes + r * 128, tmem + lanes + 256 + r * 128, r, quad, lane, s_eff};
-      const int streams = it.split && it.nt[1] > 0 ? 2 : 1;
+      const bool two = it.split && it.nt[1] > 0;
+      const int nt = max(it.nt[0], it.nt[1]);
+      if (two) ring += ring & 1;
+      const Group G{c, it, sKV, sW + r * L::W, full, s_sc, s_rows + 2 * (n & 1) + r, s_red + r * 4 * NR,
+                    smem_u32(&s_full[r]), smem_u32(&o_full[r]), &p_full[r],
+                    tmem + lanes + r * 128, tmem + lanes + 256 + r * 128, r, quad, lane, s_eff};
+      bool fail = false;
+      if constexpr (L::AHEAD) {
+        fail = !wait_uniform(smem_u32(&r_full[n & 1]), (uint32_t)(n >> 1) & 1u);
+      } else {
+        // (the codes of the item before have been read: its last scores came to this group)
+        const uint8_t* raw = L::RAW ? sRaw + r * (L::RAW / 2) : nullptr;
+        if (L::RAW) fail = !wait_uniform(smem_u32(f_full), (uint32_t)n & 1u);
+        GroupRows& R = s_rows[2 * (n & 1) + r];
+        if (NP > 0 && it.kind == 1)
+          make_rows<DH, NP == 0 ? 16 : NP * 16, 128>(c, it, r, sQ + r * L::Q, raw, R, s_eff, tid & 127);
+        else
+          make_rows<DH, NO * 16, 128>(c, it, r, sQ + r * L::Q, raw, R, s_eff, tid & 127);
+        if (L::RAW && lane == 0) mbar_arrive(f_empty);
+        if (lane == 0) mbar_arrive(&r_full[n & 1]);
+        ok = !group_any(r, fail);  // the factors and limits are there
+        if (!ok) break;
+      }
       if (NP > 0 && it.kind == 1)
-        ok = soft_item<DH, NP == 0 ? 1 : NP>(G, tiles, ring);
+        ok = soft_item<DH, NP == 0 ? 1 : NP, NS>(G, tiles, ring, fail);
       else
-        ok = soft_item<DH, NO>(G, tiles, ring);
+        ok = soft_item<DH, NO, NS>(G, tiles, ring, fail);
       if (!ok) break;
       tiles += it.nt[r];
-      ring += 2 * max(it.nt[0], it.nt[1]) * streams;
+      ring += 2 * nt * (two ? 2 : 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_empty[n & 1]);
     }
@@ -839,7 +956,8 @@ std::mutex g_mu;
 bool g_set[kMaxDev][2][4][2] = {};
 
 template <int DH, int NO, int NP>
-cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mk, const CUtensorMap& mv, dim3 grid, cudaStream_t st) {
+cudaError_t launch_one(const TcArgs& c, const CUtensorMap* m, dim3 grid, cudaStream_t st) {
+  using L = Tc8<DH, (NO > NP ? NO : NP)>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -847,21 +965,21 @@ cudaError_t launch_one(const TcArgs& c, const CUtensorMap& mk, const CUtensorMap
     std::lock_guard<std::mutex> lock(g_mu);
     bool& set = g_set[dev & (kMaxDev - 1)][DH == 128][NO - 1][NP > 0];
     if (!set || dev >= kMaxDev) {
-      e = cudaFuncSetAttribute(tc8_kernel<DH, NO, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc8<DH>::smem());
+      e = cudaFuncSetAttribute(tc8_kernel<DH, NO, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem());
       if (e != cudaSuccess) return e;
       set = true;
     }
   }
-  return launch_pdl(tc8_kernel<DH, NO, NP>, grid, dim3(TCT), Tc8<DH>::smem(), st, mk, mv, c);
+  return launch_pdl(tc8_kernel<DH, NO, NP>, grid, dim3(TCT), L::smem(), st, m[0], m[1], m[2], m[3], c);
 }
 
 template <int DH, int NP>
-cudaError_t launch_rows(const TcArgs& c, const CUtensorMap& mk, const CUtensorMap& mv, dim3 grid, cudaStream_t st) {
+cudaError_t launch_rows(const TcArgs& c, const CUtensorMap* m, dim3 grid, cudaStream_t st) {
   switch ((std::min(c.a.rows, c.tb) * c.a.G + 15) / 16) {
-    case 1: return launch_one<DH, 1, NP>(c, mk, mv, grid, st);
-    case 2: return launch_one<DH, 2, NP>(c, mk, mv, grid, st);
-    case 3: return launch_one<DH, 3, NP>(c, mk, mv, grid, st);
-    default: return launch_one<DH, 4, NP>(c, mk, mv, grid, st);
+    case 1: return launch_one<DH, 1, NP>(c, m, grid, st);
+    case 2: return launch_one<DH, 2, NP>(c, m, grid, st);
+    case 3: return launch_one<DH, 3, NP>(c, m, grid, st);
+    default: return launch_one<DH, 4, NP>(c, m, grid, st);
   }
 }
 
@@ -875,9 +993,10 @@ cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t
   c.box_rows = a.page;
   c.wait = !attn_gives_up();
   c.pre_items = pre_items;
-  CUtensorMap mk, mv;
-  cudaError_t e = make_map_pages8(&mk, a.k, a.dh, a.page, (long long)a.n_pages * a.Hkv);
-  if (e == cudaSuccess) e = make_map_pages8(&mv, a.v, a.dh, a.page, (long long)a.n_pages * a.Hkv);
+  CUtensorMap m[4];  // K, V of one head, of two
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+    e = make_map_pages8(&m[i], i & 1 ? a.v : a.k, a.dh, a.page, a.Hkv, a.n_pages, 1 + i / 2);
   if (e != cudaSuccess) return e;
   // (the line is at most as long as all tables reach)
   const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;
@@ -886,8 +1005,8 @@ cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t
   if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
   if (e != cudaSuccess) return e;
   if (pre_items > 0)
-    return a.dh == 128 ? launch_rows<128, 4>(c, mk, mv, dim3(grid), st) : launch_rows<64, 4>(c, mk, mv, dim3(grid), st);
-  return a.dh == 128 ? launch_rows<128, 0>(c, mk, mv, dim3(grid), st) : launch_rows<64, 0>(c, mk, mv, dim3(grid), st);
+    return a.dh == 128 ? launch_rows<128, 4>(c, m, dim3(grid), st) : launch_rows<64, 4>(c, m, dim3(grid), st);
+  return a.dh == 128 ? launch_rows<128, 0>(c, m, dim3(grid), st) : launch_rows<64, 0>(c, m, dim3(grid), st);
 }
 
 }  // namespace hf
