@@ -243,7 +243,7 @@ __device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r
                                           GroupRows& R, const int* s_eff, int tid) {
   const AttnRows& a = c.a;
   const ByGroup token_of(a.G);
-  constexpr int PER = DH / 8, WIDE = T / PER, BATCH = N / WIDE < 4 ? N / WIDE : 4;  // threads of a row, 8 values each; rows at a time
+  constexpr int PER = DH / 8, WIDE = T / PER;  // threads of a row, 8 values each; rows at a time
   const int part = tid % PER;
   const int heads = tile_tokens(c, it, r) * a.G, tl0 = it.split ? 0 : r * c.tb, g = it.g + (it.split ? r : 0);
   for (int n = tid; n < N; n += T) {
@@ -257,23 +257,24 @@ __device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r
     row_minus_m(R, n) = 0.f;
     if (n >= heads) row_factor(R, n) = 0.f;
   }
-#pragma unroll 1
-  for (int first = 0; first < heads; first += WIDE * BATCH) {
-    const int n0 = first + tid / PER;
-    uint4 x[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int n = n0 + i * WIDE, t = token_of(n);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (n < heads)
-        x[i] = raw ? *reinterpret_cast<const uint4*>(raw + (n * PER + part) * 16)
-                   : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl0 + t) * a.q_ld +
-                                                     (size_t)(g * a.G + n - t * a.G) * DH + part * 8);
+  auto values = [&](int n) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (n < heads) {
+      const int t = token_of(n);
+      x = raw ? *reinterpret_cast<const uint4*>(raw + (n * PER + part) * 16)
+              : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (size_t)(it.tok0 + tl0 + t) * a.q_ld +
+                                                (size_t)(g * a.G + n - t * a.G) * DH + part * 8);
     }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int n = n0 + i * WIDE;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    return x;
+  };
+  // (not unrolled: an item's first tile waits for this, and a kernel's first item for its instructions)
+  uint4 x = values(tid / PER);
+#pragma unroll 1
+  for (int first = 0; first < heads; first += WIDE) {
+    const int n = first + tid / PER;
+    const uint4 then = values(n + WIDE);
+    {
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       float v[8], top = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -284,7 +285,6 @@ __device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r
       for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
 #pragma unroll
       for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (n >= heads) continue;
       // as scale_for, for every bf16 value
       const int bits = __float_as_int(top);
       const int e = min(max((bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000), -110), 119);
@@ -297,10 +297,13 @@ __device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r
         const int piece = (part >> 1) ^ (DH == 128 ? q & 7 : (q >> 1) & 3);
         return reinterpret_cast<uint2*>(to + q * DH + piece * 16 + (part & 1) * 8);
       };
-      *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      if (part == 0) row_factor(R, n) = a.qscale * pow2f(e);
+      if (n < heads) {
+        *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if (part == 0) row_factor(R, n) = a.qscale * pow2f(e);
+      }
     }
+    x = then;
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
