@@ -363,21 +363,25 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
       const int hb = NC - h0 < HB ? NC - h0 : HB;
       float z[HB * 16];  // exponents of the weights
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float t[HB * 16];
+#pragma unroll
+      for (int i = 0; i < HB; ++i)
+        if (i < hb) {
+          tmem_ld16_async(G.ts + (h0 + i) * 16, z + i * 16);
+          tmem_ld16_async(G.ts + N + (h0 + i) * 16, t + i * 16);
+        }
+      tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < HB; ++i) {
         if (i >= hb) continue;
         const int h = h0 + i;
-        float t[16];
-        tmem_ld16_async(G.ts + h * 16, z + i * 16);
-        tmem_ld16_async(G.ts + N + h * 16, t);
-        tmem_wait_ld();
         tmem_hold16(z + i * 16);
-        tmem_hold16(t);
+        tmem_hold16(t + i * 16);
 #pragma unroll
         for (int n = 0; n < 16; n += 2) {
           const int m = i * 16 + n;
           const float4 cm = R.cm[h * 8 + n / 2];
-          const uint64_t s2 = fma2(pair(t[n], t[n + 1]), fine2, pair(z[m], z[m + 1]));
+          const uint64_t s2 = fma2(pair(t[m], t[m + 1]), fine2, pair(z[m], z[m + 1]));
           const float2 e = unpair(fma2(s2, mul2(pair(cm.x, cm.y), ks2), add2(pair(cm.z, cm.w), lv2)));
           z[m] = e.x;
           z[m + 1] = e.y;
