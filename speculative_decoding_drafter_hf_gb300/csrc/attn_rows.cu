@@ -744,15 +744,19 @@ struct PagesPlan {
   int pre_items;                        // tensor cores: items of the prefix
   size_t eff, tile0, ml, o, k, v, total; // offsets in the workspace (the line is at 0)
 };
-// More rows of a KV head than two row tiles of codes share the prefix's keys: it is turned into bf16 rows once (a
-// power of two as the scale: exactly) and taken by the kernel for those, 256 rows at a time. MEASURED
-constexpr int kDenseRows = 2 * kTileRows8;
+// Where very many rows share a long prefix, it is turned into bf16 rows once (a power of two as the scale:
+// exactly) and taken by the kernel for those, 256 rows at a time, instead of as codes, 64 or 128 at a time.
+// Whole calls, us, as rows / as codes, 8 KV heads: 192 rows of a head over 8192 tokens 59 / 50, 384 71 / 71,
+// 512 72 / 82, 2048 160 / 235; 768 over 2048 tokens 54 / 53, 1024 60 / 60.
+constexpr int kDenseRows = 384;
+constexpr long long kDenseWork = 1 << 21;  // rows of a head x tokens
 PagesPlan plan_call(AttnRows& a, int dtype) {
   PagesPlan w{};
   w.tc = attn_tc_ok(dtype, a.dh);
   const size_t N = (size_t)a.n * a.rows * a.Hq;
   size_t rows;
-  w.dense = w.tc && a.tile == kTileRows8 && a.shared > 0 && (long long)a.n * a.rows * a.G > kDenseRows;
+  const long long shared_rows = (long long)a.n * a.rows * a.G;
+  w.dense = w.tc && a.tile == kTileRows8 && shared_rows > kDenseRows && shared_rows * a.shared > kDenseWork;
   if (w.tc) {
     long long slots;
     int pre = 0;
