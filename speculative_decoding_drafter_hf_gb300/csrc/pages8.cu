@@ -39,6 +39,7 @@ struct RowsArgs {
   const int32_t* first;  // read
   const int32_t* off;
   int n, total, layer, layers;
+  int slots;  // places for the pages of all entries
 };
 
 // 16 bytes of a row as values.
@@ -59,18 +60,44 @@ __device__ __forceinline__ void unpack16(const uint4& w, float* x) {
   }
 }
 
-// Values of a lane that stay in registers between the two looks at them: 4 KB a warp.
-constexpr int KEEP = 8;
+// i / d of 0 <= i < 2^24, 1 <= d <= 256.
+struct Over {
+  uint32_t by;
+  __device__ __forceinline__ explicit Over(int d) : by((uint32_t)((0x100000000ULL + d - 1) / d)) {}
+  __device__ __forceinline__ int operator()(int i) const { return by ? (int)__umulhi((uint32_t)i, by) : i; }
+};
+
+// Magnitudes as bits: their order is that of unsigned integers, and what is not finite comes behind.
+template <typename T>
+struct Bits;
+template <>
+struct Bits<float> {
+  static constexpr uint32_t kOdd = 0x7f800000u;  // the first that is not finite
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+  static __device__ __forceinline__ uint32_t one(uint32_t m) { return m; }
+};
+template <>
+struct Bits<__nv_bfloat16> {  // two in a word
+  static constexpr uint32_t kOdd = 0x7f800000u;
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+  static __device__ __forceinline__ uint32_t one(uint32_t m) { return max(m & 0xffff0000u, m << 16); }
+};
+
+// Pieces of 16 bytes that a lane has at a time. Writing keeps them in registers between the two looks at them
+// (10656 rows of 10 heads of 128, pages of 64: 24.2 us, with four 32.9); reading back 20.6 us with four, 24.6
+// with eight.
+constexpr int KEEP = 8, READ = 4;
 constexpr int kListed = kMaxRequests;  // entries whose bounds a CTA keeps in shared memory
 
 // The list of a call as a CTA has it: bounds in shared memory (few entries) or where they lie.
 struct Entries {
   const RowsArgs& a;
   int* s_off;
+  int shift;  // of the page
   __device__ __forceinline__ int off(int i) const { return a.n <= kListed ? s_off[i] : __ldcg(&a.off[i]); }
   // An entry of c rows reaches at most c / page + 2 pages: it owns the slots [off / page + 2 e, ..) of all, so
   // that no prefix sum is needed.
-  __device__ __forceinline__ int first_slot(int e) const { return min(max(off(e), 0), a.total) / a.p.page + 2 * e; }
+  __device__ __forceinline__ int first_slot(int e) const { return (min(max(off(e), 0), a.total) >> shift) + 2 * e; }
 };
 
 // Loads the bounds; true where they decrease (names rows twice, or entries that no search finds). Bounds out of
@@ -122,8 +149,8 @@ __device__ __forceinline__ bool page_of(const Entries& E, int slot, const uint32
     ok = first >= 0 && first <= len && c <= len - first && pages_of(len, p.page) <= p.table_ld;
   }
   if (ok) {
-    const int page = first / p.page + slot - E.first_slot(e);
-    const long long base = (long long)page * p.page, end = (long long)first + c;
+    const int page = (first >> E.shift) + slot - E.first_slot(e);
+    const long long base = (long long)page << E.shift, end = (long long)first + c;
     if (base >= end) return false;
     g.r0 = (int)max(0LL, first - base);
     g.r1 = (int)min((long long)p.page, end - base);
@@ -139,24 +166,23 @@ __device__ __forceinline__ bool page_of(const Entries& E, int slot, const uint32
 // registers between the maximum and the codes (page of 64 x 128 bf16: four; what is more, 128 rows of
 // 256 fp32 values, is read twice).
 template <typename T, int WPU>
-__global__ void __launch_bounds__(CT) write8_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(CT, 4) write8_kernel(RowsArgs a) {
   constexpr int VE = 16 / sizeof(T), UNITS = CT / 32 / WPU;
   extern __shared__ int s_off[];
   __shared__ uint32_t s_seen[kMaxRequests / 32], s_twice[kMaxRequests / 32];
-  __shared__ float s_top[CT / 32];
+  __shared__ uint32_t s_top[CT / 32];
   pdl_trigger();
   pdl_wait();
   const hf_pages& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPU, H = p.n_kv_heads, dh = p.head_dim, hv = dh / VE;
   if (load_entries(a, s_off)) return;
   if (a.req) load_twice(a, s_seen, s_twice);
-  const Entries E{a, s_off};
-  const int per = a.layers * 2 * H;
-  const long long units = ((long long)a.total / p.page + 2 * a.n) * per;
-  for (long long u0 = (long long)blockIdx.x * UNITS; u0 < units; u0 += (long long)gridDim.x * UNITS) {
-    const long long u = u0 + warp / WPU;
-    const int slot = (int)(u / per);
-    int w = (int)(u % per);
+  const Entries E{a, s_off, 31 - __clz(p.page)};
+  const Over over_hv(hv);
+  const int per = a.layers * 2 * H, units = a.slots * per;
+  for (int u0 = blockIdx.x * UNITS; u0 < units; u0 += gridDim.x * UNITS) {
+    const int u = u0 + warp / WPU, slot = u / per;
+    int w = u - slot * per;
     const int h = w % H;
     w /= H;
     const int kv = w & 1, l = w >> 1;
@@ -166,15 +192,17 @@ __global__ void __launch_bounds__(CT) write8_kernel(RowsArgs a) {
     uint8_t* codes = nullptr;
     float* scale = nullptr;
     uint4 x[KEEP];
-    float top = 0.f, old = 0.f;
+    float old = 0.f;
+    uint32_t m[2] = {0, 0};  // the largest magnitude
     auto look = [&](const uint4& y) {
-      float v[VE];
-      unpack16<T>(y, v);
-#pragma unroll
-      for (int k = 0; k < VE; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+      m[0] = Bits<T>::most(Bits<T>::most(m[0], y.x), y.y);
+      m[1] = Bits<T>::most(Bits<T>::most(m[1], y.z), y.w);
     };
     const int vecs = on ? (g.r1 - g.r0) * hv : 0, i0 = sub * 32 + lane;
-    auto vec = [&](int i) { return __ldcg(reinterpret_cast<const uint4*>(rows + (long long)(i / hv) * a.ld) + i % hv); };
+    auto vec = [&](int i) {
+      const int r = over_hv(i);
+      return __ldcg(reinterpret_cast<const uint4*>(rows + (long long)r * a.ld) + i - r * hv);
+    };
     if (on) {
       rows = (kv ? a.v : a.k) + (long long)l * a.layer_stride + (long long)g.src * a.ld + (long long)h * dh * sizeof(T);
       const size_t block = ((size_t)(a.layer + l) * p.n_pages + g.id) * H + h;
@@ -184,24 +212,47 @@ __global__ void __launch_bounds__(CT) write8_kernel(RowsArgs a) {
 #pragma unroll
       for (int k = 0; k < KEEP; ++k) {
         const int i = i0 + k * WPU * 32;
-        if (i < vecs) x[k] = vec(i);
+        x[k] = i < vecs ? vec(i) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int k = 0; k < KEEP; ++k)
-        if (i0 + k * WPU * 32 < vecs) look(x[k]);
+      for (int k = 0; k < KEEP; ++k) look(x[k]);
       for (int i = i0 + KEEP * WPU * 32; i < vecs; i += WPU * 32) look(vec(i));
     }
     __syncwarp();
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    if constexpr (WPU > 1) {
-      if (lane == 0) s_top[warp] = top;
-      __syncthreads();
+    // the largest of the unit's warps
+    auto join = [&](uint32_t t) {
+      t = __reduce_max_sync(0xffffffffu, t);
+      if constexpr (WPU > 1) {
+        if (lane == 0) s_top[warp] = t;
+        __syncthreads();
 #pragma unroll
-      for (int k = 0; k < WPU; ++k) top = fmaxf(top, s_top[warp - sub + k]);
-      __syncthreads();  // (read before the next unit's)
+        for (int k = 0; k < WPU; ++k) t = max(t, s_top[warp - sub + k]);
+        __syncthreads();  // (read before the next unit's)
+      }
+      return t;
+    };
+    uint32_t top = join(Bits<T>::one(Bits<T>::most(m[0], m[1])));
+    const bool odd = top >= Bits<T>::kOdd;  // infinities or NaN among the values: they do not count
+    bool any = odd;
+    if constexpr (WPU > 1) any = __syncthreads_or(odd);
+    if (any) {
+      float t = 0.f;
+      auto careful = [&](const uint4& y) {
+        float v[VE];
+        unpack16<T>(y, v);
+#pragma unroll
+        for (int k = 0; k < VE; ++k) t = fmaxf(t, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+      };
+      if (on) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k) careful(x[k]);
+        for (int i = i0 + KEEP * WPU * 32; i < vecs; i += WPU * 32) careful(vec(i));
+      }
+      __syncwarp();
+      top = join(__float_as_uint(t));
     }
     if (!on) continue;
-    const float s = fmaxf(scale_for(top), old);
+    const float s = fmaxf(scale_for(__uint_as_float(top)), old);
     if (s > old && old > 0.f) {  // the rows that stay, again
       const float f = old / s;
       for (int i = i0; i < g.r0 * dh / 16; i += WPU * 32) {
@@ -221,7 +272,7 @@ __global__ void __launch_bounds__(CT) write8_kernel(RowsArgs a) {
       unpack16<T>(y, v);
       uint32_t c[VE / 4];
 #pragma unroll
-      for (int k = 0; k < VE; ++k) v[k] = no_inf(v[k]) * inv;
+      for (int k = 0; k < VE; ++k) v[k] = (odd ? no_inf(v[k]) : v[k]) * inv;
 #pragma unroll
       for (int k = 0; k < VE / 4; ++k)
         c[k] = to_e4m3x2(v[4 * k], v[4 * k + 1]) | to_e4m3x2(v[4 * k + 2], v[4 * k + 3]) << 16;
@@ -239,34 +290,33 @@ __global__ void __launch_bounds__(CT) write8_kernel(RowsArgs a) {
   }
 }
 
-// 4 KB of a page's codes (rows r0 .. r1 - 1 of them) to rows of values, by one warp.
+// 2 KB of a page's codes (rows r0 .. r1 - 1 of them) to rows of values, by one warp.
 template <typename T>
 __device__ __forceinline__ void read_piece(const uint4* codes, const float* scale, uint8_t* rows, long long ld, int piece,
-                                           int r0, int r1, int hv, int shift, int vecs) {
+                                           int r0, int r1, int hv, Over over_hv, int shift, int vecs) {
   const int lane = threadIdx.x & 31;
-  uint4 c[KEEP];
-  float s[KEEP];
-  int row[KEEP], col[KEEP];  // of the caller's rows, in 16 values
+  uint4 c[READ];
+  float s[READ];
+  uint8_t* to[READ];  // NULL: not asked for
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) {
-    const int i = piece * KEEP * 32 + k * 32 + lane, hr = i / hv, r = hr & ((1 << shift) - 1), h = hr >> shift;
-    row[k] = i < vecs && r >= r0 && r < r1 ? r - r0 : -1;
-    col[k] = h * hv + i - hr * hv;
-    if (row[k] >= 0) {
+  for (int k = 0; k < READ; ++k) {
+    const int i = piece * READ * 32 + k * 32 + lane, hr = over_hv(i), r = hr & ((1 << shift) - 1), h = hr >> shift;
+    to[k] = i < vecs && r >= r0 && r < r1 ? rows + (long long)(r - r0) * ld + (size_t)(h * hv + i - hr * hv) * 16 * sizeof(T)
+                                          : nullptr;
+    if (to[k]) {
       c[k] = __ldcg(codes + i);
       s[k] = __ldcg(&scale[h]);
     }
   }
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) {
-    if (row[k] < 0) continue;
+  for (int k = 0; k < READ; ++k) {
+    if (!to[k]) continue;
     const uint32_t cw[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-    uint8_t* to = rows + (long long)row[k] * ld + (size_t)col[k] * 16 * sizeof(T);
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 lo = from_e4m3x2(cw[q] & 0xffff), hi = from_e4m3x2(cw[q] >> 16);
-        reinterpret_cast<float4*>(to)[q] = make_float4(lo.x * s[k], lo.y * s[k], hi.x * s[k], hi.y * s[k]);
+        reinterpret_cast<float4*>(to[k])[q] = make_float4(lo.x * s[k], lo.y * s[k], hi.x * s[k], hi.y * s[k]);
       }
     } else {
       uint4 y[2];
@@ -277,13 +327,13 @@ __device__ __forceinline__ void read_piece(const uint4* codes, const float* scal
         y2[2 * q] = __floats2bfloat162_rn(lo.x * s[k], lo.y * s[k]);
         y2[2 * q + 1] = __floats2bfloat162_rn(hi.x * s[k], hi.y * s[k]);
       }
-      reinterpret_cast<uint4*>(to)[0] = y[0];
-      reinterpret_cast<uint4*>(to)[1] = y[1];
+      reinterpret_cast<uint4*>(to[k])[0] = y[0];
+      reinterpret_cast<uint4*>(to[k])[1] = y[1];
     }
   }
 }
 
-// One warp per 4 KB of codes of a page (all heads), layer, K or V.
+// One warp per 2 KB of codes of a page (all heads), layer, K or V.
 template <typename T>
 __global__ void __launch_bounds__(CT) read8_kernel(RowsArgs a) {
   extern __shared__ int s_off[];
@@ -292,13 +342,13 @@ __global__ void __launch_bounds__(CT) read8_kernel(RowsArgs a) {
   const hf_pages& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = p.n_kv_heads, dh = p.head_dim, hv = dh / 16;
   if (load_entries(a, s_off)) return;
-  const Entries E{a, s_off};
-  const int shift = 31 - __clz(p.page), vecs = (H * hv) << shift, pieces = (vecs + KEEP * 32 - 1) / (KEEP * 32);
-  const int per = a.layers * 2 * pieces;
-  const long long units = ((long long)a.total / p.page + 2 * a.n) * per;
-  for (long long u = (long long)blockIdx.x * (CT / 32) + warp; u < units; u += (long long)gridDim.x * (CT / 32)) {
-    const int slot = (int)(u / per);
-    int w = (int)(u % per);
+  const int shift = 31 - __clz(p.page), vecs = (H * hv) << shift, pieces = (vecs + READ * 32 - 1) / (READ * 32);
+  const Entries E{a, s_off, shift};
+  const Over over_hv(hv);
+  const int per = a.layers * 2 * pieces, units = a.slots * per;
+  for (int u = blockIdx.x * (CT / 32) + warp; u < units; u += gridDim.x * (CT / 32)) {
+    const int slot = u / per;
+    int w = u - slot * per;
     const int piece = w % pieces;
     w /= pieces;
     const int kv = w & 1, l = w >> 1;
@@ -310,7 +360,7 @@ __global__ void __launch_bounds__(CT) read8_kernel(RowsArgs a) {
     const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v : p.k) + (block * dh << shift));
     const float* scale = (kv ? a.sc.v : a.sc.k) + block;
     uint8_t* rows = (kv ? a.v : a.k) + (long long)l * a.layer_stride + (long long)g.src * a.ld;
-    read_piece<T>(codes, scale, rows, a.ld, piece, g.r0, g.r1, hv, shift, vecs);
+    read_piece<T>(codes, scale, rows, a.ld, piece, g.r0, g.r1, hv, over_hv, shift, vecs);
   }
 }
 
@@ -321,7 +371,7 @@ __global__ void __launch_bounds__(CT) prefix8_kernel(RowsArgs a) {
   pdl_wait();
   const hf_pages& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = p.n_kv_heads, dh = p.head_dim, hv = dh / 16;
-  const int shift = 31 - __clz(p.page), vecs = (H * hv) << shift, pieces = (vecs + KEEP * 32 - 1) / (KEEP * 32);
+  const int shift = 31 - __clz(p.page), vecs = (H * hv) << shift, pieces = (vecs + READ * 32 - 1) / (READ * 32);
   const int r = a.req ? __ldcg(a.req) : 0;
   if (r < 0 || r >= p.n_requests) return;  // (an entry that breaks a rule is reported by the attention)
   const int len = __ldcg(&p.lens[r]);
@@ -337,7 +387,7 @@ __global__ void __launch_bounds__(CT) prefix8_kernel(RowsArgs a) {
     const size_t block = ((size_t)a.layer * p.n_pages + id) * H;
     const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v : p.k) + (block * dh << shift));
     read_piece<__nv_bfloat16>(codes, (kv ? a.sc.v : a.sc.k) + block, (kv ? a.v : a.k) + (long long)j * p.page * a.ld, a.ld, piece, 0,
-                              p.page, hv, shift, vecs);
+                              p.page, hv, Over(hv), shift, vecs);
   }
 }
 
@@ -387,6 +437,10 @@ const char* rows_args(const hf_pages8* p, int32_t layer, int32_t layers, const v
   a.total = total;
   a.layer = layer;
   a.layers = layers;
+  const long long slots = (long long)total / c.page + 2LL * n;
+  if (slots * layers * 2 * c.n_kv_heads * ((c.page * c.head_dim + 511) / 512) > 0x3fffffffLL)
+    return "total, n or layers is too large";
+  a.slots = (int)slots;
   *run = true;
   return nullptr;
 }
@@ -396,11 +450,10 @@ cudaError_t launch_rows(void (*kern)(RowsArgs), const RowsArgs& a, long long war
   const size_t smem = a.n <= kListed ? ((size_t)a.n + 1) * sizeof(int) : 0;
   return launch_pdl(kern, dim3((unsigned)grid), dim3(CT), smem, st, a);
 }
-long long slots_of(const RowsArgs& a) { return ((long long)a.total / a.p.page + 2LL * a.n) * a.layers * 2; }
 
 template <typename T>
 cudaError_t launch_write(const RowsArgs& a, cudaStream_t st) {
-  const long long units = slots_of(a) * a.p.n_kv_heads;
+  const long long units = (long long)a.slots * a.layers * 2 * a.p.n_kv_heads;
   const int kb = a.p.page * a.p.head_dim * (int)sizeof(T) / 1024;
   if (kb <= 4) return launch_rows(write8_kernel<T, 1>, a, units, st);
   if (kb <= 8) return launch_rows(write8_kernel<T, 2>, a, units * 2, st);
@@ -421,7 +474,7 @@ cudaError_t launch_prefix_values(const hf_pages& p, PageScales sc, int layer, co
   a.req = req;
   a.total = shared;
   a.layer = layer;
-  const long long warps = (long long)shared / p.page * 2 * ((p.n_kv_heads * p.page * p.head_dim / 16 + KEEP * 32 - 1) / (KEEP * 32));
+  const long long warps = (long long)shared / p.page * 2 * ((p.n_kv_heads * p.page * p.head_dim / 16 + READ * 32 - 1) / (READ * 32));
   return launch_pdl(prefix8_kernel, dim3((unsigned)std::min<long long>((warps + CT / 32 - 1) / (CT / 32), 152 * 8)), dim3(CT),
                     0, st, a);
 }
@@ -477,7 +530,7 @@ extern "C" hf_status hf_pages8_read(const hf_pages8* p, int32_t layer, int32_t l
   if (const char* m = rows_args(p, layer, layers, k, v, ld, layer_stride, requests, first, true, offsets, n, total, a, &run))
     return refuse(m);
   if (!run) return HF_OK;
-  const int pieces = (a.p.n_kv_heads * a.p.page * a.p.head_dim / 16 + KEEP * 32 - 1) / (KEEP * 32);
-  return done(launch_rows(p->rows == HF_F32 ? read8_kernel<float> : read8_kernel<__nv_bfloat16>, a, slots_of(a) * pieces,
+  const int pieces = (a.p.n_kv_heads * a.p.page * a.p.head_dim / 16 + READ * 32 - 1) / (READ * 32);
+  return done(launch_rows(p->rows == HF_F32 ? read8_kernel<float> : read8_kernel<__nv_bfloat16>, a, (long long)a.slots * a.layers * 2 * pieces,
                           (cudaStream_t)stream));
 }
