@@ -130,9 +130,10 @@ cudaError_t launch(RotaryArgs a, bool inter, bool wide, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int ve = wide ? V : 1, H = a.hq + a.hkv;
   a.per = a.dim / 2 / ve + ((a.dh - a.dim) / ve + 1) / 2;
-  // threads enough to fill the GPU, then heads one after the other
+  // threads enough to fill the GPU four times, then heads one after the other (26041 tokens of 40 heads of 128 89.4
+  // us, 5.96 TB/s; threads for once 93.8; four heads at a time 127: more registers, fewer threads)
   const long long cells = (long long)a.rows * a.per;
-  a.step = (int)std::max<long long>(1, std::min<long long>(H, (152LL * 2048 + cells - 1) / cells));
+  a.step = (int)std::max<long long>(1, std::min<long long>(H, (152LL * 8192 + cells - 1) / cells));
   const long long grid = std::min<long long>((cells * a.step + RT - 1) / RT, 1 << 20);
   auto* kern = wide ? (inter ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>)
                     : (inter ? rotary_kernel<T, 1, true> : rotary_kernel<T, 1, false>);
