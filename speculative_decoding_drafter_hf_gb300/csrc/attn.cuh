@@ -74,6 +74,7 @@ struct AttnRows {
   int* line;       // tensor cores: an AttnLine
   int* tile0;      // [n + 1] where each entry starts on the line
   int tile;        // tensor cores: rows of a row tile
+  int item_start;  // places before an entry's tiles
   int tb, units, unit_rows;  // tokens of a row tile; units of an entry's rows
 };
 
@@ -108,11 +109,12 @@ __device__ __forceinline__ int unit_of(const AttnRows& a, int g, int t) {
 // The entries' own key tiles, entry after entry, once per unit, laid out on one line
 // that is cut into a stretch per CTA: the first `light` CTAs get `more` places each, the
 // others `less`. A piece is what a CTA has of one entry and unit. An entry with tiles
-// first has kItemStart empty places: what an item costs beside its tiles (measured, 64 x 8
-// rows: about 2.2 us a tile, 1.7 us an item).
-constexpr int kItemStart = 1;
-__device__ __forceinline__ int entry_places(int keys) {
-  return keys > 0 ? (keys + kKeyTile - 1) / kKeyTile + kItemStart : 0;
+// first has item_start empty places: what an item costs beside its tiles (measured, 64 x 8
+// rows: about 2.2 us a tile, 1.7 us an item; of an 8-bit cache without items of the prefix, whose tiles are
+// shorter, 1.6 and 5: 64 x 8 rows over 8192 and 8 to 4096 tokens, all, 148 us with three places, 158 with one).
+constexpr int kItemStart = 1, kItemStart8 = 3;
+__device__ __forceinline__ int entry_places(const AttnRows& a, int keys) {
+  return keys > 0 ? (keys + kKeyTile - 1) / kKeyTile + a.item_start : 0;
 }
 struct AttnLine {
   int tiles;  // places of all entries (times units: the line's length)

@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) join_kernel(AttnRows a) 
     const AttnLine line = {ln.x, ln.y, ln.z, ln.w};
     const int u = unit_of(a, g, t);
     if (t1 > t0) {
-      first = line.cta(u * line.tiles + t0 + kItemStart);
+      first = line.cta(u * line.tiles + t0 + a.item_start);
       own = line.cta(u * line.tiles + t1 - 1) - first + 1;
     }
     slot = u * a.n + entry;
@@ -758,6 +758,7 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   const long long shared_rows = (long long)a.n * a.rows * a.G;
   w.dense = w.tc && a.tile == kTileRows8 && shared_rows > kDenseRows && shared_rows * a.shared > kDenseWork;
   if (w.tc) {
+    if (a.tile == kTileRows8 && (w.dense || a.shared == 0)) a.item_start = kItemStart8;
     long long slots;
     int pre = 0;
     if (w.dense) {
@@ -810,7 +811,7 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
   if (shared < 0 || shared % p->page || shared > (long long)p->table_ld * p->page)
     return "shared must be a multiple of page, at most table_ld * page";
   if ((long long)n * rows * hq > 0x7fffffffLL / 4 ||
-      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart) * n * ((long long)rows * hq / (c.e4m3 ? kTileRows8 : kTileRows) + p->n_kv_heads) > 0x3fffffffLL)
+      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart8) * n * ((long long)rows * hq / (c.e4m3 ? kTileRows8 : kTileRows) + p->n_kv_heads) > 0x3fffffffLL)
     return "n * rows * n_q_heads, or that times the table's reach, is too large";
   a.Hq = hq;
   a.Hkv = p->n_kv_heads;
@@ -818,6 +819,7 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
   a.dh = p->head_dim;
   a.esize = pages_esize(c.dtype);
   a.tile = c.e4m3 ? kTileRows8 : kTileRows;
+  a.item_start = kItemStart;
   a.table = p->table;
   a.lens = p->lens;
   a.status = p->status;

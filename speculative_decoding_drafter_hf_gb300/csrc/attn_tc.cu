@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnRows a, int ctas, int he
     if (i < a.n) {
       const int len = attn_len(a, i, bad);
       a.eff[i] = len;
-      t = entry_places(len - a.shared);
+      t = entry_places(a, len - a.shared);
     }
     int x = t;
 #pragma unroll
@@ -917,7 +917,7 @@ cudaError_t launch_attn_tc_pages(const AttnRows& a, int pre_items, cudaStream_t 
   }
   if (e != cudaSuccess) return e;
   // (the line is at most as long as all tables reach)
-  const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;
+  const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + a.item_start) * a.n * a.units;
   const int grid = (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
   c.small = a.n <= kSmall;
   if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);

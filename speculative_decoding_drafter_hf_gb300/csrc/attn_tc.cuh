@@ -207,7 +207,7 @@ __device__ __forceinline__ int make_own(const TcArgs& c, const AttnLine& line, i
     else
       hi = mid;
   }
-  const int first = tile0[lo] + kItemStart, last = tile0[lo + 1], skip = max(0, first - at);
+  const int first = tile0[lo] + a.item_start, last = tile0[lo + 1], skip = max(0, first - at);
   const int take = min(end - pos, last - at) - skip, from = at + skip;
   some = take > 0;
   if (!some) return min(end - pos, skip);
@@ -250,7 +250,7 @@ __device__ __forceinline__ int scan_tiles(const AttnRows& a, const int* eff, int
   int carry = 0;
   for (int i0 = 0; i0 < a.n; i0 += 32) {
     const int i = i0 + lane;
-    const int t = i < a.n ? entry_places(eff[i] - a.shared) : 0;
+    const int t = i < a.n ? entry_places(a, eff[i] - a.shared) : 0;
     int x = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -1006,7 +1006,7 @@ cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t
     e = make_map_pages8(&m[i], i & 1 ? a.v : a.k, a.dh, a.page, a.Hkv, a.n_pages, 1 + i / 2);
   if (e != cudaSuccess) return e;
   // (the line is at most as long as all tables reach)
-  const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + kItemStart) * a.n * a.units;
+  const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + a.item_start) * a.n * a.units;
   const int grid = (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
   c.small = a.n <= kSmall;
   if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
