@@ -273,35 +273,33 @@ __device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r
   for (int first = 0; first < heads; first += WIDE) {
     const int n = first + tid / PER;
     const uint4 then = values(n + WIDE);
-    {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      float v[8], top = 0.f;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float v[8], top = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]) < INFINITY ? fabsf(v[k]) : 0.f);
 #pragma unroll
-      for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // as scale_for, for every bf16 value
-      const int bits = __float_as_int(top);
-      const int e = min(max((bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000), -110), 119);
-      const float inv = pow2f(-e);
-      uint32_t hi[4], lo[4];
+    for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // as scale_for, for every bf16 value
+    const int bits = __float_as_int(top);
+    const int e = max((bits >> 23) - 135 + ((bits & 0x7fffff) > 0x600000), -126);
+    const float inv = pow2f(-e);
+    uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split_codes(no_inf(v[2 * k]) * inv, no_inf(v[2 * k + 1]) * inv, hi[k], lo[k]);
-      // 16-byte pieces of a row change places by the row's number, as the copies of K do it
-      auto at = [&](int q) {
-        const int piece = (part >> 1) ^ (DH == 128 ? q & 7 : (q >> 1) & 3);
-        return reinterpret_cast<uint2*>(to + q * DH + piece * 16 + (part & 1) * 8);
-      };
-      if (n < heads) {
-        *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        if (part == 0) row_factor(R, n) = a.qscale * pow2f(e);
-      }
+    for (int k = 0; k < 4; ++k) split_codes(no_inf(v[2 * k]) * inv, no_inf(v[2 * k + 1]) * inv, hi[k], lo[k]);
+    // 16-byte pieces of a row change places by the row's number, as the copies of K do it
+    auto at = [&](int q) {
+      const int piece = (part >> 1) ^ (DH == 128 ? q & 7 : (q >> 1) & 3);
+      return reinterpret_cast<uint2*>(to + q * DH + piece * 16 + (part & 1) * 8);
+    };
+    if (n < heads) {
+      *at(n) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *at(N + n) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      if (part == 0) row_factor(R, n) = a.qscale * pow2f(e);
     }
     x = then;
   }
@@ -346,7 +344,7 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
   for (int n = 0; n < N / 2; ++n) l2[n] = 0;
   for (int j = 0; j < mine; ++j) {
     const int jt = j0 + j * BN, key = jt + row;
-    const int vs = (ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j)) % NS, turn = (ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j)) / NS;
+    const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j), vs = vi % NS, turn = vi / NS;  // V's place
     fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)turn & 1u);
     const float* sc = G.sc + (vs + (streams == 1 ? 0 : r)) * 32 + (row >> shift);
     const float ks = held_scale(sc[0]), vscale = held_scale(sc[16]);
@@ -399,12 +397,12 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
         // the maximum of every row over the 128 keys
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
-        if (i >= hb) continue;
-        const int h = h0 + i;
-          float t[16];
+          if (i >= hb) continue;
+          const int h = h0 + i;
+          float v[16];
 #pragma unroll
-          for (int n = 0; n < 16; ++n) t[n] = z[i * 16 + n];
-          const float m = warp_columns<false>(t, lane);
+          for (int n = 0; n < 16; ++n) v[n] = z[i * 16 + n];
+          const float m = warp_columns<false>(v, lane);
           if (!(lane & 1)) G.red[G.quad * NR + h * 16 + (lane >> 1)] = m;
         }
         if (j > 0) fail = fail || !wait_uniform(G.b_o, (uint32_t)(tiles + j - 1) & 1u);

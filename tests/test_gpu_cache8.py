@@ -46,6 +46,9 @@ ATTEND = [  # dtype, Hq, Hkv, dh, page, rows, shared, own lengths (None: an empt
     ("bf16", 4, 4, 128, 64, 1, 4096, [1] * 9),
     ("bf16", 32, 8, 128, 32, 1, 4096, [1, 700, 33]),
     ("bf16", 24, 8, 64, 8, 1, 0, [3000, 5]),
+    ("bf16", 64, 1, 128, 32, 64, 64, [70, 64]),                  # as many rows as there are: 4096 of a head
+    ("bf16", 6, 3, 128, 16, 9, 48, [200, 9, 8, 0]),              # a last head without a neighbour
+    ("bf16", 21, 3, 64, 8, 7, 16, [100, 1]),                     # row tiles of 49 rows
     ("bf16", 4, 4, 32, 16, 4, 32, [20, 3]),
     ("bf16", 3, 1, 80, 32, 2, 64, [20, 90]),
     ("bf16", 2, 1, 256, 16, 64, 16, [64, 100]),
@@ -203,6 +206,52 @@ def test_attend_nan_codes_stay_with_the_rows_that_see_them(hf, dtype, heads):
     assert np.isnan(want).any() and not c.check()
 
 
+@pytest.mark.parametrize("dh,page,odd_page", [(128, 32, False), (64, 64, False), (128, 16, True)])
+def test_attend_a_long_prefix_of_many_rows(hf, dh, page, odd_page):
+    """The prefix goes through bf16 rows: entries without tokens of their own (their first rows see part of the
+    prefix), an empty one, one that names no request, and NaN codes at the prefix's end."""
+    own = [5, 0, 200, None, 1, 40] + [3] * 10
+    pool, table, lens, refs = _shared_cache(1, dh, page, 2304, own, 21)
+    if odd_page:
+        last = table[0][2304 // page - 1]
+        pool[0].view(torch.uint8)[0, last, 0, page - 2] = 0x7f  # key 2302
+        pool[1].view(torch.uint8)[0, last, 0, page - 3, 5] = 0xff  # one value of token 2301
+    c = _on_gpu(hf, pool, table, lens, refs, "bf16")
+    q = _randn((16, 8, 8, dh), "bf16", 22)
+    want, tol = _want(q, pool, table, lens, "bf16")
+    R.check_attention(R.to64(c.attend(q.cuda(), shared=2304)), want, tol)
+    assert not c.check()
+    if odd_page:
+        assert np.isnan(want).any() and np.isfinite(want[1, 0]).all()
+    o = R.to64(c.attend(q.cuda(), C.ints([0, 1, 2, 3, -7, 5] + list(range(6, 16))), shared=2304))
+    assert (o[4] == 0).all() and c.check() == hf.CallStatus.BAD
+    o[4] = want[4]
+    R.check_attention(o, want, tol)
+    # a page of the prefix out of range is reported; an empty first entry leaves zeros
+    t = [list(r) for r in table]
+    for r in t:
+        if r[0] >= 0:
+            r[3] = len(refs)
+    c = _on_gpu(hf, pool, t, lens, refs, "bf16")
+    c.attend(q.cuda(), shared=2304)
+    assert c.check() == hf.CallStatus.BAD
+    c = _on_gpu(hf, pool, table, [0] + lens[1:], refs, "bf16")
+    assert (c.attend(q.cuda(), shared=2304) == 0).all() and c.check() == hf.CallStatus.BAD
+
+
+def test_attend_a_long_prefix_of_many_entries(hf):
+    """More entries than a CTA plans for by itself, over a prefix that goes through bf16 rows."""
+    own = [3, 17, 90, None, 64, 1]
+    pool, table, lens, refs = _shared_cache(2, 64, 128, 2048, own, 23)
+    c = _on_gpu(hf, pool, table, lens, refs, "bf16")
+    rng = random.Random(6)
+    req = [0] + [rng.randrange(len(own)) for _ in range(299)]
+    q = _randn((300, 2, 4, 64), "bf16", 24)
+    want, tol = _want(q, pool, table, lens, "bf16", req=req)
+    R.check_attention(R.to64(c.attend(q.cuda(), C.ints(req), shared=2048)), want, tol)
+    assert not c.check()
+
+
 def test_attend_scales_far_apart(hf):
     """Pages of scales from 2^-64 to 2^40 side by side, scores that differ by hundreds, and rows of very
     different sizes: the weights keep their bits."""
@@ -267,6 +316,29 @@ def test_attend_waits_that_run_out(hf):
         B.hf_debug_set_wait_limit(None, -1)
     R.check_attention(R.to64(c.attend(q.cuda(), shared=32)), want, tol)
     assert not c.check()
+    # through bf16 rows as well
+    pool, table, lens, refs = _shared_cache(1, 128, 64, 2304, [5] * 16, 25)
+    c = _on_gpu(hf, pool, table, lens, refs, "bf16")
+    q = _randn((16, 8, 8, 128), "bf16", 26)
+    want, tol = _want(q, pool, table, lens, "bf16")
+    try:
+        B.hf_debug_set_wait_limit(None, 0)
+        c.attend(q.cuda(), shared=2304)
+        assert c.check() == hf.CallStatus.TIMEOUT
+    finally:
+        B.hf_debug_set_wait_limit(None, -1)
+    R.check_attention(R.to64(c.attend(q.cuda(), shared=2304)), want, tol)
+    assert not c.check()
+
+
+def test_attend_queries_of_every_size(hf):
+    """Rows from the smallest to the largest bf16 values, with a scale to go with them."""
+    pool, table, lens, refs = _shared_cache(1, 64, 16, 0, [100], 27)
+    for size, scale in ((2.0 ** -133, 1e38), (2.0 ** -120, 1e35), (1e37, 1e-38)):
+        q = (torch.randn((1, 2, 4, 64), generator=torch.Generator().manual_seed(28)) * size * 8).to(torch.bfloat16)
+        c = _on_gpu(hf, pool, table, lens, refs, "bf16")
+        want, tol = _want(q, pool, table, lens, "bf16", scale=scale)
+        R.check_attention(R.to64(c.attend(q.cuda(), scale=scale)), want, tol)
 
 
 # ------------------------------------------------------------------ writing and reading
@@ -430,6 +502,46 @@ def test_values_at_the_ends(hf, dtype):
     c.extend(C.ints([1]))
     c.write(x[0].view(1, 1, 1, dh).cuda(), x[0].view(1, 1, 1, dh).cuda(), C.ints([0, 1]))
     assert int(c.k.view(torch.uint8)[0, 0, 0, 0, 7]) == 0x80
+
+
+def test_reading_at_the_ends_of_the_scales(hf):
+    """Every code at the least, a middle and the largest scale, as fp32 and as bf16 rows."""
+    codes = torch.arange(256, dtype=torch.uint8).view(1, 1, 1, 16, 16)
+    for dtype in (torch.float32, torch.bfloat16):
+        for e in (-64, 0, 7, 8, 63):
+            k = codes.cuda().view(torch.float8_e4m3fn)
+            s = torch.full((1, 1, 1), 2.0 ** e, device="cuda")
+            c = hf.Pages8(k, k.clone(), s, s.clone(), C.ints([[0]]), C.ints([16]), C.ints([1]), dtype=dtype)
+            got, again = c.read(C.ints([0]), C.ints([0, 16]), total=16)
+            _same(got.view(16, 16), R.to64(codes.view(torch.float8_e4m3fn).float().view(16, 16)) * 2.0 ** e, f"2^{e}")
+            assert torch.equal(got.nan_to_num(0.5), again.nan_to_num(0.5)) and not c.check()
+
+
+def test_writes_and_reads_replayed(hf):
+    """A captured round (extend, write, read back) replayed: it reads the lists and rows of its own time."""
+    page, hkv, dh = 8, 2, 64
+    c = hf.Pages8.empty(2, 30, hkv, page, dh, 3, 8)
+    ref = Cache(2, 30, hkv, page, dh, 3, 8)
+    counts, ends = C.ints([3, 3, 3]), C.ints([0, 3, 6, 9])
+    x = torch.zeros((2, 9, hkv, dh), dtype=torch.bfloat16, device="cuda")
+    first, k, v = C.ints([0, 0, 0]), torch.zeros_like(x), torch.zeros_like(x)
+    c.write(x, x, C.ints([0]))  # (nothing; the calls have been made once before the capture)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.extend(counts)
+        c.write(x, x, ends)
+        c.read(first, ends, k=k, v=v)
+    for step in range(6):
+        x.copy_(_randn(x.shape, "bf16", 30 + step, 2.0 ** (step % 3)))
+        first.copy_(C.ints(ref.lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref.extend([0, 1, 2], [3, 3, 3])
+        ref.write8([0, 1, 2], [0, 3, 6, 9], {"k": R.to64(x), "v": R.to64(x)})
+        _check_cache(c, ref)
+        want = np.concatenate([ref.tokens("k", r, 3 * step, 3) for r in range(3)], 1)
+        _same(k, R.to64(torch.tensor(want).to(torch.bfloat16)), "read")
+        assert torch.equal(k, v) and not c.check()
 
 
 def test_bad_entries_of_write_and_read(hf):
