@@ -214,7 +214,8 @@ def ablation_config(cfg) -> dict:
 
 
 # sources of the target model's half of a round: no kernel of the workloads here is built from them
-TARGET_SIDE = ("attn.cuh", "attn_rows.cu", "attn_tc.cu", "pages.cu", "pages.cuh", "verify.cu")
+TARGET_SIDE = ("attn.cuh", "attn_rows.cu", "attn_tc.cu", "attn_tc.cuh", "attn_tc8.cu", "e4m3.cuh", "pages.cu", "pages.cuh",
+               "pages8.cu", "rotary.cu", "verify.cu")
 
 
 def kernel_sources_digest() -> str:

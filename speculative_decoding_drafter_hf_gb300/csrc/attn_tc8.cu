@@ -25,6 +25,8 @@
 // an item for more: 64 x 8 rows over 4096 tokens 136 us), or fetches them, if 32; else the groups do it when they
 // come to it. Row tiles of two KV heads read pages that lie side by
 // side: one copy brings both, eight rows of one, eight of the other (4 KB for a page of 16 tokens).
+#include <cudaTypedefs.h>
+
 #include <mutex>
 
 #include "attn_tc.cuh"
@@ -954,6 +956,31 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Pages of the cache, bytes [n_pages][hkv][page][dh]: a box is one page of `heads` neighbouring KV heads, in shared
+// memory eight rows of the first head, eight of the second, the next eight of the first, .., swizzled by its
+// rows of dh bytes.
+cudaError_t make_map_pages8(CUtensorMap* map, const void* base, int dh, int page, int hkv, long long n_pages, int heads) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  static cudaError_t found = cudaSuccess;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (found == cudaSuccess && (q != cudaDriverEntryPointSuccess || !fn)) found = cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (found != cudaSuccess) return found;
+  const cuuint64_t row = dh, block = row * page;
+  const cuuint64_t dims[5] = {row, 8u, (cuuint64_t)hkv, (cuuint64_t)page / 8, (cuuint64_t)n_pages};
+  const cuuint64_t strides[4] = {row, block, 8 * row, block * hkv};
+  const cuuint32_t box[5] = {(cuuint32_t)dh, 8u, (cuuint32_t)heads, (cuuint32_t)page / 8, 1u}, step[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, dh == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 constexpr int kMaxDev = 64;

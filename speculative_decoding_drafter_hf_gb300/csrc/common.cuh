@@ -536,7 +536,6 @@ cudaError_t make_map(CUtensorMap* map, const void* base, long long rows, long lo
 // 3-D bf16 tensor map over n2 x n1 x n0 (n0 contiguous, the others' strides in
 // elements), box b2 x b1 x 64, 128-byte swizzle; parts of a box outside read zero
 // (gemm_tc.cu).
-cudaError_t make_map_pages8(CUtensorMap* map, const void* base, int dh, int page, int hkv, long long n_pages, int heads);
 cudaError_t make_map_3d(CUtensorMap* map, const void* base, long long n0, long long n1, long long n2,
                         long long stride1, long long stride2, int b1, int b2);
 // 2-D fp32 tensor map over rows x cols (row stride cols), box 32 columns x

@@ -642,23 +642,6 @@ cudaError_t make_map_3d(CUtensorMap* map, const void* base, long long n0, long l
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Pages of an 8-bit cache, bytes [n_pages][hkv][page][dh], dh 64 or 128: a box is one page of `heads` neighbouring
-// KV heads, in shared memory eight rows of the first head, eight of the second, the next eight of the first,
-// .., swizzled by its rows of dh bytes.
-cudaError_t make_map_pages8(CUtensorMap* map, const void* base, int dh, int page, int hkv, long long n_pages, int heads) {
-  cudaError_t e = get_encoder();
-  if (e != cudaSuccess) return e;
-  const cuuint64_t row = dh, block = row * page;
-  cuuint64_t dims[5] = {row, 8u, (cuuint64_t)hkv, (cuuint64_t)page / 8, (cuuint64_t)n_pages};
-  cuuint64_t strides[4] = {row, block, 8 * row, block * hkv};
-  cuuint32_t box[5] = {(cuuint32_t)dh, 8u, (cuuint32_t)heads, (cuuint32_t)page / 8, 1u};
-  cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, dh == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // 2-D fp32 tensor map over rows x cols (row stride cols elements, a multiple
 // of 4), box 32 columns (128 bytes) x box_rows, 128-byte swizzle.
 cudaError_t make_map_f32(CUtensorMap* map, const void* base, long long rows, long long cols,
