@@ -235,7 +235,10 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a, int tid, int th
 // Tensor-core variants (attn_tc.cu; an 8-bit cache: attn_tc8.cu), where attn_tc_ok.
 bool attn_tc_ok(int dtype, int dh);
 constexpr int kTileRows = 128, kTileRows8 = 64;
-cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t st);
+constexpr int kSmall = 256;    // entries of a call that every CTA plans for itself
+// busy: CTAs of a launch just before it (attn_tc_pages of a dense prefix) that this one runs beside, each as long
+// as `places` of an entry's; 0: it waits for that launch.
+cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, int busy, int places, cudaStream_t st);
 bool attn_gives_up();  // a test made every wait give up before it begins
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);
 // Over a paged cache: the prefix's pieces and the rows' units (fields of a), items of the

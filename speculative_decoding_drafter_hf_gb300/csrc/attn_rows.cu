@@ -742,7 +742,7 @@ void plan_pieces(AttnRows& a) {
 struct PagesPlan {
   bool tc, dense;                       // dense: an 8-bit cache's prefix as bf16 rows
   int pre_items;                        // tensor cores: items of the prefix
-  size_t eff, tile0, ml, o, k, v, total; // offsets in the workspace (the line is at 0)
+  size_t eff, tile0, ml, o, plan, k, v, total; // offsets in the workspace (the line is at 0)
 };
 // Where very many rows share a long prefix, it is turned into bf16 rows once (a power of two as the scale:
 // exactly) and taken by the kernel for those, 256 rows at a time, instead of as codes, 64 or 128 at a time.
@@ -783,7 +783,8 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   w.total = w.o + rows * a.dh * sizeof(float) + 16;  // (the rows start on 32 bytes)
   if (w.dense) {
     const size_t values = (size_t)a.shared * a.Hkv * a.dh * 2;
-    w.k = (w.total + 15) / 16 * 16;
+    w.plan = (w.total + 15) / 16 * 16;  // the prefix's own line, lengths and places
+    w.k = (w.plan + 16 + (2 * (size_t)a.n + 1) * sizeof(int) + 15) / 16 * 16;
     w.v = w.k + values;
     w.total = w.v + values;
   }
@@ -892,11 +893,18 @@ hf_status attend(const AnyPages& c, int32_t layer, int32_t n, int32_t rows, int3
       b.k = ws + w.k;
       b.v = ws + w.v;
       b.k_ld = b.v_ld = (long long)a.Hkv * a.dh;
+      b.line = reinterpret_cast<int*>(ws + w.plan);
+      b.eff = b.line + 4;
+      b.tile0 = b.eff + a.n;
+      // SMs that the prefix leaves free begin with the entries' own keys, and take that much more of them: a place
+      // of theirs takes 1.6 us, the prefix 1.56 us a tile and 5 an item
+      const int ctas = std::min(w.pre_items, 152), rounds = (w.pre_items + ctas - 1) / ctas;
+      const int busy = a.n <= kSmall && ctas < 152 ? ctas : 0, places = rounds * (a.pre_keys / kKeyTile + 3);
       e = launch_prefix_values(*p, c.s, layer, requests, a.shared, ws + w.k, ws + w.v, st);
       if (e == cudaSuccess) e = launch_attn_tc_pages(b, w.pre_items, st);
-      if (e == cudaSuccess) e = launch_attn_tc8_pages(a, 0, st);
+      if (e == cudaSuccess) e = launch_attn_tc8_pages(a, 0, busy, places, st);
     } else {
-      e = c.e4m3 ? launch_attn_tc8_pages(a, w.pre_items, st) : launch_attn_tc_pages(a, w.pre_items, st);
+      e = c.e4m3 ? launch_attn_tc8_pages(a, w.pre_items, 0, 0, st) : launch_attn_tc_pages(a, w.pre_items, st);
     }
   } else {
     e = launch_attn_rows_pages(c.dtype, a, st);

@@ -246,7 +246,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   int* s_tile0 = s_eff + kSmall;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_trigger();
+  const bool beside = MODE == PAGED && a.dense;
+  if (!beside) pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
@@ -277,6 +278,9 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  // The launch behind a dense prefix does not wait for it: it comes once all CTAs are here, so when what ran
+  // before them has ended.
+  if (beside) pdl_trigger();
   if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a, tid, TCT);
   __syncwarp();  // (its lanes' loops end apart, and the next instruction wants the warp together)
 

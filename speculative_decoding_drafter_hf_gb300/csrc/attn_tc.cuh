@@ -10,7 +10,6 @@ namespace hf {
 constexpr int BN = kKeyTile;   // keys per tile
 constexpr int TCT = 384;       // threads
 constexpr int kNone = 0x7fffffff;
-constexpr int kSmall = 256;    // entries of a call that every CTA plans for itself
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -131,6 +130,7 @@ struct TcArgs {
   int pre_items;   // paged: items of the prefix
   int wide;        // rows of out start on 32 bytes
   int small;       // paged: every CTA plans for itself
+  int busy, places; // 8-bit cache: launch_attn_tc8_pages
   int wait;        // 0: every wait gives up before it begins (set by a test)
 };
 

@@ -637,7 +637,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
+  if (c.busy == 0) pdl_wait();  // (else: at the end)
   __syncwarp();
 
   if (c.wait == 0) {
@@ -845,10 +845,11 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         make_prefix(c, idx, it, eff);
         put(it);
       }
-      const int heavy = c.pre_items % all;
+      // (beside another launch the first CTAs are those that found an SM free)
+      const int heavy = c.busy ? c.busy : c.pre_items % all;
       AttnLine line;
       if (c.small) {
-        line = make_line(scan_tiles(a, s_eff, s_tile0), a.units, all, heavy, prefix_places(a));
+        line = make_line(scan_tiles(a, s_eff, s_tile0), a.units, all, heavy, c.busy ? c.places : prefix_places(a));
         if (me == 0) {
           for (int i = lane; i <= a.n; i += 32) a.tile0[i] = s_tile0[i];
           if (lane == 0) *reinterpret_cast<AttnLine*>(a.line) = line;
@@ -856,7 +857,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       } else {
         line = *reinterpret_cast<const AttnLine*>(a.line);
       }
-      const int cta = (me - heavy + all) % all, end = min(line.start(cta + 1), line.tiles * a.units);
+      const int cta = c.busy ? me : (me - heavy + all) % all, end = min(line.start(cta + 1), line.tiles * a.units);
       for (int pos = line.start(cta); ok && pos < end;) {
         bool some;
         pos += make_own(c, line, cta, pos, end, it, some, eff, tile0);
@@ -956,6 +957,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (c.busy) pdl_wait();  // this launch has ended only when the one that it ran beside has: the join waits for both
 }
 
 // Pages of the cache, bytes [n_pages][hkv][page][dh]: a box is one page of `heads` neighbouring KV heads, in shared
@@ -1017,7 +1019,7 @@ cudaError_t launch_rows(const TcArgs& c, const CUtensorMap* m, dim3 grid, cudaSt
 
 }  // namespace
 
-cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t st) {
+cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, int busy, int places, cudaStream_t st) {
   TcArgs c{};
   c.a = a;
   c.tb = a.tb;
@@ -1025,6 +1027,8 @@ cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t
   c.box_rows = a.page;
   c.wait = !attn_gives_up();
   c.pre_items = pre_items;
+  c.busy = busy;
+  c.places = places;
   CUtensorMap m[4];  // K, V of one head, of two
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 4 && e == cudaSuccess; ++i)
@@ -1032,7 +1036,7 @@ cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, cudaStream_t
   if (e != cudaSuccess) return e;
   // (the line is at most as long as all tables reach)
   const long long reach = (((long long)a.table_ld * a.page - a.shared + BN - 1) / BN + a.item_start) * a.n * a.units;
-  const int grid = (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
+  const int grid = busy ? 152 : (int)std::min<long long>(std::max<long long>(pre_items + reach, 1), 152);
   c.small = a.n <= kSmall;
   if (!c.small) e = launch_attn_plan(a, grid, pre_items % grid, st);
   if (e != cudaSuccess) return e;
