@@ -375,11 +375,11 @@ __global__ void __launch_bounds__(CT) prefix8_kernel(RowsArgs a) {
   const int r = a.req ? __ldcg(a.req) : 0;
   if (r < 0 || r >= p.n_requests) return;  // (an entry that breaks a rule is reported by the attention)
   const int len = __ldcg(&p.lens[r]);
-  if (len < a.total || pages_of(len, p.page) > p.table_ld) return;
-  const int units = a.total / p.page * 2 * pieces;
+  const int units = (a.total >> shift) * 2 * pieces;
   for (int u = blockIdx.x * (CT / 32) + warp; u < units; u += gridDim.x * (CT / 32)) {
     const int piece = u % pieces, kv = u / pieces & 1, j = u / pieces / 2;
-    const int id = __ldcg(&p.table[(size_t)r * p.table_ld + j]);
+    const int id = __ldcg(&p.table[(size_t)r * p.table_ld + j]);  // (the table reaches that far, whatever the length)
+    if (len < a.total || pages_of(len, p.page) > p.table_ld) return;
     if (id < 0 || id >= p.n_pages) {
       if (lane == 0) pages_flag(p, HF_S_BAD);
       continue;
