@@ -7,6 +7,7 @@
 // to the smallest codes. Bound by the reads of the rows and the writes of the codes.
 #include <cstdio>
 
+#include "attn.cuh"
 #include "e4m3.cuh"
 #include "pages.cuh"
 
@@ -58,6 +59,22 @@ __device__ __forceinline__ void unpack16(const uint4& w, float* x) {
       x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
     }
   }
+}
+
+// 16 bytes of a row with NaN for its infinities; out of line, as few rows need it.
+template <typename T>
+__device__ __noinline__ uint4 no_inf16(uint4 y) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      if ((w[k] & 0x7fffffffu) == 0x7f800000u) w[k] = 0x7fffffffu;
+    } else {
+      if ((w[k] & 0x7fffu) == 0x7f80u) w[k] |= 0x7fffu;
+      if ((w[k] & 0x7fff0000u) == 0x7f800000u) w[k] |= 0x7fff0000u;
+    }
+  }
+  return y;
 }
 
 // i / d of 0 <= i < 2^24, 1 <= d <= 256.
@@ -267,12 +284,17 @@ __global__ void __launch_bounds__(CT, 4) write8_kernel(RowsArgs a) {
       }
     }
     const float inv = 1.f / s;  // (a power of two)
-    auto put = [&](int i, const uint4& y) {
+    auto put = [&](int i, uint4 y) {
       float v[VE];
+      if (odd) y = no_inf16<T>(y);
       unpack16<T>(y, v);
       uint32_t c[VE / 4];
 #pragma unroll
-      for (int k = 0; k < VE; ++k) v[k] = (odd ? no_inf(v[k]) : v[k]) * inv;
+      for (int k = 0; k < VE; k += 2) {
+        const float2 z = unpair(mul2(pair(v[k], v[k + 1]), pair(inv, inv)));
+        v[k] = z.x;
+        v[k + 1] = z.y;
+      }
 #pragma unroll
       for (int k = 0; k < VE / 4; ++k)
         c[k] = to_e4m3x2(v[4 * k], v[4 * k + 1]) | to_e4m3x2(v[4 * k + 2], v[4 * k + 3]) << 16;
