@@ -24,7 +24,14 @@
 // on, warp 3 turns the next one's rows into codes, if a row tile has 16 at most (one warp took longer than
 // an item for more: 64 x 8 rows over 4096 tokens 136 us), or fetches them, if 32; else the groups do it when they
 // come to it. Row tiles of two KV heads read pages that lie side by
-// side: one copy brings both, eight rows of one, eight of the other (4 KB for a page of 16 tokens).
+// side: one copy brings both, eight rows of one, eight of the other (4 KB for a page of 16 tokens; 64 x 1
+// rows over 4096 tokens with such pages 103 us, with a copy for each head 125).
+//
+// Bound by the reads where requests are long: 64 requests of 2048 to 32768 tokens, one row of 40 heads over 10 each,
+// 281 us (6.7 TB/s of 6.8 that a copy reaches; tensor pipe 9%). Shorter ones by what an item costs beside its
+// tiles (about 17000 cycles for 32 rows, 8000 for 5: codes, waits, joining the sums, storing; the first of a CTA twice
+// that, as its instructions come from the L2) and tiles by their chain (about 3000 cycles of two row tiles of
+// 32 rows: 64 x 8 rows over 4096 tokens 120 us, 4.5 TB/s; of 64 rows 5500).
 #include <cudaTypedefs.h>
 
 #include <mutex>

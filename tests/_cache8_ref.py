@@ -6,9 +6,9 @@ give the same bits.
 Attention over codes and scales, beside the terms of _target_ref.attention (u = 2^-24, n keys, dh products a
 score, the result rounded to bf16, weights to 2^-8: a code has 4 bits, so hi is off by 2^-4 of
 a weight at most and lo by 2^-4 of that): bf16 rows on the tensor cores are two codes in units
-of 2^e, amax <= 448 * 2^e, amax > 224 * 2^e. lo ends at steps of 2^-9, so a value is off by 2^-10 2^e
-< 2^-10 amax / 224 at most where hi + lo is not exact, and a score by that times sum_d |k_d| scale. A
-weight's lo ends at steps of 2^-9 too, where the largest weight of a row is 2^5 at least:
+of 2^e, amax <= 448 * 2^e, amax > 224 * 2^e. lo is a code of 16 times the rest and ends at steps of 2^-9 / 16, so
+a value is off by 2^-14 2^e < 2^-14 amax / 224 at most where hi + lo / 16 is not exact, and a score by that times
+sum_d |k_d| scale. A weight's lo ends at the same steps, where the largest weight of a row is 2^1 at least:
 2^-15 of the largest p_j s_j, and so sum_j |v_j / s_j| times that, over the sum of p.
 
 Rotary: the reduced angle is off by 2^-32 turns of the product's cut and 2^-25 of its size, pi at most, in 32
@@ -72,7 +72,7 @@ def attention(q, k, v, vs, scale, bf16, tc):
         p = np.exp(s - s.max())
         mag = p @ np.abs(v) / p.sum()
         fine = 2.0 ** -15 * (p * vs).max() * np.sum(np.abs(v) / vs[:, None], 0) / p.sum()
-        ds = 2.0 ** -10 * np.abs(q).max() / 224 * np.abs(k).sum(1).max() * scale
+        ds = 2.0 ** -14 * np.abs(q).max() / 224 * np.abs(k).sum(1).max() * scale
     return o, tol + fine + 4 * ds * mag
 
 
