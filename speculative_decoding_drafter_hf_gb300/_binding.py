@@ -733,6 +733,7 @@ class Pages:
         base.work, base.status = self._work.data_ptr(), self.status.data_ptr()
         self._d, self._keep, self._ref = base, call, ctypes.byref(call)
         self._i32, self._index, self._dtype, self._layers, self._row = i32, k.get_device(), rows, L, (hkv, dh)
+        self._u8 = torch.uint8
         self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         with torch.cuda.device(self._index):
             if not torch.cuda.is_current_stream_capturing():  # calls may come on any stream: both are zero by now
@@ -808,11 +809,11 @@ class Pages:
         if (len(shape) != (4 if layer is None else 3) or shape[-2:] != self._row
                 or (layer is None and shape[0] > self._layers)):
             raise ValueError("k must be [layers, tokens, kv heads, head_dim], or [tokens, kv heads, head_dim] with layer")
-        for t, name in ((k, "k"), (v, "v")):
-            if t.dtype is not self._dtype or t.get_device() != self._index:
-                raise TypeError(f"{name} must be {self._dtype} on cuda:{self._index}")
+        i, dt = self._index, self._dtype
+        if k.dtype is not dt or v.dtype is not dt or k.get_device() != i or v.get_device() != i:
+            raise TypeError(f"k and v must be {dt} on cuda:{i}")
         T, (hkv, dh) = shape[-3], self._row
-        ld = _heads_ld(k, T, hkv, dh, "k")
+        ld = ks[-3] if T > 1 and ks[-1] == 1 and ks[-2] == dh else _heads_ld(k, T, hkv, dh, "k")
         layers = shape[0] if layer is None else 1
         step = ks[0] if layers > 1 else 0
         if v.shape != shape or (T and vs != ks and (_heads_ld(v, T, hkv, dh, "v") != ld or (layers > 1 and vs[0] != step))):
@@ -840,30 +841,38 @@ class Pages:
     def attend(self, q, requests=None, *, layer=0, shared=0, scale=0.0, out=None, workspace=None, stream=None):
         """hf_attention_pages: q [n, rows, Hq, dh] are the newest `rows` tokens of the
         requests; returns out of the same shape."""
-        import torch
-        on = _On(self.k, stream)
-        if q.dim() != 4 or q.shape[3] != self._d.head_dim:
+        shape = q.shape
+        if len(shape) != 4 or shape[3] != self._row[1]:
             raise ValueError("q must be [requests, rows, heads, head_dim]")
-        n, rows, hq, dh = q.shape
+        n, rows, hq, dh = shape
+        dt, i = self._dtype, self._index
+        if out is None or workspace is None:
+            on = _On(self.k, stream)
+            if out is None:
+                out = on.empty(tuple(shape), dt)
+            if workspace is None:
+                workspace = on.empty((max(self._C["attend_workspace"](self._ref, n, rows, hq, shared), 16),), self._u8)
+        # (one test for the tensors that are right: a small call is bound by these checks)
+        if (q.dtype is not dt or out.dtype is not dt or q.get_device() != i or out.get_device() != i or out.shape != shape
+                or workspace.dtype is not self._u8 or workspace.get_device() != i or not workspace.is_contiguous()):
+            on = _On(self.k, stream)
+            for t, name in ((q, "q"), (out, "out")):
+                on.arg(t, name, dt, shape, False)
+            on.arg(workspace, "workspace", self._u8)
 
         def ld(t, name):
-            s = _heads_ld(t, rows, hq, dh, name)
+            s = t.stride()
+            if s[3] == 1 and s[2] == dh and (n == 1 or rows == 1 or s[0] == rows * s[1]):
+                return s[1] if rows > 1 else s[0] if n > 1 else hq * dh
+            r = _heads_ld(t, rows, hq, dh, name)
             if rows == 1 and n > 1:
-                s = t.stride(0)
-            elif n > 1 and t.stride(0) != rows * s:
+                r = s[0]
+            elif n > 1 and s[0] != rows * r:
                 raise ValueError(f"{name}: its rows must be evenly spaced")
-            return s
+            return r
 
-        qp = on.arg(q, "q", self._dtype, None, False)
-        if out is None:
-            out = on.empty(tuple(q.shape), q.dtype)
-        op = on.arg(out, "out", q.dtype, q.shape, False)
-        if workspace is None:
-            b = self._C["attend_workspace"](self._ref, n, rows, hq, shared)
-            workspace = on.empty((max(b, 16),), torch.uint8)
-        wp = on.arg(workspace, "workspace", torch.uint8)
-        on.call(self._C["attend"], self._ref, layer, n, rows, hq, qp, ld(q, "q"), self._ints(requests, n, "requests"),
-                shared, scale or 0.0, op, ld(out, "out"), wp, workspace.shape[0])
+        self._call(self._C["attend"], stream, layer, n, rows, hq, q.data_ptr(), ld(q, "q"), self._ints(requests, n, "requests"),
+                   shared, scale or 0.0, out.data_ptr(), ld(out, "out"), workspace.data_ptr(), workspace.shape[0])
         return out
 
 
@@ -949,31 +958,56 @@ class Rotary:
         self.turns = torch.from_numpy(host.view(np.int64)).to(device)  # w_i / (2 pi) in 2^-64 turns, unsigned
         if self.turns.is_cuda and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(self.turns.device).synchronize()  # calls may come on any stream
+        self._index, self._turns, self._inter, self._i32 = self.turns.get_device(), self.turns.data_ptr(), int(self.interleaved), torch.int32
+        self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
     def __call__(self, q, k, positions, *, q_out=None, k_out=None, stream=None):
         """q [T, Hq, dh] and k [T, Hkv, dh] (or None) turned by positions int32 [T]: into q_out and
         k_out, which may be q and k, or new tensors. Row strides are free. Returns (q_out, k_out)."""
-        import torch
-        on = _On(q, stream)
-        if q.dim() != 3 or q.shape[2] != self.head_dim or (k is not None and k.dim() != 3):
+        shape, i, dt = q.shape, q.get_device(), q.dtype
+        if i < 0 or i != self._index:
+            raise TypeError(f"q must be a CUDA tensor on the table's device ({self.turns.device})")
+        if len(shape) != 3 or shape[2] != self.head_dim or (k is not None and k.dim() != 3):
             raise ValueError("q and k must be [tokens, heads, head_dim]")
-        T, hq, dh = q.shape
-        dt = q.dtype
+        T, hq, dh = shape
         code = _dtype_code(q, "q")
-        tp = on.arg(self.turns, "the table")
-        pp = on.arg(positions, "positions", torch.int32, (T,))
-        if q_out is None:
-            q_out = on.empty((T, hq, dh), dt)
-        qo = on.arg(q_out, "q_out", dt, q.shape, False)
-        hkv, kp, k_ld, ko, ko_ld = 0, None, 0, None, 0
-        if k is not None:
+        if (positions.dtype is not self._i32 or positions.get_device() != i or positions.shape != (T,)
+                or not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous int32 tensor of {T} entries on cuda:{i}")
+
+        def ld(t, name, shape):
+            # (one test for the tensors that are right: a small call is bound by these checks)
+            s = t.stride()
+            if t.dtype is dt and t.get_device() == i and t.shape == shape and s[2] == 1 and s[1] == dh:
+                return s[0] if T > 1 else shape[1] * dh
+            if t.dtype is not dt or t.get_device() != i:
+                raise TypeError(f"{name} must be {dt} on cuda:{i}")
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+            return _heads_ld(t, T, shape[1], dh, name)
+
+        if q_out is None or (k is not None and k_out is None):
+            on = _On(q, stream)
+            q_out = on.empty(tuple(shape), dt) if q_out is None else q_out
+            k_out = on.empty((T, k.shape[1], dh), dt) if k is not None and k_out is None else k_out
+        if k is None:
+            hkv, kp, k_ld, ko, ko_ld = 0, None, 0, None, 0
+        else:
             hkv = k.shape[1]
-            kp = on.arg(k, "k", dt, (T, hkv, dh), False)
-            k_ld = _heads_ld(k, T, hkv, dh, "k")
-            if k_out is None:
-                k_out = on.empty((T, hkv, dh), dt)
-            ko = on.arg(k_out, "k_out", dt, k.shape, False)
-            ko_ld = _heads_ld(k_out, T, hkv, dh, "k_out")
-        on.call(hf_rotary, code, int(self.interleaved), T, hq, hkv, dh, self.dim, tp, self.attention, pp, q.data_ptr(),
-                _heads_ld(q, T, hq, dh, "q"), kp, k_ld, qo, _heads_ld(q_out, T, hq, dh, "q_out"), ko, ko_ld)
+            kv = (T, hkv, dh)
+            kp, k_ld, ko, ko_ld = k.data_ptr(), ld(k, "k", kv), k_out.data_ptr(), ld(k_out, "k_out", kv)
+        args = (code, self._inter, T, hq, hkv, dh, self.dim, self._turns, self.attention, positions.data_ptr(), q.data_ptr(),
+                ld(q, "q", shape), kp, k_ld, q_out.data_ptr(), ld(q_out, "q_out", shape), ko, ko_ld)
+        if stream is None:
+            stream = self._raw_stream(i)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if self._current() == i:
+            e = hf_rotary(*args, stream)
+        else:
+            import torch
+            with torch.cuda.device(i):
+                e = hf_rotary(*args, stream)
+        if e != 0:
+            raise HyflashError(e, hf_last_error(None).decode())
         return q_out, k_out
