@@ -422,20 +422,30 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
           // (a row that sees nothing of the first tile sees nothing of the item)
           const float down = (j == 0 ? m > -INFINITY : m > kLift) ? kLifted - m : 0.f;
           R.red[row] = down;
+          G.red[row] = j == 0 ? 1.f : ex2(down);  // (the column's maxima have been read, by this thread alone)
           row_minus_m(R, row) += down;
         }
         group_any(r, false);
         if (j > 0) {
 #pragma unroll 1
-          for (int i = 0; i < 2 * hb; ++i) {
-            const int c = (h0 + (i >> 1)) * 16, h = h0 + (i >> 1) + (i & 1) * NC;
-            float o[16];
-            tmem_ld16_async(G.to + h * 16, o);
-            tmem_wait_ld();
-            tmem_hold16(o);
+          for (int i = 0; i < hb; ++i) {
+            const float4* f4 = reinterpret_cast<const float4*>(G.red + (h0 + i) * 16);
+            const float4 f[4] = {f4[0], f4[1], f4[2], f4[3]};
+            const float* factor = reinterpret_cast<const float*>(f);
+            bool same = true;  // (mostly one row of many is raised)
 #pragma unroll
-            for (int n = 0; n < 16; ++n) o[n] *= ex2(R.red[c + n]);
-            tmem_st16(G.to + h * 16, o);
+            for (int n = 0; n < 16; ++n) same = same && factor[n] == 1.f;
+            if (same) continue;
+#pragma unroll 1
+            for (int h = h0 + i; h < 2 * NC; h += NC) {
+              float o[16];
+              tmem_ld16_async(G.to + h * 16, o);
+              tmem_wait_ld();
+              tmem_hold16(o);
+#pragma unroll
+              for (int n = 0; n < 16; ++n) o[n] *= factor[n];
+              tmem_st16(G.to + h * 16, o);
+            }
           }
           tmem_wait_st();
         }
@@ -443,7 +453,7 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
         for (int n = 0; n < HB * 16; n += 2) {
           if (n >= hb * 16) continue;
           const float2 down = *reinterpret_cast<const float2*>(&R.red[h0 * 16 + n]);
-          l2[h0 * 8 + n / 2] = mul2(l2[h0 * 8 + n / 2], pair(j > 0 ? ex2(down.x) : 1.f, j > 0 ? ex2(down.y) : 1.f));
+          l2[h0 * 8 + n / 2] = mul2(l2[h0 * 8 + n / 2], *reinterpret_cast<const uint64_t*>(&G.red[h0 * 16 + n]));
           z[n] += down.x;
           z[n + 1] += down.y;
         }
