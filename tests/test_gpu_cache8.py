@@ -302,6 +302,47 @@ def test_attend_on_another_stream_captured_and_two_at_once(hf):
     assert torch.equal(out, first) and not c.check()
 
 
+def test_attend_a_long_prefix_replayed_and_two_at_once(hf):
+    """The launches of a long prefix of many rows run into each other (the entries' own keys beside the prefix): with
+    rows that change just before, in a graph, and on two streams at once."""
+    own = [700, 3, 90, 1] * 12
+    pool, table, lens, refs = _shared_cache(2, 128, 32, 2304, own, 29)
+    c = _on_gpu(hf, pool, table, lens, refs, "bf16")
+    qs = [_randn((48, 2, 8, 128), "bf16", 30 + i).cuda() for i in range(3)]
+    firsts = []
+    for q in qs:
+        first = c.attend(q, shared=2304)
+        torch.cuda.synchronize()
+        firsts.append(first.clone())
+    want, tol = _want(qs[0], pool, table, lens, "bf16")
+    R.check_attention(R.to64(firsts[0]), want, tol)
+    q, out, ws = torch.empty_like(qs[0]), torch.empty_like(qs[0]), c.attend_workspace(qs[0], 2304)
+    ws.fill_(255)
+    for i in (0, 1, 2, 1, 0, 2):  # no wait between the calls; the rows are written by the kernel just before
+        q.copy_(qs[i])
+        c.attend(q, shared=2304, out=out, workspace=ws)
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, firsts[i])
+    graph = torch.cuda.CUDAGraph()
+    kept = [torch.empty_like(out) for _ in range(3)]
+    with torch.cuda.graph(graph):
+        for i in range(3):
+            q.copy_(qs[i])
+            c.attend(q, shared=2304, out=out, workspace=ws)
+            kept[i].copy_(out)
+    for _ in range(3):
+        for k in kept:
+            k.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(k, f) for k, f in zip(kept, firsts))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(i, c.attend(qs[i], shared=2304, stream=streams[i % 2])) for _ in range(6) for i in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, firsts[i]) for i, o in outs) and not c.check()
+
+
 def test_attend_waits_that_run_out(hf):
     from speculative_decoding_drafter_hf_gb300 import _binding as B
     pool, table, lens, refs = _shared_cache(2, 128, 16, 32, [90, 60], 18)
