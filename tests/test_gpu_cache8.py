@@ -167,7 +167,7 @@ def test_attend_strange_entries_pages_and_prefixes(hf, dtype, dh):
         assert c.check() == hf.CallStatus.BAD
     # page ids out of range: reported, the others as before
     want, tol = _want(q[:4], pool, table, lens, dtype)
-    for bad in (-1, len(refs), 1 << 30):
+    for bad in (-1, -2, len(refs), 1 << 30):
         t = [list(r) for r in table]
         t[1][5] = bad
         c = _on_gpu(hf, pool, t, lens, refs, dtype)
