@@ -665,7 +665,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       // ---- loads: K(0), then V(j), K(j+1) through the ring; of two heads a place and the next one at a time
       int ri = 0;  // places so far
       bool ok = true;
-      const int nbox = BN / a.page, shift = 31 - __clz(a.page);
+      const int nbox = BN / a.page, shift = 31 - __clz(a.page), box = lane & (nbox - 1);
       for (int n = 0; ok; ++n) {
         const Item& it = items[n & 1];
         ok = wait_uniform(smem_u32(&i_full[n & 1]), (uint32_t)(n >> 1) & 1u);
@@ -678,50 +678,39 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const int first = it.j0 >> shift, pages = j1 > it.j0 ? ((j1 - 1) >> shift) - first + 1 : 0;
         auto look_up = [&](int batch) { return batch * 32 + lane < pages ? tab[first + batch * 32 + lane] : 0; };
         int batch = 0, now = look_up(0), then = look_up(1);
-        auto place = [&]() {  // the next place of the ring, free
+        // Waits for the next place of the ring, of two heads for two: a lane looks at one of them.
+        auto place = [&](int count) {
           const int s = ri % NS;
-          if (ri >= NS) ok = ok && wait_uniform(smem_u32(&empty[s]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
+          if (ri >= NS) ok = wait_uniform(smem_u32(&empty[s + (lane & (count - 1))]), ((uint32_t)(ri / NS) & 1u) ^ 1u);
           ok = ok && !*abort_flag;
           return s;
         };
+        // (few instructions a tile: this warp's were the limit where tiles are short)
         auto tile = [&](int j, bool is_v) {
-          const int at = j * nbox, id = __shfl_sync(0xffffffffu, (at >> 5) == batch ? now : then, (at + lane) & 31);
-          const int s = place();
+          const int at = j * nbox, id = __shfl_sync(0xffffffffu, (at >> 5) == batch ? now : then, (at + box) & 31);
+          const int s = place(two ? 2 : 1);
           if (!ok) return;
-          if (two) {
-            ++ri;
-            place();
-            --ri;
-            if (!ok) return;
-          }
-          if (lane == 0) {
-            mbar_expect_tx(&full[s], two ? 2 * L::TILE : L::TILE);
-            if (two) mbar_arrive(&full[s + 1]);
-          }
+          if (lane < (two ? 2 : 1)) mbar_expect_tx(&full[s + lane], lane ? 0 : two ? 2 * L::TILE : L::TILE);
           __syncwarp();
+          const bool mine = at + box < pages, on = mine && id >= 0 && id < a.n_pages;
           if (lane < nbox) {
-            const bool mine = at + lane < pages, on = mine && id >= 0 && id < a.n_pages;
-            const int z = on ? id : a.n_pages;  // behind the pool: reads zeros
             if (mine && !on && a.status) atomicOr(a.status, HF_S_BAD);
-            uint8_t* dst = sKV + (size_t)s * L::TILE + lane * a.page * (two ? 2 * DH : DH);
-            tma_load_page(dst, two ? (is_v ? &mv2 : &mk2) : is_v ? &mv : &mk, &full[s], g, z);
-            if (is_v) {  // all scales: V's places stay until the weights are there
-              const size_t sc = on ? (size_t)id * a.Hkv + g : 0;
-              copy4(s_sc + s * 32 + lane, a.k_scale + sc, on);
-              copy4(s_sc + s * 32 + 16 + lane, a.v_scale + sc, on);
-              if (two) {
-                copy4(s_sc + (s + 1) * 32 + lane, a.k_scale + sc + on, on);
-                copy4(s_sc + (s + 1) * 32 + 16 + lane, a.v_scale + sc + on, on);
-              }
-            }
+            tma_load_page(sKV + (size_t)s * L::TILE + lane * a.page * (two ? 2 * DH : DH), two ? (is_v ? &mv2 : &mk2) : is_v ? &mv : &mk,
+                          &full[s], g, on ? id : a.n_pages);  // behind the pool: reads zeros
           }
+          if (is_v)  // all scales, one a lane: V's places stay until the weights are there
+            for (int i = lane; i < (two ? 4 : 2) * nbox; i += 32) {
+              const int q = i >> (7 - shift), head = q >> 1;  // (nbox = 128 >> shift)
+              copy4(s_sc + (s + head) * 32 + (q & 1) * 16 + box,
+                    (q & 1 ? a.v_scale : a.k_scale) + (on ? (size_t)id * a.Hkv + g + head : 0), on);
+            }
           copies_arrive(&full[s]);
           if (two) copies_arrive(&full[s + 1]);
           ri += two ? 2 : 1;
         };
         if (nt > 0) {
           if (two && (ri & 1)) {  // two places lie side by side from an even one on: this one stays empty
-            const int s = place();
+            const int s = place(1);
             if (ok) {
               if (lane == 0) mbar_arrive(&full[s]);
               copies_arrive(&full[s]);
