@@ -25,13 +25,15 @@
 // an item for more: 64 x 8 rows over 4096 tokens 136 us), or fetches them, if 32; else the groups do it when they
 // come to it. Row tiles of two KV heads read pages that lie side by
 // side: one copy brings both, eight rows of one, eight of the other (4 KB for a page of 16 tokens; 64 x 1
-// rows over 4096 tokens with such pages 103 us, with a copy for each head 125).
+// rows over 4096 tokens with such pages 105 us instead of 125, and 94 now).
 //
 // Bound by the reads where requests are long: 64 requests of 2048 to 32768 tokens, one row of 40 heads over 10 each,
-// 281 us (6.7 TB/s of 6.8 that a copy reaches; tensor pipe 9%). Shorter ones by what an item costs beside its
+// 278 us (6.8 TB/s, as a copy; tensor pipe 9%). Shorter ones by what an item costs beside its
 // tiles (about 17000 cycles for 32 rows, 8000 for 5: codes, waits, joining the sums, storing; the first of a CTA twice
 // that, as its instructions come from the L2) and tiles by their chain (about 3000 cycles of two row tiles of
-// 32 rows: 64 x 8 rows over 4096 tokens 120 us, 4.5 TB/s; of 64 rows 5500).
+// 32 rows: 64 x 8 rows over 4096 tokens 114 us, 4.8 TB/s; of 64 rows 5500). Heads of 64, 64 x 1 rows over 4096
+// tokens: 65 us (4.1 TB/s), where the copies' rows of 64 bytes seem to bound it: neither a longer ring, nor a second
+// loading warp made it faster.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -674,7 +676,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const bool two = it.split && it.nt[1] > 0;
         const int32_t* tab = attn_table(a, it.entry);
         // The item's pages, 32 at a time and 32 ahead: a look-up for every tile, though made a tile ahead, held the copies
-        // up (64 x 1 rows over 4096 tokens, heads of 64: 80 us, MEASURED).
+        // up (64 x 1 rows over 4096 tokens, heads of 64: 80 us, so 73).
         const int first = it.j0 >> shift, pages = j1 > it.j0 ? ((j1 - 1) >> shift) - first + 1 : 0;
         auto look_up = [&](int batch) { return batch * 32 + lane < pages ? tab[first + batch * 32 + lane] : 0; };
         int batch = 0, now = look_up(0), then = look_up(1);
@@ -685,7 +687,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           ok = ok && !*abort_flag;
           return s;
         };
-        // (few instructions a tile: this warp's were the limit where tiles are short)
+        // (few instructions a tile: this warp's were the limit where tiles are short; the same call 73 us before, 65 now)
         auto tile = [&](int j, bool is_v) {
           const int at = j * nbox, id = __shfl_sync(0xffffffffu, (at >> 5) == batch ? now : then, (at + box) & 31);
           const int s = place(two ? 2 : 1);
