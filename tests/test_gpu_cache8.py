@@ -633,6 +633,29 @@ def test_bad_entries_of_write_and_read(hf):
     assert torch.equal(k[30:33], k2[0])
 
 
+def test_as_many_requests_as_there_can_be(hf):
+    """A cache of 4096 requests written in one call, and read back by more entries than requests."""
+    n, page, dh = 4096, 8, 16
+    c = hf.Pages8.empty(1, 5000, 1, page, dh, n, 2, dtype=torch.float32)
+    rng = random.Random(3)
+    counts = [rng.choice([0, 1, 3, 9]) if i % 4 else 2 for i in range(n)]
+    ref = Cache(1, 5000, 1, page, dh, n, 2)
+    assert ref.extend(list(range(n)), counts) == ""
+    c.extend(C.ints(counts))
+    ends = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    x = _randn((1, ends[-1], 1, dh), "f32", 31, 3.0)
+    ref.write8(list(range(n)), ends, {"k": R.to64(x), "v": R.to64(x)})
+    c.write(x.cuda(), x.cuda(), C.ints(ends))
+    req = [rng.randrange(n) for _ in range(6000)]
+    first = [rng.randint(0, ref.lens[r]) for r in req]
+    count = [ref.lens[r] - f for r, f in zip(req, first)]
+    at = np.concatenate([[0], np.cumsum(count)]).tolist()
+    k, v = c.read(C.ints(first), C.ints(at), C.ints(req), total=at[-1])
+    want = np.concatenate([ref.tokens("k", r, f, m) for r, f, m in zip(req, first, count)], 1)
+    _same(k, R.to64(torch.tensor(want).float()), "read")
+    assert torch.equal(k, v) and not c.check()
+
+
 def test_write_and_read_beyond_32_bits(hf):
     """A pool and rows past 2^32 elements: 2 layers of 2.2 GB."""
     L, pages, hkv, page, dh = 2, 17000, 8, 128, 128

@@ -99,6 +99,19 @@ def test_no_rows_streams_and_graphs(hf):
     assert torch.equal(out, rot(x, None, pos)[0])
 
 
+def test_wrong_arguments(hf):
+    rot, x = hf.Rotary(64), torch.zeros(3, 4, 64, device="cuda")
+    pos = C.ints([0, 1, 2])
+    for bad, error in ((dict(positions=pos.cpu()), ValueError), (dict(positions=pos.long()), ValueError), (dict(positions=pos[:2]), ValueError),
+                       (dict(q=x.half()), TypeError), (dict(q=x.cpu()), TypeError), (dict(q=x[..., :32]), ValueError),
+                       (dict(q=x[0]), ValueError), (dict(k=x[:2]), ValueError), (dict(k=x.bfloat16()), TypeError),
+                       (dict(q_out=x[:, :2]), ValueError), (dict(q_out=x.bfloat16()), TypeError),
+                       (dict(q=x.transpose(0, 1).contiguous().transpose(0, 1)), ValueError)):
+        a = {"q": x, "k": None, "positions": pos, "q_out": None, **bad}
+        with pytest.raises(error):
+            rot(a["q"], a["k"], a["positions"], q_out=a["q_out"])
+
+
 def test_rows_and_strides_beyond_32_bits(hf):
     """Rows 2^31 elements apart and more."""
     rot = hf.Rotary(64)
