@@ -49,6 +49,11 @@ ATTEND = [  # dtype, Hq, Hkv, dh, page, rows, shared, own lengths (None: an empt
     ("bf16", 64, 1, 128, 32, 64, 64, [70, 64]),                  # as many rows as there are: 4096 of a head
     ("bf16", 6, 3, 128, 16, 9, 48, [200, 9, 8, 0]),              # a last head without a neighbour
     ("bf16", 21, 3, 64, 8, 7, 16, [100, 1]),                     # row tiles of 49 rows
+    ("bf16", 8, 2, 128, 16, 8, 64, [40]),                        # the prefix's row tile is the entry's own
+    ("bf16", 8, 2, 64, 16, 8, 64, [7]),
+    ("bf16", 4, 2, 64, 32, 1, 64, [40]),
+    ("bf16", 12, 2, 128, 32, 8, 64, [40, 100]),                  # row tiles of 48 rows beside a prefix's of 60
+    ("bf16", 12, 2, 64, 32, 8, 64, [40, 100, None]),
     ("bf16", 4, 4, 32, 16, 4, 32, [20, 3]),
     ("bf16", 3, 1, 80, 32, 2, 64, [20, 90]),
     ("bf16", 2, 1, 256, 16, 64, 16, [64, 100]),
