@@ -746,10 +746,11 @@ struct PagesPlan {
 };
 // Where very many rows share a long prefix, it is turned into bf16 rows once (a power of two as the scale:
 // exactly) and taken by the kernel for those, 256 rows at a time, instead of as codes, 64 or 128 at a time.
-// Whole calls, us, as rows / as codes, 8 KV heads: 192 rows of a head over 8192 tokens 59 / 50, 384 71 / 71,
-// 512 72 / 82, 2048 160 / 235; 768 over 2048 tokens 54 / 53, 1024 60 / 60.
-constexpr int kDenseRows = 384;
-constexpr long long kDenseWork = 1 << 21;  // rows of a head x tokens
+// Whole calls in a graph, us, as rows / as codes, 8 KV heads: 192 rows of a head over 8192 tokens 55.5 / 49.2, 256
+// 57.3 / 53.3, 384 59.6 / 68.2, 512 69 / 82, 2048 133 / 235; over 2048 tokens 512 47.3 / 44.7, 768 49.9 / 52.4, 1024
+// 54.9 / 59.0.
+constexpr int kDenseRows = 320;
+constexpr long long kDenseWork = 5 << 18;  // rows of a head x tokens
 PagesPlan plan_call(AttnRows& a, int dtype) {
   PagesPlan w{};
   w.tc = attn_tc_ok(dtype, a.dh);
