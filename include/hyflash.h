@@ -727,8 +727,8 @@ hf_status hf_rotary_table(int32_t dim, double base, const hf_rotary_scaling* sca
  *   q, q_out    [rows, *_ld] DEVICE: head h at columns [h*head_dim, (h+1)*head_dim);
  *               aligned to the type. n_q_heads = 0: NULL.
  *   k, k_out    the same of n_kv_heads; n_kv_heads = 0: NULL.
- * q_out may be q and k_out k (with the same stride); they may not overlap otherwise. Heads
- * start on 16 bytes in the fast form; others are turned value by value. */
+ * q_out may be q and k_out k (with the same stride); they may not overlap otherwise. Fastest where
+ * dim/2, head_dim, the strides and the buffers are multiples of 16 bytes. */
 hf_status hf_rotary(int32_t dtype, int32_t interleaved, int32_t rows, int32_t n_q_heads,
                     int32_t n_kv_heads, int32_t head_dim, int32_t dim, const uint64_t* turns,
                     float attention, const int32_t* positions, const void* q, int64_t q_ld,

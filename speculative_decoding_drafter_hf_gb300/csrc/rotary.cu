@@ -31,39 +31,37 @@ struct RotaryArgs {
   int per, step;  // chunks of a head; every step-th head is the same thread's
 };
 
+// VE values of 2 to 16 bytes in all, at once.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<2> { using type = uint16_t; };
+
 template <typename T, int VE>
 __device__ __forceinline__ void load(const T* p, float* x) {
-  if constexpr (VE == 1) {
-    x[0] = to_f(*p);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-  } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  using W = typename Word<VE * sizeof(T)>::type;
+  const W w = *reinterpret_cast<const W*>(p);
+  const T* v = reinterpret_cast<const T*>(&w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
+  for (int i = 0; i < VE; ++i) x[i] = to_f(v[i]);
 }
 template <typename T, int VE>
 __device__ __forceinline__ void store(T* p, const float* x) {
-  if constexpr (VE == 1) {
-    *p = from_f<T>(x[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-    uint4 v;
-    __nv_bfloat162* y = reinterpret_cast<__nv_bfloat162*>(&v);
+  using W = typename Word<VE * sizeof(T)>::type;
+  W w;
+  T* v = reinterpret_cast<T*>(&w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = v;
-  }
+  for (int i = 0; i < VE; ++i) v[i] = from_f<T>(x[i]);
+  *reinterpret_cast<W*>(p) = w;
 }
 
-// VE: values of a load, or 1. A thread's chunk is two loads, halves: VE values of the first half
+// VE: values of a load. A thread's chunk is two loads, halves: VE values of the first half
 // and their partners; interleaved: 2 VE neighbours. Chunks behind dim are copied.
 template <typename T, int VE, bool INTER>
 __global__ void __launch_bounds__(RT) rotary_kernel(RotaryArgs a) {
@@ -126,19 +124,27 @@ hf_status refuse(const char* m) {
   return HF_EINVAL;
 }
 
-template <typename T>
-cudaError_t launch(RotaryArgs a, bool inter, bool wide, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  const int ve = wide ? V : 1, H = a.hq + a.hkv;
-  a.per = a.dim / 2 / ve + ((a.dh - a.dim) / ve + 1) / 2;
+template <typename T, int VE>
+cudaError_t launch_wide(RotaryArgs a, bool inter, cudaStream_t st) {
+  const int H = a.hq + a.hkv;
+  a.per = a.dim / 2 / VE + ((a.dh - a.dim) / VE + 1) / 2;
   // threads enough to fill the GPU four times, then heads one after the other (26005 tokens of 40 heads of 128 89.4
   // us, 5.96 TB/s; threads for once 93.8; four heads at a time 127: more registers, fewer threads)
   const long long cells = (long long)a.rows * a.per;
   a.step = (int)std::max<long long>(1, std::min<long long>(H, (152LL * 8192 + cells - 1) / cells));
   const long long grid = std::min<long long>((cells * a.step + RT - 1) / RT, 1 << 20);
-  auto* kern = wide ? (inter ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>)
-                    : (inter ? rotary_kernel<T, 1, true> : rotary_kernel<T, 1, false>);
-  return launch_pdl(kern, dim3((unsigned)grid), dim3(RT), 0, st, a);
+  return launch_pdl(inter ? rotary_kernel<T, VE, true> : rotary_kernel<T, VE, false>, dim3((unsigned)grid), dim3(RT), 0, st, a);
+}
+
+// As many values a load as the pairs' halves, the heads and their places allow (`align` bytes of them).
+template <typename T>
+cudaError_t launch(const RotaryArgs& a, bool inter, int align, cudaStream_t st) {
+  auto fits = [&](int ve) { return align % (ve * (int)sizeof(T)) == 0 && a.dim / 2 % ve == 0 && a.dh % ve == 0; };
+  if constexpr (sizeof(T) == 2)
+    if (fits(8)) return launch_wide<T, 8>(a, inter, st);
+  if (fits(4)) return launch_wide<T, 4>(a, inter, st);
+  if (fits(2)) return launch_wide<T, 2>(a, inter, st);
+  return launch_wide<T, 1>(a, inter, st);
 }
 
 }  // namespace
@@ -211,7 +217,7 @@ extern "C" hf_status hf_rotary(int32_t dtype, int32_t interleaved, int32_t rows,
   const int esize = dtype == HF_F32 ? 4 : 2;
   auto off = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
   if (off(turns, 8) || off(positions, 4)) return refuse("turns must be 8-byte, positions 4-byte aligned");
-  bool wide = head_dim * esize % 16 == 0 && dim / 2 * esize % 16 == 0;
+  uintptr_t places = 16;  // bits of all that has to be divisible
   for (int i = 0; i < 4; ++i) {
     const void* p = i == 0 ? q : i == 1 ? q_out : i == 2 ? k : k_out;
     const int64_t ld = i == 0 ? q_ld : i == 1 ? q_out_ld : i == 2 ? k_ld : k_out_ld;
@@ -219,7 +225,7 @@ extern "C" hf_status hf_rotary(int32_t dtype, int32_t interleaved, int32_t rows,
     if (least == 0) continue;
     if (ld < least || ld > (1LL << 36)) return refuse("a row stride is smaller than heads * head_dim, or above 2^36");
     if (off(p, esize)) return refuse("q, k and their outputs must be aligned to their type");
-    wide = wide && !off(p, 16) && ld * esize % 16 == 0;
+    places |= reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * esize);
   }
   RotaryArgs a{};
   a.q = static_cast<const uint8_t*>(q);
@@ -239,8 +245,9 @@ extern "C" hf_status hf_rotary(int32_t dtype, int32_t interleaved, int32_t rows,
   a.dh = head_dim;
   a.dim = dim;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = dtype == HF_F32 ? launch<float>(a, interleaved, wide, st)
-                                        : launch<__nv_bfloat16>(a, interleaved, wide, st);
+  const int align = (int)(places & (~places + 1));  // the largest power of two that divides them, 16 at most
+  const cudaError_t e = dtype == HF_F32 ? launch<float>(a, interleaved, align, st)
+                                        : launch<__nv_bfloat16>(a, interleaved, align, st);
   if (e == cudaSuccess) return HF_OK;
   set_thread_error(cudaGetErrorString(e));
   return HF_ECUDA;

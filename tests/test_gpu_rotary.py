@@ -31,6 +31,8 @@ def _randn(shape, dtype, seed):
 @pytest.mark.parametrize("dtype,T,hq,hkv,dh,dim", [
     ("bf16", 1, 32, 8, 128, 128), ("bf16", 37, 5, 1, 128, 64), ("f32", 13, 4, 2, 64, 48), ("f32", 3, 1, 1, 6, 2),
     ("bf16", 2, 3, 3, 80, 50), ("bf16", 700, 2, 1, 256, 256), ("f32", 9, 7, 2, 33, 20), ("bf16", 5, 2, 2, 72, 8),
+    ("bf16", 11, 4, 1, 128, 24), ("bf16", 3, 2, 2, 64, 60), ("bf16", 6, 1, 3, 64, 40), ("f32", 4, 2, 1, 64, 12), ("f32", 4, 2, 1, 64, 10),
+    ("bf16", 4, 2, 1, 36, 16), ("bf16", 4, 2, 1, 34, 32), ("f32", 3, 1, 2, 258 // 2 + 1, 4), ("bf16", 3, 5, 1, 127, 126),
 ])
 def test_layouts_and_sizes(hf, dtype, T, hq, hkv, dh, dim, interleaved):
     x = _randn((T, hq + hkv + 1, dh), dtype, T)
