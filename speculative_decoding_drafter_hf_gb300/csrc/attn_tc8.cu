@@ -356,13 +356,15 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
   for (int j = 0; j < mine; ++j) {
     const int jt = j0 + j * BN, key = jt + row;
     const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j), vs = vi % NS, turn = vi / NS;  // V's place
+    fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
+    // (behind the wait for the scores: all tiles before this one have been worked on by then. A group that had no part
+    // in the item before would else come several turns of the ring early, where a parity says nothing)
     fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)turn & 1u);
+    tc_fence_after();
     const float* sc = G.sc + (vs + (streams == 1 ? 0 : r)) * 32 + (row >> shift);
     const float ks = held_scale(sc[0]), vscale = held_scale(sc[16]);
     const float lv = (float)((__float_as_int(vscale) >> 23) - 127), rv = 1.f / vscale;
     const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), rv2 = pair(rv, rv), fine2 = pair(1.f / kFine, 1.f / kFine);
-    fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
-    tc_fence_after();
     const bool cut = jt + BN > min(it.low, j1);
     uint8_t* w = G.sW + row * 16;
     // 32 rows at a time: the exponents of more do not fit the registers beside the sums
