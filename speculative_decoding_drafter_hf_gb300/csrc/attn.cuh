@@ -235,6 +235,9 @@ __device__ __forceinline__ void check_offsets(const AttnRows& a, int tid, int th
 // Tensor-core variants (attn_tc.cu; an 8-bit cache: attn_tc8.cu), where attn_tc_ok.
 bool attn_tc_ok(int dtype, int dh);
 constexpr int kTileRows = 128, kTileRows8 = 64;
+// Rows of a row tile over an 8-bit cache: as many as TMEM holds the scores and sums of two row tiles for; more only where a
+// KV head has more heads.
+inline int tile_rows8(int G) { return G > 48 ? kTileRows8 : 48; }
 constexpr int kSmall = 256;    // entries of a call that every CTA plans for itself
 // busy: CTAs of a launch just before it (attn_tc_pages of a dense prefix) that this one runs beside, each as long
 // as `places` of an entry's; 0: it waits for that launch.

@@ -757,9 +757,22 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   const size_t N = (size_t)a.n * a.rows * a.Hq;
   size_t rows;
   const long long shared_rows = (long long)a.n * a.rows * a.G;
-  w.dense = w.tc && a.tile == kTileRows8 && shared_rows > kDenseRows && shared_rows * a.shared > kDenseWork;
+  const bool e4m3 = a.tile != kTileRows;
+  w.dense = w.tc && e4m3 && shared_rows > kDenseRows && shared_rows * a.shared > kDenseWork;
   if (w.tc) {
-    if (a.tile == kTileRows8 && (w.dense || a.shared == 0)) a.item_start = kItemStart8;
+    if (e4m3) {
+      // rows that need two tiles and more are spread evenly over them (32 x 16 rows of 4
+      // heads over 4096 tokens 118 us, as 48 and 16 rows 157);
+      // an entry's own as well, or all in one tile
+      const long long most = a.tile / a.G;
+      auto even = [&](long long tokens) {
+        const long long pairs = (tokens + 2 * most - 1) / (2 * most);
+        return tokens <= most ? tokens : (tokens + 2 * pairs - 1) / (2 * pairs);
+      };
+      const long long own = even(a.rows), all = w.dense || a.shared == 0 ? own : even((long long)a.n * a.rows);
+      a.tile = (int)std::max(own, all) * a.G;
+    }
+    if (e4m3 && (w.dense || a.shared == 0)) a.item_start = kItemStart8;
     long long slots;
     int pre = 0;
     if (w.dense) {
@@ -812,6 +825,7 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
   if (rows < 1 || rows > 64) return "rows must be 1..64";
   if (shared < 0 || shared % p->page || shared > (long long)p->table_ld * p->page)
     return "shared must be a multiple of page, at most table_ld * page";
+  // (places and units of a line are int: with row tiles of 48 rows there are up to 1.3 times as many as counted here)
   if ((long long)n * rows * hq > 0x7fffffffLL / 4 ||
       ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart8) * n * ((long long)rows * hq / (c.e4m3 ? kTileRows8 : kTileRows) + p->n_kv_heads) > 0x3fffffffLL)
     return "n * rows * n_q_heads, or that times the table's reach, is too large";
@@ -820,7 +834,7 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
   a.G = hq / p->n_kv_heads;
   a.dh = p->head_dim;
   a.esize = pages_esize(c.dtype);
-  a.tile = c.e4m3 ? kTileRows8 : kTileRows;
+  a.tile = c.e4m3 ? tile_rows8(a.G) : kTileRows;
   a.item_start = kItemStart;
   a.table = p->table;
   a.lens = p->lens;

@@ -9,31 +9,36 @@
 // so that a tile's work goes by its rows (4 of a decoded token, 32 of 8 verified ones) and not by 128, and
 // a softmax thread has a key: one scale of K, one of V, one position to compare, for all rows.
 //
-// Rows and weights have more bits than a code: each goes in as two codes, hi = its nearest, lo = the
+// Rows and weights have more bits than a code. A row goes in as two codes, hi = its nearest, lo = the
 // nearest of 16 times the rest, side by side as columns of one product; of the two columns of the result the
-// second counts a sixteenth. That is 8 bits and more: a bf16 row exactly, down to 2^-22 of its
-// largest value; a weight to 2^-8, or 2^-15 of the largest one. Sums, maxima and TMEM are fp32.
+// second counts a sixteenth: a bf16 row exactly, down to 2^-22 of its largest value.
 //
-// M_i is set by an item's first tile, to where the largest weight is 2^1, and raised to there when one
-// passes 2^8: that needs the maximum over the 128 threads, so most tiles only vote on it. The sum of p_ij
-// is kept per thread, as w_ij / vs_j, and joined at an item's end.
+// A weight goes in as three e5m2 codes of 3 bits, each 8 times finer than the one before:
+// 9 bits down to 2^-14, and what is below 2^-23 is lost. The room below the largest weight matters: where
+// one key holds most of a row's sum, the others' weights, though thousands of them make up the output, are
+// 2^-10 to 2^-25 of it (two e4m3 codes, which end at 2^-15 of the largest weight, were off by 0.03 to 0.6 of such
+// outputs; V as 16-bit floats in shared memory against 16-bit weights is exact as well, but moves four times
+// V's bytes through it: 64 x 1 row over 4096 tokens 106 us). M_i is set by an item's first tile, to where the largest weight
+// is 2^8, and raised to there when one passes 2^15 (that needs the maximum over the 128 threads, so most tiles only vote on
+// it): weights keep 9 bits down to 2^-22 of the item's largest one at least, and end at 2^-31 of it. Sums, maxima and TMEM are
+// fp32; the sum of p_ij is kept per thread, as w_ij / vs_j before it is rounded, and joined at an item's end.
 //
 // The CTA's warps, items, the line of own tiles and the parts are those of attn_tc.cu: warp 0 loads
 // (TMA; the scales by 4-byte copies beside V's pages), warp 1 issues the products, warp 2 hands out
-// items, warps 4-7 and 8-11 are the softmax groups of two row tiles of up to 64 rows. While an item is worked
+// items, warps 4-7 and 8-11 are the softmax groups of two row tiles of up to 48 rows (heads of more than 48 to a KV
+// head: 64, whose scores share TMEM, so that the groups take turns). While an item is worked
 // on, warp 3 turns the next one's rows into codes, if a row tile has 16 at most (one warp took longer than
 // an item for more: 64 x 8 rows over 4096 tokens 136 us), or fetches them, if 32; else the groups do it when they
 // come to it. Row tiles of two KV heads read pages that lie side by
 // side: one copy brings both, eight rows of one, eight of the other (4 KB for a page of 16 tokens; 64 x 1
-// rows over 4096 tokens with such pages 105 us instead of 125, and 94 now).
+// rows over 4096 tokens with such pages 105 us instead of 125, and 96 now).
 //
 // Bound by the reads where requests are long: 64 requests of 2048 to 32768 tokens, one row of 40 heads over 10 each,
-// 278 us (6.8 TB/s, as a copy; tensor pipe 9%). Shorter ones by what an item costs beside its
+// 282 us (6.7 TB/s, as a copy). Shorter ones by what an item costs beside its
 // tiles (about 17000 cycles for 32 rows, 8000 for 5: codes, waits, joining the sums, storing; the first of a CTA twice
-// that, as its instructions come from the L2) and tiles by their chain (about 3000 cycles of two row tiles of
-// 32 rows: 64 x 8 rows over 4096 tokens 114 us, 4.8 TB/s; of 64 rows 5500). Heads of 64, 64 x 1 rows over 4096
-// tokens: 65 us (4.1 TB/s), where the copies' rows of 64 bytes seem to bound it: neither a longer ring, nor a second
-// loading warp made it faster.
+// that, as its instructions come from the L2) and tiles by their chain (64 x 8 rows over 4096 tokens 119 us, 4.6
+// TB/s; 4 us of them for the third code of a weight). Heads of 64, 64 x 1 rows over 4096 tokens: 74 us (3.6 TB/s), 65 with two
+// codes; there neither a longer ring, nor a second loading warp made it faster.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -44,9 +49,9 @@
 namespace hf {
 namespace {
 
-constexpr int NR = kTileRows8;  // rows of a row tile
-constexpr float kLift = 8.f, kLifted = 1.f;
-constexpr float kFine = 16.f;  // lo is held times this
+constexpr float kLift = 15.f, kLifted = 8.f;
+constexpr float kFine = 16.f;       // a row's lo is held times this
+constexpr float kFinerW = 8.f;      // a weight's second code times this, its third times the square
 
 constexpr int kItems = 160;  // bytes of two items: what comes behind them starts on 16 bytes
 static_assert(2 * sizeof(Item) <= kItems, "item slots");
@@ -54,12 +59,17 @@ static_assert(2 * sizeof(Item) <= kItems, "item slots");
 // NM: sixteens of rows of the largest row tile.
 template <int DH, int NM>
 struct Tc8 {
+  static constexpr int NR = NM * 16;                  // rows of a row tile
   static constexpr int TILE = BN * DH;                // bytes of a K or V tile
   static constexpr int Q = 2 * NM * 16 * DH;          // bytes of a row tile's codes
   static constexpr bool AHEAD = NM == 1;              // warp 3 makes the codes, of two items at a time
   static constexpr int QN = AHEAD ? 2 : 1;
   static constexpr int RAW = NM == 2 ? 2 * 32 * DH * 2 : 0;  // rows as warp 3 fetches them
-  static constexpr int W = BN * 2 * NM * 16;          // bytes of a tile's weights
+  static constexpr int W = BN * 3 * NM * 16;          // bytes of a tile's weights
+  // TMEM: the scores and the sums of both row tiles; of four sixteens the scores of one at a time
+  static constexpr bool TURNS = NM == 4;
+  static constexpr int S_COL = 2 * NM * 16, O_COL = TURNS ? S_COL : 2 * S_COL, O_STEP = 3 * NM * 16;
+  static_assert(O_COL + 2 * O_STEP <= 512, "TMEM");
   static constexpr size_t small(int slots) {          // what comes behind the tiles
     return (size_t)(2 * slots + 16) * 8 + kItems + 16 + slots * 32 * 4 + 4 * NR * 16 + 2 * NR * 16 + (2 * kSmall + 2) * 4;
   }
@@ -90,10 +100,10 @@ __device__ __forceinline__ uint32_t desc_keys(uint32_t addr) { return ((addr >> 
 __device__ __forceinline__ uint32_t desc_values(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((512u >> 4) << 16); }
 __device__ __forceinline__ uint32_t desc_weights(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((128u >> 4) << 16); }
 
-// e4m3 x e4m3 -> fp32, 128 x n; bits 15, 16: A, B across their rows.
-__device__ __forceinline__ uint32_t idesc_e4m3(int n, uint32_t across) {
-  return (1u << 4) | across | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
+// e4m3 x e4m3 -> fp32, 128 x n, along the bytes of both.
+__device__ __forceinline__ uint32_t idesc_scores(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
+// e4m3 x e5m2 (bit 10) -> fp32, 128 x n, across the rows of both (bits 15, 16).
+__device__ __forceinline__ uint32_t idesc_values(int n) { return idesc_scores(n) | (1u << 10) | (3u << 15); }
 
 __device__ __forceinline__ void mma8(uint32_t lead, uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
                                      uint32_t idesc, uint32_t acc) {
@@ -173,6 +183,31 @@ __device__ __forceinline__ void split_codes(float x, float y, uint32_t& hi, uint
   lo = r;
 }
 
+// Four weights (0 .. 2^15) as three e5m2 codes each, w = a + b / 8 + c / 64 to 9 bits. An e5m2 code is the upper byte of
+// a 16-bit float: w as one (11 bits), cut after its upper byte, leaves 8 bits, those cut again 5, exactly; the last
+// code is rounded. (NaN may become anything: the sum of a row that has one is NaN.)
+__device__ __forceinline__ void split_weights(const float* w, uint32_t& a, uint32_t& b, uint32_t& c) {
+  uint32_t x[2], y[2], z[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("{\n\t.reg .b32 e, t;\n\t"
+        "mov.b32 e, 0x48004800;\n\t"         // 8
+        "cvt.rn.f16x2.f32 %0, %4, %3;\n\t"
+        "and.b32 t, %0, 0xff00ff00;\n\t"
+        "sub.rn.f16x2 t, %0, t;\n\t"
+        "mul.rn.f16x2 %1, t, e;\n\t"
+        "and.b32 t, %1, 0xff00ff00;\n\t"
+        "sub.rn.f16x2 t, %1, t;\n\t"
+        "mul.rn.f16x2 t, t, e;\n\t"
+        "add.u32 %2, t, 0x00800080;\n\t}\n"
+        : "=&r"(x[i]), "=&r"(y[i]), "=&r"(z[i])
+        : "f"(w[2 * i]), "f"(w[2 * i + 1]));
+  }
+  a = __byte_perm(x[0], x[1], 0x7531);
+  b = __byte_perm(y[0], y[1], 0x7531);
+  c = __byte_perm(z[0], z[1], 0x7531);
+}
+
 __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int head, int page) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -182,15 +217,19 @@ __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map,
 }
 
 // What a softmax group has in shared memory for its row tile's rows.
+template <int NR>
 struct GroupRows {
   float4 cm[NR / 2];  // two rows' factors of the scores (base 2), and their -M
   int lim[NR];        // keys below it are seen
   float red[NR];      // maxima, sums or factors being joined
 };
-__device__ __forceinline__ float& row_factor(GroupRows& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + (n & 1)]; }
-__device__ __forceinline__ float& row_minus_m(GroupRows& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + 2 + (n & 1)]; }
-static_assert(sizeof(GroupRows) == NR * 16, "size in Tc8::smem");
+template <int NR>
+__device__ __forceinline__ float& row_factor(GroupRows<NR>& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + (n & 1)]; }
+template <int NR>
+__device__ __forceinline__ float& row_minus_m(GroupRows<NR>& R, int n) { return reinterpret_cast<float*>(R.cm)[(n >> 1) * 4 + 2 + (n & 1)]; }
+static_assert(sizeof(GroupRows<64>) == 64 * 16, "size in Tc8::smem");
 
+template <int NR>
 struct Group {
   const TcArgs& c;
   Item& it;
@@ -198,7 +237,7 @@ struct Group {
   uint8_t* sW;
   uint64_t* full;
   const float* sc;  // [slot][K, V][page of the tile]
-  GroupRows* rows;
+  GroupRows<NR>* rows;
   float* red;       // [4][NR]
   uint32_t b_s, b_o;
   uint64_t* p_full;
@@ -249,9 +288,9 @@ __device__ __forceinline__ int tile_tokens(const TcArgs& c, const Item& it, int 
 
 // The rows of row tile r of an item as codes, their factors and limits, by T threads. N: rows of a row tile; rows
 // without a token have no codes, and a factor of zero. raw: the rows in shared memory, or NULL: where they lie.
-template <int DH, int N, int T>
+template <int DH, int N, int T, int NR>
 __device__ __forceinline__ void make_rows(const TcArgs& c, const Item& it, int r, uint8_t* to, const uint8_t* raw,
-                                          GroupRows& R, const int* s_eff, int tid) {
+                                          GroupRows<NR>& R, const int* s_eff, int tid) {
   const AttnRows& a = c.a;
   const ByGroup token_of(a.G);
   constexpr int PER = DH / 8, WIDE = T / PER;  // threads of a row, 8 values each; rows at a time
@@ -337,15 +376,15 @@ __device__ __forceinline__ void fetch_rows(const TcArgs& c, const Item& it, uint
 
 // An item's softmax by one group, its rows in NC sixteens. tiles: key tiles of this group so far;
 // ring: tiles of the ring so far; fail: a wait has run out in this warp. False: a wait ran out (the same answer in all of the group's threads).
-template <int DH, int NC, int NS>
-__device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, bool fail) {
+template <int DH, int NC, int NS, int NR>
+__device__ __forceinline__ bool soft_item(const Group<NR>& G, int tiles, int ring, bool fail) {
   constexpr int N = NC * 16, TILE = BN * DH;
   const AttnRows& a = G.c.a;
   Item& it = G.it;
   const int r = G.r, lane = G.lane, row = G.quad * 32 + lane;
   const int split = it.split, mine = it.nt[r], j0 = it.j0, j1 = it.j1, g = it.g + (split ? r : 0);
   const int tl0 = split ? 0 : r * G.c.tb;  // first token within the item
-  GroupRows& R = *G.rows;
+  GroupRows<NR>& R = *G.rows;
   const ByGroup token_of(a.G);
 
   const int streams = split && it.nt[1] > 0 ? 2 : 1, look = it.first_cut();
@@ -356,15 +395,16 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
   for (int j = 0; j < mine; ++j) {
     const int jt = j0 + j * BN, key = jt + row;
     const int vi = ring + (streams == 1 ? 1 + 2 * j : 2 + 4 * j), vs = vi % NS, turn = vi / NS;  // V's place
-    fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
-    // (behind the wait for the scores: all tiles before this one have been worked on by then. A group that had no part
-    // in the item before would else come several turns of the ring early, where a parity says nothing)
+    // The scales of an item's first tile behind its scores: all tiles before this one have been worked on by then. A group
+    // that had no part in the item before would else come several turns of the ring early, where a parity says nothing.
+    if (j == 0) fail = fail || !wait_uniform(G.b_s, (uint32_t)tiles & 1u);
     fail = fail || !wait_uniform(smem_u32(&G.full[vs]), (uint32_t)turn & 1u);
-    tc_fence_after();
     const float* sc = G.sc + (vs + (streams == 1 ? 0 : r)) * 32 + (row >> shift);
     const float ks = held_scale(sc[0]), vscale = held_scale(sc[16]);
     const float lv = (float)((__float_as_int(vscale) >> 23) - 127), rv = 1.f / vscale;
     const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), rv2 = pair(rv, rv), fine2 = pair(1.f / kFine, 1.f / kFine);
+    if (j > 0) fail = fail || !wait_uniform(G.b_s, (uint32_t)(tiles + j) & 1u);
+    tc_fence_after();
     const bool cut = jt + BN > min(it.low, j1);
     uint8_t* w = G.sW + row * 16;
     // 32 rows at a time: the exponents of more do not fit the registers beside the sums
@@ -441,7 +481,7 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
             for (int n = 0; n < 16; ++n) same = same && factor[n] == 1.f;
             if (same) continue;
 #pragma unroll 1
-            for (int h = h0 + i; h < 2 * NC; h += NC) {
+            for (int h = h0 + i; h < 3 * NC; h += NC) {
               float o[16];
               tmem_ld16_async(G.to + h * 16, o);
               tmem_wait_ld();
@@ -466,22 +506,20 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
       for (int i = 0; i < HB; ++i) {
         if (i >= hb) continue;
         const int h = h0 + i;
-        uint32_t hi[4], lo[4];
+        uint32_t c0[4], c1[4], c2[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t hh[2], ll[2];
+          float x[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int n = q * 4 + k * 2;
-            const float x = ex2(z[i * 16 + n]), y = ex2(z[i * 16 + n + 1]);
-            l2[h * 8 + n / 2] = fma2(pair(x, y), rv2, l2[h * 8 + n / 2]);
-            split_codes(x, y, hh[k], ll[k]);
-          }
-          hi[q] = hh[0] | hh[1] << 16;
-          lo[q] = ll[0] | ll[1] << 16;
+          for (int k = 0; k < 4; ++k) x[k] = ex2(z[i * 16 + q * 4 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2)
+            l2[h * 8 + q * 2 + k / 2] = fma2(pair(x[k], x[k + 1]), rv2, l2[h * 8 + q * 2 + k / 2]);
+          split_weights(x, c0[q], c1[q], c2[q]);
         }
-        *reinterpret_cast<uint4*>(w + h * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(w + (NC + h) * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(w + h * 2048) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+        *reinterpret_cast<uint4*>(w + (NC + h) * 2048) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+        *reinterpret_cast<uint4*>(w + (2 * NC + h) * 2048) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
       }
     }
     if (j >= look) {
@@ -549,16 +587,18 @@ __device__ __forceinline__ bool soft_item(const Group& G, int tiles, int ring, b
   for (int h = 0; h < NC; ++h) {
     if (h * 16 >= heads) break;
     __syncwarp();
-    float o[16], t[16];
+    float o[16], t[16], u[16];
     if (mine > 0) {
       tmem_ld16_async(G.to + h * 16, o);
       tmem_ld16_async(G.to + N + h * 16, t);
+      tmem_ld16_async(G.to + 2 * N + h * 16, u);
       tmem_wait_ld();
       tmem_hold16(o);
       tmem_hold16(t);
+      tmem_hold16(u);
     }
 #pragma unroll
-    for (int n = 0; n < 16; ++n) o[n] = mine > 0 ? fmaf(t[n], 1.f / kFine, o[n]) : 0.f;
+    for (int n = 0; n < 16; ++n) o[n] = mine > 0 ? fmaf(fmaf(u[n], 1.f / kFinerW, t[n]), 1.f / kFinerW, o[n]) : 0.f;
     if (row >= DH) continue;
     if (from < j1) {
 #pragma unroll 1
@@ -599,7 +639,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
            const __grid_constant__ CUtensorMap mk2, const __grid_constant__ CUtensorMap mv2, const __grid_constant__ TcArgs c) {
   constexpr int NM = NO > NP ? NO : NP;
   using L = Tc8<DH, NM>;
-  constexpr int NS = L::SLOTS;
+  constexpr int NS = L::SLOTS, NR = L::NR;
   const AttnRows& a = c.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;                                        // [QN][2]
@@ -622,7 +662,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;  // tiles that the loader has asked for
   float* s_sc = reinterpret_cast<float*>(tmem_slot + 4);     // [NS][2][16]
-  GroupRows* s_rows = reinterpret_cast<GroupRows*>(s_sc + NS * 32);  // [2 items][2]
+  GroupRows<NR>* s_rows = reinterpret_cast<GroupRows<NR>*>(s_sc + NS * 32);  // [2 items][2]
   float* s_red = reinterpret_cast<float*>(s_rows + 4);       // [2][4][NR]
   int* s_eff = reinterpret_cast<int*>(s_red + 2 * 4 * NR);   // small calls: [kSmall] lengths, [kSmall + 1] places
   int* s_tile0 = s_eff + kSmall;
@@ -738,7 +778,8 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (!ok) *abort_flag = 1;
       }
     } else if (warp == 1) {
-      // ---- products: S_r(0), then V_r(j) W, S_r(j+1) for r = 0, 1 in turn
+      // ---- products: S_r(0), then V_r(j) W, S_r(j+1) for r = 0, 1 in turn; where the row tiles take turns with their
+      // scores, S_0(0), then S_1(j), V_0(j) W, V_1(j) W, S_0(j+1)
       const uint32_t lead = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t dq = desc_keys(smem_u32(sQ)), dk = desc_keys(smem_u32(sKV)), dv = desc_values(smem_u32(sKV)),
@@ -755,8 +796,8 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const int nt0 = __shfl_sync(0xffffffffu, it.nt[0], 0), nt1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
         const bool two = __shfl_sync(0xffffffffu, it.split, 0) && nt1 > 0;  // keys of two heads
         const int nt = max(nt0, nt1);
-        const int cols = 32 * (NP > 0 && __shfl_sync(0xffffffffu, it.kind, 0) == 1 ? NP : NO);
-        const uint32_t id_s = idesc_e4m3(cols, 0), id_o = idesc_e4m3(cols, 3u << 15);
+        const int cols = 16 * (NP > 0 && __shfl_sync(0xffffffffu, it.kind, 0) == 1 ? NP : NO);
+        const uint32_t id_s = idesc_scores(2 * cols), id_o = idesc_values(3 * cols);
         const uint32_t hi = two ? kHiPair<DH> : kHi<DH>, pair_r = two ? 8 * DH >> 4 : 0, groups = two ? 2 : 1;
         const uint32_t q = dq + (n % L::QN) * (2 * L::Q >> 4);
         auto next = [&]() {  // waits for the next tile
@@ -773,7 +814,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         auto score = [&](int r, int slot) {
 #pragma unroll
           for (int k = 0; k < DH / 32; ++k)
-            mma8(lead, tm + r * 128, dk + slot * (L::TILE >> 4) + r * pair_r + 2 * k, hi, q + r * (L::Q >> 4) + 2 * k, kHi<DH>,
+            mma8(lead, tm + (L::TURNS ? 0 : r * L::S_COL), dk + slot * (L::TILE >> 4) + r * pair_r + 2 * k, hi, q + r * (L::Q >> 4) + 2 * k, kHi<DH>,
                  id_s, k > 0);
           mma_commit(lead, b_s + 8 * r);
         };
@@ -789,36 +830,61 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           if (ok) {
             tc_fence_after();
             score(0, ks);
-            if (nt1 > 0) score(1, ks);
-            done(ks);
+            if (nt1 > 0 && !L::TURNS) score(1, ks);
+            if (nt1 == 0 || !L::TURNS) done(ks);
           }
           // from tile `look` on the softmax groups look V over before they hand their weights
           // on; where both have the tile, each looks at half of it
           const int look = __shfl_sync(0xffffffffu, it.first_cut(), 0);
+          auto weights = [&](int r) {  // waits for a row tile's weights
+            ok = ok && wait_uniform(b_p + 8 * r, pph[r]);
+            pph[r] ^= 1u;
+            if (ok) tc_fence_after();
+          };
+          auto values = [&](int r, int j) {
+#pragma unroll
+            for (int k = 0; k < BN / 32; ++k)
+              mma8(lead, tm + L::O_COL + r * L::O_STEP, dv + vs * (L::TILE >> 4) + r * pair_r + k * groups * (32 * DH >> 4), hi,
+                   dw + r * (L::W >> 4) + k * (512 >> 4), kHiW, id_o, j > 0 || k > 0);
+            mma_commit(lead, b_o + 8 * r);
+          };
           for (int j = 0; j < nt && ok; ++j) {
             const bool more = j + 1 < nt;
+            const int k0 = ks;
             vs = next();
             if (more) ks = next();
             const bool both = !two && j >= look && j < nt0 && j < nt1;
-            if (both) ok = ok && wait_uniform(b_p, pph[0]) && wait_uniform(b_p + 8, pph[1]);
+            if constexpr (L::TURNS) {
+              weights(0);
+              if (ok && nt1 > 0) {
+                score(1, k0);
+                done(k0);
+              }
+              if (both) weights(1);
+              if (ok) values(0, j);
+              if (nt1 > 0) {
+                if (!both) weights(1);
+                if (ok) values(1, j);
+              }
+              if (ok && more) score(0, ks);
+            } else {
+              if (both) {
+                weights(0);
+                weights(1);
+              }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int mine = r ? nt1 : nt0;
-              if (!ok || j >= mine) continue;
-              if (!both) ok = wait_uniform(b_p + 8 * r, pph[r]);
-              pph[r] ^= 1u;
-              if (!ok) continue;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < BN / 32; ++k)
-                mma8(lead, tm + 256 + r * 128, dv + vs * (L::TILE >> 4) + r * pair_r + k * groups * (32 * DH >> 4), hi,
-                     dw + r * (L::W >> 4) + k * (512 >> 4), kHiW, id_o, j > 0 || k > 0);
-              mma_commit(lead, b_o + 8 * r);
-              if (j + 1 < mine) score(r, ks);
+              for (int r = 0; r < 2; ++r) {
+                const int mine = r ? nt1 : nt0;
+                if (!ok || j >= mine) continue;
+                if (!both) weights(r);
+                if (!ok) continue;
+                values(r, j);
+                if (j + 1 < mine) score(r, ks);
+              }
             }
             if (ok) {
               done(vs);
-              if (more) done(ks);
+              if (more && (!L::TURNS || nt1 == 0)) done(ks);
             }
           }
         }
@@ -916,9 +982,9 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       const bool two = it.split && it.nt[1] > 0;
       const int nt = max(it.nt[0], it.nt[1]);
       if (two) ring += ring & 1;
-      const Group G{c, it, sKV, sW + r * L::W, full, s_sc, s_rows + 2 * (n & 1) + r, s_red + r * 4 * NR,
+      const Group<NR> G{c, it, sKV, sW + r * L::W, full, s_sc, s_rows + 2 * (n & 1) + r, s_red + r * 4 * NR,
                     smem_u32(&s_full[r]), smem_u32(&o_full[r]), &p_full[r],
-                    tmem + lanes + r * 128, tmem + lanes + 256 + r * 128, r, quad, lane, s_eff};
+                    tmem + lanes + (L::TURNS ? 0 : r * L::S_COL), tmem + lanes + L::O_COL + r * L::O_STEP, r, quad, lane, s_eff};
       bool fail = false;
       if constexpr (L::AHEAD) {
         fail = !wait_uniform(smem_u32(&r_full[n & 1]), (uint32_t)(n >> 1) & 1u);
@@ -926,7 +992,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         // (the codes of the item before have been read: its last scores came to this group)
         const uint8_t* raw = L::RAW ? sRaw + r * (L::RAW / 2) : nullptr;
         if (L::RAW) fail = !wait_uniform(smem_u32(f_full), (uint32_t)n & 1u);
-        GroupRows& R = s_rows[2 * (n & 1) + r];
+        GroupRows<NR>& R = s_rows[2 * (n & 1) + r];
         if (NP > 0 && it.kind == 1)
           make_rows<DH, NP == 0 ? 16 : NP * 16, 128>(c, it, r, sQ + r * L::Q, raw, R, s_eff, tid & 127);
         else
@@ -1018,8 +1084,8 @@ cudaError_t launch_one(const TcArgs& c, const CUtensorMap* m, dim3 grid, cudaStr
   return launch_pdl(tc8_kernel<DH, NO, NP>, grid, dim3(TCT), L::smem(), st, m[0], m[1], m[2], m[3], c);
 }
 
-// By the rows of a row tile, of an entry and of the prefix (at least as many): 1, 2, 3, 4 sixteens, and none, 1, 2 or 4.
-// (4 x 2 rows of 4 heads over 8192 tokens, all: 23.1 us with two sixteens for the prefix, 26.4 with four.)
+// By the rows of a row tile, of an entry and of the prefix (at least as many): 1, 2, 3, 4 sixteens, and none or these.
+// (4 x 2 rows of 4 heads over 8192 tokens, all: 23.9 us with two sixteens for the prefix, 25.8 with three.)
 template <int DH>
 cudaError_t launch_rows(const TcArgs& c, const CUtensorMap* m, dim3 grid, cudaStream_t st) {
   const auto sixteens = [&](long long tokens) { return (int)((std::min<long long>(tokens, c.tb) * c.a.G + 15) / 16); };
@@ -1029,12 +1095,12 @@ cudaError_t launch_rows(const TcArgs& c, const CUtensorMap* m, dim3 grid, cudaSt
       if (pre == 0) return launch_one<DH, 1, 0>(c, m, grid, st);
       if (pre == 1) return launch_one<DH, 1, 1>(c, m, grid, st);
       if (pre == 2) return launch_one<DH, 1, 2>(c, m, grid, st);
-      return launch_one<DH, 1, 4>(c, m, grid, st);
+      return launch_one<DH, 1, 3>(c, m, grid, st);
     case 2:
       if (pre == 0) return launch_one<DH, 2, 0>(c, m, grid, st);
       if (pre == 2) return launch_one<DH, 2, 2>(c, m, grid, st);
-      return launch_one<DH, 2, 4>(c, m, grid, st);
-    case 3: return pre == 0 ? launch_one<DH, 3, 0>(c, m, grid, st) : launch_one<DH, 3, 4>(c, m, grid, st);
+      return launch_one<DH, 2, 3>(c, m, grid, st);
+    case 3: return pre == 0 ? launch_one<DH, 3, 0>(c, m, grid, st) : launch_one<DH, 3, 3>(c, m, grid, st);
     default: return pre == 0 ? launch_one<DH, 4, 0>(c, m, grid, st) : launch_one<DH, 4, 4>(c, m, grid, st);
   }
 }
