@@ -728,7 +728,7 @@ void plan_pieces(AttnRows& a) {
   auto split = [](long long keys, long long tiles, int& count, int& each) {
     const long long want = (152 * 8 + tiles - 1) / std::max<long long>(tiles, 1);
     const long long c = std::max<long long>(1, std::min<long long>({want, (keys + BN - 1) / BN, 64}));
-    each = (int)(((keys + c - 1) / c + BN - 1) / BN * BN);
+    each = (int)std::max<long long>(((keys + c - 1) / c + BN - 1) / BN * BN, BN);  // (no keys: no pieces)
     count = (int)((keys + each - 1) / each);
   };
   const int bm = 8 * paged_rpt(a);
