@@ -827,7 +827,7 @@ const char* pages_args(const AnyPages& c, bool buffers, int n, int rows, int hq,
     return "shared must be a multiple of page, at most table_ld * page";
   // (places and units of a line are int: with row tiles of 48 rows there are up to 1.3 times as many as counted here)
   if ((long long)n * rows * hq > 0x7fffffffLL / 4 ||
-      ((long long)p->table_ld * p->page / kKeyTile + 1 + kItemStart8) * n * ((long long)rows * hq / (c.e4m3 ? kTileRows8 : kTileRows) + p->n_kv_heads) > 0x3fffffffLL)
+      ((long long)p->table_ld * p->page / kKeyTile + 1 + (c.e4m3 ? kItemStart8 : kItemStart)) * n * ((long long)rows * hq / (c.e4m3 ? kTileRows8 : kTileRows) + p->n_kv_heads) > 0x3fffffffLL)
     return "n * rows * n_q_heads, or that times the table's reach, is too large";
   a.Hq = hq;
   a.Hkv = p->n_kv_heads;
