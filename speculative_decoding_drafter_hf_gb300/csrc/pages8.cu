@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(CT, 4) write8_kernel(RowsArgs a) {
   }
 }
 
-// 2 KB of a page's codes (rows r0 .. r1 - 1 of them) to rows of values, by one warp.
-template <typename T>
+// 2 KB of a page's codes (rows r0 .. r1 - 1 of them) to rows of values, by one warp. ZERO: rows of zeros.
+template <typename T, bool ZERO = false>
 __device__ __forceinline__ void read_piece(const uint4* codes, const float* scale, uint8_t* rows, long long ld, int piece,
                                            int r0, int r1, int hv, Over over_hv, int shift, int vecs) {
   const int lane = threadIdx.x & 31;
@@ -331,7 +331,10 @@ __device__ __forceinline__ void read_piece(const uint4* codes, const float* scal
     const int i = piece * READ * 32 + k * 32 + lane, hr = over_hv(i), r = hr & ((1 << shift) - 1), h = hr >> shift;
     to[k] = i < vecs && r >= r0 && r < r1 ? rows + (long long)(r - r0) * ld + (size_t)(h * hv + i - hr * hv) * 16 * sizeof(T)
                                           : nullptr;
-    if (to[k]) {
+    if (ZERO) {
+      c[k] = make_uint4(0, 0, 0, 0);
+      s[k] = 0.f;
+    } else if (to[k]) {
       c[k] = __ldcg(codes + i);
       s[k] = __ldcg(&scale[h]);
     }
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(CT) read8_kernel(RowsArgs a) {
 }
 
 // The first tokens of entry 0 as rows of values, for products that many rows share (its pages that are out of
-// range are reported, their rows left as they are).
+// range are reported and read as zeros, as by the kernels that take codes).
 __global__ void __launch_bounds__(CT) prefix8_kernel(RowsArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -408,14 +411,15 @@ __global__ void __launch_bounds__(CT) prefix8_kernel(RowsArgs a) {
     const int piece = u % pieces, kv = u / pieces & 1, j = u / pieces / 2;
     const int id = __ldcg(&p.table[(size_t)r * p.table_ld + j]);  // (the table reaches that far, whatever the length)
     if (len < a.total || pages_of(len, p.page) > p.table_ld) return;
+    uint8_t* rows = (kv ? a.v : a.k) + (long long)j * p.page * a.ld;
     if (id < 0 || id >= p.n_pages) {
       if (lane == 0) pages_flag(p, HF_S_BAD);
+      read_piece<__nv_bfloat16, true>(nullptr, nullptr, rows, a.ld, piece, 0, p.page, hv, Over(hv), shift, vecs);
       continue;
     }
     const size_t block = ((size_t)a.layer * p.n_pages + id) * H;
     const uint4* codes = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v : p.k) + (block * dh << shift));
-    read_piece<__nv_bfloat16>(codes, (kv ? a.sc.v : a.sc.k) + block, (kv ? a.v : a.k) + (long long)j * p.page * a.ld, a.ld, piece, 0,
-                              p.page, hv, Over(hv), shift, vecs);
+    read_piece<__nv_bfloat16>(codes, (kv ? a.sc.v : a.sc.k) + block, rows, a.ld, piece, 0, p.page, hv, Over(hv), shift, vecs);
   }
 }
 
