@@ -63,8 +63,10 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-__device__ __forceinline__ float4 load4(const uint8_t* p, float scale) {
-  const uint32_t c = __ldcg(reinterpret_cast<const uint32_t*>(p));
+// Four codes (bits of x.x) times a scale (x.y): turned once all loads are under way.
+__device__ __forceinline__ float4 values4(const float4& x) {
+  const uint32_t c = __float_as_uint(x.x);
+  const float scale = held_scale(x.y);
   const float2 a = from_e4m3x2(c & 0xffff), b = from_e4m3x2(c >> 16);
   return make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale);
 }
@@ -174,7 +176,9 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all
         if constexpr (KV32)
           copy16(&to[j * ldq + c], src, at >= 0);
         else if constexpr (sizeof(KV) == 1)
-          x[u] = at >= 0 ? load4(src, __ldcg(&(kv ? a.v_scale : a.k_scale)[block])) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[u] = at >= 0 ? make_float4(__uint_as_float(__ldcg(reinterpret_cast<const uint32_t*>(src))),
+                                       __ldcg(&(kv ? a.v_scale : a.k_scale)[block]), 0.f, 0.f)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
         else
           x[u] = at >= 0 ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(RT) rows_kernel(AttnRows a, int pre_x, int all
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int e = e0 + u * RT;
+          if constexpr (sizeof(KV) == 1) x[u] = values4(x[u]);
           if (e < BN * c4) *reinterpret_cast<float4*>(&to[e / c4 * ldq + (e % c4) * 4]) = x[u];
         }
       }

@@ -21,7 +21,9 @@ __device__ __forceinline__ float scale_for(float top) {
 }
 // A scale as the cache holds it; what a page that nobody wrote holds counts as the least.
 __device__ __forceinline__ float held_scale(float s) {
-  return s >= pow2f(kScaleLow) && s <= pow2f(kScaleHigh) ? s : pow2f(kScaleLow);
+  // (positive floats are in the order of their bits; NaN and negative ones lie above)
+  const uint32_t low = (uint32_t)(kScaleLow + 127) << 23, high = (uint32_t)(kScaleHigh + 127) << 23;
+  return __float_as_uint(s) - low <= high - low ? s : pow2f(kScaleLow);
 }
 
 // Two values to codes, x in the lower byte: nearest, ties to even, magnitudes held to 448.

@@ -336,7 +336,7 @@ __device__ __forceinline__ void read_piece(const uint4* codes, const float* scal
       s[k] = 0.f;
     } else if (to[k]) {
       c[k] = __ldcg(codes + i);
-      s[k] = __ldcg(&scale[h]);
+      s[k] = held_scale(__ldcg(&scale[h]));
     }
   }
 #pragma unroll

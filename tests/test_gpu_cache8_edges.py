@@ -45,3 +45,27 @@ def test_a_page_of_the_prefix_out_of_range_reads_as_zeros(hf, n, rows):
         x.view(torch.uint8)[:, [table[0][3], table[0][40]]] = 0
     want, tol = _want(q, pool, table, lens, "bf16")
     R.check_attention(R.to64(out), want, tol)
+
+
+@pytest.mark.parametrize("dtype,dh,n,rows,shared", [("bf16", 128, 3, 2, 0), ("bf16", 128, 16, 8, 2304), ("bf16", 80, 3, 2, 32),
+                                                    ("f32", 64, 3, 2, 0)])
+def test_pages_without_a_scale_count_as_the_least(hf, dtype, dh, n, rows, shared):
+    """Scales that no write has set, whatever they are, by every kernel alike: reading back, codes, bf16 rows, CUDA cores."""
+    pool, table, lens, refs = _shared_cache(1, dh, 32, shared, [100] * n, 43)
+    for t in pool[2:]:
+        for p, x in ((table[0][0], float("nan")), (table[0][1], 0.0), (table[0][2], -1.0), (table[1][-2], float("inf")), (table[1][-3], 2.0 ** 64)):
+            t[:, p] = x
+    c = _on_gpu(hf, pool, table, lens, refs, dtype)
+    q = _randn((n, rows, 8, dh), dtype, 44)
+    out = c.attend(q.cuda(), shared=shared)
+    k, v = c.read(C.ints([0, 3]), C.ints([0, 90, 180]), C.ints([0, 1]), total=180)
+    for t in pool[2:]:
+        for p in (*table[0][:3], *table[1][-3:-1]):
+            t[:, p] = 2.0 ** -64
+    want, tol = _want(q, pool, table, lens, dtype)
+    R.check_attention(R.to64(out), want, tol)
+    for got, codes, scale in ((k, pool[0], pool[2]), (v, pool[1], pool[3])):
+        x = torch.from_numpy(C.values(codes, scale))[0, :, 0].to(got.dtype)  # [pages, page, dh]
+        rows0, rows1 = x[table[0]].reshape(-1, dh)[:90], x[table[1]].reshape(-1, dh)[3:93]
+        assert torch.equal(got[0, :, 0].cpu(), torch.cat((rows0, rows1)))
+    assert not c.check()
