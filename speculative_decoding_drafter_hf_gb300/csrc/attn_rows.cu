@@ -751,11 +751,13 @@ struct PagesPlan {
 };
 // Where very many rows share a long prefix, it is turned into bf16 rows once (a power of two as the scale:
 // exactly) and taken by the kernel for those, 256 rows at a time, instead of as codes, 64 or 128 at a time.
-// Whole calls in a graph, us, as rows / as codes, 8 KV heads: 192 rows of a head over 8192 tokens 55.5 / 49.2, 256
-// 57.3 / 53.3, 384 59.6 / 68.2, 512 69 / 82, 2048 133 / 235; over 2048 tokens 512 47.3 / 44.7, 768 49.9 / 52.4, 1024
-// 54.9 / 59.0.
-constexpr int kDenseRows = 320;
-constexpr long long kDenseWork = 5 << 18;  // rows of a head x tokens
+// Worth it by the work that it saves: KV heads x rows of a head, beyond what codes take as fast, x tokens. Whole calls
+// in a graph, us, as codes / as rows, heads of 128: 1 KV head, 384 rows of it over 8192 tokens 28 / 45, 1536 46 / 51, over 131072
+// 256 80 / 99, 384 133 / 112; 2, 768 over 8192 48 / 48, 1024 57 / 50; 4, 384 48 / 48, 512 56 / 49; 8, 192 48 / 56, 256 56 / 56,
+// 384 76 / 60, 1536 231 / 114, over 2048 512 48 / 48, 1024 86 / 63; 10, 256 62 / 65, 384 85 / 70. Heads of 64: 2, 512 over 8192 36 / 36;
+// 4, 256 36 / 34; 8, 192 44 / 39. (268 shapes: 1.7% behind the better of the two on average, 36% at most.)
+constexpr int kDenseRows = 180;
+constexpr long long kDenseWork = 10 << 20;
 PagesPlan plan_call(AttnRows& a, int dtype) {
   PagesPlan w{};
   w.tc = attn_tc_ok(dtype, a.dh);
@@ -763,7 +765,7 @@ PagesPlan plan_call(AttnRows& a, int dtype) {
   size_t rows;
   const long long shared_rows = (long long)a.n * a.rows * a.G;
   const bool e4m3 = a.tile != kTileRows;
-  w.dense = w.tc && e4m3 && shared_rows > kDenseRows && shared_rows * a.shared > kDenseWork;
+  w.dense = w.tc && e4m3 && a.Hkv * (shared_rows - kDenseRows) * a.shared > kDenseWork;
   if (w.tc) {
     if (e4m3) {
       // rows that need two tiles and more are spread evenly over them (32 x 16 rows of 4

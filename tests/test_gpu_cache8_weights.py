@@ -81,10 +81,10 @@ def test_a_key_that_holds_most_of_the_weight(hf, dh, keys, rows, place, share):
 
 
 @pytest.mark.parametrize("place", [3, 2000, 4096 - 300, 4096 - 20])
-@pytest.mark.parametrize("n,rows", [(24, 1), (24, 5), (64, 8)])
-def test_beside_a_shared_prefix(hf, n, rows, place):
-    """24 entries: the prefix as codes, in row tiles of 48 and 64 rows; 64: through bf16 rows."""
-    c, q, want, tol = _case(hf, 128, 4096, rows, n, place, 0.96)
+@pytest.mark.parametrize("n,rows,group", [(24, 1, 2), (24, 5, 2), (64, 8, 2), (64, 8, 4)])
+def test_beside_a_shared_prefix(hf, n, rows, group, place):
+    """48, 240 and 1024 rows of a head: the prefix as codes; 2048: through bf16 rows."""
+    c, q, want, tol = _case(hf, 128, 4096, rows, n, place, 0.96, group=group)
     out = R.to64(c.attend(q, shared=4096 - 256))
     for i in range(n):
         R.check_attention(out[i], want, tol, f"entry {i}")
