@@ -637,7 +637,8 @@ size_t hf_attention_pages_workspace(const hf_pages* p, int32_t n, int32_t rows,
  *     again where it grew); a page written from its first row starts anew.
  *   - codes are the nearest ones, ties to even; magnitudes above 448 2^63 become that.
  *   - infinities and NaN are held as NaN, and do not count for the scale.
- * Extending copies and compacting moves a page's scales with it. */
+ * Extending copies and compacting moves a page's scales with it. A scale outside 2^-64 .. 2^63, as a page that was
+ * never written may hold, counts as 2^-64. */
 typedef struct {
   hf_pages pages;  /* dtype HF_E4M3; k and v hold one byte an element; head_dim a multiple of 16 */
   float* k_scale;  /* [n_layers, n_pages, n_kv_heads] */
@@ -720,7 +721,8 @@ hf_status hf_rotary_table(int32_t dim, double base, const hf_rotary_scaling* sca
                           uint64_t* turns, float* attention);
 
 /* Turn the queries and keys of `rows` tokens. The angle is position * turns in 64-bit
- * integers, whole turns dropped: exact for every int32 position.
+ * integers, whole turns dropped: no error but the table's own, which is formed in 64-bit floating point
+ * (about 2^-55 of a turn for each position: 2^-24 turns at 2^31), and 2^-32 turns of the cut.
  *   dtype       HF_F32 or HF_BF16, of all four buffers.
  *   interleaved 0: pairs (i, i + dim/2); 1: (2i, 2i + 1).
  *   dim         even, 2 .. head_dim; head_dim <= 256.

@@ -239,8 +239,8 @@ constexpr int kTileRows = 128, kTileRows8 = 64;
 // KV head has more heads.
 inline int tile_rows8(int G) { return G > 48 ? kTileRows8 : 48; }
 constexpr int kSmall = 256;    // entries of a call that every CTA plans for itself
-// busy: CTAs of a launch just before it (attn_tc_pages of a dense prefix) that this one runs beside, each as long
-// as `places` of an entry's; 0: it waits for that launch.
+// busy: CTAs of the launch directly before it (attn_tc_pages of a dense prefix) that this one runs beside, each as long
+// as `places` of an entry's; 0: it waits for that launch. Not with more than kSmall entries: their plan would be between.
 cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, int busy, int places, cudaStream_t st);
 bool attn_gives_up();  // a test made every wait give up before it begins
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);

@@ -278,8 +278,8 @@ tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  // The launch behind a dense prefix does not wait for it: it comes once all CTAs are here, so when what ran
-  // before them has ended.
+  // The launch directly behind a dense prefix reads the cache and the rows before it waits (attn_tc8.cu, c.busy): it comes
+  // once all CTAs are here, so when what ran before them has ended and its writes are in memory. It relies on this order.
   if (beside) pdl_trigger();
   if (MODE == PROMPT && blockIdx.x == 0) check_offsets(a, tid, TCT);
   __syncwarp();  // (its lanes' loops end apart, and the next instruction wants the warp together)

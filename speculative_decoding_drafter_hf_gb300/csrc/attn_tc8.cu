@@ -698,7 +698,9 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (c.busy == 0) pdl_wait();  // (else: at the end)
+  // Beside a dense prefix the wait comes at the end: that launch, directly before this one, triggers behind its own wait
+  // only, when all launches before it have ended, and nothing that it writes is read here.
+  if (c.busy == 0) pdl_wait();
   __syncwarp();
 
   if (c.wait == 0) {

@@ -2,8 +2,10 @@
 //
 //   (a, b) -> f (a cos - b sin, b cos + a sin),  angle = position * w_i
 // w_i / (2 pi) is held in units of 2^-64 turns: the product with the position wraps at whole turns by
-// itself, so the reduced angle is right to 2^-32 turns for every position, where one formed in 32 bits
-// would be off by 0.06 at 10^6 and one in 64-bit floating point would wait for that unit.
+// itself and loses nothing but what is below 2^-32 turns, where an angle formed in 32 bits
+// would be off by 0.06 at 10^6 and one in 64-bit floating point would wait for that unit. The table's entries are 64-bit
+// floating-point results, good to about 2^-55 of a turn, so a position adds that often: 2^-32 turns at 2^23, 2^-24
+// at 2^31. The reduced angle is rounded to 24 bits for the functions.
 //
 // A thread holds the cosines and sines of its pairs and turns them in one head after the other.
 // Bound by the reads and writes where the rows are many (5.96 TB/s), by the launch where they are few (one

@@ -1,9 +1,12 @@
 """What the 8-bit cache and the calls beside it must answer without a GPU."""
 import ctypes
+import re
 
+import numpy as np
 import pytest
 
 from test_cache8_cpu import B, _cache  # noqa: F401
+from test_target_edges_cpu import _code
 
 
 def _plain_cache(B, **change):
@@ -31,3 +34,32 @@ def test_the_bf16_and_fp32_cache_take_as_many_entries_as_before(B, dtype):
 
     # (1 + 1) 2^20 (heads / 128 + heads) <= 2^30 - 1
     assert workspace(300) > 0 and workspace(508) > 0 and workspace(509) == 0
+
+
+def test_what_runs_beside_a_prefix_comes_behind_its_wait():
+    """The entries' own keys are read before that launch's wait: the launch directly before it triggers behind its own."""
+    prefix, own, calls = _code("attn_tc.cu"), _code("attn_tc8.cu"), _code("attn_rows.cu")
+    kernel = prefix[prefix.index("tc_kernel("):]
+    assert re.search(r"const bool beside = MODE == PAGED && a\.dense;\s*if \(!beside\) pdl_trigger\(\);", kernel)
+    assert re.search(r"pdl_wait\(\);\s*if \(beside\) pdl_trigger\(\);", kernel)
+    assert "if (c.busy == 0) pdl_wait();" in own and own.rindex("if (c.busy) pdl_wait();") > own.rindex("tmem_dealloc(tmem, 512)")
+    assert "const int busy = a.n <= kSmall &&" in calls and "if (!c.small) e = launch_attn_plan(" in own
+    assert re.search(r"launch_attn_tc_pages\(b, w\.pre_items, st\);\s*if \(e == cudaSuccess\) e = launch_attn_tc8_pages\(a, 0, busy", calls)
+
+
+def test_codes_of_weights_add_up():
+    """Every 16-bit float from 0 to 2^15 as three e5m2 codes, w = a + b / 8 + c / 64 to 2^-9 of it, or 2^-23: the steps of
+    split_weights (attn_tc8.cu)."""
+    bits = np.arange(0, 0x7801, dtype=np.uint16)
+    w, eight = bits.view(np.float16), np.float16(8)
+
+    def upper(x):
+        return (x.view(np.uint16) & np.uint16(0xff00)).view(np.float16)
+
+    a = upper(w)
+    rest = (w - a) * eight
+    b = upper(rest)
+    c = upper((((rest - b) * eight).view(np.uint16) + np.uint16(0x80)).view(np.float16))
+    total = a.astype(np.float64) + b.astype(np.float64) / 8 + c.astype(np.float64) / 64
+    assert np.isfinite(total).all()
+    assert (np.abs(total - w.astype(np.float64)) <= np.maximum(2.0 ** -9 * w.astype(np.float64), 2.0 ** -23)).all()
