@@ -677,9 +677,9 @@ hf_status hf_pages8_read(const hf_pages8* p, int32_t layer, int32_t layers, void
 
 /* hf_attention_pages over it: q and out are of type p->rows. HF_BF16 with head_dim 64 or 128: a row of q
  * enters the products with 8 bits a value, down to 2^-22 of its largest one; a weight (its probability
- * times the scale of V's page) with 9 bits down to 2^-22 of the row's largest weight, and with an error of 2^-31
- * of that below. The sum of the probabilities is not rounded, so what falls below 2^-31 is missing from the output alone: over a
- * million keys at most 2^-11 of the largest weight in all. A page of V whose scale is
+ * times the scale of V's page) with 9 bits down to 2^-24 of the row's largest weight, and with an error of 2^-33
+ * of that below. The sum of the probabilities is not rounded, so what falls below 2^-33 is missing from the output alone: over a
+ * million keys at most 2^-13 of the largest weight in all. A page of V whose scale is
  * more than 2^100 times smaller than another's that the row sees may lose its share of the
  * sum of the probabilities. A row of q that holds a value that is not finite gives NaN. */
 hf_status hf_attention_pages8(const hf_pages8* p, int32_t layer, int32_t n, int32_t rows,

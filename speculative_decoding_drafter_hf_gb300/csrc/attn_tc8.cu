@@ -19,9 +19,9 @@
 // 2^-10 to 2^-25 of it (two e4m3 codes, which end at 2^-15 of the largest weight, were off by 0.03 to 0.6 of such
 // outputs; V as 16-bit floats in shared memory against 16-bit weights is exact as well, but moves four times
 // V's bytes through it: 64 x 1 row over 4096 tokens 106 us). M_i is set by an item's first tile, to where the largest weight
-// is 2^8, and raised to there when one passes 2^15 (that needs the maximum over the 128 threads, so most tiles only vote on
-// it): weights keep 9 bits down to 2^-22 of the item's largest one at least, and end at 2^-31 of it. Sums, maxima and TMEM are
-// fp32; the sum of p_ij is kept per thread, as w_ij / vs_j before it is rounded, and joined at an item's end.
+// is 2^10, and raised to there when one passes 2^15 (that needs the maximum over the 128 threads, so most tiles only vote on
+// it; to 2^8 64 x 8 rows over 4096 tokens take 119 us, to 2^10 121, to 2^12 127): weights keep 9 bits down to 2^-24 of the item's
+// largest one at least, and end at 2^-33 of it. Sums, maxima and TMEM are fp32; the sum of p_ij is kept per thread, as w_ij / vs_j before it is rounded, and joined at an item's end.
 //
 // The CTA's warps, items, the line of own tiles and the parts are those of attn_tc.cu: warp 0 loads
 // (TMA; the scales by 4-byte copies beside V's pages), warp 1 issues the products, warp 2 hands out
@@ -34,9 +34,9 @@
 // rows over 4096 tokens with such pages 105 us instead of 125, and 96 now).
 //
 // Bound by the reads where requests are long: 64 requests of 2048 to 32768 tokens, one row of 40 heads over 10 each,
-// 282 us (6.7 TB/s, as a copy). Shorter ones by what an item costs beside its
+// 285 us (6.6 TB/s, as a copy). Shorter ones by what an item costs beside its
 // tiles (about 17000 cycles for 32 rows, 8000 for 5: codes, waits, joining the sums, storing; the first of a CTA twice
-// that, as its instructions come from the L2) and tiles by their chain (64 x 8 rows over 4096 tokens 119 us, 4.6
+// that, as its instructions come from the L2) and tiles by their chain (64 x 8 rows over 4096 tokens 121 us, 4.5
 // TB/s; 4 us of them for the third code of a weight). Heads of 64, 64 x 1 rows over 4096 tokens: 74 us (3.6 TB/s), 65 with two
 // codes; there neither a longer ring, nor a second loading warp made it faster.
 #include <cudaTypedefs.h>
@@ -49,7 +49,7 @@
 namespace hf {
 namespace {
 
-constexpr float kLift = 15.f, kLifted = 8.f;
+constexpr float kLift = 15.f, kLifted = 10.f;
 constexpr float kFine = 16.f;       // a row's lo is held times this
 constexpr float kFinerW = 8.f;      // a weight's second code times this, its third times the square
 

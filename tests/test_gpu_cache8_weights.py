@@ -32,8 +32,8 @@ def _codes(x):
     return (x / scale[..., None, None]).float().to(torch.float8_e4m3fn), scale.float()
 
 
-def _case(hf, dh, keys, rows, n, place, share, page=64, hkv=2, group=2, seed=1):
-    """n requests that hold the same pages. Scores are normal draws; key `place` scores as much more as gives it
+def _case(hf, dh, keys, rows, n, place, share, page=64, hkv=2, group=2, seed=1, floor=0.0):
+    """floor: how far off a weight times its page's scale may be, of the largest. n requests that hold the same pages. Scores are normal draws; key `place` scores as much more as gives it
     `share` of a row's sum, its value is zero, the others' values are around 0.3."""
     g = torch.Generator().manual_seed(seed)
     pages = -(-keys // page)
@@ -63,6 +63,10 @@ def _case(hf, dh, keys, rows, n, place, share, page=64, hkv=2, group=2, seed=1):
     ds = (dh + 4) * R.U * torch.einsum("rhgd,hkd->rhgk", qq.abs(), kk.abs()).amax() * dh ** -0.5
     ds = ds + 2.0 ** -14 * top / 224 * kk.abs().sum(-1).max() * dh ** -0.5
     tol = (4 * ds + (keys + 16) * R.U + 2.0 ** -8) * mag + 2.0 ** -8 * o.abs()
+    if floor:
+        sv = vs.double().repeat_interleave(page, 0).T[:, :keys].cuda()  # [hkv, keys]
+        top = (p * sv[None, :, None]).amax(-1).view(rows, -1, 1)
+        tol = tol + floor * top * (vv.abs() / sv[..., None]).sum(1).repeat_interleave(group, 0)
     assert 0.6 * share < float(p[..., place].min()) and float(p[..., place].max()) < 1.4 * share
     return c, q.cuda().expand(n, *q.shape).contiguous(), R.to64(o), R.to64(tol)
 
@@ -78,6 +82,18 @@ def test_a_key_that_holds_most_of_the_weight(hf, dh, keys, rows, place, share):
         for i in range(n):
             R.check_attention(out[i], want, tol, f"{n} requests, entry {i}")
         assert not c.check()
+
+
+@pytest.mark.parametrize("share", [0.999, 0.9999])
+@pytest.mark.parametrize("n", [1, 64])
+def test_a_key_that_holds_nearly_all_of_the_weight(hf, n, share):
+    """Where the weights of 32768 others end is derived: codes to half a step of 2^-22 (and 16-bit floats to half of
+    2^-24), the largest at 2^10."""
+    for place in (3, 20000):
+        c, q, want, tol = _case(hf, 128, 32768, 2, n, place, share, floor=1.25 * 2.0 ** -33)
+        out = R.to64(c.attend(q))
+        for i in range(n):
+            R.check_attention(out[i], want, tol, f"key {place}, entry {i}")
 
 
 @pytest.mark.parametrize("place", [3, 2000, 4096 - 300, 4096 - 20])
