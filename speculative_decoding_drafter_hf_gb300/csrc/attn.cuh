@@ -111,7 +111,8 @@ __device__ __forceinline__ int unit_of(const AttnRows& a, int g, int t) {
 // others `less`. A piece is what a CTA has of one entry and unit. An entry with tiles
 // first has item_start empty places: what an item costs beside its tiles (measured, 64 x 8
 // rows: about 2.2 us a tile, 1.7 us an item; of an 8-bit cache without items of the prefix, whose tiles are
-// shorter, 1.6 and 5: 64 x 8 rows over 8192 and 8 to 4096 tokens, all, 148 us with three places, 158 with one).
+// shorter, 1.6 and 5: all of 64 x 8 rows over 8192 shared and 8 to 4096 own tokens 141 us with three places, 165 with one, over
+// 2048 shared 74 and 83; 32 x 16 rows over 4096 own tokens 119 either way).
 constexpr int kItemStart = 1, kItemStart8 = 3;
 __device__ __forceinline__ int entry_places(const AttnRows& a, int keys) {
   return keys > 0 ? (keys + kKeyTile - 1) / kKeyTile + a.item_start : 0;
@@ -240,7 +241,9 @@ constexpr int kTileRows = 128, kTileRows8 = 64;
 inline int tile_rows8(int G) { return G > 48 ? kTileRows8 : 48; }
 constexpr int kSmall = 256;    // entries of a call that every CTA plans for itself
 // busy: CTAs of the launch directly before it (attn_tc_pages of a dense prefix) that this one runs beside, each as long
-// as `places` of an entry's; 0: it waits for that launch. Not with more than kSmall entries: their plan would be between.
+// as `places` of an entry's; 0: it waits for that launch. Beside it, this launch reads the cache and the rows before its own
+// wait (as a commit's early reads do): the launch directly before it triggers only behind its own wait, when all launches before
+// that have ended and their writes are in memory. Not with more than kSmall entries: their plan would be between.
 cudaError_t launch_attn_tc8_pages(const AttnRows& a, int pre_items, int busy, int places, cudaStream_t st);
 bool attn_gives_up();  // a test made every wait give up before it begins
 cudaError_t launch_attn_tc_prompt(const AttnRows& a, cudaStream_t st);

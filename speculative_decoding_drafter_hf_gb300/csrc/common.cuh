@@ -47,11 +47,6 @@ __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-
 // for the previous kernel's completion and memory (wait) before it reads or
 // writes anything that kernel may touch. Every kernel calls pdl_wait before it
 // finishes, so completion stays transitive along the stream.
-//
-// A few launches read before their own wait what launches before the previous one have
-// written (the caches of a commit, the entries' own keys beside a prefix of bf16 rows). They
-// rely on the previous launch, which must be the one directly before them, to trigger only
-// behind its own wait: all before it have ended by then, their writes in memory.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
