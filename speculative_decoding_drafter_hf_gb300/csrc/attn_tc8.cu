@@ -720,7 +720,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const bool two = it.split && it.nt[1] > 0;
         const int32_t* tab = attn_table(a, it.entry);
         // The item's pages, 32 at a time and 32 ahead: a look-up for every tile, though made a tile ahead, held the copies
-        // up (64 x 1 rows over 4096 tokens, heads of 64: 80 us, so 73).
+        // up (64 x 1 rows over 4096 tokens, heads of 64, with weights of two codes: 80 us, so 73).
         const int first = it.j0 >> shift, pages = j1 > it.j0 ? ((j1 - 1) >> shift) - first + 1 : 0;
         auto look_up = [&](int batch) { return batch * 32 + lane < pages ? tab[first + batch * 32 + lane] : 0; };
         int batch = 0, now = look_up(0), then = look_up(1);
@@ -731,7 +731,7 @@ tc8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           ok = ok && !*abort_flag;
           return s;
         };
-        // (few instructions a tile: this warp's were the limit where tiles are short; the same call 73 us before, 65 now)
+        // (few instructions a tile: this warp's were the limit where tiles are short; the same call 73 us before, then 65)
         auto tile = [&](int j, bool is_v) {
           const int at = j * nbox, id = __shfl_sync(0xffffffffu, (at >> 5) == batch ? now : then, (at + box) & 31);
           const int s = place(two ? 2 : 1);

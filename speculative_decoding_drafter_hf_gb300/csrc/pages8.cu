@@ -9,8 +9,8 @@
 // Few rows: bound by the chain of look-ups (bounds, length, page, rows), one launch each way: 64 x 8 rows into three
 // layers 10.1 us, and 64 x 8 to 23 rows of them back 10.2. Many: 10732 rows of 10 heads of 128 written in 21 us
 // (3.9 TB/s, instructions issued in 65% of the cycles), read back in 20 (4.1 TB/s); 54198 rows of 8 heads
-// in three layers read back in 170 us (5.9 TB/s, the memory). Tried and no faster: neighbouring units to one warp,
-// so that it looks a page up once (170 -> 200), codes to bf16 by their bits (169 -> 173).
+// in three layers read back in 165 us (6.0 TB/s, the memory). Tried and no faster: neighbouring units to one warp,
+// so that it looks a page up once (170 -> 200 then), codes to bf16 by their bits (169 -> 173).
 #include <cstdio>
 
 #include "attn.cuh"
